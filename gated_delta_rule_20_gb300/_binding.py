@@ -25,17 +25,26 @@ GDN_ERR_WORKSPACE = 7
 
 GDN_F32 = 0
 GDN_BF16 = 1
+GDN_F8E4M3 = 2
 
 GDN_ZERO_INITIAL_STATE = 1 << 0
 GDN_FORCE_FFMA = 1 << 1
 GDN_SINGLE_PASS = 1 << 2
+
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU, GDN_ACT_RELU = range(4)
+ACTIVATIONS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "gelu": GDN_ACT_GELU, "relu": GDN_ACT_RELU}
+
+GDN_LINEAR_WEIGHT_NK = 1 << 0
+GDN_LINEAR_GATED = 1 << 1
+GDN_LINEAR_FORCE_FFMA = 1 << 2
 
 # Every symbol include/gdn.h declares.
 EXPORTED = ("gdn_prefill", "gdn_decode_step", "gdn_prefill_workspace_bytes", "gdn_status_string",
             "gdn_device_status", "gdn_kernels_per_call", "gdn_conv1d_prefill", "gdn_conv1d_decode",
             "gdn_decode_gated", "gdn_decode_block_workspace_bytes", "gdn_decode_block", "gdn_rmsnorm_gated",
             "gdn_prefill_gated", "gdn_prefill_segments", "gdn_decode_block_noalloc",
-            "gdn_set_wait_limit_ns", "gdn_test_stall_prefill", "gdn_prefill_ws", "gdn_prefill_segment_starts")
+            "gdn_set_wait_limit_ns", "gdn_test_stall_prefill", "gdn_prefill_ws", "gdn_prefill_segment_starts",
+            "gdn_rmsnorm_residual", "gdn_linear")
 
 
 class GdnDims(ctypes.Structure):
@@ -53,6 +62,11 @@ class GdnBlockDims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("Hk", ctypes.c_int64), ("Hv", ctypes.c_int64),
                 ("Dk", ctypes.c_int64), ("Dv", ctypes.c_int64), ("K", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class GdnLinearDims(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
 class GdnError(RuntimeError):
@@ -117,6 +131,11 @@ def lib() -> ctypes.CDLL:
         L.gdn_prefill_gated.restype = ctypes.c_int
         L.gdn_prefill_gated.argtypes = [vp, vp, vp, fp, fp, vp, fp, ctypes.c_float, fp, vp, ctypes.POINTER(GdnDims),
                                         vp]
+        L.gdn_rmsnorm_residual.restype = ctypes.c_int
+        L.gdn_rmsnorm_residual.argtypes = [vp, vp, fp, vp, vp, fp, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
+                                           ctypes.c_int32, ctypes.c_float, vp]
+        L.gdn_linear.restype = ctypes.c_int
+        L.gdn_linear.argtypes = [vp, fp, vp, fp, fp, vp, vp, ctypes.POINTER(GdnLinearDims), vp]
         _lib = L
     return _lib
 
@@ -487,3 +506,166 @@ def decode_block_noalloc(hidden, W_qkv, W_z, W_a, W_b, conv_weight, conv_state, 
                                               ctypes.c_void_p(stream.cuda_stream))
     _check(code)
     return out, conv_state, state
+
+
+# ------------------------------------------------------------------ the layer around the block
+_LAYER_DTYPES = None
+
+
+def _layer_dtype(t, nm: str) -> int:
+    """gdn_dtype of a tensor of the layer operators."""
+    global _LAYER_DTYPES
+    if _LAYER_DTYPES is None:
+        torch = _torch()
+        _LAYER_DTYPES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_F8E4M3}
+    code = _LAYER_DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError("%s must be bfloat16, float32 or float8_e4m3fn, got %s" % (nm, t.dtype))
+    return code
+
+
+def _layer_tensor(nm, t, shape, dtype, device):
+    """Checks an operand of the layer operators: on ``device``, contiguous, of that shape and dtype."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor on %s" % (nm, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (nm, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (nm, tuple(shape), tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _layer_empty(shape, dtype, device, stream):
+    """A new output, allocated on the stream that writes it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _layer_call(fn, device, stream, *args):
+    """Calls an entry point on ``stream`` (default: the device's current one), with the device current."""
+    torch = _torch()
+    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, handle))
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, handle))
+
+
+def rmsnorm_residual(x, norm_weight, residual=None, *, out=None, out_scale=None, residual_out=None, out_dtype=None,
+                     eps=1e-6, stream=None):
+    """RMS norm behind the residual's addition (``gdn_rmsnorm_residual``): ``h = x + residual``,
+    ``out = h / sqrt(mean(h^2) + eps) * norm_weight`` over the last dimension.
+
+    x, residual [..., D] bf16 or fp32, norm_weight [D] fp32.  ``out_dtype`` is x's (the default) or
+    ``torch.float8_e4m3fn``: then ``out_scale`` [...] fp32 holds one scale a row, and
+    ``out * out_scale`` stands for the normalised row.  ``residual_out`` (default: a new tensor where
+    there is a residual; it may be ``residual``) receives ``h``.  Returns
+    ``(out, out_scale, residual_out)``, with None for what the call does not have."""
+    torch = _torch()
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA tensor")
+    dt, shape, device = _layer_dtype(x, "x"), x.shape, x.device
+    if dt == GDN_F8E4M3:
+        raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
+    if len(shape) < 1 or shape[-1] < 1:
+        raise ValueError("x must be [..., D] with D >= 1")
+    D = shape[-1]
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    if out is None:
+        out = _layer_empty(shape, out_dtype, device, stream)
+    odt = _layer_dtype(out, "out")
+    if odt not in (dt, GDN_F8E4M3):
+        raise TypeError("out must have x's dtype or float8_e4m3fn, got %s" % out.dtype)
+    wp = _layer_tensor("norm_weight", norm_weight, (D,), torch.float32, device)
+    op = _layer_tensor("out", out, shape, out_dtype, device)
+    sp = rp = hp = None
+    if odt == GDN_F8E4M3:
+        if out_scale is None:
+            out_scale = _layer_empty(shape[:-1], torch.float32, device, stream)
+        sp = _layer_tensor("out_scale", out_scale, shape[:-1], torch.float32, device)
+    elif out_scale is not None:
+        raise ValueError("out_scale goes with a float8_e4m3fn out only")
+    if residual is not None:
+        rp = _layer_tensor("residual", residual, shape, x.dtype, device)
+        if residual_out is None:
+            residual_out = _layer_empty(shape, x.dtype, device, stream)
+    if residual_out is not None:
+        hp = _layer_tensor("residual_out", residual_out, shape, x.dtype, device)
+    _layer_call(lib().gdn_rmsnorm_residual, device, stream, x.data_ptr(), rp, wp, hp, op, sp, x.numel() // D, D, dt, odt,
+                eps)
+    return out, out_scale, residual_out
+
+
+def _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weight_scale, out, out_dtype, force_ffma,
+            stream, gated):
+    torch = _torch()
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous CUDA tensor")
+    dt, shape, device = _layer_dtype(x, "x"), x.shape, x.device
+    if weight_layout not in ("kn", "nk"):
+        raise ValueError("weight_layout must be 'kn' or 'nk'")
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(ACTIVATIONS))
+    if len(shape) < 1 or weight.dim() != 2:
+        raise ValueError("x must be [..., K] and weight two-dimensional")
+    K = shape[-1]
+    flags = (GDN_LINEAR_FORCE_FFMA if force_ffma else 0)
+    if weight_layout == "nk":
+        cols, flags, wshape = weight.shape[0], flags | GDN_LINEAR_WEIGHT_NK, (weight.shape[0], K)
+    else:
+        cols, wshape = weight.shape[1], (K, weight.shape[1])
+    N = cols
+    if gated:
+        if cols % 2:
+            raise ValueError("a gated weight has an even number of columns, got %d" % cols)
+        N, flags = cols // 2, flags | GDN_LINEAR_GATED
+    wp = _layer_tensor("weight", weight, wshape, x.dtype, device)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.float32 if dt == GDN_F32 else torch.bfloat16
+    oshape = shape[:-1] + (N,)
+    if out is None:
+        out = _layer_empty(oshape, out_dtype, device, stream)
+    op = _layer_tensor("out", out, oshape, out_dtype, device)
+    odt = _layer_dtype(out, "out")
+    M = 1
+    for n in shape[:-1]:
+        M *= n
+    xsp = wsp = bp = rp = None
+    if (x_scale is not None or weight_scale is not None) and dt != GDN_F8E4M3:
+        raise ValueError("x_scale and weight_scale go with float8_e4m3fn operands only")
+    if dt == GDN_F8E4M3:
+        if x_scale is None or weight_scale is None:
+            raise ValueError("float8_e4m3fn operands need x_scale and weight_scale")
+        xsp = _layer_tensor("x_scale", x_scale, shape[:-1], torch.float32, device)
+        wsp = _layer_tensor("weight_scale", weight_scale, (cols,), torch.float32, device)
+    if bias is not None:
+        bp = _layer_tensor("bias", bias, (cols,), torch.float32, device)
+    if residual is not None:
+        rp = _layer_tensor("residual", residual, oshape, out_dtype, device)
+    dims = GdnLinearDims(M, N, K, dt, odt, ACTIVATIONS[activation], flags)
+    _layer_call(lib().gdn_linear, device, stream, x.data_ptr(), xsp, wp, wsp, bp, rp, op, dims)
+    return out
+
+
+def linear(x, weight, bias=None, residual=None, *, activation="none", weight_layout="kn", x_scale=None,
+           weight_scale=None, out=None, out_dtype=None, force_ffma=False, stream=None):
+    """``act(x W + bias) + residual`` (``gdn_linear``): x [..., K]; weight [K, N] (``weight_layout``
+    "kn", the decode block's) or [N, K] ("nk", nn.Linear.weight) in x's dtype, bf16, fp32 or, "nk" only,
+    float8_e4m3fn with ``x_scale`` [...] and ``weight_scale`` [N] fp32.  ``bias`` [N] fp32;
+    ``activation`` "none", "silu", "gelu" (erf) or "relu"; ``out`` and ``residual`` [..., N] in
+    ``out_dtype`` (bf16, or fp32; fp32 compute gives fp32); ``out`` may be ``residual``.  Returns ``out``."""
+    return _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weight_scale, out, out_dtype,
+                   force_ffma, stream, False)
+
+
+def linear_gated(x, weight, bias=None, residual=None, *, activation="silu", weight_layout="kn", x_scale=None,
+                 weight_scale=None, out=None, out_dtype=None, force_ffma=False, stream=None):
+    """``act(x Wg + bg) * (x Wu + bu) + residual``: ``linear`` with a weight (and bias and
+    ``weight_scale``) of 2 N columns, the gate's N first (``GDN_LINEAR_GATED``).  Returns ``out`` [..., N]."""
+    return _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weight_scale, out, out_dtype,
+                   force_ffma, stream, True)

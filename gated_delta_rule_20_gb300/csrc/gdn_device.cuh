@@ -1,8 +1,11 @@
 // gdn_device.cuh -- small device helpers shared by the kernels: conversions
-// between the compute dtype and fp32, a warp sum, and SiLU.
+// between the element types and fp32, a warp sum, a maximum that keeps NaN, and SiLU.
 #pragma once
 
+#include <cstdint>
+
 #include <cuda_bf16.h>
+#include <cuda_fp8.h>
 
 namespace gdn {
 
@@ -16,6 +19,10 @@ template <>
 __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) {
     return __bfloat162float(x);
 }
+template <>
+__device__ __forceinline__ float to_f32<__nv_fp8_e4m3>(__nv_fp8_e4m3 x) {
+    return static_cast<float>(x);
+}
 
 template <typename T>
 __device__ __forceinline__ T from_f32(float x);
@@ -26,6 +33,24 @@ __device__ __forceinline__ float from_f32<float>(float x) {
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
     return __float2bfloat16_rn(x);
+}
+
+// Two fp32 values rounded to e4m3 (to nearest even, at most +-448; NaN stays NaN), lo in the low byte.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+    return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
+}
+__device__ __forceinline__ uint8_t to_e4m3(float x) { return (uint8_t)pack_e4m3x2(x, 0.f); }
+
+// The larger of two values; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 __device__ __forceinline__ float warp_sum(float x) {

@@ -1,0 +1,311 @@
+// rmsnorm_residual.cu -- RMS norm behind the residual's addition, over rows of D
+// elements, with the normalised row in the compute dtype or in 8 bits (e4m3)
+// with one scale a row:
+//
+//     h[r, :] = x[r, :] + residual[r, :]               (fp32; written back rounded to the compute dtype)
+//     y[r, :] = h[r, :] / sqrt(mean(h[r, :]^2) + eps) * w
+//     out     = y rounded once, or
+//     scale[r] = max(max_i |y[r, i]|, GDN_FP8_AMAX_MIN) / 448,  out[r, i] = e4m3(y[r, i] / scale[r])
+//
+// One pass over HBM: the row stays in registers (or in shared memory, second
+// kernel) between its statistics and its output.  The row's maximum needs no
+// second reduction behind the norm: with s = 1 / sqrt(mean + eps), a positive
+// factor of the whole row, max |y| = s max |h w|, so the sum of squares and
+// max |h w| are reduced together.
+//
+// The statistics take the unrounded fp32 h; the only roundings are those of
+// the two outputs.  A NaN or an infinity in a row makes mean(h^2) so, and by it
+// the row's y, maximum and scale NaN, as in the formula.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+struct NormArgs {
+    const void* x;
+    const void* res;   // may be null
+    const float* w;
+    void* h;           // may be null; may be res
+    void* out;         // may be x
+    float* scale;      // e4m3 output only
+    long long rows;
+    int D;
+    float eps;
+};
+
+struct F8 {};  // tag: e4m3 output with a scale a row
+
+// (sum of squares, max |h w|) over the GROUP threads of a row.  Groups above a warp are whole
+// blocks; `part` is used in turns (`turn` = 0, 1), so that one barrier a row is enough: a
+// slot is written again only after the barrier of the row in between.
+template <int GROUP>
+__device__ __forceinline__ float2 reduce_row(float ss, float mx, float2 (*part)[GROUP / 32], int turn) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    }
+    if constexpr (GROUP > 32) {
+        if ((threadIdx.x & 31) == 0) part[turn][threadIdx.x >> 5] = make_float2(ss, mx);
+        __syncthreads();
+        ss = 0.f;
+        mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < GROUP / 32; ++i) {  // the same order in every thread
+            const float2 p = part[turn][i];
+            ss += p.x;
+            mx = max_nan(mx, p.y);
+        }
+    }
+    return make_float2(ss, mx);
+}
+
+// What turns h w into the output: the norm's factor, over the row's scale for e4m3.
+template <typename O>
+__device__ __forceinline__ float row_factor(float2 stat, const NormArgs& a, long long r, bool first) {
+    const float rinv = rsqrtf(stat.x / (float)a.D + a.eps);
+    if constexpr (std::is_same<O, F8>::value) {
+        float m = stat.y * rinv;
+        m = m < GDN_FP8_AMAX_MIN ? GDN_FP8_AMAX_MIN : m;  // a NaN stays one
+        const float scale = m / 448.f;
+        if (first) a.scale[r] = scale;
+        return rinv / scale;
+    } else {
+        return rinv;
+    }
+}
+
+// Rows of whole 16-byte pieces, 16-byte aligned: GROUP threads a row, P pieces a thread.  The
+// weights stay in registers over the rows of a thread; the next row's pieces are loaded before
+// this row's statistics are reduced, so that the barrier does not leave HBM idle.
+template <typename T, typename O, int GROUP, int P>
+__global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP)
+    rmsnorm_residual_vec_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int V = 16 / (int)sizeof(T);
+    constexpr int kBlock = GROUP == 32 ? 256 : GROUP;
+    constexpr int kRows = kBlock / GROUP;  // rows of a block at a time
+    __shared__ float2 part[2][GROUP / 32];
+    const int t = threadIdx.x % GROUP, nv = a.D / V;
+    const uint4* x = static_cast<const uint4*>(a.x);
+    const uint4* res = static_cast<const uint4*>(a.res);
+    long long r = (long long)blockIdx.x * kRows + threadIdx.x / GROUP;
+    const long long step = (long long)gridDim.x * kRows;
+    uint4 xv[P], rv[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+        const int i = t + p * GROUP;
+        xv[p] = rv[p] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < a.rows && i < nv) {
+            xv[p] = __ldcs(x + r * nv + i);
+            if (res) rv[p] = __ldcs(res + r * nv + i);
+        }
+    }
+    float w[P][V];
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int j = 0; j < V; j += 4) {
+            const int i = t + p * GROUP;
+            const float4 f = i < nv ? *reinterpret_cast<const float4*>(a.w + i * V + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+            w[p][j] = f.x;
+            w[p][j + 1] = f.y;
+            w[p][j + 2] = f.z;
+            w[p][j + 3] = f.w;
+        }
+    // blocks of several rows have one warp a row and no barrier in the loop; a block of one row leaves it as one
+    for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
+        float h[P][V], ss = 0.f, mx = 0.f;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const T* xe = reinterpret_cast<const T*>(&xv[p]);
+            const T* re = reinterpret_cast<const T*>(&rv[p]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                h[p][j] = to_f32(xe[j]);
+                if (res) h[p][j] += to_f32(re[j]);
+                ss += h[p][j] * h[p][j];
+            }
+        }
+        const long long next = r + step;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int i = t + p * GROUP;
+            if (next < a.rows && i < nv) {
+                xv[p] = __ldcs(x + next * nv + i);
+                if (res) rv[p] = __ldcs(res + next * nv + i);
+            }
+        }
+        if (a.h) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                const int i = t + p * GROUP;
+                uint4 o;
+                T* oe = reinterpret_cast<T*>(&o);
+#pragma unroll
+                for (int j = 0; j < V; ++j) oe[j] = from_f32<T>(h[p][j]);
+                if (i < nv) static_cast<uint4*>(a.h)[r * nv + i] = o;
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                h[p][j] *= w[p][j];
+                if constexpr (std::is_same<O, F8>::value) mx = max_nan(mx, fabsf(h[p][j]));
+            }
+        const float f = row_factor<O>(reduce_row<GROUP>(ss, mx, part, turn), a, r, t == 0);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+            const int i = t + p * GROUP;
+            if (i >= nv) continue;
+            if constexpr (std::is_same<O, F8>::value) {
+                uint32_t q[V / 4];
+#pragma unroll
+                for (int j = 0; j < V; j += 4)
+                    q[j / 4] = pack_e4m3x4(h[p][j] * f, h[p][j + 1] * f, h[p][j + 2] * f, h[p][j + 3] * f);
+                if constexpr (V == 8)
+                    static_cast<uint2*>(a.out)[r * nv + i] = make_uint2(q[0], q[1]);
+                else
+                    static_cast<uint32_t*>(a.out)[r * nv + i] = q[0];
+            } else {
+                uint4 o;
+                T* oe = reinterpret_cast<T*>(&o);
+#pragma unroll
+                for (int j = 0; j < V; ++j) oe[j] = from_f32<T>(h[p][j] * f);
+                static_cast<uint4*>(a.out)[r * nv + i] = o;
+            }
+        }
+    }
+}
+
+// Any D and any element alignment: the fp32 row waits in shared memory (D floats a row) for its
+// statistics.  Loads and stores of one element a thread, kUnroll of them in flight.
+template <typename T, typename O, int GROUP>
+__global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_any_kernel(const __grid_constant__ NormArgs a) {
+    constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP, kUnroll = 4;
+    extern __shared__ float row_smem[];
+    __shared__ float2 part[2][GROUP / 32];
+    const int t = threadIdx.x % GROUP;
+    const long long r = (long long)blockIdx.x * kRows + threadIdx.x / GROUP;
+    if (r >= a.rows) return;  // a whole warp (GROUP == 32), or none of the block
+    float* row = row_smem + (threadIdx.x / GROUP) * a.D;
+    const T* x = static_cast<const T*>(a.x) + r * a.D;
+    const T* res = a.res ? static_cast<const T*>(a.res) + r * a.D : nullptr;
+    T* ho = a.h ? static_cast<T*>(a.h) + r * a.D : nullptr;
+    float ss = 0.f, mx = 0.f;
+    for (int i0 = t; i0 < a.D; i0 += GROUP * kUnroll) {
+        float v[kUnroll], u[kUnroll];
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const int i = i0 + k * GROUP;
+            v[k] = i < a.D ? to_f32(x[i]) : 0.f;
+            u[k] = res && i < a.D ? to_f32(res[i]) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kUnroll; ++k) {
+            const int i = i0 + k * GROUP;
+            if (i >= a.D) continue;
+            const float h = res ? v[k] + u[k] : v[k];
+            if (ho) ho[i] = from_f32<T>(h);
+            ss += h * h;
+            const float hw = h * a.w[i];
+            row[i] = hw;  // read back by this thread only
+            if constexpr (std::is_same<O, F8>::value) mx = max_nan(mx, fabsf(hw));
+        }
+    }
+    const float f = row_factor<O>(reduce_row<GROUP>(ss, mx, part, 0), a, r, t == 0);
+    for (int i = t; i < a.D; i += GROUP) {
+        if constexpr (std::is_same<O, F8>::value)
+            static_cast<uint8_t*>(a.out)[r * a.D + i] = to_e4m3(row[i] * f);
+        else
+            static_cast<T*>(a.out)[r * a.D + i] = from_f32<T>(row[i] * f);
+    }
+}
+
+template <typename T, typename O, int GROUP, int P>
+cudaError_t launch_vec(const NormArgs& a, int sms, cudaStream_t s) {
+    constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP;
+    static const int per_sm = [] {  // of this instantiation, the same on every device the library is built for
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rmsnorm_residual_vec_kernel<T, O, GROUP, P>, kBlock, 0) ==
+                           cudaSuccess && n > 0 ? n : 1;
+    }();
+    const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sms * per_sm;
+    rmsnorm_residual_vec_kernel<T, O, GROUP, P><<<(unsigned)(need < room ? need : room), kBlock, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T, typename O, int GROUP>
+cudaError_t launch_any(const NormArgs& a, cudaStream_t s) {
+    constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP;
+    const size_t smem = (size_t)kRows * a.D * sizeof(float);
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(rmsnorm_residual_any_kernel<T, O, GROUP>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    rmsnorm_residual_any_kernel<T, O, GROUP><<<(unsigned)((a.rows + kRows - 1) / kRows), kBlock, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+// The group is the smallest that holds the row in at most 2 pieces a thread (4 for warps, whose
+// rows need no barrier, and for the widest rows).
+template <typename T, typename O>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const uintptr_t wide = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.res) |
+                           reinterpret_cast<uintptr_t>(a.h) | reinterpret_cast<uintptr_t>(a.out) |
+                           reinterpret_cast<uintptr_t>(a.w);
+    const int nv = a.D % V == 0 && (wide & 15u) == 0 ? a.D / V : INT32_MAX;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    if (nv <= 32) return launch_vec<T, O, 32, 1>(a, sms, s);
+    if (nv <= 64) return launch_vec<T, O, 32, 2>(a, sms, s);
+    if (nv <= 128) return launch_vec<T, O, 32, 4>(a, sms, s);
+    if (nv <= 256) return launch_vec<T, O, 128, 2>(a, sms, s);
+    if (nv <= 512) return launch_vec<T, O, 256, 2>(a, sms, s);
+    if (nv <= 1024) return launch_vec<T, O, 512, 2>(a, sms, s);
+    if (nv <= 2048) return launch_vec<T, O, 512, 4>(a, sms, s);
+    if (a.D <= 1024) return launch_any<T, O, 32>(a, s);
+    if (a.D <= 8192) return launch_any<T, O, 256>(a, s);
+    return launch_any<T, O, 1024>(a, s);
+}
+
+}  // namespace
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" gdn_status gdn_rmsnorm_residual(const void* x, const void* residual, const float* norm_weight,
+                                           void* residual_out, void* out, float* out_scale, int64_t rows, int64_t D,
+                                           int32_t dtype, int32_t out_dtype, float eps, gdn_stream_t stream) {
+    if ((dtype != GDN_F32 && dtype != GDN_BF16) || (out_dtype != dtype && out_dtype != GDN_F8E4M3))
+        return GDN_ERR_UNSUPPORTED;
+    if (rows < 0 || D < 1 || D > GDN_NORM_MAX_D || rows > INT32_MAX || !(eps >= 0.f)) return GDN_ERR_DIMS;
+    if (rows == 0) return GDN_OK;
+    const bool f8 = out_dtype == GDN_F8E4M3;
+    if (!x || !norm_weight || !out || (f8 && !out_scale)) return GDN_ERR_NULL;
+    if (residual_out == out) return GDN_ERR_UNSUPPORTED;  // two results in one buffer
+    const uintptr_t esz = dtype == GDN_BF16 ? 2 : 4;
+    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
+          reinterpret_cast<uintptr_t>(residual_out) | (f8 ? 0 : reinterpret_cast<uintptr_t>(out))) & (esz - 1)) ||
+        ((reinterpret_cast<uintptr_t>(norm_weight) | (f8 ? reinterpret_cast<uintptr_t>(out_scale) : 0)) & 3u))
+        return GDN_ERR_ALIGN;
+    const NormArgs a{x, residual, norm_weight, residual_out, out, out_scale, rows, (int)D, eps};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (dtype == GDN_BF16)
+        e = f8 ? launch_norm<__nv_bfloat16, F8>(a, s) : launch_norm<__nv_bfloat16, __nv_bfloat16>(a, s);
+    else
+        e = f8 ? launch_norm<float, F8>(a, s) : launch_norm<float, float>(a, s);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}

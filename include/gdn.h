@@ -53,7 +53,12 @@ typedef enum {
 /* Compute dtype = dtype of q, k, v and out ("GDN CTE Kernel API Reference",
  * Parameters / query: the query's dtype sets the compute dtype).  g_log, beta
  * and the state are always fp32. */
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+typedef enum {
+    GDN_F32 = 0,
+    GDN_BF16 = 1,
+    GDN_F8E4M3 = 2  /* 8 bits: sign, 4 exponent and 3 mantissa bits, largest finite value 448, no
+                       infinities; of the layer operators only (gdn_rmsnorm_residual, gdn_linear) */
+} gdn_dtype;
 
 enum {
     /* The "omitted" recurrent_state form (Parameters / recurrent_state): start
@@ -335,6 +340,88 @@ gdn_status gdn_rmsnorm_gated(const void* x, const void* z, const float* norm_wei
 gdn_status gdn_prefill_gated(const void* q, const void* k, const void* v, const float* g_log, const float* beta,
                              const void* z, const float* norm_weight, float scale, float* state_inout, void* out,
                              const gdn_dims* dims, gdn_stream_t stream);
+
+/*
+ * The operators of the layer around the block: the norm in front of it, the
+ * output projection behind it, and the feed-forward's products.  (The pages'
+ * block kernel leaves them to its caller.)  gdn_rmsnorm_residual's 8-bit rows and
+ * scales are gdn_linear's 8-bit x and x_scale.
+ */
+
+/*
+ * gdn_rmsnorm_residual -- RMS norm behind the residual's addition, over `rows`
+ * rows of D elements:
+ *     h[r, :] = x[r, :] + residual[r, :]        (fp32; x[r, :] alone where residual is NULL)
+ *     y[r, :] = h[r, :] / sqrt(mean(h[r, :]^2) + eps) * norm_weight
+ *   x, residual   [rows, D] in `dtype` (GDN_BF16 or GDN_F32)
+ *   norm_weight   [D] fp32
+ *   residual_out  [rows, D] in `dtype`, receives h rounded once; NULL: not written;
+ *                 may be residual (in place) or x
+ *   out           [rows, D] in out_dtype: `dtype` (y rounded once; may be x), or GDN_F8E4M3 with one scale a row:
+ *                     out_scale[r] = max(max_i |y[r, i]|, GDN_FP8_AMAX_MIN) / 448
+ *                     out[r, i]    = e4m3(y[r, i] / out_scale[r])
+ *                 so that out[r, i] * out_scale[r] stands for y[r, i]; a row with a NaN
+ *                 (or an infinity) in y is NaN whole, its scale too
+ *   out_scale     [rows] fp32, read only where out_dtype is GDN_F8E4M3
+ *   eps           >= 0
+ * rows in [0, 2^31), 1 <= D <= GDN_NORM_MAX_D; pointers aligned to their element;
+ * residual_out and out may not be the same buffer (GDN_ERR_UNSUPPORTED).
+ * Rows of whole 16-byte pieces with every pointer 16-byte aligned (and
+ * D <= 16384 in bf16, 8192 in fp32) take 128-bit accesses.  One launch on `stream`.
+ */
+#define GDN_FP8_AMAX_MIN 1e-30f
+#define GDN_NORM_MAX_D 32768
+gdn_status gdn_rmsnorm_residual(const void* x, const void* residual, const float* norm_weight, void* residual_out,
+                                void* out, float* out_scale, int64_t rows, int64_t D, int32_t dtype,
+                                int32_t out_dtype, float eps, gdn_stream_t stream);
+
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2, GDN_ACT_RELU = 3 } gdn_activation;
+
+enum {
+    /* The weight is stored [N', K] (nn.Linear.weight) instead of [K, N'] (its transpose, the
+     * decode block's layout). */
+    GDN_LINEAR_WEIGHT_NK = 1u << 0,
+    /* The gated form: the weight, weight_scale and bias have N' = 2 N columns, the gate's N first. */
+    GDN_LINEAR_GATED = 1u << 1,
+    /* Run on the fp32 FFMA kernel even where the tensor-core kernels apply (a cross-check path). */
+    GDN_LINEAR_FORCE_FFMA = 1u << 2
+};
+
+/*
+ * 0 <= M <= 4194240 rows of x (0: nothing to do), N >= 1 columns of out, K >= 1;
+ * N' = N, or 2 N under GDN_LINEAR_GATED; N' and K below 2^31 - 256.
+ */
+typedef struct {
+    int64_t M, N, K;
+    int32_t dtype;       /* of x and weight: GDN_BF16, GDN_F32 or GDN_F8E4M3 */
+    int32_t out_dtype;   /* of out and residual: GDN_F32, or GDN_BF16 unless dtype is GDN_F32 */
+    int32_t activation;  /* gdn_activation */
+    uint32_t flags;      /* GDN_LINEAR_* */
+} gdn_linear_dims;
+
+/*
+ * gdn_linear -- a matrix product with bias, activation and residual in its epilogue:
+ *     a[m, n]   = x_scale[m] * weight_scale[n] * sum_k x[m, k] W[k, n] + bias[n]
+ *     out[m, n] = act(a[m, n]) + residual[m, n]                              or, gated,
+ *     out[m, n] = act(a[m, n]) * a[m, N + n] + residual[m, n]
+ * with W[k, n] the weight's element in its layout; sums and the epilogue in fp32, one
+ * rounding to out_dtype.  silu(v) = v / (1 + e^-v), gelu(v) = v/2 (1 + erf(v / sqrt 2)),
+ * relu(v) = max(v, 0) (NaN stays NaN).
+ *   x            [M, K] in dtype
+ *   x_scale      [M] fp32 and weight_scale [N'] fp32: GDN_F8E4M3 only (NULL otherwise)
+ *   weight       [K, N'] or, under GDN_LINEAR_WEIGHT_NK, [N', K], in dtype;
+ *                GDN_F8E4M3 takes GDN_LINEAR_WEIGHT_NK only (else GDN_ERR_UNSUPPORTED)
+ *   bias         [N'] fp32, or NULL
+ *   residual     [M, N] in out_dtype, or NULL; may be out (in place)
+ *   out          [M, N] in out_dtype
+ * Pointers aligned to their element.  x or a weight whose pointer is not 16-byte aligned, or
+ * whose rows are not a multiple of 16 bytes, and fp32 compute take the FFMA kernel, at a
+ * small part of the tensor cores' rate.  One launch on `stream`.  Results do not depend on
+ * what else runs: every sum has one order for given dims and device.
+ */
+gdn_status gdn_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale,
+                      const float* bias, const void* residual, void* out, const gdn_linear_dims* dims,
+                      gdn_stream_t stream);
 
 /* Device scratch a prefill with these dims needs on the current device: the
  * segment states, maps and identity-start outputs of a split (see gdn_prefill;

@@ -1,0 +1,224 @@
+"""GPU parity of ``gdn_linear`` (``linear``, ``linear_gated``) with the fp64 oracle ``oracle.layer``.
+
+The bar of a sum of K products with fp32 accumulation, whatever its order: every one of at most K
+additions rounds (or truncates) a partial sum of magnitude at most S = sum |x w| to 2^-23 of it.  The
+errors of one sum add up like a random walk, so a few sqrt(K) of them are what can be seen; the bar
+takes 8 sqrt(K) + 8 steps of 2^-24 S (the scales' and the bias's roundings are within the 8).  It goes
+through the epilogue by the activations' slopes (at most 1.13) and the product rule, plus 16 u of the
+value for the fast exponential and division (u = 2^-24), and the output's rounding: 2^-8 of the value
+in bf16."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from oracle import layer  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "f32": torch.float32, "f8": torch.float8_e4m3fn}
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import gated_delta_rule_20_gb300 as g
+    g.lib()
+    yield g
+    assert g.device_status(0) == 0
+
+
+def _draw(M, N, K, dtype, layout, gated, bias, residual, out, seed):
+    gen = torch.Generator("cuda").manual_seed(seed)
+    n = 2 * N if gated else N
+    normal = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
+    x, w, xs, ws = normal(M, K), normal(n, K) / K ** 0.5, None, None
+    if dtype == "f8":
+        xs, ws = x.abs().amax(1) / 448, w.abs().amax(1) / 448
+        x, w = x / xs[:, None], w / ws[:, None]
+    x, w = x.to(DT[dtype]), w.to(DT[dtype])
+    if layout == "kn":
+        w = w.t().contiguous()
+    return dict(x=x, weight=w, x_scale=xs, weight_scale=ws, bias=normal(n) if bias else None,
+                residual=normal(M, N).to(DT[out]) if residual else None)
+
+
+def _check(out, t, act, layout, gated):
+    args = {k: None if t[k] is None else t[k].float().cpu() for k in t}
+    a, s = layer.affine(args["x"], args["weight"], args["bias"], args["x_scale"], args["weight_scale"], layout)
+    K = t["x"].shape[1]
+    e = (8 * K ** 0.5 + 8) * U * s
+    if gated:
+        n = a.shape[1] // 2
+        g, u, eg, eu = layer.activation(act, a[:, :n]), a[:, n:], 1.13 * e[:, :n], e[:, n:]
+        eg = eg + 16 * U * np.abs(g)
+        ref, e = g * u, eg * np.abs(u) + np.abs(g) * eu + eg * eu
+    else:
+        ref = layer.activation(act, a)
+        e = 1.13 * e + 16 * U * np.abs(ref)
+    if args["residual"] is not None:
+        ref = ref + args["residual"].double().numpy()
+    e = e + 2 * U * np.abs(ref)
+    if out.dtype == torch.bfloat16:
+        e = e + 2.0 ** -8 * (np.abs(ref) + e)
+    got = out.detach().cpu().double().numpy()
+    assert np.isfinite(got).all()
+    bad = np.abs(got - ref) > e + 1e-30
+    assert not bad.any(), "%d of %d elements beyond the bar, worst %.3g at %s" % (
+        bad.sum(), bad.size, (np.abs(got - ref) / (e + 1e-30)).max(), np.argwhere(bad)[:3].tolist())
+
+
+def _run(gdn, M, N, K, dtype="bf16", layout="nk", gated=False, act="none", bias=False, residual=False, out=None, **kw):
+    out = out or ("f32" if dtype == "f32" else "bf16")
+    t = _draw(M, N, K, dtype, layout, gated, bias, residual, out, seed=M * 31 + N * 7 + K)
+    call = gdn.linear_gated if gated else gdn.linear
+    # NaN in the output before the call: what is not written shows, and so does a write past the end
+    buf = torch.full((M * N + 64,), float("nan"), dtype=DT[out], device="cuda")
+    got = call(t["x"], t["weight"], t["bias"], t["residual"], activation=act, weight_layout=layout,
+               x_scale=t["x_scale"], weight_scale=t["weight_scale"], out=buf[:M * N].view(M, N), **kw)
+    torch.cuda.synchronize()
+    assert buf[M * N:].isnan().all()
+    _check(got, t, act, layout, gated)
+    return got, t
+
+
+# a token to many; sizes under, at and over a tile's; widths that no 16 bytes divide
+MNK = [(1, 1, 1), (1, 1, 16), (1, 128, 64), (1, 2048, 4096), (2, 130, 72), (3, 64, 48), (5, 7, 33), (16, 256, 128), (17, 200, 144),
+       (33, 96, 1040), (64, 128, 64), (65, 129, 80), (100, 1000, 272), (127, 136, 200), (128, 512, 512), (129, 640, 336), (200, 72, 16),
+       (256, 256, 2048), (257, 384, 192), (300, 1111, 96), (513, 264, 1056), (700, 2056, 520)]
+
+
+@pytest.mark.parametrize("M,N,K", MNK)
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_bf16_shapes(gdn, M, N, K, layout, gated):
+    _run(gdn, M, N, K, "bf16", layout, gated, act="silu" if gated else "none")
+
+
+@pytest.mark.parametrize("M,N,K", MNK)
+@pytest.mark.parametrize("gated", [False, True])
+def test_f8_shapes(gdn, M, N, K, gated):
+    _run(gdn, M, N, K, "f8", "nk", gated, act="silu" if gated else "none", bias=True)
+
+
+@pytest.mark.parametrize("M,N,K", MNK)
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+def test_f32_shapes(gdn, M, N, K, layout):
+    _run(gdn, M, N, K, "f32", layout, gated=M % 2 == 0, act="gelu", bias=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 136, 192), (70, 300, 520), (400, 520, 264)])
+@pytest.mark.parametrize("dtype", ["bf16", "f8", "f32"])
+@pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu"])
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("bias,residual,out", [(False, False, "f32"), (True, True, "f32"), (False, True, None), (True, False, None)])
+def test_epilogues(gdn, M, N, K, dtype, act, gated, bias, residual, out):
+    _run(gdn, M, N, K, dtype, "nk", gated, act, bias, residual, out)
+
+
+@pytest.mark.parametrize("M,N,K,dtype,layout,gated", [
+    (4096, 2048, 2048, "bf16", "kn", False), (3001, 1501, 1040, "bf16", "nk", False), (2050, 1030, 2048, "f8", "nk", True),
+    (1500, 4104, 648, "bf16", "kn", True), (5000, 300, 256, "f8", "nk", False), (1, 16384, 8192, "bf16", "nk", False)])
+def test_larger(gdn, M, N, K, dtype, layout, gated):
+    _run(gdn, M, N, K, dtype, layout, gated, "silu" if gated else "none", residual=True)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 128, 128), (300, 264, 192)])
+@pytest.mark.parametrize("dtype", ["bf16", "f8"])
+def test_tensor_cores_agree_with_ffma(gdn, M, N, K, dtype):
+    _run(gdn, M, N, K, dtype, "nk", True, "gelu", True, True, force_ffma=True)
+
+
+@pytest.mark.parametrize("which", ["x", "weight"])
+@pytest.mark.parametrize("dtype", ["bf16", "f8"])
+def test_unaligned_operands(gdn, which, dtype):
+    """An operand one element past a 16-byte boundary."""
+    t = _draw(40, 96, 128, dtype, "nk", False, False, False, "bf16", seed=2)
+    b = torch.empty(t[which].numel() + 1, dtype=t[which].dtype, device="cuda")
+    b[1:].view(t[which].shape).copy_(t[which])
+    t[which] = b[1:].view(t[which].shape)
+    got = gdn.linear(t["x"], t["weight"], weight_layout="nk", x_scale=t["x_scale"], weight_scale=t["weight_scale"])
+    torch.cuda.synchronize()
+    _check(got, t, "none", "nk", False)
+
+
+@pytest.mark.parametrize("M", [1, 100, 1000])
+@pytest.mark.parametrize("dtype", ["bf16", "f8"])
+def test_nan_and_infinity_stay_in_their_rows_and_columns(gdn, M, dtype):
+    """A NaN in a token's row makes that row NaN and no other; one in a weight column that column;
+    an infinity (a NaN in e4m3) too.  Nothing of a padded tile leaks into what is written."""
+    N, K = 72, 80
+    t = _draw(M, N, K, dtype, "nk", False, False, False, "bf16", seed=4)
+    i, j = M // 2, 41
+    t["x"].view(torch.uint8 if dtype == "f8" else torch.int16)[i, K - 1] = 0x7F if dtype == "f8" else 0x7FC0
+    t["weight"].view(torch.uint8 if dtype == "f8" else torch.int16)[j, 0] = 0x7F if dtype == "f8" else 0x7F80
+    got = gdn.linear(t["x"], t["weight"], weight_layout="nk", x_scale=t["x_scale"], weight_scale=t["weight_scale"]).float()
+    assert got[i].isnan().all()
+    rest = torch.ones(M, N, dtype=torch.bool, device="cuda")
+    rest[i] = False
+    rest[:, j] = False
+    assert got[rest].isfinite().all()
+    col = torch.cat([got[:i, j], got[i + 1:, j]])
+    assert not col.isfinite().any()
+
+
+def test_activations_at_their_ends(gdn):
+    """Sums of +-200 and of +-infinity through every activation, against the formulas' limits."""
+    x = torch.tensor([[200.0], [-200.0], [float("inf")], [float("-inf")]], device="cuda")
+    w = torch.ones(1, 1, device="cuda")
+    r = {a: gdn.linear(x, w, activation=a).flatten().tolist() for a in ("none", "silu", "gelu", "relu")}
+    inf = float("inf")
+    assert r["none"] == [200.0, -200.0, inf, -inf] and r["relu"] == [200.0, 0.0, inf, 0.0]
+    assert r["silu"][0] == 200.0 and abs(r["silu"][1]) < 1e-30 and r["silu"][2] == inf
+    assert r["gelu"][0] == 200.0 and abs(r["gelu"][1]) < 1e-30 and r["gelu"][2] == inf
+
+
+def test_in_place_residual_leading_dims_and_streams(gdn):
+    t = _draw(6 * 35, 512, 256, "bf16", "kn", False, True, True, "bf16", seed=8)
+    ref = gdn.linear(t["x"], t["weight"], t["bias"], t["residual"], activation="silu")
+    x, r = t["x"].view(6, 35, 256), t["residual"].view(6, 35, 512).clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = gdn.linear(x, t["weight"], t["bias"], r, activation="silu", out=r, stream=s)
+    s.synchronize()
+    assert out is r and torch.equal(r.view(-1, 512), ref)
+    assert gdn.linear(x[0, 0].contiguous(), t["weight"]).shape == (512,)
+    assert gdn.linear(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"), t["weight"]).shape == (0, 512)
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(1, 2048, 4096, "bf16"), (64, 2048, 2048, "f8"), (1111, 1024, 512, "bf16")])
+def test_repeats_bit_for_bit(gdn, M, N, K, dtype):
+    t = _draw(M, N, K, dtype, "nk", False, False, False, "f32", seed=1)
+    f = lambda: gdn.linear(t["x"], t["weight"], weight_layout="nk", x_scale=t["x_scale"],  # noqa: E731
+                           weight_scale=t["weight_scale"], out_dtype=torch.float32)
+    a = f()
+    for _ in range(5):
+        assert torch.equal(a, f())
+
+
+def test_refusals(gdn):
+    bf = torch.bfloat16
+    x, w = torch.zeros(4, 64, dtype=bf, device="cuda"), torch.zeros(64, 32, dtype=bf, device="cuda")
+    for bad in (dict(weight_layout="mn"), dict(activation="tanh"), dict(x_scale=torch.ones(4, device="cuda")),
+                dict(bias=torch.zeros(31, device="cuda")), dict(residual=torch.zeros(4, 31, dtype=bf, device="cuda")),
+                dict(out=torch.zeros(4, 31, dtype=bf, device="cuda")), dict(weight=w.t()), dict(weight=w[:32].contiguous()),
+                dict(weight=w.cpu())):
+        with pytest.raises(ValueError):
+            gdn.linear(**dict(dict(x=x, weight=w), **bad))
+    for bad in (dict(weight=w.float()), dict(bias=torch.zeros(32, dtype=bf, device="cuda")),
+                dict(residual=torch.zeros(4, 32, device="cuda")), dict(x=x.half(), weight=w.half())):
+        with pytest.raises(TypeError):
+            gdn.linear(**dict(dict(x=x, weight=w), **bad))
+    with pytest.raises(ValueError):
+        gdn.linear_gated(x, torch.zeros(64, 31, dtype=bf, device="cuda"))
+    x8, w8 = x.to(torch.float8_e4m3fn), torch.zeros(32, 64, device="cuda").to(torch.float8_e4m3fn)
+    with pytest.raises(ValueError):
+        gdn.linear(x8, w8, weight_layout="nk")                       # scales are missing
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.linear(x8, w8.t().contiguous(), weight_layout="kn", x_scale=torch.ones(4, device="cuda"),
+                   weight_scale=torch.ones(32, device="cuda"))
+    assert e.value.code == gdn.GDN_ERR_UNSUPPORTED
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.linear(x.float(), w.float(), out_dtype=bf)
+    assert e.value.code == gdn.GDN_ERR_UNSUPPORTED
