@@ -154,6 +154,7 @@ extern "C" gdn_status gdn_linear(const void* x, const float* x_scale, const void
                        d->activation, d->out_dtype == GDN_F32, (d->flags & GDN_LINEAR_GATED) != 0,
                        (d->flags & GDN_LINEAR_WEIGHT_NK) != 0};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!(d->flags & GDN_LINEAR_FORCE_FFMA) && linear_tc_supported(a, d->dtype)) return launch_linear_tc(a, d->dtype, s);
     const cudaError_t e = d->dtype == GDN_F32    ? launch_ffma<float>(a, s)
                           : d->dtype == GDN_BF16 ? launch_ffma<__nv_bfloat16>(a, s)
                                                  : launch_ffma<__nv_fp8_e4m3>(a, s);

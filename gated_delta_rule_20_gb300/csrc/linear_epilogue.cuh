@@ -5,8 +5,8 @@
 
 #include <cuda_bf16.h>
 
-#include "gdn.h"
 #include "gdn_device.cuh"
+#include "gdn_internal.h"
 
 namespace gdn {
 
@@ -24,6 +24,11 @@ struct LinearArgs {
     bool gated;
     bool nk;       // weight layout
 };
+
+// The tensor-core kernels (linear_tc.cu): whether the operands' alignment and types allow them,
+// and the launch.
+bool linear_tc_supported(const LinearArgs& a, int32_t dtype);
+gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, cudaStream_t s);
 
 __device__ __forceinline__ float activate(int act, float v) {
     switch (act) {  // uniform over the grid

@@ -1,0 +1,312 @@
+// linear_tc.cu -- gdn_linear on the tensor cores (bf16, and e4m3 with scales): tcgen05 with
+// fp32 accumulators in TMEM, operands by TMA.
+//
+// Both kernels issue the product transposed, D^T[n][m] = sum_k W[n][k] x[m][k]: 128 weight
+// columns n lie on the MMA's M axis (TMEM lanes), the tokens m on its N axis.  So one token
+// costs 16 MMA columns instead of 128 rows, a thread of the epilogue has one n (its bias and
+// weight scale are registers), and a warp's stores of a token are 32 neighbouring outputs in
+// any N, with no staging.  Gated, a CTA's 128 rows are 64 of the gate and the 64 of the up
+// half that belong to them (two TMA boxes), so both factors of an output meet in the CTA.
+//
+// A slab is 128 bytes of K (64 bf16, 128 e4m3): the widest 128-byte-swizzled tile row.  W comes
+// K-major ([N, K]) or, bf16 only, MN-major ([K, N], boxes of 64 columns); x K-major.  Boxes read
+// zero past the edges, so ragged M, N and K need no other care than not storing past M and N.
+//
+// linear_small_kernel (few tokens; bound by the weight's bytes): one CTA per 128 columns, K
+// split over a cluster of up to 8 CTAs so that the weight streams through every SM; the partial
+// sums meet in shared memory, are added in the ranks' order (the same result every time) and leave
+// through the epilogue of the rank that owns the token.
+//
+// linear_large_kernel (many tokens; bound by the tensor cores): persistent CTA pairs
+// (cta_group::2) on tiles of 256 columns x up to 256 tokens; every CTA loads its 128 columns and
+// half of the tokens.  Two accumulators in TMEM: the epilogue of one tile runs beside the next
+// tile's products.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "gdn_internal.h"
+#include "linear_epilogue.cuh"
+#include "sm100_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+using namespace ptx;
+
+constexpr int kSlabBytes = 128;                  // bytes of K a stage
+constexpr uint32_t kWBytes = 128 * kSlabBytes;   // a CTA's 128 weight columns of a slab
+constexpr uint32_t kHalfW = kWBytes / 2;         // one box of 64
+constexpr int kMaxStages = 12;
+
+struct TcArgs {
+    LinearArgs a;
+    int slabs, stages, bn;          // bn: MMA N (tokens of a tile)
+    uint32_t stage_bytes, tmem_cols, idesc;
+    int splits;                     // small kernel: K splits (cluster size)
+    int tiles_n, tiles_m, group;    // large kernel: the tile grid, n tiles walked together
+    int32_t* status;
+};
+
+struct SmallBars {
+    uint64_t full[kMaxStages], empty[kMaxStages], done;
+    uint32_t tmem;
+    int abort;
+};
+
+// The four 32-byte steps of K of one slab.  KN: W is MN-major (boxes of 64 columns, 2048 bytes a step).
+template <bool F8, bool KN, bool PAIR>
+__device__ __forceinline__ void mma_slab(uint32_t tmem, uint32_t stage, uint32_t idesc, bool first) {
+    const uint64_t dw = KN ? make_sdesc(stage, kHalfW, 1024) : make_sdesc(stage, 16, 1024);
+    const uint64_t dx = make_sdesc(stage + kWBytes, 16, 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        mma_step<F8, PAIR>(tmem, sdesc_add(dw, k * (KN ? 2048 : 32)), sdesc_add(dx, k * 32), idesc, !first || k > 0);
+}
+
+template <bool F8, bool KN>
+__global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
+                                                           const __grid_constant__ CUtensorMap tm_x,
+                                                           const __grid_constant__ TcArgs t) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const LinearArgs& a = t.a;
+    constexpr int kSlabElems = F8 ? 128 : 64;
+    const int stages = t.stages;
+    SmallBars* bars = reinterpret_cast<SmallBars*>(sm + stages * t.stage_bytes);
+    volatile int* abort_flag = &bars->abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = t.splits > 1 ? (int)cluster_rank() : 0;
+    const int n0 = ((int)blockIdx.x / t.splits) * (a.gated ? 64 : 128);  // outputs of this tile
+    const int n1 = a.gated ? a.N + n0 : n0 + 64;                         // weight column of the second box
+    const int m0 = (int)blockIdx.y * t.bn;
+    const int k_lo = (int)((long long)t.slabs * rank / t.splits), k_hi = (int)((long long)t.slabs * (rank + 1) / t.splits);
+
+    if (tid == 0) {
+        tma_prefetch_desc(&tm_w);
+        tma_prefetch_desc(&tm_x);
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        mbar_init(&bars->done, 1);
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars->tmem, t.tmem_cols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {  // TMA producer
+            int loaded = 0;
+            for (int i = 0; i < k_hi - k_lo; ++i) {
+                const int s = i % stages, k = (k_lo + i) * kSlabElems;
+                if (i >= stages && !mbar_wait_or_abort(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) break;
+                uint8_t* st = sm + s * t.stage_bytes;
+                mbar_arrive_expect_tx(&bars->full[s], t.stage_bytes);
+                tma_load_3d(st, &tm_w, &bars->full[s], KN ? n0 : k, KN ? k : n0, 0);
+                tma_load_3d(st + kHalfW, &tm_w, &bars->full[s], KN ? n1 : k, KN ? k : n1, 0);
+                tma_load_3d(st + kWBytes, &tm_x, &bars->full[s], k, m0, 0);
+                loaded = i + 1;
+            }
+            // every issued load has landed before the CTA can exit (bounded)
+            for (int i = (loaded > stages ? loaded - stages : 0); i < loaded; ++i)
+                (void)mbar_wait(&bars->full[i % stages], (i / stages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {  // MMA issuer
+            int issued = 0;
+            for (int i = 0; i < k_hi - k_lo; ++i) {
+                const int s = i % stages;
+                if (!mbar_wait_or_abort(&bars->full[s], (i / stages) & 1, abort_flag)) break;
+                tc_fence_after();
+                mma_slab<F8, KN, false>(tmem, smem_u32(sm) + s * t.stage_bytes, t.idesc, i == 0);
+                mma_commit(&bars->empty[s]);
+                issued = i + 1;
+            }
+            if (issued == k_hi - k_lo)
+                mma_commit(&bars->done);
+            else if (issued > 0)
+                (void)mbar_wait(&bars->empty[(issued - 1) % stages], ((issued - 1) / stages) & 1);
+        }
+    }
+    __syncwarp();
+    // The partial sums of this CTA's K range, [token][128 columns] over the stages (all of them read).
+    float* part = reinterpret_cast<float*>(sm);
+    const int cols = min(t.bn, a.M - m0);
+    const int e = tid - 64;  // epilogue thread
+    bool ok = false;
+    if (warp >= 2) {
+        ok = mbar_wait_or_abort(&bars->done, 0, abort_flag);
+        tc_fence_after();
+        if (ok) {
+            const int row = (warp & 3) * 32 + lane;
+            for (int c0 = 0; c0 < cols; c0 += 8) {
+                float v[8];
+                tmem_ld8(tmem + ((uint32_t)(row & ~31) << 16) + c0, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c0 + j < cols) part[(c0 + j) * 128 + row] = v[j];
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (t.splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (ok) {
+        const int per = a.gated ? 64 : 128;  // outputs of a token
+        const int n = n0 + e % per;
+        const uint32_t at = smem_u32(part) + (e % per) * 4;
+        for (int c = rank + t.splits * (e / per); c < cols; c += t.splits * (128 / per)) {
+            const int m = m0 + c;
+            float g[8], u[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                const uint32_t p = q < t.splits ? map_to_rank(at + c * 512, q) : 0;
+                g[q] = q < t.splits ? ld_cluster_f32(p) : 0.f;
+                u[q] = a.gated && q < t.splits ? ld_cluster_f32(p + 256) : 0.f;
+            }
+            if (n >= a.N) continue;
+#pragma unroll
+            for (int q = 1; q < 8; ++q) {  // the ranks' order
+                g[0] += g[q];
+                u[0] += u[q];
+            }
+            float v = activate(a.act, affine(a, g[0], m, n));
+            if (a.gated) v *= affine(a, u[0], m, a.N + n);
+            const long long i = (long long)m * a.N + n;
+            store_out(a, i, a.res ? v + load_out(a, i) : v);
+        }
+    }
+    __syncwarp();
+    // a CTA's shared memory stays until every rank has read it
+    if (t.splits > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+    if (tid == 0 && bars->abort) atomicExch(t.status, (int32_t)GDN_ERR_TIMEOUT);
+    if (warp == 1) tmem_dealloc(tmem, t.tmem_cols);
+}
+
+// ------------------------------------------------------------------ host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encoder() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// A [rows][cols] matrix (cols contiguous) in boxes of 128 bytes x box_rows with the 128-byte
+// swizzle; what lies outside reads as zero.
+bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long long cols, int box_rows) {
+    EncodeTiledFn enc = encoder();
+    if (!enc) return false;
+    const cuuint64_t size = f8 ? 1 : 2;
+    cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+    cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)rows * cols * size};
+    cuuint32_t box[3] = {(cuuint32_t)(kSlabBytes / size), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    return enc(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr),
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kSmemLimit = 227 * 1024;
+
+template <typename F>
+cudaError_t allow_smem(F* kernel) {  // once an instantiation (the attribute belongs to the function and device)
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+}
+
+template <bool F8, bool KN>
+cudaError_t launch_small(TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
+                         cudaStream_t s) {
+    cudaError_t e = allow_smem(linear_small_kernel<F8, KN>);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m);
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)t.splits;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = t.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, linear_small_kernel<F8, KN>, tw, tx, t);
+}
+
+gdn_status run_small(const LinearArgs& a, bool f8, int sms, cudaStream_t s) {
+    TcArgs t{};
+    t.a = a;
+    const int elems = f8 ? 128 : 64, per = a.gated ? 64 : 128;
+    t.slabs = (a.K + elems - 1) / elems;
+    t.bn = a.M >= 128 ? 128 : (a.M + 15) / 16 * 16;
+    const int tiles = (int)(((long long)a.N + per - 1) / per), tiles_m = (a.M + t.bn - 1) / t.bn;
+    // Two CTAs an SM (100 KB each): splits as long as they all run at once and have 4 slabs each.
+    t.splits = 1;
+    while (t.splits < 8 && (long long)tiles * tiles_m * t.splits * 2 <= 2LL * sms && t.slabs >= t.splits * 2 * 4)
+        t.splits *= 2;
+    t.stage_bytes = kWBytes + t.bn * kSlabBytes;
+    t.stages = (int)((100 * 1024 - sizeof(SmallBars) - 1024) / t.stage_bytes);
+    if (t.stages > kMaxStages) t.stages = kMaxStages;
+    t.tmem_cols = 32;
+    while (t.tmem_cols < (uint32_t)t.bn) t.tmem_cols <<= 1;
+    t.idesc = f8 ? make_idesc_e4m3(128, t.bn) : make_idesc_bf16(128, t.bn, a.nk ? 0 : 1, 0);
+    gdn_status st = status_word_for_current_device(&t.status);
+    if (st != GDN_OK) return st;
+    CUtensorMap tw, tx;
+    const long long wn = a.gated ? 2LL * a.N : a.N;
+    if (!encode(&tw, f8, a.w, a.nk ? wn : a.K, a.nk ? a.K : wn, 64) || !encode(&tx, f8, a.x, a.M, a.K, t.bn))
+        return GDN_ERR_CUDA;
+    const size_t smem = (size_t)t.stages * t.stage_bytes + sizeof(SmallBars) + 1024;
+    const cudaError_t e = f8     ? launch_small<true, false>(t, tw, tx, tiles, tiles_m, smem, s)
+                          : a.nk ? launch_small<false, false>(t, tw, tx, tiles, tiles_m, smem, s)
+                                 : launch_small<false, true>(t, tw, tx, tiles, tiles_m, smem, s);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+bool linear_tc_supported(const LinearArgs& a, int32_t dtype) {
+    if (dtype != GDN_BF16 && dtype != GDN_F8E4M3) return false;
+    const long long size = dtype == GDN_BF16 ? 2 : 1, wn = a.gated ? 2LL * a.N : a.N;
+    if (((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15u) || a.K * size % 16) return false;
+    if (!a.nk && wn * size % 16) return false;
+    // the up half's boxes of a [K, 2 N] weight start at column N, which TMA wants on 16 bytes
+    return a.nk || !a.gated || a.N * size % 16 == 0;
+}
+
+gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return GDN_ERR_CUDA;
+    return run_small(a, dtype == GDN_F8E4M3, sms, s);
+}
+
+}  // namespace gdn
