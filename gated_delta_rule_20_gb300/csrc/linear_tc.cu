@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
     const int e = tid - 64;  // epilogue thread
     bool ok = false;
     if (warp >= 2) {
-        ok = mbar_wait_or_abort(&bars->done, 0, abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->done, 0, abort_flag));  // one answer a warp
         tc_fence_after();
         if (ok) {
             const int row = (warp & 3) * 32 + lane;
@@ -198,6 +198,236 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
         __syncthreads();
     if (tid == 0 && bars->abort) atomicExch(t.status, (int32_t)GDN_ERR_TIMEOUT);
     if (warp == 1) tmem_dealloc(tmem, t.tmem_cols);
+}
+
+// ------------------------------------------------------------------ many tokens
+constexpr int kLargeStages = 10;
+constexpr int kEpiWarps = 8;                       // two a TMEM lane quadrant, half of the columns each
+constexpr int kLargeThreads = 64 + 32 * kEpiWarps;
+constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 directions x 16 tokens
+
+struct LargeBars {
+    uint64_t full[kLargeStages], empty[kLargeStages];  // full: the leader's are used
+    uint64_t acc_full[2], acc_empty[2];                // acc_empty: the leader's are used
+    uint32_t tmem;
+    int abort;
+};
+
+// The tile of a pair's turn: n tiles walk in groups of t.group, tokens inside a group, so that the
+// tiles that run at once share weights and tokens in L2.
+__device__ __forceinline__ void tile_at(const TcArgs& t, int i, int* n, int* m) {
+    const int g = i / (t.group * t.tiles_m), in = i - g * t.group * t.tiles_m;
+    const int width = min(t.group, t.tiles_n - g * t.group);
+    *m = in / width;
+    *n = g * t.group + in - *m * width;
+}
+
+// 32 tokens of one output column n in registers -> activation, gate, residual, store.  `u` null: not gated.
+template <int C>
+__device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const float* u, int m0, int n, bool live) {
+    float r[C];
+    if (a.res) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) r[j] = live && m0 + j < a.M ? load_out(a, (long long)(m0 + j) * a.N + n) : 0.f;
+    }
+    switch (a.act) {
+        case GDN_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_SILU, v[j]);
+            break;
+        case GDN_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_GELU, v[j]);
+            break;
+        case GDN_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_RELU, v[j]);
+            break;
+    }
+    if (u) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) v[j] *= u[j];
+    }
+    if (a.res) {
+#pragma unroll
+        for (int j = 0; j < C; ++j) v[j] += r[j];
+    }
+    if (!live) return;
+    const long long at = (long long)m0 * a.N + n;
+    const int rows = a.M - m0;
+    if (a.out_f32) {
+        float* o = static_cast<float*>(a.out) + at;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            if (j < rows) o[(long long)j * a.N] = v[j];
+    } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+            if (j < rows) o[(long long)j * a.N] = __float2bfloat16_rn(v[j]);
+    }
+}
+
+template <bool F8, bool KN>
+__global__ void __launch_bounds__(kLargeThreads, 1)
+    linear_large_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ TcArgs t) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const LinearArgs& a = t.a;
+    constexpr int kSlabElems = F8 ? 128 : 64;
+    const int stages = t.stages;
+    float* swap = reinterpret_cast<float*>(sm + stages * t.stage_bytes);
+    LargeBars* bars = reinterpret_cast<LargeBars*>(sm + stages * t.stage_bytes + (a.gated ? kSwapBytes : 0));
+    volatile int* abort_flag = &bars->abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)cluster_rank();
+    const int tiles = t.tiles_n * t.tiles_m, pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
+    const int per = a.gated ? 64 : 128;  // outputs of a CTA
+
+    if (tid == 0) {
+        tma_prefetch_desc(&tm_w);
+        tma_prefetch_desc(&tm_x);
+        for (int s = 0; s < stages; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
+        }
+        bars->abort = 0;
+        fence_mbar_init();
+    }
+    __syncwarp();
+    if (warp == 1) tmem_alloc_pair(&bars->tmem, t.tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the peer's barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {  // TMA producer: this CTA's columns and its half of the tokens
+            int i = 0;    // slabs loaded
+            bool live = true;
+            for (int tile = pair; tile < tiles && live; tile += pairs) {
+                int tn, tm;
+                tile_at(t, tile, &tn, &tm);
+                const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? a.N + n0 : n0 + 64;
+                const int m0 = tm * t.bn + rank * (t.bn / 2);
+                for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i) {
+                    const int s = i % stages;
+                    if (i >= stages && !mbar_wait_or_abort(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) {
+                        live = false;
+                        break;
+                    }
+                    uint8_t* st = sm + s * t.stage_bytes;
+                    if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * t.stage_bytes);
+                    const uint32_t bar = map_to_rank(smem_u32(&bars->full[s]), 0);
+                    tma_load_3d_pair(st, &tm_w, bar, KN ? n0 : k, KN ? k : n0, 0);
+                    tma_load_3d_pair(st + kHalfW, &tm_w, bar, KN ? n1 : k, KN ? k : n1, 0);
+                    tma_load_3d_pair(st + kWBytes, &tm_x, bar, k, m0, 0);
+                }
+            }
+            // the leader sees both CTAs' loads land before the pair can exit (bounded)
+            if (rank == 0)
+                for (int j = (i > stages ? i - stages : 0); j < i; ++j) (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {  // MMA issuer of the pair
+            int i = 0, turn = 0;
+            bool live = true;
+            for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
+                const int b = turn & 1;
+                if (turn >= 2 && !mbar_wait_or_abort(&bars->acc_empty[b], ((turn >> 1) - 1) & 1, abort_flag)) break;
+                tc_fence_after();
+                for (int k = 0; k < t.slabs; ++k, ++i) {
+                    const int s = i % stages;
+                    if (!mbar_wait_or_abort(&bars->full[s], (i / stages) & 1, abort_flag)) {
+                        live = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    mma_slab<F8, KN, true>(tmem + b * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, k == 0);
+                    mma_commit_pair(&bars->empty[s]);
+                }
+                if (live) mma_commit_pair(&bars->acc_full[b]);
+            }
+            if (i > 0) (void)mbar_wait(&bars->empty[(i - 1) % stages], ((i - 1) / stages) & 1);  // all products are done
+        }
+    } else {
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const int hc = t.bn / 2;  // this warp's columns: [half * hc, half * hc + hc)
+        const int row = quad * 32 + lane;
+        float* ex = swap + ((quad & 1) + 2 * half) * (2 * 2 * 16 * 32) + lane;
+        const uint32_t pair_bar = 1 + (quad & 1) + 2 * half;
+        int turn = 0, flip = 0;
+        for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
+            const int b = turn & 1;
+            int tn, tm;
+            tile_at(t, tile, &tn, &tm);
+            const int n0 = (tn * 2 + rank) * per;
+            // this thread's weight column and the output that it belongs to
+            const int n = n0 + (a.gated ? row & 63 : row);
+            const int col = a.gated && row >= 64 ? a.N + n : n;
+            const bool live = n < a.N;
+            const float ws = a.w_scale && live ? a.w_scale[col] : 1.f;
+            const float bias = a.bias && live ? a.bias[col] : 0.f;
+            const int m_lo = tm * t.bn + half * hc;
+            const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag));
+            // one answer for both warps of a gated pair, which meet at a barrier below
+            if (a.gated ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
+            tc_fence_after();
+            const uint32_t src = tmem + b * t.bn + half * hc + ((uint32_t)(quad * 32) << 16);
+            for (int c = 0; c < hc; c += 32) {
+                const int m0 = m_lo + c;
+                float v[32];
+                tmem_ld32(src + c, v);
+                tmem_wait_ld();
+                if (c + 32 >= hc) {  // the accumulator is read: the next product may overwrite it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&bars->acc_empty[b]), 0));
+                }
+                if (a.x_scale) {
+                    const float mine = m0 + lane < a.M ? a.x_scale[m0 + lane] : 0.f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= __shfl_sync(0xffffffffu, mine, j) * ws;
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += bias;
+                if (!a.gated) {
+                    finish<32>(a, v, nullptr, m0, n, live);
+                } else {
+                    // gate rows (quadrants 0, 1) finish the chunk's first 16 tokens, up rows the last 16:
+                    // each sends the other its factor of them
+                    const bool up = quad >= 2;
+                    float* box = ex + flip * (2 * 16 * 32);
+                    flip ^= 1;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) box[(up * 16 + j) * 32] = up ? v[j] : v[16 + j];
+                    named_bar_sync(pair_bar, 64);
+                    float g[16], w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float other = box[((up ^ 1) * 16 + j) * 32];
+                        g[j] = up ? other : v[j];
+                        w[j] = up ? v[16 + j] : other;
+                    }
+                    finish<16>(a, g, w, m0 + (up ? 16 : 0), n, live);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (tid == 0 && bars->abort) atomicExch(t.status, (int32_t)GDN_ERR_TIMEOUT);
+    __syncwarp();
+    if (warp == 1) tmem_dealloc_pair(tmem, t.tmem_cols);
+    cluster_sync();  // neither CTA exits while the pair's TMEM is being freed
 }
 
 // ------------------------------------------------------------------ host side
@@ -290,6 +520,65 @@ gdn_status run_small(const LinearArgs& a, bool f8, int sms, cudaStream_t s) {
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+template <bool F8, bool KN>
+cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int pairs, size_t smem,
+                         cudaStream_t s) {
+    cudaError_t e = allow_smem(linear_large_kernel<F8, KN>);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.blockDim = dim3(kLargeThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, linear_large_kernel<F8, KN>, tw, tx, t);
+}
+
+gdn_status run_large(const LinearArgs& a, bool f8, int sms, cudaStream_t s) {
+    TcArgs t{};
+    t.a = a;
+    const int elems = f8 ? 128 : 64, per = a.gated ? 128 : 256;
+    t.slabs = (a.K + elems - 1) / elems;
+    t.tiles_n = (int)(((long long)a.N + per - 1) / per);
+    // The widest token tile that leaves the least work to the busiest pair.
+    long long best = 0;
+    for (int bn = 256; bn >= 64; bn /= 2) {
+        const long long tiles = (long long)t.tiles_n * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
+        const long long cost = turns * (bn + 32);
+        if (bn == 256 || cost < best) {
+            best = cost;
+            t.bn = bn;
+        }
+    }
+    t.tiles_m = (a.M + t.bn - 1) / t.bn;
+    if ((long long)t.tiles_n * t.tiles_m > INT32_MAX - sms) return GDN_ERR_DIMS;
+    t.group = t.tiles_n < 8 ? t.tiles_n : 8;
+    t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
+    const size_t fixed = sizeof(LargeBars) + (a.gated ? kSwapBytes : 0) + 1024;
+    t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
+    if (t.stages > kLargeStages) t.stages = kLargeStages;
+    t.tmem_cols = 2 * t.bn;
+    t.idesc = f8 ? make_idesc_e4m3(256, t.bn) : make_idesc_bf16(256, t.bn, a.nk ? 0 : 1, 0);
+    gdn_status st = status_word_for_current_device(&t.status);
+    if (st != GDN_OK) return st;
+    CUtensorMap tw, tx;
+    const long long wn = a.gated ? 2LL * a.N : a.N;
+    if (!encode(&tw, f8, a.w, a.nk ? wn : a.K, a.nk ? a.K : wn, 64) || !encode(&tx, f8, a.x, a.M, a.K, t.bn / 2))
+        return GDN_ERR_CUDA;
+    const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
+    const int tiles = t.tiles_n * t.tiles_m, pairs = tiles < sms / 2 ? tiles : sms / 2;
+    const cudaError_t e = f8     ? launch_large<true, false>(t, tw, tx, pairs, smem, s)
+                          : a.nk ? launch_large<false, false>(t, tw, tx, pairs, smem, s)
+                                 : launch_large<false, true>(t, tw, tx, pairs, smem, s);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 }  // namespace
 
 bool linear_tc_supported(const LinearArgs& a, int32_t dtype) {
@@ -306,6 +595,7 @@ gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, cudaStream_t s) 
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         return GDN_ERR_CUDA;
+    if (a.M > 128) return run_large(a, dtype == GDN_F8E4M3, sms, s);
     return run_small(a, dtype == GDN_F8E4M3, sms, s);
 }
 
