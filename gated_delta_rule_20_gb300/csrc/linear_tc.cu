@@ -104,39 +104,40 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
 
-    if (warp == 0) {
-        if (lane == 0) {  // TMA producer
-            int loaded = 0;
-            for (int i = 0; i < k_hi - k_lo; ++i) {
-                const int s = i % stages, k = (k_lo + i) * kSlabElems;
-                if (i >= stages && !mbar_wait_or_abort(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) break;
-                uint8_t* st = sm + s * t.stage_bytes;
+    if (warp == 0) {  // TMA producer
+        int loaded = 0;
+        for (int i = 0; i < k_hi - k_lo; ++i) {
+            const int s = i % stages, k = (k_lo + i) * kSlabElems;
+            if (i >= stages && !mbar_wait_warp(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) break;
+            uint8_t* st = sm + s * t.stage_bytes;
+            if (elect_one()) {
                 mbar_arrive_expect_tx(&bars->full[s], t.stage_bytes);
                 tma_load_3d(st, &tm_w, &bars->full[s], KN ? n0 : k, KN ? k : n0, 0);
                 tma_load_3d(st + kHalfW, &tm_w, &bars->full[s], KN ? n1 : k, KN ? k : n1, 0);
                 tma_load_3d(st + kWBytes, &tm_x, &bars->full[s], k, m0, 0);
-                loaded = i + 1;
             }
-            // every issued load has landed before the CTA can exit (bounded)
-            for (int i = (loaded > stages ? loaded - stages : 0); i < loaded; ++i)
-                (void)mbar_wait(&bars->full[i % stages], (i / stages) & 1);
+            __syncwarp();
+            loaded = i + 1;
         }
-    } else if (warp == 1) {
-        if (lane == 0) {  // MMA issuer
-            int issued = 0;
-            for (int i = 0; i < k_hi - k_lo; ++i) {
-                const int s = i % stages;
-                if (!mbar_wait_or_abort(&bars->full[s], (i / stages) & 1, abort_flag)) break;
-                tc_fence_after();
+        // every issued load has landed before the CTA can exit (bounded)
+        for (int i = (loaded > stages ? loaded - stages : 0); i < loaded; ++i)
+            (void)mbar_wait(&bars->full[i % stages], (i / stages) & 1);
+    } else if (warp == 1) {  // MMA issuer
+        int issued = 0;
+        for (int i = 0; i < k_hi - k_lo; ++i) {
+            const int s = i % stages;
+            if (!mbar_wait_warp(&bars->full[s], (i / stages) & 1, abort_flag)) break;
+            tc_fence_after();
+            if (elect_one()) {
                 mma_slab<F8, KN, false>(tmem, smem_u32(sm) + s * t.stage_bytes, t.idesc, i == 0);
                 mma_commit(&bars->empty[s]);
-                issued = i + 1;
+                if (i + 1 == k_hi - k_lo) mma_commit(&bars->done);
             }
-            if (issued == k_hi - k_lo)
-                mma_commit(&bars->done);
-            else if (issued > 0)
-                (void)mbar_wait(&bars->empty[(issued - 1) % stages], ((issued - 1) / stages) & 1);
+            __syncwarp();
+            issued = i + 1;
         }
+        if (issued < k_hi - k_lo && issued > 0)  // gave up: what was issued ends first (bounded)
+            (void)mbar_wait(&bars->empty[(issued - 1) % stages], ((issued - 1) / stages) & 1);
     }
     __syncwarp();
     // The partial sums of this CTA's K range, [token][128 columns] over the stages (all of them read).
@@ -222,14 +223,28 @@ __device__ __forceinline__ void tile_at(const TcArgs& t, int i, int* n, int* m) 
     *n = g * t.group + in - *m * width;
 }
 
-// 32 tokens of one output column n in registers -> activation, gate, residual, store.  `u` null: not gated.
+// The residual of tokens m0 .. m0 + C - 1 at column n < N, raw (the last row again past M, which is
+// not stored): independent loads, issued well before they are used.
 template <int C>
-__device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const float* u, int m0, int n, bool live) {
-    float r[C];
-    if (a.res) {
+__device__ __forceinline__ void load_residual(const LinearArgs& a, uint32_t (&r)[C], int m0, int n) {
+    const int last = a.M - 1 - m0;
+    if (last < 0) return;
+    const long long at = (long long)m0 * a.N + n;
+    if (a.out_f32) {
+        const uint32_t* p = static_cast<const uint32_t*>(a.res) + at;
 #pragma unroll
-        for (int j = 0; j < C; ++j) r[j] = live && m0 + j < a.M ? load_out(a, (long long)(m0 + j) * a.N + n) : 0.f;
+        for (int j = 0; j < C; ++j) r[j] = p[(long long)min(j, last) * a.N];
+    } else {
+        const uint16_t* p = static_cast<const uint16_t*>(a.res) + at;
+#pragma unroll
+        for (int j = 0; j < C; ++j) r[j] = (uint32_t)p[(long long)min(j, last) * a.N] << 16;  // bf16 -> fp32 bits
     }
+}
+
+// C tokens of one output column n: activation, gate (u, or null), residual (raw), rounding, store.
+template <int C>
+__device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const float* u, const uint32_t (&r)[C], int m0,
+                                       int n) {
     switch (a.act) {
         case GDN_ACT_SILU:
 #pragma unroll
@@ -250,21 +265,112 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const
     }
     if (a.res) {
 #pragma unroll
-        for (int j = 0; j < C; ++j) v[j] += r[j];
+        for (int j = 0; j < C; ++j) v[j] += __uint_as_float(r[j]);
     }
-    if (!live) return;
     const long long at = (long long)m0 * a.N + n;
     const int rows = a.M - m0;
     if (a.out_f32) {
         float* o = static_cast<float*>(a.out) + at;
+        if (rows >= C) {
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (j < rows) o[(long long)j * a.N] = v[j];
+            for (int j = 0; j < C; ++j) o[(long long)j * a.N] = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                if (j < rows) o[(long long)j * a.N] = v[j];
+        }
     } else {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + at;
+        if (rows >= C) {
 #pragma unroll
-        for (int j = 0; j < C; ++j)
-            if (j < rows) o[(long long)j * a.N] = __float2bfloat16_rn(v[j]);
+            for (int j = 0; j < C; ++j) o[(long long)j * a.N] = __float2bfloat16_rn(v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                if (j < rows) o[(long long)j * a.N] = __float2bfloat16_rn(v[j]);
+        }
+    }
+}
+
+// The epilogue warps of linear_large_kernel: every tile of the pair, 32 tokens at a time.  The first
+// residual values of a tile are loaded before its products are done, the next chunk's before this
+// one's are used.
+template <bool GATED>
+__device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float* swap, uint32_t tmem, int rank, int pair,
+                                         int pairs, int tiles) {
+    constexpr int C = GATED ? 16 : 32;  // tokens of a chunk that this warp finishes
+    const LinearArgs& a = t.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const int hc = t.bn / 2;  // this warp's columns: [half * hc, half * hc + hc)
+    const int row = quad * 32 + lane;
+    // gated: rows 0 .. 63 (quadrants 0, 1) are the gate's, the others the up half's; a warp of each
+    // exchange their factors, gate rows finish a chunk's first 16 tokens and up rows its last 16
+    const bool up = GATED && quad >= 2;
+    const int own = up ? 16 : 0;
+    const uint32_t pair_bar = 1 + (quad & 1) + 2 * half;
+    float* ex = swap + ((quad & 1) + 2 * half) * (2 * 2 * 16 * 32) + lane;
+    volatile int* abort_flag = &bars->abort;
+    const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
+    int turn = 0, flip = 0;
+    for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
+        const int b = turn & 1;
+        int tn, tm;
+        tile_at(t, tile, &tn, &tm);
+        // this thread's weight column and the output that it belongs to
+        const int n = (tn * 2 + rank) * (GATED ? 64 : 128) + (GATED ? row & 63 : row);
+        const int col = up ? a.N + n : n;
+        const bool live = n < a.N;
+        const float ws = a.w_scale && live ? a.w_scale[col] : 1.f;
+        const float bias = a.bias && live ? a.bias[col] : 0.f;
+        const int m_lo = tm * t.bn + half * hc;
+        uint32_t res[C];
+        if (a.res && live) load_residual<C>(a, res, m_lo + own, n);
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag));
+        // one answer for both warps of a gated pair, which meet at a barrier below
+        if (GATED ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
+        tc_fence_after();
+        const uint32_t src = tmem + b * t.bn + half * hc + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+        for (int c = 0; c < hc; c += 32) {
+            const int m0 = m_lo + c;
+            float v[32];
+            tmem_ld32(src + c, v);
+            uint32_t r[C];
+#pragma unroll
+            for (int j = 0; j < C; ++j) r[j] = res[j];
+            if (a.res && live && c + 32 < hc) load_residual<C>(a, res, m0 + 32 + own, n);
+            tmem_wait_ld();
+            if (c + 32 >= hc) {  // the accumulator is read: the next product may overwrite it
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(b ? done1 : done0);
+            }
+            if (a.x_scale) {
+                const float mine = m0 + lane < a.M ? a.x_scale[m0 + lane] : 0.f;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= __shfl_sync(0xffffffffu, mine, j) * ws;
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] += bias;
+            if constexpr (!GATED) {
+                if (live) finish<32>(a, v, nullptr, r, m0, n);
+            } else {
+                float* box = ex + flip * (2 * 16 * 32);  // used in turns, so that one barrier a chunk is enough
+                flip ^= 1;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) box[(own + j) * 32] = up ? v[j] : v[16 + j];
+                named_bar_sync(pair_bar, 64);
+                float g[16], w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float other = box[((16 - own) + j) * 32];
+                    g[j] = up ? other : v[j];
+                    w[j] = up ? v[16 + j] : other;
+                }
+                if (live) finish<16>(a, g, w, r, m0 + own, n);
+            }
+        }
     }
 }
 
@@ -307,118 +413,63 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
 
-    if (warp == 0) {
-        if (lane == 0) {  // TMA producer: this CTA's columns and its half of the tokens
-            int i = 0;    // slabs loaded
-            bool live = true;
-            for (int tile = pair; tile < tiles && live; tile += pairs) {
-                int tn, tm;
-                tile_at(t, tile, &tn, &tm);
-                const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? a.N + n0 : n0 + 64;
-                const int m0 = tm * t.bn + rank * (t.bn / 2);
-                for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i) {
-                    const int s = i % stages;
-                    if (i >= stages && !mbar_wait_or_abort(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) {
-                        live = false;
-                        break;
-                    }
-                    uint8_t* st = sm + s * t.stage_bytes;
+    if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
+        int i = 0;    // slabs loaded
+        bool live = true;
+        for (int tile = pair; tile < tiles && live; tile += pairs) {
+            int tn, tm;
+            tile_at(t, tile, &tn, &tm);
+            const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? a.N + n0 : n0 + 64;
+            const int m0 = tm * t.bn + rank * (t.bn / 2);
+            for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i) {
+                const int s = i % stages;
+                if (i >= stages && !mbar_wait_warp(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) {
+                    live = false;
+                    break;
+                }
+                uint8_t* st = sm + s * t.stage_bytes;
+                if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * t.stage_bytes);
                     const uint32_t bar = map_to_rank(smem_u32(&bars->full[s]), 0);
                     tma_load_3d_pair(st, &tm_w, bar, KN ? n0 : k, KN ? k : n0, 0);
                     tma_load_3d_pair(st + kHalfW, &tm_w, bar, KN ? n1 : k, KN ? k : n1, 0);
                     tma_load_3d_pair(st + kWBytes, &tm_x, bar, k, m0, 0);
                 }
+                __syncwarp();
             }
-            // the leader sees both CTAs' loads land before the pair can exit (bounded)
-            if (rank == 0)
-                for (int j = (i > stages ? i - stages : 0); j < i; ++j) (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
         }
+        // the leader sees both CTAs' loads land before the pair can exit (bounded)
+        if (rank == 0)
+            for (int j = (i > stages ? i - stages : 0); j < i; ++j) (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {  // MMA issuer of the pair
+        if (rank == 0) {  // MMA issuer of the pair
             int i = 0, turn = 0;
             bool live = true;
             for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
                 const int b = turn & 1;
-                if (turn >= 2 && !mbar_wait_or_abort(&bars->acc_empty[b], ((turn >> 1) - 1) & 1, abort_flag)) break;
+                if (turn >= 2 && !mbar_wait_warp(&bars->acc_empty[b], ((turn >> 1) - 1) & 1, abort_flag)) break;
                 tc_fence_after();
                 for (int k = 0; k < t.slabs; ++k, ++i) {
                     const int s = i % stages;
-                    if (!mbar_wait_or_abort(&bars->full[s], (i / stages) & 1, abort_flag)) {
+                    if (!mbar_wait_warp(&bars->full[s], (i / stages) & 1, abort_flag)) {
                         live = false;
                         break;
                     }
                     tc_fence_after();
-                    mma_slab<F8, KN, true>(tmem + b * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, k == 0);
-                    mma_commit_pair(&bars->empty[s]);
+                    if (elect_one()) {
+                        mma_slab<F8, KN, true>(tmem + b * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, k == 0);
+                        mma_commit_pair(&bars->empty[s]);
+                        if (k + 1 == t.slabs) mma_commit_pair(&bars->acc_full[b]);
+                    }
+                    __syncwarp();
                 }
-                if (live) mma_commit_pair(&bars->acc_full[b]);
             }
             if (i > 0) (void)mbar_wait(&bars->empty[(i - 1) % stages], ((i - 1) / stages) & 1);  // all products are done
         }
+    } else if (a.gated) {
+        epilogue<true>(t, bars, swap, tmem, rank, pair, pairs, tiles);
     } else {
-        const int quad = warp & 3, half = (warp - 2) >> 2;
-        const int hc = t.bn / 2;  // this warp's columns: [half * hc, half * hc + hc)
-        const int row = quad * 32 + lane;
-        float* ex = swap + ((quad & 1) + 2 * half) * (2 * 2 * 16 * 32) + lane;
-        const uint32_t pair_bar = 1 + (quad & 1) + 2 * half;
-        int turn = 0, flip = 0;
-        for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
-            const int b = turn & 1;
-            int tn, tm;
-            tile_at(t, tile, &tn, &tm);
-            const int n0 = (tn * 2 + rank) * per;
-            // this thread's weight column and the output that it belongs to
-            const int n = n0 + (a.gated ? row & 63 : row);
-            const int col = a.gated && row >= 64 ? a.N + n : n;
-            const bool live = n < a.N;
-            const float ws = a.w_scale && live ? a.w_scale[col] : 1.f;
-            const float bias = a.bias && live ? a.bias[col] : 0.f;
-            const int m_lo = tm * t.bn + half * hc;
-            const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag));
-            // one answer for both warps of a gated pair, which meet at a barrier below
-            if (a.gated ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
-            tc_fence_after();
-            const uint32_t src = tmem + b * t.bn + half * hc + ((uint32_t)(quad * 32) << 16);
-            for (int c = 0; c < hc; c += 32) {
-                const int m0 = m_lo + c;
-                float v[32];
-                tmem_ld32(src + c, v);
-                tmem_wait_ld();
-                if (c + 32 >= hc) {  // the accumulator is read: the next product may overwrite it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&bars->acc_empty[b]), 0));
-                }
-                if (a.x_scale) {
-                    const float mine = m0 + lane < a.M ? a.x_scale[m0 + lane] : 0.f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= __shfl_sync(0xffffffffu, mine, j) * ws;
-                }
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += bias;
-                if (!a.gated) {
-                    finish<32>(a, v, nullptr, m0, n, live);
-                } else {
-                    // gate rows (quadrants 0, 1) finish the chunk's first 16 tokens, up rows the last 16:
-                    // each sends the other its factor of them
-                    const bool up = quad >= 2;
-                    float* box = ex + flip * (2 * 16 * 32);
-                    flip ^= 1;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) box[(up * 16 + j) * 32] = up ? v[j] : v[16 + j];
-                    named_bar_sync(pair_bar, 64);
-                    float g[16], w[16];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float other = box[((up ^ 1) * 16 + j) * 32];
-                        g[j] = up ? other : v[j];
-                        w[j] = up ? v[16 + j] : other;
-                    }
-                    finish<16>(a, g, w, m0 + (up ? 16 : 0), n, live);
-                }
-            }
-        }
+        epilogue<false>(t, bars, swap, tmem, rank, pair, pairs, tiles);
     }
     __syncwarp();
     tc_fence_before();

@@ -104,6 +104,23 @@ __device__ __forceinline__ bool mbar_wait_or_abort(uint64_t* bar, uint32_t parit
     return mbar_try_wait(bar, parity) || mbar_wait_or_abort_loop(bar, parity, abort);
 }
 
+// The same wait by a whole (converged) warp, with one answer for all of its lanes.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    return __all_sync(0xffffffffu, mbar_wait_or_abort(bar, parity, abort));
+}
+// One lane of a converged warp, the same one each time.  Code under it may take its operands from
+// uniform registers: single-lane work behind `lane == 0` may not, and there every tcgen05.mma and TMA
+// instruction is issued through a loop over the lanes' values.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // ---------------------------------------------------------------- named barriers
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
