@@ -509,50 +509,58 @@ def decode_block_noalloc(hidden, W_qkv, W_z, W_a, W_b, conv_weight, conv_state, 
 
 
 # ------------------------------------------------------------------ the layer around the block
-_LAYER_DTYPES = None
+# These calls are short (a decode step's norm runs for about 3 us), so the checks are written to cost
+# little: torch's names are looked up once, and an operand is taken apart only when it is refused.
+_T = None          # torch
+_LAYER_CODES = {}  # torch dtype -> gdn_dtype
+_raw_stream = None
 
 
-def _layer_dtype(t, nm: str) -> int:
-    """gdn_dtype of a tensor of the layer operators."""
-    global _LAYER_DTYPES
-    if _LAYER_DTYPES is None:
-        torch = _torch()
-        _LAYER_DTYPES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_F8E4M3}
-    code = _LAYER_DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError("%s must be bfloat16, float32 or float8_e4m3fn, got %s" % (nm, t.dtype))
-    return code
+def _layer_init():
+    global _T, _raw_stream
+    import torch
+    _LAYER_CODES.update({torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_F8E4M3})
+    # the handle of a device's current stream without a Stream object (2 us less), where torch has it
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    lib()
+    _T = torch
 
 
-def _layer_tensor(nm, t, shape, dtype, device):
-    """Checks an operand of the layer operators: on ``device``, contiguous, of that shape and dtype."""
+def _layer_bad(nm, t, shape, dtype, device):
+    """Raises what is wrong with an operand of the layer operators."""
     if t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous CUDA tensor on %s" % (nm, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (nm, dtype, t.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (nm, tuple(shape), tuple(t.shape)))
+    raise ValueError("%s must have shape %s, got %s" % (nm, tuple(shape), tuple(t.shape)))
+
+
+def _layer_ptr(nm, t, shape, dtype, device):
+    """The address of an operand that is on ``device``, contiguous, of that shape and dtype."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        _layer_bad(nm, t, shape, dtype, device)
     return t.data_ptr()
 
 
 def _layer_empty(shape, dtype, device, stream):
     """A new output, allocated on the stream that writes it."""
-    torch = _torch()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _T.empty(shape, dtype=dtype, device=device)
+    with _T.cuda.stream(stream):
+        return _T.empty(shape, dtype=dtype, device=device)
 
 
 def _layer_call(fn, device, stream, *args):
     """Calls an entry point on ``stream`` (default: the device's current one), with the device current."""
-    torch = _torch()
-    handle = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, handle))
-        return
-    with torch.cuda.device(device):
-        _check(fn(*args, handle))
+    handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
+    if device.index == _T.cuda.current_device():
+        code = fn(*args, handle)
+    else:
+        with _T.cuda.device(device):
+            code = fn(*args, handle)
+    if code:
+        _check(code)
 
 
 def rmsnorm_residual(x, norm_weight, residual=None, *, out=None, out_scale=None, residual_out=None, out_dtype=None,
@@ -565,90 +573,116 @@ def rmsnorm_residual(x, norm_weight, residual=None, *, out=None, out_scale=None,
     ``out * out_scale`` stands for the normalised row.  ``residual_out`` (default: a new tensor where
     there is a residual; it may be ``residual``) receives ``h``.  Returns
     ``(out, out_scale, residual_out)``, with None for what the call does not have."""
-    torch = _torch()
+    if _T is None:
+        _layer_init()
     if not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA tensor")
-    dt, shape, device = _layer_dtype(x, "x"), x.shape, x.device
-    if dt == GDN_F8E4M3:
-        raise TypeError("x must be bfloat16 or float32, got %s" % x.dtype)
-    if len(shape) < 1 or shape[-1] < 1:
+    dtype, shape, device = x.dtype, x.shape, x.device
+    code = _LAYER_CODES.get(dtype, GDN_F8E4M3)
+    if code == GDN_F8E4M3:
+        raise TypeError("x must be bfloat16 or float32, got %s" % dtype)
+    if not shape or not shape[-1]:
         raise ValueError("x must be [..., D] with D >= 1")
     D = shape[-1]
-    if out_dtype is None:
-        out_dtype = x.dtype if out is None else out.dtype
+    if out is not None:
+        out_dtype = out.dtype if out_dtype is None else out_dtype
+    elif out_dtype is None:
+        out_dtype = dtype
+    ocode = _LAYER_CODES.get(out_dtype)
+    if ocode != code and ocode != GDN_F8E4M3:
+        raise TypeError("out must have x's dtype or float8_e4m3fn, got %s" % out_dtype)
     if out is None:
         out = _layer_empty(shape, out_dtype, device, stream)
-    odt = _layer_dtype(out, "out")
-    if odt not in (dt, GDN_F8E4M3):
-        raise TypeError("out must have x's dtype or float8_e4m3fn, got %s" % out.dtype)
-    wp = _layer_tensor("norm_weight", norm_weight, (D,), torch.float32, device)
-    op = _layer_tensor("out", out, shape, out_dtype, device)
+        op = out.data_ptr()
+    else:
+        op = _layer_ptr("out", out, shape, out_dtype, device)
+    wp = _layer_ptr("norm_weight", norm_weight, (D,), _T.float32, device)
     sp = rp = hp = None
-    if odt == GDN_F8E4M3:
+    if ocode == GDN_F8E4M3:
         if out_scale is None:
-            out_scale = _layer_empty(shape[:-1], torch.float32, device, stream)
-        sp = _layer_tensor("out_scale", out_scale, shape[:-1], torch.float32, device)
+            out_scale = _layer_empty(shape[:-1], _T.float32, device, stream)
+            sp = out_scale.data_ptr()
+        else:
+            sp = _layer_ptr("out_scale", out_scale, shape[:-1], _T.float32, device)
     elif out_scale is not None:
         raise ValueError("out_scale goes with a float8_e4m3fn out only")
     if residual is not None:
-        rp = _layer_tensor("residual", residual, shape, x.dtype, device)
+        rp = _layer_ptr("residual", residual, shape, dtype, device)
         if residual_out is None:
-            residual_out = _layer_empty(shape, x.dtype, device, stream)
+            residual_out = _layer_empty(shape, dtype, device, stream)
     if residual_out is not None:
-        hp = _layer_tensor("residual_out", residual_out, shape, x.dtype, device)
-    _layer_call(lib().gdn_rmsnorm_residual, device, stream, x.data_ptr(), rp, wp, hp, op, sp, x.numel() // D, D, dt, odt,
-                eps)
+        hp = _layer_ptr("residual_out", residual_out, shape, dtype, device)
+    _layer_call(_lib.gdn_rmsnorm_residual, device, stream, x.data_ptr(), rp, wp, hp, op, sp, x.numel() // D, D, code,
+                ocode, eps)
     return out, out_scale, residual_out
 
 
 def _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weight_scale, out, out_dtype, force_ffma,
-            stream, gated):
-    torch = _torch()
+            stream, flags):
+    if _T is None:
+        _layer_init()
     if not x.is_cuda or not x.is_contiguous():
         raise ValueError("x must be a contiguous CUDA tensor")
-    dt, shape, device = _layer_dtype(x, "x"), x.shape, x.device
-    if weight_layout not in ("kn", "nk"):
-        raise ValueError("weight_layout must be 'kn' or 'nk'")
-    if activation not in ACTIVATIONS:
+    dtype, shape, device = x.dtype, x.shape, x.device
+    code = _LAYER_CODES.get(dtype)
+    if code is None:
+        raise TypeError("x must be bfloat16, float32 or float8_e4m3fn, got %s" % dtype)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
         raise ValueError("activation must be one of %s" % ", ".join(ACTIVATIONS))
-    if len(shape) < 1 or weight.dim() != 2:
+    if not shape or weight.dim() != 2:
         raise ValueError("x must be [..., K] and weight two-dimensional")
     K = shape[-1]
-    flags = (GDN_LINEAR_FORCE_FFMA if force_ffma else 0)
     if weight_layout == "nk":
-        cols, flags, wshape = weight.shape[0], flags | GDN_LINEAR_WEIGHT_NK, (weight.shape[0], K)
+        cols = weight.shape[0]
+        wshape = (cols, K)
+        flags |= GDN_LINEAR_WEIGHT_NK
+    elif weight_layout == "kn":
+        cols = weight.shape[1]
+        wshape = (K, cols)
     else:
-        cols, wshape = weight.shape[1], (K, weight.shape[1])
+        raise ValueError("weight_layout must be 'kn' or 'nk'")
+    if force_ffma:
+        flags |= GDN_LINEAR_FORCE_FFMA
     N = cols
-    if gated:
+    if flags & GDN_LINEAR_GATED:
         if cols % 2:
             raise ValueError("a gated weight has an even number of columns, got %d" % cols)
-        N, flags = cols // 2, flags | GDN_LINEAR_GATED
-    wp = _layer_tensor("weight", weight, wshape, x.dtype, device)
-    if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.float32 if dt == GDN_F32 else torch.bfloat16
-    oshape = shape[:-1] + (N,)
+        N = cols // 2
+    wp = _layer_ptr("weight", weight, wshape, dtype, device)
+    rows = shape[:-1]
+    oshape = rows + (N,)
     if out is None:
+        if out_dtype is None:
+            out_dtype = _T.float32 if code == GDN_F32 else _T.bfloat16
+        elif out_dtype not in _LAYER_CODES:
+            raise TypeError("out must be bfloat16 or float32, got %s" % out_dtype)
         out = _layer_empty(oshape, out_dtype, device, stream)
-    op = _layer_tensor("out", out, oshape, out_dtype, device)
-    odt = _layer_dtype(out, "out")
+        op = out.data_ptr()
+    else:
+        if out_dtype is None:
+            out_dtype = out.dtype
+        op = _layer_ptr("out", out, oshape, out_dtype, device)
+    ocode = _LAYER_CODES.get(out_dtype)
+    if ocode is None:
+        raise TypeError("out must be bfloat16 or float32, got %s" % out_dtype)
     M = 1
-    for n in shape[:-1]:
+    for n in rows:
         M *= n
     xsp = wsp = bp = rp = None
-    if (x_scale is not None or weight_scale is not None) and dt != GDN_F8E4M3:
-        raise ValueError("x_scale and weight_scale go with float8_e4m3fn operands only")
-    if dt == GDN_F8E4M3:
+    if code == GDN_F8E4M3:
         if x_scale is None or weight_scale is None:
             raise ValueError("float8_e4m3fn operands need x_scale and weight_scale")
-        xsp = _layer_tensor("x_scale", x_scale, shape[:-1], torch.float32, device)
-        wsp = _layer_tensor("weight_scale", weight_scale, (cols,), torch.float32, device)
+        xsp = _layer_ptr("x_scale", x_scale, rows, _T.float32, device)
+        wsp = _layer_ptr("weight_scale", weight_scale, (cols,), _T.float32, device)
+    elif x_scale is not None or weight_scale is not None:
+        raise ValueError("x_scale and weight_scale go with float8_e4m3fn operands only")
     if bias is not None:
-        bp = _layer_tensor("bias", bias, (cols,), torch.float32, device)
+        bp = _layer_ptr("bias", bias, (cols,), _T.float32, device)
     if residual is not None:
-        rp = _layer_tensor("residual", residual, oshape, out_dtype, device)
-    dims = GdnLinearDims(M, N, K, dt, odt, ACTIVATIONS[activation], flags)
-    _layer_call(lib().gdn_linear, device, stream, x.data_ptr(), xsp, wp, wsp, bp, rp, op, dims)
+        rp = _layer_ptr("residual", residual, oshape, out_dtype, device)
+    _layer_call(_lib.gdn_linear, device, stream, x.data_ptr(), xsp, wp, wsp, bp, rp, op,
+                GdnLinearDims(M, N, K, code, ocode, act, flags))
     return out
 
 
@@ -660,7 +694,7 @@ def linear(x, weight, bias=None, residual=None, *, activation="none", weight_lay
     ``activation`` "none", "silu", "gelu" (erf) or "relu"; ``out`` and ``residual`` [..., N] in
     ``out_dtype`` (bf16, or fp32; fp32 compute gives fp32); ``out`` may be ``residual``.  Returns ``out``."""
     return _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weight_scale, out, out_dtype,
-                   force_ffma, stream, False)
+                   force_ffma, stream, 0)
 
 
 def linear_gated(x, weight, bias=None, residual=None, *, activation="silu", weight_layout="kn", x_scale=None,
@@ -668,4 +702,4 @@ def linear_gated(x, weight, bias=None, residual=None, *, activation="silu", weig
     """``act(x Wg + bg) * (x Wu + bu) + residual``: ``linear`` with a weight (and bias and
     ``weight_scale``) of 2 N columns, the gate's N first (``GDN_LINEAR_GATED``).  Returns ``out`` [..., N]."""
     return _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weight_scale, out, out_dtype,
-                   force_ffma, stream, True)
+                   force_ffma, stream, GDN_LINEAR_GATED)

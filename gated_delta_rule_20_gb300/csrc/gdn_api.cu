@@ -4,6 +4,7 @@
 // Argument rules follow the "GDN CTE Kernel API Reference" page (Parameters,
 // Notes, Dimensions): Dq == Dk <= 128, Dv <= 128, Hv % Hk == 0, fp32 g_log /
 // beta / state, compute dtype from the query.  A failed check launches nothing.
+#include <atomic>
 #include <cstdint>
 #include <mutex>
 
@@ -15,7 +16,6 @@ namespace {
 // device address is looked up once per device, with that device current.
 __device__ int32_t g_status_word;
 
-constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 int32_t* g_status_addr[kMaxDevices] = {};
 
@@ -31,6 +31,17 @@ gdn_status status_word_for_current_device(int32_t** out) {
         g_status_addr[dev] = static_cast<int32_t*>(p);
     }
     *out = g_status_addr[dev];
+    return GDN_OK;
+}
+
+gdn_status current_device_sms(int* dev, int* sms) {
+    static std::atomic<int> known[kMaxDevices];
+    if (cudaGetDevice(dev) != cudaSuccess || *dev < 0 || *dev >= kMaxDevices) return GDN_ERR_CUDA;
+    *sms = known[*dev].load(std::memory_order_relaxed);
+    if (*sms == 0) {
+        if (cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, *dev) != cudaSuccess) return GDN_ERR_CUDA;
+        known[*dev].store(*sms, std::memory_order_relaxed);
+    }
     return GDN_OK;
 }
 

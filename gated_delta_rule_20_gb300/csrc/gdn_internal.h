@@ -28,6 +28,10 @@ struct Problem {
 // else a gdn_status written by a kernel whose wait gave up).
 gdn_status status_word_for_current_device(int32_t** out);
 
+// The current device and its SM count (looked up once a device).
+gdn_status current_device_sms(int* dev, int* sms);
+constexpr int kMaxDevices = 64;  // devices whose facts are kept
+
 // The argument checks of gdn_prefill, without launching anything.
 gdn_status prefill_checked(const void* q, const void* k, const void* v, const float* g_log, const float* beta,
                            float* state, void* out, const gdn_dims* d);

@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "gdn_internal.h"
@@ -516,15 +517,20 @@ bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long lon
 
 constexpr int kSmemLimit = 227 * 1024;
 
+// The shared-memory limit of a kernel, raised once a device (`done`: that kernel's own marks).
 template <typename F>
-cudaError_t allow_smem(F* kernel) {  // once an instantiation (the attribute belongs to the function and device)
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+cudaError_t allow_smem(F* kernel, std::atomic<bool> (&done)[kMaxDevices], int dev) {
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
 }
 
 template <bool F8, bool KN>
 cudaError_t launch_small(TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
-                         cudaStream_t s) {
-    cudaError_t e = allow_smem(linear_small_kernel<F8, KN>);
+                         int dev, cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];
+    cudaError_t e = allow_smem(linear_small_kernel<F8, KN>, done, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m);
@@ -541,7 +547,7 @@ cudaError_t launch_small(TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx
     return cudaLaunchKernelEx(&cfg, linear_small_kernel<F8, KN>, tw, tx, t);
 }
 
-gdn_status run_small(const LinearArgs& a, bool f8, int sms, cudaStream_t s) {
+gdn_status run_small(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_t s) {
     TcArgs t{};
     t.a = a;
     const int elems = f8 ? 128 : 64, per = a.gated ? 64 : 128;
@@ -565,16 +571,17 @@ gdn_status run_small(const LinearArgs& a, bool f8, int sms, cudaStream_t s) {
     if (!encode(&tw, f8, a.w, a.nk ? wn : a.K, a.nk ? a.K : wn, 64) || !encode(&tx, f8, a.x, a.M, a.K, t.bn))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + sizeof(SmallBars) + 1024;
-    const cudaError_t e = f8     ? launch_small<true, false>(t, tw, tx, tiles, tiles_m, smem, s)
-                          : a.nk ? launch_small<false, false>(t, tw, tx, tiles, tiles_m, smem, s)
-                                 : launch_small<false, true>(t, tw, tx, tiles, tiles_m, smem, s);
+    const cudaError_t e = f8     ? launch_small<true, false>(t, tw, tx, tiles, tiles_m, smem, dev, s)
+                          : a.nk ? launch_small<false, false>(t, tw, tx, tiles, tiles_m, smem, dev, s)
+                                 : launch_small<false, true>(t, tw, tx, tiles, tiles_m, smem, dev, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 template <bool F8, bool KN>
 cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int pairs, size_t smem,
-                         cudaStream_t s) {
-    cudaError_t e = allow_smem(linear_large_kernel<F8, KN>);
+                         int dev, cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];
+    cudaError_t e = allow_smem(linear_large_kernel<F8, KN>, done, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * pairs));
@@ -591,7 +598,7 @@ cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorM
     return cudaLaunchKernelEx(&cfg, linear_large_kernel<F8, KN>, tw, tx, t);
 }
 
-gdn_status run_large(const LinearArgs& a, bool f8, int sms, cudaStream_t s) {
+gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_t s) {
     TcArgs t{};
     t.a = a;
     const int elems = f8 ? 128 : 64, per = a.gated ? 128 : 256;
@@ -624,9 +631,9 @@ gdn_status run_large(const LinearArgs& a, bool f8, int sms, cudaStream_t s) {
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
     const int tiles = t.tiles_n * t.tiles_m, pairs = tiles < sms / 2 ? tiles : sms / 2;
-    const cudaError_t e = f8     ? launch_large<true, false>(t, tw, tx, pairs, smem, s)
-                          : a.nk ? launch_large<false, false>(t, tw, tx, pairs, smem, s)
-                                 : launch_large<false, true>(t, tw, tx, pairs, smem, s);
+    const cudaError_t e = f8     ? launch_large<true, false>(t, tw, tx, pairs, smem, dev, s)
+                          : a.nk ? launch_large<false, false>(t, tw, tx, pairs, smem, dev, s)
+                                 : launch_large<false, true>(t, tw, tx, pairs, smem, dev, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -643,11 +650,10 @@ bool linear_tc_supported(const LinearArgs& a, int32_t dtype) {
 
 gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, cudaStream_t s) {
     int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return GDN_ERR_CUDA;
-    if (a.M > 128) return run_large(a, dtype == GDN_F8E4M3, sms, s);
-    return run_small(a, dtype == GDN_F8E4M3, sms, s);
+    const gdn_status st = current_device_sms(&dev, &sms);
+    if (st != GDN_OK) return st;
+    if (a.M > 128) return run_large(a, dtype == GDN_F8E4M3, dev, sms, s);
+    return run_small(a, dtype == GDN_F8E4M3, dev, sms, s);
 }
 
 }  // namespace gdn

@@ -265,9 +265,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
                            reinterpret_cast<uintptr_t>(a.w);
     const int nv = a.D % V == 0 && (wide & 15u) == 0 ? a.D / V : INT32_MAX;
     int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    if (current_device_sms(&dev, &sms) != GDN_OK) return cudaErrorInvalidDevice;
     if (nv <= 32) return launch_vec<T, O, 32, 1>(a, sms, s);
     if (nv <= 64) return launch_vec<T, O, 32, 2>(a, sms, s);
     if (nv <= 128) return launch_vec<T, O, 32, 4>(a, sms, s);
