@@ -48,6 +48,7 @@ struct TcArgs {
     uint32_t stage_bytes, tmem_cols, idesc;
     int splits;                     // small kernel: K splits (cluster size)
     int tiles_n, tiles_m, group;    // large kernel: the tile grid, n tiles walked together
+    bool staged;                    // large kernel: bf16 output (and residual) by TMA
     int32_t* status;
 };
 
@@ -206,14 +207,21 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
 constexpr int kLargeStages = 10;
 constexpr int kEpiWarps = 8;                       // two a TMEM lane quadrant, half of the columns each
 constexpr int kLargeThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 directions x 16 tokens
+constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 directions x 16 values
+constexpr uint32_t kBoxRow = 64;                   // a staged output row: 32 bf16 columns
 
 struct LargeBars {
     uint64_t full[kLargeStages], empty[kLargeStages];  // full: the leader's are used
     uint64_t acc_full[2], acc_empty[2];                // acc_empty: the leader's are used
+    uint64_t res_full[kEpiWarps][2];                   // staged residual boxes
     uint32_t tmem;
     int abort;
 };
+
+// Shared memory of the staged output boxes: two a warp, of 64 tokens (gated 32) x 32 columns.
+__host__ __device__ inline uint32_t box_bytes(const TcArgs& t) {
+    return t.staged ? kEpiWarps * 2 * (t.a.gated ? 32 : 64) * kBoxRow : 0;
+}
 
 // The tile of a pair's turn: n tiles walk in groups of t.group, tokens inside a group, so that the
 // tiles that run at once share weights and tokens in L2.
@@ -242,11 +250,10 @@ __device__ __forceinline__ void load_residual(const LinearArgs& a, uint32_t (&r)
     }
 }
 
-// C tokens of one output column n: activation, gate (u, or null), residual (raw), rounding, store.
+// The activation of C values (the choice is uniform over the grid).
 template <int C>
-__device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const float* u, const uint32_t (&r)[C], int m0,
-                                       int n) {
-    switch (a.act) {
+__device__ __forceinline__ void activate_all(int act, float (&v)[C]) {
+    switch (act) {
         case GDN_ACT_SILU:
 #pragma unroll
             for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_SILU, v[j]);
@@ -260,6 +267,13 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const
             for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_RELU, v[j]);
             break;
     }
+}
+
+// C tokens of one output column n: activation, gate (u, or null), residual (raw), rounding, store.
+template <int C>
+__device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const float* u, const uint32_t (&r)[C], int m0,
+                                       int n) {
+    activate_all<C>(a.act, v);
     if (u) {
 #pragma unroll
         for (int j = 0; j < C; ++j) v[j] *= u[j];
@@ -293,7 +307,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const
     }
 }
 
-// The epilogue warps of linear_large_kernel: every tile of the pair, 32 tokens at a time.  The first
+// The epilogue warps of linear_large_kernel, for any output: every tile of the pair, 32 tokens at a time.  The first
 // residual values of a tile are loaded before its products are done, the next chunk's before this
 // one's are used.
 template <bool GATED>
@@ -375,17 +389,181 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     }
 }
 
+// The same for bf16 outputs that TMA can store (N a multiple of 8, 16-byte aligned; bn >= 128).  A warp
+// takes units of 64 tokens x its 32 columns.  It reads TMEM in the layout of 8x8 fragments, in which a
+// thread has pairs of neighbouring tokens: packed to bf16, four fragments a stmatrix land transposed,
+// as rows of 64 bytes a token, with an eighth of the shared-memory stores that single elements take and
+// no address arithmetic; one TMA store takes the box away (and clips it to the matrix).  The residual
+// comes the same way back: a TMA load into the box, a unit ahead, and ldmatrix.
+template <bool GATED>
+__device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorMap* tm_out, const CUtensorMap* tm_res,
+                                                LargeBars* bars, uint8_t* boxes, float* swap, uint32_t tmem, int rank,
+                                                int pair, int pairs, int tiles) {
+    constexpr int kTokens = GATED ? 32 : 64;        // tokens of a unit that this warp finishes
+    constexpr int kPieces = kTokens / 8;            // fragments of 8 tokens among them
+    constexpr uint32_t kBoxBytes = kTokens * kBoxRow;
+    const LinearArgs& a = t.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3, half = (warp - 2) >> 2;
+    const bool up = GATED && quad >= 2;
+    const int own = up ? 32 : 0;  // gated: gate rows finish a unit's first 32 tokens, up rows its last 32
+    const uint32_t pair_bar = 1 + (quad & 1) + 2 * half;
+    float* ex = swap + ((quad & 1) + 2 * half) * (2 * 2 * 16 * 32) + lane;
+    uint8_t* box = boxes + (warp - 2) * 2 * kBoxBytes;
+    uint64_t* res_full = bars->res_full[warp - 2];
+    volatile int* abort_flag = &bars->abort;
+    const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
+    const int hc = t.bn / 2, per_tile = hc / 64;
+    const int units = tiles > pair ? ((tiles - pair - 1) / pairs + 1) * per_tile : 0;
+    // first column and token of unit i's output box
+    auto place = [&](int i, int* n, int* m) {
+        int tn, tm;
+        tile_at(t, pair + i / per_tile * pairs, &tn, &tm);
+        *n = (tn * 2 + rank) * (GATED ? 64 : 128) + (GATED ? quad & 1 : quad) * 32;
+        *m = tm * t.bn + half * hc + i % per_tile * 64 + own;
+    };
+    auto fetch_residual = [&](int i) {  // elected lane
+        int n, m;
+        place(i, &n, &m);
+        if (n >= a.N || m >= a.M) return;
+        mbar_arrive_expect_tx(&res_full[i & 1], kBoxBytes);
+        tma_load_3d(box + (i & 1) * kBoxBytes, tm_res, &res_full[i & 1], n, m, 0);
+    };
+    const bool has_res = a.res != nullptr;
+    if (has_res && units > 0 && elect_one()) fetch_residual(0);
+    __syncwarp();
+    uint32_t phase = 0;  // bit b: parity of the next residual in box b
+    int flip = 0, i = 0;
+    float ws[2][2], bias[2][2];
+    for (; i < units; ++i) {
+        const int turn = i / per_tile, sub = i % per_tile, b = turn & 1;
+        int n_box, m_box;
+        place(i, &n_box, &m_box);
+        const bool live = n_box < a.N && m_box < a.M;
+        const int m0 = m_box - own;
+        if (sub == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const int n = n_box + 16 * h + 8 * g + (lane >> 2);
+                    const int col = up ? a.N + n : n;
+                    ws[h][g] = a.w_scale && n < a.N ? a.w_scale[col] : 1.f;
+                    bias[h][g] = a.bias && n < a.N ? a.bias[col] : 0.f;
+                }
+            const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag));
+            if (GATED ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
+            tc_fence_after();
+        }
+        float xs[16];  // of tokens 8 k + 2 (lane % 4) + {0, 1}
+        if (a.x_scale) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    xs[2 * k + e] = a.x_scale[min(m0 + 8 * k + 2 * (lane & 3) + e, a.M - 1)];
+        }
+        if (has_res) {
+            if (live) {
+                if (!mbar_wait_warp(&res_full[i & 1], (phase >> (i & 1)) & 1, abort_flag)) {
+                    if (!GATED) break;  // gated: the partner still waits below; the next vote ends both
+                } else
+                    phase ^= 1u << (i & 1);
+            }
+        } else {  // the store of two units ago has read its box
+            if (elect_one()) tma_store_wait_read1();
+            __syncwarp();
+        }
+        const uint32_t at = smem_u32(box + (i & 1) * kBoxBytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // 16 columns (TMEM lanes) at a time
+            float v[32];
+            tmem_ld16x256_x8(tmem + b * t.bn + half * hc + sub * 64 + ((uint32_t)(quad * 32 + 16 * h) << 16), v);
+            tmem_wait_ld();
+            if (h == 1 && sub == per_tile - 1) {  // the accumulator is read
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(b ? done1 : done0);
+            }
+            if (a.x_scale) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= xs[2 * (j >> 2) + (j & 1)] * ws[h][(j >> 1) & 1];
+            }
+            if (a.bias) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += bias[h][(j >> 1) & 1];
+            }
+            if constexpr (!GATED) {
+                activate_all<32>(a.act, v);
+            } else {
+                float* sw = ex + flip * (2 * 16 * 32);  // used in turns, so that one barrier an exchange is enough
+                flip ^= 1;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) sw[(own / 2 + j) * 32] = up ? v[j] : v[16 + j];
+                named_bar_sync(pair_bar, 64);
+                float g[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) g[j] = up ? sw[j * 32] : v[j];
+                activate_all<16>(a.act, g);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = g[j] * (up ? v[16 + j] : sw[(16 + j) * 32]);
+            }
+            if (live) {
+#pragma unroll
+                for (int k = 0; k < kPieces; k += 2) {
+                    // matrix lane / 8 of the four: tokens 8 (k + its high bit), columns 16 h + 8 (its low bit)
+                    const uint32_t token = 8 * (k + (lane >> 4)) + (lane & 7), chunk = 2 * h + ((lane >> 3) & 1);
+                    const uint32_t addr = at + token * kBoxRow + ((chunk ^ ((token >> 1) & 3)) << 4);
+                    if (has_res) {
+                        uint32_t r[4];
+                        ldmatrix_x4_trans(addr, r);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            v[4 * k + 2 * q] += bf16lo_to_f32(r[q]);
+                            v[4 * k + 2 * q + 1] += bf16hi_to_f32(r[q]);
+                        }
+                    }
+                    stmatrix_x4_trans(addr, pack_bf16x2(v[4 * k], v[4 * k + 1]), pack_bf16x2(v[4 * k + 2], v[4 * k + 3]),
+                                      pack_bf16x2(v[4 * k + 4], v[4 * k + 5]), pack_bf16x2(v[4 * k + 6], v[4 * k + 7]));
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (elect_one()) {
+            if (has_res && i + 1 < units) {
+                tma_store_wait_read0();  // the other box's store (of the last unit) has read it
+                fetch_residual(i + 1);
+            }
+            if (live) {
+                tma_store_3d(tm_out, box + (i & 1) * kBoxBytes, n_box, m_box, 0);
+            }
+            tma_store_commit();
+        }
+        __syncwarp();
+    }
+    if (i < units && has_res) {  // gave up: a residual load in flight lands before the CTA exits (bounded)
+        int n, m;
+        place(i, &n, &m);
+        if (n < a.N && m < a.M) (void)mbar_wait(&res_full[i & 1], (phase >> (i & 1)) & 1);
+    }
+    if (elect_one()) tma_store_wait_all0();
+    __syncwarp();
+}
+
 template <bool F8, bool KN>
 __global__ void __launch_bounds__(kLargeThreads, 1)
     linear_large_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
+                        const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_res,
                         const __grid_constant__ TcArgs t) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const LinearArgs& a = t.a;
     constexpr int kSlabElems = F8 ? 128 : 64;
     const int stages = t.stages;
-    float* swap = reinterpret_cast<float*>(sm + stages * t.stage_bytes);
-    LargeBars* bars = reinterpret_cast<LargeBars*>(sm + stages * t.stage_bytes + (a.gated ? kSwapBytes : 0));
+    uint8_t* boxes = sm + stages * t.stage_bytes;
+    float* swap = reinterpret_cast<float*>(boxes + box_bytes(t));
+    LargeBars* bars = reinterpret_cast<LargeBars*>(boxes + box_bytes(t) + (a.gated ? kSwapBytes : 0));
     volatile int* abort_flag = &bars->abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)cluster_rank();
@@ -402,6 +580,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
             mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
+            for (int w = 0; w < kEpiWarps; ++w) mbar_init(&bars->res_full[w][b], 1);
         }
         bars->abort = 0;
         fence_mbar_init();
@@ -467,6 +646,11 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
             }
             if (i > 0) (void)mbar_wait(&bars->empty[(i - 1) % stages], ((i - 1) / stages) & 1);  // all products are done
         }
+    } else if (t.staged) {
+        if (a.gated)
+            epilogue_staged<true>(t, &tm_out, &tm_res, bars, boxes, swap, tmem, rank, pair, pairs, tiles);
+        else
+            epilogue_staged<false>(t, &tm_out, &tm_res, bars, boxes, swap, tmem, rank, pair, pairs, tiles);
     } else if (a.gated) {
         epilogue<true>(t, bars, swap, tmem, rank, pair, pairs, tiles);
     } else {
@@ -501,17 +685,19 @@ EncodeTiledFn encoder() {
     return fn;
 }
 
-// A [rows][cols] matrix (cols contiguous) in boxes of 128 bytes x box_rows with the 128-byte
-// swizzle; what lies outside reads as zero.
-bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long long cols, int box_rows) {
+// A [rows][cols] matrix (cols contiguous) in boxes of 128 (or 64) bytes x box_rows with the swizzle
+// of that width; what lies outside reads as zero and is not written.
+bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long long cols, int box_rows,
+            int box_bytes = kSlabBytes) {
     EncodeTiledFn enc = encoder();
     if (!enc) return false;
     const cuuint64_t size = f8 ? 1 : 2;
     cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
     cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)rows * cols * size};
-    cuuint32_t box[3] = {(cuuint32_t)(kSlabBytes / size), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    cuuint32_t box[3] = {(cuuint32_t)(box_bytes / size), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
     return enc(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr),
-               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -578,7 +764,8 @@ gdn_status run_small(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
 }
 
 template <bool F8, bool KN>
-cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int pairs, size_t smem,
+cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& to,
+                         const CUtensorMap& tr, int pairs, size_t smem,
                          int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
     cudaError_t e = allow_smem(linear_large_kernel<F8, KN>, done, dev);
@@ -595,7 +782,7 @@ cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorM
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_large_kernel<F8, KN>, tw, tx, t);
+    return cudaLaunchKernelEx(&cfg, linear_large_kernel<F8, KN>, tw, tx, to, tr, t);
 }
 
 gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_t s) {
@@ -618,7 +805,9 @@ gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
     if ((long long)t.tiles_n * t.tiles_m > INT32_MAX - sms) return GDN_ERR_DIMS;
     t.group = t.tiles_n < 8 ? t.tiles_n : 8;
     t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
-    const size_t fixed = sizeof(LargeBars) + (a.gated ? kSwapBytes : 0) + 1024;
+    t.staged = !a.out_f32 && a.N % 8 == 0 && t.bn >= 128 &&
+               ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.res)) & 15u) == 0;
+    const size_t fixed = sizeof(LargeBars) + box_bytes(t) + (a.gated ? kSwapBytes : 0) + 1024;
     t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
     if (t.stages > kLargeStages) t.stages = kLargeStages;
     t.tmem_cols = 2 * t.bn;
@@ -629,11 +818,16 @@ gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
     const long long wn = a.gated ? 2LL * a.N : a.N;
     if (!encode(&tw, f8, a.w, a.nk ? wn : a.K, a.nk ? a.K : wn, 64) || !encode(&tx, f8, a.x, a.M, a.K, t.bn / 2))
         return GDN_ERR_CUDA;
+    CUtensorMap to{}, tr{};
+    const int tokens = a.gated ? 32 : 64;
+    if (t.staged && (!encode(&to, false, a.out, a.M, a.N, tokens, kBoxRow) ||
+                     (a.res && !encode(&tr, false, a.res, a.M, a.N, tokens, kBoxRow))))
+        return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
     const int tiles = t.tiles_n * t.tiles_m, pairs = tiles < sms / 2 ? tiles : sms / 2;
-    const cudaError_t e = f8     ? launch_large<true, false>(t, tw, tx, pairs, smem, dev, s)
-                          : a.nk ? launch_large<false, false>(t, tw, tx, pairs, smem, dev, s)
-                                 : launch_large<false, true>(t, tw, tx, pairs, smem, dev, s);
+    const cudaError_t e = f8     ? launch_large<true, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
+                          : a.nk ? launch_large<false, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
+                                 : launch_large<false, true>(t, tw, tx, to, tr, pairs, smem, dev, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

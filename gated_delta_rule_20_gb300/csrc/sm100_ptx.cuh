@@ -178,6 +178,13 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t m0, ui
                  "r"(m2), "r"(m3)
                  : "memory");
 }
+// The inverse: four 8x8 b16 matrices read from their transposed form, with the same addresses and registers.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&m)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3])
+                 : "r"(addr)
+                 : "memory");
+}
 // 4-byte asynchronous copy global -> shared.  It is not tracked by the register
 // scoreboard, so barriers and mbarrier waits do not stall on it; the issuing
 // thread sees the data after cp_async_wait_all.
