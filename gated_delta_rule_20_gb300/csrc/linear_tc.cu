@@ -207,20 +207,20 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
 constexpr int kLargeStages = 10;
 constexpr int kEpiWarps = 8;                       // two a TMEM lane quadrant, half of the columns each
 constexpr int kLargeThreads = 64 + 32 * kEpiWarps;
-constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 directions x 16 values
-constexpr uint32_t kBoxRow = 64;                   // a staged output row: 32 bf16 columns
+constexpr uint32_t kSwapBytes = 4 * 2 * 32 * 32 * 4;  // gated: 4 warp pairs x 2 directions x 32 values x 32 lanes
+constexpr uint32_t kBoxRow = 128;                  // a staged output row: 64 bf16 columns
 
 struct LargeBars {
     uint64_t full[kLargeStages], empty[kLargeStages];  // full: the leader's are used
     uint64_t acc_full[2], acc_empty[2];                // acc_empty: the leader's are used
-    uint64_t res_full[kEpiWarps][2];                   // staged residual boxes
+    uint64_t res_full[kEpiWarps / 2];                  // staged residual boxes
     uint32_t tmem;
     int abort;
 };
 
-// Shared memory of the staged output boxes: two a warp, of 64 tokens (gated 32) x 32 columns.
+// Shared memory of the staged output boxes: two of 64 tokens (gated 32) x 64 columns for two warps.
 __host__ __device__ inline uint32_t box_bytes(const TcArgs& t) {
-    return t.staged ? kEpiWarps * 2 * (t.a.gated ? 32 : 64) * kBoxRow : 0;
+    return t.staged ? kEpiWarps / 2 * 2 * (t.a.gated ? 32 : 64) * kBoxRow : 0;
 }
 
 // The tile of a pair's turn: n tiles walk in groups of t.group, tokens inside a group, so that the
@@ -231,6 +231,20 @@ __device__ __forceinline__ void tile_at(const TcArgs& t, int i, int* n, int* m) 
     *m = in / width;
     *n = g * t.group + in - *m * width;
 }
+
+// The tiles of a pair in turn, for a converged warp: every lane works out one of the next 32 (the
+// divisions take a few hundred cycles, which would stall the loads at every tile), and hands it out.
+struct Tiles {
+    int n, m;
+    __device__ __forceinline__ void get(const TcArgs& t, int turn, int pair, int pairs, int tiles, int* tn, int* tm) {
+        if ((turn & 31) == 0) {
+            const int mine = pair + (turn + (int)(threadIdx.x & 31)) * pairs;
+            tile_at(t, mine < tiles ? mine : 0, &n, &m);
+        }
+        *tn = __shfl_sync(0xffffffffu, n, turn & 31);
+        *tm = __shfl_sync(0xffffffffu, m, turn & 31);
+    }
+};
 
 // The residual of tokens m0 .. m0 + C - 1 at column n < N, raw (the last row again past M, which is
 // not stored): independent loads, issued well before they are used.
@@ -328,10 +342,11 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     volatile int* abort_flag = &bars->abort;
     const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
     int turn = 0, flip = 0;
+    Tiles walk;
     for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
         const int b = turn & 1;
         int tn, tm;
-        tile_at(t, tile, &tn, &tm);
+        walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
         // this thread's weight column and the output that it belongs to
         const int n = (tn * 2 + rank) * (GATED ? 64 : 128) + (GATED ? row & 63 : row);
         const int col = up ? a.N + n : n;
@@ -389,165 +404,183 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     }
 }
 
-// The same for bf16 outputs that TMA can store (N a multiple of 8, 16-byte aligned; bn >= 128).  A warp
-// takes units of 64 tokens x its 32 columns.  It reads TMEM in the layout of 8x8 fragments, in which a
-// thread has pairs of neighbouring tokens: packed to bf16, four fragments a stmatrix land transposed,
-// as rows of 64 bytes a token, with an eighth of the shared-memory stores that single elements take and
-// no address arithmetic; one TMA store takes the box away (and clips it to the matrix).  The residual
-// comes the same way back: a TMA load into the box, a unit ahead, and ldmatrix.
+// The same for bf16 outputs that TMA can store (N a multiple of 8, 16-byte aligned; bn >= 128).  Two
+// warps (64 TMEM lanes) fill boxes of 64 tokens.  They read TMEM in the layout of 8x8 fragments, in
+// which a thread has pairs of neighbouring tokens: packed to bf16, four fragments a stmatrix land
+// transposed, as a row of 64 columns (128 bytes, a whole line) a token, with an eighth of the
+// shared-memory stores that single elements take and no address arithmetic; a TMA store takes the box
+// away (and clips it to the matrix).  The residual comes the same way back: a TMA load into the box
+// while the tile's products run, and ldmatrix.  The two warps meet twice a tile (boxes free, boxes full).
 template <bool GATED>
 __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorMap* tm_out, const CUtensorMap* tm_res,
                                                 LargeBars* bars, uint8_t* boxes, float* swap, uint32_t tmem, int rank,
                                                 int pair, int pairs, int tiles) {
-    constexpr int kTokens = GATED ? 32 : 64;        // tokens of a unit that this warp finishes
-    constexpr int kPieces = kTokens / 8;            // fragments of 8 tokens among them
+    constexpr int kTokens = GATED ? 32 : 64;  // of 64 tokens, those that this warp finishes
+    constexpr int kPieces = kTokens / 8;      // fragments of 8 tokens among them
     constexpr uint32_t kBoxBytes = kTokens * kBoxRow;
     const LinearArgs& a = t.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quad = warp & 3, half = (warp - 2) >> 2;
-    const bool up = GATED && quad >= 2;
-    const int own = up ? 32 : 0;  // gated: gate rows finish a unit's first 32 tokens, up rows its last 32
-    const uint32_t pair_bar = 1 + (quad & 1) + 2 * half;
-    float* ex = swap + ((quad & 1) + 2 * half) * (2 * 2 * 16 * 32) + lane;
-    uint8_t* box = boxes + (warp - 2) * 2 * kBoxBytes;
-    uint64_t* res_full = bars->res_full[warp - 2];
+    const int quad = warp & 3, half = (warp - 2) >> 2, duo = quad >> 1;
+    const bool issuer = (quad & 1) == 0;  // of the two warps of a box
+    const bool up = GATED && duo == 1;
+    const int own = up ? 32 : 0;  // gated: gate rows finish the first 32 of 64 tokens, up rows the others
+    // the warps that share boxes (gated: all four of a half of the tokens); the warps of a gate and its up rows
+    const uint32_t box_bar = GATED ? 1 + half : 1 + half * 2 + duo, box_threads = GATED ? 128 : 64;
+    const uint32_t swap_bar = 5 + half * 2 + (quad & 1);
+    float* sw = swap + (half * 2 + (quad & 1)) * (2 * 32 * 32) + lane;  // gated: [up][32 values][lane]
+    uint8_t* box = boxes + (half * 2 + duo) * 2 * kBoxBytes;
+    uint64_t* res_full = &bars->res_full[half * 2 + duo];
     volatile int* abort_flag = &bars->abort;
     const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
     const int hc = t.bn / 2, per_tile = hc / 64;
-    const int units = tiles > pair ? ((tiles - pair - 1) / pairs + 1) * per_tile : 0;
-    // first column and token of unit i's output box
-    auto place = [&](int i, int* n, int* m) {
-        int tn, tm;
-        tile_at(t, pair + i / per_tile * pairs, &tn, &tm);
-        *n = (tn * 2 + rank) * (GATED ? 64 : 128) + (GATED ? quad & 1 : quad) * 32;
-        *m = tm * t.bn + half * hc + i % per_tile * 64 + own;
-    };
-    auto fetch_residual = [&](int i) {  // elected lane
-        int n, m;
-        place(i, &n, &m);
-        if (n >= a.N || m >= a.M) return;
-        mbar_arrive_expect_tx(&res_full[i & 1], kBoxBytes);
-        tma_load_3d(box + (i & 1) * kBoxBytes, tm_res, &res_full[i & 1], n, m, 0);
-    };
     const bool has_res = a.res != nullptr;
-    if (has_res && units > 0 && elect_one()) fetch_residual(0);
+    // first column of the boxes and first token of this half of a tile
+    Tiles walk;
+    auto place = [&](int turn, int* n, int* m) {
+        int tn, tm;
+        walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
+        *n = (tn * 2 + rank) * (GATED ? 64 : 128) + (GATED ? 0 : duo * 64);
+        *m = tm * t.bn + half * hc;
+    };
+    // whether a tile has residual boxes here (those past the matrix are not loaded), and their loads (one lane)
+    auto some = [&](int n, int m) { return has_res && n < a.N && m + own < a.M; };
+    auto fetch_residual = [&](int n, int m) {
+        if (!some(n, m)) return;
+        const int count = per_tile == 2 && m + 64 + own < a.M ? 2 : 1;
+        mbar_arrive_expect_tx(res_full, count * kBoxBytes);
+        for (int i = 0; i < count; ++i) tma_load_3d(box + i * kBoxBytes, tm_res, res_full, n, m + i * 64 + own, 0);
+    };
+    auto load_scales = [&](float (&xs)[16], int m) {  // of tokens m + 8 k + 2 (lane % 4) + {0, 1}
+#pragma unroll
+        for (int k = 0; k < 16; ++k) xs[k] = a.x_scale[min(m + 8 * (k >> 1) + 2 * (lane & 3) + (k & 1), a.M - 1)];
+    };
+    int n_box = a.N, m_tile = a.M, turn = 0;
+    uint32_t phase = 0;  // parity of the next residual
+    bool ok = true;
+    if (pair < tiles) place(0, &n_box, &m_tile);
+    if (issuer && elect_one()) fetch_residual(n_box, m_tile);
     __syncwarp();
-    uint32_t phase = 0;  // bit b: parity of the next residual in box b
-    int flip = 0, i = 0;
-    float ws[2][2], bias[2][2];
-    for (; i < units; ++i) {
-        const int turn = i / per_tile, sub = i % per_tile, b = turn & 1;
-        int n_box, m_box;
-        place(i, &n_box, &m_box);
-        const bool live = n_box < a.N && m_box < a.M;
-        const int m0 = m_box - own;
-        if (sub == 0) {
+    bool in_flight = some(n_box, m_tile);  // the residual of the tile has been asked for and not been waited for
+    for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
+        const int b = turn & 1;
+        int n_next = a.N, m_next = a.M;
+        if (tile + pairs < tiles) place(turn + 1, &n_next, &m_next);
+        float ws[2][2], bias[2][2], xs[16];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const int n = n_box + 16 * h + 8 * g + (lane >> 2);
-                    const int col = up ? a.N + n : n;
-                    ws[h][g] = a.w_scale && n < a.N ? a.w_scale[col] : 1.f;
-                    bias[h][g] = a.bias && n < a.N ? a.bias[col] : 0.f;
-                }
-            const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag));
-            if (GATED ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
-            tc_fence_after();
-        }
-        float xs[16];  // of tokens 8 k + 2 (lane % 4) + {0, 1}
-        if (a.x_scale) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    xs[2 * k + e] = a.x_scale[min(m0 + 8 * k + 2 * (lane & 3) + e, a.M - 1)];
-        }
-        if (has_res) {
-            if (live) {
-                if (!mbar_wait_warp(&res_full[i & 1], (phase >> (i & 1)) & 1, abort_flag)) {
-                    if (!GATED) break;  // gated: the partner still waits below; the next vote ends both
-                } else
-                    phase ^= 1u << (i & 1);
+            for (int g = 0; g < 2; ++g) {
+                const int n = n_box + (quad & 1) * 32 + 16 * h + 8 * g + (lane >> 2);
+                const int col = up ? a.N + n : n;
+                ws[h][g] = a.w_scale && n < a.N ? a.w_scale[col] : 1.f;
+                bias[h][g] = a.bias && n < a.N ? a.bias[col] : 0.f;
             }
-        } else {  // the store of two units ago has read its box
-            if (elect_one()) tma_store_wait_read1();
+        if (a.x_scale) load_scales(xs, m_tile);
+        if (issuer && !has_res) {  // the last tile's stores have read the boxes (with a residual: waited for below)
+            if (elect_one()) tma_store_wait_read0();
             __syncwarp();
         }
-        const uint32_t at = smem_u32(box + (i & 1) * kBoxBytes);
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag)) && ok;
+        if (in_flight) {
+            ok = mbar_wait_warp(res_full, phase, abort_flag) && ok;
+            if (ok) {
+                phase ^= 1;
+                in_flight = false;
+            }
+        }
+        if (named_bar_any(box_bar, box_threads, !ok)) break;  // the boxes are free; and one answer for all who meet here
+        tc_fence_after();
+        for (int sub = 0; sub < per_tile; ++sub) {
+            const bool live = n_box < a.N && m_tile + sub * 64 + own < a.M;
+            float v[2][32];  // 16 columns (TMEM lanes) each
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {  // 16 columns (TMEM lanes) at a time
-            float v[32];
-            tmem_ld16x256_x8(tmem + b * t.bn + half * hc + sub * 64 + ((uint32_t)(quad * 32 + 16 * h) << 16), v);
+            for (int h = 0; h < 2; ++h)
+                tmem_ld16x256_x8(tmem + b * t.bn + half * hc + sub * 64 + ((uint32_t)(quad * 32 + 16 * h) << 16), v[h]);
             tmem_wait_ld();
-            if (h == 1 && sub == per_tile - 1) {  // the accumulator is read
+            if (sub == per_tile - 1) {  // the accumulator is read
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(b ? done1 : done0);
             }
             if (a.x_scale) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= xs[2 * (j >> 2) + (j & 1)] * ws[h][(j >> 1) & 1];
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[h][j] *= xs[2 * (j >> 2) + (j & 1)] * ws[h][(j >> 1) & 1];
+                if (sub + 1 < per_tile) load_scales(xs, m_tile + (sub + 1) * 64);
             }
             if (a.bias) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] += bias[h][(j >> 1) & 1];
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[h][j] += bias[h][(j >> 1) & 1];
             }
             if constexpr (!GATED) {
-                activate_all<32>(a.act, v);
+                activate_all<32>(a.act, v[0]);
+                activate_all<32>(a.act, v[1]);
             } else {
-                float* sw = ex + flip * (2 * 16 * 32);  // used in turns, so that one barrier an exchange is enough
-                flip ^= 1;
+                if (sub > 0) named_bar_sync(swap_bar, 64);  // the last values are read (between tiles: box_bar)
+                // gate rows hand over their last 32 tokens and up rows their first 32
 #pragma unroll
-                for (int j = 0; j < 16; ++j) sw[(own / 2 + j) * 32] = up ? v[j] : v[16 + j];
-                named_bar_sync(pair_bar, 64);
-                float g[16];
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) g[j] = up ? sw[j * 32] : v[j];
-                activate_all<16>(a.act, g);
+                    for (int j = 0; j < 16; ++j) sw[(own + 16 * h + j) * 32] = up ? v[h][j] : v[h][16 + j];
+                named_bar_sync(swap_bar, 64);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = g[j] * (up ? v[16 + j] : sw[(16 + j) * 32]);
-            }
-            if (live) {
+                for (int h = 0; h < 2; ++h) {
+                    float g[16];
 #pragma unroll
-                for (int k = 0; k < kPieces; k += 2) {
-                    // matrix lane / 8 of the four: tokens 8 (k + its high bit), columns 16 h + 8 (its low bit)
-                    const uint32_t token = 8 * (k + (lane >> 4)) + (lane & 7), chunk = 2 * h + ((lane >> 3) & 1);
-                    const uint32_t addr = at + token * kBoxRow + ((chunk ^ ((token >> 1) & 3)) << 4);
-                    if (has_res) {
-                        uint32_t r[4];
-                        ldmatrix_x4_trans(addr, r);
+                    for (int j = 0; j < 16; ++j) g[j] = up ? sw[(16 * h + j) * 32] : v[h][j];
+                    activate_all<16>(a.act, g);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            v[4 * k + 2 * q] += bf16lo_to_f32(r[q]);
-                            v[4 * k + 2 * q + 1] += bf16hi_to_f32(r[q]);
-                        }
-                    }
-                    stmatrix_x4_trans(addr, pack_bf16x2(v[4 * k], v[4 * k + 1]), pack_bf16x2(v[4 * k + 2], v[4 * k + 3]),
-                                      pack_bf16x2(v[4 * k + 4], v[4 * k + 5]), pack_bf16x2(v[4 * k + 6], v[4 * k + 7]));
+                    for (int j = 0; j < 16; ++j) v[h][j] = g[j] * (up ? v[h][16 + j] : sw[(32 + 16 * h + j) * 32]);
                 }
             }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (elect_one()) {
-            if (has_res && i + 1 < units) {
-                tma_store_wait_read0();  // the other box's store (of the last unit) has read it
-                fetch_residual(i + 1);
-            }
             if (live) {
-                tma_store_3d(tm_out, box + (i & 1) * kBoxBytes, n_box, m_box, 0);
+                const uint32_t at = smem_u32(box + sub * kBoxBytes);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < kPieces; k += 2) {
+                        // matrix lane / 8 of the four: tokens 8 (k + its high bit), columns 16 h + 8 (its low bit)
+                        const uint32_t token = 8 * (k + (lane >> 4)) + (lane & 7);
+                        const uint32_t chunk = 4 * (quad & 1) + 2 * h + ((lane >> 3) & 1);
+                        const uint32_t addr = at + token * kBoxRow + ((chunk ^ (token & 7)) << 4);
+                        float* f = &v[h][4 * k];
+                        if (has_res) {
+                            uint32_t r[4];
+                            ldmatrix_x4_trans(addr, r);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                f[2 * q] += bf16lo_to_f32(r[q]);
+                                f[2 * q + 1] += bf16hi_to_f32(r[q]);
+                            }
+                        }
+                        stmatrix_x4_trans(addr, pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                                          pack_bf16x2(f[6], f[7]));
+                    }
+                fence_proxy_async_smem();
             }
+        }
+        named_bar_sync(box_bar, box_threads);  // the boxes are full
+        if (issuer && elect_one()) {
+            for (int sub = 0; sub < per_tile; ++sub)
+                if (n_box < a.N && m_tile + sub * 64 + own < a.M)
+                    tma_store_3d(tm_out, box + sub * kBoxBytes, n_box, m_tile + sub * 64 + own, 0);
             tma_store_commit();
+            if (has_res) {  // the next tile's residual takes the boxes as soon as they are read
+                tma_store_wait_read0();
+                fetch_residual(n_next, m_next);
+            }
         }
         __syncwarp();
+        n_box = n_next;
+        m_tile = m_next;
+        in_flight = some(n_box, m_tile);
     }
-    if (i < units && has_res) {  // gave up: a residual load in flight lands before the CTA exits (bounded)
-        int n, m;
-        place(i, &n, &m);
-        if (n < a.N && m < a.M) (void)mbar_wait(&res_full[i & 1], (phase >> (i & 1)) & 1);
-    }
-    if (elect_one()) tma_store_wait_all0();
+    if (in_flight) (void)mbar_wait(res_full, phase);  // gave up: the load lands first (bounded)
+    __syncwarp();
+    if (issuer && elect_one()) tma_store_wait_all0();
     __syncwarp();
 }
 
@@ -580,8 +613,8 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
             mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
-            for (int w = 0; w < kEpiWarps; ++w) mbar_init(&bars->res_full[w][b], 1);
         }
+        for (int w = 0; w < kEpiWarps / 2; ++w) mbar_init(&bars->res_full[w], 1);
         bars->abort = 0;
         fence_mbar_init();
     }
@@ -596,9 +629,11 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
     if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
         int i = 0;    // slabs loaded
         bool live = true;
-        for (int tile = pair; tile < tiles && live; tile += pairs) {
+        Tiles walk;
+        int turn = 0;
+        for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
             int tn, tm;
-            tile_at(t, tile, &tn, &tm);
+            walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
             const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? a.N + n0 : n0 + 64;
             const int m0 = tm * t.bn + rank * (t.bn / 2);
             for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i) {
@@ -685,19 +720,17 @@ EncodeTiledFn encoder() {
     return fn;
 }
 
-// A [rows][cols] matrix (cols contiguous) in boxes of 128 (or 64) bytes x box_rows with the swizzle
-// of that width; what lies outside reads as zero and is not written.
-bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long long cols, int box_rows,
-            int box_bytes = kSlabBytes) {
+// A [rows][cols] matrix (cols contiguous) in boxes of 128 bytes x box_rows with the 128-byte
+// swizzle; what lies outside reads as zero and is not written.
+bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long long cols, int box_rows) {
     EncodeTiledFn enc = encoder();
     if (!enc) return false;
     const cuuint64_t size = f8 ? 1 : 2;
     cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
     cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)rows * cols * size};
-    cuuint32_t box[3] = {(cuuint32_t)(box_bytes / size), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    cuuint32_t box[3] = {(cuuint32_t)(kSlabBytes / size), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
     return enc(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr),
-               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -803,7 +836,7 @@ gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
     }
     t.tiles_m = (a.M + t.bn - 1) / t.bn;
     if ((long long)t.tiles_n * t.tiles_m > INT32_MAX - sms) return GDN_ERR_DIMS;
-    t.group = t.tiles_n < 8 ? t.tiles_n : 8;
+    t.group = t.tiles_n < 16 ? t.tiles_n : 16;
     t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
     t.staged = !a.out_f32 && a.N % 8 == 0 && t.bn >= 128 &&
                ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.res)) & 15u) == 0;
@@ -820,8 +853,8 @@ gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
         return GDN_ERR_CUDA;
     CUtensorMap to{}, tr{};
     const int tokens = a.gated ? 32 : 64;
-    if (t.staged && (!encode(&to, false, a.out, a.M, a.N, tokens, kBoxRow) ||
-                     (a.res && !encode(&tr, false, a.res, a.M, a.N, tokens, kBoxRow))))
+    if (t.staged && (!encode(&to, false, a.out, a.M, a.N, tokens) ||
+                     (a.res && !encode(&tr, false, a.res, a.M, a.N, tokens))))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
     const int tiles = t.tiles_n * t.tiles_m, pairs = tiles < sms / 2 ? tiles : sms / 2;
