@@ -47,6 +47,7 @@ struct TcArgs {
     int slabs, stages, bn;          // bn: MMA N (tokens of a tile)
     uint32_t stage_bytes, tmem_cols, idesc;
     int splits;                     // small kernel: K splits (cluster size)
+    bool wide_out;                  // small kernel: 4 outputs a store
     int tiles_n, tiles_m, group;    // large kernel: the tile grid, n tiles walked together
     bool staged;                    // large kernel: bf16 output (and residual) by TMA
     int32_t* status;
@@ -68,6 +69,63 @@ __device__ __forceinline__ void mma_slab(uint32_t tmem, uint32_t stage, uint32_t
         mma_step<F8, PAIR>(tmem, sdesc_add(dw, k * (KN ? 2048 : 32)), sdesc_add(dx, k * 32), idesc, !first || k > 0);
 }
 
+// The sum over the S ranks' partial sums (in the ranks' order) of 4 neighbouring columns a thread, and
+// the epilogue, for the tokens rank, rank + S, ... of the tile.  e: thread of 128; part: [token][128].
+template <int S>
+__device__ __forceinline__ void join_splits(const TcArgs& t, uint32_t part, int e, int rank, int n0, int m0, int cols) {
+    const LinearArgs& a = t.a;
+    const int width = a.gated ? 16 : 32;  // threads of a token
+    const int n = n0 + e % width * 4;
+    if (n >= a.N) return;
+    const uint32_t at = part + e % width * 16;
+    uint32_t peer[S];
+#pragma unroll
+    for (int q = 0; q < S; ++q) peer[q] = S > 1 ? map_to_rank(at, q) : at;
+    for (int c = rank + S * (e / width); c < cols; c += S * (128 / width)) {
+        float4 g[S], u[S];
+#pragma unroll
+        for (int q = 0; q < S; ++q) {
+            g[q] = ld_cluster_f32x4(peer[q] + c * 512);
+            if (a.gated) u[q] = ld_cluster_f32x4(peer[q] + c * 512 + 256);
+        }
+        const int m = m0 + c;
+        const long long i = (long long)m * a.N + n;
+        float v[4], w[4], r[4];
+        if (a.res) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = load_out(a, i + min(j, a.N - 1 - n));
+        }
+#pragma unroll
+        for (int q = 1; q < S; ++q) {
+            g[0].x += g[q].x, g[0].y += g[q].y, g[0].z += g[q].z, g[0].w += g[q].w;
+            if (a.gated) u[0].x += u[q].x, u[0].y += u[q].y, u[0].z += u[q].z, u[0].w += u[q].w;
+        }
+        v[0] = g[0].x, v[1] = g[0].y, v[2] = g[0].z, v[3] = g[0].w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = activate(a.act, affine(a, v[j], m, n + min(j, a.N - 1 - n)));
+        if (a.gated) {
+            w[0] = u[0].x, w[1] = u[0].y, w[2] = u[0].z, w[3] = u[0].w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] *= affine(a, w[j], m, a.N + n + min(j, a.N - 1 - n));
+        }
+        if (a.res) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += r[j];
+        }
+        if (t.wide_out) {  // N a multiple of 4, the output aligned to 4 elements
+            if (a.out_f32)
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + i) = make_float4(v[0], v[1], v[2], v[3]);
+            else
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + i) =
+                    make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n + j < a.N) store_out(a, i + j, v[j]);
+        }
+    }
+}
+
 template <bool F8, bool KN>
 __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                            const __grid_constant__ CUtensorMap tm_x,
@@ -84,6 +142,7 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
     const int n0 = ((int)blockIdx.x / t.splits) * (a.gated ? 64 : 128);  // outputs of this tile
     const int n1 = a.gated ? a.N + n0 : n0 + 64;                         // weight column of the second box
     const int m0 = (int)blockIdx.y * t.bn;
+    griddep_launch_dependents();  // the next kernel's CTAs may be set up beside this one (they wait as below)
     const int k_lo = (int)((long long)t.slabs * rank / t.splits), k_hi = (int)((long long)t.slabs * (rank + 1) / t.splits);
 
     if (tid == 0) {
@@ -105,6 +164,7 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
+    griddep_wait();  // the preceding kernel's results; nothing of the caller's is read before
 
     if (warp == 0) {  // TMA producer
         int loaded = 0;
@@ -169,28 +229,11 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
     else
         __syncthreads();
     if (ok) {
-        const int per = a.gated ? 64 : 128;  // outputs of a token
-        const int n = n0 + e % per;
-        const uint32_t at = smem_u32(part) + (e % per) * 4;
-        for (int c = rank + t.splits * (e / per); c < cols; c += t.splits * (128 / per)) {
-            const int m = m0 + c;
-            float g[8], u[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                const uint32_t p = q < t.splits ? map_to_rank(at + c * 512, q) : 0;
-                g[q] = q < t.splits ? ld_cluster_f32(p) : 0.f;
-                u[q] = a.gated && q < t.splits ? ld_cluster_f32(p + 256) : 0.f;
-            }
-            if (n >= a.N) continue;
-#pragma unroll
-            for (int q = 1; q < 8; ++q) {  // the ranks' order
-                g[0] += g[q];
-                u[0] += u[q];
-            }
-            float v = activate(a.act, affine(a, g[0], m, n));
-            if (a.gated) v *= affine(a, u[0], m, a.N + n);
-            const long long i = (long long)m * a.N + n;
-            store_out(a, i, a.res ? v + load_out(a, i) : v);
+        switch (t.splits) {
+            case 1: join_splits<1>(t, smem_u32(part), e, rank, n0, m0, cols); break;
+            case 2: join_splits<2>(t, smem_u32(part), e, rank, n0, m0, cols); break;
+            case 4: join_splits<4>(t, smem_u32(part), e, rank, n0, m0, cols); break;
+            default: join_splits<8>(t, smem_u32(part), e, rank, n0, m0, cols); break;
         }
     }
     __syncwarp();
@@ -602,6 +645,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
     const int rank = (int)cluster_rank();
     const int tiles = t.tiles_n * t.tiles_m, pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
     const int per = a.gated ? 64 : 128;  // outputs of a CTA
+    griddep_launch_dependents();  // as in the small kernel
 
     if (tid == 0) {
         tma_prefetch_desc(&tm_w);
@@ -625,6 +669,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
     cluster_sync();  // the peer's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
+    griddep_wait();
 
     if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
         int i = 0;    // slabs loaded
@@ -745,25 +790,36 @@ cudaError_t allow_smem(F* kernel, std::atomic<bool> (&done)[kMaxDevices], int de
     return e;
 }
 
-template <bool F8, bool KN>
-cudaError_t launch_small(TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
-                         int dev, cudaStream_t s) {
-    static std::atomic<bool> done[kMaxDevices];
-    cudaError_t e = allow_smem(linear_small_kernel<F8, KN>, done, dev);
+// A launch in clusters of `cluster` CTAs that may be set up while the stream's preceding kernel ends
+// (programmatic stream serialization; the kernels wait for that kernel before they read anything).
+template <typename... P, typename... Q>
+cudaError_t launch(void (*kernel)(P...), std::atomic<bool> (&done)[kMaxDevices], int dev, dim3 grid, int threads, size_t smem,
+                   int cluster, cudaStream_t s, const Q&... args) {
+    const cudaError_t e = allow_smem(kernel, done, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m);
-    cfg.blockDim = dim3(192);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)t.splits;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = t.splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, linear_small_kernel<F8, KN>, tw, tx, t);
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <bool F8, bool KN>
+cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
+                         int dev, cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];
+    return launch(linear_small_kernel<F8, KN>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), 192, smem,
+                  t.splits, s, tw, tx, t);
 }
 
 gdn_status run_small(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_t s) {
@@ -777,6 +833,7 @@ gdn_status run_small(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
     t.splits = 1;
     while (t.splits < 8 && (long long)tiles * tiles_m * t.splits * 2 <= 2LL * sms && t.slabs >= t.splits * 2 * 4)
         t.splits *= 2;
+    t.wide_out = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & (a.out_f32 ? 15u : 7u)) == 0;
     t.stage_bytes = kWBytes + t.bn * kSlabBytes;
     t.stages = (int)((100 * 1024 - sizeof(SmallBars) - 1024) / t.stage_bytes);
     if (t.stages > kMaxStages) t.stages = kMaxStages;
@@ -798,24 +855,10 @@ gdn_status run_small(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
 
 template <bool F8, bool KN>
 cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& to,
-                         const CUtensorMap& tr, int pairs, size_t smem,
-                         int dev, cudaStream_t s) {
+                         const CUtensorMap& tr, int pairs, size_t smem, int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
-    cudaError_t e = allow_smem(linear_large_kernel<F8, KN>, done, dev);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cfg.blockDim = dim3(kLargeThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, linear_large_kernel<F8, KN>, tw, tx, to, tr, t);
+    return launch(linear_large_kernel<F8, KN>, done, dev, dim3((unsigned)(2 * pairs)), kLargeThreads, smem, 2, s, tw, tx, to,
+                  tr, t);
 }
 
 gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_t s) {

@@ -24,6 +24,7 @@
 
 #include "gdn_device.cuh"
 #include "gdn_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -92,6 +93,8 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP)
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP;
     constexpr int kRows = kBlock / GROUP;  // rows of a block at a time
     __shared__ float2 part[2][GROUP / 32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();  // the preceding kernel's results (see launch)
     const int t = threadIdx.x % GROUP, nv = a.D / V;
     const uint4* x = static_cast<const uint4*>(a.x);
     const uint4* res = static_cast<const uint4*>(a.res);
@@ -192,6 +195,8 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_an
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP, kUnroll = 4;
     extern __shared__ float row_smem[];
     __shared__ float2 part[2][GROUP / 32];
+    ptx::griddep_launch_dependents();
+    ptx::griddep_wait();
     const int t = threadIdx.x % GROUP;
     const long long r = (long long)blockIdx.x * kRows + threadIdx.x / GROUP;
     if (r >= a.rows) return;  // a whole warp (GROUP == 32), or none of the block
@@ -229,6 +234,22 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_an
     }
 }
 
+// The kernels' CTAs may be set up while the stream's preceding kernel ends (programmatic stream
+// serialization); they wait for it before they read anything.
+cudaError_t launch(void (*kernel)(NormArgs), unsigned grid, int threads, size_t smem, cudaStream_t s, const NormArgs& a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <typename T, typename O, int GROUP, int P>
 cudaError_t launch_vec(const NormArgs& a, int sms, cudaStream_t s) {
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP;
@@ -238,8 +259,7 @@ cudaError_t launch_vec(const NormArgs& a, int sms, cudaStream_t s) {
                            cudaSuccess && n > 0 ? n : 1;
     }();
     const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sms * per_sm;
-    rmsnorm_residual_vec_kernel<T, O, GROUP, P><<<(unsigned)(need < room ? need : room), kBlock, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch(rmsnorm_residual_vec_kernel<T, O, GROUP, P>, (unsigned)(need < room ? need : room), kBlock, 0, s, a);
 }
 
 template <typename T, typename O, int GROUP>
@@ -251,8 +271,7 @@ cudaError_t launch_any(const NormArgs& a, cudaStream_t s) {
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    rmsnorm_residual_any_kernel<T, O, GROUP><<<(unsigned)((a.rows + kRows - 1) / kRows), kBlock, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch(rmsnorm_residual_any_kernel<T, O, GROUP>, (unsigned)((a.rows + kRows - 1) / kRows), kBlock, smem, s, a);
 }
 
 // The group is the smallest that holds the row in at most 2 pieces a thread (4 for warps, whose
