@@ -53,10 +53,26 @@ struct TcArgs {
     int32_t* status;
 };
 
+constexpr int kEpiWarps = 8;                    // two a TMEM lane quadrant, half of the columns each
+constexpr int kThreads = 64 + 32 * kEpiWarps;   // and a warp for the loads, one for the products
+
 struct SmallBars {
     uint64_t full[kMaxStages], empty[kMaxStages], done;
     uint32_t tmem;
     int abort;
+};
+
+// A place in the ring of stages: the stage and the parity of the barrier phase that its next use waits
+// for.  (Kept by counting: a division by the runtime number of stages costs more than the wait.)
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+        }
+    }
 };
 
 // The four 32-byte steps of K of one slab.  KN: W is MN-major (boxes of 64 columns, 2048 bytes a step).
@@ -70,7 +86,7 @@ __device__ __forceinline__ void mma_slab(uint32_t tmem, uint32_t stage, uint32_t
 }
 
 // The sum over the S ranks' partial sums (in the ranks' order) of 4 neighbouring columns a thread, and
-// the epilogue, for the tokens rank, rank + S, ... of the tile.  e: thread of 128; part: [token][128].
+// the epilogue, for the tokens rank, rank + S, ... of the tile.  e: epilogue thread; part: [token][128].
 template <int S>
 __device__ __forceinline__ void join_splits(const TcArgs& t, uint32_t part, int e, int rank, int n0, int m0, int cols) {
     const LinearArgs& a = t.a;
@@ -81,7 +97,7 @@ __device__ __forceinline__ void join_splits(const TcArgs& t, uint32_t part, int 
     uint32_t peer[S];
 #pragma unroll
     for (int q = 0; q < S; ++q) peer[q] = S > 1 ? map_to_rank(at, q) : at;
-    for (int c = rank + S * (e / width); c < cols; c += S * (128 / width)) {
+    for (int c = rank + S * (e / width); c < cols; c += S * (32 * kEpiWarps / width)) {
         float4 g[S], u[S];
 #pragma unroll
         for (int q = 0; q < S; ++q) {
@@ -127,7 +143,7 @@ __device__ __forceinline__ void join_splits(const TcArgs& t, uint32_t part, int 
 }
 
 template <bool F8, bool KN>
-__global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
+__global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                            const __grid_constant__ CUtensorMap tm_x,
                                                            const __grid_constant__ TcArgs t) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -168,9 +184,10 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
 
     if (warp == 0) {  // TMA producer
         int loaded = 0;
-        for (int i = 0; i < k_hi - k_lo; ++i) {
-            const int s = i % stages, k = (k_lo + i) * kSlabElems;
-            if (i >= stages && !mbar_wait_warp(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) break;
+        Ring at;
+        for (int i = 0; i < k_hi - k_lo; ++i, at.next(stages)) {
+            const int s = at.s, k = (k_lo + i) * kSlabElems;
+            if (i >= stages && !mbar_wait_warp(&bars->empty[s], at.phase ^ 1, abort_flag)) break;
             uint8_t* st = sm + s * t.stage_bytes;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&bars->full[s], t.stage_bytes);
@@ -186,9 +203,10 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
             (void)mbar_wait(&bars->full[i % stages], (i / stages) & 1);
     } else if (warp == 1) {  // MMA issuer
         int issued = 0;
-        for (int i = 0; i < k_hi - k_lo; ++i) {
-            const int s = i % stages;
-            if (!mbar_wait_warp(&bars->full[s], (i / stages) & 1, abort_flag)) break;
+        Ring at;
+        for (int i = 0; i < k_hi - k_lo; ++i, at.next(stages)) {
+            const int s = at.s;
+            if (!mbar_wait_warp(&bars->full[s], at.phase, abort_flag)) break;
             tc_fence_after();
             if (elect_one()) {
                 mma_slab<F8, KN, false>(tmem, smem_u32(sm) + s * t.stage_bytes, t.idesc, i == 0);
@@ -212,7 +230,7 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
         tc_fence_after();
         if (ok) {
             const int row = (warp & 3) * 32 + lane;
-            for (int c0 = 0; c0 < cols; c0 += 8) {
+            for (int c0 = (warp - 2) / 4 * 8; c0 < cols; c0 += 16) {
                 float v[8];
                 tmem_ld8(tmem + ((uint32_t)(row & ~31) << 16) + c0, v);
                 tmem_wait_ld();
@@ -248,8 +266,6 @@ __global__ void __launch_bounds__(192) linear_small_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ many tokens
 constexpr int kLargeStages = 10;
-constexpr int kEpiWarps = 8;                       // two a TMEM lane quadrant, half of the columns each
-constexpr int kLargeThreads = 64 + 32 * kEpiWarps;
 constexpr uint32_t kSwapBytes = 4 * 2 * 32 * 32 * 4;  // gated: 4 warp pairs x 2 directions x 32 values x 32 lanes
 constexpr uint32_t kBoxRow = 128;                  // a staged output row: 64 bf16 columns
 
@@ -628,7 +644,7 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
 }
 
 template <bool F8, bool KN>
-__global__ void __launch_bounds__(kLargeThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     linear_large_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_res,
                         const __grid_constant__ TcArgs t) {
@@ -675,15 +691,16 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
         int i = 0;    // slabs loaded
         bool live = true;
         Tiles walk;
+        Ring at;
         int turn = 0;
         for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
             int tn, tm;
             walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
             const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? a.N + n0 : n0 + 64;
             const int m0 = tm * t.bn + rank * (t.bn / 2);
-            for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i) {
-                const int s = i % stages;
-                if (i >= stages && !mbar_wait_warp(&bars->empty[s], ((i / stages) - 1) & 1, abort_flag)) {
+            for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i, at.next(stages)) {
+                const int s = at.s;
+                if (i >= stages && !mbar_wait_warp(&bars->empty[s], at.phase ^ 1, abort_flag)) {
                     live = false;
                     break;
                 }
@@ -704,14 +721,15 @@ __global__ void __launch_bounds__(kLargeThreads, 1)
     } else if (warp == 1) {
         if (rank == 0) {  // MMA issuer of the pair
             int i = 0, turn = 0;
+            Ring at;
             bool live = true;
             for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
                 const int b = turn & 1;
                 if (turn >= 2 && !mbar_wait_warp(&bars->acc_empty[b], ((turn >> 1) - 1) & 1, abort_flag)) break;
                 tc_fence_after();
-                for (int k = 0; k < t.slabs; ++k, ++i) {
-                    const int s = i % stages;
-                    if (!mbar_wait_warp(&bars->full[s], (i / stages) & 1, abort_flag)) {
+                for (int k = 0; k < t.slabs; ++k, ++i, at.next(stages)) {
+                    const int s = at.s;
+                    if (!mbar_wait_warp(&bars->full[s], at.phase, abort_flag)) {
                         live = false;
                         break;
                     }
@@ -818,7 +836,7 @@ template <bool F8, bool KN>
 cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
                          int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_small_kernel<F8, KN>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), 192, smem,
+    return launch(linear_small_kernel<F8, KN>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), kThreads, smem,
                   t.splits, s, tw, tx, t);
 }
 
@@ -857,7 +875,7 @@ template <bool F8, bool KN>
 cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& to,
                          const CUtensorMap& tr, int pairs, size_t smem, int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_large_kernel<F8, KN>, done, dev, dim3((unsigned)(2 * pairs)), kLargeThreads, smem, 2, s, tw, tx, to,
+    return launch(linear_large_kernel<F8, KN>, done, dev, dim3((unsigned)(2 * pairs)), kThreads, smem, 2, s, tw, tx, to,
                   tr, t);
 }
 
