@@ -230,13 +230,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
         tc_fence_after();
         if (ok) {
             const int row = (warp & 3) * 32 + lane;
-            for (int c0 = (warp - 2) / 4 * 8; c0 < cols; c0 += 16) {
-                float v[8];
-                tmem_ld8(tmem + ((uint32_t)(row & ~31) << 16) + c0, v);
+            const uint32_t lanes = tmem + ((uint32_t)(row & ~31) << 16);
+            for (int c0 = (warp - 2) / 4 * 16; c0 < cols; c0 += 32) {  // (columns come in 16s: t.bn)
+                float v[2][8];
+                tmem_ld8(lanes + c0, v[0]);
+                tmem_ld8(lanes + c0 + 8, v[1]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (c0 + j < cols) part[(c0 + j) * 128 + row] = v[j];
+                for (int j = 0; j < 16; ++j)
+                    if (c0 + j < cols) part[(c0 + j) * 128 + row] = v[j / 8][j % 8];
             }
         }
     }
@@ -840,20 +842,64 @@ cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorM
                   t.splits, s, tw, tx, t);
 }
 
-gdn_status run_small(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_t s) {
+// What runs: the pair kernel on tiles of bn tokens, or the small one on tiles of bn tokens with K over
+// `splits` CTAs.
+struct Plan {
+    bool large;
+    int bn, splits;
+};
+
+// The estimated time of every choice, in us, and the least of them.  A slab is 16 KB of weight and 128
+// bytes of every token of the tile.  Fitted to sweeps of M = 1 .. 512, K and N = 512 .. 8192 (bf16, us in a
+// graph over weights larger than L2):
+//   - small: one CTA takes in about 85 KB/us and two on an SM 115, all together at most 6.3 MB/us; the
+//     partial sums' way through TMEM and shared memory costs 0.3 + bn / 60, a third more over 8 CTAs.  M = 64, K = N = 2048: 12.4 (32 tokens, no split), 8.3 (2), 6.8 (4), 6.9 (8);
+//   - pairs: 0.20 us a slab up to 128 tokens and 0.28 at 256 (the tensor cores' time), 1 us more set-up
+//     and an epilogue of bn / 200.  M = 512, K = N = 4096: 20.8 the best small plan, 18.5 pairs at 128,
+//     23.2 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
+Plan plan(const LinearArgs& a, int slabs, int sms) {
+    const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
+    const double weight_mb = tiles1 * slabs * (16.0 / 1024);
+    Plan best{true, 256, 1};
+    double least = 1e30;
+    for (int bn = 64; bn <= 256; bn *= 2) {
+        const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
+        double t = 1.0 + bn / 200.0 + (double)turns * slabs * (bn == 256 ? 0.28 : 0.20);
+        if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
+        if (t < least) least = t, best = Plan{true, bn, 1};
+    }
+    for (int bn = 16; bn <= 128; bn *= 2) {
+        if (bn > 16 && bn / 2 >= a.M) break;
+        const long long tiles_m = (a.M + bn - 1) / bn;
+        for (int S = 1; S <= 8 && S * 2 <= (slabs > 2 ? slabs : 2); S *= 2) {
+            const long long ctas = tiles1 * tiles_m * S;
+            const long long room = 8LL * (sms / 8 * 2 / S) * S;  // CTAs at once: clusters stay inside one of 8 groups of SMs
+            const long long waves = (ctas + room - 1) / room;
+            const long long an_sm = ctas <= sms ? 1 : waves * 2;  // CTAs one after another, or beside one another
+            const double kb = (double)an_sm * ((slabs + S - 1) / S) * (16 + bn / 8.0);
+            double t = kb / (an_sm == 1 ? 85 : 115);
+            if (t < weight_mb / 6.3) t = weight_mb / 6.3;
+            double join = 0.3 + bn / 60.0;
+            if (S == 8) join = join * 1.3 + 0.2;
+            t += join * waves + 3.0 * (waves - 1);
+            if (t < least) least = t, best = Plan{false, bn, S};
+        }
+    }
+    return best;
+}
+
+gdn_status run_small(const LinearArgs& a, bool f8, Plan how, int dev, cudaStream_t s) {
     TcArgs t{};
     t.a = a;
     const int elems = f8 ? 128 : 64, per = a.gated ? 64 : 128;
     t.slabs = (a.K + elems - 1) / elems;
-    t.bn = a.M >= 128 ? 128 : (a.M + 15) / 16 * 16;
-    const int tiles = (int)(((long long)a.N + per - 1) / per), tiles_m = (a.M + t.bn - 1) / t.bn;
-    // Two CTAs an SM (100 KB each): splits as long as they all run at once and have 4 slabs each.
-    t.splits = 1;
-    while (t.splits < 8 && (long long)tiles * tiles_m * t.splits * 2 <= 2LL * sms && t.slabs >= t.splits * 2 * 4)
-        t.splits *= 2;
+    t.bn = how.bn;
+    t.splits = how.splits;
+    const long long tiles = ((long long)a.N + per - 1) / per, tiles_m = (a.M + t.bn - 1) / t.bn;
+    if (tiles * t.splits > INT32_MAX || tiles_m > 65535) return GDN_ERR_DIMS;
     t.wide_out = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & (a.out_f32 ? 15u : 7u)) == 0;
     t.stage_bytes = kWBytes + t.bn * kSlabBytes;
-    t.stages = (int)((100 * 1024 - sizeof(SmallBars) - 1024) / t.stage_bytes);
+    t.stages = (int)((112 * 1024 - sizeof(SmallBars) - 1024) / t.stage_bytes);  // two CTAs an SM
     if (t.stages > kMaxStages) t.stages = kMaxStages;
     t.tmem_cols = 32;
     while (t.tmem_cols < (uint32_t)t.bn) t.tmem_cols <<= 1;
@@ -865,9 +911,9 @@ gdn_status run_small(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_
     if (!encode(&tw, f8, a.w, a.nk ? wn : a.K, a.nk ? a.K : wn, 64) || !encode(&tx, f8, a.x, a.M, a.K, t.bn))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + sizeof(SmallBars) + 1024;
-    const cudaError_t e = f8     ? launch_small<true, false>(t, tw, tx, tiles, tiles_m, smem, dev, s)
-                          : a.nk ? launch_small<false, false>(t, tw, tx, tiles, tiles_m, smem, dev, s)
-                                 : launch_small<false, true>(t, tw, tx, tiles, tiles_m, smem, dev, s);
+    const cudaError_t e = f8     ? launch_small<true, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
+                          : a.nk ? launch_small<false, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
+                                 : launch_small<false, true>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -879,22 +925,13 @@ cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorM
                   tr, t);
 }
 
-gdn_status run_large(const LinearArgs& a, bool f8, int dev, int sms, cudaStream_t s) {
+gdn_status run_large(const LinearArgs& a, bool f8, Plan how, int dev, int sms, cudaStream_t s) {
     TcArgs t{};
     t.a = a;
     const int elems = f8 ? 128 : 64, per = a.gated ? 128 : 256;
     t.slabs = (a.K + elems - 1) / elems;
     t.tiles_n = (int)(((long long)a.N + per - 1) / per);
-    // The widest token tile that leaves the least work to the busiest pair.
-    long long best = 0;
-    for (int bn = 256; bn >= 64; bn /= 2) {
-        const long long tiles = (long long)t.tiles_n * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
-        const long long cost = turns * (bn + 32);
-        if (bn == 256 || cost < best) {
-            best = cost;
-            t.bn = bn;
-        }
-    }
+    t.bn = how.bn;
     t.tiles_m = (a.M + t.bn - 1) / t.bn;
     if ((long long)t.tiles_n * t.tiles_m > INT32_MAX - sms) return GDN_ERR_DIMS;
     t.group = t.tiles_n < 16 ? t.tiles_n : 16;
@@ -940,8 +977,9 @@ gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, cudaStream_t s) 
     int dev = 0, sms = 0;
     const gdn_status st = current_device_sms(&dev, &sms);
     if (st != GDN_OK) return st;
-    if (a.M > 128) return run_large(a, dtype == GDN_F8E4M3, dev, sms, s);
-    return run_small(a, dtype == GDN_F8E4M3, dev, sms, s);
+    const bool f8 = dtype == GDN_F8E4M3;
+    const Plan how = plan(a, (a.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64), sms);
+    return how.large ? run_large(a, f8, how, dev, sms, s) : run_small(a, f8, how, dev, s);
 }
 
 }  // namespace gdn
