@@ -39,6 +39,25 @@ __device__ __forceinline__ float activate(int act, float v) {
     }
 }
 
+// The activation of C values (the choice is uniform over the grid).
+template <int C>
+__device__ __forceinline__ void activate_all(int act, float (&v)[C]) {
+    switch (act) {
+        case GDN_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_SILU, v[j]);
+            break;
+        case GDN_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_GELU, v[j]);
+            break;
+        case GDN_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_RELU, v[j]);
+            break;
+    }
+}
+
 __device__ __forceinline__ float load_out(const LinearArgs& a, long long i) {
     return a.out_f32 ? static_cast<const float*>(a.res)[i]
                      : __bfloat162float(static_cast<const __nv_bfloat16*>(a.res)[i]);

@@ -325,25 +325,6 @@ __device__ __forceinline__ void load_residual(const LinearArgs& a, uint32_t (&r)
     }
 }
 
-// The activation of C values (the choice is uniform over the grid).
-template <int C>
-__device__ __forceinline__ void activate_all(int act, float (&v)[C]) {
-    switch (act) {
-        case GDN_ACT_SILU:
-#pragma unroll
-            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_SILU, v[j]);
-            break;
-        case GDN_ACT_GELU:
-#pragma unroll
-            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_GELU, v[j]);
-            break;
-        case GDN_ACT_RELU:
-#pragma unroll
-            for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_RELU, v[j]);
-            break;
-    }
-}
-
 // C tokens of one output column n: activation, gate (u, or null), residual (raw), rounding, store.
 template <int C>
 __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const float* u, const uint32_t (&r)[C], int m0,
