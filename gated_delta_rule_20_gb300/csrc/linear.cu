@@ -4,8 +4,8 @@
 //     out[m, n] = act(x_scale[m] w_scale[n] sum_k x[m, k] W[k, n] + bias[n]) + residual[m, n]
 //
 // (gated: act of the gate's column times the up column).  The FFMA kernel is right for every
-// type, layout, size and alignment; it is the path of fp32 compute and of operands whose rows
-// TMA cannot take (pointer or row pitch not a multiple of 16 bytes).
+// type, layout, size and alignment; it is the path of fp32 compute and of small products of operands
+// whose rows TMA cannot take (pointer or row pitch not a multiple of 16 bytes).
 //
 // FFMA kernel: 16 x 16 threads on a tile of 16 TM tokens x 16 TM columns, TM x TM sums a thread as pairs
 // of neighbouring columns (fma.rn.f32x2: half the issue slots of single FFMAs, which leaves room for the
@@ -350,9 +350,13 @@ extern "C" gdn_status gdn_linear(const void* x, const float* x_scale, const void
                        d->activation, d->out_dtype == GDN_F32, (d->flags & GDN_LINEAR_GATED) != 0,
                        (d->flags & GDN_LINEAR_WEIGHT_NK) != 0};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!(d->flags & GDN_LINEAR_FORCE_FFMA) && linear_tc_supported(a, d->dtype)) return launch_linear_tc(a, d->dtype, s);
     int dev = 0, sms = 0;
     if (current_device_sms(&dev, &sms) != GDN_OK) return GDN_ERR_CUDA;
+    if (!(d->flags & GDN_LINEAR_FORCE_FFMA)) {
+        bool taken = false;
+        const gdn_status tc = launch_linear_tc(a, d->dtype, dev, sms, s, &taken);
+        if (taken || tc != GDN_OK) return tc;
+    }
     const cudaError_t e = d->dtype == GDN_F32    ? launch_ffma<float>(a, sms, s)
                           : d->dtype == GDN_BF16 ? launch_ffma<__nv_bfloat16>(a, sms, s)
                                                  : launch_ffma<__nv_fp8_e4m3>(a, sms, s);

@@ -25,10 +25,9 @@ struct LinearArgs {
     bool nk;       // weight layout
 };
 
-// The tensor-core kernels (linear_tc.cu): whether the operands' alignment and types allow them,
-// and the launch.
-bool linear_tc_supported(const LinearArgs& a, int32_t dtype);
-gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, cudaStream_t s);
+// The tensor-core kernels (linear_tc.cu).  *taken: whether they do the call (they do not for fp32, nor for
+// small products of operands that TMA cannot take).
+gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, int dev, int sms, cudaStream_t s, bool* taken);
 
 __device__ __forceinline__ float activate(int act, float v) {
     switch (act) {  // uniform over the grid

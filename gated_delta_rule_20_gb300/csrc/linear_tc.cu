@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstring>
 #include <mutex>
 
 #include "gdn_internal.h"
@@ -46,6 +47,7 @@ struct TcArgs {
     LinearArgs a;
     int slabs, stages, bn;          // bn: MMA N (tokens of a tile)
     uint32_t stage_bytes, tmem_cols, idesc;
+    int up;                         // gated: the weight column where the up half starts (see Operands)
     int splits;                     // small kernel: K splits (cluster size)
     bool wide_out;                  // small kernel: 4 outputs a store
     int tiles_n, tiles_m, group;    // large kernel: the tile grid, n tiles walked together
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = t.splits > 1 ? (int)cluster_rank() : 0;
     const int n0 = ((int)blockIdx.x / t.splits) * (a.gated ? 64 : 128);  // outputs of this tile
-    const int n1 = a.gated ? a.N + n0 : n0 + 64;                         // weight column of the second box
+    const int n1 = a.gated ? t.up + n0 : n0 + 64;                        // weight column of the second box
     const int m0 = (int)blockIdx.y * t.bn;
     griddep_launch_dependents();  // the next kernel's CTAs may be set up beside this one (they wait as below)
     const int k_lo = (int)((long long)t.slabs * rank / t.splits), k_hi = (int)((long long)t.slabs * (rank + 1) / t.splits);
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
             int tn, tm;
             walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
-            const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? a.N + n0 : n0 + 64;
+            const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? t.up + n0 : n0 + 64;
             const int m0 = tm * t.bn + rank * (t.bn / 2);
             for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i, at.next(stages)) {
                 const int s = at.s;
@@ -766,14 +768,14 @@ EncodeTiledFn encoder() {
     return fn;
 }
 
-// A [rows][cols] matrix (cols contiguous) in boxes of 128 bytes x box_rows with the 128-byte
-// swizzle; what lies outside reads as zero and is not written.
-bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long long cols, int box_rows) {
+// A [rows][cols] matrix (cols contiguous, rows `pitch` elements apart) in boxes of 128 bytes x box_rows
+// with the 128-byte swizzle; what lies outside reads as zero and is not written.
+bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long long cols, long long pitch, int box_rows) {
     EncodeTiledFn enc = encoder();
     if (!enc) return false;
     const cuuint64_t size = f8 ? 1 : 2;
     cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
-    cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)rows * cols * size};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch * size, (cuuint64_t)rows * pitch * size};
     cuuint32_t box[3] = {(cuuint32_t)(kSlabBytes / size), (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
     return enc(map, f8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr),
                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -814,6 +816,14 @@ cudaError_t launch(void (*kernel)(P...), std::atomic<bool> (&done)[kMaxDevices],
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// Where TMA finds x and the weight: the caller's arrays, or copies of them with rows of whole 16-byte
+// pieces.  Pitches in elements; up: the weight column where a gated weight's up half starts.
+struct Operands {
+    const void *x, *w;
+    long long x_pitch, w_pitch, w_cols;
+    int up;
+};
 
 template <bool F8, bool KN>
 cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
@@ -869,9 +879,10 @@ Plan plan(const LinearArgs& a, int slabs, int sms) {
     return best;
 }
 
-gdn_status run_small(const LinearArgs& a, bool f8, Plan how, int dev, cudaStream_t s) {
+gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how, int dev, cudaStream_t s) {
     TcArgs t{};
     t.a = a;
+    t.up = op.up;
     const int elems = f8 ? 128 : 64, per = a.gated ? 64 : 128;
     t.slabs = (a.K + elems - 1) / elems;
     t.bn = how.bn;
@@ -888,8 +899,8 @@ gdn_status run_small(const LinearArgs& a, bool f8, Plan how, int dev, cudaStream
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
     CUtensorMap tw, tx;
-    const long long wn = a.gated ? 2LL * a.N : a.N;
-    if (!encode(&tw, f8, a.w, a.nk ? wn : a.K, a.nk ? a.K : wn, 64) || !encode(&tx, f8, a.x, a.M, a.K, t.bn))
+    if (!encode(&tw, f8, op.w, a.nk ? op.w_cols : a.K, a.nk ? a.K : op.w_cols, op.w_pitch, 64) ||
+        !encode(&tx, f8, op.x, a.M, a.K, op.x_pitch, t.bn))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + sizeof(SmallBars) + 1024;
     const cudaError_t e = f8     ? launch_small<true, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
@@ -906,9 +917,10 @@ cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorM
                   tr, t);
 }
 
-gdn_status run_large(const LinearArgs& a, bool f8, Plan how, int dev, int sms, cudaStream_t s) {
+gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how, int dev, int sms, cudaStream_t s) {
     TcArgs t{};
     t.a = a;
+    t.up = op.up;
     const int elems = f8 ? 128 : 64, per = a.gated ? 128 : 256;
     t.slabs = (a.K + elems - 1) / elems;
     t.tiles_n = (int)(((long long)a.N + per - 1) / per);
@@ -927,13 +939,13 @@ gdn_status run_large(const LinearArgs& a, bool f8, Plan how, int dev, int sms, c
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
     CUtensorMap tw, tx;
-    const long long wn = a.gated ? 2LL * a.N : a.N;
-    if (!encode(&tw, f8, a.w, a.nk ? wn : a.K, a.nk ? a.K : wn, 64) || !encode(&tx, f8, a.x, a.M, a.K, t.bn / 2))
+    if (!encode(&tw, f8, op.w, a.nk ? op.w_cols : a.K, a.nk ? a.K : op.w_cols, op.w_pitch, 64) ||
+        !encode(&tx, f8, op.x, a.M, a.K, op.x_pitch, t.bn / 2))
         return GDN_ERR_CUDA;
     CUtensorMap to{}, tr{};
     const int tokens = a.gated ? 32 : 64;
-    if (t.staged && (!encode(&to, false, a.out, a.M, a.N, tokens) ||
-                     (a.res && !encode(&tr, false, a.res, a.M, a.N, tokens))))
+    if (t.staged && (!encode(&to, false, a.out, a.M, a.N, a.N, tokens) ||
+                     (a.res && !encode(&tr, false, a.res, a.M, a.N, a.N, tokens))))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
     const int tiles = t.tiles_n * t.tiles_m, pairs = tiles < sms / 2 ? tiles : sms / 2;
@@ -945,22 +957,105 @@ gdn_status run_large(const LinearArgs& a, bool f8, Plan how, int dev, int sms, c
 
 }  // namespace
 
-bool linear_tc_supported(const LinearArgs& a, int32_t dtype) {
-    if (dtype != GDN_BF16 && dtype != GDN_F8E4M3) return false;
-    const long long size = dtype == GDN_BF16 ? 2 : 1, wn = a.gated ? 2LL * a.N : a.N;
-    if (((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.w)) & 15u) || a.K * size % 16) return false;
-    if (!a.nk && wn * size % 16) return false;
-    // the up half's boxes of a [K, 2 N] weight start at column N, which TMA wants on 16 bytes
-    return a.nk || !a.gated || a.N * size % 16 == 0;
+namespace {
+
+// Rows of `cols` elements with any alignment, copied to rows `pitch` elements apart (whole 16-byte
+// pieces): the first `half` columns to column 0, the others to column `up`.
+struct CopyJob {
+    const void* src;
+    void* dst;
+    long long rows, cols, pitch, half, up;
+};
+
+template <typename E>
+__global__ void __launch_bounds__(256) linear_align_kernel(const __grid_constant__ CopyJob x, const __grid_constant__ CopyJob w) {
+    constexpr int V = 16 / (int)sizeof(E);
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long x_pieces = x.rows * (x.pitch / V), pieces = x_pieces + w.rows * (w.pitch / V);
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (long long)gridDim.x * 256) {
+        const CopyJob& c = i < x_pieces ? x : w;
+        const long long at = i < x_pieces ? i : i - x_pieces, row = at / (c.pitch / V), d0 = at % (c.pitch / V) * V;
+        const E* src = static_cast<const E*>(c.src) + row * c.cols;
+        E e[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const long long d = d0 + j, from = d < c.half ? d : d >= c.up ? c.half + d - c.up : c.cols;
+            e[j] = from < c.cols ? src[from] : E(0);
+        }
+        uint4 o;
+        memcpy(&o, e, 16);
+        reinterpret_cast<uint4*>(c.dst)[row * (c.pitch / V) + at % (c.pitch / V)] = o;
+    }
 }
 
-gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    const gdn_status st = current_device_sms(&dev, &sms);
-    if (st != GDN_OK) return st;
-    const bool f8 = dtype == GDN_F8E4M3;
+// Whether TMA can take an operand of `cols`-element rows as it lies.
+bool takes(const void* p, long long cols, int size) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && cols * size % 16 == 0;
+}
+
+gdn_status run_tc(const LinearArgs& a, const Operands& op, bool f8, int dev, int sms, cudaStream_t s) {
     const Plan how = plan(a, (a.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64), sms);
-    return how.large ? run_large(a, f8, how, dev, sms, s) : run_small(a, f8, how, dev, s);
+    return how.large ? run_large(a, op, f8, how, dev, sms, s) : run_small(a, op, f8, how, dev, s);
+}
+
+}  // namespace
+
+gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, int dev, int sms, cudaStream_t s, bool* taken) {
+    *taken = false;
+    if (dtype != GDN_BF16 && dtype != GDN_F8E4M3) return GDN_OK;
+    const bool f8 = dtype == GDN_F8E4M3;
+    const int size = f8 ? 1 : 2, piece = 16 / size;
+    const long long wn = a.gated ? 2LL * a.N : a.N, w_row = a.nk ? a.K : wn, w_rows = a.nk ? wn : a.K;
+    Operands op{a.x, a.w, a.K, w_row, wn, a.N};
+    const bool x_fits = takes(a.x, a.K, size);
+    // the up half's boxes of a [K, 2 N] weight start at column N, which TMA wants on 16 bytes too
+    const bool w_fits = takes(a.w, w_row, size) && (a.nk || !a.gated || a.N % piece == 0);
+    if (x_fits && w_fits) {
+        *taken = true;
+        return run_tc(a, op, f8, dev, sms, s);
+    }
+    // Operands that do not fit are copied to aligned rows first, where that pays: the copies and the scratch
+    // cost about 10 us and then HBM's rate, the FFMA kernel does 45 TFLOP/s.  M = 4000, K = 3001, N = 5000
+    // (bf16): 2.9 ms by FFMA.
+    if (2.0 * a.M * wn * a.K < 1e9) return GDN_OK;
+    auto up_to = [&](long long n) { return (n + piece - 1) / piece * piece; };
+    CopyJob x{a.x, nullptr, 0, a.K, up_to(a.K), a.K, up_to(a.K)}, w{a.w, nullptr, 0, w_row, up_to(w_row), w_row, up_to(w_row)};
+    if (!x_fits) x.rows = a.M;
+    if (!w_fits) {
+        w.rows = w_rows;
+        if (!a.nk && a.gated) {  // both halves start on a piece
+            w.half = a.N;
+            w.up = up_to(a.N);
+            w.pitch = 2 * w.up;
+        }
+    }
+    const size_t x_bytes = (size_t)(x.rows * x.pitch * size), bytes = x_bytes + (size_t)(w.rows * w.pitch * size);
+    void* scratch = nullptr;
+    if (cudaMallocAsync(&scratch, bytes, s) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return GDN_OK;  // the FFMA kernel needs none
+    }
+    *taken = true;
+    if (!x_fits) {
+        op.x = x.dst = scratch;
+        op.x_pitch = x.pitch;
+    }
+    if (!w_fits) {
+        op.w = w.dst = static_cast<uint8_t*>(scratch) + x_bytes;
+        op.w_pitch = w.pitch;
+        if (!a.nk && a.gated) {
+            op.up = (int)w.up;
+            op.w_cols = w.up + a.N;
+        }
+    }
+    if (f8)
+        linear_align_kernel<uint8_t><<<8 * sms, 256, 0, s>>>(x, w);
+    else
+        linear_align_kernel<uint16_t><<<8 * sms, 256, 0, s>>>(x, w);
+    gdn_status st = cudaGetLastError() == cudaSuccess ? run_tc(a, op, f8, dev, sms, s) : GDN_ERR_CUDA;
+    if (cudaFreeAsync(scratch, s) != cudaSuccess && st == GDN_OK) st = GDN_ERR_CUDA;
+    return st;
 }
 
 }  // namespace gdn

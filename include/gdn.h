@@ -414,10 +414,13 @@ typedef struct {
  *   bias         [N'] fp32, or NULL
  *   residual     [M, N] in out_dtype, or NULL; may be out (in place)
  *   out          [M, N] in out_dtype
- * Pointers aligned to their element.  x or a weight whose pointer is not 16-byte aligned, or
- * whose rows are not a multiple of 16 bytes, and fp32 compute take the FFMA kernel, at a
- * small part of the tensor cores' rate.  One launch on `stream`.  Results do not depend on
- * what else runs: every sum has one order for given dims and device.
+ * Pointers aligned to their element.  fp32 compute runs on an FFMA kernel, bf16 and e4m3 on
+ * the tensor cores, in one launch on `stream`, where x and the weight are 16-byte aligned with
+ * rows of a multiple of 16 bytes (a gated [K, 2 N] weight: also N).  An operand that is not is
+ * copied to such rows first (one more launch; scratch from cudaMallocAsync on `stream`, freed
+ * there) where the product is large enough to pay for it (1e9 operations); smaller ones, and
+ * calls whose scratch cannot be had, run on the FFMA kernel.  Results do not depend on what
+ * else runs: every sum has one order for given arguments and device.
  */
 gdn_status gdn_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale,
                       const float* bias, const void* residual, void* out, const gdn_linear_dims* dims,

@@ -69,6 +69,32 @@ def _check(out, t, act, layout, gated):
         bad.sum(), bad.size, (np.abs(got - ref) / (e + 1e-30)).max(), np.argwhere(bad)[:3].tolist())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f8"])
+@pytest.mark.parametrize("M", [1, 64, 700])
+def test_graph_capture(gdn, M, dtype):
+    """A norm and a product behind it, captured and replayed (programmatic launches in a graph)."""
+    D, N = 1024, 768
+    gen = torch.Generator("cuda").manual_seed(M)
+    x, r = (torch.randn(M, D, generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    nw = torch.ones(D, device="cuda")
+    w = torch.randn(N, D, generator=gen, device="cuda") / D ** 0.5
+    ws = w.abs().amax(1) / 448 if dtype == "f8" else None
+    w = (w / ws[:, None]).to(DT["f8"]) if dtype == "f8" else w.to(DT["bf16"])
+
+    def layer():
+        y, s, h = gdn.rmsnorm_residual(x, nw, r, out_dtype=DT[dtype])
+        return gdn.linear(y, w, weight_layout="nk", x_scale=s, weight_scale=ws), h
+    ref = layer()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layer()
+    for _ in range(3):
+        out[0].zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
+
+
 def _run(gdn, M, N, K, dtype="bf16", layout="nk", gated=False, act="none", bias=False, residual=False, out=None, **kw):
     out = out or ("f32" if dtype == "f32" else "bf16")
     t = _draw(M, N, K, dtype, layout, gated, bias, residual, out, seed=M * 31 + N * 7 + K)
@@ -122,6 +148,33 @@ def test_epilogues(gdn, M, N, K, dtype, act, gated, bias, residual, out):
     (1500, 4104, 648, "bf16", "kn", True), (5000, 300, 256, "f8", "nk", False), (1, 16384, 8192, "bf16", "nk", False)])
 def test_larger(gdn, M, N, K, dtype, layout, gated):
     _run(gdn, M, N, K, dtype, layout, gated, "silu" if gated else "none", residual=True)
+
+
+@pytest.mark.parametrize("M,N,K,dtype,layout,gated", [
+    (1000, 1001, 1003, "bf16", "kn", False), (1000, 1001, 1003, "bf16", "nk", False), (515, 700, 1404, "bf16", "kn", True),
+    (515, 701, 1408, "bf16", "kn", True), (2000, 3001, 130, "bf16", "nk", True), (1037, 1111, 1001, "f8", "nk", False),
+    (700, 803, 1030, "f8", "nk", True), (9, 16001, 4001, "bf16", "kn", False), (4100, 129, 2050, "bf16", "kn", False)])
+def test_large_products_of_rows_off_16_bytes(gdn, M, N, K, dtype, layout, gated):
+    """Odd row pitches (and a gated [K, 2 N] weight whose halves do not start on 16 bytes) in products
+    of 1e9 operations and more, whose operands are copied to aligned rows; also from unaligned addresses
+    and under graph capture."""
+    assert 2 * M * N * (2 if gated else 1) * K >= 1e9
+    got, t = _run(gdn, M, N, K, dtype, layout, gated, "silu" if gated else "none", bias=True, residual=True)
+    for which in ("x", "weight"):
+        b = torch.empty(t[which].numel() + 1, dtype=t[which].dtype, device="cuda")
+        b[1:].view(t[which].shape).copy_(t[which])
+        t[which] = b[1:].view(t[which].shape)
+    call = gdn.linear_gated if gated else gdn.linear
+    f = lambda: call(t["x"], t["weight"], t["bias"], t["residual"], activation="silu" if gated else "none",  # noqa: E731
+                     weight_layout=layout, x_scale=t["x_scale"], weight_scale=t["weight_scale"])
+    assert torch.equal(f(), got)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = f()
+    out.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, got)
 
 
 @pytest.mark.parametrize("M,N,K", [(5, 128, 128), (300, 264, 192)])
