@@ -592,7 +592,7 @@ def rmsnorm_residual(x, norm_weight, residual=None, *, out=None, out_scale=None,
     if ocode != code and ocode != GDN_F8E4M3:
         raise TypeError("out must have x's dtype or float8_e4m3fn, got %s" % out_dtype)
     if out is None:
-        out = _layer_empty(shape, out_dtype, device, stream)
+        out = _T.empty_like(x, dtype=out_dtype) if stream is None else _layer_empty(shape, out_dtype, device, stream)
         op = out.data_ptr()
     else:
         op = _layer_ptr("out", out, shape, out_dtype, device)
@@ -609,7 +609,7 @@ def rmsnorm_residual(x, norm_weight, residual=None, *, out=None, out_scale=None,
     if residual is not None:
         rp = _layer_ptr("residual", residual, shape, dtype, device)
         if residual_out is None:
-            residual_out = _layer_empty(shape, dtype, device, stream)
+            residual_out = _T.empty_like(x) if stream is None else _layer_empty(shape, dtype, device, stream)
     if residual_out is not None:
         hp = _layer_ptr("residual_out", residual_out, shape, dtype, device)
     _layer_call(_lib.gdn_rmsnorm_residual, device, stream, x.data_ptr(), rp, wp, hp, op, sp, x.numel() // D, D, code,

@@ -862,6 +862,7 @@ Plan plan(const LinearArgs& a, int slabs, int sms) {
     for (int bn = 16; bn <= 128; bn *= 2) {
         if (bn > 16 && bn / 2 >= a.M) break;
         const long long tiles_m = (a.M + bn - 1) / bn;
+        if (tiles_m > 65535) continue;  // the grid's limit
         for (int S = 1; S <= 8 && S * 2 <= (slabs > 2 ? slabs : 2); S *= 2) {
             const long long ctas = tiles1 * tiles_m * S;
             const long long room = 8LL * (sms / 8 * 2 / S) * S;  // CTAs at once: clusters stay inside one of 8 groups of SMs

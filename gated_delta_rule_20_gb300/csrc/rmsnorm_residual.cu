@@ -75,6 +75,7 @@ __device__ __forceinline__ float row_factor(float2 stat, const NormArgs& a, long
     if constexpr (std::is_same<O, F8>::value) {
         float m = stat.y * rinv;
         m = m < GDN_FP8_AMAX_MIN ? GDN_FP8_AMAX_MIN : m;  // a NaN stays one
+        if (m > 3.4e38f) m = __int_as_float(0x7fc00000);  // an infinite weight: no scale stands for the row
         const float scale = m / 448.f;
         if (first) a.scale[r] = scale;
         return rinv / scale;
@@ -83,47 +84,95 @@ __device__ __forceinline__ float row_factor(float2 stat, const NormArgs& a, long
     }
 }
 
-// Rows of whole 16-byte pieces, 16-byte aligned: GROUP threads a row, P pieces a thread.  The
-// weights stay in registers over the rows of a thread; the next row's pieces are loaded before
-// this row's statistics are reduced, so that the barrier does not leave HBM idle.
-template <typename T, typename O, int GROUP, int P>
-__global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP)
-    rmsnorm_residual_vec_kernel(const __grid_constant__ NormArgs a) {
+// V elements as a 16-byte piece of the flat array.  One that reaches past the array's end (its last piece,
+// kOdd only) is put together from the elements that exist.  (A piece over a row's end holds elements of
+// the neighbouring row too, which another block may be writing: they are replaced by zeros, see below.)
+template <typename T, bool kOdd>
+__device__ __forceinline__ uint4 load_piece(const T* p, long long piece, long long elements) {
+    constexpr int V = 16 / (int)sizeof(T);
+    if (!kOdd || (piece + 1) * V <= elements) return __ldcs(reinterpret_cast<const uint4*>(p) + piece);
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (piece * V + j < elements) e[j] = p[piece * V + j];
+    return v;
+}
+// V elements of a row (`col`: the column of the first) stored as a piece, or one by one where the piece
+// reaches past the row's ends; W: a word of V elements of E.
+template <typename E, typename W, bool kOdd>
+__device__ __forceinline__ void store_piece(E* p, long long piece, int col, int D, W v) {
+    constexpr int V = (int)(sizeof(W) / sizeof(E));
+    if (!kOdd || (col >= 0 && col + V <= D)) {
+        reinterpret_cast<W*>(p)[piece] = v;
+        return;
+    }
+    const E* e = reinterpret_cast<const E*>(&v);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (col + j >= 0 && col + j < D) p[piece * V + j] = e[j];
+}
+
+// Arrays on 16 bytes: GROUP threads a row, P pieces of 16 bytes a thread.  The next row's pieces are loaded
+// before this row's statistics are reduced, so that the barrier does not leave HBM idle.
+// Rows of whole pieces keep their weights in registers.  Rows that are not (kOdd) start anywhere in a
+// piece: the pieces are still those of the flat array, the ones at a row's ends go element by element, and
+// the weights, whose place in the pieces changes from row to row, are read from shared memory, one word in
+// V left out so that the threads' words lie in different banks.
+template <typename T, typename O, int GROUP, int P, bool kOdd>
+__global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_vec_kernel(const __grid_constant__ NormArgs a) {
     constexpr int V = 16 / (int)sizeof(T);
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP;
     constexpr int kRows = kBlock / GROUP;  // rows of a block at a time
     __shared__ float2 part[2][GROUP / 32];
+    extern __shared__ float w_smem[];  // kOdd: [D + D / V]
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();  // the preceding kernel's results (see launch)
-    const int t = threadIdx.x % GROUP, nv = a.D / V;
-    const uint4* x = static_cast<const uint4*>(a.x);
-    const uint4* res = static_cast<const uint4*>(a.res);
+    const int t = threadIdx.x % GROUP, D = a.D;
+    const T* x = static_cast<const T*>(a.x);
+    const T* res = static_cast<const T*>(a.res);
     long long r = (long long)blockIdx.x * kRows + threadIdx.x / GROUP;
     const long long step = (long long)gridDim.x * kRows;
     uint4 xv[P], rv[P];
+    // columns between a row's first piece and its start; pieces of the row
+    auto shift_of = [&](long long row) { return kOdd ? (int)(row * D % V) : 0; };
+    auto load = [&](long long row, int shift) {
+        const long long first = (row * D - shift) / V;
+        const int pieces = (shift + D + V - 1) / V;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int i = t + p * GROUP;
-        xv[p] = rv[p] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < a.rows && i < nv) {
-            xv[p] = __ldcs(x + r * nv + i);
-            if (res) rv[p] = __ldcs(res + r * nv + i);
-        }
-    }
-    float w[P][V];
-#pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int j = 0; j < V; j += 4) {
+        for (int p = 0; p < P; ++p) {
             const int i = t + p * GROUP;
-            const float4 f = i < nv ? *reinterpret_cast<const float4*>(a.w + i * V + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-            w[p][j] = f.x;
-            w[p][j + 1] = f.y;
-            w[p][j + 2] = f.z;
-            w[p][j + 3] = f.w;
+            if (i < pieces) {
+                xv[p] = load_piece<T, kOdd>(x, first + i, a.rows * D);
+                if (res) rv[p] = load_piece<T, kOdd>(res, first + i, a.rows * D);
+            }
         }
+    };
+#pragma unroll
+    for (int p = 0; p < P; ++p) xv[p] = rv[p] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < a.rows) load(r, shift_of(r));
+    float w[kOdd ? 1 : P][V];
+    if constexpr (kOdd) {
+        for (int i = threadIdx.x; i < D; i += kBlock) w_smem[i + i / V] = a.w[i];
+        __syncthreads();
+    } else {
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int j = 0; j < V; j += 4) {
+                const int i = t + p * GROUP;
+                const float4 f =
+                    i < D / V ? *reinterpret_cast<const float4*>(a.w + i * V + j) : make_float4(0.f, 0.f, 0.f, 0.f);
+                w[p][j] = f.x;
+                w[p][j + 1] = f.y;
+                w[p][j + 2] = f.z;
+                w[p][j + 3] = f.w;
+            }
+    }
     // blocks of several rows have one warp a row and no barrier in the loop; a block of one row leaves it as one
     for (int turn = 0; r < a.rows; r += step, turn ^= 1) {
+        const int shift = shift_of(r), pieces = (shift + D + V - 1) / V;
+        const long long first = (r * D - shift) / V;
         float h[P][V], ss = 0.f, mx = 0.f;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
@@ -133,18 +182,20 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP)
             for (int j = 0; j < V; ++j) {
                 h[p][j] = to_f32(xe[j]);
                 if (res) h[p][j] += to_f32(re[j]);
-                ss += h[p][j] * h[p][j];
             }
+            if constexpr (kOdd) {  // zeros for what is not the row's
+                const int col = (t + p * GROUP) * V - shift;
+                if (col < 0 || col + V > D) {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (col + j < 0 || col + j >= D) h[p][j] = 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) ss += h[p][j] * h[p][j];
         }
         const long long next = r + step;
-#pragma unroll
-        for (int p = 0; p < P; ++p) {
-            const int i = t + p * GROUP;
-            if (next < a.rows && i < nv) {
-                xv[p] = __ldcs(x + next * nv + i);
-                if (res) rv[p] = __ldcs(res + next * nv + i);
-            }
-        }
+        if (next < a.rows) load(next, shift_of(next));
         if (a.h) {
 #pragma unroll
             for (int p = 0; p < P; ++p) {
@@ -153,36 +204,45 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP)
                 T* oe = reinterpret_cast<T*>(&o);
 #pragma unroll
                 for (int j = 0; j < V; ++j) oe[j] = from_f32<T>(h[p][j]);
-                if (i < nv) static_cast<uint4*>(a.h)[r * nv + i] = o;
+                if (i < pieces) store_piece<T, uint4, kOdd>(static_cast<T*>(a.h), first + i, i * V - shift, D, o);
             }
         }
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                h[p][j] *= w[p][j];
+                if constexpr (kOdd) {
+                    // column c = i V - shift + j of piece i lies at c + c / V, that is i (V + 1) - shift + j, and one
+                    // before where j < shift; columns past the row's ends read some other weight, for an h of 0
+                    const int i = t + p * GROUP;
+                    const int at = i * (V + 1) - shift + j - (j < shift ? 1 : 0);
+                    h[p][j] *= w_smem[min(max(at, 0), D + D / V - 1)];
+                } else {
+                    h[p][j] *= w[p][j];
+                }
                 if constexpr (std::is_same<O, F8>::value) mx = max_nan(mx, fabsf(h[p][j]));
             }
         const float f = row_factor<O>(reduce_row<GROUP>(ss, mx, part, turn), a, r, t == 0);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int i = t + p * GROUP;
-            if (i >= nv) continue;
+            if (i >= pieces) continue;
             if constexpr (std::is_same<O, F8>::value) {
                 uint32_t q[V / 4];
 #pragma unroll
                 for (int j = 0; j < V; j += 4)
                     q[j / 4] = pack_e4m3x4(h[p][j] * f, h[p][j + 1] * f, h[p][j + 2] * f, h[p][j + 3] * f);
                 if constexpr (V == 8)
-                    static_cast<uint2*>(a.out)[r * nv + i] = make_uint2(q[0], q[1]);
+                    store_piece<uint8_t, uint2, kOdd>(static_cast<uint8_t*>(a.out), first + i, i * V - shift, D,
+                                                      make_uint2(q[0], q[1]));
                 else
-                    static_cast<uint32_t*>(a.out)[r * nv + i] = q[0];
+                    store_piece<uint8_t, uint32_t, kOdd>(static_cast<uint8_t*>(a.out), first + i, i * V - shift, D, q[0]);
             } else {
                 uint4 o;
                 T* oe = reinterpret_cast<T*>(&o);
 #pragma unroll
                 for (int j = 0; j < V; ++j) oe[j] = from_f32<T>(h[p][j] * f);
-                static_cast<uint4*>(a.out)[r * nv + i] = o;
+                store_piece<T, uint4, kOdd>(static_cast<T*>(a.out), first + i, i * V - shift, D, o);
             }
         }
     }
@@ -250,16 +310,31 @@ cudaError_t launch(void (*kernel)(NormArgs), unsigned grid, int threads, size_t 
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <typename T, typename O, int GROUP, int P>
-cudaError_t launch_vec(const NormArgs& a, int sms, cudaStream_t s) {
+template <typename T, typename O, int GROUP, int P, bool kOdd>
+cudaError_t launch_rows(const NormArgs& a, int sms, cudaStream_t s) {
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP;
-    static const int per_sm = [] {  // of this instantiation, the same on every device the library is built for
+    static const int fit = [] {  // blocks an SM of this instantiation, the same on every device the library is built for
         int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rmsnorm_residual_vec_kernel<T, O, GROUP, P>, kBlock, 0) ==
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>, kBlock, 0) ==
                            cudaSuccess && n > 0 ? n : 1;
     }();
+    constexpr int V = 16 / (int)sizeof(T);
+    const size_t smem = kOdd ? (a.D + a.D / V) * sizeof(float) : 0;
+    int per_sm = fit;
+    if (kOdd && per_sm > (int)(220 * 1024 / (smem + 2048))) per_sm = (int)(220 * 1024 / (smem + 2048));
+    if (smem > 40 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
     const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sms * per_sm;
-    return launch(rmsnorm_residual_vec_kernel<T, O, GROUP, P>, (unsigned)(need < room ? need : room), kBlock, 0, s, a);
+    return launch(rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>, (unsigned)(need < room ? need : room), kBlock, smem, s, a);
+}
+
+template <typename T, typename O, int GROUP, int P>
+cudaError_t launch_vec(const NormArgs& a, int sms, cudaStream_t s) {
+    return a.D % (16 / (int)sizeof(T)) == 0 ? launch_rows<T, O, GROUP, P, false>(a, sms, s)
+                                            : launch_rows<T, O, GROUP, P, true>(a, sms, s);
 }
 
 template <typename T, typename O, int GROUP>
@@ -274,23 +349,27 @@ cudaError_t launch_any(const NormArgs& a, cudaStream_t s) {
     return launch(rmsnorm_residual_any_kernel<T, O, GROUP>, (unsigned)((a.rows + kRows - 1) / kRows), kBlock, smem, s, a);
 }
 
-// The group is the smallest that holds the row in at most 2 pieces a thread (4 for warps, whose
-// rows need no barrier, and for the widest rows).
+// The group is the smallest that holds the row in 2 or 3 pieces a thread (4 for warps, whose rows
+// need no barrier, and for the widest rows).
 template <typename T, typename O>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     const uintptr_t wide = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.res) |
                            reinterpret_cast<uintptr_t>(a.h) | reinterpret_cast<uintptr_t>(a.out) |
                            reinterpret_cast<uintptr_t>(a.w);
-    const int nv = a.D % V == 0 && (wide & 15u) == 0 ? a.D / V : INT32_MAX;
+    // pieces of a row (rows that are not whole pieces: with those that reach past their ends)
+    const int nv = (wide & 15u) != 0 ? INT32_MAX : a.D % V == 0 ? a.D / V : (a.D + 2 * V - 2) / V;
     int dev = 0, sms = 0;
     if (current_device_sms(&dev, &sms) != GDN_OK) return cudaErrorInvalidDevice;
     if (nv <= 32) return launch_vec<T, O, 32, 1>(a, sms, s);
     if (nv <= 64) return launch_vec<T, O, 32, 2>(a, sms, s);
     if (nv <= 128) return launch_vec<T, O, 32, 4>(a, sms, s);
     if (nv <= 256) return launch_vec<T, O, 128, 2>(a, sms, s);
+    if (nv <= 384) return launch_vec<T, O, 128, 3>(a, sms, s);
     if (nv <= 512) return launch_vec<T, O, 256, 2>(a, sms, s);
+    if (nv <= 768) return launch_vec<T, O, 256, 3>(a, sms, s);
     if (nv <= 1024) return launch_vec<T, O, 512, 2>(a, sms, s);
+    if (nv <= 1536) return launch_vec<T, O, 512, 3>(a, sms, s);
     if (nv <= 2048) return launch_vec<T, O, 512, 4>(a, sms, s);
     if (a.D <= 1024) return launch_any<T, O, 32>(a, s);
     if (a.D <= 8192) return launch_any<T, O, 256>(a, s);

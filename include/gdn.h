@@ -366,8 +366,8 @@ gdn_status gdn_prefill_gated(const void* q, const void* k, const void* v, const 
  *   eps           >= 0
  * rows in [0, 2^31), 1 <= D <= GDN_NORM_MAX_D; pointers aligned to their element;
  * residual_out and out may not be the same buffer (GDN_ERR_UNSUPPORTED).
- * Rows of whole 16-byte pieces with every pointer 16-byte aligned (and
- * D <= 16384 in bf16, 8192 in fp32) take 128-bit accesses.  One launch on `stream`.
+ * With every pointer 16-byte aligned (and D <= 16384 in bf16, 8192 in fp32; a little less
+ * where rows are not whole 16-byte pieces) the accesses are of 128 bits.  One launch on `stream`.
  */
 #define GDN_FP8_AMAX_MIN 1e-30f
 #define GDN_NORM_MAX_D 32768

@@ -240,6 +240,31 @@ def test_in_place_residual_leading_dims_and_streams(gdn):
     assert gdn.linear(torch.empty(0, 256, dtype=torch.bfloat16, device="cuda"), t["weight"]).shape == (0, 512)
 
 
+@pytest.mark.parametrize("M,N,K,dtype,layout,gated", [
+    (40000, 65536, 64, "bf16", "nk", False), (40001, 65537, 32, "f8", "nk", False), (70000, 32768, 64, "bf16", "kn", True),
+    (4, 1 << 17, 16400, "bf16", "kn", False), (3, 1 << 17, 16400, "f8", "nk", False), (140000, 16, 16384, "bf16", "nk", False),
+    (3, 1 << 16, 40000, "f32", "kn", False), (4100000, 64, 16, "bf16", "nk", False), (4194240, 3, 5, "f32", "kn", False)])
+def test_offsets_past_32_bits(gdn, M, N, K, dtype, layout, gated):
+    """Outputs, weights and rows of more than 2^31 elements, and the most rows that a call takes; a sample of
+    rows and columns at both ends is checked."""
+    gen = torch.Generator("cuda").manual_seed(N)
+    n = 2 * N if gated else N
+    x = torch.randn(M, K, generator=gen, device="cuda", dtype=torch.bfloat16).to(DT[dtype])
+    w = torch.randn(*((K, n) if layout == "kn" else (n, K)), generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = w.to(DT[dtype])
+    xs, ws = (torch.rand(M, device="cuda"), torch.rand(n, device="cuda")) if dtype == "f8" else (None, None)
+    call = gdn.linear_gated if gated else gdn.linear
+    out = call(x, w, activation="none", weight_layout=layout, x_scale=xs, weight_scale=ws)
+    rows = torch.tensor(sorted({0, M // 2, max(0, M - 130), M - 1}), device="cuda")
+    cols = torch.tensor(sorted({0, N // 2, max(0, N - 131), N - 1}), device="cuda")
+    at = torch.cat([cols, cols + N]) if gated else cols
+    pick = (lambda v: v[:, at]) if layout == "kn" else (lambda v: v.view(torch.uint8)[at].view(DT["f8"]) if dtype == "f8" else v[at])
+    xr = x.view(torch.uint8)[rows].view(DT["f8"]) if dtype == "f8" else x[rows]
+    t = dict(x=xr, weight=pick(w), bias=None, residual=None, x_scale=None if xs is None else xs[rows],
+             weight_scale=None if ws is None else ws[at])
+    _check(out[rows][:, cols], t, "none", layout, gated)
+
+
 @pytest.mark.parametrize("M,N,K,dtype", [(1, 2048, 4096, "bf16"), (64, 2048, 2048, "f8"), (1111, 1024, 512, "bf16")])
 def test_repeats_bit_for_bit(gdn, M, N, K, dtype):
     t = _draw(M, N, K, dtype, "nk", False, False, False, "f32", seed=1)

@@ -113,6 +113,36 @@ def test_in_place_and_leading_dims(gdn):
     assert scale.shape == (4, 6)
 
 
+@pytest.mark.parametrize("rows,D,dtype", [(900, 641, "bf16"), (4000, 1027, "bf16"), (700, 4099, "f32"), (5, 16381, "bf16"),
+                                          (3000, 3, "f32"), (2000, 13, "bf16")])
+def test_rows_off_16_bytes_in_place(gdn, rows, D, dtype):
+    """Rows that start anywhere in a 16-byte piece: neighbouring rows share pieces, which a row in place must
+    not disturb; more rows than run at once; guard bands behind the arrays."""
+    x, w, r = _draw(rows, D, dtype, seed=D)
+    ref = gdn.rmsnorm_residual(x, w, r)
+    _check(x, w, r, ref[0], None, ref[2])
+    xb = torch.full((rows * D + 9,), 5.0, dtype=x.dtype, device="cuda")
+    rb = torch.full((rows * D + 9,), 5.0, dtype=x.dtype, device="cuda")
+    xi, ri = xb[:rows * D].view(rows, D), rb[:rows * D].view(rows, D)
+    xi.copy_(x)
+    ri.copy_(r)
+    gdn.rmsnorm_residual(xi, w, ri, out=xi, residual_out=ri)
+    assert torch.equal(xi, ref[0]) and torch.equal(ri, ref[2])
+    assert (xb[rows * D:] == 5).all() and (rb[rows * D:] == 5).all()
+
+
+@pytest.mark.parametrize("D", [4096, 4100, 4099])
+def test_offsets_past_32_bits(gdn, D):
+    """More than 2^31 elements (8-bit output: more than 2^32 bytes of input); a sample of rows is checked."""
+    rows = 2 ** 31 // D + 70
+    gen = torch.Generator("cuda").manual_seed(D)
+    x = torch.randn(rows, D, generator=gen, device="cuda", dtype=torch.bfloat16)
+    w = torch.rand(D, generator=gen, device="cuda") + 0.5
+    q, s, _ = gdn.rmsnorm_residual(x, w, out_dtype=torch.float8_e4m3fn)
+    for r in (0, rows // 2, rows - 60, rows - 1):
+        _check(x[r:r + 1], w, None, q[r:r + 1], s[r:r + 1], None)
+
+
 @pytest.mark.parametrize("D", [256, 2048, 2049])
 def test_rows_of_zeros_infinities_and_nan(gdn, D):
     """Zero rows give zeros (and the least scale); a NaN or an infinity stays in its own row."""
