@@ -29,10 +29,25 @@ struct LinearArgs {
 // small products of operands that TMA cannot take).
 gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, int dev, int sms, cudaStream_t s, bool* taken);
 
+// gelu(v) = v Phi(v), Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by the rational approximation 7.1.26 of Abramowitz
+// and Stegun's Handbook (Hastings): erfc(z) = (a1 s + ... + a5 s^5) e^(-z^2), s = 1 / (1 + 0.3275911 z), off by
+// at most 1.5e-7, so gelu by 0.75e-7 |v|, about one rounding of v.  Half the instructions of erff: M = 16384,
+// K = 512, N = 4096 with GELU takes 96 us, and 122 with erff (without an activation 55).
+__device__ __forceinline__ float gelu(float v) {
+    const float z = fabsf(v) * 0.70710678118654752f;
+    const float s = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
+    float p = fmaf(1.061405429f, s, -1.453152027f);
+    p = fmaf(p, s, 1.421413741f);
+    p = fmaf(p, s, -0.284496736f);
+    p = fmaf(p, s, 0.254829592f);
+    const float q = 0.5f * p * s * __expf(-z * z);  // Phi(-|v|)
+    return v * (v > 0.f ? 1.f - q : q);  // (+infinity stays)
+}
+
 __device__ __forceinline__ float activate(int act, float v) {
     switch (act) {  // uniform over the grid
         case GDN_ACT_SILU: return silu_fast(v);
-        case GDN_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+        case GDN_ACT_GELU: return gelu(v);
         case GDN_ACT_RELU: return v < 0.f ? 0.f : v;  // NaN stays NaN
         default: return v;
     }

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
 
 // ------------------------------------------------------------------ many tokens
 constexpr int kLargeStages = 10;
-constexpr uint32_t kSwapBytes = 4 * 2 * 32 * 32 * 4;  // gated: 4 warp pairs x 2 directions x 32 values x 32 lanes
+constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 directions x 16 values x 32 lanes
 constexpr uint32_t kBoxRow = 128;                  // a staged output row: 64 bf16 columns
 
 struct LargeBars {
@@ -281,9 +281,14 @@ struct LargeBars {
     int abort;
 };
 
-// Shared memory of the staged output boxes: two of 64 tokens (gated 32) x 64 columns for two warps.
+// A tile's tokens are worked off in chunks of 32, the first half of them (rounded up) by the first four
+// epilogue warps, the rest by the others: this warp's first chunk and their number.
+__device__ __forceinline__ int first_chunk(const TcArgs& t, int half) { return half ? (t.bn / 32 + 1) / 2 : 0; }
+__device__ __forceinline__ int chunks_of(const TcArgs& t, int half) { return (t.bn / 32 + 1 - half) / 2; }
+
+// Shared memory of the staged output boxes: one a chunk, of 32 tokens (gated 16) x 64 columns, for two warps.
 __host__ __device__ inline uint32_t box_bytes(const TcArgs& t) {
-    return t.staged ? kEpiWarps / 2 * 2 * (t.a.gated ? 32 : 64) * kBoxRow : 0;
+    return t.staged ? kEpiWarps / 2 * ((t.bn / 32 + 1) / 2) * (t.a.gated ? 16 : 32) * kBoxRow : 0;
 }
 
 // The tile of a pair's turn: n tiles walk in groups of t.group, tokens inside a group, so that the
@@ -375,7 +380,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     const LinearArgs& a = t.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int quad = warp & 3, half = (warp - 2) >> 2;
-    const int hc = t.bn / 2;  // this warp's columns: [half * hc, half * hc + hc)
+    const int c_lo = first_chunk(t, half) * 32, hc = chunks_of(t, half) * 32;  // this warp's columns of the tile
     const int row = quad * 32 + lane;
     // gated: rows 0 .. 63 (quadrants 0, 1) are the gate's, the others the up half's; a warp of each
     // exchange their factors, gate rows finish a chunk's first 16 tokens and up rows its last 16
@@ -397,14 +402,14 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
         const bool live = n < a.N;
         const float ws = a.w_scale && live ? a.w_scale[col] : 1.f;
         const float bias = a.bias && live ? a.bias[col] : 0.f;
-        const int m_lo = tm * t.bn + half * hc;
+        const int m_lo = tm * t.bn + c_lo;
         uint32_t res[C];
         if (a.res && live) load_residual<C>(a, res, m_lo + own, n);
         const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag));
         // one answer for both warps of a gated pair, which meet at a barrier below
         if (GATED ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
         tc_fence_after();
-        const uint32_t src = tmem + b * t.bn + half * hc + ((uint32_t)(quad * 32) << 16);
+        const uint32_t src = tmem + b * t.bn + c_lo + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
         for (int c = 0; c < hc; c += 32) {
             const int m0 = m_lo + c;
@@ -448,18 +453,18 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     }
 }
 
-// The same for bf16 outputs that TMA can store (N a multiple of 8, 16-byte aligned; bn >= 128).  Two
-// warps (64 TMEM lanes) fill boxes of 64 tokens.  They read TMEM in the layout of 8x8 fragments, in
-// which a thread has pairs of neighbouring tokens: packed to bf16, four fragments a stmatrix land
-// transposed, as a row of 64 columns (128 bytes, a whole line) a token, with an eighth of the
-// shared-memory stores that single elements take and no address arithmetic; a TMA store takes the box
-// away (and clips it to the matrix).  The residual comes the same way back: a TMA load into the box
-// while the tile's products run, and ldmatrix.  The two warps meet twice a tile (boxes free, boxes full).
+// The same for bf16 outputs that TMA can store (N a multiple of 8, 16-byte aligned).  Two warps (64 TMEM
+// lanes) fill boxes of a chunk's 32 tokens.  They read TMEM in the layout of 8x8 fragments, in which a
+// thread has pairs of neighbouring tokens: packed to bf16, four fragments a stmatrix land transposed, as a
+// row of 64 columns (128 bytes, a whole line) a token, with an eighth of the shared-memory stores that
+// single elements take and no address arithmetic; a TMA store takes the box away (and clips it to the
+// matrix).  The residual comes the same way back: a TMA load into the box while the tile's products run,
+// and ldmatrix.  The two warps meet twice a tile (boxes free, boxes full).
 template <bool GATED>
 __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorMap* tm_out, const CUtensorMap* tm_res,
                                                 LargeBars* bars, uint8_t* boxes, float* swap, uint32_t tmem, int rank,
                                                 int pair, int pairs, int tiles) {
-    constexpr int kTokens = GATED ? 32 : 64;  // of 64 tokens, those that this warp finishes
+    constexpr int kTokens = GATED ? 16 : 32;  // of a chunk's 32 tokens, those that this warp finishes
     constexpr int kPieces = kTokens / 8;      // fragments of 8 tokens among them
     constexpr uint32_t kBoxBytes = kTokens * kBoxRow;
     const LinearArgs& a = t.a;
@@ -467,49 +472,49 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
     const int quad = warp & 3, half = (warp - 2) >> 2, duo = quad >> 1;
     const bool issuer = (quad & 1) == 0;  // of the two warps of a box
     const bool up = GATED && duo == 1;
-    const int own = up ? 32 : 0;  // gated: gate rows finish the first 32 of 64 tokens, up rows the others
-    // the warps that share boxes (gated: all four of a half of the tokens); the warps of a gate and its up rows
+    const int own = up ? 16 : 0;  // gated: gate rows finish a chunk's first 16 tokens, up rows the others
+    // the warps that share boxes (gated: all four of a half of the chunks); the warps of a gate and its up rows
     const uint32_t box_bar = GATED ? 1 + half : 1 + half * 2 + duo, box_threads = GATED ? 128 : 64;
     const uint32_t swap_bar = 5 + half * 2 + (quad & 1);
-    float* sw = swap + (half * 2 + (quad & 1)) * (2 * 32 * 32) + lane;  // gated: [up][32 values][lane]
-    uint8_t* box = boxes + (half * 2 + duo) * 2 * kBoxBytes;
+    float* sw = swap + (half * 2 + (quad & 1)) * (2 * 2 * 16 * 32) + lane;  // gated: [turn][up][16 values][lane]
+    const int c_lo = first_chunk(t, half) * 32, chunks = chunks_of(t, half);
+    uint8_t* box = boxes + (half * 2 + duo) * ((t.bn / 32 + 1) / 2) * kBoxBytes;
     uint64_t* res_full = &bars->res_full[half * 2 + duo];
     volatile int* abort_flag = &bars->abort;
     const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
-    const int hc = t.bn / 2, per_tile = hc / 64;
     const bool has_res = a.res != nullptr;
-    // first column of the boxes and first token of this half of a tile
     Tiles walk;
+    // first column of the boxes and first token of these chunks of a tile
     auto place = [&](int turn, int* n, int* m) {
         int tn, tm;
         walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
         *n = (tn * 2 + rank) * (GATED ? 64 : 128) + (GATED ? 0 : duo * 64);
-        *m = tm * t.bn + half * hc;
+        *m = tm * t.bn + c_lo;
     };
-    // whether a tile has residual boxes here (those past the matrix are not loaded), and their loads (one lane)
-    auto some = [&](int n, int m) { return has_res && n < a.N && m + own < a.M; };
-    auto fetch_residual = [&](int n, int m) {
-        if (!some(n, m)) return;
-        const int count = per_tile == 2 && m + 64 + own < a.M ? 2 : 1;
+    // a tile's boxes here that hold something of the matrix
+    auto boxes_in = [&](int n, int m) { return n < a.N ? max(0, min(chunks, (a.M - m - own + 31) / 32)) : 0; };
+    auto fetch_residual = [&](int n, int m) {  // one lane
+        const int count = has_res ? boxes_in(n, m) : 0;
+        if (count == 0) return;
         mbar_arrive_expect_tx(res_full, count * kBoxBytes);
-        for (int i = 0; i < count; ++i) tma_load_3d(box + i * kBoxBytes, tm_res, res_full, n, m + i * 64 + own, 0);
+        for (int i = 0; i < count; ++i) tma_load_3d(box + i * kBoxBytes, tm_res, res_full, n, m + i * 32 + own, 0);
     };
-    auto load_scales = [&](float (&xs)[16], int m) {  // of tokens m + 8 k + 2 (lane % 4) + {0, 1}
+    auto load_scales = [&](float (&xs)[8], int m) {  // of tokens m + 8 k + 2 (lane % 4) + {0, 1}
 #pragma unroll
-        for (int k = 0; k < 16; ++k) xs[k] = a.x_scale[min(m + 8 * (k >> 1) + 2 * (lane & 3) + (k & 1), a.M - 1)];
+        for (int k = 0; k < 8; ++k) xs[k] = a.x_scale[min(m + 8 * (k >> 1) + 2 * (lane & 3) + (k & 1), a.M - 1)];
     };
-    int n_box = a.N, m_tile = a.M, turn = 0;
+    int n_box = a.N, m_tile = a.M, turn = 0, flip = 0;
     uint32_t phase = 0;  // parity of the next residual
     bool ok = true;
     if (pair < tiles) place(0, &n_box, &m_tile);
     if (issuer && elect_one()) fetch_residual(n_box, m_tile);
     __syncwarp();
-    bool in_flight = some(n_box, m_tile);  // the residual of the tile has been asked for and not been waited for
+    bool in_flight = has_res && boxes_in(n_box, m_tile) > 0;  // the tile's residual has been asked for, not waited for
     for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
-        const int b = turn & 1;
+        const int b = turn & 1, live = boxes_in(n_box, m_tile);
         int n_next = a.N, m_next = a.M;
         if (tile + pairs < tiles) place(turn + 1, &n_next, &m_next);
-        float ws[2][2], bias[2][2], xs[16];
+        float ws[2][2], bias[2][2], xs[8];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -534,14 +539,16 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
         }
         if (named_bar_any(box_bar, box_threads, !ok)) break;  // the boxes are free; and one answer for all who meet here
         tc_fence_after();
-        for (int sub = 0; sub < per_tile; ++sub) {
-            const bool live = n_box < a.N && m_tile + sub * 64 + own < a.M;
-            float v[2][32];  // 16 columns (TMEM lanes) each
+        // (Two chunks at a time, or the next one read ahead, gain nothing: the code of an activation over 64 values
+        // is fetched anew at every tile.  M = 16384, K = 512, N = 4096 with GELU: 96 us so, 152 with two.)
+#pragma unroll 1
+        for (int chunk = 0; chunk < chunks; ++chunk) {
+            float v[2][16];  // 16 columns (TMEM lanes) each
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                tmem_ld16x256_x8(tmem + b * t.bn + half * hc + sub * 64 + ((uint32_t)(quad * 32 + 16 * h) << 16), v[h]);
+                tmem_ld16x256_x4(tmem + b * t.bn + c_lo + chunk * 32 + ((uint32_t)(quad * 32 + 16 * h) << 16), v[h]);
             tmem_wait_ld();
-            if (sub == per_tile - 1) {  // the accumulator is read
+            if (chunk == chunks - 1) {  // the accumulator is read
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(b ? done1 : done0);
@@ -550,46 +557,45 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[h][j] *= xs[2 * (j >> 2) + (j & 1)] * ws[h][(j >> 1) & 1];
-                if (sub + 1 < per_tile) load_scales(xs, m_tile + (sub + 1) * 64);
+                    for (int j = 0; j < 16; ++j) v[h][j] *= xs[2 * (j >> 2) + (j & 1)] * ws[h][(j >> 1) & 1];
+                if (chunk + 1 < chunks) load_scales(xs, m_tile + (chunk + 1) * 32);
             }
             if (a.bias) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[h][j] += bias[h][(j >> 1) & 1];
+                    for (int j = 0; j < 16; ++j) v[h][j] += bias[h][(j >> 1) & 1];
             }
             if constexpr (!GATED) {
-                activate_all<32>(a.act, v[0]);
-                activate_all<32>(a.act, v[1]);
+                activate_all<16>(a.act, v[0]);
+                activate_all<16>(a.act, v[1]);
             } else {
-                if (sub > 0) named_bar_sync(swap_bar, 64);  // the last values are read (between tiles: box_bar)
-                // gate rows hand over their last 32 tokens and up rows their first 32
+                // gate rows hand over their last 16 tokens and up rows their first 16, through two buffers in turn
+                // (the barrier of the exchange in between tells that a buffer has been read)
+                float* ex = sw + flip * (2 * 16 * 32);
+                flip ^= 1;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) sw[(own + 16 * h + j) * 32] = up ? v[h][j] : v[h][16 + j];
+                    for (int j = 0; j < 8; ++j) ex[(own + 8 * h + j) * 32] = up ? v[h][j] : v[h][8 + j];
                 named_bar_sync(swap_bar, 64);
+                float g[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float g[16];
+                for (int j = 0; j < 16; ++j) g[j] = up ? ex[j * 32] : v[j >> 3][j & 7];
+                activate_all<16>(a.act, g);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) g[j] = up ? sw[(16 * h + j) * 32] : v[h][j];
-                    activate_all<16>(a.act, g);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[h][j] = g[j] * (up ? v[h][16 + j] : sw[(32 + 16 * h + j) * 32]);
-                }
+                for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] = g[j] * (up ? v[j >> 3][8 + (j & 7)] : ex[(16 + j) * 32]);
             }
-            if (live) {
-                const uint32_t at = smem_u32(box + sub * kBoxBytes);
+            if (chunk < live) {
+                const uint32_t at = smem_u32(box + chunk * kBoxBytes);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int k = 0; k < kPieces; k += 2) {
                         // matrix lane / 8 of the four: tokens 8 (k + its high bit), columns 16 h + 8 (its low bit)
                         const uint32_t token = 8 * (k + (lane >> 4)) + (lane & 7);
-                        const uint32_t chunk = 4 * (quad & 1) + 2 * h + ((lane >> 3) & 1);
-                        const uint32_t addr = at + token * kBoxRow + ((chunk ^ (token & 7)) << 4);
+                        const uint32_t column = 4 * (quad & 1) + 2 * h + ((lane >> 3) & 1);  // in pieces of 8
+                        const uint32_t addr = at + token * kBoxRow + ((column ^ (token & 7)) << 4);
                         float* f = &v[h][4 * k];
                         if (has_res) {
                             uint32_t r[4];
@@ -608,9 +614,7 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
         }
         named_bar_sync(box_bar, box_threads);  // the boxes are full
         if (issuer && elect_one()) {
-            for (int sub = 0; sub < per_tile; ++sub)
-                if (n_box < a.N && m_tile + sub * 64 + own < a.M)
-                    tma_store_3d(tm_out, box + sub * kBoxBytes, n_box, m_tile + sub * 64 + own, 0);
+            for (int i = 0; i < live; ++i) tma_store_3d(tm_out, box + i * kBoxBytes, n_box, m_tile + i * 32 + own, 0);
             tma_store_commit();
             if (has_res) {  // the next tile's residual takes the boxes as soon as they are read
                 tma_store_wait_read0();
@@ -620,7 +624,7 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
         __syncwarp();
         n_box = n_next;
         m_tile = m_next;
-        in_flight = some(n_box, m_tile);
+        in_flight = has_res && boxes_in(n_box, m_tile) > 0;
     }
     if (in_flight) (void)mbar_wait(res_full, phase);  // gave up: the load lands first (bounded)
     __syncwarp();
@@ -845,17 +849,17 @@ struct Plan {
 // graph over weights larger than L2):
 //   - small: one CTA takes in about 85 KB/us and two on an SM 115, all together at most 6.3 MB/us; the
 //     partial sums' way through TMEM and shared memory costs 0.3 + bn / 60, a third more over 8 CTAs.  M = 64, K = N = 2048: 12.4 (32 tokens, no split), 8.3 (2), 6.8 (4), 6.9 (8);
-//   - pairs: 0.20 us a slab up to 128 tokens and 0.28 at 256 (the tensor cores' time), 1 us more set-up
-//     and an epilogue of bn / 200.  M = 512, K = N = 4096: 20.8 the best small plan, 18.5 pairs at 128,
+//   - pairs: 0.28 us a slab at 256 tokens (the tensor cores' time), in proportion down to 0.20 (its issue),
+//     1 us more set-up and an epilogue of bn / 200.  M = 512, K = N = 4096: 20.8 the best small plan, 18.5 pairs at 128,
 //     23.2 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
 Plan plan(const LinearArgs& a, int slabs, int sms) {
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
     const double weight_mb = tiles1 * slabs * (16.0 / 1024);
     Plan best{true, 256, 1};
     double least = 1e30;
-    for (int bn = 64; bn <= 256; bn *= 2) {
+    for (int bn = 256; bn >= 64; bn -= 32) {
         const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
-        double t = 1.0 + bn / 200.0 + (double)turns * slabs * (bn == 256 ? 0.28 : 0.20);
+        double t = 1.0 + bn / 200.0 + (double)turns * slabs * (bn > 182 ? bn * (0.28 / 256) : 0.20);
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
         if (t < least) least = t, best = Plan{true, bn, 1};
     }
@@ -930,12 +934,13 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     if ((long long)t.tiles_n * t.tiles_m > INT32_MAX - sms) return GDN_ERR_DIMS;
     t.group = t.tiles_n < 16 ? t.tiles_n : 16;
     t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
-    t.staged = !a.out_f32 && a.N % 8 == 0 && t.bn >= 128 &&
+    t.staged = !a.out_f32 && a.N % 8 == 0 &&
                ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.res)) & 15u) == 0;
     const size_t fixed = sizeof(LargeBars) + box_bytes(t) + (a.gated ? kSwapBytes : 0) + 1024;
     t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
     if (t.stages > kLargeStages) t.stages = kLargeStages;
-    t.tmem_cols = 2 * t.bn;
+    t.tmem_cols = 128;
+    while (t.tmem_cols < 2 * (uint32_t)t.bn) t.tmem_cols <<= 1;
     t.idesc = f8 ? make_idesc_e4m3(256, t.bn) : make_idesc_bf16(256, t.bn, a.nk ? 0 : 1, 0);
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
@@ -944,7 +949,7 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
         !encode(&tx, f8, op.x, a.M, a.K, op.x_pitch, t.bn / 2))
         return GDN_ERR_CUDA;
     CUtensorMap to{}, tr{};
-    const int tokens = a.gated ? 32 : 64;
+    const int tokens = a.gated ? 16 : 32;
     if (t.staged && (!encode(&to, false, a.out, a.M, a.N, a.N, tokens) ||
                      (a.res && !encode(&tr, false, a.res, a.M, a.N, a.N, tokens))))
         return GDN_ERR_CUDA;

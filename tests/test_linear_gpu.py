@@ -145,7 +145,11 @@ def test_epilogues(gdn, M, N, K, dtype, act, gated, bias, residual, out):
 
 @pytest.mark.parametrize("M,N,K,dtype,layout,gated", [
     (4096, 2048, 2048, "bf16", "kn", False), (3001, 1501, 1040, "bf16", "nk", False), (2050, 1030, 2048, "f8", "nk", True),
-    (1500, 4104, 648, "bf16", "kn", True), (5000, 300, 256, "f8", "nk", False), (1, 16384, 8192, "bf16", "nk", False)])
+    (1500, 4104, 648, "bf16", "kn", True), (5000, 300, 256, "f8", "nk", False),
+    # token tiles of every width from 64 to 256
+    (1003, 5000, 512, "bf16", "nk", False), (1024, 5120, 256, "bf16", "kn", False), (1531, 2600, 384, "f8", "nk", True),
+    (930, 4096, 256, "f8", "nk", False), (1300, 3400, 256, "bf16", "nk", True), (2222, 2048, 320, "bf16", "kn", False),
+    (640, 6000, 264, "bf16", "nk", False), (1100, 4999, 256, "bf16", "nk", False), (377, 9001, 256, "f8", "nk", True), (1, 16384, 8192, "bf16", "nk", False)])
 def test_larger(gdn, M, N, K, dtype, layout, gated):
     _run(gdn, M, N, K, dtype, layout, gated, "silu" if gated else "none", residual=True)
 
@@ -214,6 +218,16 @@ def test_nan_and_infinity_stay_in_their_rows_and_columns(gdn, M, dtype):
     assert got[rest].isfinite().all()
     col = torch.cat([got[:i, j], got[i + 1:, j]])
     assert not col.isfinite().any()
+
+
+def test_activations_over_their_range(gdn):
+    """gelu within its approximation's 0.75e-7 |v| and 8 roundings of v, silu within 16 roundings of the value."""
+    v = torch.cat([torch.linspace(-14, 14, 40001), torch.logspace(-30, 1, 4000), -torch.logspace(-30, 1, 4000)])
+    w = torch.ones(1, 1, device="cuda")
+    for act, bar in (("gelu", lambda r: (0.75e-7 + 8 * U) * v.abs().numpy()), ("silu", lambda r: 16 * U * np.abs(r))):
+        ref = layer.activation(act, v.double().numpy())
+        got = gdn.linear(v.cuda()[:, None].contiguous(), w, activation=act).flatten().cpu().double().numpy()
+        assert (np.abs(got - ref) <= bar(ref) + 1e-37).all(), act
 
 
 def test_activations_at_their_ends(gdn):
