@@ -44,7 +44,7 @@ EXPORTED = ("gdn_prefill", "gdn_decode_step", "gdn_prefill_workspace_bytes", "gd
             "gdn_decode_gated", "gdn_decode_block_workspace_bytes", "gdn_decode_block", "gdn_rmsnorm_gated",
             "gdn_prefill_gated", "gdn_prefill_segments", "gdn_decode_block_noalloc",
             "gdn_set_wait_limit_ns", "gdn_test_stall_prefill", "gdn_prefill_ws", "gdn_prefill_segment_starts",
-            "gdn_rmsnorm_residual", "gdn_linear")
+            "gdn_rmsnorm_residual", "gdn_linear", "gdn_linear_ws", "gdn_linear_workspace_bytes")
 
 
 class GdnDims(ctypes.Structure):
@@ -136,6 +136,10 @@ def lib() -> ctypes.CDLL:
                                            ctypes.c_int32, ctypes.c_float, vp]
         L.gdn_linear.restype = ctypes.c_int
         L.gdn_linear.argtypes = [vp, fp, vp, fp, fp, vp, vp, ctypes.POINTER(GdnLinearDims), vp]
+        L.gdn_linear_ws.restype = ctypes.c_int
+        L.gdn_linear_ws.argtypes = L.gdn_linear.argtypes[:-1] + [vp, ctypes.c_size_t, vp]
+        L.gdn_linear_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_linear_workspace_bytes.argtypes = [vp, vp, ctypes.POINTER(GdnLinearDims)]
         _lib = L
     return _lib
 
@@ -681,8 +685,17 @@ def _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weigh
         bp = _layer_ptr("bias", bias, (cols,), _T.float32, device)
     if residual is not None:
         rp = _layer_ptr("residual", residual, oshape, out_dtype, device)
-    _layer_call(_lib.gdn_linear, device, stream, x.data_ptr(), xsp, wp, wsp, bp, rp, op,
-                GdnLinearDims(M, N, K, code, ocode, act, flags))
+    xp, dims, ws, need = x.data_ptr(), GdnLinearDims(M, N, K, code, ocode, act, flags), None, 0
+    if code == GDN_F32 or (xp | wp | K * (3 - code) | (cols * (3 - code) if weight_layout == "kn" else 0)) & 15 or \
+            (flags & GDN_LINEAR_GATED and weight_layout == "kn" and N & 7):
+        # operands that are laid out anew: the scratch comes from torch, which keeps it between calls
+        need = _lib.gdn_linear_workspace_bytes(xp, wp, dims)
+        if need:
+            ws = _layer_empty((need,), _T.uint8, device, stream)
+    if ws is None:
+        _layer_call(_lib.gdn_linear, device, stream, xp, xsp, wp, wsp, bp, rp, op, dims)
+    else:
+        _layer_call(_lib.gdn_linear_ws, device, stream, xp, xsp, wp, wsp, bp, rp, op, dims, ws.data_ptr(), need)
     return out
 
 

@@ -69,7 +69,7 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t u, uint64_t v) {
 
 // kNK: the weight is [N', K]; splits: CTAs of the cluster, each with its part of K (TM = 4 only).
 template <typename T, int TM, bool kNK, bool kVec>
-__global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_constant__ LinearArgs a, int splits) {
+__global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_constant__ LinearArgs a, int splits, const uint8_t* unfit, int marks) {
     constexpr int SIDE = 16, kThreads = SIDE * SIDE, kTile = TM * SIDE, kPitch = kTile + 4;
     constexpr int kQuads = kTile * kBK / 4 / kThreads;       // 4-element loads a thread
     constexpr int kAhead = TM == 8 ? 1 : 4;                  // steps loaded ahead
@@ -86,6 +86,11 @@ __global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_consta
     const int k_hi = rank + 1 == splits ? a.K : (int)((long long)steps * (rank + 1) / splits) * kBK;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
+    if (unfit) {  // only for operands that the tensor cores' parts do not fit (one answer for the whole grid)
+        int any = 0;
+        for (int i = tid; i < marks; i += kThreads) any |= unfit[i];
+        if (!__syncthreads_or(any)) return;
+    }
     // This thread's pieces: of x (and of a [N', K] weight) 4 elements of K of rows tid / 4 + i kThreads / 4, of a
     // [K, N'] weight 4 columns of one k.  Their addresses at k = 0, and how many elements of the piece's
     // own direction exist (columns: up to 4; rows: all or none).
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_consta
 }
 
 template <typename T, int TM, bool kNK, bool kVec>
-cudaError_t launch_tile(const LinearArgs& a, int splits, cudaStream_t s) {
+cudaError_t launch_tile(const LinearArgs& a, int splits, const LinearMarks& marks, cudaStream_t s) {
     const int tile = 16 * TM, cols = a.gated ? tile / 2 : tile;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((a.N + (long long)cols - 1) / cols * splits), (unsigned)((a.M + (long long)tile - 1) / tile));
@@ -286,34 +291,33 @@ cudaError_t launch_tile(const LinearArgs& a, int splits, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_ffma_kernel<T, TM, kNK, kVec>, a, splits);
+    return cudaLaunchKernelEx(&cfg, linear_ffma_kernel<T, TM, kNK, kVec>, a, splits, marks.unfit, marks.count);
 }
 
 template <typename T, int TM>
-cudaError_t launch_layout(const LinearArgs& a, int splits, cudaStream_t s) {
+cudaError_t launch_layout(const LinearArgs& a, int splits, const LinearMarks& marks, cudaStream_t s) {
     // pieces of 4 elements: rows that they divide, from an address that they divide
     auto four = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % (4 * sizeof(T)) == 0; };
     const long long wn = a.gated ? 2LL * a.N : a.N;
     const bool vec = four(a.x) && four(a.w) && a.K % 4 == 0 && (a.nk || (wn % 4 == 0 && a.N % 4 == 0));
     if constexpr (!std::is_same<T, __nv_fp8_e4m3>::value) {  // e4m3 weights are [N', K]
-        if (!a.nk) return vec ? launch_tile<T, TM, false, true>(a, splits, s) : launch_tile<T, TM, false, false>(a, splits, s);
+        if (!a.nk) return vec ? launch_tile<T, TM, false, true>(a, splits, marks, s) : launch_tile<T, TM, false, false>(a, splits, marks, s);
     }
-    return vec ? launch_tile<T, TM, true, true>(a, splits, s) : launch_tile<T, TM, true, false>(a, splits, s);
+    return vec ? launch_tile<T, TM, true, true>(a, splits, marks, s) : launch_tile<T, TM, true, false>(a, splits, marks, s);
 }
 
 template <typename T>
-cudaError_t launch_ffma(const LinearArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_ffma(const LinearArgs& a, int sms, const LinearMarks& marks, cudaStream_t s) {
     const long long wn = a.gated ? 2LL * a.N : a.N;
     auto tiles = [&](int t) { return ((a.M + (long long)t - 1) / t) * ((wn + t - 1) / t); };
-    if (tiles(128) >= sms) return launch_layout<T, 8>(a, 1, s);
+    if (tiles(128) >= sms) return launch_layout<T, 8>(a, 1, marks, s);
     // Small products: 64-wide tiles, and K over as many CTAs as give two an SM (4 steps of K each at least).
     int splits = 1;
     while (splits < 8 && tiles(64) * splits * 2 <= 2LL * sms && a.K >= kBK * 4 * 2 * splits) splits *= 2;
-    return launch_layout<T, 4>(a, splits, s);
+    return launch_layout<T, 4>(a, splits, marks, s);
 }
 
-gdn_status check_linear(const void* x, const float* x_scale, const void* w, const float* w_scale, const float* bias,
-                        const void* res, const void* out, const gdn_linear_dims* d) {
+gdn_status check_dims(const gdn_linear_dims* d) {
     if (!d) return GDN_ERR_NULL;
     const bool f8 = d->dtype == GDN_F8E4M3, f32 = d->dtype == GDN_F32;
     if (!f8 && !f32 && d->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
@@ -326,7 +330,14 @@ gdn_status check_linear(const void* x, const float* x_scale, const void* w, cons
     const long long lim = INT32_MAX - 256;  // tile origins are 32-bit in the kernels
     if (d->M > 64LL * 65535 || d->N > lim || d->K > lim || ((d->flags & GDN_LINEAR_GATED) && d->N > lim / 2))
         return GDN_ERR_DIMS;  // (the FFMA kernel's grid has at most 65535 tiles of 64 tokens)
-    if (d->M == 0) return GDN_OK;
+    return GDN_OK;
+}
+
+gdn_status check_linear(const void* x, const float* x_scale, const void* w, const float* w_scale, const float* bias,
+                        const void* res, const void* out, const gdn_linear_dims* d) {
+    const gdn_status st = check_dims(d);
+    if (st != GDN_OK || d->M == 0) return st;
+    const bool f8 = d->dtype == GDN_F8E4M3, f32 = d->dtype == GDN_F32;
     if (!x || !w || !out || (f8 && (!x_scale || !w_scale))) return GDN_ERR_NULL;
     if (!f8 && (x_scale || w_scale)) return GDN_ERR_UNSUPPORTED;
     auto off = [](const void* p, uintptr_t size) { return (reinterpret_cast<uintptr_t>(p) & (size - 1)) != 0; };
@@ -341,24 +352,59 @@ gdn_status check_linear(const void* x, const float* x_scale, const void* w, cons
 
 using namespace gdn;
 
+namespace {
+
+LinearArgs args_of(const void* x, const float* x_scale, const void* weight, const float* weight_scale, const float* bias,
+                   const void* residual, void* out, const gdn_linear_dims* d) {
+    return LinearArgs{x, x_scale, weight, weight_scale, bias, residual, out, (int)d->M, (int)d->N, (int)d->K, d->activation,
+                      d->out_dtype == GDN_F32, (d->flags & GDN_LINEAR_GATED) != 0, (d->flags & GDN_LINEAR_WEIGHT_NK) != 0};
+}
+
+LinearPlan plan_of(const LinearArgs& a, const gdn_linear_dims* d) {
+    if (d->flags & GDN_LINEAR_FORCE_FFMA) return LinearPlan{LinearRoute::kFfma, 0};
+    return plan_linear(a, d->dtype);
+}
+
+}  // namespace
+
+extern "C" size_t gdn_linear_workspace_bytes(const void* x, const void* weight, const gdn_linear_dims* d) {
+    if (check_dims(d) != GDN_OK || d->M == 0) return 0;
+    return plan_of(args_of(x, nullptr, weight, nullptr, nullptr, nullptr, nullptr, d), d).scratch;
+}
+
+extern "C" gdn_status gdn_linear_ws(const void* x, const float* x_scale, const void* weight, const float* weight_scale,
+                                    const float* bias, const void* residual, void* out, const gdn_linear_dims* d,
+                                    void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+    gdn_status st = check_linear(x, x_scale, weight, weight_scale, bias, residual, out, d);
+    if (st != GDN_OK) return st;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15u) return GDN_ERR_ALIGN;
+    if (d->M == 0) return GDN_OK;
+    const LinearArgs a = args_of(x, x_scale, weight, weight_scale, bias, residual, out, d);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    LinearPlan how = plan_of(a, d);
+    if (workspace && workspace_bytes < how.scratch) return GDN_ERR_WORKSPACE;
+    int dev = 0, sms = 0;
+    if (current_device_sms(&dev, &sms) != GDN_OK) return GDN_ERR_CUDA;
+    void* own = nullptr;
+    if (how.scratch > 0 && !workspace && cudaMallocAsync(&own, how.scratch, s) != cudaSuccess) {
+        (void)cudaGetLastError();
+        how.route = LinearRoute::kFfma;  // needs none
+    }
+    LinearMarks marks{nullptr, 0};
+    if (how.route != LinearRoute::kFfma)
+        st = launch_linear_tc(a, d->dtype, how.route, own ? own : workspace, dev, sms, s, &marks);
+    if (st == GDN_OK && (how.route == LinearRoute::kFfma || how.route == LinearRoute::kParts)) {
+        const cudaError_t e = d->dtype == GDN_F32    ? launch_ffma<float>(a, sms, marks, s)
+                              : d->dtype == GDN_BF16 ? launch_ffma<__nv_bfloat16>(a, sms, marks, s)
+                                                     : launch_ffma<__nv_fp8_e4m3>(a, sms, marks, s);
+        if (e != cudaSuccess) st = GDN_ERR_CUDA;
+    }
+    if (own && cudaFreeAsync(own, s) != cudaSuccess && st == GDN_OK) st = GDN_ERR_CUDA;
+    return st;
+}
+
 extern "C" gdn_status gdn_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale,
                                  const float* bias, const void* residual, void* out, const gdn_linear_dims* d,
                                  gdn_stream_t stream) {
-    const gdn_status st = check_linear(x, x_scale, weight, weight_scale, bias, residual, out, d);
-    if (st != GDN_OK || d->M == 0) return st;
-    const LinearArgs a{x, x_scale, weight, weight_scale, bias, residual, out, (int)d->M, (int)d->N, (int)d->K,
-                       d->activation, d->out_dtype == GDN_F32, (d->flags & GDN_LINEAR_GATED) != 0,
-                       (d->flags & GDN_LINEAR_WEIGHT_NK) != 0};
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    int dev = 0, sms = 0;
-    if (current_device_sms(&dev, &sms) != GDN_OK) return GDN_ERR_CUDA;
-    if (!(d->flags & GDN_LINEAR_FORCE_FFMA)) {
-        bool taken = false;
-        const gdn_status tc = launch_linear_tc(a, d->dtype, dev, sms, s, &taken);
-        if (taken || tc != GDN_OK) return tc;
-    }
-    const cudaError_t e = d->dtype == GDN_F32    ? launch_ffma<float>(a, sms, s)
-                          : d->dtype == GDN_BF16 ? launch_ffma<__nv_bfloat16>(a, sms, s)
-                                                 : launch_ffma<__nv_fp8_e4m3>(a, sms, s);
-    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return gdn_linear_ws(x, x_scale, weight, weight_scale, bias, residual, out, d, nullptr, 0, stream);
 }

@@ -25,9 +25,24 @@ struct LinearArgs {
     bool nk;       // weight layout
 };
 
-// The tensor-core kernels (linear_tc.cu).  *taken: whether they do the call (they do not for fp32, nor for
-// small products of operands that TMA cannot take).
-gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, int dev, int sms, cudaStream_t s, bool* taken);
+// How a product is done (linear_tc.cu): on the tensor cores as it lies, from copies of operands that TMA cannot
+// take, from bf16 parts of fp32 operands, or by the FFMA kernel; and the scratch that this takes.
+enum class LinearRoute { kTensor, kCopies, kParts, kFfma };
+struct LinearPlan {
+    LinearRoute route;
+    size_t scratch;
+};
+LinearPlan plan_linear(const LinearArgs& a, int32_t dtype);
+
+// Marks of blocks that met an infinity or a NaN, known on the device: with any of them the product by parts has
+// not been done, and the FFMA kernel behind it does it (else that one does nothing).
+struct LinearMarks {
+    const uint8_t* unfit;
+    int count;
+};
+// Enqueues every route but kFfma; marks are set for kParts.
+gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, LinearRoute route, void* scratch, int dev, int sms,
+                            cudaStream_t s, LinearMarks* marks);
 
 // gelu(v) = v Phi(v), Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by the rational approximation 7.1.26 of Abramowitz
 // and Stegun's Handbook (Hastings): erfc(z) = (a1 s + ... + a5 s^5) e^(-z^2), s = 1 / (1 + 0.3275911 z), off by

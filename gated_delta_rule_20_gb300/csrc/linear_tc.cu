@@ -42,6 +42,7 @@ constexpr int kSlabBytes = 128;                  // bytes of K a stage
 constexpr uint32_t kWBytes = 128 * kSlabBytes;   // a CTA's 128 weight columns of a slab
 constexpr uint32_t kHalfW = kWBytes / 2;         // one box of 64
 constexpr int kMaxStages = 12;
+constexpr int kMaxAccs = 4;
 
 struct TcArgs {
     LinearArgs a;
@@ -53,6 +54,9 @@ struct TcArgs {
     int tiles_n, tiles_m, group;    // large kernel: the tile grid, n tiles walked together
     bool staged;                    // large kernel: bf16 output (and residual) by TMA
     int32_t* status;
+    int accs, starts[kMaxAccs];     // fp32 by parts: accumulators of a tile, each from its first slab (else one)
+    const uint8_t* unfit;           // fp32 by parts: marks of `marks` blocks; any of them: not for this kernel
+    int marks;
 };
 
 constexpr int kEpiWarps = 8;                    // two a TMEM lane quadrant, half of the columns each
@@ -74,6 +78,32 @@ struct Ring {
             s = 0;
             phase ^= 1;
         }
+    }
+};
+
+// The accumulator of a tile that slab k goes to.
+__device__ __forceinline__ int acc_at(const TcArgs& t, int k) {
+    int q = 0;
+    for (int i = 1; i < t.accs; ++i) q += k >= t.starts[i];
+    return q;
+}
+// The same for slab after slab from k_lo: one comparison a slab.
+template <bool PARTS>
+struct AccWalk {
+    int q = 0, next = INT32_MAX;
+    __device__ __forceinline__ AccWalk(const TcArgs& t, int k_lo) {
+        if constexpr (PARTS) {
+            q = acc_at(t, k_lo);
+            look(t);
+        }
+    }
+    __device__ __forceinline__ void look(const TcArgs& t) { next = q + 1 < t.accs ? t.starts[q + 1] : INT32_MAX; }
+    // Slab k: whether it is the first of its accumulator.
+    __device__ __forceinline__ bool step(const TcArgs& t, int k) {
+        if (!PARTS || k != next) return false;
+        ++q;
+        look(t);
+        return true;
     }
 };
 
@@ -144,7 +174,15 @@ __device__ __forceinline__ void join_splits(const TcArgs& t, uint32_t part, int 
     }
 }
 
-template <bool F8, bool KN>
+// Whether any block has left its mark, for all threads of the CTA.
+__device__ __forceinline__ bool any_mark(const uint8_t* marks, int count) {
+    int any = 0;
+    for (int i = threadIdx.x; i < count; i += (int)blockDim.x) any |= marks[i];
+    return __syncthreads_or(any) != 0;
+}
+
+// PARTS: an fp32 product by bf16 parts (several accumulators a tile, marks).
+template <bool F8, bool KN, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                            const __grid_constant__ CUtensorMap tm_x,
                                                            const __grid_constant__ TcArgs t) {
@@ -183,8 +221,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     griddep_wait();  // the preceding kernel's results; nothing of the caller's is read before
+    const bool run = !(PARTS && any_mark(t.unfit, t.marks));  // one answer for the whole grid
 
-    if (warp == 0) {  // TMA producer
+    if (warp == 0 && run) {  // TMA producer
         int loaded = 0;
         Ring at;
         for (int i = 0; i < k_hi - k_lo; ++i, at.next(stages)) {
@@ -203,15 +242,17 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
         // every issued load has landed before the CTA can exit (bounded)
         for (int i = (loaded > stages ? loaded - stages : 0); i < loaded; ++i)
             (void)mbar_wait(&bars->full[i % stages], (i / stages) & 1);
-    } else if (warp == 1) {  // MMA issuer
+    } else if (warp == 1 && run) {  // MMA issuer
         int issued = 0;
         Ring at;
+        AccWalk<PARTS> acc(t, k_lo);
         for (int i = 0; i < k_hi - k_lo; ++i, at.next(stages)) {
             const int s = at.s;
             if (!mbar_wait_warp(&bars->full[s], at.phase, abort_flag)) break;
             tc_fence_after();
+            const bool first = acc.step(t, k_lo + i) || i == 0;
             if (elect_one()) {
-                mma_slab<F8, KN, false>(tmem, smem_u32(sm) + s * t.stage_bytes, t.idesc, i == 0);
+                mma_slab<F8, KN, false>(tmem + acc.q * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, first);
                 mma_commit(&bars->empty[s]);
                 if (i + 1 == k_hi - k_lo) mma_commit(&bars->done);
             }
@@ -227,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     const int cols = min(t.bn, a.M - m0);
     const int e = tid - 64;  // epilogue thread
     bool ok = false;
-    if (warp >= 2) {
+    if (warp >= 2 && run) {
         ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->done, 0, abort_flag));  // one answer a warp
         tc_fence_after();
         if (ok) {
@@ -238,6 +279,18 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
                 tmem_ld8(lanes + c0, v[0]);
                 tmem_ld8(lanes + c0 + 8, v[1]);
                 tmem_wait_ld();
+                if constexpr (PARTS) {  // the sum of the accumulators that this rank's slabs went to
+                    float sum[16] = {};
+                    for (int q = acc_at(t, k_lo); q <= acc_at(t, k_hi - 1); ++q) {
+                        tmem_ld8(lanes + q * t.bn + c0, v[0]);
+                        tmem_ld8(lanes + q * t.bn + c0 + 8, v[1]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[j] += v[j / 8][j % 8];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = sum[j];
+                }
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     if (c0 + j < cols) part[(c0 + j) * 128 + row] = v[j / 8][j % 8];
@@ -299,6 +352,13 @@ __device__ __forceinline__ void tile_at(const TcArgs& t, int i, int* n, int* m) 
     *m = in / width;
     *n = g * t.group + in - *m * width;
 }
+
+// Tiles take the two accumulators in turns; fp32 by parts takes all of TMEM for every tile.  The (first)
+// accumulator of a turn, and how many tiles have had it before.
+template <bool PARTS>
+__device__ __forceinline__ int acc_of(int turn) { return PARTS ? 0 : turn & 1; }
+template <bool PARTS>
+__device__ __forceinline__ int acc_use(int turn) { return PARTS ? turn : turn >> 1; }
 
 // The tiles of a pair in turn, for a converged warp: every lane works out one of the next 32 (the
 // divisions take a few hundred cycles, which would stall the loads at every tile), and hands it out.
@@ -373,7 +433,7 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const
 // The epilogue warps of linear_large_kernel, for any output: every tile of the pair, 32 tokens at a time.  The first
 // residual values of a tile are loaded before its products are done, the next chunk's before this
 // one's are used.
-template <bool GATED>
+template <bool GATED, bool PARTS>
 __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float* swap, uint32_t tmem, int rank, int pair,
                                          int pairs, int tiles) {
     constexpr int C = GATED ? 16 : 32;  // tokens of a chunk that this warp finishes
@@ -393,7 +453,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     int turn = 0, flip = 0;
     Tiles walk;
     for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
-        const int b = turn & 1;
+        const int b = acc_of<PARTS>(turn);
         int tn, tm;
         walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
         // this thread's weight column and the output that it belongs to
@@ -405,7 +465,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
         const int m_lo = tm * t.bn + c_lo;
         uint32_t res[C];
         if (a.res && live) load_residual<C>(a, res, m_lo + own, n);
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], (turn >> 1) & 1, abort_flag));
+        const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], acc_use<PARTS>(turn) & 1, abort_flag));
         // one answer for both warps of a gated pair, which meet at a barrier below
         if (GATED ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
         tc_fence_after();
@@ -420,6 +480,16 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
             for (int j = 0; j < C; ++j) r[j] = res[j];
             if (a.res && live && c + 32 < hc) load_residual<C>(a, res, m0 + 32 + own, n);
             tmem_wait_ld();
+            for (int q = 1; PARTS && q < t.accs; ++q) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    float w[8];
+                    tmem_ld8(src + q * t.bn + c + i, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i + j] += w[j];
+                }
+            }
             if (c + 32 >= hc) {  // the accumulator is read: the next product may overwrite it
                 tc_fence_before();
                 __syncwarp();
@@ -632,7 +702,7 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
     __syncwarp();
 }
 
-template <bool F8, bool KN>
+template <bool F8, bool KN, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_large_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_res,
@@ -675,8 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     griddep_wait();
+    const bool run = !(PARTS && any_mark(t.unfit, t.marks));  // one answer for the whole grid
 
-    if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
+    if (!run) {
+    } else if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
         int i = 0;    // slabs loaded
         bool live = true;
         Tiles walk;
@@ -713,9 +785,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             Ring at;
             bool live = true;
             for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
-                const int b = turn & 1;
-                if (turn >= 2 && !mbar_wait_warp(&bars->acc_empty[b], ((turn >> 1) - 1) & 1, abort_flag)) break;
+                const int b = acc_of<PARTS>(turn), use = acc_use<PARTS>(turn);
+                if (use >= 1 && !mbar_wait_warp(&bars->acc_empty[b], (use - 1) & 1, abort_flag)) break;
                 tc_fence_after();
+                AccWalk<PARTS> acc(t, 0);
                 for (int k = 0; k < t.slabs; ++k, ++i, at.next(stages)) {
                     const int s = at.s;
                     if (!mbar_wait_warp(&bars->full[s], at.phase, abort_flag)) {
@@ -723,8 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     tc_fence_after();
+                    const bool first = acc.step(t, k) || k == 0;
                     if (elect_one()) {
-                        mma_slab<F8, KN, true>(tmem + b * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, k == 0);
+                        mma_slab<F8, KN, true>(tmem + (b + acc.q) * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, first);
                         mma_commit_pair(&bars->empty[s]);
                         if (k + 1 == t.slabs) mma_commit_pair(&bars->acc_full[b]);
                     }
@@ -733,15 +807,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (i > 0) (void)mbar_wait(&bars->empty[(i - 1) % stages], ((i - 1) / stages) & 1);  // all products are done
         }
-    } else if (t.staged) {
+    } else if (!PARTS && t.staged) {
         if (a.gated)
             epilogue_staged<true>(t, &tm_out, &tm_res, bars, boxes, swap, tmem, rank, pair, pairs, tiles);
         else
             epilogue_staged<false>(t, &tm_out, &tm_res, bars, boxes, swap, tmem, rank, pair, pairs, tiles);
     } else if (a.gated) {
-        epilogue<true>(t, bars, swap, tmem, rank, pair, pairs, tiles);
+        epilogue<true, PARTS>(t, bars, swap, tmem, rank, pair, pairs, tiles);
     } else {
-        epilogue<false>(t, bars, swap, tmem, rank, pair, pairs, tiles);
+        epilogue<false, PARTS>(t, bars, swap, tmem, rank, pair, pairs, tiles);
     }
     __syncwarp();
     tc_fence_before();
@@ -827,13 +901,16 @@ struct Operands {
     const void *x, *w;
     long long x_pitch, w_pitch, w_cols;
     int up;
+    const uint8_t* unfit = nullptr;  // see TcArgs
+    int marks = 0;
+    int accs = 1, starts[kMaxAccs] = {};
 };
 
-template <bool F8, bool KN>
+template <bool F8, bool KN, bool PARTS>
 cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
                          int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_small_kernel<F8, KN>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), kThreads, smem,
+    return launch(linear_small_kernel<F8, KN, PARTS>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), kThreads, smem,
                   t.splits, s, tw, tx, t);
 }
 
@@ -852,18 +929,18 @@ struct Plan {
 //   - pairs: 0.28 us a slab at 256 tokens (the tensor cores' time), in proportion down to 0.20 (its issue),
 //     1 us more set-up and an epilogue of bn / 200.  M = 512, K = N = 4096: 20.8 the best small plan, 18.5 pairs at 128,
 //     23.2 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
-Plan plan(const LinearArgs& a, int slabs, int sms) {
+Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
     const double weight_mb = tiles1 * slabs * (16.0 / 1024);
     Plan best{true, 256, 1};
     double least = 1e30;
-    for (int bn = 256; bn >= 64; bn -= 32) {
+    for (int bn = accs > 1 ? 512 / accs / 32 * 32 : 256; bn >= 64; bn -= 32) {  // (TMEM: 512 columns)
         const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
         double t = 1.0 + bn / 200.0 + (double)turns * slabs * (bn > 182 ? bn * (0.28 / 256) : 0.20);
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
         if (t < least) least = t, best = Plan{true, bn, 1};
     }
-    for (int bn = 16; bn <= 128; bn *= 2) {
+    for (int bn = 16; bn <= (accs > 1 ? 256 / accs : 128); bn *= 2) {  // (two CTAs an SM share TMEM)
         if (bn > 16 && bn / 2 >= a.M) break;
         const long long tiles_m = (a.M + bn - 1) / bn;
         if (tiles_m > 65535) continue;  // the grid's limit
@@ -888,6 +965,10 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     TcArgs t{};
     t.a = a;
     t.up = op.up;
+    t.unfit = op.unfit;
+    t.marks = op.marks;
+    t.accs = op.accs;
+    for (int q = 0; q < kMaxAccs; ++q) t.starts[q] = op.starts[q];
     const int elems = f8 ? 128 : 64, per = a.gated ? 64 : 128;
     t.slabs = (a.K + elems - 1) / elems;
     t.bn = how.bn;
@@ -899,7 +980,7 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.stages = (int)((112 * 1024 - sizeof(SmallBars) - 1024) / t.stage_bytes);  // two CTAs an SM
     if (t.stages > kMaxStages) t.stages = kMaxStages;
     t.tmem_cols = 32;
-    while (t.tmem_cols < (uint32_t)t.bn) t.tmem_cols <<= 1;
+    while (t.tmem_cols < (uint32_t)(t.accs * t.bn)) t.tmem_cols <<= 1;
     t.idesc = f8 ? make_idesc_e4m3(128, t.bn) : make_idesc_bf16(128, t.bn, a.nk ? 0 : 1, 0);
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
@@ -908,17 +989,19 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
         !encode(&tx, f8, op.x, a.M, a.K, op.x_pitch, t.bn))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + sizeof(SmallBars) + 1024;
-    const cudaError_t e = f8     ? launch_small<true, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
-                          : a.nk ? launch_small<false, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
-                                 : launch_small<false, true>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s);
+    const cudaError_t e = f8              ? launch_small<true, false, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
+                          : op.accs == 1 ? (a.nk ? launch_small<false, false, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
+                                                 : launch_small<false, true, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s))
+                          : a.nk         ? launch_small<false, false, true>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
+                                         : launch_small<false, true, true>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
-template <bool F8, bool KN>
+template <bool F8, bool KN, bool PARTS>
 cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& to,
                          const CUtensorMap& tr, int pairs, size_t smem, int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_large_kernel<F8, KN>, done, dev, dim3((unsigned)(2 * pairs)), kThreads, smem, 2, s, tw, tx, to,
+    return launch(linear_large_kernel<F8, KN, PARTS>, done, dev, dim3((unsigned)(2 * pairs)), kThreads, smem, 2, s, tw, tx, to,
                   tr, t);
 }
 
@@ -926,6 +1009,10 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     TcArgs t{};
     t.a = a;
     t.up = op.up;
+    t.unfit = op.unfit;
+    t.marks = op.marks;
+    t.accs = op.accs;
+    for (int q = 0; q < kMaxAccs; ++q) t.starts[q] = op.starts[q];
     const int elems = f8 ? 128 : 64, per = a.gated ? 128 : 256;
     t.slabs = (a.K + elems - 1) / elems;
     t.tiles_n = (int)(((long long)a.N + per - 1) / per);
@@ -940,7 +1027,7 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
     if (t.stages > kLargeStages) t.stages = kLargeStages;
     t.tmem_cols = 128;
-    while (t.tmem_cols < 2 * (uint32_t)t.bn) t.tmem_cols <<= 1;
+    while (t.tmem_cols < (uint32_t)((t.accs > 2 ? t.accs : 2) * t.bn)) t.tmem_cols <<= 1;
     t.idesc = f8 ? make_idesc_e4m3(256, t.bn) : make_idesc_bf16(256, t.bn, a.nk ? 0 : 1, 0);
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
@@ -955,9 +1042,11 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
     const int tiles = t.tiles_n * t.tiles_m, pairs = tiles < sms / 2 ? tiles : sms / 2;
-    const cudaError_t e = f8     ? launch_large<true, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
-                          : a.nk ? launch_large<false, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
-                                 : launch_large<false, true>(t, tw, tx, to, tr, pairs, smem, dev, s);
+    const cudaError_t e = f8              ? launch_large<true, false, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
+                          : op.accs == 1 ? (a.nk ? launch_large<false, false, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
+                                                 : launch_large<false, true, false>(t, tw, tx, to, tr, pairs, smem, dev, s))
+                          : a.nk         ? launch_large<false, false, true>(t, tw, tx, to, tr, pairs, smem, dev, s)
+                                         : launch_large<false, true, true>(t, tw, tx, to, tr, pairs, smem, dev, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -995,60 +1084,123 @@ __global__ void __launch_bounds__(256) linear_align_kernel(const __grid_constant
     }
 }
 
+// fp32 operands as three bf16 parts each: x = x1 + x2 + x3, every part the rounding of what the ones before
+// leave (24 bits in three times 8, so the sum is exact).  Of the nine products of parts the six of 2^-16 and
+// more are taken, the five small ones into an accumulator of their own:
+//     x' = [x1 x3 x2 x1 x2 | x1],  w' = [w3 w1 w2 w2 w1 | w1]  along K.
+// The tensor cores truncate a sum at every step of 16 terms, always towards zero, so that it falls short by
+// about K 1e-9 of itself (2.1e-6 at K = 2048; fp32 sums with rounding 0.8e-6).  The x1 w1, whose sum that is,
+// therefore go to an accumulator for every 704 of K, three at the most, which are added with rounding.
+constexpr int kParts = 6;
+__device__ __constant__ const uint8_t kPartOf[2][kParts] = {{0, 2, 1, 0, 1, 0}, {2, 0, 1, 1, 0, 0}};  // x, w
+
+// Splits one operand: rows_in x cols fp32 -> rows_out x width parts, rows `pitch` apart and copies `plane`
+// apart; columns as in CopyJob, what lies outside is zero.
+struct SplitJob {
+    const float* src;
+    __nv_bfloat16* dst;
+    long long rows_in, rows_out, cols, width, pitch, plane, half, up;
+};
+
+// marks[block]: whether the block met an infinity or a NaN, for which parts do not add up.
+__global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ SplitJob x, const __grid_constant__ SplitJob w,
+                                                           uint8_t* marks) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const long long x_pieces = x.rows_out * (x.width / 8), pieces = x_pieces + w.rows_out * (w.width / 8);
+    int bad = 0;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (long long)gridDim.x * 256) {
+        const int which = i < x_pieces ? 0 : 1;
+        const SplitJob& c = which == 0 ? x : w;
+        const long long at = which == 0 ? i : i - x_pieces, row = at / (c.width / 8), d0 = at % (c.width / 8) * 8;
+        const float* src = c.src + row * c.cols;
+        __nv_bfloat16 part[3][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const long long d = d0 + j, from = d < c.half ? d : d >= c.up ? c.half + d - c.up : c.cols;
+            const float v = row < c.rows_in && from < c.cols ? src[from] : 0.f;
+            bad |= !(fabsf(v) <= 3.4028235e38f);
+            // (a rounding past the largest bf16 would be an infinity: truncated instead)
+            __nv_bfloat16 p = fabsf(v) >= 3.38e38f ? __float2bfloat16_rz(v) : __float2bfloat16_rn(v);
+            part[0][j] = p;
+            float left = v - __bfloat162float(p);
+            part[1][j] = p = __float2bfloat16_rn(left);
+            left -= __bfloat162float(p);
+            part[2][j] = __float2bfloat16_rn(left);
+        }
+        uint4 o[3];
+        memcpy(o, part, sizeof(o));
+        uint4* dst = reinterpret_cast<uint4*>(c.dst + row * c.pitch + d0);
+#pragma unroll
+        for (int k = 0; k < kParts; ++k) dst[k * (c.plane / 8)] = o[kPartOf[which][k]];
+    }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0) marks[blockIdx.x] = bad != 0;
+}
+
 // Whether TMA can take an operand of `cols`-element rows as it lies.
 bool takes(const void* p, long long cols, int size) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && cols * size % 16 == 0;
 }
 
 gdn_status run_tc(const LinearArgs& a, const Operands& op, bool f8, int dev, int sms, cudaStream_t s) {
-    const Plan how = plan(a, (a.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64), sms);
+    const Plan how = plan(a, (a.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64), op.accs, sms);
     return how.large ? run_large(a, op, f8, how, dev, sms, s) : run_small(a, op, f8, how, dev, s);
 }
 
-}  // namespace
-
-gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, int dev, int sms, cudaStream_t s, bool* taken) {
-    *taken = false;
-    if (dtype != GDN_BF16 && dtype != GDN_F8E4M3) return GDN_OK;
-    const bool f8 = dtype == GDN_F8E4M3;
-    const int size = f8 ? 1 : 2, piece = 16 / size;
-    const long long wn = a.gated ? 2LL * a.N : a.N, w_row = a.nk ? a.K : wn, w_rows = a.nk ? wn : a.K;
-    Operands op{a.x, a.w, a.K, w_row, wn, a.N};
-    const bool x_fits = takes(a.x, a.K, size);
-    // the up half's boxes of a [K, 2 N] weight start at column N, which TMA wants on 16 bytes too
-    const bool w_fits = takes(a.w, w_row, size) && (a.nk || !a.gated || a.N % piece == 0);
-    if (x_fits && w_fits) {
-        *taken = true;
-        return run_tc(a, op, f8, dev, sms, s);
-    }
-    // Operands that do not fit are copied to aligned rows first, where that pays: the copies and the scratch
-    // cost about 10 us and then HBM's rate, the FFMA kernel does 45 TFLOP/s.  M = 4000, K = 3001, N = 5000
-    // (bf16): 2.9 ms by FFMA.
-    if (2.0 * a.M * wn * a.K < 1e9) return GDN_OK;
+// What the two routes that lay operands out anew need: the jobs (without their destinations), and their bytes.
+void copy_jobs(const LinearArgs& a, int size, CopyJob* x, CopyJob* w) {
+    const int piece = 16 / size;
+    const long long wn = a.gated ? 2LL * a.N : a.N, w_row = a.nk ? a.K : wn;
     auto up_to = [&](long long n) { return (n + piece - 1) / piece * piece; };
-    CopyJob x{a.x, nullptr, 0, a.K, up_to(a.K), a.K, up_to(a.K)}, w{a.w, nullptr, 0, w_row, up_to(w_row), w_row, up_to(w_row)};
-    if (!x_fits) x.rows = a.M;
-    if (!w_fits) {
-        w.rows = w_rows;
-        if (!a.nk && a.gated) {  // both halves start on a piece
-            w.half = a.N;
-            w.up = up_to(a.N);
-            w.pitch = 2 * w.up;
-        }
+    *x = CopyJob{a.x, nullptr, 0, a.K, up_to(a.K), a.K, up_to(a.K)};
+    *w = CopyJob{a.w, nullptr, 0, w_row, up_to(w_row), w_row, up_to(w_row)};
+    if (!takes(a.x, a.K, size)) x->rows = a.M;
+    // the up half's boxes of a [K, 2 N] weight start at column N, which TMA wants on 16 bytes too
+    const bool halves = !a.nk && a.gated;
+    if (takes(a.w, w_row, size) && (!halves || a.N % piece == 0)) return;
+    w->rows = a.nk ? wn : a.K;
+    if (halves) {  // both halves start on a piece
+        w->half = a.N;
+        w->up = up_to(a.N);
+        w->pitch = 2 * w->up;
     }
-    const size_t x_bytes = (size_t)(x.rows * x.pitch * size), bytes = x_bytes + (size_t)(w.rows * w.pitch * size);
-    void* scratch = nullptr;
-    if (cudaMallocAsync(&scratch, bytes, s) != cudaSuccess) {
-        (void)cudaGetLastError();
-        return GDN_OK;  // the FFMA kernel needs none
+}
+size_t job_bytes(const CopyJob& c, int size) { return (size_t)(c.rows * c.pitch * size); }
+
+void split_jobs(const LinearArgs& a, SplitJob* x, SplitJob* w) {
+    const long long wn = a.gated ? 2LL * a.N : a.N;
+    auto up_to = [](long long n) { return (n + 7) / 8 * 8; };
+    const long long kp = (a.K + 63) / 64 * 64LL;  // whole slabs a term
+    *x = SplitJob{static_cast<const float*>(a.x), nullptr, a.M, a.M, a.K, kp, kParts * kp, kp, kp, kp};
+    *w = *x;
+    w->src = static_cast<const float*>(a.w);
+    if (a.nk) {
+        w->rows_in = w->rows_out = wn;
+        return;
     }
-    *taken = true;
-    if (!x_fits) {
+    w->rows_in = a.K;
+    w->rows_out = kp;
+    w->cols = wn;
+    w->half = a.gated ? a.N : up_to(wn);
+    w->up = a.gated ? up_to(a.N) : up_to(wn);
+    w->width = w->pitch = a.gated ? 2 * w->up : up_to(wn);
+    w->plane = kp * w->pitch;
+}
+size_t job_bytes(const SplitJob& c, bool planes) { return (size_t)((planes ? kParts * c.plane : c.rows_out * c.pitch) * 2); }
+constexpr int kSplitBlocks = 1216;  // (8 a GB300's SM)
+
+gdn_status run_copies(const LinearArgs& a, bool f8, uint8_t* scratch, int dev, int sms, cudaStream_t s) {
+    const int size = f8 ? 1 : 2;
+    CopyJob x, w;
+    copy_jobs(a, size, &x, &w);
+    Operands op{a.x, a.w, a.K, w.cols, a.gated ? 2LL * a.N : a.N, a.N};
+    if (x.rows) {
         op.x = x.dst = scratch;
         op.x_pitch = x.pitch;
     }
-    if (!w_fits) {
-        op.w = w.dst = static_cast<uint8_t*>(scratch) + x_bytes;
+    if (w.rows) {
+        op.w = w.dst = scratch + job_bytes(x, size);
         op.w_pitch = w.pitch;
         if (!a.nk && a.gated) {
             op.up = (int)w.up;
@@ -1059,9 +1211,64 @@ gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, int dev, int sms
         linear_align_kernel<uint8_t><<<8 * sms, 256, 0, s>>>(x, w);
     else
         linear_align_kernel<uint16_t><<<8 * sms, 256, 0, s>>>(x, w);
-    gdn_status st = cudaGetLastError() == cudaSuccess ? run_tc(a, op, f8, dev, sms, s) : GDN_ERR_CUDA;
-    if (cudaFreeAsync(scratch, s) != cudaSuccess && st == GDN_OK) st = GDN_ERR_CUDA;
-    return st;
+    return cudaGetLastError() == cudaSuccess ? run_tc(a, op, f8, dev, sms, s) : GDN_ERR_CUDA;
+}
+
+gdn_status run_parts(const LinearArgs& a, uint8_t* scratch, int dev, int sms, cudaStream_t s, LinearMarks* marks) {
+    SplitJob x, w;
+    split_jobs(a, &x, &w);
+    x.dst = reinterpret_cast<__nv_bfloat16*>(scratch);
+    w.dst = reinterpret_cast<__nv_bfloat16*>(scratch + job_bytes(x, false));
+    uint8_t* unfit = scratch + job_bytes(x, false) + job_bytes(w, !a.nk);
+    *marks = LinearMarks{unfit, kSplitBlocks};
+    linear_split_kernel<<<kSplitBlocks, 256, 0, s>>>(x, w, unfit);
+    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    LinearArgs b = a;
+    b.K = (int)x.pitch;
+    const bool halves = !a.nk && a.gated;
+    Operands op{x.dst, w.dst, x.pitch, w.pitch, halves ? w.up + a.N : a.gated ? 2LL * a.N : a.N, halves ? (int)w.up : a.N};
+    op.unfit = unfit;
+    op.marks = kSplitBlocks;
+    // the x1 w1 terms: an accumulator for every 704 of K, three at the most
+    const int small = (int)((kParts - 1) * x.plane / 64), main = (int)(x.plane / 64);
+    const int wanted = (main + 10) / 11 < kMaxAccs - 1 ? (main + 10) / 11 : kMaxAccs - 1, share = (main + wanted - 1) / wanted;
+    op.accs = 1 + (main + share - 1) / share;
+    for (int q = 1; q < op.accs; ++q) op.starts[q] = small + (q - 1) * share;
+    return run_tc(b, op, false, dev, sms, s);
+}
+
+}  // namespace
+
+LinearPlan plan_linear(const LinearArgs& a, int32_t dtype) {
+    const double ops = 2.0 * a.M * (a.gated ? 2LL * a.N : a.N) * a.K;
+    if (dtype == GDN_F32) {
+        // Worth the split and two more launches (about 15 us) from 3e8 operations: M = 333, K = 770, N = 1030 takes the
+        // FFMA kernel 35 us.  Up to K = 4096 the accumulators' truncation stays near the error of fp32 sums (at 2048
+        // 7e-7 and 8e-7 of the result).
+        if (ops < 3e8 || a.K > 4096 || a.M < 32) return LinearPlan{LinearRoute::kFfma, 0};
+        SplitJob x, w;
+        split_jobs(a, &x, &w);
+        const size_t bytes = job_bytes(x, false) + job_bytes(w, !a.nk) + kSplitBlocks;
+        return bytes > (size_t)4 << 30 ? LinearPlan{LinearRoute::kFfma, 0} : LinearPlan{LinearRoute::kParts, bytes};
+    }
+    const int size = dtype == GDN_BF16 ? 2 : 1;
+    CopyJob x, w;
+    copy_jobs(a, size, &x, &w);
+    if (x.rows == 0 && w.rows == 0) return LinearPlan{LinearRoute::kTensor, 0};
+    // Copies cost about 10 us and then HBM's rate, the FFMA kernel does 45 TFLOP/s: M = 4000, K = 3001, N = 5000
+    // (bf16) 100 us and 2.6 ms.
+    if (ops < 1e9) return LinearPlan{LinearRoute::kFfma, 0};
+    return LinearPlan{LinearRoute::kCopies, job_bytes(x, size) + job_bytes(w, size)};
+}
+
+gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, LinearRoute route, void* scratch, int dev, int sms,
+                            cudaStream_t s, LinearMarks* marks) {
+    uint8_t* p = static_cast<uint8_t*>(scratch);
+    const bool f8 = dtype == GDN_F8E4M3;
+    if (route == LinearRoute::kParts) return run_parts(a, p, dev, sms, s, marks);
+    if (route == LinearRoute::kCopies) return run_copies(a, f8, p, dev, sms, s);
+    const long long wn = a.gated ? 2LL * a.N : a.N;
+    return run_tc(a, Operands{a.x, a.w, a.K, a.nk ? a.K : wn, wn, a.N}, f8, dev, sms, s);
 }
 
 }  // namespace gdn

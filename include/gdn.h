@@ -414,17 +414,37 @@ typedef struct {
  *   bias         [N'] fp32, or NULL
  *   residual     [M, N] in out_dtype, or NULL; may be out (in place)
  *   out          [M, N] in out_dtype
- * Pointers aligned to their element.  fp32 compute runs on an FFMA kernel, bf16 and e4m3 on
- * the tensor cores, in one launch on `stream`, where x and the weight are 16-byte aligned with
- * rows of a multiple of 16 bytes (a gated [K, 2 N] weight: also N).  An operand that is not is
- * copied to such rows first (one more launch; scratch from cudaMallocAsync on `stream`, freed
- * there) where the product is large enough to pay for it (1e9 operations); smaller ones, and
- * calls whose scratch cannot be had, run on the FFMA kernel.  Results do not depend on what
- * else runs: every sum has one order for given arguments and device.
+ * Pointers aligned to their element.  bf16 and e4m3 run on the tensor cores, in one launch on
+ * `stream`, where x and the weight are 16-byte aligned with rows of a multiple of 16 bytes (a
+ * gated [K, 2 N] weight: also N).  An operand that is not is copied to such rows first (one more
+ * launch) where the product is large enough to pay for it (1e9 operations), and smaller ones run
+ * on an FFMA kernel.  fp32 runs on the FFMA kernel, from 3e8 operations, 32 rows and up to
+ * K = 4096 on the tensor cores: the operands are split into three bf16 parts each, which add up
+ * exactly, and the products of parts down to 2^-16 are summed in fp32 (three launches; operands
+ * with infinities or NaN are found on the device and left to the FFMA kernel).  Copies and parts
+ * lie in scratch from cudaMallocAsync on `stream`, freed there (gdn_linear_ws takes it from the
+ * caller); calls whose scratch cannot be had, or would pass 4 GiB of parts, run on the FFMA
+ * kernel.  Results do not depend on what else runs: every sum has one order for given arguments
+ * and device.
  */
 gdn_status gdn_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale,
                       const float* bias, const void* residual, void* out, const gdn_linear_dims* dims,
                       gdn_stream_t stream);
+
+/* Device scratch of a gdn_linear call with these operands (only their alignment matters) and
+ * dims: 0 where none is needed, and for invalid dims.  Host only. */
+size_t gdn_linear_workspace_bytes(const void* x, const void* weight, const gdn_linear_dims* dims);
+
+/*
+ * gdn_linear_ws -- gdn_linear with its scratch supplied by the caller, so that the call
+ * allocates nothing: device memory of workspace_bytes >= gdn_linear_workspace_bytes(x, weight,
+ * dims) bytes, 16-byte aligned, not touched by anything else until the call's work on `stream`
+ * has finished; NULL: the call behaves exactly like gdn_linear.  A workspace that is too small
+ * returns GDN_ERR_WORKSPACE (misaligned: GDN_ERR_ALIGN) and launches nothing.
+ */
+gdn_status gdn_linear_ws(const void* x, const float* x_scale, const void* weight, const float* weight_scale,
+                         const float* bias, const void* residual, void* out, const gdn_linear_dims* dims,
+                         void* workspace, size_t workspace_bytes, gdn_stream_t stream);
 
 /* Device scratch a prefill with these dims needs on the current device: the
  * segment states, maps and identity-start outputs of a split (see gdn_prefill;

@@ -65,6 +65,33 @@ def test_linear_argument_checks(L):
     assert call(**dict(f8, xs=P + 2)) == gdn.GDN_ERR_ALIGN and call(**dict(f8, ws=P + 2)) == gdn.GDN_ERR_ALIGN
 
 
+def test_linear_workspace(L):
+    """The scratch of a product: none for operands that the tensor cores take as they lie or that are small, and
+    what the copies or parts need otherwise; a workspace that is too small or misaligned is refused."""
+    def need(M, N, K, dtype=gdn.GDN_BF16, out=gdn.GDN_F32, flags=0, x=P, w=P):
+        return L.gdn_linear_workspace_bytes(x, w, ctypes.byref(gdn.GdnLinearDims(M, N, K, dtype, out, 0, flags)))
+    nk, gated, ffma = gdn.GDN_LINEAR_WEIGHT_NK, gdn.GDN_LINEAR_GATED, gdn.GDN_LINEAR_FORCE_FFMA
+    assert need(4096, 4096, 4096) == 0 and need(4096, 4096, 4096, flags=nk) == 0
+    assert need(10, 11, 13) == 0                                        # FFMA kernel
+    assert need(1000, 1000, 1001) == 1000 * 1008 * 2                    # x only: the [K, N] weight's rows fit
+    assert need(1000, 1000, 1001, flags=nk) == 2 * 1000 * 1008 * 2
+    assert need(1000, 1001, 1000) == 1000 * 1008 * 2                    # the weight only
+    assert need(1000, 1001, 1000, flags=nk) == 0
+    assert need(1000, 1004, 1000, flags=gated) == 1000 * 2 * 1008 * 2   # its halves do not start on 16 bytes
+    assert need(1000, 1000, 1000, x=P + 2) == 1000 * 1000 * 2
+    assert need(1000, 1000, 1001, gdn.GDN_F8E4M3, flags=nk) == 2 * 1000 * 1008
+    assert need(1000, 1000, 1001, flags=ffma) == 0
+    assert need(1000, 1000, 1000, gdn.GDN_F32) >= 6 * 2 * 2 * 1000 * 1024   # six parts of both
+    assert need(1000, 1000, 8192, gdn.GDN_F32) == 0 and need(8, 10000, 4096, gdn.GDN_F32) == 0
+    assert need(1000000, 1000, 4096, gdn.GDN_F32) == 0                  # past 4 GiB
+    assert need(0, 1000, 1001) == 0 and need(1000, 0, 1001) == 0
+    assert L.gdn_linear_workspace_bytes(P, P, None) == 0
+    d = gdn.GdnLinearDims(1000, 1000, 1001, gdn.GDN_BF16, gdn.GDN_BF16, 0, 0)
+    call = lambda ws, n: L.gdn_linear_ws(P, None, P, None, None, None, P, ctypes.byref(d), ws, n, None)  # noqa: E731
+    assert call(P, 1000 * 1008 * 2 - 1) == gdn.GDN_ERR_WORKSPACE
+    assert call(P + 8, 1 << 30) == gdn.GDN_ERR_ALIGN
+
+
 def test_binding_refuses_host_tensors():
     x, w = torch.zeros(2, 8, dtype=torch.bfloat16), torch.ones(8)
     with pytest.raises(ValueError):

@@ -181,6 +181,69 @@ def test_large_products_of_rows_off_16_bytes(gdn, M, N, K, dtype, layout, gated)
     assert torch.equal(out, got)
 
 
+@pytest.mark.parametrize("M,N,K,layout,gated", [
+    (333, 1030, 770, "kn", False), (333, 1030, 770, "nk", False), (1000, 1001, 1003, "kn", False), (600, 515, 1000, "kn", True),
+    (600, 513, 999, "nk", True), (64, 4096, 1024, "nk", False), (32, 2048, 4096, "kn", False), (3000, 700, 130, "kn", False),
+    (1024, 1024, 1024, "kn", False)])
+def test_fp32_products_by_parts(gdn, M, N, K, layout, gated):
+    """fp32 products large enough for the tensor cores (parts of 8 bits), at the bar of fp32 sums: the products
+    of parts left out are under 2 x 2^-24 of every term.  Also with operands of the widest range: the largest
+    fp32 numbers, subnormal ones, and neighbours of powers of two."""
+    assert 2 * M * N * (2 if gated else 1) * K >= 3e8
+    got, t = _run(gdn, M, N, K, "f32", layout, gated, "gelu", bias=True, residual=True)
+    gen = torch.Generator("cuda").manual_seed(K)
+    x = torch.randn(M, K, generator=gen, device="cuda") * 2.0 ** torch.randint(-40, 40, (M, 1), generator=gen, device="cuda")
+    x[1], x[2] = x[1].sign() * 2.0 ** -140, 3.4028235e38 * x[2].sign()
+    x[3] = torch.where(x[3] > 0, 1 + 2.0 ** -23, 1 - 2.0 ** -24)
+    w = t["weight"].clone()
+    w[0] *= 2.0 ** -20
+    w[-1] *= 2.0 ** -60
+    wide = dict(t, x=x, weight=w * 2.0 ** -20, bias=None, residual=None)
+    call = gdn.linear_gated if gated else gdn.linear
+    out = call(x, wide["weight"], activation="none", weight_layout=layout)
+    if gated:  # the product of two huge sums may pass fp32's range
+        keep = torch.ones(M, dtype=torch.bool, device="cuda")
+        keep[2] = False
+        out, wide["x"] = out[keep], x[keep]
+    _check(out, wide, "none", layout, gated)
+
+
+@pytest.mark.parametrize("M,N,K,dtype", [(1000, 1001, 1003, "bf16"), (500, 700, 900, "f32"), (40, 64, 64, "bf16")])
+def test_scratch_of_the_library_and_of_the_caller(gdn, M, N, K, dtype):
+    """gdn_linear (stream-ordered scratch of its own) and gdn_linear_ws give the same bits; a workspace is not
+    written past its size."""
+    import ctypes
+    from gated_delta_rule_20_gb300 import _binding as b
+    t = _draw(M, N, K, dtype, "kn", False, False, False, "f32", seed=6)
+    L, code = gdn.lib(), gdn.GDN_BF16 if dtype == "bf16" else gdn.GDN_F32
+    d = gdn.GdnLinearDims(M, N, K, code, gdn.GDN_F32, 0, 0)
+    outs = [torch.full((M, N), float("nan"), device="cuda") for _ in range(3)]
+    x, w, s = t["x"].data_ptr(), t["weight"].data_ptr(), torch.cuda.current_stream().cuda_stream
+    b._check(L.gdn_linear(x, None, w, None, None, None, outs[0].data_ptr(), ctypes.byref(d), s))
+    need = L.gdn_linear_workspace_bytes(x, w, ctypes.byref(d))
+    ws = torch.full((need + 64,), 0x5A, dtype=torch.uint8, device="cuda")
+    b._check(L.gdn_linear_ws(x, None, w, None, None, None, outs[1].data_ptr(), ctypes.byref(d), ws.data_ptr(), need, s))
+    outs[2] = gdn.linear(t["x"], t["weight"], out=outs[2])
+    torch.cuda.synchronize()
+    assert (need > 0) == (K > 64) and (ws[need:] == 0x5A).all()
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("where", ["x", "weight"])
+def test_fp32_products_with_infinities_and_nan(gdn, where, bad, gated):
+    """An operand that has one is left to the FFMA kernel: the same bits as when it is asked for, and the
+    residual in place is added once."""
+    t = _draw(400, 500, 900, "f32", "nk", gated, False, True, "f32", seed=3)
+    t[where][77, 11] = bad
+    call = gdn.linear_gated if gated else gdn.linear
+    ref = call(t["x"], t["weight"], None, t["residual"], activation="silu", weight_layout="nk", force_ffma=True)
+    r = t["residual"].clone()
+    got = call(t["x"], t["weight"], None, r, activation="silu", weight_layout="nk", out=r)
+    assert torch.equal(got.view(torch.int32), ref.view(torch.int32)) and not torch.isfinite(ref).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 128, 128), (300, 264, 192)])
 @pytest.mark.parametrize("dtype", ["bf16", "f8"])
 def test_tensor_cores_agree_with_ffma(gdn, M, N, K, dtype):
