@@ -34,7 +34,7 @@ struct LinearPlan {
 };
 LinearPlan plan_linear(const LinearArgs& a, int32_t dtype);
 
-// Marks of blocks that met an infinity or a NaN, known on the device: with any of them the product by parts has
+// Marks of blocks that met elements which parts are not for, known on the device: with any of them the product by parts has
 // not been done, and the FFMA kernel behind it does it (else that one does nothing).
 struct LinearMarks {
     const uint8_t* unfit;

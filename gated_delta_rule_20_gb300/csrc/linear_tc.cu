@@ -20,7 +20,7 @@
 // linear_large_kernel (many tokens; bound by the tensor cores): persistent CTA pairs
 // (cta_group::2) on tiles of 256 columns x up to 256 tokens; every CTA loads its 128 columns and
 // half of the tokens.  Two accumulators in TMEM: the epilogue of one tile runs beside the next
-// tile's products.
+// tile's products.  (fp32 by bf16 parts, at the end of the file, takes all of TMEM for one tile.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,7 +54,8 @@ struct TcArgs {
     int tiles_n, tiles_m, group;    // large kernel: the tile grid, n tiles walked together
     bool staged;                    // large kernel: bf16 output (and residual) by TMA
     int32_t* status;
-    int accs, starts[kMaxAccs];     // fp32 by parts: accumulators of a tile, each from its first slab (else one)
+    int accs, starts[kMaxAccs];     // fp32 by parts: accumulators of a tile, from 1 on each from its first slab (else one)
+    int plane;                      // fp32 by parts: elements of K from one part to the next
     const uint8_t* unfit;           // fp32 by parts: marks of `marks` blocks; any of them: not for this kernel
     int marks;
 };
@@ -81,7 +82,7 @@ struct Ring {
     }
 };
 
-// The accumulator of a tile that slab k goes to.
+// The accumulator of a tile that slab k goes to (fp32 by parts: its x1 w1; the small products go to accumulator 0).
 __device__ __forceinline__ int acc_at(const TcArgs& t, int k) {
     int q = 0;
     for (int i = 1; i < t.accs; ++i) q += k >= t.starts[i];
@@ -107,14 +108,59 @@ struct AccWalk {
     }
 };
 
-// The four 32-byte steps of K of one slab.  KN: W is MN-major (boxes of 64 columns, 2048 bytes a step).
+// The four 32-byte steps of K of one slab, of the weight's stage and x's.  KN: W is MN-major (boxes of 64
+// columns, 2048 bytes a step).
 template <bool F8, bool KN, bool PAIR>
-__device__ __forceinline__ void mma_slab(uint32_t tmem, uint32_t stage, uint32_t idesc, bool first) {
-    const uint64_t dw = KN ? make_sdesc(stage, kHalfW, 1024) : make_sdesc(stage, 16, 1024);
-    const uint64_t dx = make_sdesc(stage + kWBytes, 16, 1024);
+__device__ __forceinline__ void mma_slab(uint32_t tmem, uint32_t w, uint32_t x, uint32_t idesc, bool first) {
+    const uint64_t dw = KN ? make_sdesc(w, kHalfW, 1024) : make_sdesc(w, 16, 1024);
+    const uint64_t dx = make_sdesc(x + kWBytes, 16, 1024);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         mma_step<F8, PAIR>(tmem, sdesc_add(dw, k * (KN ? 2048 : 32)), sdesc_add(dx, k * 32), idesc, !first || k > 0);
+}
+
+// Waits for the stages of a slab, s, from `at` on (left at the last of them); false: given up.
+template <bool PARTS>
+__device__ __forceinline__ bool wait_slab(uint64_t* full, Ring& at, int stages, int* s, volatile int* abort_flag) {
+#pragma unroll
+    for (int p = 0; p < (PARTS ? 3 : 1); ++p) {
+        if (p > 0) at.next(stages);
+        s[p] = at.s;
+        if (!mbar_wait_warp(&full[at.s], at.phase, abort_flag)) return false;
+    }
+    return true;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+    if constexpr (PAIR)
+        mma_commit_pair(bar);
+    else
+        mma_commit(bar);
+}
+
+// The products of one slab and the hand-back of its stages.  first: of this tile, main: of its accumulator.  By
+// parts a slab is three stages, the third parts in the first: each stage is loaded once for its two to three
+// products and handed back as early as their order allows.
+template <bool F8, bool KN, bool PARTS, bool PAIR>
+__device__ __forceinline__ void mma_stages(const TcArgs& t, uint32_t tmem, uint32_t sm, const int* at, uint64_t* empty, int acc,
+                                           bool first, bool main) {
+    const uint32_t s0 = sm + at[0] * t.stage_bytes;
+    if constexpr (!PARTS) {
+        mma_slab<F8, KN, PAIR>(tmem, s0, s0, t.idesc, main);
+        commit<PAIR>(&empty[at[0]]);
+    } else {
+        const uint32_t s1 = sm + at[1] * t.stage_bytes, s2 = sm + at[2] * t.stage_bytes;
+        mma_slab<F8, KN, PAIR>(tmem, s0, s2, t.idesc, first);  // w3 x1
+        mma_slab<F8, KN, PAIR>(tmem, s2, s0, t.idesc, false);  // w1 x3
+        commit<PAIR>(&empty[at[0]]);
+        mma_slab<F8, KN, PAIR>(tmem, s1, s1, t.idesc, false);  // w2 x2
+        mma_slab<F8, KN, PAIR>(tmem, s1, s2, t.idesc, false);  // w2 x1
+        mma_slab<F8, KN, PAIR>(tmem, s2, s1, t.idesc, false);  // w1 x2
+        commit<PAIR>(&empty[at[1]]);
+        mma_slab<F8, KN, PAIR>(tmem + acc * t.bn, s2, s2, t.idesc, main);  // w1 x1
+        commit<PAIR>(&empty[at[2]]);
+    }
 }
 
 // The sum over the S ranks' partial sums (in the ranks' order) of 4 neighbouring columns a thread, and
@@ -189,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const LinearArgs& a = t.a;
-    constexpr int kSlabElems = F8 ? 128 : 64;
+    constexpr int kSlabElems = F8 ? 128 : 64, kSlabStages = PARTS ? 3 : 1;
     const int stages = t.stages;
     SmallBars* bars = reinterpret_cast<SmallBars*>(sm + stages * t.stage_bytes);
     volatile int* abort_flag = &bars->abort;
@@ -224,11 +270,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     const bool run = !(PARTS && any_mark(t.unfit, t.marks));  // one answer for the whole grid
 
     if (warp == 0 && run) {  // TMA producer
-        int loaded = 0;
+        int loaded = 0, part = kSlabStages - 1, slab = k_lo * kSlabElems;
         Ring at;
-        for (int i = 0; i < k_hi - k_lo; ++i, at.next(stages)) {
-            const int s = at.s, k = (k_lo + i) * kSlabElems;
+        for (int i = 0; i < (k_hi - k_lo) * kSlabStages; ++i, at.next(stages)) {
+            const int s = at.s, k = PARTS ? slab + part * t.plane : slab;
             if (i >= stages && !mbar_wait_warp(&bars->empty[s], at.phase ^ 1, abort_flag)) break;
+            if (!PARTS || --part < 0) {
+                part = kSlabStages - 1;
+                slab += kSlabElems;
+            }
             uint8_t* st = sm + s * t.stage_bytes;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&bars->full[s], t.stage_bytes);
@@ -247,19 +297,18 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
         Ring at;
         AccWalk<PARTS> acc(t, k_lo);
         for (int i = 0; i < k_hi - k_lo; ++i, at.next(stages)) {
-            const int s = at.s;
-            if (!mbar_wait_warp(&bars->full[s], at.phase, abort_flag)) break;
+            int s[kSlabStages];
+            if (!wait_slab<PARTS>(bars->full, at, stages, s, abort_flag)) break;
             tc_fence_after();
-            const bool first = acc.step(t, k_lo + i) || i == 0;
+            const bool main = acc.step(t, k_lo + i) || i == 0;
             if (elect_one()) {
-                mma_slab<F8, KN, false>(tmem + acc.q * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, first);
-                mma_commit(&bars->empty[s]);
+                mma_stages<F8, KN, PARTS, false>(t, tmem, smem_u32(sm), s, bars->empty, acc.q, i == 0, main);
                 if (i + 1 == k_hi - k_lo) mma_commit(&bars->done);
             }
             __syncwarp();
-            issued = i + 1;
+            issued = (i + 1) * kSlabStages;
         }
-        if (issued < k_hi - k_lo && issued > 0)  // gave up: what was issued ends first (bounded)
+        if (issued < (k_hi - k_lo) * kSlabStages && issued > 0)  // gave up: what was issued ends first (bounded)
             (void)mbar_wait(&bars->empty[(issued - 1) % stages], ((issued - 1) / stages) & 1);
     }
     __syncwarp();
@@ -279,8 +328,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
                 tmem_ld8(lanes + c0, v[0]);
                 tmem_ld8(lanes + c0 + 8, v[1]);
                 tmem_wait_ld();
-                if constexpr (PARTS) {  // the sum of the accumulators that this rank's slabs went to
-                    float sum[16] = {};
+                if constexpr (PARTS) {  // and of the accumulators that this rank's slabs went to
+                    float sum[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[j] = v[j / 8][j % 8];
                     for (int q = acc_at(t, k_lo); q <= acc_at(t, k_hi - 1); ++q) {
                         tmem_ld8(lanes + q * t.bn + c0, v[0]);
                         tmem_ld8(lanes + q * t.bn + c0 + 8, v[1]);
@@ -710,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const LinearArgs& a = t.a;
-    constexpr int kSlabElems = F8 ? 128 : 64;
+    constexpr int kSlabElems = F8 ? 128 : 64, kSlabStages = PARTS ? 3 : 1;
     const int stages = t.stages;
     uint8_t* boxes = sm + stages * t.stage_bytes;
     float* swap = reinterpret_cast<float*>(boxes + box_bytes(t));
@@ -759,11 +810,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
             const int n0 = (tn * 2 + rank) * per, n1 = a.gated ? t.up + n0 : n0 + 64;
             const int m0 = tm * t.bn + rank * (t.bn / 2);
-            for (int k = 0; k < t.slabs * kSlabElems; k += kSlabElems, ++i, at.next(stages)) {
-                const int s = at.s;
+            int part = kSlabStages - 1, slab = 0;
+            for (int j = 0; j < t.slabs * kSlabStages; ++j, ++i, at.next(stages)) {
+                const int s = at.s, k = PARTS ? slab + part * t.plane : slab;
                 if (i >= stages && !mbar_wait_warp(&bars->empty[s], at.phase ^ 1, abort_flag)) {
                     live = false;
                     break;
+                }
+                if (!PARTS || --part < 0) {
+                    part = kSlabStages - 1;
+                    slab += kSlabElems;
                 }
                 uint8_t* st = sm + s * t.stage_bytes;
                 if (elect_one()) {
@@ -789,17 +845,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (use >= 1 && !mbar_wait_warp(&bars->acc_empty[b], (use - 1) & 1, abort_flag)) break;
                 tc_fence_after();
                 AccWalk<PARTS> acc(t, 0);
-                for (int k = 0; k < t.slabs; ++k, ++i, at.next(stages)) {
-                    const int s = at.s;
-                    if (!mbar_wait_warp(&bars->full[s], at.phase, abort_flag)) {
+                for (int k = 0; k < t.slabs; ++k, i += kSlabStages, at.next(stages)) {
+                    int s[kSlabStages];
+                    if (!wait_slab<PARTS>(bars->full, at, stages, s, abort_flag)) {
                         live = false;
                         break;
                     }
                     tc_fence_after();
-                    const bool first = acc.step(t, k) || k == 0;
+                    const bool main = acc.step(t, k) || k == 0;
                     if (elect_one()) {
-                        mma_slab<F8, KN, true>(tmem + (b + acc.q) * t.bn, smem_u32(sm) + s * t.stage_bytes, t.idesc, first);
-                        mma_commit_pair(&bars->empty[s]);
+                        mma_stages<F8, KN, PARTS, true>(t, tmem + b * t.bn, smem_u32(sm), s, bars->empty, acc.q, k == 0, main);
                         if (k + 1 == t.slabs) mma_commit_pair(&bars->acc_full[b]);
                     }
                     __syncwarp();
@@ -904,6 +959,8 @@ struct Operands {
     const uint8_t* unfit = nullptr;  // see TcArgs
     int marks = 0;
     int accs = 1, starts[kMaxAccs] = {};
+    int plane = 0;  // of parts: see TcArgs (depth: the rows or columns of K that there are)
+    long long depth(const LinearArgs& a) const { return plane ? 3LL * plane : a.K; }
 };
 
 template <bool F8, bool KN, bool PARTS>
@@ -931,12 +988,15 @@ struct Plan {
 //     23.2 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
 Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
-    const double weight_mb = tiles1 * slabs * (16.0 / 1024);
+    const int parts = accs > 1 ? 3 : 1, products = accs > 1 ? 6 : 1;  // stages and products of a slab
+    const double weight_mb = tiles1 * slabs * parts * (16.0 / 1024);
     Plan best{true, 256, 1};
     double least = 1e30;
     for (int bn = accs > 1 ? 512 / accs / 32 * 32 : 256; bn >= 64; bn -= 32) {  // (TMEM: 512 columns)
         const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
-        double t = 1.0 + bn / 200.0 + (double)turns * slabs * (bn > 182 ? bn * (0.28 / 256) : 0.20);
+        const double mma = products * bn * (0.28 / 256), in = parts * (accs > 1 ? (16 + bn / 16) / 118.0 : 0.20);
+        double t = 1.0 + bn / 200.0 + (double)turns * slabs * (mma > in ? mma : in);
+        if (accs > 1) t += (turns - 1) * accs * bn / 200.0;  // epilogues that nothing runs beside
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
         if (t < least) least = t, best = Plan{true, bn, 1};
     }
@@ -946,11 +1006,13 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
         if (tiles_m > 65535) continue;  // the grid's limit
         for (int S = 1; S <= 8 && S * 2 <= (slabs > 2 ? slabs : 2); S *= 2) {
             const long long ctas = tiles1 * tiles_m * S;
-            const long long room = 8LL * (sms / 8 * 2 / S) * S;  // CTAs at once: clusters stay inside one of 8 groups of SMs
+            const int beside = accs > 1 ? 1 : 2;
+            // CTAs at once: clusters stay inside one of 8 groups of SMs (of 16 to 20: two clusters of 8 do not fit in each)
+            const long long room = 8LL * ((sms / 8 * beside - (S == 8 ? 4 : 0)) / S) * S;
             const long long waves = (ctas + room - 1) / room;
-            const long long an_sm = ctas <= sms ? 1 : waves * 2;  // CTAs one after another, or beside one another
-            const double kb = (double)an_sm * ((slabs + S - 1) / S) * (16 + bn / 8.0);
-            double t = kb / (an_sm == 1 ? 85 : 115);
+            const long long an_sm = ctas <= sms ? 1 : waves * beside;  // CTAs one after another, or beside one another
+            const double kb = (double)an_sm * ((slabs + S - 1) / S) * parts * (16 + bn / 8.0);
+            double t = kb / (an_sm == 1 || beside == 1 ? 85 : 115);
             if (t < weight_mb / 6.3) t = weight_mb / 6.3;
             double join = 0.3 + bn / 60.0;
             if (S == 8) join = join * 1.3 + 0.2;
@@ -969,6 +1031,7 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.marks = op.marks;
     t.accs = op.accs;
     for (int q = 0; q < kMaxAccs; ++q) t.starts[q] = op.starts[q];
+    t.plane = op.plane;
     const int elems = f8 ? 128 : 64, per = a.gated ? 64 : 128;
     t.slabs = (a.K + elems - 1) / elems;
     t.bn = how.bn;
@@ -977,7 +1040,7 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     if (tiles * t.splits > INT32_MAX || tiles_m > 65535) return GDN_ERR_DIMS;
     t.wide_out = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & (a.out_f32 ? 15u : 7u)) == 0;
     t.stage_bytes = kWBytes + t.bn * kSlabBytes;
-    t.stages = (int)((112 * 1024 - sizeof(SmallBars) - 1024) / t.stage_bytes);  // two CTAs an SM
+    t.stages = (int)(((op.plane ? kSmemLimit : 112 * 1024) - sizeof(SmallBars) - 1024) / t.stage_bytes);  // two CTAs an SM
     if (t.stages > kMaxStages) t.stages = kMaxStages;
     t.tmem_cols = 32;
     while (t.tmem_cols < (uint32_t)(t.accs * t.bn)) t.tmem_cols <<= 1;
@@ -985,8 +1048,9 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
     CUtensorMap tw, tx;
-    if (!encode(&tw, f8, op.w, a.nk ? op.w_cols : a.K, a.nk ? a.K : op.w_cols, op.w_pitch, 64) ||
-        !encode(&tx, f8, op.x, a.M, a.K, op.x_pitch, t.bn))
+    const long long depth = op.depth(a);
+    if (!encode(&tw, f8, op.w, a.nk ? op.w_cols : depth, a.nk ? depth : op.w_cols, op.w_pitch, 64) ||
+        !encode(&tx, f8, op.x, a.M, depth, op.x_pitch, t.bn))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + sizeof(SmallBars) + 1024;
     const cudaError_t e = f8              ? launch_small<true, false, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
@@ -1013,6 +1077,7 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.marks = op.marks;
     t.accs = op.accs;
     for (int q = 0; q < kMaxAccs; ++q) t.starts[q] = op.starts[q];
+    t.plane = op.plane;
     const int elems = f8 ? 128 : 64, per = a.gated ? 128 : 256;
     t.slabs = (a.K + elems - 1) / elems;
     t.tiles_n = (int)(((long long)a.N + per - 1) / per);
@@ -1021,7 +1086,7 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     if ((long long)t.tiles_n * t.tiles_m > INT32_MAX - sms) return GDN_ERR_DIMS;
     t.group = t.tiles_n < 16 ? t.tiles_n : 16;
     t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
-    t.staged = !a.out_f32 && a.N % 8 == 0 &&
+    t.staged = !op.plane && !a.out_f32 && a.N % 8 == 0 &&
                ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.res)) & 15u) == 0;
     const size_t fixed = sizeof(LargeBars) + box_bytes(t) + (a.gated ? kSwapBytes : 0) + 1024;
     t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
@@ -1032,8 +1097,9 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
     CUtensorMap tw, tx;
-    if (!encode(&tw, f8, op.w, a.nk ? op.w_cols : a.K, a.nk ? a.K : op.w_cols, op.w_pitch, 64) ||
-        !encode(&tx, f8, op.x, a.M, a.K, op.x_pitch, t.bn / 2))
+    const long long depth = op.depth(a);
+    if (!encode(&tw, f8, op.w, a.nk ? op.w_cols : depth, a.nk ? depth : op.w_cols, op.w_pitch, 64) ||
+        !encode(&tx, f8, op.x, a.M, depth, op.x_pitch, t.bn / 2))
         return GDN_ERR_CUDA;
     CUtensorMap to{}, tr{};
     const int tokens = a.gated ? 16 : 32;
@@ -1086,15 +1152,13 @@ __global__ void __launch_bounds__(256) linear_align_kernel(const __grid_constant
 
 // fp32 operands as three bf16 parts each: x = x1 + x2 + x3, every part the rounding of what the ones before
 // leave (24 bits in three times 8, so the sum is exact).  Of the nine products of parts the six of 2^-16 and
-// more are taken, the five small ones into an accumulator of their own:
-//     x' = [x1 x3 x2 x1 x2 | x1],  w' = [w3 w1 w2 w2 w1 | w1]  along K.
+// more are taken, the five small ones (x1 w3, x3 w1, x2 w2, x1 w2, x2 w1) into an accumulator of their own.
 // The tensor cores truncate a sum at every step of 16 terms, always towards zero, so that it falls short by
 // about K 1e-9 of itself (2.1e-6 at K = 2048; fp32 sums with rounding 0.8e-6).  The x1 w1, whose sum that is,
 // therefore go to an accumulator for every 704 of K, three at the most, which are added with rounding.
-constexpr int kParts = 6;
-__device__ __constant__ const uint8_t kPartOf[2][kParts] = {{0, 2, 1, 0, 1, 0}, {2, 0, 1, 1, 0, 0}};  // x, w
+constexpr int kParts = 3;
 
-// Splits one operand: rows_in x cols fp32 -> rows_out x width parts, rows `pitch` apart and copies `plane`
+// Splits one operand: rows_in x cols fp32 -> rows_out x width parts, rows `pitch` apart and parts `plane`
 // apart; columns as in CopyJob, what lies outside is zero.
 struct SplitJob {
     const float* src;
@@ -1102,7 +1166,11 @@ struct SplitJob {
     long long rows_in, rows_out, cols, width, pitch, plane, half, up;
 };
 
-// marks[block]: whether the block met an infinity or a NaN, for which parts do not add up.
+// marks[block]: whether the block met an element that parts are not for: an infinity or a NaN, for which they do
+// not add up, or one past 2^63, whose products of parts could be infinities of both signs where the product is one.
+// 16 bytes are read at a time where a piece lies whole and on such a boundary (2048 x 2048 twice: 28 us by elements).
+constexpr float kPartMax = 9.2233720e18f;
+
 __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ SplitJob x, const __grid_constant__ SplitJob w,
                                                            uint8_t* marks) {
     griddep_launch_dependents();
@@ -1110,18 +1178,28 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
     const long long x_pieces = x.rows_out * (x.width / 8), pieces = x_pieces + w.rows_out * (w.width / 8);
     int bad = 0;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (long long)gridDim.x * 256) {
-        const int which = i < x_pieces ? 0 : 1;
-        const SplitJob& c = which == 0 ? x : w;
-        const long long at = which == 0 ? i : i - x_pieces, row = at / (c.width / 8), d0 = at % (c.width / 8) * 8;
+        const SplitJob& c = i < x_pieces ? x : w;
+        const long long at = i < x_pieces ? i : i - x_pieces, row = at / (c.width / 8), d0 = at % (c.width / 8) * 8;
         const float* src = c.src + row * c.cols;
+        float in[8];
+        const long long first = d0 < c.half ? d0 : c.half + d0 - c.up;  // the source column of d0, if it has one
+        const bool whole = row < c.rows_in && (d0 + 8 <= c.half || d0 >= c.up) && first + 8 <= c.cols;
+        if (whole && (reinterpret_cast<uintptr_t>(src + first) & 15u) == 0) {
+            const float4 p = *reinterpret_cast<const float4*>(src + first), q = *reinterpret_cast<const float4*>(src + first + 4);
+            in[0] = p.x, in[1] = p.y, in[2] = p.z, in[3] = p.w, in[4] = q.x, in[5] = q.y, in[6] = q.z, in[7] = q.w;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const long long d = d0 + j, from = d < c.half ? d : d >= c.up ? c.half + d - c.up : c.cols;
+                in[j] = row < c.rows_in && from < c.cols ? src[from] : 0.f;
+            }
+        }
         __nv_bfloat16 part[3][8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const long long d = d0 + j, from = d < c.half ? d : d >= c.up ? c.half + d - c.up : c.cols;
-            const float v = row < c.rows_in && from < c.cols ? src[from] : 0.f;
-            bad |= !(fabsf(v) <= 3.4028235e38f);
-            // (a rounding past the largest bf16 would be an infinity: truncated instead)
-            __nv_bfloat16 p = fabsf(v) >= 3.38e38f ? __float2bfloat16_rz(v) : __float2bfloat16_rn(v);
+            const float v = in[j];
+            bad |= !(fabsf(v) <= kPartMax);
+            __nv_bfloat16 p = __float2bfloat16_rn(v);
             part[0][j] = p;
             float left = v - __bfloat162float(p);
             part[1][j] = p = __float2bfloat16_rn(left);
@@ -1132,7 +1210,7 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
         memcpy(o, part, sizeof(o));
         uint4* dst = reinterpret_cast<uint4*>(c.dst + row * c.pitch + d0);
 #pragma unroll
-        for (int k = 0; k < kParts; ++k) dst[k * (c.plane / 8)] = o[kPartOf[which][k]];
+        for (int k = 0; k < kParts; ++k) dst[k * (c.plane / 8)] = o[k];
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0) marks[blockIdx.x] = bad != 0;
@@ -1223,18 +1301,17 @@ gdn_status run_parts(const LinearArgs& a, uint8_t* scratch, int dev, int sms, cu
     *marks = LinearMarks{unfit, kSplitBlocks};
     linear_split_kernel<<<kSplitBlocks, 256, 0, s>>>(x, w, unfit);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
-    LinearArgs b = a;
-    b.K = (int)x.pitch;
     const bool halves = !a.nk && a.gated;
     Operands op{x.dst, w.dst, x.pitch, w.pitch, halves ? w.up + a.N : a.gated ? 2LL * a.N : a.N, halves ? (int)w.up : a.N};
     op.unfit = unfit;
     op.marks = kSplitBlocks;
     // the x1 w1 terms: an accumulator for every 704 of K, three at the most
-    const int small = (int)((kParts - 1) * x.plane / 64), main = (int)(x.plane / 64);
-    const int wanted = (main + 10) / 11 < kMaxAccs - 1 ? (main + 10) / 11 : kMaxAccs - 1, share = (main + wanted - 1) / wanted;
-    op.accs = 1 + (main + share - 1) / share;
-    for (int q = 1; q < op.accs; ++q) op.starts[q] = small + (q - 1) * share;
-    return run_tc(b, op, false, dev, sms, s);
+    const int slabs = (a.K + 63) / 64, wanted = (slabs + 10) / 11 < kMaxAccs - 1 ? (slabs + 10) / 11 : kMaxAccs - 1;
+    const int share = (slabs + wanted - 1) / wanted;
+    op.accs = 1 + (slabs + share - 1) / share;
+    for (int q = 1; q < op.accs; ++q) op.starts[q] = (q - 1) * share;
+    op.plane = 64 * slabs;
+    return run_tc(a, op, false, dev, sms, s);
 }
 
 }  // namespace
@@ -1242,10 +1319,11 @@ gdn_status run_parts(const LinearArgs& a, uint8_t* scratch, int dev, int sms, cu
 LinearPlan plan_linear(const LinearArgs& a, int32_t dtype) {
     const double ops = 2.0 * a.M * (a.gated ? 2LL * a.N : a.N) * a.K;
     if (dtype == GDN_F32) {
-        // Worth the split and two more launches (about 15 us) from 3e8 operations: M = 333, K = 770, N = 1030 takes the
-        // FFMA kernel 35 us.  Up to K = 4096 the accumulators' truncation stays near the error of fp32 sums (at 2048
-        // 7e-7 and 8e-7 of the result).
-        if (ops < 3e8 || a.K > 4096 || a.M < 32) return LinearPlan{LinearRoute::kFfma, 0};
+        // Worth the split and two more launches from 3e8 operations.  By parts and on the FFMA kernel, us: M = 128,
+        // K = N = 1024 (2.7e8) 14.1 and 11.6, M = 192 15.3 and 19.4; M = 64, K = N = 2048 19.8 and 19.7, M = 96 26.9 and 34.9;
+        // M = 16, K = 4096, N = 8192 93 and 126.  Fewer rows than a tile's 16 stay on the FFMA kernel.  Up to K = 4096 the
+        // accumulators' truncation stays near the error of fp32 sums (sums of 2048 positive products: 9.8e-7 and 8.9e-7).
+        if (ops < 3e8 || a.K > 4096 || a.M < 16) return LinearPlan{LinearRoute::kFfma, 0};
         SplitJob x, w;
         split_jobs(a, &x, &w);
         const size_t bytes = job_bytes(x, false) + job_bytes(w, !a.nk) + kSplitBlocks;

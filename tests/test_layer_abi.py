@@ -81,7 +81,8 @@ def test_linear_workspace(L):
     assert need(1000, 1000, 1000, x=P + 2) == 1000 * 1000 * 2
     assert need(1000, 1000, 1001, gdn.GDN_F8E4M3, flags=nk) == 2 * 1000 * 1008
     assert need(1000, 1000, 1001, flags=ffma) == 0
-    assert need(1000, 1000, 1000, gdn.GDN_F32) >= 6 * 2 * 2 * 1000 * 1024   # six parts of both
+    assert need(1000, 1000, 1000, gdn.GDN_F32) >= 3 * 2 * 2 * 1000 * 1024   # three parts of both
+    assert need(15, 4096, 4096, gdn.GDN_F32) == 0 < need(16, 4096, 4096, gdn.GDN_F32)
     assert need(1000, 1000, 8192, gdn.GDN_F32) == 0 and need(8, 10000, 4096, gdn.GDN_F32) == 0
     assert need(1000000, 1000, 4096, gdn.GDN_F32) == 0                  # past 4 GiB
     assert need(0, 1000, 1001) == 0 and need(1000, 0, 1001) == 0

@@ -244,6 +244,41 @@ def test_fp32_products_with_infinities_and_nan(gdn, where, bad, gated):
     assert torch.equal(got.view(torch.int32), ref.view(torch.int32)) and not torch.isfinite(ref).all()
 
 
+@pytest.mark.parametrize("M,N,K,layout,gated", [
+    (65, 2080, 1200, "kn", False), (65, 2080, 4096, "nk", False), (97, 1032, 2000, "kn", True), (257, 515, 1409, "nk", True),
+    (2000, 1300, 64, "kn", False), (900, 2100, 3001, "kn", False), (700, 3001, 1999, "kn", True), (2000, 1999, 705, "nk", False)])
+def test_fp32_parts_of_every_plan(gdn, M, N, K, layout, gated):
+    """K of one slab to 4096 (one to three accumulators of the largest products), few and many tokens, odd rows;
+    operands up to 2^63, and rows whose elements lie 2^40 apart."""
+    assert 2 * M * N * (2 if gated else 1) * K >= 3e8
+    t = _draw(M, N, K, "f32", layout, gated, False, False, "f32", seed=K)
+    gen = torch.Generator("cuda").manual_seed(M)
+    x = t["x"] * 2.0 ** torch.randint(-20, 20, (M, K), generator=gen, device="cuda")
+    x[1] = 9.2e18 * x[1].sign()
+    x[2] = torch.where(x[2] > 0, 1 + 2.0 ** -23, 1 - 2.0 ** -24)
+    t = dict(t, x=x)
+    out = (gdn.linear_gated if gated else gdn.linear)(x, t["weight"], activation="none", weight_layout=layout)
+    torch.cuda.synchronize()
+    if gated:  # (the product of two sums of 1e18 passes fp32's range)
+        keep = torch.ones(M, dtype=torch.bool, device="cuda")
+        keep[1] = False
+        out, t["x"] = out[keep], x[keep]
+    _check(out, t, "none", layout, gated)
+
+
+def test_fp32_products_past_the_range(gdn):
+    """Products that pass fp32's range are infinities of the sum's sign, not NaN."""
+    gen = torch.Generator("cuda").manual_seed(5)
+    x = torch.rand(300, 700, generator=gen, device="cuda") + 0.5
+    w = torch.rand(800, 700, generator=gen, device="cuda") + 0.5
+    x[7] *= 1e30
+    w[9] *= -1e30
+    out = gdn.linear(x, w, weight_layout="nk")
+    far = torch.zeros_like(out, dtype=torch.bool)
+    far[7, 9] = True
+    assert out[7, 9] == float("-inf") and torch.isfinite(out[~far]).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(5, 128, 128), (300, 264, 192)])
 @pytest.mark.parametrize("dtype", ["bf16", "f8"])
 def test_tensor_cores_agree_with_ffma(gdn, M, N, K, dtype):
