@@ -22,7 +22,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdn.so")
 
 SOURCES = ["gdn_api.cu", "decode.cu", "prefill_ffma.cu", "prefill_tc.cu", "conv1d.cu", "decode_gated.cu", "block.cu",
-           "rmsnorm_gated.cu", "rmsnorm_residual.cu", "linear.cu", "linear_tc.cu"]
+           "rmsnorm_gated.cu", "rmsnorm_residual.cu", "linear.cu", "linear_few.cu", "linear_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

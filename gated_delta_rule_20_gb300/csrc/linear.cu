@@ -5,7 +5,8 @@
 //
 // (gated: act of the gate's column times the up column).  The FFMA kernel is right for every
 // type, layout, size and alignment; it is the path of fp32 compute and of small products of operands
-// whose rows TMA cannot take (pointer or row pitch not a multiple of 16 bytes).
+// whose rows TMA cannot take (pointer or row pitch not a multiple of 16 bytes).  Up to 12 rows linear_few.cu does
+// the same.
 //
 // FFMA kernel: 16 x 16 threads on a tile of 16 TM tokens x 16 TM columns, TM x TM sums a thread as pairs
 // of neighbouring columns (fma.rn.f32x2: half the issue slots of single FFMAs, which leaves room for the
@@ -307,7 +308,11 @@ cudaError_t launch_layout(const LinearArgs& a, int splits, const LinearMarks& ma
 }
 
 template <typename T>
-cudaError_t launch_ffma(const LinearArgs& a, int sms, const LinearMarks& marks, cudaStream_t s) {
+cudaError_t launch_ffma(const LinearArgs& a, int32_t dtype, int sms, const LinearMarks& marks, cudaStream_t s) {
+    // Few rows: a kernel that reads the weight once for every 4.  It and the tiles below, us: fp32 K = N = 2048 M = 12
+    // 13.9 and 18.8, M = 16 13.8 and 18.9 but K = 4097, N = 2001 51 and 38; e4m3 K = 4097, N = 2001 M = 8 50 and 50, M = 12
+    // 57 and 50.
+    if (a.M <= (dtype == GDN_F8E4M3 ? 8 : 12) && !marks.unfit) return launch_linear_few(a, dtype, sms, s);
     const long long wn = a.gated ? 2LL * a.N : a.N;
     auto tiles = [&](int t) { return ((a.M + (long long)t - 1) / t) * ((wn + t - 1) / t); };
     if (tiles(128) >= sms) return launch_layout<T, 8>(a, 1, marks, s);
@@ -394,9 +399,9 @@ extern "C" gdn_status gdn_linear_ws(const void* x, const float* x_scale, const v
     if (how.route != LinearRoute::kFfma)
         st = launch_linear_tc(a, d->dtype, how.route, own ? own : workspace, dev, sms, s, &marks);
     if (st == GDN_OK && (how.route == LinearRoute::kFfma || how.route == LinearRoute::kParts)) {
-        const cudaError_t e = d->dtype == GDN_F32    ? launch_ffma<float>(a, sms, marks, s)
-                              : d->dtype == GDN_BF16 ? launch_ffma<__nv_bfloat16>(a, sms, marks, s)
-                                                     : launch_ffma<__nv_fp8_e4m3>(a, sms, marks, s);
+        const cudaError_t e = d->dtype == GDN_F32    ? launch_ffma<float>(a, d->dtype, sms, marks, s)
+                              : d->dtype == GDN_BF16 ? launch_ffma<__nv_bfloat16>(a, d->dtype, sms, marks, s)
+                                                     : launch_ffma<__nv_fp8_e4m3>(a, d->dtype, sms, marks, s);
         if (e != cudaSuccess) st = GDN_ERR_CUDA;
     }
     if (own && cudaFreeAsync(own, s) != cudaSuccess && st == GDN_OK) st = GDN_ERR_CUDA;

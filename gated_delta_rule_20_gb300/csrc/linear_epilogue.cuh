@@ -44,6 +44,9 @@ struct LinearMarks {
 gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, LinearRoute route, void* scratch, int dev, int sms,
                             cudaStream_t s, LinearMarks* marks);
 
+// The kernel for few rows on the FMA units (linear_few.cu), for every type, layout, size and alignment.
+cudaError_t launch_linear_few(const LinearArgs& a, int32_t dtype, int sms, cudaStream_t s);
+
 // gelu(v) = v Phi(v), Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by the rational approximation 7.1.26 of Abramowitz
 // and Stegun's Handbook (Hastings): erfc(z) = (a1 s + ... + a5 s^5) e^(-z^2), s = 1 / (1 + 0.3275911 z), off by
 // at most 1.5e-7, so gelu by 0.75e-7 |v|, about one rounding of v.  Half the instructions of erff: M = 16384,

@@ -244,6 +244,30 @@ def test_fp32_products_with_infinities_and_nan(gdn, where, bad, gated):
     assert torch.equal(got.view(torch.int32), ref.view(torch.int32)) and not torch.isfinite(ref).all()
 
 
+@pytest.mark.parametrize("dtype,layout", [("f32", "kn"), ("f32", "nk"), ("bf16", "kn"), ("bf16", "nk"), ("f8", "nk")])
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 1), (1, 31, 37), (1, 64, 128), (1, 600, 130), (1, 33, 9000), (1, 2000, 1025), (1, 16, 12345), (2, 130, 257), (3, 48, 512),
+    (4, 96, 2048), (4, 129, 8193), (5, 72, 1000), (8, 256, 4112), (8, 515, 1537), (9, 40, 300), (12, 136, 640), (12, 7, 3001)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_few_rows_on_the_fma_units(gdn, M, N, K, dtype, layout, gated):
+    """Few rows without tensor cores: K inside, at and over the pieces, the chunks and the ranks' shares."""
+    _run(gdn, M, N, K, dtype, layout, gated, "silu" if gated else "none", bias=True, residual=M % 2 == 0, force_ffma=True)
+
+
+@pytest.mark.parametrize("dtype,layout", [("f32", "kn"), ("f32", "nk"), ("bf16", "kn"), ("bf16", "nk"), ("f8", "nk")])
+def test_few_rows_keep_nan_apart(gdn, dtype, layout):
+    """A NaN in x stays in its row and one in the weight in its column, at sizes with rows and columns to spare."""
+    M, N, K = 5, 70, 777
+    t = _draw(M, N, K, dtype, layout, False, False, False, "f32", seed=9)
+    nan = torch.tensor(float("nan"), device="cuda").to(DT[dtype])
+    t["x"][3, 5] = nan
+    t["weight"][(11, 60) if layout == "kn" else (60, 11)] = nan
+    out = gdn.linear(t["x"], t["weight"], weight_layout=layout, x_scale=t["x_scale"], weight_scale=t["weight_scale"], force_ffma=True)
+    far = torch.zeros(M, N, dtype=torch.bool, device="cuda")
+    far[3], far[:, 60] = True, True
+    assert torch.equal(out.isnan(), far)
+
+
 @pytest.mark.parametrize("M,N,K,layout,gated", [
     (65, 2080, 1200, "kn", False), (65, 2080, 4096, "nk", False), (97, 1032, 2000, "kn", True), (257, 515, 1409, "nk", True),
     (2000, 1300, 64, "kn", False), (900, 2100, 3001, "kn", False), (700, 3001, 1999, "kn", True), (2000, 1999, 705, "nk", False)])
