@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_consta
                 store_out(a, o, a.res ? v[j] + load_out(a, o) : v[j]);
             }
         }
-        if (splits > 1) ptx::cluster_sync();  // a CTA's shared memory stays until every rank has read it
+        if (splits > 1) ptx::cluster_sync_relaxed();  // a CTA's shared memory stays until every rank has read it
     } else {
 #pragma unroll
         for (int i = 0; i < TM; ++i) {

@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads) linear_few_kernel(const __grid_const
         const long long o = (long long)m * a.N + n;
         store_out(a, o, a.res ? v + load_out(a, o) : v);
     }
-    if (splits > 1) ptx::cluster_sync();  // a CTA's shared memory stays until every rank has read it
+    if (splits > 1) ptx::cluster_sync_relaxed();  // a CTA's shared memory stays until every rank has read it
 }
 
 template <typename T, int R, bool kNK, bool kVec>

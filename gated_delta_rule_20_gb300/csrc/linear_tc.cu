@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     __syncwarp();
     // a CTA's shared memory stays until every rank has read it
     if (t.splits > 1)
-        cluster_sync();
+        cluster_sync_relaxed();
     else
         __syncthreads();
     if (tid == 0 && bars->abort) atomicExch(t.status, (int32_t)GDN_ERR_TIMEOUT);
@@ -541,7 +541,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
                     for (int j = 0; j < 8; ++j) v[i + j] += w[j];
                 }
             }
-            if (c + 32 >= hc) {  // the accumulator is read: the next product may overwrite it
+            if (c + 32 >= hc && tile + (PARTS ? 1 : 2) * pairs < tiles) {  // read: a later product may overwrite it
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(b ? done1 : done0);
@@ -669,7 +669,8 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
             for (int h = 0; h < 2; ++h)
                 tmem_ld16x256_x4(tmem + b * t.bn + c_lo + chunk * 32 + ((uint32_t)(quad * 32 + 16 * h) << 16), v[h]);
             tmem_wait_ld();
-            if (chunk == chunks - 1) {  // the accumulator is read
+            // the accumulator is read (told only where it is used again: the arrival waits for earlier writes, 0.5 us)
+            if (chunk == chunks - 1 && tile + 2 * pairs < tiles) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(b ? done1 : done0);
@@ -749,7 +750,7 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
     }
     if (in_flight) (void)mbar_wait(res_full, phase);  // gave up: the load lands first (bounded)
     __syncwarp();
-    if (issuer && elect_one()) tma_store_wait_all0();
+    if (issuer && elect_one()) tma_store_wait_read0();
     __syncwarp();
 }
 
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) tmem_alloc_pair(&bars->tmem, t.tmem_cols);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // the peer's barriers are initialised
+    cluster_sync_relaxed();  // the peer's barriers are initialised (fence_mbar_init)
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     griddep_wait();
@@ -875,11 +876,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    cluster_sync();
+    cluster_sync_relaxed();
     if (tid == 0 && bars->abort) atomicExch(t.status, (int32_t)GDN_ERR_TIMEOUT);
     __syncwarp();
     if (warp == 1) tmem_dealloc_pair(tmem, t.tmem_cols);
-    cluster_sync();  // neither CTA exits while the pair's TMEM is being freed
+    cluster_sync_relaxed();  // neither CTA exits while the pair's TMEM is being freed
 }
 
 // ------------------------------------------------------------------ host side

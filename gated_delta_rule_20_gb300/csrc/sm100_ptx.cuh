@@ -87,12 +87,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
 // in flight, which must land before the CTA exits.
 static __device__ unsigned long long g_wait_limit_ns = 1000000000ull;
 static __device__ __noinline__ bool mbar_wait_or_abort_loop(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    const uint64_t t0 = globaltimer_ns();
-    const uint64_t limit = *const_cast<volatile unsigned long long*>(&g_wait_limit_ns);
+    uint64_t t0 = 0, limit = 0;  // (read when the wait turns out to be long)
     for (uint32_t i = 1;; ++i) {
         if (mbar_try_wait(bar, parity)) return true;
         if ((i & 15u) == 0) {
             if (*abort) return false;
+            if (t0 == 0) {
+                t0 = globaltimer_ns();
+                limit = *const_cast<volatile unsigned long long*>(&g_wait_limit_ns);
+            }
             if (globaltimer_ns() - t0 > limit) {
                 *abort = 1;
                 return false;
@@ -454,6 +457,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 // Every thread of every CTA of the cluster; shared-memory writes before it are seen after it.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same for execution alone: no earlier write is waited for.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // The shared::cluster address of this CTA's address `a` in CTA `rank` of the cluster.
