@@ -247,16 +247,20 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     griddep_launch_dependents();  // the next kernel's CTAs may be set up beside this one (they wait as below)
     const int k_lo = (int)((long long)t.slabs * rank / t.splits), k_hi = (int)((long long)t.slabs * (rank + 1) / t.splits);
 
-    if (tid == 0) {
-        tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_x);
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+    if (warp == 0) {  // a barrier a lane
+        if (lane < stages) {
+            mbar_init(&bars->full[lane], 1);
+            mbar_init(&bars->empty[lane], 1);
+        } else if (lane == 30) {
+            mbar_init(&bars->done, 1);
+            bars->abort = 0;
         }
-        mbar_init(&bars->done, 1);
-        bars->abort = 0;
         fence_mbar_init();
+        if (lane == 31) {
+            tma_prefetch_desc(&tm_w);
+            tma_prefetch_desc(&tm_x);
+        }
+        __syncwarp();
     }
     if (warp == 1) {
         tmem_alloc(&bars->tmem, t.tmem_cols);
@@ -774,22 +778,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int per = a.gated ? 64 : 128;  // outputs of a CTA
     griddep_launch_dependents();  // as in the small kernel
 
-    if (tid == 0) {
-        tma_prefetch_desc(&tm_w);
-        tma_prefetch_desc(&tm_x);
-        for (int s = 0; s < stages; ++s) {
-            mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+    if (warp == 0) {  // (a barrier a lane: one after another they were 0.1 us)
+        if (lane < stages) {
+            mbar_init(&bars->full[lane], 1);
+            mbar_init(&bars->empty[lane], 1);
+        } else if (lane >= 16 && lane < 18) {
+            mbar_init(&bars->acc_full[lane - 16], 1);
+            mbar_init(&bars->acc_empty[lane - 16], 2 * kEpiWarps);
+        } else if (lane >= 20 && lane < 20 + kEpiWarps / 2) {
+            mbar_init(&bars->res_full[lane - 20], 1);
+        } else if (lane == 30) {
+            bars->abort = 0;
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
-        }
-        for (int w = 0; w < kEpiWarps / 2; ++w) mbar_init(&bars->res_full[w], 1);
-        bars->abort = 0;
         fence_mbar_init();
+        if (lane == 31) {
+            tma_prefetch_desc(&tm_w);
+            tma_prefetch_desc(&tm_x);
+        }
+        __syncwarp();
     }
-    __syncwarp();
     if (warp == 1) tmem_alloc_pair(&bars->tmem, t.tmem_cols);
     tc_fence_before();
     __syncthreads();
@@ -984,9 +991,10 @@ struct Plan {
 // graph over weights larger than L2):
 //   - small: one CTA takes in about 85 KB/us and two on an SM 115, all together at most 6.3 MB/us; the
 //     partial sums' way through TMEM and shared memory costs 0.3 + bn / 60, a third more over 8 CTAs.  M = 64, K = N = 2048: 12.4 (32 tokens, no split), 8.3 (2), 6.8 (4), 6.9 (8);
-//   - pairs: 0.28 us a slab at 256 tokens (the tensor cores' time), in proportion down to 0.20 (its issue),
-//     1 us more set-up and an epilogue of bn / 200.  M = 512, K = N = 4096: 20.8 the best small plan, 18.5 pairs at 128,
-//     23.2 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
+//   - pairs: 0.28 us a slab at 256 tokens (the tensor cores' time), in proportion down to 0.19 (the weight's way
+//     from L2), and bn / 300 for the last tile's outputs.  M = 512, K = N = 4096: 20.6 the best small plan, 16.9 pairs
+//     at 128, 22.4 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
+// On 91 shapes (M = 1 .. 2048) the choice is 0.8 % behind the best of all on average; by parts, on 17 shapes, it is it.
 Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
     const int parts = accs > 1 ? 3 : 1, products = accs > 1 ? 6 : 1;  // stages and products of a slab
@@ -995,8 +1003,8 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     double least = 1e30;
     for (int bn = accs > 1 ? 512 / accs / 32 * 32 : 256; bn >= 64; bn -= 32) {  // (TMEM: 512 columns)
         const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
-        const double mma = products * bn * (0.28 / 256), in = parts * (accs > 1 ? (16 + bn / 16) / 118.0 : 0.20);
-        double t = 1.0 + bn / 200.0 + (double)turns * slabs * (mma > in ? mma : in);
+        const double mma = products * bn * (0.28 / 256), in = parts * (accs > 1 ? (16 + bn / 16) / 118.0 : 0.19);
+        double t = bn / 300.0 + (double)turns * slabs * (mma > in ? mma : in);
         if (accs > 1) t += (turns - 1) * accs * bn / 200.0;  // epilogues that nothing runs beside
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
         if (t < least) least = t, best = Plan{true, bn, 1};
