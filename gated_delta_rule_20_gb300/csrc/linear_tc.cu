@@ -1003,7 +1003,7 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     double least = 1e30;
     for (int bn = accs > 1 ? 512 / accs / 32 * 32 : 256; bn >= 64; bn -= 32) {  // (TMEM: 512 columns)
         const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
-        const double mma = products * bn * (0.28 / 256), in = parts * (accs > 1 ? (16 + bn / 16) / 118.0 : 0.19);
+        const double mma = products * bn * (0.28 / 256), in = parts * (accs > 1 ? (16 + bn / 16) / 105.0 : 0.19);
         double t = bn / 300.0 + (double)turns * slabs * (mma > in ? mma : in);
         if (accs > 1) t += (turns - 1) * accs * bn / 200.0;  // epilogues that nothing runs beside
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
