@@ -95,6 +95,30 @@ def test_graph_capture(gdn, M, dtype):
         assert torch.equal(out[0], ref[0]) and torch.equal(out[1], ref[1])
 
 
+@pytest.mark.parametrize("M,N,K,dtype", [(2048, 2048, 256, "bf16"), (700, 1536, 512, "bf16"), (64, 2048, 2048, "bf16"), (300, 1024, 1024, "f32"),
+                                         (3, 2048, 2048, "f32"), (1500, 2048, 128, "f8")])
+def test_outputs_reach_the_next_kernel(gdn, M, N, K, dtype):
+    """A product, a norm of it and a product of the norm, launched at once behind one another into reused buffers,
+    against the same calls with a synchronisation after each: the same bits, forty times over."""
+    out = "f32" if dtype == "f32" else "bf16"
+    t = [_draw(M, N, K, dtype, "nk", False, False, False, out, seed=i) for i in range(4)]
+    nw, w2 = torch.ones(N, device="cuda"), t[0]["weight"].new_zeros((256, N)).float().normal_().to(DT[out])
+    y, z = torch.empty(M, N, dtype=DT[out], device="cuda"), torch.empty(M, 256, dtype=DT[out], device="cuda")
+
+    def chain(i, wait):
+        gdn.linear(t[i]["x"], t[i]["weight"], weight_layout="nk", x_scale=t[i]["x_scale"], weight_scale=t[i]["weight_scale"], out=y)
+        if wait:
+            torch.cuda.synchronize()
+        n = gdn.rmsnorm_residual(y, nw)[0]
+        if wait:
+            torch.cuda.synchronize()
+        gdn.linear(n, w2, weight_layout="nk", out=z)
+        return z.clone()
+    ref = [chain(i, True) for i in range(4)]
+    got = [chain(i % 4, False) for i in range(40)]
+    assert all(torch.equal(got[i], ref[i % 4]) for i in range(40))
+
+
 def _run(gdn, M, N, K, dtype="bf16", layout="nk", gated=False, act="none", bias=False, residual=False, out=None, **kw):
     out = out or ("f32" if dtype == "f32" else "bf16")
     t = _draw(M, N, K, dtype, layout, gated, bias, residual, out, seed=M * 31 + N * 7 + K)
