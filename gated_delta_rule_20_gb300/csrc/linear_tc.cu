@@ -21,6 +21,8 @@
 // (cta_group::2) on tiles of 256 columns x up to 256 tokens; every CTA loads its 128 columns and
 // half of the tokens.  Two accumulators in TMEM: the epilogue of one tile runs beside the next
 // tile's products.  (fp32 by bf16 parts, at the end of the file, takes all of TMEM for one tile.)
+//
+// linear_joint_kernel (a few tiles and a long K): two to four such pairs on a tile, each with its part of K.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -890,6 +892,208 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_sync_relaxed();  // neither CTA exits while the pair's TMEM is being freed
 }
 
+// ------------------------------------------------------------------ a few tiles, K split over pairs
+// One tile a cluster of `splits` CTA pairs, each with its part of K; then pair q finishes the 32-token chunks
+// q, q + splits, ... of the tile: every pair sends its sums of the others' chunks into their shared memory (the
+// stages, which are free by then), and adds what it gets in the pairs' order.
+//
+// Bound as linear_large_kernel, by the weight's and the tokens' way from L2; with fewer tiles than pairs of SMs the
+// parts of K fill the others, or allow larger tiles.
+constexpr uint32_t kChunkBytes = 128 * 32 * 4;  // a chunk's partial sums in a CTA: [token / 4][row][4]
+
+// Where the sums of chunk c from pair `from` lie in the CTA that finishes it.
+__device__ __forceinline__ uint32_t chunk_slot(int c, int from, int splits) {
+    const int owner = c % splits;
+    return (uint32_t)(c / splits * (splits - 1) + (from < owner ? from : from - 1)) * kChunkBytes;
+}
+
+// The chunks that this warp finishes of the tile at (tn, tm); `part`: the shared memory that the others have filled.
+template <bool GATED>
+__device__ __forceinline__ void finish_chunks(const TcArgs& t, float* swap, uint32_t part, uint32_t tmem, int rank, int q, int tn,
+                                              int tm) {
+    constexpr int C = GATED ? 16 : 32;
+    const LinearArgs& a = t.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3, half = (warp - 2) >> 2, row = quad * 32 + lane, S = t.splits;
+    const bool up = GATED && quad >= 2;  // as in `epilogue`
+    const int own = up ? 16 : 0;
+    const uint32_t pair_bar = 1 + (quad & 1) + 2 * half;
+    float* ex = swap + ((quad & 1) + 2 * half) * (2 * 2 * 16 * 32) + lane;
+    const int n = (tn * 2 + rank) * (GATED ? 64 : 128) + (GATED ? row & 63 : row), col = up ? a.N + n : n;
+    const bool live = n < a.N;
+    const float ws = a.w_scale && live ? a.w_scale[col] : 1.f;
+    const float bias = a.bias && live ? a.bias[col] : 0.f;
+    int flip = 0;
+#pragma unroll 1
+    for (int c = q + half * S; c < t.bn / 32; c += 2 * S) {
+        const int m0 = tm * t.bn + c * 32;
+        uint32_t r[C];
+        if (a.res && live) load_residual<C>(a, r, m0 + own, n);
+        float v[32], sum[32];
+        tmem_ld32(tmem + c * 32 + ((uint32_t)(quad * 32) << 16), v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[j] = 0.f;
+#pragma unroll 1
+        for (int p = 0; p < S; ++p) {
+            if (p == q) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[j] += v[j];
+                continue;
+            }
+            const uint32_t at = part + chunk_slot(c, p, S) + row * 16;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const float4 w = ld_cluster_f32x4(at + j / 4 * 2048);
+                sum[j] += w.x, sum[j + 1] += w.y, sum[j + 2] += w.z, sum[j + 3] += w.w;
+            }
+        }
+        if (a.x_scale) {
+            const float mine = m0 + lane < a.M ? a.x_scale[m0 + lane] : 0.f;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[j] *= __shfl_sync(0xffffffffu, mine, j) * ws;
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[j] += bias;
+        if constexpr (!GATED) {
+            if (live) finish<32>(a, sum, nullptr, r, m0, n);
+        } else {
+            float* box = ex + flip * (2 * 16 * 32);
+            flip ^= 1;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) box[(own + j) * 32] = up ? sum[j] : sum[16 + j];
+            named_bar_sync(pair_bar, 64);
+            float g[16], w[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float other = box[((16 - own) + j) * 32];
+                g[j] = up ? other : sum[j];
+                w[j] = up ? sum[16 + j] : other;
+            }
+            if (live) finish<16>(a, g, w, r, m0 + own, n);
+        }
+    }
+}
+
+template <bool F8, bool KN>
+__global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_constant__ CUtensorMap tm_w,
+                                                                   const __grid_constant__ CUtensorMap tm_x,
+                                                                   const __grid_constant__ TcArgs t) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const LinearArgs& a = t.a;
+    constexpr int kSlabElems = F8 ? 128 : 64;
+    const int stages = t.stages, S = t.splits;
+    float* swap = reinterpret_cast<float*>(sm + stages * t.stage_bytes);
+    LargeBars* bars = reinterpret_cast<LargeBars*>(sm + stages * t.stage_bytes + (a.gated ? kSwapBytes : 0));
+    volatile int* abort_flag = &bars->abort;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int place = (int)cluster_rank(), q = place >> 1, rank = place & 1, leader = place & ~1;
+    const int tile = (int)blockIdx.x / (2 * S), tm = tile / t.tiles_n, tn = tile - tm * t.tiles_n;
+    const int k_lo = (int)((long long)t.slabs * q / S), k_hi = (int)((long long)t.slabs * (q + 1) / S);
+    griddep_launch_dependents();
+
+    if (warp == 0) {
+        if (lane < stages) {
+            mbar_init(&bars->full[lane], 1);
+            mbar_init(&bars->empty[lane], 1);
+        } else if (lane == 16) {
+            mbar_init(&bars->acc_full[0], 1);
+        } else if (lane == 30) {
+            bars->abort = 0;
+        }
+        fence_mbar_init();
+        if (lane == 31) {
+            tma_prefetch_desc(&tm_w);
+            tma_prefetch_desc(&tm_x);
+        }
+        __syncwarp();
+    }
+    if (warp == 1) tmem_alloc_pair(&bars->tmem, t.tmem_cols);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_relaxed();  // the peers' barriers are initialised (fence_mbar_init)
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    griddep_wait();
+
+    bool ok = false;
+    if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
+        const int per = a.gated ? 64 : 128, n0 = (tn * 2 + rank) * per, n1 = a.gated ? t.up + n0 : n0 + 64;
+        const int m0 = tm * t.bn + rank * (t.bn / 2);
+        int i = 0;
+        Ring at;
+        for (; i < k_hi - k_lo; ++i, at.next(stages)) {
+            const int s = at.s, k = (k_lo + i) * kSlabElems;
+            if (i >= stages && !mbar_wait_warp(&bars->empty[s], at.phase ^ 1, abort_flag)) break;
+            uint8_t* st = sm + s * t.stage_bytes;
+            if (elect_one()) {
+                if (rank == 0) mbar_arrive_expect_tx(&bars->full[s], 2 * t.stage_bytes);
+                const uint32_t bar = map_to_rank(smem_u32(&bars->full[s]), leader);
+                tma_load_3d_pair(st, &tm_w, bar, KN ? n0 : k, KN ? k : n0, 0);
+                tma_load_3d_pair(st + kHalfW, &tm_w, bar, KN ? n1 : k, KN ? k : n1, 0);
+                tma_load_3d_pair(st + kWBytes, &tm_x, bar, k, m0, 0);
+            }
+            __syncwarp();
+        }
+        if (rank == 0)  // the leader sees both CTAs' loads land (bounded)
+            for (int j = (i > stages ? i - stages : 0); j < i; ++j) (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
+    } else if (warp == 1) {
+        if (rank == 0) {  // MMA issuer of the pair
+            const uint32_t both = 3u << leader;
+            int i = 0;
+            Ring at;
+            for (; i < k_hi - k_lo; ++i, at.next(stages)) {
+                if (!mbar_wait_warp(&bars->full[at.s], at.phase, abort_flag)) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t st = smem_u32(sm) + at.s * t.stage_bytes;
+                    mma_slab<F8, KN, true>(tmem, st, st, t.idesc, i == 0);
+                    mma_commit_pair(&bars->empty[at.s], both);
+                    if (i + 1 == k_hi - k_lo) mma_commit_pair(&bars->acc_full[0], both);
+                }
+                __syncwarp();
+            }
+            if (i > 0) (void)mbar_wait(&bars->empty[(i - 1) % stages], ((i - 1) / stages) & 1);  // all products are done
+        }
+    } else {
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[0], 0, abort_flag));
+    }
+    __syncwarp();
+    cluster_sync();  // every pair's products are done: the stages are free
+    if (ok) {
+        tc_fence_after();
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        for (int c = half; c < t.bn / 32; c += 2) {
+            if (c % S == q) continue;
+            float v[32];
+            tmem_ld32(tmem + c * 32 + ((uint32_t)(quad * 32) << 16), v);
+            tmem_wait_ld();
+            const uint32_t to = map_to_rank(smem_u32(sm) + chunk_slot(c, q, S) + (quad * 32 + lane) * 16, 2 * (c % S) + rank);
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) st_cluster_f32x4(to + j / 4 * 2048, v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+    }
+    __syncwarp();
+    cluster_sync();  // the partial sums are there
+    if (warp >= 2) {
+        const uint32_t pair_bar = 1 + (warp & 1) + 2 * ((warp - 2) >> 2);
+        if (a.gated) ok = !named_bar_any(pair_bar, 64, !ok);  // one answer for the warps that meet at a barrier
+        if (ok && a.gated)
+            finish_chunks<true>(t, swap, smem_u32(sm), tmem, rank, q, tn, tm);
+        else if (ok)
+            finish_chunks<false>(t, swap, smem_u32(sm), tmem, rank, q, tn, tm);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_relaxed();
+    if (tid == 0 && bars->abort) atomicExch(t.status, (int32_t)GDN_ERR_TIMEOUT);
+    __syncwarp();
+    if (warp == 1) tmem_dealloc_pair(tmem, t.tmem_cols);
+    cluster_sync_relaxed();  // neither CTA exits while the pair's TMEM is being freed
+}
+
 // ------------------------------------------------------------------ host side
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -979,8 +1183,8 @@ cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorM
                   t.splits, s, tw, tx, t);
 }
 
-// What runs: the pair kernel on tiles of bn tokens, or the small one on tiles of bn tokens with K over
-// `splits` CTAs.
+// What runs, on tiles of bn tokens: pairs (large), with K over `splits` of them where that is more than one, or
+// the small kernel with K over `splits` CTAs.
 struct Plan {
     bool large;
     int bn, splits;
@@ -994,7 +1198,11 @@ struct Plan {
 //   - pairs: 0.28 us a slab at 256 tokens (the tensor cores' time), in proportion down to 0.19 (the weight's way
 //     from L2), and bn / 300 for the last tile's outputs.  M = 512, K = N = 4096: 20.6 the best small plan, 16.9 pairs
 //     at 128, 22.4 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
-// On 91 shapes (M = 1 .. 2048) the choice is 0.8 % behind the best of all on average; by parts, on 17 shapes, it is it.
+//   - pairs that split K: the same for their share of K, and 0.6 us a pair and bn 0.012 for the sums' way.  Where not
+//     all clusters fit at once this is no choice (of 4, 6 and 8 CTAs 36, 23 and 15 do on 152 SMs).  M = 768, K = 8192,
+//     N = 2048: 28.7 pairs, 20.5 two a tile of 192; M = 384, K = 4096, N = 2048: 13.7 small, 15.8 pairs, 11.6 two a tile
+//     of 128; M = 1024, K = N = 2048: 10.3 pairs, 12.5 two a tile of 256.
+// On 48 shapes (M = 64 .. 1024) the choice is 0.3 % behind the best of all on average; by parts, on 17 shapes, it is it.
 Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
     const int parts = accs > 1 ? 3 : 1, products = accs > 1 ? 6 : 1;  // stages and products of a slab
@@ -1008,6 +1216,13 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
         if (accs > 1) t += (turns - 1) * accs * bn / 200.0;  // epilogues that nothing runs beside
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
         if (t < least) least = t, best = Plan{true, bn, 1};
+        for (int S = 2; S <= 4 && accs == 1 && 2 * S <= slabs; ++S) {
+            if (tiles > sms / (2 * S) - 2 * (S - 1)) break;
+            t = (slabs + S - 1) / S * (mma > in ? mma : in);
+            if (t < weight_mb / 6.3) t = weight_mb / 6.3;
+            t += 0.012 * bn + 0.6 * S;
+            if (t < least) least = t, best = Plan{true, bn, S};
+        }
     }
     for (int bn = 16; bn <= (accs > 1 ? 256 / accs : 128); bn *= 2) {  // (two CTAs an SM share TMEM)
         if (bn > 16 && bn / 2 >= a.M) break;
@@ -1125,6 +1340,47 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+template <bool F8, bool KN>
+cudaError_t launch_joint(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, size_t smem, int dev,
+                         cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];
+    return launch(linear_joint_kernel<F8, KN>, done, dev, dim3((unsigned)(tiles * 2 * t.splits)), kThreads, smem, 2 * t.splits, s,
+                  tw, tx, t);
+}
+
+gdn_status run_joint(const LinearArgs& a, const Operands& op, bool f8, Plan how, int dev, cudaStream_t s) {
+    TcArgs t{};
+    t.a = a;
+    t.up = op.up;
+    t.accs = 1;
+    const int elems = f8 ? 128 : 64, per = a.gated ? 128 : 256;
+    t.slabs = (a.K + elems - 1) / elems;
+    t.tiles_n = (int)(((long long)a.N + per - 1) / per);
+    t.bn = how.bn;
+    t.splits = how.splits;
+    t.tiles_m = (a.M + t.bn - 1) / t.bn;
+    t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
+    // (the others' sums of a CTA's chunks, 96 KB at the most, fit the stages, 184 KB at the least)
+    const size_t fixed = sizeof(LargeBars) + (a.gated ? kSwapBytes : 0) + 1024;
+    t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
+    if (t.stages > kLargeStages) t.stages = kLargeStages;
+    t.tmem_cols = 32;
+    while (t.tmem_cols < (uint32_t)t.bn) t.tmem_cols <<= 1;
+    t.idesc = f8 ? make_idesc_e4m3(256, t.bn) : make_idesc_bf16(256, t.bn, a.nk ? 0 : 1, 0);
+    gdn_status st = status_word_for_current_device(&t.status);
+    if (st != GDN_OK) return st;
+    CUtensorMap tw, tx;
+    if (!encode(&tw, f8, op.w, a.nk ? op.w_cols : a.K, a.nk ? a.K : op.w_cols, op.w_pitch, 64) ||
+        !encode(&tx, f8, op.x, a.M, a.K, op.x_pitch, t.bn / 2))
+        return GDN_ERR_CUDA;
+    const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
+    const int tiles = t.tiles_n * t.tiles_m;
+    const cudaError_t e = f8     ? launch_joint<true, false>(t, tw, tx, tiles, smem, dev, s)
+                          : a.nk ? launch_joint<false, false>(t, tw, tx, tiles, smem, dev, s)
+                                 : launch_joint<false, true>(t, tw, tx, tiles, smem, dev, s);
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 }  // namespace
 
 namespace {
@@ -1232,6 +1488,7 @@ bool takes(const void* p, long long cols, int size) {
 
 gdn_status run_tc(const LinearArgs& a, const Operands& op, bool f8, int dev, int sms, cudaStream_t s) {
     const Plan how = plan(a, (a.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64), op.accs, sms);
+    if (how.large && how.splits > 1) return run_joint(a, op, f8, how, dev, s);
     return how.large ? run_large(a, op, f8, how, dev, sms, s) : run_small(a, op, f8, how, dev, s);
 }
 

@@ -433,11 +433,11 @@ __device__ __forceinline__ void mma_step(uint32_t d_tmem, uint64_t adesc, uint64
         mma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
 }
 // Arrive once on the barrier at bar's offset in both CTAs of the pair when every MMA issued so far is done.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint32_t ctas = 3) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)ctas)
         : "memory");
 }
 // TMEM of a CTA pair: a warp of each CTA takes part, and each CTA gets the columns at the same address.
@@ -479,6 +479,9 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
     return v;
+}
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t a, float x, float y, float z, float w) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(x), "f"(y), "f"(z), "f"(w) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");

@@ -268,6 +268,17 @@ def test_fp32_products_with_infinities_and_nan(gdn, where, bad, gated):
     assert torch.equal(got.view(torch.int32), ref.view(torch.int32)) and not torch.isfinite(ref).all()
 
 
+@pytest.mark.parametrize("M,N,K,dtype,layout,gated,out", [
+    (384, 2048, 4096, "bf16", "kn", False, "bf16"), (391, 2041, 4104, "bf16", "nk", False, "bf16"), (768, 2048, 8192, "bf16", "kn", False, "f32"),
+    (250, 1100, 6000, "bf16", "nk", False, "bf16"), (513, 1024, 8192, "bf16", "nk", True, "bf16"), (300, 1016, 4120, "bf16", "kn", True, "f32"),
+    (500, 2048, 8192, "f8", "nk", False, "bf16"), (380, 1001, 8208, "f8", "nk", True, "bf16"), (1100, 500, 16000, "bf16", "nk", False, "f32")])
+@pytest.mark.parametrize("full", [False, True])
+def test_few_tiles_and_a_long_K(gdn, M, N, K, dtype, layout, gated, out, full):
+    """The sizes of the pairs that split K: whole and ragged tiles, uneven shares of K, odd rows; with everything in
+    the epilogue and without."""
+    _run(gdn, M, N, K, dtype, layout, gated, "gelu" if full else "none", bias=full, residual=full, out=out)
+
+
 @pytest.mark.parametrize("dtype,layout", [("f32", "kn"), ("f32", "nk"), ("bf16", "kn"), ("bf16", "nk"), ("f8", "nk")])
 @pytest.mark.parametrize("M,N,K", [
     (1, 1, 1), (1, 31, 37), (1, 64, 128), (1, 600, 130), (1, 33, 9000), (1, 2000, 1025), (1, 16, 12345), (2, 130, 257), (3, 48, 512),
