@@ -70,7 +70,8 @@ __device__ __forceinline__ void fma2(uint64_t& acc, uint64_t u, uint64_t v) {
 
 // kNK: the weight is [N', K]; splits: CTAs of the cluster, each with its part of K (TM = 4 only).
 template <typename T, int TM, bool kNK, bool kVec>
-__global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_constant__ LinearArgs a, int splits, const uint8_t* unfit, int marks) {
+__global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_constant__ LinearArgs a, int splits,
+                                                             const LinearMarks marks) {
     constexpr int SIDE = 16, kThreads = SIDE * SIDE, kTile = TM * SIDE, kPitch = kTile + 4;
     constexpr int kQuads = kTile * kBK / 4 / kThreads;       // 4-element loads a thread
     constexpr int kAhead = TM == 8 ? 1 : 4;                  // steps loaded ahead
@@ -87,10 +88,9 @@ __global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_consta
     const int k_hi = rank + 1 == splits ? a.K : (int)((long long)steps * (rank + 1) / splits) * kBK;
     ptx::griddep_launch_dependents();
     ptx::griddep_wait();
-    if (unfit) {  // only for operands that the tensor cores' parts do not fit (one answer for the whole grid)
-        int any = 0;
-        for (int i = tid; i < marks; i += kThreads) any |= unfit[i];
-        if (!__syncthreads_or(any)) return;
+    if (marks.tops) {  // only for operands that the tensor cores' parts do not fit (one answer for the whole grid)
+        __shared__ uint32_t tops[kThreads / 32];
+        if (parts_fit_all<kThreads>(marks.tops, marks.count, a.K, tops)) return;
     }
     // This thread's pieces: of x (and of a [N', K] weight) 4 elements of K of rows tid / 4 + i kThreads / 4, of a
     // [K, N'] weight 4 columns of one k.  Their addresses at k = 0, and how many elements of the piece's
@@ -292,7 +292,7 @@ cudaError_t launch_tile(const LinearArgs& a, int splits, const LinearMarks& mark
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = splits > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_ffma_kernel<T, TM, kNK, kVec>, a, splits, marks.unfit, marks.count);
+    return cudaLaunchKernelEx(&cfg, linear_ffma_kernel<T, TM, kNK, kVec>, a, splits, marks);
 }
 
 template <typename T, int TM>
@@ -312,7 +312,7 @@ cudaError_t launch_ffma(const LinearArgs& a, int32_t dtype, int sms, const Linea
     // Few rows: a kernel that reads the weight once for every 4.  It and the tiles below, us: fp32 K = N = 2048 M = 12
     // 13.9 and 18.8, M = 16 13.8 and 18.9 but K = 4097, N = 2001 51 and 38; e4m3 K = 4097, N = 2001 M = 8 50 and 50, M = 12
     // 57 and 50.
-    if (a.M <= (dtype == GDN_F8E4M3 ? 8 : 12) && !marks.unfit) return launch_linear_few(a, dtype, sms, s);
+    if (a.M <= (dtype == GDN_F8E4M3 ? 8 : 12) && !marks.tops) return launch_linear_few(a, dtype, sms, s);
     const long long wn = a.gated ? 2LL * a.N : a.N;
     auto tiles = [&](int t) { return ((a.M + (long long)t - 1) / t) * ((wn + t - 1) / t); };
     if (tiles(128) >= sms) return launch_layout<T, 8>(a, 1, marks, s);

@@ -34,12 +34,48 @@ struct LinearPlan {
 };
 LinearPlan plan_linear(const LinearArgs& a, int32_t dtype);
 
-// Marks of blocks that met elements which parts are not for, known on the device: with any of them the product by parts has
-// not been done, and the FFMA kernel behind it does it (else that one does nothing).
+// What fp32 operands by parts are found to be on the device: of `count` blocks, the exponents (biased, as in the number's
+// bits; 255 for infinities and NaN, 0 where all is zero) of the largest elements that they met of x, and behind those of
+// the weight.  Where parts_fit says no the product by parts does nothing, and the FFMA kernel behind it does it all (else
+// that one does nothing).
 struct LinearMarks {
-    const uint8_t* unfit;
+    const uint8_t* tops;
     int count;
 };
+
+// Whether products of K by parts give what fp32 sums give, for operands under 2^(ex - 126) and 2^(ew - 126):
+//   - infinities and NaN do not add up from parts; the largest numbers (ex = 254) round up to an infinite first part;
+//   - no sum of the parts' products may pass the range: an infinity of one accumulator could meet another's of the
+//     opposite sign.  Every accumulator stays under K 2^(ex + ew - 252), which is held to 2^127.
+__device__ __forceinline__ bool parts_fit(int ex, int ew, int K) {
+    const int log_k = 32 - __clz(K - 1);  // (rounded up; 0 for K = 1)
+    if (max(ex, ew) >= 254) return false;
+    if (min(ex, ew) == 0) return true;  // zeros
+    return ex + ew <= 379 - log_k;
+}
+
+// The same from the blocks' tops, for all threads of a CTA of kThreads (room: a word a warp in shared memory).
+template <int kThreads>
+__device__ __forceinline__ bool parts_fit_all(const uint8_t* tops, int count, int K, uint32_t* room) {
+    const uint32_t* words = reinterpret_cast<const uint32_t*>(tops);  // (count is a multiple of 4)
+    uint32_t x = 0, w = 0;
+    for (int i = threadIdx.x; i < count / 4; i += kThreads) {
+        x = __vmaxu4(x, words[i]);
+        w = __vmaxu4(w, words[count / 4 + i]);
+    }
+    auto top = [](uint32_t v) {
+        v = __vmaxu4(v, v >> 16);
+        return __reduce_max_sync(0xffffffffu, max(v & 0xffu, (v >> 8) & 0xffu));
+    };
+    const uint32_t ex = top(x), ew = top(w);
+    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = ex | ew << 16;
+    __syncthreads();
+    uint32_t both = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) both = __vmaxu2(both, room[i]);
+    return parts_fit((int)(both & 0xffffu), (int)(both >> 16), K);
+}
+
 // Enqueues every route but kFfma; marks are set for kParts.
 gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, LinearRoute route, void* scratch, int dev, int sms,
                             cudaStream_t s, LinearMarks* marks);

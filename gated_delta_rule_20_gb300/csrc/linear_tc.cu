@@ -58,7 +58,7 @@ struct TcArgs {
     int32_t* status;
     int accs, starts[kMaxAccs];     // fp32 by parts: accumulators of a tile, from 1 on each from its first slab (else one)
     int plane;                      // fp32 by parts: elements of K from one part to the next
-    const uint8_t* unfit;           // fp32 by parts: marks of `marks` blocks; any of them: not for this kernel
+    const uint8_t* tops;            // fp32 by parts: see LinearMarks (null otherwise)
     int marks;
 };
 
@@ -69,6 +69,7 @@ struct SmallBars {
     uint64_t full[kMaxStages], empty[kMaxStages], done;
     uint32_t tmem;
     int abort;
+    uint32_t tops[kThreads / 32];  // fp32 by parts: see parts_fit_all
 };
 
 // A place in the ring of stages: the stage and the parity of the barrier phase that its next use waits
@@ -222,14 +223,7 @@ __device__ __forceinline__ void join_splits(const TcArgs& t, uint32_t part, int 
     }
 }
 
-// Whether any block has left its mark, for all threads of the CTA.
-__device__ __forceinline__ bool any_mark(const uint8_t* marks, int count) {
-    int any = 0;
-    for (int i = threadIdx.x; i < count; i += (int)blockDim.x) any |= marks[i];
-    return __syncthreads_or(any) != 0;
-}
-
-// PARTS: an fp32 product by bf16 parts (several accumulators a tile, marks).
+// PARTS: an fp32 product by bf16 parts (several accumulators a tile, operands that parts may not fit).
 template <bool F8, bool KN, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                            const __grid_constant__ CUtensorMap tm_x,
@@ -273,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     griddep_wait();  // the preceding kernel's results; nothing of the caller's is read before
-    const bool run = !(PARTS && any_mark(t.unfit, t.marks));  // one answer for the whole grid
+    const bool run = !PARTS || parts_fit_all<kThreads>(t.tops, t.marks, a.K, bars->tops);  // one answer for the whole grid
 
     if (warp == 0 && run) {  // TMA producer
         int loaded = 0, part = kSlabStages - 1, slab = k_lo * kSlabElems;
@@ -389,6 +383,7 @@ struct LargeBars {
     uint64_t res_full[kEpiWarps / 2];                  // staged residual boxes
     uint32_t tmem;
     int abort;
+    uint32_t tops[kThreads / 32];                      // fp32 by parts: see parts_fit_all
 };
 
 // A tile's tokens are worked off in chunks of 32, the first half of them (rounded up) by the first four
@@ -806,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     griddep_wait();
-    const bool run = !(PARTS && any_mark(t.unfit, t.marks));  // one answer for the whole grid
+    const bool run = !PARTS || parts_fit_all<kThreads>(t.tops, t.marks, a.K, bars->tops);  // one answer for the whole grid
 
     if (!run) {
     } else if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
@@ -1168,7 +1163,7 @@ struct Operands {
     const void *x, *w;
     long long x_pitch, w_pitch, w_cols;
     int up;
-    const uint8_t* unfit = nullptr;  // see TcArgs
+    const uint8_t* tops = nullptr;  // see TcArgs
     int marks = 0;
     int accs = 1, starts[kMaxAccs] = {};
     int plane = 0;  // of parts: see TcArgs (depth: the rows or columns of K that there are)
@@ -1251,7 +1246,7 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     TcArgs t{};
     t.a = a;
     t.up = op.up;
-    t.unfit = op.unfit;
+    t.tops = op.tops;
     t.marks = op.marks;
     t.accs = op.accs;
     for (int q = 0; q < kMaxAccs; ++q) t.starts[q] = op.starts[q];
@@ -1297,7 +1292,7 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     TcArgs t{};
     t.a = a;
     t.up = op.up;
-    t.unfit = op.unfit;
+    t.tops = op.tops;
     t.marks = op.marks;
     t.accs = op.accs;
     for (int q = 0; q < kMaxAccs; ++q) t.starts[q] = op.starts[q];
@@ -1431,17 +1426,16 @@ struct SplitJob {
     long long rows_in, rows_out, cols, width, pitch, plane, half, up;
 };
 
-// marks[block]: whether the block met an element that parts are not for: an infinity or a NaN, for which they do
-// not add up, or one past 2^63, whose products of parts could be infinities of both signs where the product is one.
+// tops[block], tops[gridDim.x + block]: the exponents of the largest elements of x and of the weight that the block
+// met (see LinearMarks).
 // 16 bytes are read at a time where a piece lies whole and on such a boundary (2048 x 2048 twice: 28 us by elements).
-constexpr float kPartMax = 9.2233720e18f;
-
 __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ SplitJob x, const __grid_constant__ SplitJob w,
-                                                           uint8_t* marks) {
+                                                           uint8_t* tops) {
+    __shared__ uint32_t warp_tops[2][256 / 32];
     griddep_launch_dependents();
     griddep_wait();
     const long long x_pieces = x.rows_out * (x.width / 8), pieces = x_pieces + w.rows_out * (w.width / 8);
-    int bad = 0;
+    uint32_t top_x = 0, top_w = 0;  // (magnitudes are ordered as their bits are, infinities and NaN above all)
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (long long)gridDim.x * 256) {
         const SplitJob& c = i < x_pieces ? x : w;
         const long long at = i < x_pieces ? i : i - x_pieces, row = at / (c.width / 8), d0 = at % (c.width / 8) * 8;
@@ -1460,10 +1454,11 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
             }
         }
         __nv_bfloat16 part[3][8];
+        uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float v = in[j];
-            bad |= !(fabsf(v) <= kPartMax);
+            top = max(top, __float_as_uint(v) & 0x7fffffffu);
             __nv_bfloat16 p = __float2bfloat16_rn(v);
             part[0][j] = p;
             float left = v - __bfloat162float(p);
@@ -1476,9 +1471,21 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
         uint4* dst = reinterpret_cast<uint4*>(c.dst + row * c.pitch + d0);
 #pragma unroll
         for (int k = 0; k < kParts; ++k) dst[k * (c.plane / 8)] = o[k];
+        if (i < x_pieces)
+            top_x = max(top_x, top);
+        else
+            top_w = max(top_w, top);
     }
-    bad = __syncthreads_or(bad);
-    if (threadIdx.x == 0) marks[blockIdx.x] = bad != 0;
+    top_x = __reduce_max_sync(0xffffffffu, top_x);
+    top_w = __reduce_max_sync(0xffffffffu, top_w);
+    if ((threadIdx.x & 31) == 0) warp_tops[0][threadIdx.x >> 5] = top_x, warp_tops[1][threadIdx.x >> 5] = top_w;
+    __syncthreads();
+    if (threadIdx.x < 2) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 256 / 32; ++i) top = max(top, warp_tops[threadIdx.x][i]);
+        tops[threadIdx.x * gridDim.x + blockIdx.x] = (uint8_t)(top == 0 ? 0 : max(top >> 23, 1u));
+    }
 }
 
 // Whether TMA can take an operand of `cols`-element rows as it lies.
@@ -1532,7 +1539,7 @@ void split_jobs(const LinearArgs& a, SplitJob* x, SplitJob* w) {
     w->plane = kp * w->pitch;
 }
 size_t job_bytes(const SplitJob& c, bool planes) { return (size_t)((planes ? kParts * c.plane : c.rows_out * c.pitch) * 2); }
-constexpr int kSplitBlocks = 1216;  // (8 a GB300's SM)
+constexpr int kSplitBlocks = 1216;  // (8 a GB300's SM; a multiple of 4: see parts_fit_all)
 
 gdn_status run_copies(const LinearArgs& a, bool f8, uint8_t* scratch, int dev, int sms, cudaStream_t s) {
     const int size = f8 ? 1 : 2;
@@ -1563,13 +1570,13 @@ gdn_status run_parts(const LinearArgs& a, uint8_t* scratch, int dev, int sms, cu
     split_jobs(a, &x, &w);
     x.dst = reinterpret_cast<__nv_bfloat16*>(scratch);
     w.dst = reinterpret_cast<__nv_bfloat16*>(scratch + job_bytes(x, false));
-    uint8_t* unfit = scratch + job_bytes(x, false) + job_bytes(w, !a.nk);
-    *marks = LinearMarks{unfit, kSplitBlocks};
-    linear_split_kernel<<<kSplitBlocks, 256, 0, s>>>(x, w, unfit);
+    uint8_t* tops = scratch + job_bytes(x, false) + job_bytes(w, !a.nk);
+    *marks = LinearMarks{tops, kSplitBlocks};
+    linear_split_kernel<<<kSplitBlocks, 256, 0, s>>>(x, w, tops);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
     const bool halves = !a.nk && a.gated;
     Operands op{x.dst, w.dst, x.pitch, w.pitch, halves ? w.up + a.N : a.gated ? 2LL * a.N : a.N, halves ? (int)w.up : a.N};
-    op.unfit = unfit;
+    op.tops = tops;
     op.marks = kSplitBlocks;
     // the x1 w1 terms: an accumulator for every 704 of K, three at the most
     const int slabs = (a.K + 63) / 64, wanted = (slabs + 10) / 11 < kMaxAccs - 1 ? (slabs + 10) / 11 : kMaxAccs - 1;
@@ -1592,7 +1599,7 @@ LinearPlan plan_linear(const LinearArgs& a, int32_t dtype) {
         if (ops < 3e8 || a.K > 4096 || a.M < 16) return LinearPlan{LinearRoute::kFfma, 0};
         SplitJob x, w;
         split_jobs(a, &x, &w);
-        const size_t bytes = job_bytes(x, false) + job_bytes(w, !a.nk) + kSplitBlocks;
+        const size_t bytes = job_bytes(x, false) + job_bytes(w, !a.nk) + 2 * kSplitBlocks;
         return bytes > (size_t)4 << 30 ? LinearPlan{LinearRoute::kFfma, 0} : LinearPlan{LinearRoute::kParts, bytes};
     }
     const int size = dtype == GDN_BF16 ? 2 : 1;
