@@ -46,12 +46,14 @@ struct LinearMarks {
 // Whether products of K by parts give what fp32 sums give, for operands under 2^(ex - 126) and 2^(ew - 126):
 //   - infinities and NaN do not add up from parts; the largest numbers (ex = 254) round up to an infinite first part;
 //   - no sum of the parts' products may pass the range: an infinity of one accumulator could meet another's of the
-//     opposite sign.  Every accumulator stays under K 2^(ex + ew - 252), which is held to 2^127.
+//     opposite sign.  Every accumulator stays under K 2^(ex + ew - 252), which is held to 2^127;
+//   - the least bf16 number, 2^-133, is below 2^-24 of an operand's largest elements by a factor of 2^-8 (ex >= 27), and
+//     the largest products are far enough above the least normal number (2^-100; ex + ew >= 154).
 __device__ __forceinline__ bool parts_fit(int ex, int ew, int K) {
     const int log_k = 32 - __clz(K - 1);  // (rounded up; 0 for K = 1)
     if (max(ex, ew) >= 254) return false;
     if (min(ex, ew) == 0) return true;  // zeros
-    return ex + ew <= 379 - log_k;
+    return min(ex, ew) >= 27 && ex + ew >= 154 && ex + ew <= 379 - log_k;
 }
 
 // The same from the blocks' tops, for all threads of a CTA of kThreads (room: a word a warp in shared memory).

@@ -421,10 +421,11 @@ typedef struct {
  * on an FFMA kernel.  fp32 runs on the FFMA kernel, from 3e8 operations, 16 rows and up to
  * K = 4096 on the tensor cores: the operands are split into three bf16 parts each, which add up
  * exactly, and the products of parts down to 2^-16 are summed in fp32 (three launches).  Operands
- * that parts do not fit are found on the device and left to the FFMA kernel: infinities and NaN,
- * and operands whose sums could pass fp32's range (K times the product of their largest magnitudes,
- * each rounded up to a power of two, above 2^127).  What an operand has below 2^-133, the least bf16
- * number, is lost.  Copies and parts lie in scratch from cudaMallocAsync on `stream`, freed there (gdn_linear_ws takes it from the
+ * that parts do not fit are found on the device and left to the FFMA kernel: infinities and NaN;
+ * operands whose sums could pass fp32's range (K times the product of their largest magnitudes,
+ * each rounded up to a power of two, above 2^127); an operand that is below 2^-100 whole, or both
+ * where the product of their largest magnitudes is.  In the others, what single elements have below
+ * 2^-133, the least bf16 number, is lost.  Copies and parts lie in scratch from cudaMallocAsync on `stream`, freed there (gdn_linear_ws takes it from the
  * caller); calls whose scratch cannot be had, or would pass 4 GiB of parts, run on the FFMA
  * kernel.  Results do not depend on what else runs: every sum has one order for given arguments
  * and device.

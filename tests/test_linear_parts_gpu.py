@@ -135,6 +135,16 @@ def test_largest_sums_in_range(gdn):
 
 
 @gpu
+@pytest.mark.parametrize("M,N,K,layout", [(333, 1030, 770, "kn"), (64, 2048, 2048, "nk")])
+@pytest.mark.parametrize("ax,aw", [(-118, 0), (0, -115), (-118, 60), (60, -118), (-52, -56)])
+def test_operands_that_are_tiny_whole(gdn, M, N, K, layout, ax, aw):
+    """Operands whose parts would pass below the least bf16 number keep the accuracy of fp32 sums."""
+    x, w = _operands(M, N, K, seed=7)
+    x, w = x * 2.0 ** ax, w * 2.0 ** aw
+    assert _norm_error(_linear(gdn, x, w, layout), _exact(x, w)) <= _norm_bar(K)
+
+
+@gpu
 @pytest.mark.parametrize("which", ["x", "weight"])
 def test_tiny_rows_among_others(gdn, which):
     """Rows of x (or columns of the weight) of 2^-100 to 2^-140 beside ordinary ones: what an element has below 2^-133 may
