@@ -14,8 +14,11 @@
 // max |h w| are reduced together.
 //
 // The statistics take the unrounded fp32 h; the only roundings are those of
-// the two outputs.  A NaN or an infinity in a row makes mean(h^2) so, and by it
-// the row's y, maximum and scale NaN, as in the formula.
+// the two outputs.  A NaN in a row makes mean(h^2) one, and by it the row's y,
+// maximum and scale, as in the formula; an infinity makes its own y NaN and the
+// row's others 0 (finite / infinity), and in 8 bits the whole row and its scale
+// NaN.  A row of numbers whose sum of squares passes fp32's range (|h| of 1e19
+// and more) comes out as zeros.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -68,9 +71,11 @@ __device__ __forceinline__ float2 reduce_row(float ss, float mx, float2 (*part)[
     return make_float2(ss, mx);
 }
 
-// What turns h w into the output: the norm's factor, over the row's scale for e4m3.
+// What turns h w into the output, (h w x) y: the norm's factor, over the row's scale for e4m3 (x = 1).  Where that passes
+// fp32's range (rows of the least scale with a small eps, zeros among them: from 1 / sqrt(eps) = 7.6e5 on), the factor and the
+// scale's inverse are applied one after the other.
 template <typename O>
-__device__ __forceinline__ float row_factor(float2 stat, const NormArgs& a, long long r, bool first) {
+__device__ __forceinline__ float2 row_factor(float2 stat, const NormArgs& a, long long r, bool first) {
     const float rinv = rsqrtf(stat.x / (float)a.D + a.eps);
     if constexpr (std::is_same<O, F8>::value) {
         float m = stat.y * rinv;
@@ -78,10 +83,17 @@ __device__ __forceinline__ float row_factor(float2 stat, const NormArgs& a, long
         if (m > 3.4e38f) m = __int_as_float(0x7fc00000);  // an infinite weight: no scale stands for the row
         const float scale = m / 448.f;
         if (first) a.scale[r] = scale;
-        return rinv / scale;
+        const float f = rinv / scale;
+        return f > 3.4e38f && rinv < 3.4e38f ? make_float2(rinv, 1.f / scale) : make_float2(1.f, f);
     } else {
-        return rinv;
+        return make_float2(1.f, rinv);
     }
+}
+// h w, scaled as row_factor says.
+template <typename O>
+__device__ __forceinline__ float scaled(float hw, float2 f) {
+    if constexpr (std::is_same<O, F8>::value) hw *= f.x;
+    return hw * f.y;
 }
 
 // V elements as a 16-byte piece of the flat array.  One that reaches past the array's end (its last piece,
@@ -222,7 +234,7 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_ve
                 }
                 if constexpr (std::is_same<O, F8>::value) mx = max_nan(mx, fabsf(h[p][j]));
             }
-        const float f = row_factor<O>(reduce_row<GROUP>(ss, mx, part, turn), a, r, t == 0);
+        const float2 f = row_factor<O>(reduce_row<GROUP>(ss, mx, part, turn), a, r, t == 0);
 #pragma unroll
         for (int p = 0; p < P; ++p) {
             const int i = t + p * GROUP;
@@ -231,7 +243,8 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_ve
                 uint32_t q[V / 4];
 #pragma unroll
                 for (int j = 0; j < V; j += 4)
-                    q[j / 4] = pack_e4m3x4(h[p][j] * f, h[p][j + 1] * f, h[p][j + 2] * f, h[p][j + 3] * f);
+                    q[j / 4] = pack_e4m3x4(scaled<O>(h[p][j], f), scaled<O>(h[p][j + 1], f), scaled<O>(h[p][j + 2], f),
+                                           scaled<O>(h[p][j + 3], f));
                 if constexpr (V == 8)
                     store_piece<uint8_t, uint2, kOdd>(static_cast<uint8_t*>(a.out), first + i, i * V - shift, D,
                                                       make_uint2(q[0], q[1]));
@@ -241,7 +254,7 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_ve
                 uint4 o;
                 T* oe = reinterpret_cast<T*>(&o);
 #pragma unroll
-                for (int j = 0; j < V; ++j) oe[j] = from_f32<T>(h[p][j] * f);
+                for (int j = 0; j < V; ++j) oe[j] = from_f32<T>(scaled<O>(h[p][j], f));
                 store_piece<T, uint4, kOdd>(static_cast<T*>(a.out), first + i, i * V - shift, D, o);
             }
         }
@@ -285,12 +298,12 @@ __global__ void __launch_bounds__(GROUP == 32 ? 256 : GROUP) rmsnorm_residual_an
             if constexpr (std::is_same<O, F8>::value) mx = max_nan(mx, fabsf(hw));
         }
     }
-    const float f = row_factor<O>(reduce_row<GROUP>(ss, mx, part, 0), a, r, t == 0);
+    const float2 f = row_factor<O>(reduce_row<GROUP>(ss, mx, part, 0), a, r, t == 0);
     for (int i = t; i < a.D; i += GROUP) {
         if constexpr (std::is_same<O, F8>::value)
-            static_cast<uint8_t*>(a.out)[r * a.D + i] = to_e4m3(row[i] * f);
+            static_cast<uint8_t*>(a.out)[r * a.D + i] = to_e4m3(scaled<O>(row[i], f));
         else
-            static_cast<T*>(a.out)[r * a.D + i] = from_f32<T>(row[i] * f);
+            static_cast<T*>(a.out)[r * a.D + i] = from_f32<T>(scaled<O>(row[i], f));
     }
 }
 

@@ -364,6 +364,8 @@ gdn_status gdn_prefill_gated(const void* q, const void* k, const void* v, const 
  *                 (or an infinity) in y is NaN whole, its scale too
  *   out_scale     [rows] fp32, read only where out_dtype is GDN_F8E4M3
  *   eps           >= 0
+ * The squares are summed in fp32: a row whose sum passes its range (|h| of 1e19 and more) comes out as
+ * zeros, and with eps = 0 one whose sum is zero (|h| of 1e-23 and less) as infinities or NaN.
  * rows in [0, 2^31), 1 <= D <= GDN_NORM_MAX_D; pointers aligned to their element;
  * residual_out and out may not be the same buffer (GDN_ERR_UNSUPPORTED).
  * With every pointer 16-byte aligned (and D <= 16384 in bf16, 8192 in fp32; a little less
