@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "gdn.h"
 
 namespace gdn {
@@ -31,6 +33,17 @@ gdn_status status_word_for_current_device(int32_t** out);
 // The current device and its SM count (looked up once a device).
 gdn_status current_device_sms(int* dev, int* sms);
 constexpr int kMaxDevices = 64;  // devices whose facts are kept
+
+// The dynamic shared memory that launches of a kernel may ask for, raised once a device to `bytes`, the most that any
+// of its launches needs (`done`: that kernel's own marks).  The limit belongs to the kernel and not to a launch: set to
+// each launch's size it could be lowered by another thread's call just before the launch.
+template <typename F>
+cudaError_t allow_smem(F* kernel, int bytes, std::atomic<bool> (&done)[kMaxDevices], int dev) {
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
+    return e;
+}
 
 // The argument checks of gdn_prefill, without launching anything.
 gdn_status prefill_checked(const void* q, const void* k, const void* v, const float* g_log, const float* beta,

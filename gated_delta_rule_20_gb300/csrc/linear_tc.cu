@@ -1124,21 +1124,12 @@ bool encode(CUtensorMap* map, bool f8, const void* ptr, long long rows, long lon
 
 constexpr int kSmemLimit = 227 * 1024;
 
-// The shared-memory limit of a kernel, raised once a device (`done`: that kernel's own marks).
-template <typename F>
-cudaError_t allow_smem(F* kernel, std::atomic<bool> (&done)[kMaxDevices], int dev) {
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
-    return e;
-}
-
 // A launch in clusters of `cluster` CTAs that may be set up while the stream's preceding kernel ends
 // (programmatic stream serialization; the kernels wait for that kernel before they read anything).
 template <typename... P, typename... Q>
 cudaError_t launch(void (*kernel)(P...), std::atomic<bool> (&done)[kMaxDevices], int dev, dim3 grid, int threads, size_t smem,
                    int cluster, cudaStream_t s, const Q&... args) {
-    const cudaError_t e = allow_smem(kernel, done, dev);
+    const cudaError_t e = allow_smem(kernel, kSmemLimit, done, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;

@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -324,7 +325,7 @@ cudaError_t launch(void (*kernel)(NormArgs), unsigned grid, int threads, size_t 
 }
 
 template <typename T, typename O, int GROUP, int P, bool kOdd>
-cudaError_t launch_rows(const NormArgs& a, int sms, cudaStream_t s) {
+cudaError_t launch_rows(const NormArgs& a, int dev, int sms, cudaStream_t s) {
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP;
     static const int fit = [] {  // blocks an SM of this instantiation, the same on every device the library is built for
         int n = 0;
@@ -335,9 +336,10 @@ cudaError_t launch_rows(const NormArgs& a, int sms, cudaStream_t s) {
     const size_t smem = kOdd ? (a.D + a.D / V) * sizeof(float) : 0;
     int per_sm = fit;
     if (kOdd && per_sm > (int)(220 * 1024 / (smem + 2048))) per_sm = (int)(220 * 1024 / (smem + 2048));
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr int kMost = GROUP * P * (V + 1) * (int)sizeof(float);  // the longest row's weights and the words left out
+    if constexpr (kOdd && kMost > 40 * 1024) {
+        static std::atomic<bool> done[kMaxDevices];
+        const cudaError_t e = allow_smem(rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>, kMost, done, dev);
         if (e != cudaSuccess) return e;
     }
     const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sms * per_sm;
@@ -345,18 +347,19 @@ cudaError_t launch_rows(const NormArgs& a, int sms, cudaStream_t s) {
 }
 
 template <typename T, typename O, int GROUP, int P>
-cudaError_t launch_vec(const NormArgs& a, int sms, cudaStream_t s) {
-    return a.D % (16 / (int)sizeof(T)) == 0 ? launch_rows<T, O, GROUP, P, false>(a, sms, s)
-                                            : launch_rows<T, O, GROUP, P, true>(a, sms, s);
+cudaError_t launch_vec(const NormArgs& a, int dev, int sms, cudaStream_t s) {
+    return a.D % (16 / (int)sizeof(T)) == 0 ? launch_rows<T, O, GROUP, P, false>(a, dev, sms, s)
+                                            : launch_rows<T, O, GROUP, P, true>(a, dev, sms, s);
 }
 
 template <typename T, typename O, int GROUP>
-cudaError_t launch_any(const NormArgs& a, cudaStream_t s) {
+cudaError_t launch_any(const NormArgs& a, int dev, cudaStream_t s) {
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP;
     const size_t smem = (size_t)kRows * a.D * sizeof(float);
-    if (smem > 40 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(rmsnorm_residual_any_kernel<T, O, GROUP>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if constexpr (GROUP == 1024) {  // (the others' rows take 32 KB at the most)
+        static std::atomic<bool> done[kMaxDevices];
+        const cudaError_t e =
+            allow_smem(rmsnorm_residual_any_kernel<T, O, GROUP>, GDN_NORM_MAX_D * (int)sizeof(float), done, dev);
         if (e != cudaSuccess) return e;
     }
     return launch(rmsnorm_residual_any_kernel<T, O, GROUP>, (unsigned)((a.rows + kRows - 1) / kRows), kBlock, smem, s, a);
@@ -374,19 +377,19 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
     const int nv = (wide & 15u) != 0 ? INT32_MAX : a.D % V == 0 ? a.D / V : (a.D + 2 * V - 2) / V;
     int dev = 0, sms = 0;
     if (current_device_sms(&dev, &sms) != GDN_OK) return cudaErrorInvalidDevice;
-    if (nv <= 32) return launch_vec<T, O, 32, 1>(a, sms, s);
-    if (nv <= 64) return launch_vec<T, O, 32, 2>(a, sms, s);
-    if (nv <= 128) return launch_vec<T, O, 32, 4>(a, sms, s);
-    if (nv <= 256) return launch_vec<T, O, 128, 2>(a, sms, s);
-    if (nv <= 384) return launch_vec<T, O, 128, 3>(a, sms, s);
-    if (nv <= 512) return launch_vec<T, O, 256, 2>(a, sms, s);
-    if (nv <= 768) return launch_vec<T, O, 256, 3>(a, sms, s);
-    if (nv <= 1024) return launch_vec<T, O, 512, 2>(a, sms, s);
-    if (nv <= 1536) return launch_vec<T, O, 512, 3>(a, sms, s);
-    if (nv <= 2048) return launch_vec<T, O, 512, 4>(a, sms, s);
-    if (a.D <= 1024) return launch_any<T, O, 32>(a, s);
-    if (a.D <= 8192) return launch_any<T, O, 256>(a, s);
-    return launch_any<T, O, 1024>(a, s);
+    if (nv <= 32) return launch_vec<T, O, 32, 1>(a, dev, sms, s);
+    if (nv <= 64) return launch_vec<T, O, 32, 2>(a, dev, sms, s);
+    if (nv <= 128) return launch_vec<T, O, 32, 4>(a, dev, sms, s);
+    if (nv <= 256) return launch_vec<T, O, 128, 2>(a, dev, sms, s);
+    if (nv <= 384) return launch_vec<T, O, 128, 3>(a, dev, sms, s);
+    if (nv <= 512) return launch_vec<T, O, 256, 2>(a, dev, sms, s);
+    if (nv <= 768) return launch_vec<T, O, 256, 3>(a, dev, sms, s);
+    if (nv <= 1024) return launch_vec<T, O, 512, 2>(a, dev, sms, s);
+    if (nv <= 1536) return launch_vec<T, O, 512, 3>(a, dev, sms, s);
+    if (nv <= 2048) return launch_vec<T, O, 512, 4>(a, dev, sms, s);
+    if (a.D <= 1024) return launch_any<T, O, 32>(a, dev, s);
+    if (a.D <= 8192) return launch_any<T, O, 256>(a, dev, s);
+    return launch_any<T, O, 1024>(a, dev, s);
 }
 
 }  // namespace
