@@ -361,8 +361,10 @@ namespace {
 
 LinearArgs args_of(const void* x, const float* x_scale, const void* weight, const float* weight_scale, const float* bias,
                    const void* residual, void* out, const gdn_linear_dims* d) {
-    return LinearArgs{x, x_scale, weight, weight_scale, bias, residual, out, (int)d->M, (int)d->N, (int)d->K, d->activation,
-                      d->out_dtype == GDN_F32, (d->flags & GDN_LINEAR_GATED) != 0, (d->flags & GDN_LINEAR_WEIGHT_NK) != 0};
+    const bool f32 = d->out_dtype == GDN_F32;
+    const int act = f32 && d->activation == GDN_ACT_GELU ? kGeluF32 : d->activation;
+    return LinearArgs{x, x_scale, weight, weight_scale, bias, residual, out, (int)d->M, (int)d->N, (int)d->K, act, f32,
+                      (d->flags & GDN_LINEAR_GATED) != 0, (d->flags & GDN_LINEAR_WEIGHT_NK) != 0};
 }
 
 LinearPlan plan_of(const LinearArgs& a, const gdn_linear_dims* d) {

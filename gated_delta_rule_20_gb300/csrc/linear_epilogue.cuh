@@ -19,7 +19,7 @@ struct LinearArgs {
     const void* res;       // may be null; may be out
     void* out;
     int M, N, K;
-    int act;       // gdn_activation
+    int act;       // gdn_activation, or kGeluF32
     bool out_f32;  // else bf16
     bool gated;
     bool nk;       // weight layout
@@ -85,10 +85,11 @@ gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, LinearRoute rout
 // The kernel for few rows on the FMA units (linear_few.cu), for every type, layout, size and alignment.
 cudaError_t launch_linear_few(const LinearArgs& a, int32_t dtype, int sms, cudaStream_t s);
 
-// gelu(v) = v Phi(v), Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by the rational approximation 7.1.26 of Abramowitz
-// and Stegun's Handbook (Hastings): erfc(z) = (a1 s + ... + a5 s^5) e^(-z^2), s = 1 / (1 + 0.3275911 z), off by
-// at most 1.5e-7, so gelu by 0.75e-7 |v|, about one rounding of v.  Half the instructions of erff: M = 16384,
-// K = 512, N = 4096 with GELU takes 96 us, and 122 with erff (without an activation 55).
+// gelu(v) = v Phi(v) for bf16 outputs: Phi(-|v|) = erfc(|v| / sqrt 2) / 2 by the rational approximation 7.1.26 of
+// Abramowitz and Stegun's Handbook (Hastings): erfc(z) = (a1 s + ... + a5 s^5) e^(-z^2), s = 1 / (1 + 0.3275911 z), off by
+// at most 1.5e-7, so gelu by 0.75e-7 |v|: of the value 5e-5 at v = -3 and 1.6e-3 at -5, where half a step of bf16 is
+// 2e-3 to 4e-3.  Half the instructions of erff: M = 16384, K = 512, N = 4096 with GELU takes 96 us, and 122 with erff
+// (without an activation 55).
 __device__ __forceinline__ float gelu(float v) {
     const float z = fabsf(v) * 0.70710678118654752f;
     const float s = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
@@ -100,17 +101,35 @@ __device__ __forceinline__ float gelu(float v) {
     return v * (v > 0.f ? 1.f - q : q);  // (+infinity stays)
 }
 
+// gelu for fp32 outputs, with the relative error of fp32 down to its smallest values: Phi(-a) e^(a^2 / 2) = s (c0 + c1 s + ...
+// + c7 s^7), s = 1 / (1 + 0.31 a), a least-maximum fit of the relative error over a = 0 .. 15 (1.6e-7; with the roundings
+// 1e-6 of gelu for v > -5 and 4e-6 at -12).  (erfcf instead spills the registers of 32 values in linear_large_kernel.)
+constexpr int kGeluF32 = 16;
+__device__ __forceinline__ float gelu_f32(float v) {
+    const float s = __fdividef(1.f, fmaf(0.31f, fabsf(v), 1.f));
+    float p = fmaf(0.035890512f, s, -0.14181866f);
+    p = fmaf(p, s, 0.15545815f);
+    p = fmaf(p, s, -0.015285325f);
+    p = fmaf(p, s, 0.11032595f);
+    p = fmaf(p, s, 0.10770097f);
+    p = fmaf(p, s, 0.12407242f);
+    p = fmaf(p, s, 0.12365606f);
+    const float q = p * s * __expf(-0.5f * v * v);  // Phi(-|v|)
+    return v * (v > 0.f ? 1.f - q : q);
+}
+
 __device__ __forceinline__ float activate(int act, float v) {
     switch (act) {  // uniform over the grid
         case GDN_ACT_SILU: return silu_fast(v);
         case GDN_ACT_GELU: return gelu(v);
+        case kGeluF32: return gelu_f32(v);
         case GDN_ACT_RELU: return v < 0.f ? 0.f : v;  // NaN stays NaN
         default: return v;
     }
 }
 
-// The activation of C values (the choice is uniform over the grid).
-template <int C>
+// The activation of C values (the choice is uniform over the grid).  kBf16: of a kernel for bf16 outputs only.
+template <int C, bool kBf16 = false>
 __device__ __forceinline__ void activate_all(int act, float (&v)[C]) {
     switch (act) {
         case GDN_ACT_SILU:
@@ -120,6 +139,12 @@ __device__ __forceinline__ void activate_all(int act, float (&v)[C]) {
         case GDN_ACT_GELU:
 #pragma unroll
             for (int j = 0; j < C; ++j) v[j] = activate(GDN_ACT_GELU, v[j]);
+            break;
+        case kGeluF32:
+            if constexpr (!kBf16) {
+#pragma unroll
+                for (int j = 0; j < C; ++j) v[j] = activate(kGeluF32, v[j]);
+            }
             break;
         case GDN_ACT_RELU:
 #pragma unroll

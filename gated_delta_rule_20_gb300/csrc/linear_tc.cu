@@ -690,8 +690,8 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
                     for (int j = 0; j < 16; ++j) v[h][j] += bias[h][(j >> 1) & 1];
             }
             if constexpr (!GATED) {
-                activate_all<16>(a.act, v[0]);
-                activate_all<16>(a.act, v[1]);
+                activate_all<16, true>(a.act, v[0]);
+                activate_all<16, true>(a.act, v[1]);
             } else {
                 // gate rows hand over their last 16 tokens and up rows their first 16, through two buffers in turn
                 // (the barrier of the exchange in between tells that a buffer has been read)
@@ -705,7 +705,7 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
                 float g[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) g[j] = up ? ex[j * 32] : v[j >> 3][j & 7];
-                activate_all<16>(a.act, g);
+                activate_all<16, true>(a.act, g);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j >> 3][j & 7] = g[j] * (up ? v[j >> 3][8 + (j & 7)] : ex[(16 + j) * 32]);
             }
