@@ -44,7 +44,8 @@ EXPORTED = ("gdn_prefill", "gdn_decode_step", "gdn_prefill_workspace_bytes", "gd
             "gdn_decode_gated", "gdn_decode_block_workspace_bytes", "gdn_decode_block", "gdn_rmsnorm_gated",
             "gdn_prefill_gated", "gdn_prefill_segments", "gdn_decode_block_noalloc",
             "gdn_set_wait_limit_ns", "gdn_test_stall_prefill", "gdn_prefill_ws", "gdn_prefill_segment_starts",
-            "gdn_rmsnorm_residual", "gdn_linear", "gdn_linear_ws", "gdn_linear_workspace_bytes")
+            "gdn_rmsnorm_residual", "gdn_linear", "gdn_linear_ws", "gdn_linear_workspace_bytes",
+            "gdn_linear_plan")
 
 
 class GdnDims(ctypes.Structure):
@@ -67,6 +68,10 @@ class GdnBlockDims(ctypes.Structure):
 class GdnLinearDims(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class GdnLinearPlanInfo(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("operands", ctypes.c_int32), ("tokens", ctypes.c_int32), ("splits", ctypes.c_int32)]
 
 
 class GdnError(RuntimeError):
@@ -140,6 +145,8 @@ def lib() -> ctypes.CDLL:
         L.gdn_linear_ws.argtypes = L.gdn_linear.argtypes[:-1] + [vp, ctypes.c_size_t, vp]
         L.gdn_linear_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_linear_workspace_bytes.argtypes = [vp, vp, ctypes.POINTER(GdnLinearDims)]
+        L.gdn_linear_plan.restype = ctypes.c_int
+        L.gdn_linear_plan.argtypes = [vp, vp, ctypes.POINTER(GdnLinearDims), ctypes.c_int32, ctypes.POINTER(GdnLinearPlanInfo)]
         _lib = L
     return _lib
 
@@ -716,3 +723,25 @@ def linear_gated(x, weight, bias=None, residual=None, *, activation="silu", weig
     ``weight_scale``) of 2 N columns, the gate's N first (``GDN_LINEAR_GATED``).  Returns ``out`` [..., N]."""
     return _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weight_scale, out, out_dtype,
                    force_ffma, stream, GDN_LINEAR_GATED)
+
+
+LINEAR_KERNELS = ("none", "few", "ffma", "small", "pairs", "joint")
+LINEAR_OPERANDS = ("as they lie", "copied", "in parts")
+
+
+def linear_plan(M, N, K, dtype=GDN_BF16, out_dtype=None, *, weight_layout="kn", gated=False, force_ffma=False, x_offset=0,
+                weight_offset=0, sm_count=None):
+    """``gdn_linear_plan``: ``(kernel, operands, tokens, splits)`` of a call with these sizes and operands ``x_offset`` and
+    ``weight_offset`` bytes past 16-byte boundaries, on a device with ``sm_count`` SMs (default: the current CUDA
+    device's).  kernel is one of LINEAR_KERNELS, operands of LINEAR_OPERANDS; host only."""
+    if sm_count is None:
+        sm_count = _torch().cuda.get_device_properties(_torch().cuda.current_device()).multi_processor_count
+    if weight_layout not in ("kn", "nk"):
+        raise ValueError("weight_layout must be 'kn' or 'nk'")
+    flags = ((GDN_LINEAR_WEIGHT_NK if weight_layout == "nk" else 0) | (GDN_LINEAR_GATED if gated else 0)
+             | (GDN_LINEAR_FORCE_FFMA if force_ffma else 0))
+    if out_dtype is None:
+        out_dtype = GDN_F32 if dtype == GDN_F32 else GDN_BF16
+    d, info = GdnLinearDims(M, N, K, dtype, out_dtype, GDN_ACT_NONE, flags), GdnLinearPlanInfo()
+    _check(lib().gdn_linear_plan(4096 + x_offset, 4096 + weight_offset, ctypes.byref(d), int(sm_count), ctypes.byref(info)))
+    return LINEAR_KERNELS[info.kernel], LINEAR_OPERANDS[info.operands], info.tokens, info.splits

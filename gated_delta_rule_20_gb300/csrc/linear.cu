@@ -307,12 +307,14 @@ cudaError_t launch_layout(const LinearArgs& a, int splits, const LinearMarks& ma
     return vec ? launch_tile<T, TM, true, true>(a, splits, marks, s) : launch_tile<T, TM, true, false>(a, splits, marks, s);
 }
 
+// Few rows: a kernel that reads the weight once for every 4.  It and the tiles of launch_ffma, us: fp32 K = N = 2048 M = 12
+// 13.9 and 18.8, M = 16 13.8 and 18.9 but K = 4097, N = 2001 51 and 38; e4m3 K = 4097, N = 2001 M = 8 50 and 50, M = 12
+// 57 and 50.
+bool few_rows(const LinearArgs& a, int32_t dtype) { return a.M <= (dtype == GDN_F8E4M3 ? 8 : 12); }
+
 template <typename T>
 cudaError_t launch_ffma(const LinearArgs& a, int32_t dtype, int sms, const LinearMarks& marks, cudaStream_t s) {
-    // Few rows: a kernel that reads the weight once for every 4.  It and the tiles below, us: fp32 K = N = 2048 M = 12
-    // 13.9 and 18.8, M = 16 13.8 and 18.9 but K = 4097, N = 2001 51 and 38; e4m3 K = 4097, N = 2001 M = 8 50 and 50, M = 12
-    // 57 and 50.
-    if (a.M <= (dtype == GDN_F8E4M3 ? 8 : 12) && !marks.tops) return launch_linear_few(a, dtype, sms, s);
+    if (few_rows(a, dtype) && !marks.tops) return launch_linear_few(a, dtype, sms, s);
     const long long wn = a.gated ? 2LL * a.N : a.N;
     auto tiles = [&](int t) { return ((a.M + (long long)t - 1) / t) * ((wn + t - 1) / t); };
     if (tiles(128) >= sms) return launch_layout<T, 8>(a, 1, marks, s);
@@ -377,6 +379,26 @@ LinearPlan plan_of(const LinearArgs& a, const gdn_linear_dims* d) {
 extern "C" size_t gdn_linear_workspace_bytes(const void* x, const void* weight, const gdn_linear_dims* d) {
     if (check_dims(d) != GDN_OK || d->M == 0) return 0;
     return plan_of(args_of(x, nullptr, weight, nullptr, nullptr, nullptr, nullptr, d), d).scratch;
+}
+
+extern "C" gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_dims* d, int32_t sm_count,
+                                      gdn_linear_plan_info* info) {
+    const gdn_status st = check_dims(d);
+    if (st != GDN_OK) return st;
+    if (!info) return GDN_ERR_NULL;
+    if (sm_count < 1) return GDN_ERR_DIMS;
+    *info = gdn_linear_plan_info{GDN_LINEAR_KERNEL_NONE, GDN_LINEAR_OPERANDS_AS_THEY_LIE, 0, 0};
+    if (d->M == 0) return GDN_OK;
+    const LinearArgs a = args_of(x, nullptr, weight, nullptr, nullptr, nullptr, nullptr, d);
+    const LinearPlan how = plan_of(a, d);
+    if (how.route == LinearRoute::kFfma) {
+        info->kernel = few_rows(a, d->dtype) ? GDN_LINEAR_KERNEL_FEW : GDN_LINEAR_KERNEL_FFMA;
+        return GDN_OK;
+    }
+    if (how.route == LinearRoute::kCopies) info->operands = GDN_LINEAR_OPERANDS_COPIED;
+    if (how.route == LinearRoute::kParts) info->operands = GDN_LINEAR_OPERANDS_IN_PARTS;
+    linear_tc_tiles(a, d->dtype, how.route, sm_count, info);
+    return GDN_OK;
 }
 
 extern "C" gdn_status gdn_linear_ws(const void* x, const float* x_scale, const void* weight, const float* weight_scale,

@@ -33,6 +33,8 @@ struct LinearPlan {
     size_t scratch;
 };
 LinearPlan plan_linear(const LinearArgs& a, int32_t dtype);
+// The tensor-core kernel of such a product, its token tile and its splits of K on a device of `sms` SMs.
+void linear_tc_tiles(const LinearArgs& a, int32_t dtype, LinearRoute route, int sms, gdn_linear_plan_info* info);
 
 // What fp32 operands by parts are found to be on the device: of `count` blocks, the exponents (biased, as in the number's
 // bits; 255 for infinities and NaN, 0 where all is zero) of the largest elements that they met of x, and behind those of

@@ -1193,10 +1193,11 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
     const int parts = accs > 1 ? 3 : 1, products = accs > 1 ? 6 : 1;  // stages and products of a slab
     const double weight_mb = tiles1 * slabs * parts * (16.0 / 1024);
+    const int pairs = sms > 1 ? sms / 2 : 1;
     Plan best{true, 256, 1};
     double least = 1e30;
     for (int bn = accs > 1 ? 512 / accs / 32 * 32 : 256; bn >= 64; bn -= 32) {  // (TMEM: 512 columns)
-        const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + sms / 2 - 1) / (sms / 2);
+        const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + pairs - 1) / pairs;
         const double mma = products * bn * (0.28 / 256), in = parts * (accs > 1 ? (16 + bn / 16) / 105.0 : 0.19);
         double t = bn / 300.0 + (double)turns * slabs * (mma > in ? mma : in);
         if (accs > 1) t += (turns - 1) * accs * bn / 200.0;  // epilogues that nothing runs beside
@@ -1217,8 +1218,10 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
         for (int S = 1; S <= 8 && S * 2 <= (slabs > 2 ? slabs : 2); S *= 2) {
             const long long ctas = tiles1 * tiles_m * S;
             const int beside = accs > 1 ? 1 : 2;
-            // CTAs at once: clusters stay inside one of 8 groups of SMs (of 16 to 20: two clusters of 8 do not fit in each)
+            // CTAs at once: clusters stay inside one of 8 groups of SMs (of 16 to 20: two clusters of 8 do not fit in each).
+            // (Fewer than 48 SMs have no room for clusters of 8 CTAs, and by parts fewer than 96.)
             const long long room = 8LL * ((sms / 8 * beside - (S == 8 ? 4 : 0)) / S) * S;
+            if (room <= 0) continue;
             const long long waves = (ctas + room - 1) / room;
             const long long an_sm = ctas <= sms ? 1 : waves * beside;  // CTAs one after another, or beside one another
             const double kb = (double)an_sm * ((slabs + S - 1) / S) * parts * (16 + bn / 8.0);
@@ -1317,7 +1320,7 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
                      (a.res && !encode(&tr, false, a.res, a.M, a.N, a.N, tokens))))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + fixed;
-    const int tiles = t.tiles_n * t.tiles_m, pairs = tiles < sms / 2 ? tiles : sms / 2;
+    const int tiles = t.tiles_n * t.tiles_m, most = sms > 1 ? sms / 2 : 1, pairs = tiles < most ? tiles : most;
     const cudaError_t e = f8              ? launch_large<true, false, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
                           : op.accs == 1 ? (a.nk ? launch_large<false, false, false>(t, tw, tx, to, tr, pairs, smem, dev, s)
                                                  : launch_large<false, true, false>(t, tw, tx, to, tr, pairs, smem, dev, s))
@@ -1484,8 +1487,18 @@ bool takes(const void* p, long long cols, int size) {
     return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && cols * size % 16 == 0;
 }
 
+int slabs_of(int K, bool f8) { return (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
+
+// The accumulators of a tile by parts: one for the small products and, for the x1 w1, one for every `share` slabs (704
+// of K, more where that would be more than three).
+int accs_of(int slabs, int* share) {
+    const int wanted = (slabs + 10) / 11 < kMaxAccs - 1 ? (slabs + 10) / 11 : kMaxAccs - 1;
+    *share = (slabs + wanted - 1) / wanted;
+    return 1 + (slabs + *share - 1) / *share;
+}
+
 gdn_status run_tc(const LinearArgs& a, const Operands& op, bool f8, int dev, int sms, cudaStream_t s) {
-    const Plan how = plan(a, (a.K + (f8 ? 127 : 63)) / (f8 ? 128 : 64), op.accs, sms);
+    const Plan how = plan(a, slabs_of(a.K, f8), op.accs, sms);
     if (how.large && how.splits > 1) return run_joint(a, op, f8, how, dev, s);
     return how.large ? run_large(a, op, f8, how, dev, sms, s) : run_small(a, op, f8, how, dev, s);
 }
@@ -1569,10 +1582,9 @@ gdn_status run_parts(const LinearArgs& a, uint8_t* scratch, int dev, int sms, cu
     Operands op{x.dst, w.dst, x.pitch, w.pitch, halves ? w.up + a.N : a.gated ? 2LL * a.N : a.N, halves ? (int)w.up : a.N};
     op.tops = tops;
     op.marks = kSplitBlocks;
-    // the x1 w1 terms: an accumulator for every 704 of K, three at the most
-    const int slabs = (a.K + 63) / 64, wanted = (slabs + 10) / 11 < kMaxAccs - 1 ? (slabs + 10) / 11 : kMaxAccs - 1;
-    const int share = (slabs + wanted - 1) / wanted;
-    op.accs = 1 + (slabs + share - 1) / share;
+    const int slabs = slabs_of(a.K, false);
+    int share = 0;
+    op.accs = accs_of(slabs, &share);
     for (int q = 1; q < op.accs; ++q) op.starts[q] = (q - 1) * share;
     op.plane = 64 * slabs;
     return run_tc(a, op, false, dev, sms, s);
@@ -1601,6 +1613,15 @@ LinearPlan plan_linear(const LinearArgs& a, int32_t dtype) {
     // (bf16) 100 us and 2.6 ms.
     if (ops < 1e9) return LinearPlan{LinearRoute::kFfma, 0};
     return LinearPlan{LinearRoute::kCopies, job_bytes(x, size) + job_bytes(w, size)};
+}
+
+void linear_tc_tiles(const LinearArgs& a, int32_t dtype, LinearRoute route, int sms, gdn_linear_plan_info* info) {
+    const int slabs = slabs_of(a.K, dtype == GDN_F8E4M3);
+    int share = 0;
+    const Plan how = plan(a, slabs, route == LinearRoute::kParts ? accs_of(slabs, &share) : 1, sms);
+    info->kernel = !how.large ? GDN_LINEAR_KERNEL_SMALL : how.splits > 1 ? GDN_LINEAR_KERNEL_JOINT : GDN_LINEAR_KERNEL_PAIRS;
+    info->tokens = how.bn;
+    info->splits = how.splits;
 }
 
 gdn_status launch_linear_tc(const LinearArgs& a, int32_t dtype, LinearRoute route, void* scratch, int dev, int sms,

@@ -451,6 +451,29 @@ gdn_status gdn_linear_ws(const void* x, const float* x_scale, const void* weight
                          const float* bias, const void* residual, void* out, const gdn_linear_dims* dims,
                          void* workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/* How gdn_linear runs a call. */
+typedef enum {
+    GDN_LINEAR_KERNEL_NONE = 0,   /* M = 0 */
+    GDN_LINEAR_KERNEL_FEW = 1,    /* FMA units, few rows */
+    GDN_LINEAR_KERNEL_FFMA = 2,   /* FMA units */
+    GDN_LINEAR_KERNEL_SMALL = 3,  /* tensor cores, a CTA a tile of 128 weight columns, K over `splits` of them */
+    GDN_LINEAR_KERNEL_PAIRS = 4,  /* tensor cores, a CTA pair a tile of 256 weight columns */
+    GDN_LINEAR_KERNEL_JOINT = 5   /* the same with K over `splits` pairs */
+} gdn_linear_kernel;
+enum { GDN_LINEAR_OPERANDS_AS_THEY_LIE = 0, GDN_LINEAR_OPERANDS_COPIED = 1, GDN_LINEAR_OPERANDS_IN_PARTS = 2 };
+typedef struct {
+    int32_t kernel;    /* gdn_linear_kernel */
+    int32_t operands;  /* GDN_LINEAR_OPERANDS_* (in parts: the FFMA kernel where the operands turn out not to fit) */
+    int32_t tokens;    /* rows of x in a tile, and the CTAs or pairs that share K; tensor-core kernels only, else 0 */
+    int32_t splits;
+} gdn_linear_plan_info;
+
+/* gdn_linear_plan -- how a gdn_linear call with these operands (only their alignment matters)
+ * and dims runs on a device with sm_count SMs; invalid dims return gdn_linear's code for
+ * them, sm_count < 1 GDN_ERR_DIMS.  Host only. */
+gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_dims* dims, int32_t sm_count,
+                           gdn_linear_plan_info* info);
+
 /* Device scratch a prefill with these dims needs on the current device: the
  * segment states, maps and identity-start outputs of a split (see gdn_prefill;
  * the split depends on the device's SM count), 0 when the call runs one pass.  0 as well for
