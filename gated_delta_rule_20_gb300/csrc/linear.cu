@@ -429,6 +429,7 @@ extern "C" gdn_status gdn_linear_ws(const void* x, const float* x_scale, const v
         if (e != cudaSuccess) st = GDN_ERR_CUDA;
     }
     if (own && cudaFreeAsync(own, s) != cudaSuccess && st == GDN_OK) st = GDN_ERR_CUDA;
+    if (st == GDN_ERR_CUDA) (void)cudaGetLastError();  // reported here, and not by the thread's next call again
     return st;
 }
 

@@ -1148,6 +1148,17 @@ cudaError_t launch(void (*kernel)(P...), std::atomic<bool> (&done)[kMaxDevices],
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// A launch of 256 threads a CTA behind everything before it.  (Its own result: cudaGetLastError would also report an
+// earlier error of the calling thread.)
+template <typename... P, typename... Q>
+cudaError_t launch_plain(void (*kernel)(P...), unsigned grid, cudaStream_t s, const Q&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Where TMA finds x and the weight: the caller's arrays, or copies of them with rows of whole 16-byte
 // pieces.  Pitches in elements; up: the weight column where a gated weight's up half starts.
 struct Operands {
@@ -1562,11 +1573,9 @@ gdn_status run_copies(const LinearArgs& a, bool f8, uint8_t* scratch, int dev, i
             op.w_cols = w.up + a.N;
         }
     }
-    if (f8)
-        linear_align_kernel<uint8_t><<<8 * sms, 256, 0, s>>>(x, w);
-    else
-        linear_align_kernel<uint16_t><<<8 * sms, 256, 0, s>>>(x, w);
-    return cudaGetLastError() == cudaSuccess ? run_tc(a, op, f8, dev, sms, s) : GDN_ERR_CUDA;
+    const cudaError_t e = f8 ? launch_plain(linear_align_kernel<uint8_t>, 8u * sms, s, x, w)
+                             : launch_plain(linear_align_kernel<uint16_t>, 8u * sms, s, x, w);
+    return e == cudaSuccess ? run_tc(a, op, f8, dev, sms, s) : GDN_ERR_CUDA;
 }
 
 gdn_status run_parts(const LinearArgs& a, uint8_t* scratch, int dev, int sms, cudaStream_t s, LinearMarks* marks) {
@@ -1576,8 +1585,7 @@ gdn_status run_parts(const LinearArgs& a, uint8_t* scratch, int dev, int sms, cu
     w.dst = reinterpret_cast<__nv_bfloat16*>(scratch + job_bytes(x, false));
     uint8_t* tops = scratch + job_bytes(x, false) + job_bytes(w, !a.nk);
     *marks = LinearMarks{tops, kSplitBlocks};
-    linear_split_kernel<<<kSplitBlocks, 256, 0, s>>>(x, w, tops);
-    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    if (launch_plain(linear_split_kernel, kSplitBlocks, s, x, w, tops) != cudaSuccess) return GDN_ERR_CUDA;
     const bool halves = !a.nk && a.gated;
     Operands op{x.dst, w.dst, x.pitch, w.pitch, halves ? w.up + a.N : a.gated ? 2LL * a.N : a.N, halves ? (int)w.up : a.N};
     op.tops = tops;

@@ -419,5 +419,7 @@ extern "C" gdn_status gdn_rmsnorm_residual(const void* x, const void* residual, 
         e = f8 ? launch_norm<__nv_bfloat16, F8>(a, s) : launch_norm<__nv_bfloat16, __nv_bfloat16>(a, s);
     else
         e = f8 ? launch_norm<float, F8>(a, s) : launch_norm<float, float>(a, s);
-    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    if (e == cudaSuccess) return GDN_OK;
+    (void)cudaGetLastError();  // reported here, and not by the thread's next call again
+    return GDN_ERR_CUDA;
 }

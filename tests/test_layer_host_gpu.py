@@ -47,3 +47,50 @@ def test_rows_of_different_lengths_from_two_threads(gdn, D):
     assert not errors, errors
     for o in out:
         assert (o == 1).all()
+
+
+def _fail_once(call):
+    """Runs ``call(stream)`` on a stream whose capture has been invalidated by a forbidden call: its launch is refused."""
+    rt = ctypes.CDLL("libcudart.so.%s" % torch.version.cuda.split(".")[0])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(ctypes.c_void_p(s.cuda_stream), 0) == 0
+    assert rt.cudaDeviceSynchronize() != 0
+    try:
+        call(s)
+    finally:
+        graph = ctypes.c_void_p()
+        assert rt.cudaStreamEndCapture(ctypes.c_void_p(s.cuda_stream), ctypes.byref(graph)) != 0
+        rt.cudaGetLastError()
+
+
+@pytest.mark.parametrize("failing", ["linear", "linear_parts", "norm"])
+def test_a_failed_call_does_not_fail_the_next(gdn, failing):
+    """A refused launch is that call's error only: the products that lay their operands out anew, the older entry points
+    and the norm work afterwards."""
+    gen = torch.Generator("cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    xf, wf = rand(300, 1024), rand(1024, 1024)
+    xb, wb = rand(700, 1001).bfloat16(), rand(1001, 1001).bfloat16()
+    cx, cw = rand(1, 256, 16).bfloat16(), rand(256, 4)
+    n, nw = rand(4, 256), torch.ones(256, device="cuda")
+    out, outn = torch.empty(300, 1024, device="cuda"), torch.empty_like(n)
+    ws = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    calls = [lambda: gdn.linear(xf, wf), lambda: gdn.linear(xb, wb), lambda: gdn.conv1d_prefill(cx, cw)[0],
+             lambda: gdn.rmsnorm_residual(n, nw)[0]]
+    ref = [c() for c in calls]
+
+    def fail(s):
+        with pytest.raises(gdn.GdnError) as e:
+            if failing == "norm":
+                gdn.rmsnorm_residual(n, nw, out=outn, stream=s)
+            elif failing == "linear":
+                gdn.linear(xf, wf, out=out, force_ffma=True, stream=s)
+            else:
+                d = gdn.GdnLinearDims(300, 1024, 1024, gdn.GDN_F32, gdn.GDN_F32, 0, 0)
+                gdn._binding._check(gdn.lib().gdn_linear_ws(xf.data_ptr(), None, wf.data_ptr(), None, None, None, out.data_ptr(),
+                                                           ctypes.byref(d), ws.data_ptr(), ws.numel(), s.cuda_stream))
+        assert e.value.code == gdn.GDN_ERR_CUDA
+    for c, r in zip(calls, ref):
+        _fail_once(fail)
+        assert torch.equal(c(), r)
