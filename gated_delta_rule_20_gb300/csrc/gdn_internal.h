@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cstdint>
 
 #include "gdn.h"
 
@@ -43,6 +44,15 @@ cudaError_t allow_smem(F* kernel, int bytes, std::atomic<bool> (&done)[kMaxDevic
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_relaxed);
     return e;
+}
+
+// Whether two arrays share memory (null: no array), and whether they do without being one array.
+inline bool overlap(const void* p, long long p_bytes, const void* q, long long q_bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a && b && a < b + (uintptr_t)q_bytes && b < a + (uintptr_t)p_bytes;
+}
+inline bool overlap_in_part(const void* p, long long p_bytes, const void* q, long long q_bytes) {
+    return overlap(p, p_bytes, q, q_bytes) && (p != q || p_bytes != q_bytes);
 }
 
 // The argument checks of gdn_prefill, without launching anything.

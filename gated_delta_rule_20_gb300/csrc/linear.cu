@@ -412,6 +412,12 @@ extern "C" gdn_status gdn_linear_ws(const void* x, const float* x_scale, const v
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     LinearPlan how = plan_of(a, d);
     if (workspace && workspace_bytes < how.scratch) return GDN_ERR_WORKSPACE;
+    // An output over an operand would be read after other rows and columns are written.
+    const long long e = d->dtype == GDN_F32 ? 4 : d->dtype == GDN_BF16 ? 2 : 1, wn = a.gated ? 2 * d->N : d->N;
+    const long long out_bytes = d->M * d->N * (a.out_f32 ? 4 : 2);
+    if (overlap(out, out_bytes, x, d->M * d->K * e) || overlap(out, out_bytes, weight, wn * d->K * e) ||
+        overlap_in_part(out, out_bytes, residual, out_bytes))
+        return GDN_ERR_UNSUPPORTED;
     int dev = 0, sms = 0;
     if (current_device_sms(&dev, &sms) != GDN_OK) return GDN_ERR_CUDA;
     void* own = nullptr;

@@ -412,6 +412,12 @@ extern "C" gdn_status gdn_rmsnorm_residual(const void* x, const void* residual, 
           reinterpret_cast<uintptr_t>(residual_out) | (f8 ? 0 : reinterpret_cast<uintptr_t>(out))) & (esz - 1)) ||
         ((reinterpret_cast<uintptr_t>(norm_weight) | (f8 ? reinterpret_cast<uintptr_t>(out_scale) : 0)) & 3u))
         return GDN_ERR_ALIGN;
+    // in place: element by element, or not at all
+    const long long in_bytes = rows * D * (long long)esz, out_bytes = f8 ? rows * D : in_bytes;
+    if (overlap(out, out_bytes, residual_out, in_bytes) || overlap_in_part(out, out_bytes, x, in_bytes) ||
+        overlap_in_part(out, out_bytes, residual, in_bytes) || overlap_in_part(residual_out, in_bytes, x, in_bytes) ||
+        overlap_in_part(residual_out, in_bytes, residual, in_bytes))
+        return GDN_ERR_UNSUPPORTED;
     const NormArgs a{x, residual, norm_weight, residual_out, out, out_scale, rows, (int)D, eps};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;

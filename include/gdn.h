@@ -367,7 +367,8 @@ gdn_status gdn_prefill_gated(const void* q, const void* k, const void* v, const 
  * The squares are summed in fp32: a row whose sum passes its range (|h| of 1e19 and more) comes out as
  * zeros, and with eps = 0 one whose sum is zero (|h| of 1e-23 and less) as infinities or NaN.
  * rows in [0, 2^31), 1 <= D <= GDN_NORM_MAX_D; pointers aligned to their element;
- * residual_out and out may not be the same buffer (GDN_ERR_UNSUPPORTED).
+ * residual_out and out may not share memory, nor with x or residual other than as whole arrays in
+ * their place (an 8-bit out not at all): GDN_ERR_UNSUPPORTED.
  * With every pointer 16-byte aligned (and D <= 16384 in bf16, 8192 in fp32; a little less
  * where rows are not whole 16-byte pieces) the accesses are of 128 bits.  One launch on `stream`.
  */
@@ -415,7 +416,8 @@ typedef struct {
  *                GDN_F8E4M3 takes GDN_LINEAR_WEIGHT_NK only (else GDN_ERR_UNSUPPORTED)
  *   bias         [N'] fp32, or NULL
  *   residual     [M, N] in out_dtype, or NULL; may be out (in place)
- *   out          [M, N] in out_dtype
+ *   out          [M, N] in out_dtype; may not share memory with x, the weight or, other than in
+ *                its place, the residual (GDN_ERR_UNSUPPORTED)
  * Pointers aligned to their element.  bf16 and e4m3 run on the tensor cores, in one launch on
  * `stream`, where x and the weight are 16-byte aligned with rows of a multiple of 16 bytes (a
  * gated [K, 2 N] weight: also N).  An operand that is not is copied to such rows first (one more
