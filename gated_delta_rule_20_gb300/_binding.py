@@ -698,7 +698,10 @@ def _linear(x, weight, bias, residual, activation, weight_layout, x_scale, weigh
         # operands that are laid out anew: the scratch comes from torch, which keeps it between calls
         need = _lib.gdn_linear_workspace_bytes(xp, wp, dims)
         if need:
-            ws = _layer_empty((need,), _T.uint8, device, stream)
+            try:
+                ws = _layer_empty((need,), _T.uint8, device, stream)
+            except _T.OutOfMemoryError:
+                pass  # the library asks for its own, and does without where there is none
     if ws is None:
         _layer_call(_lib.gdn_linear, device, stream, xp, xsp, wp, wsp, bp, rp, op, dims)
     else:

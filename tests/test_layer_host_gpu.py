@@ -94,3 +94,25 @@ def test_a_failed_call_does_not_fail_the_next(gdn, failing):
     for c, r in zip(calls, ref):
         _fail_once(fail)
         assert torch.equal(c(), r)
+
+
+def test_products_without_memory_for_scratch(gdn):
+    """Operands that are laid out anew where torch has no memory for it: the call still gives its result."""
+    gen = torch.Generator("cuda").manual_seed(1)
+    x, w = (torch.randn(n, 2048, generator=gen, device="cuda") for n in (4096, 2048))
+    xb, wb = x.view(-1)[:4001 * 2047].view(4001, 2047).bfloat16(), w.view(-1)[:2047 * 2048].view(2047, 2048).bfloat16()
+    ref, refb = gdn.linear(x, w, weight_layout="nk"), gdn.linear(xb, wb)
+    out, outb = torch.zeros_like(ref), torch.zeros_like(refb)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    held = torch.cuda.memory_reserved()
+    torch.cuda.set_per_process_memory_fraction((held + (1 << 20)) / torch.cuda.get_device_properties(0).total_memory)
+    try:
+        with pytest.raises(torch.OutOfMemoryError):
+            torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+        gdn.linear(x, w, weight_layout="nk", out=out)
+        gdn.linear(xb, wb, out=outb)
+        torch.cuda.synchronize()
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert torch.equal(out, ref) and torch.equal(outb, refb)
