@@ -96,23 +96,21 @@ def test_a_failed_call_does_not_fail_the_next(gdn, failing):
         assert torch.equal(c(), r)
 
 
-def test_products_without_memory_for_scratch(gdn):
+def test_products_without_memory_for_scratch(gdn, monkeypatch):
     """Operands that are laid out anew where torch has no memory for it: the call still gives its result."""
     gen = torch.Generator("cuda").manual_seed(1)
     x, w = (torch.randn(n, 2048, generator=gen, device="cuda") for n in (4096, 2048))
     xb, wb = x.view(-1)[:4001 * 2047].view(4001, 2047).bfloat16(), w.view(-1)[:2047 * 2048].view(2047, 2048).bfloat16()
-    ref, refb = gdn.linear(x, w, weight_layout="nk"), gdn.linear(xb, wb)
-    out, outb = torch.zeros_like(ref), torch.zeros_like(refb)
-    torch.cuda.synchronize()
-    torch.cuda.empty_cache()
-    held = torch.cuda.memory_reserved()
-    torch.cuda.set_per_process_memory_fraction((held + (1 << 20)) / torch.cuda.get_device_properties(0).total_memory)
-    try:
-        with pytest.raises(torch.OutOfMemoryError):
-            torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
-        gdn.linear(x, w, weight_layout="nk", out=out)
-        gdn.linear(xb, wb, out=outb)
-        torch.cuda.synchronize()
-    finally:
-        torch.cuda.set_per_process_memory_fraction(1.0)
-    assert torch.equal(out, ref) and torch.equal(outb, refb)
+    calls = (lambda: gdn.linear(x, w, weight_layout="nk"), lambda: gdn.linear(xb, wb))
+    ref = [c() for c in calls]
+    empty, refused = gdn._binding._layer_empty, []
+
+    def short_of_memory(shape, dtype, device, stream):
+        if dtype is torch.uint8:
+            refused.append(shape)
+            raise torch.OutOfMemoryError("no memory for scratch")
+        return empty(shape, dtype, device, stream)
+    monkeypatch.setattr(gdn._binding, "_layer_empty", short_of_memory)
+    for c, r in zip(calls, ref):
+        assert torch.equal(c(), r)
+    assert len(refused) == 2
