@@ -58,6 +58,7 @@ struct TcArgs {
     int32_t* status;
     int accs, starts[kMaxAccs];     // fp32 by parts: accumulators of a tile, from 1 on each from its first slab (else one)
     int plane;                      // fp32 by parts: elements of K from one part to the next
+    int block, blocks, ring;        // slabs of a block of K, the tile's (small kernel: CTA's) blocks, and their accumulators (see block_of)
     const uint8_t* tops;            // fp32 by parts: see LinearMarks (null otherwise)
     int marks;
 };
@@ -67,6 +68,7 @@ constexpr int kThreads = 64 + 32 * kEpiWarps;   // and a warp for the loads, one
 
 struct SmallBars {
     uint64_t full[kMaxStages], empty[kMaxStages], done;
+    uint64_t acc_full[2], acc_empty[2];  // blocks of K before the last
     uint32_t tmem;
     int abort;
     uint32_t tops[kThreads / 32];  // fp32 by parts: see parts_fit_all
@@ -84,6 +86,46 @@ struct Ring {
         }
     }
 };
+
+// The tensor cores truncate a sum at every step of 16 terms, always towards zero, so that a sum of K bf16 products of both
+// signs is off by about K 1e-9 of the sums' norm (2.1e-6 at K = 2048 and 1.9e-5 at 16384; fp32 sums 4e-7 and 1.5e-6), and sums
+// of one sign by up to 4e-9 K.  bf16 outputs round that away; for fp32 outputs K is worked off in blocks of at most 8 slabs (512
+// in bf16: 5e-7), in two accumulators in turns, and the epilogue warps add every block to the tile's sums, with rounding, while
+// the next one's products run (kernels with BLOCKED).  The sums of a CTA pair's tile are in registers, 96 a thread at the most
+// (192 tokens); those of the small kernel, which has half the registers, in TMEM behind the accumulators.
+constexpr int kBlockSlabs = 8;
+__host__ __device__ inline int block_of(int slabs, bool blocked) {
+    const int blocks = blocked ? (slabs + kBlockSlabs - 1) / kBlockSlabs : 1;
+    return (slabs + blocks - 1) / blocks;
+}
+
+// Adds a block's accumulator to the sums, the first `cols` (32, 64 or 96) columns of it.
+__device__ __forceinline__ void add_block(float (&sum)[3][32], uint32_t acc, int cols) {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        if (j * 32 >= cols) break;
+        float v[32];
+        tmem_ld32(acc + j * 32, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[j][i] += v[i];
+    }
+}
+// The same for 16 columns whose sums lie in TMEM (the first block of a tile: sets them).
+__device__ __forceinline__ void add_block_tmem(uint32_t sums, uint32_t acc, bool first) {
+    float v[2][8], w[2][8];
+    tmem_ld8(acc, v[0]);
+    tmem_ld8(acc + 8, v[1]);
+    if (!first) {
+        tmem_ld8(sums, w[0]);
+        tmem_ld8(sums + 8, w[1]);
+    }
+    tmem_wait_ld();
+    uint32_t out[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) out[j] = __float_as_uint(first ? v[j / 8][j % 8] : v[j / 8][j % 8] + w[j / 8][j % 8]);
+    tmem_st16u(sums, out);
+}
 
 // The accumulator of a tile that slab k goes to (fp32 by parts: its x1 w1; the small products go to accumulator 0).
 __device__ __forceinline__ int acc_at(const TcArgs& t, int k) {
@@ -224,7 +266,8 @@ __device__ __forceinline__ void join_splits(const TcArgs& t, uint32_t part, int 
 }
 
 // PARTS: an fp32 product by bf16 parts (several accumulators a tile, operands that parts may not fit).
-template <bool F8, bool KN, bool PARTS>
+// BLOCKED: several blocks of K (see block_of).
+template <bool F8, bool KN, bool PARTS, bool BLOCKED>
 __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                            const __grid_constant__ CUtensorMap tm_x,
                                                            const __grid_constant__ TcArgs t) {
@@ -247,6 +290,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
         if (lane < stages) {
             mbar_init(&bars->full[lane], 1);
             mbar_init(&bars->empty[lane], 1);
+        } else if (BLOCKED && lane >= 16 && lane < 18) {
+            mbar_init(&bars->acc_full[lane - 16], 1);
+            mbar_init(&bars->acc_empty[lane - 16], kEpiWarps);
         } else if (lane == 30) {
             mbar_init(&bars->done, 1);
             bars->abort = 0;
@@ -293,19 +339,28 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
         for (int i = (loaded > stages ? loaded - stages : 0); i < loaded; ++i)
             (void)mbar_wait(&bars->full[i % stages], (i / stages) & 1);
     } else if (warp == 1 && run) {  // MMA issuer
-        int issued = 0;
+        int issued = 0, block = 0, in = 0;  // the block of K, and the slab in it
         Ring at;
         AccWalk<PARTS> acc(t, k_lo);
         for (int i = 0; i < k_hi - k_lo; ++i, at.next(stages)) {
             int s[kSlabStages];
+            if (BLOCKED && in == t.block) {
+                if (++block >= 2 && !mbar_wait_warp(&bars->acc_empty[block & 1], ((block - 2) >> 1) & 1, abort_flag)) break;
+                in = 0;
+            }
             if (!wait_slab<PARTS>(bars->full, at, stages, s, abort_flag)) break;
             tc_fence_after();
-            const bool main = acc.step(t, k_lo + i) || i == 0;
+            const bool main = acc.step(t, k_lo + i) || (BLOCKED ? in : i) == 0;
             if (elect_one()) {
-                mma_stages<F8, KN, PARTS, false>(t, tmem, smem_u32(sm), s, bars->empty, acc.q, i == 0, main);
-                if (i + 1 == k_hi - k_lo) mma_commit(&bars->done);
+                mma_stages<F8, KN, PARTS, false>(t, BLOCKED ? tmem + (block & 1) * t.bn : tmem, smem_u32(sm), s, bars->empty,
+                                                 acc.q, i == 0, main);
+                if (i + 1 == k_hi - k_lo)
+                    mma_commit(&bars->done);
+                else if (BLOCKED && in + 1 == t.block)
+                    mma_commit(&bars->acc_full[block & 1]);
             }
             __syncwarp();
+            ++in;
             issued = (i + 1) * kSlabStages;
         }
         if (issued < (k_hi - k_lo) * kSlabStages && issued > 0)  // gave up: what was issued ends first (bounded)
@@ -318,11 +373,23 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     const int e = tid - 64;  // epilogue thread
     bool ok = false;
     if (warp >= 2 && run) {
-        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->done, 0, abort_flag));  // one answer a warp
+        const int row = (warp & 3) * 32 + lane, blocks = BLOCKED ? (k_hi - k_lo + t.block - 1) / t.block : 1;
+        const uint32_t base = tmem + ((uint32_t)(row & ~31) << 16), sums = base + 2 * t.bn;
+        ok = true;
+        for (int q = 0; BLOCKED && q + 1 < blocks; ++q) {  // the blocks of K before the last
+            ok = mbar_wait_warp(&bars->acc_full[q & 1], (q >> 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            for (int c0 = (warp - 2) / 4 * 16; c0 < cols; c0 += 32) add_block_tmem(sums + c0, base + (q & 1) * t.bn + c0, q == 0);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && q + 2 < blocks) mbar_arrive(&bars->acc_empty[q & 1]);
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->done, 0, abort_flag)) && ok;  // one answer a warp
         tc_fence_after();
         if (ok) {
-            const int row = (warp & 3) * 32 + lane;
-            const uint32_t lanes = tmem + ((uint32_t)(row & ~31) << 16);
+            const uint32_t lanes = BLOCKED ? base + ((blocks - 1) & 1) * t.bn : base;
             for (int c0 = (warp - 2) / 4 * 16; c0 < cols; c0 += 32) {  // (columns come in 16s: t.bn)
                 float v[2][8];
                 tmem_ld8(lanes + c0, v[0]);
@@ -341,6 +408,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = sum[j];
+                } else if (BLOCKED && blocks > 1) {
+                    float w[2][8];
+                    tmem_ld8(sums + c0, w[0]);
+                    tmem_ld8(sums + c0 + 8, w[1]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j / 8][j % 8] += w[j / 8][j % 8];
                 }
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -374,12 +448,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
 
 // ------------------------------------------------------------------ many tokens
 constexpr int kLargeStages = 10;
+constexpr int kMaxRing = 4;                        // accumulators of a CTA pair (two, unless BLOCKED)
 constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 directions x 16 values x 32 lanes
 constexpr uint32_t kBoxRow = 128;                  // a staged output row: 64 bf16 columns
 
 struct LargeBars {
     uint64_t full[kLargeStages], empty[kLargeStages];  // full: the leader's are used
-    uint64_t acc_full[2], acc_empty[2];                // acc_empty: the leader's are used
+    uint64_t acc_full[kMaxRing], acc_empty[kMaxRing];  // acc_empty: the leader's are used
     uint64_t res_full[kEpiWarps / 2];                  // staged residual boxes
     uint32_t tmem;
     int abort;
@@ -405,8 +480,8 @@ __device__ __forceinline__ void tile_at(const TcArgs& t, int i, int* n, int* m) 
     *n = g * t.group + in - *m * width;
 }
 
-// Tiles take the two accumulators in turns; fp32 by parts takes all of TMEM for every tile.  The (first)
-// accumulator of a turn, and how many tiles have had it before.
+// A pair's turns: its tiles, or their blocks of K.  They take the two accumulators alternately; fp32 by parts takes all of
+// TMEM for every tile.  The (first) accumulator of a turn, and how many turns have had it before.
 template <bool PARTS>
 __device__ __forceinline__ int acc_of(int turn) { return PARTS ? 0 : turn & 1; }
 template <bool PARTS>
@@ -485,7 +560,32 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const
 // The epilogue warps of linear_large_kernel, for any output: every tile of the pair, 32 tokens at a time.  The first
 // residual values of a tile are loaded before its products are done, the next chunk's before this
 // one's are used.
-template <bool GATED, bool PARTS>
+// A tile's blocks of K added up, from the accumulator `at` of the ring on; the sums are left in the last block's, from where
+// they are finished as those of other tiles.  left: blocks of this and later tiles of the pair.  (Not inlined: the 96 sums
+// leave no registers for what the epilogue has there, which went to local memory at every block.)
+__device__ __noinline__ bool add_blocks(LargeBars* bars, uint32_t base, int bn, int ring, int cols, Ring at, int blocks, int left) {
+    float sum[3][32];
+#pragma unroll
+    for (int j = 0; j < 96; ++j) sum[j / 32][j % 32] = 0.f;
+    for (int q = 0;; ++q) {
+        if (!mbar_wait_warp(&bars->acc_full[at.s], at.phase, &bars->abort)) return false;
+        tc_fence_after();
+        add_block(sum, base + at.s * bn, cols);
+        if (q + 1 == blocks) break;
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0 && q + ring < left) mbar_arrive_cluster(map_to_rank(smem_u32(&bars->acc_empty[at.s]), 0));
+        at.next(ring);
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+        if (j * 32 < cols) tmem_st32(base + at.s * bn + j * 32, sum[j]);
+    tmem_wait_st();
+    return true;
+}
+
+// BLOCKED: tiles of several blocks of K (see block_of).
+template <bool GATED, bool PARTS, bool BLOCKED>
 __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float* swap, uint32_t tmem, int rank, int pair,
                                          int pairs, int tiles) {
     constexpr int C = GATED ? 16 : 32;  // tokens of a chunk that this warp finishes
@@ -503,9 +603,10 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     volatile int* abort_flag = &bars->abort;
     const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
     int turn = 0, flip = 0;
+    const int turns = (tiles - pair + pairs - 1) / pairs;
+    Ring acc_at;  // BLOCKED: of the accumulators
     Tiles walk;
     for (int tile = pair; tile < tiles; tile += pairs, ++turn) {
-        const int b = acc_of<PARTS>(turn);
         int tn, tm;
         walk.get(t, turn, pair, pairs, tiles, &tn, &tm);
         // this thread's weight column and the output that it belongs to
@@ -516,12 +617,20 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
         const float bias = a.bias && live ? a.bias[col] : 0.f;
         const int m_lo = tm * t.bn + c_lo;
         uint32_t res[C];
+        const uint32_t base = tmem + c_lo + ((uint32_t)(quad * 32) << 16);
+        bool ok = true;
+        const int left = (turns - turn) * t.blocks;
+        if constexpr (BLOCKED) {
+            ok = add_blocks(bars, base, t.bn, t.ring, hc, acc_at, t.blocks, left);
+            for (int q = 0; q + 1 < t.blocks; ++q) acc_at.next(t.ring);
+        }
+        const int b = BLOCKED ? acc_at.s : acc_of<PARTS>(turn);
         if (a.res && live) load_residual<C>(a, res, m_lo + own, n);
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], acc_use<PARTS>(turn) & 1, abort_flag));
+        if (!BLOCKED) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], acc_use<PARTS>(turn) & 1, abort_flag));
         // one answer for both warps of a gated pair, which meet at a barrier below
         if (GATED ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
         tc_fence_after();
-        const uint32_t src = tmem + b * t.bn + c_lo + ((uint32_t)(quad * 32) << 16);
+        const uint32_t src = base + b * t.bn;
 #pragma unroll 1
         for (int c = 0; c < hc; c += 32) {
             const int m0 = m_lo + c;
@@ -542,10 +651,12 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
                     for (int j = 0; j < 8; ++j) v[i + j] += w[j];
                 }
             }
-            if (c + 32 >= hc && tile + (PARTS ? 1 : 2) * pairs < tiles) {  // read: a later product may overwrite it
+            // read: a later product may overwrite it
+            if (c + 32 >= hc && (BLOCKED ? t.blocks - 1 + t.ring < left : turn + (PARTS ? 1 : 2) < turns)) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(b ? done1 : done0);
+                if (lane == 0)
+                    mbar_arrive_cluster(BLOCKED ? map_to_rank(smem_u32(&bars->acc_empty[b]), 0) : b ? done1 : done0);
             }
             if (a.x_scale) {
                 const float mine = m0 + lane < a.M ? a.x_scale[m0 + lane] : 0.f;
@@ -572,6 +683,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
                 if (live) finish<16>(a, g, w, r, m0 + own, n);
             }
         }
+        if (BLOCKED) acc_at.next(t.ring);
     }
 }
 
@@ -755,7 +867,7 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
     __syncwarp();
 }
 
-template <bool F8, bool KN, bool PARTS>
+template <bool F8, bool KN, bool PARTS, bool BLOCKED>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_large_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                         const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_res,
@@ -779,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane < stages) {
             mbar_init(&bars->full[lane], 1);
             mbar_init(&bars->empty[lane], 1);
-        } else if (lane >= 16 && lane < 18) {
+        } else if (lane >= 16 && lane < (BLOCKED ? 16 + kMaxRing : 18)) {
             mbar_init(&bars->acc_full[lane - 16], 1);
             mbar_init(&bars->acc_empty[lane - 16], 2 * kEpiWarps);
         } else if (lane >= 20 && lane < 20 + kEpiWarps / 2) {
@@ -843,39 +955,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (rank == 0) {  // MMA issuer of the pair
             int i = 0, turn = 0;
-            Ring at;
+            Ring at, acc_at;  // acc_at: of the accumulators, BLOCKED
             bool live = true;
-            for (int tile = pair; tile < tiles && live; tile += pairs, ++turn) {
-                const int b = acc_of<PARTS>(turn), use = acc_use<PARTS>(turn);
-                if (use >= 1 && !mbar_wait_warp(&bars->acc_empty[b], (use - 1) & 1, abort_flag)) break;
-                tc_fence_after();
+            for (int tile = pair; tile < tiles && live; tile += pairs) {
                 AccWalk<PARTS> acc(t, 0);
+                int b = 0, end = 0;  // the turn's accumulator and the end of its slabs
                 for (int k = 0; k < t.slabs; ++k, i += kSlabStages, at.next(stages)) {
+                    const bool first = BLOCKED ? k == end : k == 0;
+                    if (first) {
+                        const bool used = BLOCKED ? turn >= t.ring : acc_use<PARTS>(turn) >= 1;
+                        const uint32_t phase = BLOCKED ? acc_at.phase : acc_use<PARTS>(turn) & 1;
+                        b = BLOCKED ? acc_at.s : acc_of<PARTS>(turn);
+                        end = BLOCKED ? min(k + t.block, t.slabs) : t.slabs;
+                        ++turn;
+                        if (BLOCKED) acc_at.next(t.ring);
+                        if (used && !mbar_wait_warp(&bars->acc_empty[b], phase ^ 1, abort_flag)) {
+                            live = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
                     int s[kSlabStages];
                     if (!wait_slab<PARTS>(bars->full, at, stages, s, abort_flag)) {
                         live = false;
                         break;
                     }
                     tc_fence_after();
-                    const bool main = acc.step(t, k) || k == 0;
+                    const bool main = acc.step(t, k) || first;
                     if (elect_one()) {
                         mma_stages<F8, KN, PARTS, true>(t, tmem + b * t.bn, smem_u32(sm), s, bars->empty, acc.q, k == 0, main);
-                        if (k + 1 == t.slabs) mma_commit_pair(&bars->acc_full[b]);
+                        if (k + 1 == end) mma_commit_pair(&bars->acc_full[b]);
                     }
                     __syncwarp();
                 }
             }
             if (i > 0) (void)mbar_wait(&bars->empty[(i - 1) % stages], ((i - 1) / stages) & 1);  // all products are done
         }
-    } else if (!PARTS && t.staged) {
+    } else if (!PARTS && !BLOCKED && t.staged) {
         if (a.gated)
             epilogue_staged<true>(t, &tm_out, &tm_res, bars, boxes, swap, tmem, rank, pair, pairs, tiles);
         else
             epilogue_staged<false>(t, &tm_out, &tm_res, bars, boxes, swap, tmem, rank, pair, pairs, tiles);
     } else if (a.gated) {
-        epilogue<true, PARTS>(t, bars, swap, tmem, rank, pair, pairs, tiles);
+        epilogue<true, PARTS, BLOCKED>(t, bars, swap, tmem, rank, pair, pairs, tiles);
     } else {
-        epilogue<false, PARTS>(t, bars, swap, tmem, rank, pair, pairs, tiles);
+        epilogue<false, PARTS, BLOCKED>(t, bars, swap, tmem, rank, pair, pairs, tiles);
     }
     __syncwarp();
     tc_fence_before();
@@ -970,7 +1094,7 @@ __device__ __forceinline__ void finish_chunks(const TcArgs& t, float* swap, uint
     }
 }
 
-template <bool F8, bool KN>
+template <bool F8, bool KN, bool BLOCKED>
 __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_constant__ CUtensorMap tm_w,
                                                                    const __grid_constant__ CUtensorMap tm_x,
                                                                    const __grid_constant__ TcArgs t) {
@@ -992,8 +1116,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
         if (lane < stages) {
             mbar_init(&bars->full[lane], 1);
             mbar_init(&bars->empty[lane], 1);
-        } else if (lane == 16) {
-            mbar_init(&bars->acc_full[0], 1);
+        } else if (lane >= 16 && lane < (BLOCKED ? 18 : 17)) {
+            mbar_init(&bars->acc_full[lane - 16], 1);
+            if (BLOCKED) mbar_init(&bars->acc_empty[lane - 16], 2 * kEpiWarps);
         } else if (lane == 30) {
             bars->abort = 0;
         }
@@ -1013,6 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
     griddep_wait();
 
     bool ok = false;
+    float sum[3][32];  // BLOCKED: of the chunks whose blocks this warp adds
     if (warp == 0) {  // TMA producer: this CTA's columns and its half of the tokens
         const int per = a.gated ? 64 : 128, n0 = (tn * 2 + rank) * per, n1 = a.gated ? t.up + n0 : n0 + 64;
         const int m0 = tm * t.bn + rank * (t.bn / 2);
@@ -1036,20 +1162,51 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
     } else if (warp == 1) {
         if (rank == 0) {  // MMA issuer of the pair
             const uint32_t both = 3u << leader;
-            int i = 0;
+            int i = 0, block = 0, in = 0;  // the block of K, and the slab in it
             Ring at;
             for (; i < k_hi - k_lo; ++i, at.next(stages)) {
+                if (BLOCKED && in == t.block) {
+                    if (++block >= 2 && !mbar_wait_warp(&bars->acc_empty[block & 1], ((block - 2) >> 1) & 1, abort_flag)) break;
+                    in = 0;
+                }
                 if (!mbar_wait_warp(&bars->full[at.s], at.phase, abort_flag)) break;
                 tc_fence_after();
+                const int b = BLOCKED ? block & 1 : 0;
                 if (elect_one()) {
                     const uint32_t st = smem_u32(sm) + at.s * t.stage_bytes;
-                    mma_slab<F8, KN, true>(tmem, st, st, t.idesc, i == 0);
+                    mma_slab<F8, KN, true>(tmem + b * t.bn, st, st, t.idesc, (BLOCKED ? in : i) == 0);
                     mma_commit_pair(&bars->empty[at.s], both);
-                    if (i + 1 == k_hi - k_lo) mma_commit_pair(&bars->acc_full[0], both);
+                    if (i + 1 == k_hi - k_lo || (BLOCKED && in + 1 == t.block)) mma_commit_pair(&bars->acc_full[b], both);
                 }
                 __syncwarp();
+                ++in;
             }
             if (i > 0) (void)mbar_wait(&bars->empty[(i - 1) % stages], ((i - 1) / stages) & 1);  // all products are done
+        }
+    } else if constexpr (BLOCKED) {
+        const int blocks = (k_hi - k_lo + t.block - 1) / t.block;
+        const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), leader);
+        const uint32_t done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), leader);
+        // this warp's chunks `half`, half + 2, half + 4
+        const uint32_t at = tmem + ((warp - 2) >> 2) * 32 + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+        for (int i = 0; i < 96; ++i) sum[i / 32][i % 32] = 0.f;
+        for (int b = 0; b < blocks; ++b) {
+            ok = mbar_wait_warp(&bars->acc_full[b & 1], (b >> 1) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+                if (((warp - 2) >> 2) + 2 * j >= t.bn / 32) break;
+                float v[32];
+                tmem_ld32(at + (b & 1) * t.bn + j * 64, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum[j][i] += v[i];
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && b + 2 < blocks) mbar_arrive_cluster(b & 1 ? done1 : done0);
         }
     } else {
         ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[0], 0, abort_flag));
@@ -1059,19 +1216,35 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
     if (ok) {
         tc_fence_after();
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        for (int c = half; c < t.bn / 32; c += 2) {
-            if (c % S == q) continue;
+#pragma unroll
+        for (int j = 0; j < (BLOCKED ? 3 : 4); ++j) {
+            const int c = half + 2 * j;
+            if (c >= t.bn / 32) break;
+            const uint32_t mine = tmem + c * 32 + ((uint32_t)(quad * 32) << 16);
             float v[32];
-            tmem_ld32(tmem + c * 32 + ((uint32_t)(quad * 32) << 16), v);
-            tmem_wait_ld();
+            if constexpr (BLOCKED) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = sum[j][i];
+                if (c % S == q) {  // finished below, by another warp
+                    tmem_st32(mine, v);
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+            }
+            if (c % S == q) continue;
+            if constexpr (!BLOCKED) {
+                tmem_ld32(mine, v);
+                tmem_wait_ld();
+            }
             const uint32_t to = map_to_rank(smem_u32(sm) + chunk_slot(c, q, S) + (quad * 32 + lane) * 16, 2 * (c % S) + rank);
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) st_cluster_f32x4(to + j / 4 * 2048, v[j], v[j + 1], v[j + 2], v[j + 3]);
+            for (int i = 0; i < 32; i += 4) st_cluster_f32x4(to + i / 4 * 2048, v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
     }
     __syncwarp();
     cluster_sync();  // the partial sums are there
     if (warp >= 2) {
+        if (BLOCKED) tc_fence_after();
         const uint32_t pair_bar = 1 + (warp & 1) + 2 * ((warp - 2) >> 2);
         if (a.gated) ok = !named_bar_any(pair_bar, 64, !ok);  // one answer for the warps that meet at a barrier
         if (ok && a.gated)
@@ -1172,12 +1345,20 @@ struct Operands {
     long long depth(const LinearArgs& a) const { return plane ? 3LL * plane : a.K; }
 };
 
+template <bool F8, bool KN, bool PARTS, bool BLOCKED>
+cudaError_t launch_small_as(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
+                         int dev, cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];
+    return launch(linear_small_kernel<F8, KN, PARTS, BLOCKED>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), kThreads, smem,
+                  t.splits, s, tw, tx, t);
+}
 template <bool F8, bool KN, bool PARTS>
 cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
                          int dev, cudaStream_t s) {
-    static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_small_kernel<F8, KN, PARTS>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), kThreads, smem,
-                  t.splits, s, tw, tx, t);
+    if constexpr (!PARTS) {
+        if (t.blocks > 1) return launch_small_as<F8, KN, false, true>(t, tw, tx, tiles, tiles_m, smem, dev, s);
+    }
+    return launch_small_as<F8, KN, PARTS, false>(t, tw, tx, tiles, tiles_m, smem, dev, s);
 }
 
 // What runs, on tiles of bn tokens: pairs (large), with K over `splits` of them where that is more than one, or
@@ -1200,12 +1381,16 @@ struct Plan {
 //     N = 2048: 28.7 pairs, 20.5 two a tile of 192; M = 384, K = 4096, N = 2048: 13.7 small, 15.8 pairs, 11.6 two a tile
 //     of 128; M = 1024, K = N = 2048: 10.3 pairs, 12.5 two a tile of 256.
 // On 48 shapes (M = 64 .. 1024) the choice is 0.3 % behind the best of all on average; by parts, on 17 shapes, it is it.
+// Blocks of K (see block_of) take tiles of at most 160 tokens, pairs that split K of 192, the small kernel of 64 (two CTAs an SM
+// share TMEM); pairs lose about 2 us and 0.2 a block, where they split K half of that.  M = 64, K = 2048, N = 8192: 13.4 pairs of
+// 64 tokens (10.1 without blocks), 10.9 small; M = 1024, K = 8192, N = 2048: 36.8 pairs, 47 small.
 Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
+    const bool blocked = a.out_f32 && accs == 1;
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
     const int parts = accs > 1 ? 3 : 1, products = accs > 1 ? 6 : 1;  // stages and products of a slab
     const double weight_mb = tiles1 * slabs * parts * (16.0 / 1024);
     const int pairs = sms > 1 ? sms / 2 : 1;
-    Plan best{true, 256, 1};
+    Plan best{true, 64, 1};
     double least = 1e30;
     for (int bn = accs > 1 ? 512 / accs / 32 * 32 : 256; bn >= 64; bn -= 32) {  // (TMEM: 512 columns)
         const long long tiles = tiles2 * ((a.M + bn - 1) / bn), turns = (tiles + pairs - 1) / pairs;
@@ -1213,12 +1398,15 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
         double t = bn / 300.0 + (double)turns * slabs * (mma > in ? mma : in);
         if (accs > 1) t += (turns - 1) * accs * bn / 200.0;  // epilogues that nothing runs beside
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
-        if (t < least) least = t, best = Plan{true, bn, 1};
+        if (blocked && slabs > kBlockSlabs) t += 2.0 + 0.2 * (slabs / kBlockSlabs);
+        if (t < least && !(bn > 160 && blocked && slabs > kBlockSlabs)) least = t, best = Plan{true, bn, 1};
         for (int S = 2; S <= 4 && accs == 1 && 2 * S <= slabs; ++S) {
+            if (bn > 192 && blocked && (slabs + S - 1) / S > kBlockSlabs) continue;
             if (tiles > sms / (2 * S) - 2 * (S - 1)) break;
             t = (slabs + S - 1) / S * (mma > in ? mma : in);
             if (t < weight_mb / 6.3) t = weight_mb / 6.3;
             t += 0.012 * bn + 0.6 * S;
+            if (blocked && (slabs + S - 1) / S > kBlockSlabs) t += 1.0 + 0.1 * (slabs / S / kBlockSlabs);
             if (t < least) least = t, best = Plan{true, bn, S};
         }
     }
@@ -1228,6 +1416,7 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
         if (tiles_m > 65535) continue;  // the grid's limit
         for (int S = 1; S <= 8 && S * 2 <= (slabs > 2 ? slabs : 2); S *= 2) {
             const long long ctas = tiles1 * tiles_m * S;
+            if (blocked && bn > 64 && (slabs + S - 1) / S > kBlockSlabs) continue;
             const int beside = accs > 1 ? 1 : 2;
             // CTAs at once: clusters stay inside one of 8 groups of SMs (of 16 to 20: two clusters of 8 do not fit in each).
             // (Fewer than 48 SMs have no room for clusters of 8 CTAs, and by parts fewer than 96.)
@@ -1260,6 +1449,8 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.slabs = (a.K + elems - 1) / elems;
     t.bn = how.bn;
     t.splits = how.splits;
+    t.block = block_of((t.slabs + t.splits - 1) / t.splits, a.out_f32 && t.accs == 1);
+    t.blocks = ((t.slabs + t.splits - 1) / t.splits + t.block - 1) / t.block;
     const long long tiles = ((long long)a.N + per - 1) / per, tiles_m = (a.M + t.bn - 1) / t.bn;
     if (tiles * t.splits > INT32_MAX || tiles_m > 65535) return GDN_ERR_DIMS;
     t.wide_out = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & (a.out_f32 ? 15u : 7u)) == 0;
@@ -1267,7 +1458,7 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.stages = (int)(((op.plane ? kSmemLimit : 112 * 1024) - sizeof(SmallBars) - 1024) / t.stage_bytes);  // two CTAs an SM
     if (t.stages > kMaxStages) t.stages = kMaxStages;
     t.tmem_cols = 32;
-    while (t.tmem_cols < (uint32_t)(t.accs * t.bn)) t.tmem_cols <<= 1;
+    while (t.tmem_cols < (uint32_t)((t.blocks > 1 ? 3 : t.accs) * t.bn)) t.tmem_cols <<= 1;
     t.idesc = f8 ? make_idesc_e4m3(128, t.bn) : make_idesc_bf16(128, t.bn, a.nk ? 0 : 1, 0);
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
@@ -1285,12 +1476,21 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+template <bool F8, bool KN, bool PARTS, bool BLOCKED>
+cudaError_t launch_large_as(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& to,
+                            const CUtensorMap& tr, int pairs, size_t smem, int dev, cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];
+    return launch(linear_large_kernel<F8, KN, PARTS, BLOCKED>, done, dev, dim3((unsigned)(2 * pairs)), kThreads, smem, 2, s, tw, tx, to,
+                  tr, t);
+}
+
 template <bool F8, bool KN, bool PARTS>
 cudaError_t launch_large(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& to,
                          const CUtensorMap& tr, int pairs, size_t smem, int dev, cudaStream_t s) {
-    static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_large_kernel<F8, KN, PARTS>, done, dev, dim3((unsigned)(2 * pairs)), kThreads, smem, 2, s, tw, tx, to,
-                  tr, t);
+    if constexpr (!PARTS) {
+        if (t.blocks > 1) return launch_large_as<F8, KN, false, true>(t, tw, tx, to, tr, pairs, smem, dev, s);
+    }
+    return launch_large_as<F8, KN, PARTS, false>(t, tw, tx, to, tr, pairs, smem, dev, s);
 }
 
 gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how, int dev, int sms, cudaStream_t s) {
@@ -1306,6 +1506,9 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.slabs = (a.K + elems - 1) / elems;
     t.tiles_n = (int)(((long long)a.N + per - 1) / per);
     t.bn = how.bn;
+    t.block = block_of(t.slabs, a.out_f32 && t.accs == 1);
+    t.blocks = (t.slabs + t.block - 1) / t.block;
+    t.ring = t.blocks == 1 ? 2 : 512 / t.bn < kMaxRing ? 512 / t.bn : kMaxRing;
     t.tiles_m = (a.M + t.bn - 1) / t.bn;
     if ((long long)t.tiles_n * t.tiles_m > INT32_MAX - sms) return GDN_ERR_DIMS;
     t.group = t.tiles_n < 16 ? t.tiles_n : 16;
@@ -1316,7 +1519,7 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
     if (t.stages > kLargeStages) t.stages = kLargeStages;
     t.tmem_cols = 128;
-    while (t.tmem_cols < (uint32_t)((t.accs > 2 ? t.accs : 2) * t.bn)) t.tmem_cols <<= 1;
+    while (t.tmem_cols < (uint32_t)((t.accs > t.ring ? t.accs : t.ring) * t.bn)) t.tmem_cols <<= 1;
     t.idesc = f8 ? make_idesc_e4m3(256, t.bn) : make_idesc_bf16(256, t.bn, a.nk ? 0 : 1, 0);
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
@@ -1340,12 +1543,18 @@ gdn_status run_large(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+template <bool F8, bool KN, bool BLOCKED>
+cudaError_t launch_joint_as(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, size_t smem, int dev,
+                            cudaStream_t s) {
+    static std::atomic<bool> done[kMaxDevices];
+    return launch(linear_joint_kernel<F8, KN, BLOCKED>, done, dev, dim3((unsigned)(tiles * 2 * t.splits)), kThreads, smem,
+                  2 * t.splits, s, tw, tx, t);
+}
 template <bool F8, bool KN>
 cudaError_t launch_joint(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, size_t smem, int dev,
                          cudaStream_t s) {
-    static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_joint_kernel<F8, KN>, done, dev, dim3((unsigned)(tiles * 2 * t.splits)), kThreads, smem, 2 * t.splits, s,
-                  tw, tx, t);
+    return t.blocks > 1 ? launch_joint_as<F8, KN, true>(t, tw, tx, tiles, smem, dev, s)
+                        : launch_joint_as<F8, KN, false>(t, tw, tx, tiles, smem, dev, s);
 }
 
 gdn_status run_joint(const LinearArgs& a, const Operands& op, bool f8, Plan how, int dev, cudaStream_t s) {
@@ -1358,6 +1567,8 @@ gdn_status run_joint(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.tiles_n = (int)(((long long)a.N + per - 1) / per);
     t.bn = how.bn;
     t.splits = how.splits;
+    t.block = block_of((t.slabs + t.splits - 1) / t.splits, a.out_f32);
+    t.blocks = ((t.slabs + t.splits - 1) / t.splits + t.block - 1) / t.block;
     t.tiles_m = (a.M + t.bn - 1) / t.bn;
     t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
     // (the others' sums of a CTA's chunks, 96 KB at the most, fit the stages, 184 KB at the least)
@@ -1365,7 +1576,7 @@ gdn_status run_joint(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
     if (t.stages > kLargeStages) t.stages = kLargeStages;
     t.tmem_cols = 32;
-    while (t.tmem_cols < (uint32_t)t.bn) t.tmem_cols <<= 1;
+    while (t.tmem_cols < (uint32_t)((t.blocks > 1 ? 2 : 1) * t.bn)) t.tmem_cols <<= 1;
     t.idesc = f8 ? make_idesc_e4m3(256, t.bn) : make_idesc_bf16(256, t.bn, a.nk ? 0 : 1, 0);
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;

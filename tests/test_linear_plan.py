@@ -155,3 +155,25 @@ def test_every_variant(L, M, N, K, dtype, layout, gated, kernel, tokens, splits,
     t._run(gdn, M, N, K, dtype, layout, gated, "silu" if full else "none", bias=full, residual=full,
            out=None if full else "f32")
     assert gdn.device_status(0) == 0
+
+
+def test_plans_of_fp32_outputs(L):
+    """Sums of more than 8 slabs a CTA are worked off in blocks, which have smaller tiles: 160 tokens, 192 where pairs split
+    K, 64 in the small kernel; shorter ones have bf16 outputs' plans."""
+    seen = set()
+    for dtype, elems in (("bf16", 64), ("f8", 128)):
+        for M in (1, 17, 64, 130, 300, 768, 2000, 16384):
+            for N in (64, 1000, 2048, 8192):
+                for K in (128, 512, 1024, 2056, 4096, 8192, 16384):
+                    if K % 16:
+                        continue
+                    of = lambda out: gdn.linear_plan(M, N, K, CODES[dtype], out, weight_layout="nk", sm_count=SMS)  # noqa: E731
+                    kernel, _, tokens, splits = of(gdn.GDN_F32)
+                    slabs = -(-K // elems)
+                    share = -(-slabs // splits)
+                    if share > 8:
+                        assert tokens <= {"pairs": 160, "joint": 192, "small": 64}[kernel]
+                        seen.add((dtype, kernel))
+                    if slabs <= 8:
+                        assert of(gdn.GDN_F32) == of(gdn.GDN_BF16)
+    assert seen == {(d, k) for d in ("bf16", "f8") for k in ("small", "pairs", "joint")}
