@@ -44,7 +44,7 @@ constexpr int kSlabBytes = 128;                  // bytes of K a stage
 constexpr uint32_t kWBytes = 128 * kSlabBytes;   // a CTA's 128 weight columns of a slab
 constexpr uint32_t kHalfW = kWBytes / 2;         // one box of 64
 constexpr int kMaxStages = 12;
-constexpr int kMaxAccs = 4;
+constexpr int kMaxAccs = 5;
 
 struct TcArgs {
     LinearArgs a;
@@ -1410,7 +1410,7 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
             if (t < least) least = t, best = Plan{true, bn, S};
         }
     }
-    for (int bn = 16; bn <= (accs > 1 ? 256 / accs : 128); bn *= 2) {  // (two CTAs an SM share TMEM)
+    for (int bn = 16; bn <= (accs > 4 ? 64 : accs > 1 ? 256 / accs : 128); bn *= 2) {  // (two CTAs an SM share TMEM; by parts one)
         if (bn > 16 && bn / 2 >= a.M) break;
         const long long tiles_m = (a.M + bn - 1) / bn;
         if (tiles_m > 65535) continue;  // the grid's limit
@@ -1631,7 +1631,8 @@ __global__ void __launch_bounds__(256) linear_align_kernel(const __grid_constant
 // more are taken, the five small ones (x1 w3, x3 w1, x2 w2, x1 w2, x2 w1) into an accumulator of their own.
 // The tensor cores truncate a sum at every step of 16 terms, always towards zero, so that it falls short by
 // about K 1e-9 of itself (2.1e-6 at K = 2048; fp32 sums with rounding 0.8e-6).  The x1 w1, whose sum that is,
-// therefore go to an accumulator for every 704 of K, three at the most, which are added with rounding.
+// therefore go to an accumulator for every 704 to 1024 of K (see accs_of), which are added with rounding: at K = 4096 sums of
+// one sign are off by 8.3e-7 (fp32 sums 8.4e-7; with three accumulators 1.57e-6).
 constexpr int kParts = 3;
 
 // Splits one operand: rows_in x cols fp32 -> rows_out x width parts, rows `pitch` apart and parts `plane`
@@ -1711,10 +1712,10 @@ bool takes(const void* p, long long cols, int size) {
 
 int slabs_of(int K, bool f8) { return (K + (f8 ? 127 : 63)) / (f8 ? 128 : 64); }
 
-// The accumulators of a tile by parts: one for the small products and, for the x1 w1, one for every `share` slabs (704
-// of K, more where that would be more than three).
+// The accumulators of a tile by parts: one for the small products and, for the x1 w1, one for every `share` slabs: 704 of
+// K, up to 1024 where that would be more than three (and four of them past K = 3072).
 int accs_of(int slabs, int* share) {
-    const int wanted = (slabs + 10) / 11 < kMaxAccs - 1 ? (slabs + 10) / 11 : kMaxAccs - 1;
+    const int wanted = slabs > 48 ? 4 : slabs > 22 ? 3 : (slabs + 10) / 11;
     *share = (slabs + wanted - 1) / wanted;
     return 1 + (slabs + *share - 1) / *share;
 }
