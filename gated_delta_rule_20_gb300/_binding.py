@@ -71,7 +71,8 @@ class GdnLinearDims(ctypes.Structure):
 
 
 class GdnLinearPlanInfo(ctypes.Structure):
-    _fields_ = [("kernel", ctypes.c_int32), ("operands", ctypes.c_int32), ("tokens", ctypes.c_int32), ("splits", ctypes.c_int32)]
+    _fields_ = [("kernel", ctypes.c_int32), ("operands", ctypes.c_int32), ("tokens", ctypes.c_int32),
+                ("splits", ctypes.c_int32)]
 
 
 class GdnError(RuntimeError):
@@ -146,7 +147,8 @@ def lib() -> ctypes.CDLL:
         L.gdn_linear_workspace_bytes.restype = ctypes.c_size_t
         L.gdn_linear_workspace_bytes.argtypes = [vp, vp, ctypes.POINTER(GdnLinearDims)]
         L.gdn_linear_plan.restype = ctypes.c_int
-        L.gdn_linear_plan.argtypes = [vp, vp, ctypes.POINTER(GdnLinearDims), ctypes.c_int32, ctypes.POINTER(GdnLinearPlanInfo)]
+        L.gdn_linear_plan.argtypes = [vp, vp, ctypes.POINTER(GdnLinearDims), ctypes.c_int32,
+                                      ctypes.POINTER(GdnLinearPlanInfo)]
         _lib = L
     return _lib
 

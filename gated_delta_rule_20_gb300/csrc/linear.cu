@@ -130,9 +130,10 @@ __global__ void __launch_bounds__(256, 2) linear_ffma_kernel(const __grid_consta
                 buf[turn][0][tid % 4 * 4 + j][tid / 4 + i * (kThreads / 4)] = xr[i][j];
                 if constexpr (kNK) buf[turn][1][tid % 4 * 4 + j][tid / 4 + i * (kThreads / 4)] = wr[i][j];
             }
-            if constexpr (!kNK)
-                *reinterpret_cast<float4*>(&buf[turn][1][(tid + i * kThreads) / (kTile / 4)][(tid + i * kThreads) % (kTile / 4) * 4]) =
-                    make_float4(wr[i][0], wr[i][1], wr[i][2], wr[i][3]);
+            if constexpr (!kNK) {
+                const int row = (tid + i * kThreads) / (kTile / 4), at = (tid + i * kThreads) % (kTile / 4) * 4;
+                *reinterpret_cast<float4*>(&buf[turn][1][row][at]) = make_float4(wr[i][0], wr[i][1], wr[i][2], wr[i][3]);
+            }
         }
     };
     // The thread's tokens: TM / 2 of the tile's first half and TM / 2 of its second; its columns likewise.
@@ -280,7 +281,8 @@ template <typename T, int TM, bool kNK, bool kVec>
 cudaError_t launch_tile(const LinearArgs& a, int splits, const LinearMarks& marks, cudaStream_t s) {
     const int tile = 16 * TM, cols = a.gated ? tile / 2 : tile;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((a.N + (long long)cols - 1) / cols * splits), (unsigned)((a.M + (long long)tile - 1) / tile));
+    cfg.gridDim = dim3((unsigned)((a.N + (long long)cols - 1) / cols * splits),
+                       (unsigned)((a.M + (long long)tile - 1) / tile));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -302,7 +304,9 @@ cudaError_t launch_layout(const LinearArgs& a, int splits, const LinearMarks& ma
     const long long wn = a.gated ? 2LL * a.N : a.N;
     const bool vec = four(a.x) && four(a.w) && a.K % 4 == 0 && (a.nk || (wn % 4 == 0 && a.N % 4 == 0));
     if constexpr (!std::is_same<T, __nv_fp8_e4m3>::value) {  // e4m3 weights are [N', K]
-        if (!a.nk) return vec ? launch_tile<T, TM, false, true>(a, splits, marks, s) : launch_tile<T, TM, false, false>(a, splits, marks, s);
+        if (!a.nk)
+            return vec ? launch_tile<T, TM, false, true>(a, splits, marks, s)
+                       : launch_tile<T, TM, false, false>(a, splits, marks, s);
     }
     return vec ? launch_tile<T, TM, true, true>(a, splits, marks, s) : launch_tile<T, TM, true, false>(a, splits, marks, s);
 }

@@ -103,9 +103,10 @@ __device__ __forceinline__ float gelu(float v) {
     return v * (v > 0.f ? 1.f - q : q);  // (+infinity stays)
 }
 
-// gelu for fp32 outputs, with the relative error of fp32 down to its smallest values: Phi(-a) e^(a^2 / 2) = s (c0 + c1 s + ...
-// + c7 s^7), s = 1 / (1 + 0.31 a), a least-maximum fit of the relative error over a = 0 .. 15 (1.6e-7; with the roundings
-// 1e-6 of gelu for v > -5 and 4e-6 at -12).  (erfcf instead spills the registers of 32 values in linear_large_kernel.)
+// gelu for fp32 outputs, with the relative error of fp32 down to its smallest values: Phi(-a) e^(a^2 / 2) = s (c0 + c1 s
+// + ... + c7 s^7), s = 1 / (1 + 0.31 a), a least-maximum fit of the relative error over a = 0 .. 15 (1.6e-7; with the
+// roundings 1e-6 of gelu for v > -5 and 4e-6 at -12).  (erfcf instead spills registers in linear_large_kernel.)  M = 16384,
+// K = 512, N = 4096 with fp32 output 140 us, 125 by the formula above.
 constexpr int kGeluF32 = 16;
 __device__ __forceinline__ float gelu_f32(float v) {
     const float s = __fdividef(1.f, fmaf(0.31f, fabsf(v), 1.f));

@@ -20,7 +20,8 @@
 // linear_large_kernel (many tokens; bound by the tensor cores): persistent CTA pairs
 // (cta_group::2) on tiles of 256 columns x up to 256 tokens; every CTA loads its 128 columns and
 // half of the tokens.  Two accumulators in TMEM: the epilogue of one tile runs beside the next
-// tile's products.  (fp32 by bf16 parts, at the end of the file, takes all of TMEM for one tile.)
+// tile's products.  (fp32 by bf16 parts, at the end of the file, takes all of TMEM for one tile; fp32 outputs of long
+// sums add up blocks of K, see block_of.)
 //
 // linear_joint_kernel (a few tiles and a long K): two to four such pairs on a tile, each with its part of K.
 #include <cuda.h>
@@ -30,6 +31,7 @@
 #include <atomic>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "gdn_internal.h"
 #include "linear_epilogue.cuh"
@@ -58,7 +60,7 @@ struct TcArgs {
     int32_t* status;
     int accs, starts[kMaxAccs];     // fp32 by parts: accumulators of a tile, from 1 on each from its first slab (else one)
     int plane;                      // fp32 by parts: elements of K from one part to the next
-    int block, blocks, ring;        // slabs of a block of K, the tile's (small kernel: CTA's) blocks, and their accumulators (see block_of)
+    int block, blocks, ring;        // slabs of a block of K, blocks of a tile (small kernel: of a CTA), accumulators
     const uint8_t* tops;            // fp32 by parts: see LinearMarks (null otherwise)
     int marks;
 };
@@ -87,12 +89,14 @@ struct Ring {
     }
 };
 
-// The tensor cores truncate a sum at every step of 16 terms, always towards zero, so that a sum of K bf16 products of both
-// signs is off by about K 1e-9 of the sums' norm (2.1e-6 at K = 2048 and 1.9e-5 at 16384; fp32 sums 4e-7 and 1.5e-6), and sums
-// of one sign by up to 4e-9 K.  bf16 outputs round that away; for fp32 outputs K is worked off in blocks of at most 8 slabs (512
-// in bf16: 5e-7), in two accumulators in turns, and the epilogue warps add every block to the tile's sums, with rounding, while
-// the next one's products run (kernels with BLOCKED).  The sums of a CTA pair's tile are in registers, 96 a thread at the most
-// (192 tokens); those of the small kernel, which has half the registers, in TMEM behind the accumulators.
+// The tensor cores truncate a sum at every step of 16 terms, always towards zero, so that a sum of K bf16 products of
+// both signs is off by about K 1e-9 of the sums' norm (2.1e-6 at K = 2048 and 1.9e-5 at 16384; fp32 sums 4e-7 and
+// 1.5e-6), and sums of one sign by up to 4e-9 K.  bf16 outputs round that away; for fp32 outputs K is worked off in
+// blocks of at most 8 slabs (512 in bf16: 5e-7) in a ring of accumulators, and the epilogue warps add every block to
+// the tile's sums, with rounding, while the next ones' products run (kernels with BLOCKED).  The sums of a CTA pair's
+// tile are in registers, 96 a thread; those of the small kernel, which has half the registers, in TMEM behind its two
+// accumulators.  M = 16384, K = 4096, N = 2048 194 us (151 in one accumulator): tiles have 160 tokens where 224 are
+// best, for three accumulators beside one another; with two of 192 tokens 209, the products wait for a tile's end.
 constexpr int kBlockSlabs = 8;
 __host__ __device__ inline int block_of(int slabs, bool blocked) {
     const int blocks = blocked ? (slabs + kBlockSlabs - 1) / kBlockSlabs : 1;
@@ -188,8 +192,8 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 // parts a slab is three stages, the third parts in the first: each stage is loaded once for its two to three
 // products and handed back as early as their order allows.
 template <bool F8, bool KN, bool PARTS, bool PAIR>
-__device__ __forceinline__ void mma_stages(const TcArgs& t, uint32_t tmem, uint32_t sm, const int* at, uint64_t* empty, int acc,
-                                           bool first, bool main) {
+__device__ __forceinline__ void mma_stages(const TcArgs& t, uint32_t tmem, uint32_t sm, const int* at, uint64_t* empty,
+                                           int acc, bool first, bool main) {
     const uint32_t s0 = sm + at[0] * t.stage_bytes;
     if constexpr (!PARTS) {
         mma_slab<F8, KN, PAIR>(tmem, s0, s0, t.idesc, main);
@@ -380,7 +384,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
             ok = mbar_wait_warp(&bars->acc_full[q & 1], (q >> 1) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
-            for (int c0 = (warp - 2) / 4 * 16; c0 < cols; c0 += 32) add_block_tmem(sums + c0, base + (q & 1) * t.bn + c0, q == 0);
+            for (int c0 = (warp - 2) / 4 * 16; c0 < cols; c0 += 32)
+                add_block_tmem(sums + c0, base + (q & 1) * t.bn + c0, q == 0);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
 // ------------------------------------------------------------------ many tokens
 constexpr int kLargeStages = 10;
 constexpr int kMaxRing = 4;                        // accumulators of a CTA pair (two, unless BLOCKED)
-constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 directions x 16 values x 32 lanes
+constexpr uint32_t kSwapBytes = 4 * 2 * 2 * 16 * 32 * 4;  // gated: 4 warp pairs x 2 turns x 2 ways x 16 values x 32 lanes
 constexpr uint32_t kBoxRow = 128;                  // a staged output row: 64 bf16 columns
 
 struct LargeBars {
@@ -560,10 +565,11 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float (&v)[C], const
 // The epilogue warps of linear_large_kernel, for any output: every tile of the pair, 32 tokens at a time.  The first
 // residual values of a tile are loaded before its products are done, the next chunk's before this
 // one's are used.
-// A tile's blocks of K added up, from the accumulator `at` of the ring on; the sums are left in the last block's, from where
-// they are finished as those of other tiles.  left: blocks of this and later tiles of the pair.  (Not inlined: the 96 sums
-// leave no registers for what the epilogue has there, which went to local memory at every block.)
-__device__ __noinline__ bool add_blocks(LargeBars* bars, uint32_t base, int bn, int ring, int cols, Ring at, int blocks, int left) {
+// A tile's blocks of K added up, from the accumulator `at` of the ring on; the sums are left in the last block's, from
+// where they are finished as those of other tiles.  left: blocks of this and later tiles of the pair.  (Not inlined: the
+// 96 sums leave no registers for what the epilogue has there, which went to local memory at every block.)
+__device__ __noinline__ bool add_blocks(LargeBars* bars, uint32_t base, int bn, int ring, int cols, Ring at, int blocks,
+                                        int left) {
     float sum[3][32];
 #pragma unroll
     for (int j = 0; j < 96; ++j) sum[j / 32][j % 32] = 0.f;
@@ -574,7 +580,8 @@ __device__ __noinline__ bool add_blocks(LargeBars* bars, uint32_t base, int bn, 
         if (q + 1 == blocks) break;
         tc_fence_before();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0 && q + ring < left) mbar_arrive_cluster(map_to_rank(smem_u32(&bars->acc_empty[at.s]), 0));
+        if ((threadIdx.x & 31) == 0 && q + ring < left)
+            mbar_arrive_cluster(map_to_rank(smem_u32(&bars->acc_empty[at.s]), 0));
         at.next(ring);
     }
 #pragma unroll
@@ -601,7 +608,8 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
     const uint32_t pair_bar = 1 + (quad & 1) + 2 * half;
     float* ex = swap + ((quad & 1) + 2 * half) * (2 * 2 * 16 * 32) + lane;
     volatile int* abort_flag = &bars->abort;
-    const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
+    const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0);
+    const uint32_t done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
     int turn = 0, flip = 0;
     const int turns = (tiles - pair + pairs - 1) / pairs;
     Ring acc_at;  // BLOCKED: of the accumulators
@@ -626,7 +634,7 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
         }
         const int b = BLOCKED ? acc_at.s : acc_of<PARTS>(turn);
         if (a.res && live) load_residual<C>(a, res, m_lo + own, n);
-        if (!BLOCKED) ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[b], acc_use<PARTS>(turn) & 1, abort_flag));
+        if (!BLOCKED) ok = mbar_wait_warp(&bars->acc_full[b], acc_use<PARTS>(turn) & 1, abort_flag);
         // one answer for both warps of a gated pair, which meet at a barrier below
         if (GATED ? named_bar_any(pair_bar, 64, !ok) : !ok) break;
         tc_fence_after();
@@ -715,7 +723,8 @@ __device__ __forceinline__ void epilogue_staged(const TcArgs& t, const CUtensorM
     uint8_t* box = boxes + (half * 2 + duo) * ((t.bn / 32 + 1) / 2) * kBoxBytes;
     uint64_t* res_full = &bars->res_full[half * 2 + duo];
     volatile int* abort_flag = &bars->abort;
-    const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0), done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
+    const uint32_t done0 = map_to_rank(smem_u32(&bars->acc_empty[0]), 0);
+    const uint32_t done1 = map_to_rank(smem_u32(&bars->acc_empty[1]), 0);
     const bool has_res = a.res != nullptr;
     Tiles walk;
     // first column of the boxes and first token of these chunks of a tile
@@ -951,7 +960,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // the leader sees both CTAs' loads land before the pair can exit (bounded)
         if (rank == 0)
-            for (int j = (i > stages ? i - stages : 0); j < i; ++j) (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
+            for (int j = (i > stages ? i - stages : 0); j < i; ++j)
+                (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
     } else if (warp == 1) {
         if (rank == 0) {  // MMA issuer of the pair
             int i = 0, turn = 0;
@@ -983,7 +993,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const bool main = acc.step(t, k) || first;
                     if (elect_one()) {
-                        mma_stages<F8, KN, PARTS, true>(t, tmem + b * t.bn, smem_u32(sm), s, bars->empty, acc.q, k == 0, main);
+                        mma_stages<F8, KN, PARTS, true>(t, tmem + b * t.bn, smem_u32(sm), s, bars->empty, acc.q, k == 0,
+                                                        main);
                         if (k + 1 == end) mma_commit_pair(&bars->acc_full[b]);
                     }
                     __syncwarp();
@@ -1028,8 +1039,8 @@ __device__ __forceinline__ uint32_t chunk_slot(int c, int from, int splits) {
 
 // The chunks that this warp finishes of the tile at (tn, tm); `part`: the shared memory that the others have filled.
 template <bool GATED>
-__device__ __forceinline__ void finish_chunks(const TcArgs& t, float* swap, uint32_t part, uint32_t tmem, int rank, int q, int tn,
-                                              int tm) {
+__device__ __forceinline__ void finish_chunks(const TcArgs& t, float* swap, uint32_t part, uint32_t tmem, int rank, int q,
+                                              int tn, int tm) {
     constexpr int C = GATED ? 16 : 32;
     const LinearArgs& a = t.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1158,7 +1169,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
             __syncwarp();
         }
         if (rank == 0)  // the leader sees both CTAs' loads land (bounded)
-            for (int j = (i > stages ? i - stages : 0); j < i; ++j) (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
+            for (int j = (i > stages ? i - stages : 0); j < i; ++j)
+                (void)mbar_wait(&bars->full[j % stages], (j / stages) & 1);
     } else if (warp == 1) {
         if (rank == 0) {  // MMA issuer of the pair
             const uint32_t both = 3u << leader;
@@ -1166,7 +1178,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
             Ring at;
             for (; i < k_hi - k_lo; ++i, at.next(stages)) {
                 if (BLOCKED && in == t.block) {
-                    if (++block >= 2 && !mbar_wait_warp(&bars->acc_empty[block & 1], ((block - 2) >> 1) & 1, abort_flag)) break;
+                    if (++block >= 2 && !mbar_wait_warp(&bars->acc_empty[block & 1], ((block - 2) >> 1) & 1, abort_flag))
+                        break;
                     in = 0;
                 }
                 if (!mbar_wait_warp(&bars->full[at.s], at.phase, abort_flag)) break;
@@ -1236,7 +1249,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
                 tmem_ld32(mine, v);
                 tmem_wait_ld();
             }
-            const uint32_t to = map_to_rank(smem_u32(sm) + chunk_slot(c, q, S) + (quad * 32 + lane) * 16, 2 * (c % S) + rank);
+            const uint32_t slot = smem_u32(sm) + chunk_slot(c, q, S) + (quad * 32 + lane) * 16;
+            const uint32_t to = map_to_rank(slot, 2 * (c % S) + rank);
 #pragma unroll
             for (int i = 0; i < 32; i += 4) st_cluster_f32x4(to + i / 4 * 2048, v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
@@ -1300,8 +1314,8 @@ constexpr int kSmemLimit = 227 * 1024;
 // A launch in clusters of `cluster` CTAs that may be set up while the stream's preceding kernel ends
 // (programmatic stream serialization; the kernels wait for that kernel before they read anything).
 template <typename... P, typename... Q>
-cudaError_t launch(void (*kernel)(P...), std::atomic<bool> (&done)[kMaxDevices], int dev, dim3 grid, int threads, size_t smem,
-                   int cluster, cudaStream_t s, const Q&... args) {
+cudaError_t launch(void (*kernel)(P...), std::atomic<bool> (&done)[kMaxDevices], int dev, dim3 grid, int threads,
+                   size_t smem, int cluster, cudaStream_t s, const Q&... args) {
     const cudaError_t e = allow_smem(kernel, kSmemLimit, done, dev);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -1346,11 +1360,11 @@ struct Operands {
 };
 
 template <bool F8, bool KN, bool PARTS, bool BLOCKED>
-cudaError_t launch_small_as(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
-                         int dev, cudaStream_t s) {
+cudaError_t launch_small_as(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m,
+                            size_t smem, int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_small_kernel<F8, KN, PARTS, BLOCKED>, done, dev, dim3((unsigned)(tiles * t.splits), (unsigned)tiles_m), kThreads, smem,
-                  t.splits, s, tw, tx, t);
+    const dim3 grid((unsigned)(tiles * t.splits), (unsigned)tiles_m);
+    return launch(linear_small_kernel<F8, KN, PARTS, BLOCKED>, done, dev, grid, kThreads, smem, t.splits, s, tw, tx, t);
 }
 template <bool F8, bool KN, bool PARTS>
 cudaError_t launch_small(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, int tiles, int tiles_m, size_t smem,
@@ -1372,7 +1386,8 @@ struct Plan {
 // bytes of every token of the tile.  Fitted to sweeps of M = 1 .. 512, K and N = 512 .. 8192 (bf16, us in a
 // graph over weights larger than L2):
 //   - small: one CTA takes in about 85 KB/us and two on an SM 115, all together at most 6.3 MB/us; the
-//     partial sums' way through TMEM and shared memory costs 0.3 + bn / 60, a third more over 8 CTAs.  M = 64, K = N = 2048: 12.4 (32 tokens, no split), 8.3 (2), 6.8 (4), 6.9 (8);
+//     partial sums' way through TMEM and shared memory costs 0.3 + bn / 60, a third more over 8 CTAs.  M = 64,
+//     K = N = 2048: 12.4 (32 tokens, no split), 8.3 (2), 6.8 (4), 6.9 (8);
 //   - pairs: 0.28 us a slab at 256 tokens (the tensor cores' time), in proportion down to 0.19 (the weight's way
 //     from L2), and bn / 300 for the last tile's outputs.  M = 512, K = N = 4096: 20.6 the best small plan, 16.9 pairs
 //     at 128, 22.4 at 256; K = 16384, N = 512: 17.1 small, 55 pairs.
@@ -1380,10 +1395,11 @@ struct Plan {
 //     all clusters fit at once this is no choice (of 4, 6 and 8 CTAs 36, 23 and 15 do on 152 SMs).  M = 768, K = 8192,
 //     N = 2048: 28.7 pairs, 20.5 two a tile of 192; M = 384, K = 4096, N = 2048: 13.7 small, 15.8 pairs, 11.6 two a tile
 //     of 128; M = 1024, K = N = 2048: 10.3 pairs, 12.5 two a tile of 256.
-// On 48 shapes (M = 64 .. 1024) the choice is 0.3 % behind the best of all on average; by parts, on 17 shapes, it is it.
-// Blocks of K (see block_of) take tiles of at most 160 tokens, pairs that split K of 192, the small kernel of 64 (two CTAs an SM
-// share TMEM); pairs lose about 2 us and 0.2 a block, where they split K half of that.  M = 64, K = 2048, N = 8192: 13.4 pairs of
-// 64 tokens (10.1 without blocks), 10.9 small; M = 1024, K = 8192, N = 2048: 36.8 pairs, 47 small.
+// On the 48 shapes (M = 64 .. 1024) that it was fitted to the choice is 0.3 % behind the best of all on average, by parts
+// on 17 shapes it is it; on others it may be further off (M = 32, K = N = 8192 with fp32 output: 33 us, 25 the best).
+//   - blocks of K (see block_of): tiles of at most 160 tokens, pairs that split K 192, the small kernel 64 (two CTAs an SM
+//     share TMEM); pairs lose about 2 us and 0.2 a block, where they split K half of that.  M = 64, K = 2048, N = 8192:
+//     13.4 pairs of 64 tokens (10.1 without blocks), 10.9 small; M = 1024, K = 8192, N = 2048: 36.8 pairs, 47 small.
 Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     const bool blocked = a.out_f32 && accs == 1;
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
@@ -1410,7 +1426,8 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
             if (t < least) least = t, best = Plan{true, bn, S};
         }
     }
-    for (int bn = 16; bn <= (accs > 4 ? 64 : accs > 1 ? 256 / accs : 128); bn *= 2) {  // (two CTAs an SM share TMEM; by parts one)
+    // (TMEM: 256 columns where two CTAs share an SM's, by parts all of it)
+    for (int bn = 16; bn <= (accs > 4 ? 64 : accs > 1 ? 256 / accs : 128); bn *= 2) {
         if (bn > 16 && bn / 2 >= a.M) break;
         const long long tiles_m = (a.M + bn - 1) / bn;
         if (tiles_m > 65535) continue;  // the grid's limit
@@ -1418,7 +1435,7 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
             const long long ctas = tiles1 * tiles_m * S;
             if (blocked && bn > 64 && (slabs + S - 1) / S > kBlockSlabs) continue;
             const int beside = accs > 1 ? 1 : 2;
-            // CTAs at once: clusters stay inside one of 8 groups of SMs (of 16 to 20: two clusters of 8 do not fit in each).
+            // CTAs at once: clusters stay inside one of 8 groups of SMs (of 16 to 20: two clusters of 8 do not fit).
             // (Fewer than 48 SMs have no room for clusters of 8 CTAs, and by parts fewer than 96.)
             const long long room = 8LL * ((sms / 8 * beside - (S == 8 ? 4 : 0)) / S) * S;
             if (room <= 0) continue;
@@ -1468,11 +1485,15 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
         !encode(&tx, f8, op.x, a.M, depth, op.x_pitch, t.bn))
         return GDN_ERR_CUDA;
     const size_t smem = (size_t)t.stages * t.stage_bytes + sizeof(SmallBars) + 1024;
-    const cudaError_t e = f8              ? launch_small<true, false, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
-                          : op.accs == 1 ? (a.nk ? launch_small<false, false, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
-                                                 : launch_small<false, true, false>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s))
-                          : a.nk         ? launch_small<false, false, true>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s)
-                                         : launch_small<false, true, true>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s);
+    auto run = [&](auto e4m3, auto kn, auto parts) {
+        constexpr bool kF8 = decltype(e4m3)::value, kKN = decltype(kn)::value, kParts3 = decltype(parts)::value;
+        return launch_small<kF8, kKN, kParts3>(t, tw, tx, (int)tiles, (int)tiles_m, smem, dev, s);
+    };
+    const std::true_type yes{};
+    const std::false_type no{};
+    const cudaError_t e = f8              ? run(yes, no, no)
+                          : op.accs == 1 ? (a.nk ? run(no, no, no) : run(no, yes, no))
+                                         : (a.nk ? run(no, no, yes) : run(no, yes, yes));
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -1480,8 +1501,8 @@ template <bool F8, bool KN, bool PARTS, bool BLOCKED>
 cudaError_t launch_large_as(const TcArgs& t, const CUtensorMap& tw, const CUtensorMap& tx, const CUtensorMap& to,
                             const CUtensorMap& tr, int pairs, size_t smem, int dev, cudaStream_t s) {
     static std::atomic<bool> done[kMaxDevices];
-    return launch(linear_large_kernel<F8, KN, PARTS, BLOCKED>, done, dev, dim3((unsigned)(2 * pairs)), kThreads, smem, 2, s, tw, tx, to,
-                  tr, t);
+    return launch(linear_large_kernel<F8, KN, PARTS, BLOCKED>, done, dev, dim3((unsigned)(2 * pairs)), kThreads, smem, 2, s,
+                  tw, tx, to, tr, t);
 }
 
 template <bool F8, bool KN, bool PARTS>
@@ -1571,7 +1592,7 @@ gdn_status run_joint(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.blocks = ((t.slabs + t.splits - 1) / t.splits + t.block - 1) / t.block;
     t.tiles_m = (a.M + t.bn - 1) / t.bn;
     t.stage_bytes = kWBytes + t.bn / 2 * kSlabBytes;
-    // (the others' sums of a CTA's chunks, 96 KB at the most, fit the stages, 184 KB at the least)
+    // (the others' sums of a CTA's chunks, 96 KB at the most, fit the stages, 168 KB at the least)
     const size_t fixed = sizeof(LargeBars) + (a.gated ? kSwapBytes : 0) + 1024;
     t.stages = (int)((kSmemLimit - fixed) / t.stage_bytes);
     if (t.stages > kLargeStages) t.stages = kLargeStages;
@@ -1605,7 +1626,8 @@ struct CopyJob {
 };
 
 template <typename E>
-__global__ void __launch_bounds__(256) linear_align_kernel(const __grid_constant__ CopyJob x, const __grid_constant__ CopyJob w) {
+__global__ void __launch_bounds__(256) linear_align_kernel(const __grid_constant__ CopyJob x,
+                                                           const __grid_constant__ CopyJob w) {
     constexpr int V = 16 / (int)sizeof(E);
     griddep_launch_dependents();
     griddep_wait();
@@ -1631,8 +1653,8 @@ __global__ void __launch_bounds__(256) linear_align_kernel(const __grid_constant
 // more are taken, the five small ones (x1 w3, x3 w1, x2 w2, x1 w2, x2 w1) into an accumulator of their own.
 // The tensor cores truncate a sum at every step of 16 terms, always towards zero, so that it falls short by
 // about K 1e-9 of itself (2.1e-6 at K = 2048; fp32 sums with rounding 0.8e-6).  The x1 w1, whose sum that is,
-// therefore go to an accumulator for every 704 to 1024 of K (see accs_of), which are added with rounding: at K = 4096 sums of
-// one sign are off by 8.3e-7 (fp32 sums 8.4e-7; with three accumulators 1.57e-6).
+// therefore go to an accumulator for every 704 to 1024 of K (see accs_of), which are added with rounding: at K = 4096
+// sums of one sign are off by 8.3e-7 (fp32 sums 8.4e-7; with three accumulators 1.57e-6).
 constexpr int kParts = 3;
 
 // Splits one operand: rows_in x cols fp32 -> rows_out x width parts, rows `pitch` apart and parts `plane`
@@ -1646,8 +1668,8 @@ struct SplitJob {
 // tops[block], tops[gridDim.x + block]: the exponents of the largest elements of x and of the weight that the block
 // met (see LinearMarks).
 // 16 bytes are read at a time where a piece lies whole and on such a boundary (2048 x 2048 twice: 28 us by elements).
-__global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ SplitJob x, const __grid_constant__ SplitJob w,
-                                                           uint8_t* tops) {
+__global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant__ SplitJob x,
+                                                           const __grid_constant__ SplitJob w, uint8_t* tops) {
     __shared__ uint32_t warp_tops[2][256 / 32];
     griddep_launch_dependents();
     griddep_wait();
@@ -1661,7 +1683,8 @@ __global__ void __launch_bounds__(256) linear_split_kernel(const __grid_constant
         const long long first = d0 < c.half ? d0 : c.half + d0 - c.up;  // the source column of d0, if it has one
         const bool whole = row < c.rows_in && (d0 + 8 <= c.half || d0 >= c.up) && first + 8 <= c.cols;
         if (whole && (reinterpret_cast<uintptr_t>(src + first) & 15u) == 0) {
-            const float4 p = *reinterpret_cast<const float4*>(src + first), q = *reinterpret_cast<const float4*>(src + first + 4);
+            const float4* at16 = reinterpret_cast<const float4*>(src + first);
+            const float4 p = at16[0], q = at16[1];
             in[0] = p.x, in[1] = p.y, in[2] = p.z, in[3] = p.w, in[4] = q.x, in[5] = q.y, in[6] = q.z, in[7] = q.w;
         } else {
 #pragma unroll
@@ -1765,7 +1788,9 @@ void split_jobs(const LinearArgs& a, SplitJob* x, SplitJob* w) {
     w->width = w->pitch = a.gated ? 2 * w->up : up_to(wn);
     w->plane = kp * w->pitch;
 }
-size_t job_bytes(const SplitJob& c, bool planes) { return (size_t)((planes ? kParts * c.plane : c.rows_out * c.pitch) * 2); }
+size_t job_bytes(const SplitJob& c, bool planes) {
+    return (size_t)((planes ? kParts * c.plane : c.rows_out * c.pitch) * 2);
+}
 constexpr int kSplitBlocks = 1216;  // (8 a GB300's SM; a multiple of 4: see parts_fit_all)
 
 gdn_status run_copies(const LinearArgs& a, bool f8, uint8_t* scratch, int dev, int sms, cudaStream_t s) {
@@ -1816,9 +1841,11 @@ LinearPlan plan_linear(const LinearArgs& a, int32_t dtype) {
     const double ops = 2.0 * a.M * (a.gated ? 2LL * a.N : a.N) * a.K;
     if (dtype == GDN_F32) {
         // Worth the split and two more launches from 3e8 operations.  By parts and on the FFMA kernel, us: M = 128,
-        // K = N = 1024 (2.7e8) 14.1 and 11.6, M = 192 15.3 and 19.4; M = 64, K = N = 2048 19.8 and 19.7, M = 96 26.9 and 34.9;
-        // M = 16, K = 4096, N = 8192 93 and 126.  Fewer rows than a tile's 16 stay on the FFMA kernel.  Up to K = 4096 the
-        // accumulators' truncation stays near the error of fp32 sums (sums of 2048 positive products: 9.8e-7 and 8.9e-7).
+        // K = N = 1024 (2.7e8) 14.1 and 11.6, M = 192 15.3 and 19.4; M = 64, K = N = 2048 19.8 and 19.7, M = 96 26.9 and
+        // 34.9; M = 16, K = 4096, N = 8192 93 and 126.  Fewer rows than a tile's 16 stay on the FFMA kernel.  Up to
+        // K = 4096 the accumulators of a tile are enough for the error to stay that of fp32 sums; past it nothing empties
+        // them in between, and the FFMA kernel does the work at 53 TFLOP/s (M = N = 4096, K = 8192: 5.2 ms; 310 by parts
+        // at K = 4096, and a library's fp32 product 67).
         if (ops < 3e8 || a.K > 4096 || a.M < 16) return LinearPlan{LinearRoute::kFfma, 0};
         SplitJob x, w;
         split_jobs(a, &x, &w);
@@ -1829,7 +1856,7 @@ LinearPlan plan_linear(const LinearArgs& a, int32_t dtype) {
     CopyJob x, w;
     copy_jobs(a, size, &x, &w);
     if (x.rows == 0 && w.rows == 0) return LinearPlan{LinearRoute::kTensor, 0};
-    // Copies cost about 10 us and then HBM's rate, the FFMA kernel does 45 TFLOP/s: M = 4000, K = 3001, N = 5000
+    // Copies cost about 10 us and then HBM's rate, the FFMA kernel does 47 TFLOP/s: M = 4000, K = 3001, N = 5000
     // (bf16) 100 us and 2.6 ms.
     if (ops < 1e9) return LinearPlan{LinearRoute::kFfma, 0};
     return LinearPlan{LinearRoute::kCopies, job_bytes(x, size) + job_bytes(w, size)};
@@ -1839,7 +1866,9 @@ void linear_tc_tiles(const LinearArgs& a, int32_t dtype, LinearRoute route, int 
     const int slabs = slabs_of(a.K, dtype == GDN_F8E4M3);
     int share = 0;
     const Plan how = plan(a, slabs, route == LinearRoute::kParts ? accs_of(slabs, &share) : 1, sms);
-    info->kernel = !how.large ? GDN_LINEAR_KERNEL_SMALL : how.splits > 1 ? GDN_LINEAR_KERNEL_JOINT : GDN_LINEAR_KERNEL_PAIRS;
+    info->kernel = !how.large         ? GDN_LINEAR_KERNEL_SMALL
+                   : how.splits > 1 ? GDN_LINEAR_KERNEL_JOINT
+                                    : GDN_LINEAR_KERNEL_PAIRS;
     info->tokens = how.bn;
     info->splits = how.splits;
 }

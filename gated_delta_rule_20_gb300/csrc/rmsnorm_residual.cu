@@ -72,9 +72,9 @@ __device__ __forceinline__ float2 reduce_row(float ss, float mx, float2 (*part)[
     return make_float2(ss, mx);
 }
 
-// What turns h w into the output, (h w x) y: the norm's factor, over the row's scale for e4m3 (x = 1).  Where that passes
-// fp32's range (rows of the least scale with a small eps, zeros among them: from 1 / sqrt(eps) = 7.6e5 on), the factor and the
-// scale's inverse are applied one after the other.
+// What turns h w into the output, (h w x) y: the norm's factor, over the row's scale for e4m3 (x = 1).  Where that
+// passes fp32's range (rows of the least scale with a small eps, zeros among them: from 1 / sqrt(eps) = 7.6e5 on), the
+// factor and the scale's inverse are applied one after the other.
 template <typename O>
 __device__ __forceinline__ float2 row_factor(float2 stat, const NormArgs& a, long long r, bool first) {
     const float rinv = rsqrtf(stat.x / (float)a.D + a.eps);
@@ -329,8 +329,9 @@ cudaError_t launch_rows(const NormArgs& a, int dev, int sms, cudaStream_t s) {
     constexpr int kBlock = GROUP == 32 ? 256 : GROUP, kRows = kBlock / GROUP;
     static const int fit = [] {  // blocks an SM of this instantiation, the same on every device the library is built for
         int n = 0;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>, kBlock, 0) ==
-                           cudaSuccess && n > 0 ? n : 1;
+        const cudaError_t e =
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>, kBlock, 0);
+        return e == cudaSuccess && n > 0 ? n : 1;
     }();
     constexpr int V = 16 / (int)sizeof(T);
     const size_t smem = kOdd ? (a.D + a.D / V) * sizeof(float) : 0;
@@ -343,7 +344,8 @@ cudaError_t launch_rows(const NormArgs& a, int dev, int sms, cudaStream_t s) {
         if (e != cudaSuccess) return e;
     }
     const long long need = (a.rows + kRows - 1) / kRows, room = (long long)sms * per_sm;
-    return launch(rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>, (unsigned)(need < room ? need : room), kBlock, smem, s, a);
+    const unsigned grid = (unsigned)(need < room ? need : room);
+    return launch(rmsnorm_residual_vec_kernel<T, O, GROUP, P, kOdd>, grid, kBlock, smem, s, a);
 }
 
 template <typename T, typename O, int GROUP, int P>

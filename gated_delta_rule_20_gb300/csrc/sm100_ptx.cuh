@@ -477,7 +477,10 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
 }
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t a) {
     float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ void st_cluster_f32x4(uint32_t a, float x, float y, float z, float w) {

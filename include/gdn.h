@@ -409,7 +409,8 @@ typedef struct {
  *     out[m, n] = act(a[m, n]) * a[m, N + n] + residual[m, n]
  * with W[k, n] the weight's element in its layout; sums and the epilogue in fp32, one
  * rounding to out_dtype.  silu(v) = v / (1 + e^-v), gelu(v) = v/2 (1 + erf(v / sqrt 2)),
- * relu(v) = max(v, 0) (NaN stays NaN).
+ * relu(v) = max(v, 0) (NaN stays NaN).  silu's relative error is at most (5 + 1.2 |v|) 2^-23 for v > -87, gelu's of
+ * fp32 outputs (v^2 + 5) 2^-22 for v > -13, of bf16 outputs 0.75e-7 |v| before their rounding.
  *   x            [M, K] in dtype
  *   x_scale      [M] fp32 and weight_scale [N'] fp32: GDN_F8E4M3 only (NULL otherwise)
  *   weight       [K, N'] or, under GDN_LINEAR_WEIGHT_NK, [N', K], in dtype;
@@ -432,10 +433,10 @@ typedef struct {
  * operands whose sums could pass fp32's range (K times the product of their largest magnitudes,
  * each rounded up to a power of two, above 2^127); an operand that is below 2^-100 whole, or both
  * where the product of their largest magnitudes is.  In the others, what single elements have below
- * 2^-133, the least bf16 number, is lost.  Copies and parts lie in scratch from cudaMallocAsync on `stream`, freed there (gdn_linear_ws takes it from the
- * caller); calls whose scratch cannot be had, or would pass 4 GiB of parts, run on the FFMA
- * kernel.  Results do not depend on what else runs: every sum has one order for given arguments
- * and device.
+ * 2^-133, the least bf16 number, is lost.  Copies and parts lie in scratch from cudaMallocAsync on
+ * `stream`, freed there (gdn_linear_ws takes it from the caller); calls whose scratch cannot be had,
+ * or would pass 4 GiB of parts, run on the FFMA kernel.  Results do not depend on what else runs:
+ * every sum has one order for given arguments and device.
  */
 gdn_status gdn_linear(const void* x, const float* x_scale, const void* weight, const float* weight_scale,
                       const float* bias, const void* residual, void* out, const gdn_linear_dims* dims,

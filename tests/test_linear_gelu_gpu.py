@@ -70,3 +70,14 @@ def test_every_kernel(gdn, M, N, K, dtype, layout, ffma, gated):
     torch.cuda.synchronize()
     assert got.shape == (M, N) and (got == got[:, :1]).all()
     _check(got[:, 0], v.float(), -0.5 if gated else 1.0)
+
+
+def test_silu_over_its_range(gdn):
+    """The header's bound of silu: (5 + 1.2 |v|) 2^-23 of the value for v > -87 (the fast exponential's error grows with
+    its argument)."""
+    v = torch.cat([torch.linspace(-86.9, 88, 60001), torch.logspace(-20, 1, 4000), -torch.logspace(-20, 1, 4000)])
+    v = v[v != 0]
+    got = gdn.linear(v.cuda()[:, None].contiguous(), torch.ones(1, 1, device="cuda"), activation="silu")
+    got, v = got.flatten().cpu().double().numpy(), v.double().numpy()
+    ref = v / (1 + np.exp(-v))
+    assert (np.abs(got - ref) <= (5 + 1.2 * np.abs(v)) * 2.0 ** -23 * np.abs(ref)).all()
