@@ -95,8 +95,8 @@ struct Ring {
 // blocks of at most 8 slabs (512 in bf16: 5e-7) in a ring of accumulators, and the epilogue warps add every block to
 // the tile's sums, with rounding, while the next ones' products run (kernels with BLOCKED).  The sums of a CTA pair's
 // tile are in registers, 96 a thread; those of the small kernel, which has half the registers, in TMEM behind its two
-// accumulators.  M = 16384, K = 4096, N = 2048 194 us (151 in one accumulator): tiles have 160 tokens where 224 are
-// best, for three accumulators beside one another; with two of 192 tokens 209, the products wait for a tile's end.
+// accumulators.  M = 16384, K = 4096, N = 2048 184 us (152 in one accumulator): tiles have 192 tokens at the most where
+// 224 are best, and the products wait for the epilogue at a tile's end.
 constexpr int kBlockSlabs = 8;
 __host__ __device__ inline int block_of(int slabs, bool blocked) {
     const int blocks = blocked ? (slabs + kBlockSlabs - 1) / kBlockSlabs : 1;
@@ -581,7 +581,7 @@ __device__ __noinline__ bool add_blocks(LargeBars* bars, uint32_t base, int bn, 
         tc_fence_before();
         __syncwarp();
         if ((threadIdx.x & 31) == 0 && q + ring < left)
-            mbar_arrive_cluster(map_to_rank(smem_u32(&bars->acc_empty[at.s]), 0));
+            mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(&bars->acc_empty[at.s]), 0));
         at.next(ring);
     }
 #pragma unroll
@@ -663,8 +663,12 @@ __device__ __forceinline__ void epilogue(const TcArgs& t, LargeBars* bars, float
             if (c + 32 >= hc && (BLOCKED ? t.blocks - 1 + t.ring < left : turn + (PARTS ? 1 : 2) < turns)) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_cluster(BLOCKED ? map_to_rank(smem_u32(&bars->acc_empty[b]), 0) : b ? done1 : done0);
+                if (lane == 0) {
+                    if constexpr (BLOCKED)
+                        mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(&bars->acc_empty[b]), 0));
+                    else
+                        mbar_arrive_cluster(b ? done1 : done0);
+                }
             }
             if (a.x_scale) {
                 const float mine = m0 + lane < a.M ? a.x_scale[m0 + lane] : 0.f;
@@ -1219,7 +1223,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_joint_kernel(const __grid_
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && b + 2 < blocks) mbar_arrive_cluster(b & 1 ? done1 : done0);
+            if (lane == 0 && b + 2 < blocks) mbar_arrive_cluster_relaxed(b & 1 ? done1 : done0);
         }
     } else {
         ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->acc_full[0], 0, abort_flag));
@@ -1397,9 +1401,9 @@ struct Plan {
 //     of 128; M = 1024, K = N = 2048: 10.3 pairs, 12.5 two a tile of 256.
 // On the 48 shapes (M = 64 .. 1024) that it was fitted to the choice is 0.3 % behind the best of all on average, by parts
 // on 17 shapes it is it; on others it may be further off (M = 32, K = N = 8192 with fp32 output: 33 us, 25 the best).
-//   - blocks of K (see block_of): tiles of at most 160 tokens, pairs that split K 192, the small kernel 64 (two CTAs an SM
-//     share TMEM); pairs lose about 2 us and 0.2 a block, where they split K half of that.  M = 64, K = 2048, N = 8192:
-//     13.4 pairs of 64 tokens (10.1 without blocks), 10.9 small; M = 1024, K = 8192, N = 2048: 36.8 pairs, 47 small.
+//   - blocks of K (see block_of): tiles of at most 192 tokens, in the small kernel 64 (two CTAs an SM share TMEM); pairs
+//     lose about 2 us and 0.2 a block, where they split K half of that.  M = 64, K = 2048, N = 8192: 13.4 pairs of 64 tokens
+//     (10.1 without blocks), 10.9 small; M = 1024, K = 8192, N = 2048: 36.8 pairs, 47 small.
 Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
     const bool blocked = a.out_f32 && accs == 1;
     const long long wn = a.gated ? 2LL * a.N : a.N, tiles1 = (wn + 127) / 128, tiles2 = (wn + 255) / 256;
@@ -1415,7 +1419,7 @@ Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
         if (accs > 1) t += (turns - 1) * accs * bn / 200.0;  // epilogues that nothing runs beside
         if (t < 1.0 + weight_mb / 6.3) t = 1.0 + weight_mb / 6.3;
         if (blocked && slabs > kBlockSlabs) t += 2.0 + 0.2 * (slabs / kBlockSlabs);
-        if (t < least && !(bn > 160 && blocked && slabs > kBlockSlabs)) least = t, best = Plan{true, bn, 1};
+        if (t < least && !(bn > 192 && blocked && slabs > kBlockSlabs)) least = t, best = Plan{true, bn, 1};
         for (int S = 2; S <= 4 && accs == 1 && 2 * S <= slabs; ++S) {
             if (bn > 192 && blocked && (slabs + S - 1) / S > kBlockSlabs) continue;
             if (tiles > sms / (2 * S) - 2 * (S - 1)) break;

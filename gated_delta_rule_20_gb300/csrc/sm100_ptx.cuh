@@ -489,6 +489,11 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t a, float x, float y, f
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
+// The same without waiting for this thread's earlier writes: for reads that are done (tcgen05.wait::ld), whose place may be
+// written again.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // 3-D tiled load into this CTA's shared memory whose bytes are counted on a barrier of either CTA of
 // the pair (`cluster_bar`: its shared::cluster address).
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, uint32_t cluster_bar, int c0, int c1,

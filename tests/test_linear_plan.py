@@ -158,8 +158,8 @@ def test_every_variant(L, M, N, K, dtype, layout, gated, kernel, tokens, splits,
 
 
 def test_plans_of_fp32_outputs(L):
-    """Sums of more than 8 slabs a CTA are worked off in blocks, which have smaller tiles: 160 tokens, 192 where pairs split
-    K, 64 in the small kernel; shorter ones have bf16 outputs' plans."""
+    """Sums of more than 8 slabs a CTA are worked off in blocks, which have smaller tiles: 192 tokens, 64 in the small
+    kernel; shorter ones have bf16 outputs' plans."""
     seen = set()
     for dtype, elems in (("bf16", 64), ("f8", 128)):
         for M in (1, 17, 64, 130, 300, 768, 2000, 16384):
@@ -172,7 +172,7 @@ def test_plans_of_fp32_outputs(L):
                     slabs = -(-K // elems)
                     share = -(-slabs // splits)
                     if share > 8:
-                        assert tokens <= {"pairs": 160, "joint": 192, "small": 64}[kernel]
+                        assert tokens <= {"pairs": 192, "joint": 192, "small": 64}[kernel]
                         seen.add((dtype, kernel))
                     if slabs <= 8:
                         assert of(gdn.GDN_F32) == of(gdn.GDN_BF16)
