@@ -93,10 +93,11 @@ struct Ring {
 // both signs is off by about K 1e-9 of the sums' norm (2.1e-6 at K = 2048 and 1.9e-5 at 16384; fp32 sums 4e-7 and
 // 1.5e-6), and sums of one sign by up to 4e-9 K.  bf16 outputs round that away; for fp32 outputs K is worked off in
 // blocks of at most 8 slabs (512 in bf16: 5e-7) in a ring of accumulators, and the epilogue warps add every block to
-// the tile's sums, with rounding, while the next ones' products run (kernels with BLOCKED).  The sums of a CTA pair's
-// tile are in registers, 96 a thread; those of the small kernel, which has half the registers, in TMEM behind its two
-// accumulators.  M = 16384, K = 4096, N = 2048 184 us (152 in one accumulator): tiles have 192 tokens at the most where
-// 224 are best, and the products wait for the epilogue at a tile's end.
+// the tile's sums, in registers, with rounding, while the next ones' products run (kernels with BLOCKED).  A CTA pair's
+// tile has 192 tokens at the most then (96 sums a thread), one of the small kernel 64: two accumulators of those are
+// the 128 columns of TMEM that its widest tile takes without blocks, so that two CTAs always find room on an SM.
+// M = 16384, K = 4096, N = 2048 184 us (152 in one accumulator): tiles of 224 tokens are best there, and the products wait
+// for the epilogue at a tile's end.
 constexpr int kBlockSlabs = 8;
 __host__ __device__ inline int block_of(int slabs, bool blocked) {
     const int blocks = blocked ? (slabs + kBlockSlabs - 1) / kBlockSlabs : 1;
@@ -115,20 +116,14 @@ __device__ __forceinline__ void add_block(float (&sum)[3][32], uint32_t acc, int
         for (int i = 0; i < 32; ++i) sum[j][i] += v[i];
     }
 }
-// The same for 16 columns whose sums lie in TMEM (the first block of a tile: sets them).
-__device__ __forceinline__ void add_block_tmem(uint32_t sums, uint32_t acc, bool first) {
-    float v[2][8], w[2][8];
+// The same for 16 columns.
+__device__ __forceinline__ void add_columns(float (&sum)[2][8], uint32_t acc) {
+    float v[2][8];
     tmem_ld8(acc, v[0]);
     tmem_ld8(acc + 8, v[1]);
-    if (!first) {
-        tmem_ld8(sums, w[0]);
-        tmem_ld8(sums + 8, w[1]);
-    }
     tmem_wait_ld();
-    uint32_t out[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) out[j] = __float_as_uint(first ? v[j / 8][j % 8] : v[j / 8][j % 8] + w[j / 8][j % 8]);
-    tmem_st16u(sums, out);
+    for (int j = 0; j < 16; ++j) sum[j / 8][j % 8] += v[j / 8][j % 8];
 }
 
 // The accumulator of a tile that slab k goes to (fp32 by parts: its x1 w1; the small products go to accumulator 0).
@@ -378,24 +373,41 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
     bool ok = false;
     if (warp >= 2 && run) {
         const int row = (warp & 3) * 32 + lane, blocks = BLOCKED ? (k_hi - k_lo + t.block - 1) / t.block : 1;
-        const uint32_t base = tmem + ((uint32_t)(row & ~31) << 16), sums = base + 2 * t.bn;
+        const uint32_t base = tmem + ((uint32_t)(row & ~31) << 16);
+        const int first = (warp - 2) / 4 * 16;  // this warp's columns: first, first + 32, ... and the 15 behind each
         ok = true;
-        for (int q = 0; BLOCKED && q + 1 < blocks; ++q) {  // the blocks of K before the last
-            ok = mbar_wait_warp(&bars->acc_full[q & 1], (q >> 1) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            for (int c0 = (warp - 2) / 4 * 16; c0 < cols; c0 += 32)
-                add_block_tmem(sums + c0, base + (q & 1) * t.bn + c0, q == 0);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0 && q + 2 < blocks) mbar_arrive(&bars->acc_empty[q & 1]);
+        float sum[2][2][8];  // BLOCKED: of the blocks of K (at most 64 columns)
+        if constexpr (BLOCKED) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[j / 16][j / 8 % 2][j % 8] = 0.f;
+            for (int q = 0; q + 1 < blocks; ++q) {
+                ok = mbar_wait_warp(&bars->acc_full[q & 1], (q >> 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (first + 32 * h < cols) add_columns(sum[h], base + (q & 1) * t.bn + first + 32 * h);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && q + 2 < blocks) mbar_arrive(&bars->acc_empty[q & 1]);
+            }
         }
         ok = __all_sync(0xffffffffu, mbar_wait_or_abort(&bars->done, 0, abort_flag)) && ok;  // one answer a warp
         tc_fence_after();
         if (ok) {
-            const uint32_t lanes = BLOCKED ? base + ((blocks - 1) & 1) * t.bn : base;
-            for (int c0 = (warp - 2) / 4 * 16; c0 < cols; c0 += 32) {  // (columns come in 16s: t.bn)
+            if constexpr (BLOCKED) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c0 = first + 32 * h;
+                    if (c0 >= cols) break;
+                    add_columns(sum[h], base + ((blocks - 1) & 1) * t.bn + c0);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c0 + j < cols) part[(c0 + j) * 128 + row] = sum[h][j / 8][j % 8];
+                }
+            }
+            const uint32_t lanes = base;
+            for (int c0 = first; !BLOCKED && c0 < cols; c0 += 32) {  // (columns come in 16s: t.bn)
                 float v[2][8];
                 tmem_ld8(lanes + c0, v[0]);
                 tmem_ld8(lanes + c0 + 8, v[1]);
@@ -413,13 +425,6 @@ __global__ void __launch_bounds__(kThreads, 2) linear_small_kernel(const __grid_
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j / 8][j % 8] = sum[j];
-                } else if (BLOCKED && blocks > 1) {
-                    float w[2][8];
-                    tmem_ld8(sums + c0, w[0]);
-                    tmem_ld8(sums + c0 + 8, w[1]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j / 8][j % 8] += w[j / 8][j % 8];
                 }
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
@@ -1401,7 +1406,7 @@ struct Plan {
 //     of 128; M = 1024, K = N = 2048: 10.3 pairs, 12.5 two a tile of 256.
 // On the 48 shapes (M = 64 .. 1024) that it was fitted to the choice is 0.3 % behind the best of all on average, by parts
 // on 17 shapes it is it; on others it may be further off (M = 32, K = N = 8192 with fp32 output: 33 us, 25 the best).
-//   - blocks of K (see block_of): tiles of at most 192 tokens, in the small kernel 64 (two CTAs an SM share TMEM); pairs
+//   - blocks of K (see block_of): tiles of at most 192 tokens, in the small kernel 64; pairs
 //     lose about 2 us and 0.2 a block, where they split K half of that.  M = 64, K = 2048, N = 8192: 13.4 pairs of 64 tokens
 //     (10.1 without blocks), 10.9 small; M = 1024, K = 8192, N = 2048: 36.8 pairs, 47 small.
 Plan plan(const LinearArgs& a, int slabs, int accs, int sms) {
@@ -1479,7 +1484,7 @@ gdn_status run_small(const LinearArgs& a, const Operands& op, bool f8, Plan how,
     t.stages = (int)(((op.plane ? kSmemLimit : 112 * 1024) - sizeof(SmallBars) - 1024) / t.stage_bytes);  // two CTAs an SM
     if (t.stages > kMaxStages) t.stages = kMaxStages;
     t.tmem_cols = 32;
-    while (t.tmem_cols < (uint32_t)((t.blocks > 1 ? 3 : t.accs) * t.bn)) t.tmem_cols <<= 1;
+    while (t.tmem_cols < (uint32_t)((t.blocks > 1 ? 2 : t.accs) * t.bn)) t.tmem_cols <<= 1;
     t.idesc = f8 ? make_idesc_e4m3(128, t.bn) : make_idesc_bf16(128, t.bn, a.nk ? 0 : 1, 0);
     gdn_status st = status_word_for_current_device(&t.status);
     if (st != GDN_OK) return st;
