@@ -30,6 +30,7 @@ GDN_F8E4M3 = 2
 GDN_ZERO_INITIAL_STATE = 1 << 0
 GDN_FORCE_FFMA = 1 << 1
 GDN_SINGLE_PASS = 1 << 2
+GDN_HEAD_DECAY = 1 << 3
 
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU, GDN_ACT_RELU = range(4)
 ACTIVATIONS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "gelu": GDN_ACT_GELU, "relu": GDN_ACT_RELU}
@@ -38,6 +39,11 @@ GDN_LINEAR_WEIGHT_NK = 1 << 0
 GDN_LINEAR_GATED = 1 << 1
 GDN_LINEAR_FORCE_FFMA = 1 << 2
 
+GDN_ROTARY_INTERLEAVED = 1 << 0
+GDN_ROTARY_INVERSE = 1 << 1
+GDN_ROTARY_POSITIONS_I32 = 1 << 2
+ROTARY_LAYOUTS = {"half": 0, "interleaved": GDN_ROTARY_INTERLEAVED}
+
 # Every symbol include/gdn.h declares.
 EXPORTED = ("gdn_prefill", "gdn_decode_step", "gdn_prefill_workspace_bytes", "gdn_status_string",
             "gdn_device_status", "gdn_kernels_per_call", "gdn_conv1d_prefill", "gdn_conv1d_decode",
@@ -45,7 +51,8 @@ EXPORTED = ("gdn_prefill", "gdn_decode_step", "gdn_prefill_workspace_bytes", "gd
             "gdn_prefill_gated", "gdn_prefill_segments", "gdn_decode_block_noalloc",
             "gdn_set_wait_limit_ns", "gdn_test_stall_prefill", "gdn_prefill_ws", "gdn_prefill_segment_starts",
             "gdn_rmsnorm_residual", "gdn_linear", "gdn_linear_ws", "gdn_linear_workspace_bytes",
-            "gdn_linear_plan")
+            "gdn_linear_plan", "gdn_linear_attn_prefill", "gdn_linear_attn_segments",
+            "gdn_linear_attn_workspace_bytes", "gdn_linear_attn_step", "gdn_rotary")
 
 
 class GdnDims(ctypes.Structure):
@@ -73,6 +80,17 @@ class GdnLinearDims(ctypes.Structure):
 class GdnLinearPlanInfo(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int32), ("operands", ctypes.c_int32), ("tokens", ctypes.c_int32),
                 ("splits", ctypes.c_int32)]
+
+
+_Strides = ctypes.c_int64 * 3
+
+
+class GdnRotaryDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64), ("S", ctypes.c_int64),
+                ("D", ctypes.c_int64), ("R", ctypes.c_int64), ("q_strides", _Strides), ("k_strides", _Strides),
+                ("q_out_strides", _Strides), ("k_out_strides", _Strides), ("position_stride", ctypes.c_int64),
+                ("first_position", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
+                ("amplitude", ctypes.c_float)]
 
 
 class GdnError(RuntimeError):
@@ -149,6 +167,17 @@ def lib() -> ctypes.CDLL:
         L.gdn_linear_plan.restype = ctypes.c_int
         L.gdn_linear_plan.argtypes = [vp, vp, ctypes.POINTER(GdnLinearDims), ctypes.c_int32,
                                       ctypes.POINTER(GdnLinearPlanInfo)]
+        L.gdn_linear_attn_prefill.restype = ctypes.c_int
+        L.gdn_linear_attn_prefill.argtypes = [vp, vp, vp, fp, vp, ctypes.c_float, fp, fp, vp, ctypes.POINTER(GdnDims), vp,
+                                              ctypes.c_size_t, vp]
+        L.gdn_linear_attn_segments.restype = ctypes.c_int32
+        L.gdn_linear_attn_segments.argtypes = [ctypes.POINTER(GdnDims), ctypes.c_int32]
+        L.gdn_linear_attn_workspace_bytes.restype = ctypes.c_size_t
+        L.gdn_linear_attn_workspace_bytes.argtypes = [ctypes.POINTER(GdnDims)]
+        L.gdn_linear_attn_step.restype = ctypes.c_int
+        L.gdn_linear_attn_step.argtypes = [vp, vp, vp, fp, ctypes.c_float, fp, fp, vp, ctypes.POINTER(GdnDims), vp]
+        L.gdn_rotary.restype = ctypes.c_int
+        L.gdn_rotary.argtypes = [vp, vp, vp, vp, vp, vp, ctypes.POINTER(GdnRotaryDims), vp]
         _lib = L
     return _lib
 
@@ -750,3 +779,208 @@ def linear_plan(M, N, K, dtype=GDN_BF16, out_dtype=None, *, weight_layout="kn", 
     d, info = GdnLinearDims(M, N, K, dtype, out_dtype, GDN_ACT_NONE, flags), GdnLinearPlanInfo()
     _check(lib().gdn_linear_plan(4096 + x_offset, 4096 + weight_offset, ctypes.byref(d), int(sm_count), ctypes.byref(info)))
     return LINEAR_KERNELS[info.kernel], LINEAR_OPERANDS[info.operands], info.tokens, info.splits
+
+
+# ------------------------------------------------------------------ linear attention with a decay for each head
+def _linear_attn_operands(q, k, v, g_log, state, state_out, out, stream, lengths=None):
+    """Checked operands of the two calls: ``(dims, device, pointers, out, state_out)``, with new outputs where
+    none were given."""
+    if _T is None:
+        _layer_init()
+    if not q.is_cuda or not q.is_contiguous():
+        raise ValueError("q must be a contiguous CUDA tensor")
+    dtype, device = q.dtype, q.device
+    code = _LAYER_CODES.get(dtype, GDN_F8E4M3)
+    if code == GDN_F8E4M3:
+        raise TypeError("q must be bfloat16 or float32, got %s" % dtype)
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("q and k must be [B, Hk, S, Dk] and v [B, Hv, S, Dv]")
+    (B, Hk, S, Dk), Hv, Dv = q.shape, v.shape[1], v.shape[3]
+    kp = _layer_ptr("k", k, q.shape, dtype, device)
+    vp = _layer_ptr("v", v, (B, Hv, S, Dv), dtype, device)
+    flags = GDN_HEAD_DECAY if g_log.dim() == 1 else 0
+    gp = _layer_ptr("g_log", g_log, (Hv,) if flags else (B, Hv, S), _T.float32, device)
+    sshape = (B, Hv, Dk, Dv)
+    sp = None if state is None else _layer_ptr("state", state, sshape, _T.float32, device)
+    if state_out is None:
+        state_out = state if state is not None else _layer_empty(sshape, _T.float32, device, stream)
+    np_ = _layer_ptr("state_out", state_out, sshape, _T.float32, device)
+    if out is None:
+        # rows behind a sequence's length are not written: in a new tensor they are zeros
+        out = _layer_empty(v.shape, dtype, device, stream)
+        if lengths is not None:
+            with _T.cuda.stream(stream if stream is not None else _T.cuda.current_stream(device)):
+                out.zero_()
+        op = out.data_ptr()
+    else:
+        op = _layer_ptr("out", out, v.shape, dtype, device)
+    return GdnDims(B, Hk, Hv, S, Dk, Dv, code, flags), device, (q.data_ptr(), kp, vp, gp), sp, np_, op, out, state_out
+
+
+def linear_attn_prefill(q, k, v, g_log, scale, state=None, out=None, *, lengths=None, state_out=None, force_ffma=False,
+                        single_pass=False, stream=None, workspace=None):
+    """Linear attention with a decay for each head over whole prompts (``gdn_linear_attn_prefill``):
+    ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``, ``o_t = scale S_t^T q_t``.
+
+    q, k [B, Hk, S, Dk] and v [B, Hv, S, Dv] bf16 or fp32; ``g_log`` fp32 [B, Hv, S], or [Hv] for one decay a
+    head; ``state`` [B, Hv, Dk, Dv] fp32 (None: zeros).  The state behind the prompt goes to ``state_out``, by default
+    ``state`` itself (a new tensor where that is None).  ``lengths`` [B] int32: sequence b has lengths[b] tokens; rows
+    behind them have no influence and are not written (zeros in a new ``out``).  ``single_pass`` sets
+    ``GDN_SINGLE_PASS``; ``workspace``: a uint8 CUDA tensor of ``linear_attn_workspace_bytes`` bytes (default: torch's).
+    Returns ``(out, state_out)``."""
+    d, device, (qp, kp, vp, gp), sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
+                                                                                    stream, lengths)
+    lp = None if lengths is None else _layer_ptr("lengths", lengths, q.shape[:1], _T.int32, device)
+    d.flags |= (GDN_FORCE_FFMA if force_ffma else 0) | (GDN_SINGLE_PASS if single_pass else 0)
+    wp, nbytes = None, 0
+    if workspace is not None:
+        if workspace.device != device or workspace.dtype != _T.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 CUDA tensor on %s" % device)
+        wp, nbytes = workspace.data_ptr(), workspace.numel()
+    else:
+        with _T.cuda.device(device):
+            nbytes = _lib.gdn_linear_attn_workspace_bytes(d)
+        if nbytes:  # from torch, which keeps it between calls
+            try:
+                workspace = _layer_empty((nbytes,), _T.uint8, device, stream)
+                wp = workspace.data_ptr()
+            except _T.OutOfMemoryError:
+                nbytes = 0  # the library asks for its own, and runs one pass where there is none
+    _layer_call(_lib.gdn_linear_attn_prefill, device, stream, qp, kp, vp, gp, lp, scale, sp, np_, op, d, wp, nbytes)
+    return out, state_out
+
+
+def linear_attn_segments(B, Hk, Hv, S, Dk=128, Dv=128, dtype=GDN_BF16, sm_count=None, *, single_pass=False,
+                         force_ffma=False) -> int:
+    """``gdn_linear_attn_segments``: the segments ``linear_attn_prefill`` cuts each sequence into (1: none) on a device
+    with ``sm_count`` SMs (default: the current CUDA device's)."""
+    if sm_count is None:
+        sm_count = _torch().cuda.get_device_properties(_torch().cuda.current_device()).multi_processor_count
+    flags = (GDN_FORCE_FFMA if force_ffma else 0) | (GDN_SINGLE_PASS if single_pass else 0)
+    return int(lib().gdn_linear_attn_segments(ctypes.byref(make_dims(B, Hk, Hv, S, Dk, Dv, dtype, flags)), int(sm_count)))
+
+
+def linear_attn_workspace_bytes(B, Hk, Hv, S, Dk=128, Dv=128, dtype=GDN_BF16, *, single_pass=False,
+                                force_ffma=False) -> int:
+    """``gdn_linear_attn_workspace_bytes`` on the current CUDA device (0 for one pass or without a device)."""
+    flags = (GDN_FORCE_FFMA if force_ffma else 0) | (GDN_SINGLE_PASS if single_pass else 0)
+    return int(lib().gdn_linear_attn_workspace_bytes(ctypes.byref(make_dims(B, Hk, Hv, S, Dk, Dv, dtype, flags))))
+
+
+def linear_attn_step(q, k, v, g_log, scale, state, out=None, *, state_out=None, stream=None):
+    """One token of every sequence (``gdn_linear_attn_step``): q, k [B, Hk, 1, Dk], v [B, Hv, 1, Dv], ``g_log``
+    [B, Hv, 1] or [Hv]; the new state goes to ``state_out``, by default ``state`` itself (which may be None, for
+    zeros).  Returns ``(out, state_out)``."""
+    d, device, (qp, kp, vp, gp), sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
+                                                                                    stream)
+    _layer_call(_lib.gdn_linear_attn_step, device, stream, qp, kp, vp, gp, scale, sp, np_, op, d)
+    return out, state_out
+
+
+# ------------------------------------------------------------------ rotary positions
+def _rotary_tensor(nm, x, y, like, stream):
+    """``(pointer, strides, heads, output, its pointer, its strides)`` of q or k."""
+    if x.device != like.device or x.dtype != like.dtype:
+        raise ValueError("%s must be a CUDA tensor of q's dtype on %s" % (nm, like.device))
+    if x.dim() != 4 or (x.shape[0], x.shape[2], x.shape[3]) != (like.shape[0], like.shape[2], like.shape[3]):
+        raise ValueError("%s must be [B, H, S, D] with q's B, S and D, got %s" % (nm, tuple(x.shape)))
+    if x.stride(3) != 1 and x.shape[3] > 1:
+        raise ValueError("%s must have contiguous channels" % nm)
+    if y is None:
+        y = _layer_empty(x.shape, x.dtype, x.device, stream)
+    elif y.device != x.device or y.dtype != x.dtype or y.shape != x.shape or (y.stride(3) != 1 and y.shape[3] > 1):
+        raise ValueError("%s_out must be %s's shape and dtype, with contiguous channels, on %s" % (nm, nm, x.device))
+    return x.data_ptr(), x.stride()[:3], x.shape[1], y, y.data_ptr(), y.stride()[:3]
+
+
+def rotary(q, k, inv_freq, positions=None, *, layout="half", amplitude=1.0, inverse=False, first_position=0, q_out=None,
+           k_out=None, stream=None):
+    """Rotary positions of q [B, Hq, S, D] and, unless None, k [B, Hk, S, D], bf16 or fp32, in one launch
+    (``gdn_rotary``).  Any strides with contiguous channels: views into a packed projection's rows are taken as they
+    lie.  The outputs are new contiguous tensors unless given (``q_out=q, k_out=k``: in place).
+
+    ``inv_freq`` [R/2] float64, radians a position: the first R channels are turned, in pairs (i, i + R/2) (``layout``
+    "half") or (2i, 2i + 1) ("interleaved"), and multiplied by ``amplitude``; the rest is copied.
+    ``rotary_frequencies`` makes both, also scaled for long contexts.  ``positions`` int64 or int32 [B, S] or
+    [S]; None: ``first_position + s``.  ``inverse`` turns back, which is also the gradient.  Returns ``(q_out, k_out)``
+    (k_out None without k)."""
+    if _T is None:
+        _layer_init()
+    if not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a CUDA tensor [B, H, S, D]")
+    device = q.device
+    code = _LAYER_CODES.get(q.dtype, GDN_F8E4M3)
+    if code == GDN_F8E4M3:
+        raise TypeError("q must be bfloat16 or float32, got %s" % q.dtype)
+    flags = ROTARY_LAYOUTS.get(layout)
+    if flags is None:
+        raise ValueError("layout must be one of %s" % ", ".join(ROTARY_LAYOUTS))
+    if inverse:
+        flags |= GDN_ROTARY_INVERSE
+    B, _, S, D = q.shape
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be [R / 2]")
+    fp = _layer_ptr("inv_freq", inv_freq, inv_freq.shape, _T.float64, device)
+    pp, pstride = None, 0
+    if positions is not None:
+        if positions.dtype is _T.int32:
+            flags |= GDN_ROTARY_POSITIONS_I32
+        elif positions.dtype is not _T.int64:
+            raise TypeError("positions must be int64 or int32, got %s" % positions.dtype)
+        if positions.device != device or positions.shape not in ((B, S), (S,)) or (S > 1 and positions.stride(-1) != 1):
+            raise ValueError("positions must be [B, S] or [S] on %s, tokens contiguous" % device)
+        pp = positions.data_ptr()
+        pstride = positions.stride(0) if positions.dim() == 2 else 0
+    qp, qs, Hq, q_out, yp, ys = _rotary_tensor("q", q, q_out, q, stream)
+    kp = zp = None
+    ks = zs = (0, 0, 0)
+    Hk = 0
+    if k is not None:
+        kp, ks, Hk, k_out, zp, zs = _rotary_tensor("k", k, k_out, q, stream)
+    elif k_out is not None:
+        raise ValueError("k_out goes with k only")
+    d = GdnRotaryDims(B, Hq, Hk, S, D, 2 * inv_freq.shape[0], qs, ks, ys, zs, pstride, first_position, code, flags, amplitude)
+    _layer_call(_lib.gdn_rotary, device, stream, qp, kp, fp, pp, yp, zp, d)
+    return q_out, k_out
+
+
+def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, original_length=None, fast_turns=32.0,
+                       slow_turns=1.0, device=None):
+    """``(inv_freq, amplitude)`` of ``rotary``: inv_freq[i] = base^(-2i / rotary_dim), float64 on ``device``, scaled
+    for contexts ``factor`` times as long as a model was trained for:
+
+    "linear"  every position counts 1 / factor;
+    "ntk"     a larger base, base * factor^(R / (R - 2)): the slowest pair is slowed by factor, the fastest not;
+    "yarn"    pairs that turn less than ``slow_turns`` times over ``original_length`` are slowed by factor, those with more than
+              ``fast_turns`` not, with a ramp over the pairs' index between them, and amplitude = 0.1 ln(factor) + 1;
+    "bands"   the same two limits with a ramp over the turns themselves, and amplitude 1."""
+    import math
+    torch = _torch()
+    R = int(rotary_dim)
+    if R < 2 or R % 2:
+        raise ValueError("rotary_dim must be even and at least 2, got %s" % rotary_dim)
+    if not base > 0 or not factor >= 1:
+        raise ValueError("base must be positive and factor at least 1")
+    i = torch.arange(R // 2, dtype=torch.float64)
+    if scaling == "ntk":
+        if R == 2:
+            raise ValueError("scaling 'ntk' needs rotary_dim > 2")
+        base = base * factor ** (R / (R - 2))
+    f, amplitude = float(base) ** (-2.0 * i / R), 1.0
+    if scaling in ("yarn", "bands"):
+        if original_length is None or not original_length > 0 or not fast_turns > slow_turns > 0:
+            raise ValueError("scaling '%s' needs original_length and fast_turns > slow_turns > 0" % scaling)
+        if scaling == "yarn":
+            at = lambda turns: R * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))  # noqa: E731
+            lo, hi = max(math.floor(at(fast_turns)), 0), min(math.ceil(at(slow_turns)), R - 1)
+            slow = ((i - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            amplitude = 0.1 * math.log(factor) + 1.0
+        else:
+            turns = original_length * f / (2 * math.pi)
+            slow = 1 - ((turns - slow_turns) / (fast_turns - slow_turns)).clamp(0, 1)
+        f = f * (1 - slow) + f / factor * slow
+    elif scaling == "linear":
+        f = f / factor
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling must be None, 'linear', 'ntk', 'yarn' or 'bands', got %r" % (scaling,))
+    return f.to(device) if device is not None else f, amplitude

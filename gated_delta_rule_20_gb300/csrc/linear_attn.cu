@@ -1,0 +1,526 @@
+// linear_attn.cu -- linear attention with a decay for each head: entry points, the single-token step and the
+// prefill on the FMA units.
+//
+//     S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = scale * S_t^T q_t        S fp32 [Dk, Dv] per (batch, value head)
+//
+// Step.  One pass over the state: S' = e^g S + k v^T is written as it is read and o = scale q^T S' summed on the
+// way, so the state's bytes bound it.  Columns of S are independent: a CTA owns one head's slice of 32, 64 or
+// 128 columns.
+//
+// Prefill on the FMA units (fp32 compute, and head dims off the tensor-core kernel): the recurrence itself, token by
+// token, with the state in registers.  Its 2 Dk Dv multiply-adds a token are the fewest of any form (a chunked one adds
+// C (Dk + Dv) / 2), and every one is an fp32 FMA on operands that lie in shared memory.  A warp owns 16
+// columns: lane (d, e) = (lane % 8, lane / 8) holds rows 32 m + 4 d + {0..3} of columns 4 e + {0..3}, so that the 8 lanes of a
+// column read 128 contiguous bytes of q and of k, and o is summed over them with 4 shuffles.  Rows go in pairs
+// (fma.rn.f32x2).  The state is kept as S~_t = e^{-c_t} S_t, with c the sum of the log-decays since the first of 16
+// staged tokens: S~ += (e^{-c_t} k_t) v_t^T, o_t = e^{c_t} scale S~^T q_t, and one product by e^{c_16} a block.  That is a third
+// fewer operations than a decay a token, and one rounding of a decay in 16: with decays near 1 the functions' errors
+// would add up (1.5e-6 after 290 tokens at e^-0.0005).  Blocks that decay by more than e^-8 take a product a token; they
+// forget within a few tokens.
+#include <cuda_bf16.h>
+
+#include <atomic>
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+#include "linear_attn.h"
+#include "sm100_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kMaxD = 128;
+
+// ------------------------------------------------------------------ single-token step
+constexpr int kStepThreads = 256;
+
+template <typename T, int C4, bool kVec>
+__global__ void __launch_bounds__(kStepThreads) linear_attn_step_kernel(LinearAttn p) {
+    constexpr int kRg = kStepThreads / C4, kRows = kMaxD / kRg, kCols = 4 * C4;
+    __shared__ float s_q[kMaxD], s_k[kMaxD];
+    __shared__ __align__(16) float s_red[kRg][kCols];
+    const long long bh = blockIdx.x;
+    const int b = (int)(bh / p.Hv), h = (int)(bh - (long long)b * p.Hv), hk = h / (p.Hv / p.Hk);
+    const int tid = threadIdx.x, cg = tid % C4, rg = tid / C4, base = blockIdx.y * kCols;
+    const int Dk = p.Dk, Dv = p.Dv;
+    // a thread's 4 columns: neighbours for 128-bit accesses, else C4 apart so that lanes are neighbours
+    int c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = base + (kVec ? 4 * cg + j : cg + j * C4);
+    const size_t at = (size_t)bh * Dk * Dv;
+    ptx::griddep_wait();
+
+    float4 S[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = rg + i * kRg;
+        S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (p.state_in && r < Dk) {
+            const float* row = p.state_in + at + (size_t)r * Dv;
+            if (kVec) {
+                if (c[0] < Dv) S[i] = __ldcs(reinterpret_cast<const float4*>(row + c[0]));
+            } else {
+                if (c[0] < Dv) S[i].x = row[c[0]];
+                if (c[1] < Dv) S[i].y = row[c[1]];
+                if (c[2] < Dv) S[i].z = row[c[2]];
+                if (c[3] < Dv) S[i].w = row[c[3]];
+            }
+        }
+    }
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = c[j] < Dv ? to_f32(static_cast<const T*>(p.v)[(size_t)bh * Dv + c[j]]) : 0.f;
+    if (tid < Dk) {
+        const size_t row = ((size_t)b * p.Hk + hk) * Dk + tid;
+        s_q[tid] = to_f32(static_cast<const T*>(p.q)[row]);
+        s_k[tid] = to_f32(static_cast<const T*>(p.k)[row]);
+    }
+    const float a = expf(fmaxf(p.g_log[p.head_decay ? h : bh], kMinLogDecay));
+    __syncthreads();
+
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int r = rg + i * kRg;
+        if (r < Dk) {
+            const float k = s_k[r], q = s_q[r];
+            float4 x;
+            x.x = fmaf(a, S[i].x, k * v[0]);
+            x.y = fmaf(a, S[i].y, k * v[1]);
+            x.z = fmaf(a, S[i].z, k * v[2]);
+            x.w = fmaf(a, S[i].w, k * v[3]);
+            o[0] = fmaf(q, x.x, o[0]);
+            o[1] = fmaf(q, x.y, o[1]);
+            o[2] = fmaf(q, x.z, o[2]);
+            o[3] = fmaf(q, x.w, o[3]);
+            float* row = p.state_out + at + (size_t)r * Dv;
+            if (kVec) {
+                if (c[0] < Dv) __stcs(reinterpret_cast<float4*>(row + c[0]), x);
+            } else {
+                if (c[0] < Dv) row[c[0]] = x.x;
+                if (c[1] < Dv) row[c[1]] = x.y;
+                if (c[2] < Dv) row[c[2]] = x.z;
+                if (c[3] < Dv) row[c[3]] = x.w;
+            }
+        }
+    }
+    ptx::griddep_launch_dependents();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s_red[rg][c[j] - base] = o[j];
+    __syncthreads();
+    if (tid < kCols && base + tid < Dv) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < kRg; ++i) sum += s_red[i][tid];
+        static_cast<T*>(p.out)[(size_t)bh * Dv + base + tid] = from_f32<T>(p.scale * sum);
+    }
+}
+
+template <typename K, typename... A>
+cudaError_t launch_after(K* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const A&... a) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a...);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <typename T, int C4>
+cudaError_t launch_step_cols(const LinearAttn& p, cudaStream_t stream) {
+    const dim3 grid((unsigned)(p.B * p.Hv), (unsigned)((p.Dv + 4 * C4 - 1) / (4 * C4)));
+    if (p.Dv % 4 == 0 && aligned16(p.state_in) && aligned16(p.state_out))
+        return launch_after(linear_attn_step_kernel<T, C4, true>, grid, kStepThreads, 0, stream, p);
+    return launch_after(linear_attn_step_kernel<T, C4, false>, grid, kStepThreads, 0, stream, p);
+}
+
+template <typename T>
+cudaError_t launch_step(const LinearAttn& p, int sms, cudaStream_t stream) {
+    // Slices as wide as leave every SM a CTA: whole rows of 128 columns keep the most loads in flight a
+    // thread, narrow ones spread a few heads over the card.
+    const long long heads = (long long)p.B * p.Hv;
+    if (p.Dv > 64 && heads >= sms) return launch_step_cols<T, 32>(p, stream);
+    if (p.Dv > 32 && heads * ((p.Dv + 63) / 64) >= sms) return launch_step_cols<T, 16>(p, stream);
+    return launch_step_cols<T, 8>(p, stream);
+}
+
+// ------------------------------------------------------------------ prefill on the FMA units
+constexpr int kTok = 16;           // tokens staged at once
+constexpr float kMostBlock = 8.f;  // largest log-decay of a block that is taken off its keys
+
+union Pair {
+    float2 f;
+    unsigned long long u;
+};
+__device__ __forceinline__ Pair pair_of(float x, float y) {
+    Pair r;
+    r.f = make_float2(x, y);
+    return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.u) : "l"(a.u), "l"(b.u), "l"(c.u));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.u) : "l"(a.u), "l"(b.u));
+    return r;
+}
+
+template <int MB>
+__device__ __forceinline__ void scale_state(Pair (&S)[MB][2][4], float a) {
+    const Pair aa = pair_of(a, a);
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[m][u][j] = mul2(aa, S[m][u][j]);
+}
+
+// MB: blocks of 32 rows of the state.  States only (the first pass of a split): segments 0 .. P - 2, end states
+// and decays to the split's arrays, no outputs.
+template <typename T, int MB, bool kStatesOnly>
+__global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, LinearAttnSplit split) {
+    constexpr int kDk = 32 * MB;
+    __shared__ __align__(16) float s_q[kStatesOnly ? 1 : kTok][kDk], s_k[kTok][kDk];
+    __shared__ __align__(16) float s_v[kTok][kMaxD];
+    __shared__ float s_o[kStatesOnly ? 1 : kTok][kMaxD];
+    __shared__ float2 s_a[kTok];  // what a token's state is multiplied by before it, and its output by
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d = lane & 7, e = lane >> 3;
+    const int cols = (int)blockDim.x / 2, base = blockIdx.y * cols;  // 16 columns a warp
+    const int mine = warp * 16 + e * 4;                              // this lane's first column of the slice
+    const long long heads = (long long)p.B * p.Hv, bh = blockIdx.x;
+    const int seg = blockIdx.z;
+    const int b = (int)(bh / p.Hv), h = (int)(bh - (long long)b * p.Hv), hk = h / (p.Hv / p.Hk);
+    const int Dk = p.Dk, Dv = p.Dv;
+    const long long n_state = (long long)Dk * Dv;
+    ptx::griddep_wait();
+    int len = p.S;
+    if (p.lengths) len = max(0, min(p.S, p.lengths[b]));
+    const int t0 = seg * split.len, t1 = min(len, split.P > 1 ? t0 + split.len : len);
+
+    // the start state
+    Pair S[MB][2][4];
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x[2];
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int r = 32 * m + 4 * d + 2 * u + w, c = base + mine + j;
+                    const long long i = (long long)r * Dv + c;
+                    x[w] = 0.f;
+                    if (r < Dk && c < Dv) {
+                        if (kStatesOnly || split.P == 1) {
+                            if (seg == 0 && p.state_in) x[w] = p.state_in[bh * n_state + i];
+                            if (kStatesOnly && seg == 0) split.parts[((split.P - 1) * heads + bh) * n_state + i] = x[w];
+                        } else if (seg == 0) {
+                            x[w] = split.parts[((split.P - 1) * heads + bh) * n_state + i];
+                        } else {
+                            x[w] = linear_attn_start(split, seg, bh, heads, n_state, i);
+                        }
+                    }
+                }
+                S[m][u][j] = pair_of(x[0], x[1]);
+            }
+    const T* qr = static_cast<const T*>(p.q) + ((size_t)b * p.Hk + hk) * p.S * Dk;
+    const T* kr = static_cast<const T*>(p.k) + ((size_t)b * p.Hk + hk) * p.S * Dk;
+    const T* vr = static_cast<const T*>(p.v) + (size_t)bh * p.S * Dv;
+    T* orow = static_cast<T*>(p.out) + (size_t)bh * p.S * Dv;
+    float decay = 1.f;
+
+    for (int t = t0; t < t1; t += kTok) {
+        const int n = min(kTok, t1 - t);
+        // every warp sums the log-decays: lane i has token i's
+        const float g = lane >= n ? 0.f
+                                  : fmaxf(p.head_decay ? p.g_log[h] : p.g_log[(size_t)bh * p.S + t + lane], kMinLogDecay);
+        float c_in = g;
+#pragma unroll
+        for (int o = 1; o < kTok; o <<= 1) {
+            const float y = __shfl_up_sync(0xffffffffu, c_in, o);
+            if (lane >= o) c_in += y;
+        }
+        const bool blockwise = __all_sync(0xffffffffu, !(fabsf(c_in) > kMostBlock) || lane >= kTok);
+        const float fk = blockwise ? expf(-c_in) : 1.f;
+        const float total = __shfl_sync(0xffffffffu, c_in, kTok - 1);
+        __syncthreads();  // the previous tokens' operands have been read
+        if (warp == 0 && lane < kTok) s_a[lane] = blockwise ? make_float2(1.f, expf(c_in)) : make_float2(expf(g), 1.f);
+        for (int i = tid; i < kTok * kDk; i += blockDim.x) {
+            const int tok = i / kDk, c = i % kDk;
+            const bool in = tok < n && c < Dk;
+            const float f = __shfl_sync(0xffffffffu, fk, tok);  // (a warp's 32 channels are one token's)
+            s_k[tok][c] = in ? f * to_f32(kr[(size_t)(t + tok) * Dk + c]) : 0.f;
+            if (!kStatesOnly) s_q[tok][c] = in ? to_f32(qr[(size_t)(t + tok) * Dk + c]) : 0.f;
+        }
+        for (int i = tid; i < kTok * cols; i += blockDim.x) {
+            const int tok = i / cols, c = i % cols;
+            s_v[tok][c] = tok < n && base + c < Dv ? to_f32(vr[(size_t)(t + tok) * Dv + base + c]) : 0.f;
+        }
+        __syncthreads();
+        if (kStatesOnly) decay *= expf(total);
+        for (int i = 0; i < n; ++i) {
+            const float2 a = s_a[i];
+            if (!blockwise) scale_state(S, a.x);
+            const float4 v4 = *reinterpret_cast<const float4*>(&s_v[i][mine]);
+            const Pair vv[4] = {pair_of(v4.x, v4.x), pair_of(v4.y, v4.y), pair_of(v4.z, v4.z), pair_of(v4.w, v4.w)};
+            Pair o[4] = {};
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                const float4 k4 = *reinterpret_cast<const float4*>(&s_k[i][32 * m + 4 * d]);
+                const Pair kk[2] = {pair_of(k4.x, k4.y), pair_of(k4.z, k4.w)};
+                Pair qq[2] = {};
+                if (!kStatesOnly) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(&s_q[i][32 * m + 4 * d]);
+                    qq[0] = pair_of(q4.x, q4.y);
+                    qq[1] = pair_of(q4.z, q4.w);
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        S[m][u][j] = fma2(kk[u], vv[j], S[m][u][j]);
+                        if (!kStatesOnly) o[j] = fma2(qq[u], S[m][u][j], o[j]);
+                    }
+            }
+            if (!kStatesOnly) {
+                // the sum over the 8 lanes of a column group: each keeps two columns, then one
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = o[j].f.x + o[j].f.y;
+                const bool up = d & 4, up2 = d & 2;
+                const float y0 = (up ? x[2] : x[0]) + __shfl_xor_sync(0xffffffffu, up ? x[0] : x[2], 4);
+                const float y1 = (up ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, up ? x[1] : x[3], 4);
+                float z = (up2 ? y1 : y0) + __shfl_xor_sync(0xffffffffu, up2 ? y0 : y1, 2);
+                z += __shfl_xor_sync(0xffffffffu, z, 1);
+                if (!(d & 1)) s_o[i][mine + (up ? 2 : 0) + (up2 ? 1 : 0)] = a.y * z;
+            }
+        }
+        if (blockwise) scale_state(S, expf(total));
+        if (!kStatesOnly) {
+            __syncthreads();
+            for (int i = tid; i < n * cols; i += blockDim.x) {
+                const int tok = i / cols, c = i % cols;
+                if (base + c < Dv) orow[(size_t)(t + tok) * Dv + base + c] = from_f32<T>(p.scale * s_o[tok][c]);
+            }
+        }
+    }
+    ptx::griddep_launch_dependents();
+
+    float* dst = nullptr;
+    if (kStatesOnly) {
+        dst = split.parts + (seg * heads + bh) * n_state;
+        if (tid == 0 && blockIdx.y == 0) split.decays[seg * heads + bh] = decay;
+    } else if (seg == split.P - 1) {
+        dst = p.state_out + bh * n_state;
+    }
+    if (!dst) return;
+#pragma unroll
+    for (int m = 0; m < MB; ++m)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int r = 32 * m + 4 * d + 2 * u + w, c = base + mine + j;
+                    if (r < Dk && c < Dv) dst[(long long)r * Dv + c] = w ? S[m][u][j].f.y : S[m][u][j].f.x;
+                }
+}
+
+template <typename T, int MB>
+cudaError_t launch_ffma_rows(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream) {
+    // as many columns a CTA as leave every SM two CTAs (its warps share the staged q and k)
+    const long long heads = (long long)p.B * p.Hv;
+    int warps = 8;
+    while (warps > 1 && (16 * (warps / 2) >= p.Dv || heads * s.P * ((p.Dv + 16 * warps - 1) / (16 * warps)) < 2 * sms))
+        warps /= 2;
+    const unsigned slices = (unsigned)((p.Dv + 16 * warps - 1) / (16 * warps));
+    if (s.P > 1) {
+        const cudaError_t e = launch_after(linear_attn_ffma_kernel<T, MB, true>,
+                                           dim3((unsigned)heads, slices, (unsigned)(s.P - 1)), 32 * warps, 0, stream, p, s);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_after(linear_attn_ffma_kernel<T, MB, false>, dim3((unsigned)heads, slices, (unsigned)s.P), 32 * warps, 0,
+                        stream, p, s);
+}
+
+template <typename T>
+cudaError_t launch_ffma(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream) {
+    switch ((p.Dk + 31) / 32) {
+        case 1: return launch_ffma_rows<T, 1>(p, s, sms, stream);
+        case 2: return launch_ffma_rows<T, 2>(p, s, sms, stream);
+        case 3: return launch_ffma_rows<T, 3>(p, s, sms, stream);
+        default: return launch_ffma_rows<T, 4>(p, s, sms, stream);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+constexpr uint32_t kKnownFlags = GDN_FORCE_FFMA | GDN_SINGLE_PASS | GDN_HEAD_DECAY;
+
+gdn_status check_dims(const gdn_dims* d, bool step) {
+    if (!d) return GDN_ERR_NULL;
+    if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+    if (d->flags & ~kKnownFlags) return GDN_ERR_UNSUPPORTED;
+    if (d->B < 0 || d->Hk < 1 || d->Hv < 1 || d->S < 0 || d->Dk < 1 || d->Dv < 1) return GDN_ERR_DIMS;
+    if (d->Dk > kMaxD || d->Dv > kMaxD || d->Hv % d->Hk != 0 || (step && d->S != 1)) return GDN_ERR_DIMS;
+    if (d->B > INT32_MAX || d->Hv > INT32_MAX || d->S > INT32_MAX || d->B * d->Hv > INT32_MAX) return GDN_ERR_DIMS;
+    if (d->B * d->Hv > (int64_t(1) << 48) / (d->S + 1)) return GDN_ERR_DIMS;  // byte counts stay within 64 bits
+    return GDN_OK;
+}
+
+gdn_status check(const void* q, const void* k, const void* v, const float* g_log, const int32_t* lengths, float scale,
+                 const float* state_in, float* state_out, void* out, const gdn_dims* d, bool step, LinearAttn* p) {
+    const gdn_status s = check_dims(d, step);
+    if (s != GDN_OK) return s;
+    if (d->B == 0) {
+        p->B = 0;
+        return GDN_OK;
+    }
+    const bool empty = d->S == 0;
+    if (!state_out || (!empty && (!q || !k || !v || !g_log || !out))) return GDN_ERR_NULL;
+    const uintptr_t el = d->dtype == GDN_BF16 ? 2 : 4;
+    const auto off = [](const void* a, uintptr_t n) { return (reinterpret_cast<uintptr_t>(a) & (n - 1)) != 0; };
+    if (off(q, el) || off(k, el) || off(v, el) || off(out, el) || off(g_log, 4) || off(lengths, 4) || off(state_in, 4) ||
+        off(state_out, 4))
+        return GDN_ERR_ALIGN;
+    const long long qk = d->B * d->Hk * d->S * d->Dk * (long long)el, vo = d->B * d->Hv * d->S * d->Dv * (long long)el;
+    const long long st = d->B * d->Hv * d->Dk * d->Dv * 4;
+    const long long gs = (d->flags & GDN_HEAD_DECAY ? d->Hv : d->B * d->Hv * d->S) * 4;
+    // what is written lies over nothing that is read, but for the state in its own place
+    if (overlap(out, vo, q, qk) || overlap(out, vo, k, qk) || overlap(out, vo, v, vo) || overlap(out, vo, g_log, gs) ||
+        overlap(out, vo, state_in, st) || overlap(out, vo, state_out, st) || overlap(out, vo, lengths, 4 * d->B) ||
+        overlap(state_out, st, q, qk) || overlap(state_out, st, k, qk) || overlap(state_out, st, v, vo) ||
+        overlap(state_out, st, g_log, gs) || overlap(state_out, st, lengths, 4 * d->B) ||
+        overlap_in_part(state_out, st, state_in, st))
+        return GDN_ERR_UNSUPPORTED;
+    *p = LinearAttn{q, k, v, g_log, lengths, state_in, state_out, out, scale, (int)d->B, (int)d->Hk, (int)d->Hv, (int)d->S,
+                    (int)d->Dk, (int)d->Dv, d->dtype == GDN_BF16, (d->flags & GDN_HEAD_DECAY) != 0};
+    return GDN_OK;
+}
+
+bool on_tensor_cores(const LinearAttn& p, const gdn_dims* d) {
+    return !(d->flags & GDN_FORCE_FFMA) && linear_attn_tc_supported(p);
+}
+
+// Segments a sequence is cut into.
+int segments(const gdn_dims* d, bool tc, int sms, int* len) {
+    (void)sms;
+    (void)tc;
+    *len = (int)d->S;
+    return 1;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" {
+
+gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, const float* g_log, const int32_t* lengths,
+                                   float scale, const float* state_in, float* state_out, void* out, const gdn_dims* dims,
+                                   void* workspace, size_t workspace_bytes, gdn_stream_t stream) {
+    gdn::LinearAttn p{};
+    gdn_status s = gdn::check(q, k, v, g_log, lengths, scale, state_in, state_out, out, dims, false, &p);
+    if (s != GDN_OK || p.B == 0) return s;
+    if (!gdn::aligned16(workspace)) return GDN_ERR_ALIGN;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (p.S == 0) {  // no tokens: the state is the one that came in
+        const size_t bytes = (size_t)p.B * p.Hv * p.Dk * p.Dv * sizeof(float);
+        if (state_in == state_out) return GDN_OK;
+        const cudaError_t e = state_in ? cudaMemcpyAsync(state_out, state_in, bytes, cudaMemcpyDeviceToDevice, st)
+                                       : cudaMemsetAsync(state_out, 0, bytes, st);
+        return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    int dev = 0, sms = 0;
+    s = gdn::current_device_sms(&dev, &sms);
+    if (s != GDN_OK) return s;
+    const bool tc = gdn::on_tensor_cores(p, dims);
+    gdn::LinearAttnSplit split{1, p.S, nullptr, nullptr};
+    int len = 0;
+    const int P = gdn::segments(dims, tc, sms, &len);
+    bool own = false;
+    void* ws = nullptr;
+    if (P > 1) {
+        const size_t need = gdn::linear_attn_split_bytes(p, P);
+        if (workspace) {
+            if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
+            ws = workspace;
+        } else if (cudaMallocAsync(&ws, need, st) == cudaSuccess) {
+            own = true;
+        } else {
+            (void)cudaGetLastError();  // one pass instead
+            ws = nullptr;
+        }
+        if (ws) {
+            float* f = static_cast<float*>(ws);
+            split = {P, len, f, f + (size_t)P * p.B * p.Hv * p.Dk * p.Dv};
+        }
+    }
+    if (tc) {
+        int32_t* status = nullptr;
+        s = gdn::status_word_for_current_device(&status);
+        if (s == GDN_OK) s = gdn::launch_linear_attn_tc(p, split, dev, sms, status, st);
+    } else {
+        const cudaError_t e = p.bf16 ? gdn::launch_ffma<__nv_bfloat16>(p, split, sms, st)
+                                     : gdn::launch_ffma<float>(p, split, sms, st);
+        s = e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    }
+    if (s != GDN_OK) (void)cudaGetLastError();
+    if (own && cudaFreeAsync(ws, st) != cudaSuccess && s == GDN_OK) s = GDN_ERR_CUDA;
+    return s;
+}
+
+gdn_status gdn_linear_attn_step(const void* q, const void* k, const void* v, const float* g_log, float scale,
+                                const float* state_in, float* state_out, void* out, const gdn_dims* dims,
+                                gdn_stream_t stream) {
+    gdn::LinearAttn p{};
+    gdn_status s = gdn::check(q, k, v, g_log, nullptr, scale, state_in, state_out, out, dims, true, &p);
+    if (s != GDN_OK || p.B == 0) return s;
+    int dev = 0, sms = 0;
+    s = gdn::current_device_sms(&dev, &sms);
+    if (s != GDN_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = p.bf16 ? gdn::launch_step<__nv_bfloat16>(p, sms, st) : gdn::launch_step<float>(p, sms, st);
+    if (e == cudaSuccess) return GDN_OK;
+    (void)cudaGetLastError();
+    return GDN_ERR_CUDA;
+}
+
+int32_t gdn_linear_attn_segments(const gdn_dims* dims, int32_t sm_count) {
+    if (gdn::check_dims(dims, false) != GDN_OK || sm_count < 1) return 0;
+    int len = 0;
+    gdn::LinearAttn p{};
+    p.Dk = (int)dims->Dk;
+    p.Dv = (int)dims->Dv;
+    p.bf16 = dims->dtype == GDN_BF16;
+    if (dims->B == 0 || dims->S == 0) return 1;
+    return gdn::segments(dims, gdn::on_tensor_cores(p, dims), sm_count, &len);
+}
+
+size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims) {
+    int dev = 0, sms = 0;
+    if (gdn::check_dims(dims, false) != GDN_OK) return 0;
+    if (gdn::current_device_sms(&dev, &sms) != GDN_OK) {
+        (void)cudaGetLastError();
+        return 0;
+    }
+    gdn::LinearAttn p{};
+    p.B = (int)dims->B;
+    p.Hv = (int)dims->Hv;
+    p.Dk = (int)dims->Dk;
+    p.Dv = (int)dims->Dv;
+    return gdn::linear_attn_split_bytes(p, gdn_linear_attn_segments(dims, sms));
+}
+
+}  // extern "C"

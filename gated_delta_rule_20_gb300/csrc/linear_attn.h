@@ -1,0 +1,62 @@
+// linear_attn.h -- declarations shared by the parts of linear attention with a decay for each head
+// (linear_attn.cu: entry points, the single-token step and the fp32 kernel; linear_attn_tc.cu: the
+// tensor-core kernel).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gdn.h"
+
+namespace gdn {
+
+// One call's arguments after host-side validation.
+struct LinearAttn {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g_log;      // [B, Hv, S], or [Hv] with head_decay
+    const int32_t* lengths;  // [B], or null: S tokens each
+    const float* state_in;   // null: zeros
+    float* state_out;
+    void* out;
+    float scale;
+    int B, Hk, Hv, S, Dk, Dv;
+    bool bf16, head_decay;
+};
+
+// Least log-decay that is told from the others: e^-100 = 3.7e-44 is (nearly) the least fp32 number, so that
+// nothing is left of a state behind it, and sums of a chunk's log-decays stay finite (a g_log of -inf
+// starts a new sequence).
+constexpr float kMinLogDecay = -100.f;
+
+// Segments of every sequence (P = 1: whole).  Segment j holds tokens [j len, (j + 1) len) of S.  The runs of
+// segments 0 .. P - 2 from zero (segment 0: from state_in) come first and leave their end states X_j in
+// `parts` [P][B Hv][Dk Dv] and their decays F_j in `decays` [P][B Hv]; the start state of segment j is then
+// X_{j-1} + F_{j-1} (X_{j-2} + F_{j-2} (...)).  Slot P - 1 of `parts` keeps a copy of state_in, since segment
+// P - 1 may write state_out in its place while segment 0 has not read it.
+struct LinearAttnSplit {
+    int P, len;
+    float* parts;
+    float* decays;
+};
+inline size_t linear_attn_split_bytes(const LinearAttn& p, int P) {
+    return P <= 1 ? 0 : (size_t)P * p.B * p.Hv * ((size_t)p.Dk * p.Dv + 1) * sizeof(float);
+}
+
+// bf16 with head dims of whole 16-byte rows, on aligned pointers.
+bool linear_attn_tc_supported(const LinearAttn& p);
+// Both passes of a split, or the one of P = 1.
+gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
+                                 cudaStream_t stream);
+
+// The start state of segment j at element i of head bh (`stride` = B Hv, `n` = Dk Dv).
+__device__ __forceinline__ float linear_attn_start(const LinearAttnSplit& s, int j, long long bh, long long heads,
+                                                   long long n, long long i) {
+    float x = s.parts[bh * n + i];
+    for (int m = 1; m < j; ++m) x = fmaf(s.decays[m * heads + bh], x, s.parts[(m * heads + bh) * n + i]);
+    return x;
+}
+
+}  // namespace gdn

@@ -1,0 +1,321 @@
+// rotary.cu -- rotary positions of q and k.
+//
+//     theta = position * inv_freq[i]:   (a, b) -> amplitude (a cos - b sin, b cos + a sin)
+//
+// on channel pairs (i, i + R/2) or (2i, 2i + 1) of the first R channels; the rest is copied.
+//
+// The angle is kept in turns, as a 64-bit binary fraction of one: f = inv_freq / 2 pi mod 1, and position * f wraps
+// around as whole turns do.  The product is exact, so that far positions keep the accuracy of near ones: the angle's error is
+// 2^-64 of a turn a position, from f, where an fp32 product loses 2^-24 of the angle itself (a radian at position 10^7).
+//
+// Bound by bytes: a row is read and written once.  A CTA takes a few tokens and all (or some) of their heads; it first
+// makes the tokens' sines and cosines in shared memory, once for all heads, then streams 16-byte pieces.
+#include <cuda_bf16.h>
+
+#include "gdn_device.cuh"
+#include "gdn_internal.h"
+#include "sm100_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 16;      // of a CTA
+constexpr int kTableFloats = 8192;  // of its sines and cosines
+
+struct RotaryTensor {
+    const void* x;
+    void* y;
+    int64_t xs[3], ys[3];  // strides in elements: batch, head, token
+    int heads;
+};
+struct RotaryArgs {
+    RotaryTensor t[2];  // q, k
+    const double* inv_freq;
+    const void* positions;  // null: first + token
+    long long pos_batch;    // its batch stride
+    long long first;
+    int B, S, R, D;
+    int tokens;        // of a CTA
+    int heads_cta;     // of a CTA, q's and k's counted through
+    int rot_slots;     // pieces of a head that are turned
+    int slots;         // and all of them (the rest are copied)
+    bool pos32, inverse;
+    float amplitude;
+};
+
+// inv_freq / 2 pi mod 1 in units of 2^-64 of a turn.  2^64 / (2 pi) = kInv2Pi / 4 with kInv2Pi = 2^66 / (2 pi)
+// rounded down; the double's 53 bits are multiplied as integers (a double's units are few on this chip).
+constexpr unsigned long long kInv2Pi = 0xA2F9836E4E441529ull;  // 2 / pi in units of 2^-64
+__device__ __forceinline__ unsigned long long turns_of(double f) {
+    const unsigned long long bits = (unsigned long long)__double_as_longlong(f);
+    const int e = (int)((bits >> 52) & 0x7ff);
+    if (e == 0 || e == 0x7ff) return 0;  // zero (and below 2^-1022); infinities and NaN turn nothing
+    // f = m 2^(e - 1023 - 63), m in [2^63, 2^64);  turns = f (2 / pi) / 4
+    const unsigned long long m = (bits << 11) | (1ull << 63);
+    const unsigned long long hi = __umul64hi(m, kInv2Pi), lo = m * kInv2Pi;  // m (2 / pi) 2^64
+    const int sh = e - 1024;  // turns 2^64 = (hi : lo) 2^(e - 1023 - 63 - 2), its integer part from hi on at e = 1024
+    unsigned long long t;
+    if (sh >= 0)
+        t = sh < 64 ? (sh ? (hi << sh) | (lo >> (64 - sh)) : hi) : sh < 128 ? lo << (sh - 64) : 0;
+    else
+        t = sh > -64 ? hi >> -sh : 0;
+    return (long long)bits < 0 ? 0ull - t : t;
+}
+
+template <typename T, int V>
+struct Piece {
+    T e[V];
+};
+template <typename T, int V>
+struct alignas(sizeof(T) * V) PieceAligned : Piece<T, V> {};
+
+// One 2 V-element pair of pieces (half layout), or one piece (interleaved pairs, copies).
+// V elements an access; interleaved pairs need two elements a thread, which V = 1 takes in two accesses.
+template <typename T, int V, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
+    using P = PieceAligned<T, V>;
+    constexpr int W = kInterleaved && V == 1 ? 2 : V;  // elements of a piece
+    constexpr int kUnroll = 4;
+    extern __shared__ __align__(16) float s_cs[];  // [tokens][R / 2] cosines, then sines
+    const int tid = threadIdx.x, half = a.R / 2;
+    const int per_seq = (a.S + a.tokens - 1) / a.tokens;
+    const int b = blockIdx.x / per_seq, s0 = (blockIdx.x - b * per_seq) * a.tokens;
+    const int n = min(a.tokens, a.S - s0);
+    float* s_cos = s_cs;
+    float* s_sin = s_cs + a.tokens * half;
+    ptx::griddep_wait();
+    for (int i = tid; i < n * half; i += kThreads) {
+        const int tok = i / half, f = i - tok * half;
+        long long pos = a.first + s0 + tok;
+        if (a.positions) {
+            const long long at = b * a.pos_batch + s0 + tok;
+            pos = a.pos32 ? (long long)static_cast<const int32_t*>(a.positions)[at]
+                          : static_cast<const long long*>(a.positions)[at];
+        }
+        const long long angle = (long long)((unsigned long long)pos * turns_of(a.inv_freq[f]));
+        float sn, cs;
+        sincospif(__ll2float_rn(angle) * 0x1p-63f, &sn, &cs);  // half turns in [-1, 1]
+        s_cos[i] = a.amplitude * cs;
+        s_sin[i] = a.amplitude * (a.inverse ? -sn : sn);
+    }
+    __syncthreads();
+
+    const int h_lo = blockIdx.y * a.heads_cta, h_n = min(a.heads_cta, a.t[0].heads + a.t[1].heads - h_lo);
+    const int rows = h_n * n;  // (head, token), tokens fastest
+    // this thread's (row, slot), moved on by kThreads pieces at a time
+    const int step_row = kThreads / a.slots, step_slot = kThreads - step_row * a.slots;
+    int row = tid / a.slots, slot = tid - row * a.slots;
+    while (row < rows) {
+        P x[kUnroll][kInterleaved ? (W / V) : 2];
+        T* dst[kUnroll];
+        int tk[kUnroll], sl[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            sl[u] = -1;
+            if (row < rows) {
+                const int hh = row / n, tok = row - hh * n;
+                int h = h_lo + hh;
+                const int w = h >= a.t[0].heads;
+                if (w) h -= a.t[0].heads;
+                const RotaryTensor& t = a.t[w];
+                const long long s = s0 + tok;
+                int c;  // first channel
+                if (slot < a.rot_slots) c = slot * W;
+                else c = a.R + (slot - a.rot_slots) * V;
+                const T* src = static_cast<const T*>(t.x) + b * t.xs[0] + h * t.xs[1] + s * t.xs[2] + c;
+                dst[u] = static_cast<T*>(t.y) + b * t.ys[0] + h * t.ys[1] + s * t.ys[2] + c;
+                sl[u] = slot;
+                tk[u] = tok;
+                x[u][0] = *reinterpret_cast<const P*>(src);
+                if (slot < a.rot_slots) {
+                    if (kInterleaved) {
+                        if (W != V) x[u][W / V - 1] = *reinterpret_cast<const P*>(src + 1);
+                    } else {
+                        x[u][1 % (kInterleaved ? (W / V) : 2)] = *reinterpret_cast<const P*>(src + half);
+                    }
+                }
+                slot += step_slot;
+                row += step_row;
+                if (slot >= a.slots) {
+                    slot -= a.slots;
+                    ++row;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (sl[u] < 0) continue;
+            if (sl[u] < a.rot_slots) {
+                if (kInterleaved) {
+                    const float* cs = s_cos + tk[u] * half + sl[u] * (W / 2);
+                    const float* sn = s_sin + tk[u] * half + sl[u] * (W / 2);
+#pragma unroll
+                    for (int i = 0; i < W / 2; ++i) {
+                        T& ea = x[u][0].e[V == 1 ? 0 : 2 * i];
+                        T& eb = x[u][W / V - 1].e[V == 1 ? 0 : 2 * i + 1];
+                        const float fa = to_f32(ea), fb = to_f32(eb);
+                        ea = from_f32<T>(fa * cs[i] - fb * sn[i]);
+                        eb = from_f32<T>(fb * cs[i] + fa * sn[i]);
+                    }
+                    if (W != V) *reinterpret_cast<P*>(dst[u] + 1) = x[u][W / V - 1];
+                } else {
+                    const float* cs = s_cos + tk[u] * half + sl[u] * V;
+                    const float* sn = s_sin + tk[u] * half + sl[u] * V;
+                    constexpr int k1 = kInterleaved ? 0 : 1;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float fa = to_f32(x[u][0].e[i]), fb = to_f32(x[u][k1].e[i]);
+                        x[u][0].e[i] = from_f32<T>(fa * cs[i] - fb * sn[i]);
+                        x[u][k1].e[i] = from_f32<T>(fb * cs[i] + fa * sn[i]);
+                    }
+                    *reinterpret_cast<P*>(dst[u] + half) = x[u][k1];
+                }
+            }
+            *reinterpret_cast<P*>(dst[u]) = x[u][0];
+        }
+    }
+    ptx::griddep_launch_dependents();
+}
+
+template <typename T, int V, bool kInterleaved>
+cudaError_t launch(RotaryArgs a, int sms, cudaStream_t stream) {
+    constexpr int W = kInterleaved && V == 1 ? 2 : V;
+    a.rot_slots = kInterleaved ? a.R / W : a.R / 2 / V;
+    const bool copies = a.t[0].x != a.t[0].y || (a.t[1].heads && a.t[1].x != a.t[1].y);
+    a.slots = a.rot_slots + (copies ? (a.D - a.R) / V : 0);
+    // tokens of a CTA: many, so that a sine serves all heads of a wave of CTAs' worth of work; fewer where
+    // they would leave SMs without a CTA, and then the heads are shared out too
+    const int heads = a.t[0].heads + a.t[1].heads, half = a.R / 2;
+    int tokens = kMaxTokens;
+    while (tokens > 1 && (tokens * half * 2 > kTableFloats || (long long)a.B * ((a.S + tokens - 1) / tokens) < 2 * sms))
+        tokens /= 2;
+    a.tokens = tokens;
+    const long long ctas = (long long)a.B * ((a.S + tokens - 1) / tokens);
+    int split = 1;
+    while (ctas * split < sms && (long long)heads * tokens * a.slots > (long long)split * kThreads) split *= 2;
+    a.heads_cta = (heads + split - 1) / split;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((heads + a.heads_cta - 1) / a.heads_cta));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)tokens * half * 2 * sizeof(float);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rotary_kernel<T, V, kInterleaved>, a);
+}
+
+template <typename T, bool kInterleaved>
+cudaError_t launch_width(const RotaryArgs& a, int v, int sms, cudaStream_t stream) {
+    if constexpr (sizeof(T) == 2)
+        if (v == 8) return launch<T, 8, kInterleaved>(a, sms, stream);
+    if (v >= 4) return launch<T, 4, kInterleaved>(a, sms, stream);
+    if (v == 2) return launch<T, 2, kInterleaved>(a, sms, stream);
+    return launch<T, 1, kInterleaved>(a, sms, stream);
+}
+
+// Elements from the lowest to behind the highest that the strides reach.
+long long extent(const gdn_rotary_dims* d, int64_t heads, const int64_t* st) {
+    return (d->B - 1) * st[0] + (heads - 1) * st[1] + (d->S - 1) * st[2] + d->D;
+}
+
+// Whether rows of D elements at these strides lie over one another: each stride has to pass all that the
+// smaller ones reach.
+bool rows_meet(const int64_t* sizes, const int64_t* st, int64_t D) {
+    bool done[3] = {};
+    long long reach = D;
+    for (int n = 0; n < 3; ++n) {
+        int least = -1;
+        for (int j = 0; j < 3; ++j)
+            if (!done[j] && sizes[j] > 1 && (least < 0 || st[j] < st[least])) least = j;
+        if (least < 0) return false;
+        if (st[least] < reach) return true;
+        reach += (sizes[least] - 1) * st[least];
+        done[least] = true;
+    }
+    return false;
+}
+
+}  // namespace
+}  // namespace gdn
+
+extern "C" gdn_status gdn_rotary(const void* q, const void* k, const double* inv_freq, const void* positions, void* q_out,
+                                 void* k_out, const gdn_rotary_dims* d, gdn_stream_t stream) {
+    using namespace gdn;
+    if (!d) return GDN_ERR_NULL;
+    if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
+    constexpr uint32_t kFlags = GDN_ROTARY_INTERLEAVED | GDN_ROTARY_INVERSE | GDN_ROTARY_POSITIONS_I32;
+    if (d->flags & ~kFlags) return GDN_ERR_UNSUPPORTED;
+    if (d->B < 0 || d->S < 0 || d->Hq < 0 || d->Hk < 0 || d->D < 1 || d->R < 2 || d->R > d->D || d->R % 2 ||
+        d->D > GDN_ROTARY_MAX_D || d->Hq > 65536 || d->Hk > 65536)
+        return GDN_ERR_DIMS;
+    if (d->B > INT32_MAX || d->S > INT32_MAX || d->B * d->S > INT32_MAX) return GDN_ERR_DIMS;
+    if (d->B == 0 || d->S == 0 || d->Hq + d->Hk == 0) return GDN_OK;
+    if (!inv_freq || (d->Hq && (!q || !q_out)) || (d->Hk && (!k || !k_out))) return GDN_ERR_NULL;
+    const int el = d->dtype == GDN_BF16 ? 2 : 4;
+    const bool i32 = (d->flags & GDN_ROTARY_POSITIONS_I32) != 0;
+    if ((reinterpret_cast<uintptr_t>(inv_freq) & 7) || (reinterpret_cast<uintptr_t>(positions) & (i32 ? 3 : 7)))
+        return GDN_ERR_ALIGN;
+    RotaryArgs a{};
+    const bool inter = (d->flags & GDN_ROTARY_INTERLEAVED) != 0;
+    // elements of an access: the most that the pointers, the strides and the channel counts are multiples of
+    uint64_t odd = (inter ? (uint64_t)d->R : (uint64_t)d->R / 2) | (uint64_t)(d->D - d->R);
+    const void* xs[2] = {q, k};
+    void* ys[2] = {q_out, k_out};
+    const int64_t* xst[2] = {d->q_strides, d->k_strides};
+    const int64_t* yst[2] = {d->q_out_strides, d->k_out_strides};
+    const int64_t heads[2] = {d->Hq, d->Hk};
+    for (int i = 0; i < 2; ++i) {
+        a.t[i].heads = (int)heads[i];
+        if (!heads[i]) continue;
+        const uintptr_t px = reinterpret_cast<uintptr_t>(xs[i]), py = reinterpret_cast<uintptr_t>(ys[i]);
+        if ((px | py) & (el - 1)) return GDN_ERR_ALIGN;
+        a.t[i].x = xs[i];
+        a.t[i].y = ys[i];
+        const int64_t sizes[3] = {d->B, heads[i], d->S};
+        bool same = true;
+        for (int j = 0; j < 3; ++j) {
+            constexpr int64_t kMost = int64_t(1) << 40;  // (what a tensor spans is below 2^31 2^40 elements a dim)
+            if (xst[i][j] < 0 || yst[i][j] < 0 || (sizes[j] > 1 && (xst[i][j] > kMost || yst[i][j] > kMost)))
+                return GDN_ERR_DIMS;
+            const bool used = sizes[j] > 1;  // a stride that is never taken may be anything
+            a.t[i].xs[j] = used ? xst[i][j] : 0;
+            a.t[i].ys[j] = used ? yst[i][j] : 0;
+            odd |= (uint64_t)a.t[i].xs[j] | (uint64_t)a.t[i].ys[j];
+            same = same && a.t[i].xs[j] == a.t[i].ys[j];
+        }
+        if (rows_meet(sizes, a.t[i].ys, d->D)) return GDN_ERR_DIMS;
+        odd |= (px | py) / el;
+        const long long nx = extent(d, heads[i], a.t[i].xs) * el, ny = extent(d, heads[i], a.t[i].ys) * el;
+        if (overlap(xs[i], nx, ys[i], ny) && !(px == py && same)) return GDN_ERR_UNSUPPORTED;
+        if (overlap(ys[i], ny, inv_freq, d->R * 4)) return GDN_ERR_UNSUPPORTED;
+    }
+    int v = 16 / el;
+    while (v > 1 && odd % v) v /= 2;
+    a.inv_freq = inv_freq;
+    a.positions = positions;
+    a.pos_batch = d->position_stride;
+    a.first = d->first_position;
+    a.B = (int)d->B;
+    a.S = (int)d->S;
+    a.R = (int)d->R;
+    a.D = (int)d->D;
+    a.pos32 = i32;
+    a.inverse = (d->flags & GDN_ROTARY_INVERSE) != 0;
+    a.amplitude = d->amplitude;
+    int dev = 0, sms = 0;
+    const gdn_status s = current_device_sms(&dev, &sms);
+    if (s != GDN_OK) return s;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (d->dtype == GDN_BF16)
+        e = inter ? launch_width<__nv_bfloat16, true>(a, v, sms, st) : launch_width<__nv_bfloat16, false>(a, v, sms, st);
+    else
+        e = inter ? launch_width<float, true>(a, v, sms, st) : launch_width<float, false>(a, v, sms, st);
+    if (e == cudaSuccess) return GDN_OK;
+    (void)cudaGetLastError();
+    return GDN_ERR_CUDA;
+}

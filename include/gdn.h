@@ -70,7 +70,9 @@ enum {
     GDN_FORCE_FFMA = 1u << 1,
     /* Never split a sequence into segments (see gdn_prefill): one pass over
      * every sequence, whatever the SM count, so results do not depend on it. */
-    GDN_SINGLE_PASS = 1u << 2
+    GDN_SINGLE_PASS = 1u << 2,
+    /* Linear attention only (gdn_linear_attn_*): g_log is [Hv], one decay a head for all tokens. */
+    GDN_HEAD_DECAY = 1u << 3
 };
 
 /*
@@ -479,6 +481,101 @@ typedef struct {
  * them, sm_count < 1 GDN_ERR_DIMS.  Host only. */
 gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_dims* dims, int32_t sm_count,
                            gdn_linear_plan_info* info);
+
+/*
+ * Linear attention with a decay for each head: the recurrence without the delta rule's correction, of layers
+ * that stand beside the gated delta rule's, with the same heads and the same state:
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,     o_t = scale * S_t^T q_t
+ *
+ * gdn_linear_attn_prefill -- whole prompts.
+ *   q, k        [B, Hk, S, Dk]  compute dtype (need not be normalised)
+ *   v           [B, Hv, S, Dv]  compute dtype
+ *   g_log       [B, Hv, S] fp32 log-decays, or [Hv] under GDN_HEAD_DECAY; <= 0 (not checked).  Values below -100
+ *               count as -100 (e^-100 is 3.7e-44): -infinity drops what came before the token
+ *   lengths     [B] int32 or NULL: sequence b has lengths[b] tokens (below 0: 0, above S: S).  Rows of q, k, v
+ *               and g_log behind them have no influence, whatever they hold, and rows of out are left as they were
+ *   state_in    [B, Hv, Dk, Dv] fp32, Dv contiguous, or NULL: zeros
+ *   state_out   the same, receives the state behind the last token; may be state_in
+ *   out         [B, Hv, S, Dv]  compute dtype
+ *   dims        gdn_dims; flags: GDN_HEAD_DECAY, GDN_FORCE_FFMA, GDN_SINGLE_PASS.  S = 0 copies the state
+ *   workspace   device memory of workspace_bytes >= gdn_linear_attn_workspace_bytes(dims) bytes, 16-byte
+ *               aligned, not touched by anything else until the call's work on `stream` has finished; NULL: the call
+ *               takes what it needs with cudaMallocAsync on `stream`, and runs one pass where that fails.  Too small:
+ *               GDN_ERR_WORKSPACE
+ * Pointers aligned to their element; out and state_out may not share memory with an input or one
+ * another, but for state_out in state_in's place (GDN_ERR_UNSUPPORTED).
+ * bf16 with Dk and Dv multiples of 8 and q, k, v and out on 16 bytes runs on the tensor cores, in chunks of 128
+ * tokens: products of bf16 operands with fp32 sums; the decayed scores and the copy of the state that the queries
+ * read are rounded to bf16 once (the outputs' own type).  The state itself is fp32 and is updated with
+ * three bf16 parts of exp(.) v, which add up to its 24 bits.  What a chunk's decays leave of the state is taken as
+ * e^-64 of it at least in the chunk's outputs (1.6e-28).  fp32, and other head dims, run the recurrence on the FMA units.
+ * Few sequences of many tokens are cut into segments that run at once (gdn_linear_attn_segments; GDN_SINGLE_PASS:
+ * never): a first launch runs all but the last from zero and keeps their states and decays, the second starts each segment
+ * from the state that they add up to.  Results of a split agree with one pass's to within rounding.
+ */
+gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, const float* g_log,
+                                   const int32_t* lengths, float scale, const float* state_in, float* state_out,
+                                   void* out, const gdn_dims* dims, void* workspace, size_t workspace_bytes,
+                                   gdn_stream_t stream);
+
+/* Segments that gdn_linear_attn_prefill cuts each sequence into on a device with sm_count SMs (1: none); 0 for
+ * invalid dims or sm_count < 1.  Host only. */
+int32_t gdn_linear_attn_segments(const gdn_dims* dims, int32_t sm_count);
+
+/* Device scratch of gdn_linear_attn_prefill on the current device: a state a segment and head; 0 for one pass,
+ * for invalid dims and without a device.  Host only. */
+size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims);
+
+/*
+ * gdn_linear_attn_step -- one token of every sequence (dims->S == 1, else GDN_ERR_DIMS): the arguments of
+ * gdn_linear_attn_prefill, in fp32 throughout.  The state is read once and written once, in one launch.
+ */
+gdn_status gdn_linear_attn_step(const void* q, const void* k, const void* v, const float* g_log, float scale,
+                                const float* state_in, float* state_out, void* out, const gdn_dims* dims,
+                                gdn_stream_t stream);
+
+enum {
+    /* Channel pairs (2i, 2i + 1) instead of (i, i + R/2). */
+    GDN_ROTARY_INTERLEAVED = 1u << 0,
+    /* Turns back (by -theta): the transpose, so the gradient too. */
+    GDN_ROTARY_INVERSE = 1u << 1,
+    /* positions are int32 instead of int64. */
+    GDN_ROTARY_POSITIONS_I32 = 1u << 2
+};
+#define GDN_ROTARY_MAX_D 4096
+
+/*
+ * B, S >= 0 (B S < 2^31); Hq, Hk in [0, 65536] heads of q and of k (0: that tensor is not there); head dim
+ * 1 <= D <= GDN_ROTARY_MAX_D, of which the first R are turned (even, 2 <= R <= D).  Strides in elements over
+ * (batch, head, token), >= 0; channels are contiguous.
+ */
+typedef struct {
+    int64_t B, Hq, Hk, S, D, R;
+    int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];
+    int64_t position_stride;  /* of positions over the batch, in elements (0: one row for all) */
+    int64_t first_position;   /* where positions is NULL: token s is at first_position + s */
+    int32_t dtype;            /* GDN_F32 or GDN_BF16 */
+    uint32_t flags;           /* GDN_ROTARY_* */
+    float amplitude;          /* what turned channels are multiplied by (1, or a long-context scaling's factor) */
+} gdn_rotary_dims;
+
+/*
+ * gdn_rotary -- rotary positions of q and k in one launch: with theta = position * inv_freq[i],
+ *     y_a = amplitude (x_a cos theta - x_b sin theta),   y_b = amplitude (x_b cos theta + x_a sin theta)
+ * for the channel pairs (a, b) = (i, i + R/2), or (2i, 2i + 1), i < R/2; channels from R on are copied.
+ *   q, q_out   [B, Hq, S, D] in dtype at their strides (views into packed rows, head-major or token-major);
+ *              q_out may be q at the same strides, and otherwise may not share memory with it
+ *              (GDN_ERR_UNSUPPORTED); its rows may not lie over one another (GDN_ERR_DIMS).  k, k_out likewise
+ *   inv_freq   [R/2] fp64, radians a position (fp32 ones of a model: widened)
+ *   positions  int64 (or int32) [B, S], tokens contiguous, or NULL
+ * theta is taken mod one turn exactly (2^-64 of a turn a position), so that its accuracy does not fall with
+ * the position; cos and sin in fp32, one rounding to dtype.  Infinite and NaN frequencies turn nothing.
+ * Pointers aligned to their element; accesses are as wide, up to 16 bytes, as every pointer, stride, R/2 (R for
+ * GDN_ROTARY_INTERLEAVED) and D - R are multiples of.
+ */
+gdn_status gdn_rotary(const void* q, const void* k, const double* inv_freq, const void* positions, void* q_out,
+                      void* k_out, const gdn_rotary_dims* dims, gdn_stream_t stream);
 
 /* Device scratch a prefill with these dims needs on the current device: the
  * segment states, maps and identity-start outputs of a split (see gdn_prefill;
