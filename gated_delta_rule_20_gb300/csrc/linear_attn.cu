@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kStepThreads) linear_attn_step_kernel(LinearAt
         s_q[tid] = to_f32(static_cast<const T*>(p.q)[row]);
         s_k[tid] = to_f32(static_cast<const T*>(p.k)[row]);
     }
-    const float a = expf(fmaxf(p.g_log[p.head_decay ? h : bh], kMinLogDecay));
+    const float a = expf(least_decay(p.g_log[p.head_decay ? h : bh]));
     __syncthreads();
 
     float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -244,8 +244,7 @@ __global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, 
     for (int t = t0; t < t1; t += kTok) {
         const int n = min(kTok, t1 - t);
         // every warp sums the log-decays: lane i has token i's
-        const float g = lane >= n ? 0.f
-                                  : fmaxf(p.head_decay ? p.g_log[h] : p.g_log[(size_t)bh * p.S + t + lane], kMinLogDecay);
+        const float g = lane >= n ? 0.f : least_decay(p.g_log[p.head_decay ? h : (size_t)bh * p.S + t + lane]);
         float c_in = g;
 #pragma unroll
         for (int o = 1; o < kTok; o <<= 1) {

@@ -30,6 +30,7 @@ struct LinearAttn {
 // nothing is left of a state behind it, and sums of a chunk's log-decays stay finite (a g_log of -inf
 // starts a new sequence).
 constexpr float kMinLogDecay = -100.f;
+__device__ __forceinline__ float least_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // (NaN stays)
 
 // Segments of every sequence (P = 1: whole).  Segment j holds tokens [j len, (j + 1) len) of S.  The runs of
 // segments 0 .. P - 2 from zero (segment 0: from state_in) come first and leave their end states X_j in
