@@ -6,9 +6,11 @@
 //
 // Products, 128 x 128 x 128 each (Dk = Dv = 128), all issued by one thread in this order a chunk:
 //   QK   scores[i, j]        A = Q, B = K                  (shared memory)
-//   QS   O = Q S             A = Q, B = S^T in bf16        (shared memory)
 //   KV   X[dv, dk] = (e^. V)^T K in three parts: A = part of (e^. V)^T (TMEM), B = K
+//   QS   O = Q S             A = Q, B = S^T in bf16        (shared memory)
 //   PV   O += P V            A = P (TMEM, over the scores), B = V
+// so that while KV and QS run (two thirds of the products' time) the scores become P, and while QK and KV run the
+// outputs before are written and the state is rounded.
 // The state is fp32: X is added to it on the FMA units, and e^. v is cut into three bf16 parts that add up to its 24
 // bits, so that the state is as exact as an fp32 recurrence's.  O sums both terms in one accumulator: a row is kept divided
 // by e^{m_i}, m_i = max(c_i, -64), which is 1 in front of Q S, and its scores are e^{c_i - c_j - m_i}: at most
@@ -19,7 +21,7 @@
 // a score off the diagonal blocks takes e^{c_i - R} e^{R - c_j}, R the end of j's block, a factor of its row and one of its
 // column, and only the 32 x 32 diagonal blocks take an exponential an element.
 //
-// Roles (768 threads): 4 warps turn scores into P, 8 hold the state (a thread: 64 rows of a column dv in fp32 registers), 4
+// Roles (896 threads): 4 warps turn scores into P, 8 hold the state (a thread: 64 rows of a column dv in fp32 registers), 8
 // make the parts of e^. V, 4 write the outputs; one warp each for TMA, the products and the decays.  A CTA walks its
 // sequences' chunks without a break: the pipeline runs through from one sequence to the next.
 #include <cuda_bf16.h>
@@ -37,17 +39,17 @@ namespace {
 using namespace ptx;
 
 constexpr int kC = 128;  // tokens of a chunk
-constexpr int kThreads = 768;
+constexpr int kThreads = 896;
 constexpr uint32_t kHalf = 16384, kTile = 2 * kHalf;  // 128 rows x 64 channels, and 128
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffS = 6 * kTile, kOffSmall = 7 * kTile;
-constexpr int kSub = 16, kSlots = 5;  // tokens a slot of the parts of e^. V, and slots
-// TMEM columns: scores (P over their first 64), O, X, the parts' slots of 3 x 8
-constexpr uint32_t kColP = 0, kColO = 128, kColX = 256, kColV = 384, kSlotCols = 24;
+constexpr int kSub = 32, kSlots = 2;  // tokens a slot of the parts of e^. V, and slots
+// TMEM columns: scores (P over their first 64), O, X, the parts' slots of 3 x 16
+constexpr uint32_t kColP = 0, kColO = 128, kColX = 256, kColV = 384, kSlotCols = 48;
 constexpr float kMinRow = -64.f * kLog2e;  // least m_i, in powers of two
 
 // Registers a thread of each role; what the block is launched with covers their sum (launch checks it).
-constexpr int kRegsP = 80, kRegsS = 120, kRegsV = 64, kRegsO = 48, kRegsCtl = 48;
-constexpr int kRegsSum = (kRegsP + 2 * kRegsS + kRegsV + kRegsO + kRegsCtl) * 128;
+constexpr int kRegsP = 72, kRegsS = 112, kRegsV = 56, kRegsO = 48, kRegsCtl = 48;
+constexpr int kRegsSum = (kRegsP + 2 * kRegsS + 2 * kRegsV + kRegsO + kRegsCtl) * 128;
 
 struct Small {
     float c[2][kC];      // sums of log2-decays within blocks of 32
@@ -57,7 +59,7 @@ struct Small {
     float total[2];      // e^(the chunk's)
     uint64_t kvfull[2], kvfree[2], qfull[2], qfree[2], decfull[2], decfree[2];
     uint64_t vfull[kSlots], vfree[kSlots];
-    uint64_t sfull, xfull, qkfull, pfull, ofull, ofree, drain;
+    uint64_t sfull, sfree, xfull, xfree, qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
     int abort;
 };
@@ -89,20 +91,20 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
-// Waits as ptx::mbar_wait_or_abort's, but inline: a kernel that shares out its registers cannot call functions.
+// Waits as ptx::mbar_wait_or_abort's, but inline (a kernel that shares out its registers cannot call functions), and
+// with the limit of about a second in clocks: reading the global timer takes longer than most of these waits.
+constexpr long long kWaitClocks = 2000000000ll;
 __device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort) {
     if (mbar_try_wait(bar, parity)) return true;
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 15u) == 0) {
-            if (abort && *abort) return false;
-            const uint64_t t = globaltimer_ns();
-            if (t0 == 0) t0 = t;
-            if (t - t0 > 1000000000ull) {
-                if (abort) *abort = 1;
-                return false;
-            }
+    const long long t0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (abort && *abort) return false;
+        if (clock64() - t0 > kWaitClocks) {
+            if (abort) *abort = 1;
+            return false;
         }
     }
 }
@@ -111,6 +113,29 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volati
 }
 // What is in flight when a role gives up: waited for with the time limit alone.
 __device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) { (void)wait_inline(bar, parity, nullptr); }
+
+// The two bf16 values in m, times d, as the sum of three bf16 values each: an fp32 product's 24 bits cut off 8 at a
+// time.  The cut parts' differences are exact.
+__device__ __forceinline__ void three_parts(uint32_t m, float2 d, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+    constexpr uint32_t kCut = 0xffff0000u;
+    const auto pair = [](uint32_t lo, uint32_t hi) { return (unsigned long long)hi << 32 | lo; };
+    const unsigned long long dd = pair(__float_as_uint(d.x), __float_as_uint(d.y));
+    unsigned long long x = pair(m << 16, m & kCut), r, r2;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(x), "l"(dd));
+    uint32_t a = (uint32_t)x, b = (uint32_t)(x >> 32);
+    p0 = __byte_perm(a, b, 0x7632);
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(pair(a & kCut, b & kCut)));
+    a = (uint32_t)r, b = (uint32_t)(r >> 32);
+    p1 = __byte_perm(a, b, 0x7632);
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r2) : "l"(r), "l"(pair(a & kCut, b & kCut)));
+    p2 = __byte_perm((uint32_t)r2, (uint32_t)(r2 >> 32), 0x7632);
+}
+
+__device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
 
 struct Chunks {  // the walk over a CTA's items: (segment, head), and the chunks of each
     int seg, b, h, bh, t0, t1, n;
@@ -130,12 +155,66 @@ __device__ __forceinline__ Chunks chunks_of(const LinearAttn& p, const LinearAtt
     return c;
 }
 
+// Descriptors in two words: an offset within shared memory is added to the low one (no carry leaves its address field).
+struct Desc {
+    uint32_t lo, hi;
+};
+__device__ __forceinline__ Desc desc_of(uint32_t saddr, uint32_t lbo) {
+    const uint64_t d = make_sdesc(saddr, lbo, 1024);
+    return Desc{(uint32_t)d, (uint32_t)(d >> 32)};
+}
+// One 128 x N x 16 step of D (+)= A B^T, A in shared memory or in tensor memory.
+template <bool kAdd>
+__device__ __forceinline__ void step_ss(uint32_t d, Desc a, uint32_t a_at, Desc b, uint32_t b_at, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+        "r"(a.lo + (a_at >> 4)), "r"(a.hi), "r"(b.lo + (b_at >> 4)), "r"(b.hi), "r"(idesc), "n"(kAdd ? 1 : 0)
+        : "memory");
+}
+template <bool kAdd>
+__device__ __forceinline__ void step_ts(uint32_t d, uint32_t a, Desc b, uint32_t b_at, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo + (b_at >> 4)), "r"(b.hi), "r"(idesc), "n"(kAdd ? 1 : 0)
+        : "memory");
+}
+// D = A B^T over `ksteps` steps of 16 along the rows of two tiles.  All eight steps of 128 channels run without a branch
+// between them: products issued so follow one another every 66 cycles, their own time, and with a test or a
+// descriptor made anew before each every 140.
+__device__ __forceinline__ void product_rows(uint32_t d, Desc a, Desc b, uint32_t idesc, int ksteps) {
+    step_ss<false>(d, a, 0, b, 0, idesc);
+    if (ksteps == 8) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) {
+            const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
+            step_ss<true>(d, a, at, b, at, idesc);
+        }
+    } else {
+#pragma unroll 1
+        for (int k = 1; k < ksteps; ++k) {
+            const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
+            step_ss<true>(d, a, at, b, at, idesc);
+        }
+    }
+}
+// The six steps of one slot's 32 tokens: three parts, 16 tokens each.
+template <bool kFirst>
+__device__ __forceinline__ void product_parts(uint32_t d, uint32_t a, Desc b, uint32_t idesc) {
+    step_ts<!kFirst>(d, a, b, 0, idesc);
+    step_ts<true>(d, a + 16, b, 0, idesc);
+    step_ts<true>(d, a + 32, b, 0, idesc);
+    step_ts<true>(d, a + 8, b, 2048, idesc);
+    step_ts<true>(d, a + 24, b, 2048, idesc);
+    step_ts<true>(d, a + 40, b, 2048, idesc);
+}
+
 // kStatesOnly: the first pass of a split (end states and decays of segments 0 .. P - 2; only KV is formed).
 template <bool kStatesOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
-                          const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split,
+                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split,
                           int32_t* status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small& sh = *reinterpret_cast<Small*>(sm + kOffSmall);
@@ -154,14 +233,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.qfull[i], 1);
             mbar_init(&sh.qfree[i], 1);
             mbar_init(&sh.decfull[i], 32);
-            mbar_init(&sh.decfree[i], kStatesOnly ? 384 : 640);
+            mbar_init(&sh.decfree[i], kStatesOnly ? 512 : 768);
         }
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&sh.vfull[i], 128);
+            mbar_init(&sh.vfull[i], 256);
             mbar_init(&sh.vfree[i], 1);
         }
         mbar_init(&sh.sfull, 256);
+        mbar_init(&sh.sfree, 1);
         mbar_init(&sh.xfull, 1);
+        mbar_init(&sh.xfree, 256);
         mbar_init(&sh.qkfull, 1);
         mbar_init(&sh.pfull, 128);
         mbar_init(&sh.ofull, 1);
@@ -169,14 +250,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.drain, 1);
         fence_mbar_init();
     }
-    if (warp == 21) tmem_alloc(&sh.tmem, 512);
-    if (warp == 20 && elect_one()) {
+    if (warp == 25) tmem_alloc(&sh.tmem, 512);
+    if (warp == 24 && elect_one()) {
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
-        if (!kStatesOnly) {
-            tma_prefetch_desc(&tq);
-            tma_prefetch_desc(&to);
-        }
+        if (!kStatesOnly) tma_prefetch_desc(&tq);
     }
     tc_fence_before();
     __syncthreads();
@@ -200,49 +278,57 @@ __global__ void __launch_bounds__(kThreads, 1)
                     float R = 0.f;
                     for (int m = 0; m < a; ++m) R += sh.T[s][m];
                     const float ci = sh.c[s][32 * a + lane], shift = ci - fmaxf(R + ci, kMinRow);
-                    float u[3];  // off the diagonal: 2^(c_i - m_i - (end of block b))
-#pragma unroll
-                    for (int b = 0; b < 3; ++b) {
-                        float x = shift;
-                        for (int m = b + 1; m < a; ++m) x += sh.T[s][m];
-                        u[b] = exp2_approx(x);
-                    }
                     fail = !wait_warp(&sh.qkfull, cn & 1, abort);
                     if (fail) break;
                     tc_fence_after();
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t pk[16];
-                        if (b > a) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) pk[j] = 0;
-                        } else {
-                            float x[32];
-                            tmem_ld32(tq4 + kColP + 32 * b, x);
+                    // 16 columns at a time, in loops that stay small: the roles share the instruction caches
+                    float between = shift;  // c_i - m_i less the end of block b
+                    for (int m = 1; m < a; ++m) between += sh.T[s][m];
+#pragma unroll 1
+                    for (int b = 0; b < a; ++b) {
+                        const float u = exp2_approx(between);
+                        between -= b + 1 < a ? sh.T[s][b + 1] : 0.f;
+#pragma unroll 1
+                        for (int j0 = 0; j0 < 32; j0 += 16) {
+                            float x[16];
+                            uint32_t pk[8];
+                            tmem_ld16(tq4 + kColP + 32 * b + j0, x);
+                            const float4* h = reinterpret_cast<const float4*>(&sh.h[s][32 * b + j0]);
                             tmem_wait_ld();
-                            if (b < a) {
-                                const float ub = u[b < 3 ? b : 0];
 #pragma unroll
-                                for (int j = 0; j < 32; j += 4) {
-                                    const float4 h = *reinterpret_cast<const float4*>(&sh.h[s][32 * b + j]);
-                                    pk[j / 2] = pack_bf16x2(x[j] * (ub * h.x), x[j + 1] * (ub * h.y));
-                                    pk[j / 2 + 1] = pack_bf16x2(x[j + 2] * (ub * h.z), x[j + 3] * (ub * h.w));
-                                }
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 32; j += 4) {
-                                    const float4 cj = *reinterpret_cast<const float4*>(&sh.c[s][32 * b + j]);
-                                    const float y0 = j <= lane ? x[j] * exp2_approx(shift - cj.x) : 0.f;
-                                    const float y1 = j + 1 <= lane ? x[j + 1] * exp2_approx(shift - cj.y) : 0.f;
-                                    const float y2 = j + 2 <= lane ? x[j + 2] * exp2_approx(shift - cj.z) : 0.f;
-                                    const float y3 = j + 3 <= lane ? x[j + 3] * exp2_approx(shift - cj.w) : 0.f;
-                                    pk[j / 2] = pack_bf16x2(y0, y1);
-                                    pk[j / 2 + 1] = pack_bf16x2(y2, y3);
-                                }
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 hj = h[j / 4];
+                                pk[j / 2] = pack_bf16x2(x[j] * (u * hj.x), x[j + 1] * (u * hj.y));
+                                pk[j / 2 + 1] = pack_bf16x2(x[j + 2] * (u * hj.z), x[j + 3] * (u * hj.w));
                             }
+                            // (over score columns that this warp has read)
+                            tmem_st8u(tq4 + kColP + 16 * b + j0 / 2, pk);
                         }
-                        // (over score columns that this warp has read: 16 b + 15 < 32 (b + 1))
-                        tmem_st16u(tq4 + kColP + 16 * b, pk);
+                    }
+#pragma unroll 1
+                    for (int j0 = 0; j0 < 32; j0 += 16) {  // the diagonal block
+                        float x[16];
+                        uint32_t pk[8];
+                        tmem_ld16(tq4 + kColP + 32 * a + j0, x);
+                        const float4* cc = reinterpret_cast<const float4*>(&sh.c[s][32 * a + j0]);
+                        tmem_wait_ld();
+                        const int k = lane - j0;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            const float4 cj = cc[j / 4];
+                            const float y0 = j <= k ? x[j] * exp2_approx(shift - cj.x) : 0.f;
+                            const float y1 = j + 1 <= k ? x[j + 1] * exp2_approx(shift - cj.y) : 0.f;
+                            const float y2 = j + 2 <= k ? x[j + 2] * exp2_approx(shift - cj.z) : 0.f;
+                            const float y3 = j + 3 <= k ? x[j + 3] * exp2_approx(shift - cj.w) : 0.f;
+                            pk[j / 2] = pack_bf16x2(y0, y1);
+                            pk[j / 2 + 1] = pack_bf16x2(y2, y3);
+                        }
+                        tmem_st8u(tq4 + kColP + 16 * a + j0 / 2, pk);
+                    }
+#pragma unroll 1
+                    for (int b = 2 * a + 2; b < 8; ++b) {  // columns behind the row's block
+                        const uint32_t zero[8] = {};
+                        tmem_st8u(tq4 + kColP + 8 * b, zero);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -296,7 +382,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < w.n; ++c, ++cn) {
                 const int s = cn & 1;
                 if (!kStatesOnly) {
-                    // S^T in bf16, rows dv: the products that read the previous one are done (xfull)
+                    // S^T in bf16, rows dv, when the product that reads the previous one is done
+                    fail = cn > 0 && !wait_warp(&sh.sfree, (cn - 1) & 1, abort);
+                    if (fail) break;
 #pragma unroll
                     for (int ch = 0; ch < 8; ++ch) {
                         const float* x = S + 8 * ch;
@@ -305,12 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        pack_bf16x2(x[6], x[7]));
                     }
                     fence_proxy_async_smem();
+                    mbar_arrive(&sh.sfull);
                 }
-                mbar_arrive(&sh.sfull);
                 fail = !wait_warp(&sh.decfull[s], (cn >> 1) & 1, abort);
                 if (fail) break;
                 const float e = sh.total[s];
                 decay *= e;
+                mbar_arrive(&sh.decfree[s]);
                 fail = !wait_warp(&sh.xfull, cn & 1, abort);
                 if (fail) break;
                 tc_fence_after();
@@ -325,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&sh.decfree[s]);
+                mbar_arrive(&sh.xfree);
             }
             if (fail) break;
             float* dst = nullptr;
@@ -344,10 +433,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         // ------------------------------------------------------------ parts of e^. V
         regs_dec<kRegsV>();
-        int vi = 0;  // slots so far
+        const int o2 = (warp - 12) >> 2;  // which 16 tokens of a slot
+        int vi = 0;                       // slots so far
         bool fail = false;
         for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
             const Chunks w = chunks_of(p, split, item);
@@ -358,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (fail) break;
                 uint8_t* vt = sm + kOffV + s * kTile;
                 if (n < subs * kSub && p.lengths) {
-                    // rows behind the last token in the last 16: whatever they hold is not multiplied, not even by zero.
-                    // A warp clears the columns that it reads itself, of V and of K
+                    // rows behind the last token in the last 32: whatever they hold is not multiplied, not even by zero.
+                    // A warp clears the columns that it reads itself, of V and of K (two warps the same ones)
                     const int rows = subs * kSub - n;
                     for (int i = lane; i < rows * 8; i += 32) {
                         const uint32_t at =
@@ -370,41 +460,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                 }
                 const uint32_t vh = smem_u32(vt) + (quad >> 1) * kHalf;
+#pragma unroll 1
                 for (int u = 0; u < subs; ++u, ++vi) {
-                    const int slot = vi % kSlots, turn = vi / kSlots;
+                    const int slot = vi & 1, turn = vi >> 1;
+                    uint32_t part[3][2][4];  // [part][8 tokens][8 columns dv], made before the slot is free
+                    if (quad * 32 < p.Dv) {
+                        const float wb = sh.w[s][u];
+#pragma unroll
+                        for (int o = 0; o < 2; ++o) {
+                            const int tok = u * kSub + o2 * 16 + o * 8;
+                            uint32_t m[4];
+                            ldmatrix_x4_trans(vh + sw128_offset(tok + (lane & 7), (quad & 1) * 64 + (lane >> 3) * 16), m);
+                            const float2 h = *reinterpret_cast<const float2*>(&sh.h[s][tok + 2 * (lane & 3)]);
+                            const float2 d = make_float2(h.x * wb, h.y * wb);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) three_parts(m[i], d, part[0][o][i], part[1][o][i], part[2][o][i]);
+                        }
+                    }
                     if (turn > 0) {
                         fail = !wait_warp(&sh.vfree[slot], (turn - 1) & 1, abort);
                         if (fail) break;
                     }
                     if (quad * 32 < p.Dv) {
                         tc_fence_after();
-                        const float wb = sh.w[s][u >> 1];
-                        uint32_t part[3][2][4];  // [part][8 tokens][8 columns dv]
-#pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            const int tok = u * kSub + o * 8;
-                            uint32_t m[4];
-                            ldmatrix_x4_trans(
-                                vh + sw128_offset(tok + (lane & 7), (quad & 1) * 64 + (lane >> 3) * 16), m);
-                            const float2 h = *reinterpret_cast<const float2*>(&sh.h[s][tok + 2 * (lane & 3)]);
-                            const float d0 = h.x * wb, d1 = h.y * wb;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float x0 = bf16lo_to_f32(m[i]) * d0, x1 = bf16hi_to_f32(m[i]) * d1;
-#pragma unroll
-                                for (int q = 0; q < 3; ++q) {
-                                    const uint32_t r = pack_bf16x2(x0, x1);
-                                    part[q][o][i] = r;
-                                    x0 -= bf16lo_to_f32(r);
-                                    x1 -= bf16hi_to_f32(r);
-                                }
-                            }
-                        }
-                        const uint32_t at = tq4 + kColV + slot * kSlotCols;
+                        const uint32_t at = tq4 + kColV + slot * kSlotCols + 8 * o2;
 #pragma unroll
                         for (int q = 0; q < 3; ++q) {
-                            tmem_st16x128_x2(at + 8 * q, part[q][0][0], part[q][0][1], part[q][1][0], part[q][1][1]);
-                            tmem_st16x128_x2(at + 8 * q + (16u << 16), part[q][0][2], part[q][0][3], part[q][1][2],
+                            tmem_st16x128_x2(at + 16 * q, part[q][0][0], part[q][0][1], part[q][1][0], part[q][1][1]);
+                            tmem_st16x128_x2(at + 16 * q + (16u << 16), part[q][0][2], part[q][0][3], part[q][1][2],
                                              part[q][1][3]);
                         }
                         tmem_wait_st();
@@ -415,92 +498,79 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!fail) mbar_arrive(&sh.decfree[s]);
             }
         }
-    } else if (warp < 20) {
+    } else if (warp < 24) {
         // ------------------------------------------------------------ outputs
         regs_dec<kRegsO>();
         if (!kStatesOnly) {
             const int r = quad * 32 + lane;
-            bool stop = false;
-            for (int item = blockIdx.x; item < items && !stop; item += gridDim.x) {
-                const Chunks w = chunks_of(p, split, item);
-                for (int c = 0; c < w.n; ++c, ++cn) {
-                    const int s = cn & 1, t = w.t0 + c * kC, n = min(kC, w.t1 - t);
-                    bool fail = !wait_warp(&sh.decfull[s], (cn >> 1) & 1, abort);
-                    float f = 0.f;
-                    if (!fail) {
-                        float R = 0.f;
-                        for (int m = 0; m < quad; ++m) R += sh.T[s][m];
-                        f = p.scale * exp2_approx(fmaxf(R + sh.c[s][r], kMinRow));
-                        fail = !wait_warp(&sh.ofull, cn & 1, abort);
-                    }
-                    if (named_bar_any(2, 128, fail)) {
-                        stop = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    // whole chunks and the end of the tensor by TMA, out of q's tile; rows that a length ends by themselves
-                    const bool tma = n == kC || t + n == p.S;
-                    uint8_t* tile = sm + kOffQ + s * kTile;
-                    uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)w.bh * p.S + t + r) * (long long)p.Dv * 2;
-#pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        if (16 * b < p.Dv) {
-                            float x[16];
-                            tmem_ld16(tq4 + kColO + 16 * b, x);
-                            tmem_wait_ld();
-                            if (16 * (b + 1) >= p.Dv) {  // the last columns have been read
-                                tc_fence_before();
-                                mbar_arrive(&sh.ofree);
-                            }
-#pragma unroll
-                            for (int ch = 0; ch < 2; ++ch) {
-                                const float* y = x + 8 * ch;
-                                const uint4 o = make_uint4(pack_bf16x2(f * y[0], f * y[1]), pack_bf16x2(f * y[2], f * y[3]),
-                                                           pack_bf16x2(f * y[4], f * y[5]), pack_bf16x2(f * y[6], f * y[7]));
-                                if (tma)
-                                    *reinterpret_cast<uint4*>(tile + (b >> 2) * kHalf +
-                                                              sw128_offset(r, (b & 3) * 32 + ch * 16)) = o;
-                                else if (r < n && 16 * b + 8 * ch < p.Dv)
-                                    *reinterpret_cast<uint4*>(row + 32 * b + 16 * ch) = o;
-                            }
-                        }
-                    }
-                    mbar_arrive(&sh.decfree[s]);
-                    if (tma) {
-                        fence_proxy_async_smem();
-                        named_bar_sync(2, 128);
-                    }
-                    if (warp == 16 && elect_one()) {
-                        if (tma) {
-                            tma_store_3d(&to, tile, 0, t, w.bh);
-                            if (p.Dv > 64) tma_store_3d(&to, tile + kHalf, 64, t, w.bh);
-                            tma_store_commit();
-                            tma_store_wait_read0();
-                        }
-                        mbar_arrive(&sh.qfree[s]);
-                    }
-                    __syncwarp();
-                }
-            }
-            if (warp == 16) tma_store_wait_all0();
-        }
-    } else {
-        regs_dec<kRegsCtl>();
-        if (warp == 20) {
-            // -------------------------------------------------------- TMA
-            const uint32_t kb = p.Dk > 64 ? kTile : kHalf, vb = p.Dv > 64 ? kTile : kHalf;
-            int kv_issued = 0, q_issued = 0;
+            // a thread writes its token's row: 32 bytes at a time, whole sectors, where rows are multiples of that
+            const bool wide = (((uint32_t)p.Dv * 2) | (uint32_t)reinterpret_cast<uintptr_t>(p.out)) % 32 == 0;
             bool fail = false;
             for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
                 const Chunks w = chunks_of(p, split, item);
-                const int bhk = w.b * p.Hk + w.h / (p.Hv / p.Hk);
                 for (int c = 0; c < w.n; ++c, ++cn) {
                     const int s = cn & 1, t = w.t0 + c * kC;
-                    if (cn >= 2) {
-                        fail = !wait_warp(&sh.kvfree[s], ((cn >> 1) - 1) & 1, abort);
-                        if (fail) break;
+                    fail = !wait_warp(&sh.decfull[s], (cn >> 1) & 1, abort);
+                    if (fail) break;
+                    float R = 0.f;
+                    for (int m = 0; m < quad; ++m) R += sh.T[s][m];
+                    const float f = p.scale * exp2_approx(fmaxf(R + sh.c[s][r], kMinRow));
+                    mbar_arrive(&sh.decfree[s]);
+                    uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)w.bh * p.S + t + r) * p.Dv * 2;
+                    const bool in = t + r < w.t1;
+                    fail = !wait_warp(&sh.ofull, cn & 1, abort);
+                    if (fail) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int b = 0; 16 * b < p.Dv; ++b) {
+                        float x[16];
+                        tmem_ld16(tq4 + kColO + 16 * b, x);
+                        tmem_wait_ld();
+                        uint32_t o[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(f * x[2 * j], f * x[2 * j + 1]);
+                        if (in) {
+                            if (wide) {
+                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(row + 32 * b),
+                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]),
+                                             "r"(o[7])
+                                             : "memory");
+                            } else {
+                                *reinterpret_cast<uint4*>(row + 32 * b) = make_uint4(o[0], o[1], o[2], o[3]);
+                                if (16 * b + 8 < p.Dv)
+                                    *reinterpret_cast<uint4*>(row + 32 * b + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+                            }
+                        }
                     }
-                    if (elect_one()) {
+                    tc_fence_before();
+                    mbar_arrive(&sh.ofree);
+                }
+            }
+        }
+    } else {
+        regs_dec<kRegsCtl>();
+        if (warp == 24) {
+            // -------------------------------------------------------- TMA, one thread
+            if (elect_one()) {
+                const uint32_t kb = p.Dk > 64 ? kTile : kHalf, vb = p.Dv > 64 ? kTile : kHalf;
+                int kv_issued = 0, q_issued = 0;
+                bool fail = false;
+                for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
+                    const Chunks w = chunks_of(p, split, item);
+                    const int bhk = w.b * p.Hk + w.h / (p.Hv / p.Hk);
+                    for (int c = 0; c < w.n; ++c, ++cn) {
+                        const int s = cn & 1, t = w.t0 + c * kC;
+                        if (!kStatesOnly) {
+                            if (cn >= 2) fail = !wait_inline(&sh.qfree[s], ((cn >> 1) - 1) & 1, abort);
+                            if (fail) break;
+                            uint8_t* qt = sm + kOffQ + s * kTile;
+                            mbar_arrive_expect_tx(&sh.qfull[s], kb);
+                            tma_load_3d(qt, &tq, &sh.qfull[s], 0, t, bhk);
+                            if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, t, bhk);
+                            q_issued = cn + 1;
+                        }
+                        if (cn >= 2) fail = !wait_inline(&sh.kvfree[s], ((cn >> 1) - 1) & 1, abort);
+                        if (fail) break;
                         uint8_t* kt = sm + kOffK + s * kTile;
                         uint8_t* vt = sm + kOffV + s * kTile;
                         mbar_arrive_expect_tx(&sh.kvfull[s], kb + vb);
@@ -508,117 +578,93 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, t, bhk);
                         tma_load_3d(vt, &tv, &sh.kvfull[s], 0, t, w.bh);
                         if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, t, w.bh);
-                    }
-                    __syncwarp();
-                    kv_issued = cn + 1;
-                    if (!kStatesOnly) {
-                        if (cn >= 2) {
-                            fail = !wait_warp(&sh.qfree[s], ((cn >> 1) - 1) & 1, abort);
-                            if (fail) break;
-                        }
-                        if (elect_one()) {
-                            uint8_t* qt = sm + kOffQ + s * kTile;
-                            mbar_arrive_expect_tx(&sh.qfull[s], kb);
-                            tma_load_3d(qt, &tq, &sh.qfull[s], 0, t, bhk);
-                            if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, t, bhk);
-                        }
-                        __syncwarp();
-                        q_issued = cn + 1;
+                        kv_issued = cn + 1;
                     }
                 }
+                // every load has landed before the CTA ends (bounded)
+                for (int i = max(0, kv_issued - 2); i < kv_issued; ++i) wait_drain(&sh.kvfull[i & 1], (i >> 1) & 1);
+                for (int i = max(0, q_issued - 2); i < q_issued; ++i) wait_drain(&sh.qfull[i & 1], (i >> 1) & 1);
             }
-            // every load has landed before the CTA ends (bounded)
-            for (int i = max(0, kv_issued - 2); i < kv_issued; ++i) wait_drain(&sh.kvfull[i & 1], (i >> 1) & 1);
-            for (int i = max(0, q_issued - 2); i < q_issued; ++i) wait_drain(&sh.qfull[i & 1], (i >> 1) & 1);
-        } else if (warp == 21) {
-            // -------------------------------------------------------- products
-            const int Nk = (p.Dk + 15) & ~15, Nv = (p.Dv + 15) & ~15, ksteps = Nk / 16;
-            constexpr uint32_t kIdQK = make_idesc_bf16(128, 128, 0, 0);
-            const uint32_t id_qs = make_idesc_bf16(128, Nv, 0, 0), id_pv = make_idesc_bf16(128, Nv, 0, 1),
-                           id_kv = make_idesc_bf16(128, Nk, 0, 1);
-            int vi = 0, last = -1;  // (last: the last chunk with a commit to wait for)
-            bool fail = false;
-            const uint64_t ds = make_sdesc(sbase + kOffS, 16, 1024);
-            for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
-                const Chunks w = chunks_of(p, split, item);
-                for (int c = 0; c < w.n && !fail; ++c, ++cn) {
-                    const int s = cn & 1, n = min(kC, w.t1 - w.t0 - c * kC), subs = (n + kSub - 1) / kSub;
-                    const uint32_t kt = sbase + kOffK + s * kTile, vt = sbase + kOffV + s * kTile;
-                    const uint64_t dq = make_sdesc(sbase + kOffQ + s * kTile, 16, 1024), dk = make_sdesc(kt, 16, 1024),
-                                   dkm = make_sdesc(kt, kHalf, 1024), dvm = make_sdesc(vt, kHalf, 1024);
-                    fail = !wait_warp(&sh.kvfull[s], (cn >> 1) & 1, abort);
-                    if (fail) break;
-                    if (!kStatesOnly) {
-                        fail = !wait_warp(&sh.qfull[s], (cn >> 1) & 1, abort);
+            __syncwarp();
+        } else if (warp == 25) {
+            // -------------------------------------------------------- products, all by one thread
+            if (elect_one()) {
+                const int Nk = (p.Dk + 15) & ~15, Nv = (p.Dv + 15) & ~15, ksteps = Nk / 16;
+                constexpr uint32_t kIdQK = make_idesc_bf16(128, 128, 0, 0);
+                const uint32_t id_qs = make_idesc_bf16(128, Nv, 0, 0), id_pv = make_idesc_bf16(128, Nv, 0, 1),
+                               id_kv = make_idesc_bf16(128, Nk, 0, 1);
+                const Desc ds = desc_of(sbase + kOffS, 16);
+                int vi = 0;
+                bool fail = false;
+                for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
+                    const Chunks w = chunks_of(p, split, item);
+                    for (int c = 0; c < w.n; ++c, ++cn) {
+                        const int s = cn & 1, n = min(kC, w.t1 - w.t0 - c * kC), subs = (n + kSub - 1) / kSub;
+                        const uint32_t kt = sbase + kOffK + s * kTile, vt = sbase + kOffV + s * kTile;
+                        const Desc dq = desc_of(sbase + kOffQ + s * kTile, 16), dkm = desc_of(kt, kHalf);
+                        fail = !wait_inline(&sh.kvfull[s], (cn >> 1) & 1, abort);
                         if (fail) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            for (int k = 0; k < ksteps; ++k) {
-                                const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
-                                mma_bf16(tmem + kColP, sdesc_add(dq, at), sdesc_add(dk, at), kIdQK, k > 0);
-                            }
+                        if (!kStatesOnly) {
+                            fail = !wait_inline(&sh.qfull[s], (cn >> 1) & 1, abort);
+                            if (fail) break;
+                            tc_fence_after();
+                            product_rows(tmem + kColP, dq, desc_of(kt, 16), kIdQK, ksteps);
                             mma_commit(&sh.qkfull);
                         }
-                        __syncwarp();
-                        fail = (cn > 0 && !wait_warp(&sh.ofree, (cn - 1) & 1, abort));
+                        // X of the chunk before has been read
+                        if (cn > 0) fail = !wait_inline(&sh.xfree, (cn - 1) & 1, abort);
                         if (fail) break;
-                    }
-                    fail = !wait_warp(&sh.sfull, cn & 1, abort);
-                    if (fail) break;
-                    tc_fence_after();
-                    if (!kStatesOnly && elect_one()) {
-                        for (int k = 0; k < ksteps; ++k) {
-                            const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
-                            mma_bf16(tmem + kColO, sdesc_add(dq, at), sdesc_add(ds, at), id_qs, k > 0);
-                        }
-                    }
-                    __syncwarp();
-                    for (int u = 0; u < subs; ++u, ++vi) {
-                        const int slot = vi % kSlots;
-                        fail = !wait_warp(&sh.vfull[slot], (vi / kSlots) & 1, abort);
-                        if (fail) break;
-                        tc_fence_after();
-                        if (elect_one()) {
-                            const uint32_t a = tmem + kColV + slot * kSlotCols;
-                            const uint64_t b = sdesc_add(dkm, u * 2048);
-                            mma_bf16_tmem_a(tmem + kColX, a, b, id_kv, u > 0);
-                            mma_bf16_tmem_a(tmem + kColX, a + 8, b, id_kv, 1);
-                            mma_bf16_tmem_a(tmem + kColX, a + 16, b, id_kv, 1);
+#pragma unroll 1
+                        for (int u = 0; u < subs; ++u, ++vi) {
+                            const int slot = vi & 1;
+                            fail = !wait_inline(&sh.vfull[slot], (vi >> 1) & 1, abort);
+                            if (fail) break;
+                            tc_fence_after();
+                            const uint32_t av = tmem + kColV + slot * kSlotCols;
+                            Desc b = dkm;
+                            b.lo += u * (kSub * 128 / 16);
+                            if (u == 0)
+                                product_parts<true>(tmem + kColX, av, b, id_kv);
+                            else
+                                product_parts<false>(tmem + kColX, av, b, id_kv);
                             mma_commit(&sh.vfree[slot]);
-                            if (u == subs - 1) {
-                                mma_commit(&sh.xfull);
-                                if (kStatesOnly) mma_commit(&sh.kvfree[s]);
-                            }
                         }
-                        __syncwarp();
-                    }
-                    if (fail) break;
-                    if (!kStatesOnly) {
-                        fail = !wait_warp(&sh.pfull, cn & 1, abort);
+                        if (fail) break;
+                        mma_commit(&sh.xfull);
+                        if (kStatesOnly) {
+                            mma_commit(&sh.kvfree[s]);
+                            continue;
+                        }
+                        fail = !wait_inline(&sh.sfull, cn & 1, abort) ||
+                               (cn > 0 && !wait_inline(&sh.ofree, (cn - 1) & 1, abort));
                         if (fail) break;
                         tc_fence_after();
-                        if (elect_one()) {
-                            for (int k = 0; k < subs; ++k)
-                                mma_bf16_tmem_a(tmem + kColO, tmem + kColP + 8 * k, sdesc_add(dvm, k * 2048), id_pv, 1);
-                            mma_commit(&sh.ofull);
-                            mma_commit(&sh.kvfree[s]);
+                        product_rows(tmem + kColO, dq, ds, id_qs, ksteps);
+                        mma_commit(&sh.sfree);
+                        mma_commit(&sh.qfree[s]);
+                        fail = !wait_inline(&sh.pfull, cn & 1, abort);
+                        if (fail) break;
+                        tc_fence_after();
+                        const Desc dvm = desc_of(vt, kHalf);
+                        if (subs == kC / kSub) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                step_ts<true>(tmem + kColO, tmem + kColP + 8 * k, dvm, k * 2048, id_pv);
+                        } else {
+#pragma unroll 1
+                            for (int k = 0; k < 2 * subs; ++k)
+                                step_ts<true>(tmem + kColO, tmem + kColP + 8 * k, dvm, k * 2048, id_pv);
                         }
-                        __syncwarp();
+                        mma_commit(&sh.ofull);
+                        mma_commit(&sh.kvfree[s]);
                     }
-                    last = cn;
                 }
+                // every product has ended before the tensor memory is freed (bounded)
+                mma_commit(&sh.drain);
+                wait_drain(&sh.drain, 0);
             }
-            if (fail) {
-                // products in flight end before the tensor memory is freed: a commit behind all of them (bounded).
-                if (elect_one()) {
-                    mma_commit(&sh.drain);
-                    wait_drain(&sh.drain, 0);
-                }
-                __syncwarp();
-            } else if (last >= 0) {
-                wait_drain(&sh.kvfree[last & 1], (last >> 1) & 1);
-            }
-        } else if (warp == 22) {
+            __syncwarp();
+        } else if (warp == 26) {
             // -------------------------------------------------------- decays
             bool fail = false;
             for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
@@ -667,7 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 21) {
+    if (warp == 25) {
         tmem_relinquish();
         tmem_dealloc(tmem, 512);
     }
@@ -704,7 +750,7 @@ bool encode(CUtensorMap* map, const void* ptr, long long heads, int S, int D) {
 }
 
 template <bool kStatesOnly>
-gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
+gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
                   int32_t* status, cudaStream_t stream) {
     auto* kernel = linear_attn_tc_kernel<kStatesOnly>;
     static const int regs = [&] {
@@ -727,7 +773,7 @@ gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], p, s, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], p, s, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -739,10 +785,9 @@ bool linear_attn_tc_supported(const LinearAttn& p) {
 
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream) {
-    CUtensorMap m[4];
+    CUtensorMap m[3];
     const long long hk = (long long)p.B * p.Hk, hv = (long long)p.B * p.Hv;
-    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv) ||
-        !encode(&m[3], p.out, hv, p.S, p.Dv))
+    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv))
         return GDN_ERR_CUDA;
     if (s.P > 1) {
         const gdn_status e = launch<true>(m, p, s, dev, sms, status, stream);
