@@ -57,11 +57,12 @@ struct Small {
     float T[2][4];       // the blocks' log2-decays
     float w[2][4];       // e^(the log-decays behind the block)
     float total[2];      // e^(the chunk's)
+    int bh[2], t[2], n[2];  // its head, its first token, and how many it has (0: there is no further chunk)
     uint64_t kvfull[2], kvfree[2], qfull[2], qfree[2], decfull[2], decfree[2];
     uint64_t vfull[kSlots], vfree[kSlots];
     uint64_t sfull, sfree, xfull, xfree, qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
-    int abort;
+    int gave_up;
 };
 constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -91,43 +92,56 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
         : "r"(taddr));
 }
 
-// Waits as ptx::mbar_wait_or_abort's, but inline (a kernel that shares out its registers cannot call functions), and
-// with the limit of about a second in clocks: reading the global timer takes longer than most of these waits.
-constexpr long long kWaitClocks = 2000000000ll;
-__device__ __forceinline__ bool wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const long long t0 = clock64();
-    for (;;) {
+// Waits, inline (a kernel that shares out its registers cannot call functions) and few instructions long (there are many
+// of them): 4 million tests, each of which blocks for a short time that the hardware chooses, then false.
+constexpr uint32_t kMostTests = 1u << 22;
+__device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
+    uint32_t i = 0;
 #pragma unroll 1
-        for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (abort && *abort) return false;
-        if (clock64() - t0 > kWaitClocks) {
-            if (abort) *abort = 1;
-            return false;
-        }
-    }
+    while (!mbar_try_wait(bar, parity))
+        if (++i == kMostTests) return false;
+    return true;
 }
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-    return __all_sync(0xffffffffu, wait_inline(bar, parity, abort));
+// By a warp, with one answer for its lanes.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_one(bar, parity));
 }
-// What is in flight when a role gives up: waited for with the time limit alone.
-__device__ __forceinline__ void wait_drain(uint64_t* bar, uint32_t parity) { (void)wait_inline(bar, parity, nullptr); }
+
+// Two fp32 values in one operation.
+__device__ __forceinline__ unsigned long long pair(float lo, float hi) {
+    return (unsigned long long)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ float pair_lo(unsigned long long x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float pair_hi(unsigned long long x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long sub2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(unsigned long long x) { return pack_bf16x2(pair_lo(x), pair_hi(x)); }
 
 // The two bf16 values in m, times d, as the sum of three bf16 values each: an fp32 product's 24 bits cut off 8 at a
 // time.  The cut parts' differences are exact.
-__device__ __forceinline__ void three_parts(uint32_t m, float2 d, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+__device__ __forceinline__ void three_parts(uint32_t m, unsigned long long d, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
     constexpr uint32_t kCut = 0xffff0000u;
-    const auto pair = [](uint32_t lo, uint32_t hi) { return (unsigned long long)hi << 32 | lo; };
-    const unsigned long long dd = pair(__float_as_uint(d.x), __float_as_uint(d.y));
-    unsigned long long x = pair(m << 16, m & kCut), r, r2;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(x), "l"(dd));
+    const auto join = [](uint32_t lo, uint32_t hi) { return (unsigned long long)hi << 32 | lo; };
+    const unsigned long long x = mul2(join(m << 16, m & kCut), d);
     uint32_t a = (uint32_t)x, b = (uint32_t)(x >> 32);
     p0 = __byte_perm(a, b, 0x7632);
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(pair(a & kCut, b & kCut)));
+    const unsigned long long r = sub2(x, join(a & kCut, b & kCut));
     a = (uint32_t)r, b = (uint32_t)(r >> 32);
     p1 = __byte_perm(a, b, 0x7632);
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r2) : "l"(r), "l"(pair(a & kCut, b & kCut)));
+    const unsigned long long r2 = sub2(r, join(a & kCut, b & kCut));
     p2 = __byte_perm((uint32_t)r2, (uint32_t)(r2 >> 32), 0x7632);
 }
 
@@ -137,22 +151,59 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]
                  : "memory");
 }
 
-struct Chunks {  // the walk over a CTA's items: (segment, head), and the chunks of each
-    int seg, b, h, bh, t0, t1, n;
+// n / d for 0 <= n < 2^31 as the high half of a product: m = ceil(2^(31 + s) / d), 2^(s - 1) < d <= 2^s.
+struct Divisor {
+    uint32_t m;
+    int s;
+    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi(2u * (uint32_t)n, m) >> s); }
 };
-__device__ __forceinline__ Chunks chunks_of(const LinearAttn& p, const LinearAttnSplit& s, int item) {
-    Chunks c;
-    const int heads = p.B * p.Hv;
-    c.seg = item / heads;
-    c.bh = item - c.seg * heads;
-    c.b = c.bh / p.Hv;
-    c.h = c.bh - c.b * p.Hv;
+Divisor divisor(int d) {
+    int s = 0;
+    while ((1ll << s) < d) ++s;
+    return Divisor{(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s};
+}
+// What the kernel's walk over its items needs: (segment, head) pairs, heads fastest, every gridDim-th of them a CTA's.
+struct Items {
+    int heads, segs, len;  // B Hv; segments that this launch runs; tokens of one (S where there is one)
+    Divisor hv, group;     // by Hv: the batch; by Hv / Hk: the key head, counted over the batch
+};
+struct Walk {  // a CTA's chunks one after another, over all of its items that have any
+    int bh, seg, t, end;  // head (over the batch), segment, the chunk's first token and the item's end
+};
+__device__ __forceinline__ void next_item(Walk& k, const Items& it) {
+    k.bh += gridDim.x;
+    while (k.bh >= it.heads) {
+        k.bh -= it.heads;
+        ++k.seg;
+    }
+}
+__device__ __forceinline__ void tokens_of(Walk& k, const LinearAttn& p, const Items& it) {
     int len = p.S;
-    if (p.lengths) len = max(0, min(p.S, p.lengths[c.b]));
-    c.t0 = s.P > 1 ? c.seg * s.len : 0;
-    c.t1 = s.P > 1 ? min(len, c.t0 + s.len) : len;
-    c.n = c.t1 > c.t0 ? (c.t1 - c.t0 + kC - 1) / kC : 0;
-    return c;
+    if (p.lengths) len = max(0, min(len, p.lengths[it.hv.of(k.bh)]));
+    k.t = k.seg * it.len;
+    k.end = len - k.t > it.len ? k.t + it.len : len;
+}
+__device__ __forceinline__ bool settle(Walk& k, const LinearAttn& p, const Items& it) {
+#pragma unroll 1
+    for (; k.seg < it.segs; next_item(k, it)) {
+        tokens_of(k, p, it);
+        if (k.t < k.end) return true;
+    }
+    return false;
+}
+__device__ __forceinline__ Walk first_item(const Items& it) {
+    Walk k{(int)blockIdx.x, 0, 0, 0};
+    while (k.bh >= it.heads) {
+        k.bh -= it.heads;
+        ++k.seg;
+    }
+    return k;
+}
+__device__ __forceinline__ bool next_chunk(Walk& k, const LinearAttn& p, const Items& it) {
+    k.t += kC;
+    if (k.t < k.end) return true;
+    next_item(k, it);
+    return settle(k, p, it);
 }
 
 // Descriptors in two words: an offset within shared memory is added to the low one (no carry leaves its address field).
@@ -200,9 +251,12 @@ __device__ __forceinline__ void product_rows(uint32_t d, Desc a, Desc b, uint32_
     }
 }
 // The six steps of one slot's 32 tokens: three parts, 16 tokens each.
-template <bool kFirst>
-__device__ __forceinline__ void product_parts(uint32_t d, uint32_t a, Desc b, uint32_t idesc) {
-    step_ts<!kFirst>(d, a, b, 0, idesc);
+__device__ __forceinline__ void product_parts(uint32_t d, uint32_t a, Desc b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\tsetp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"((int)add)
+        : "memory");
     step_ts<true>(d, a + 16, b, 0, idesc);
     step_ts<true>(d, a + 32, b, 0, idesc);
     step_ts<true>(d, a + 8, b, 2048, idesc);
@@ -210,30 +264,46 @@ __device__ __forceinline__ void product_parts(uint32_t d, uint32_t a, Desc b, ui
     step_ts<true>(d, a + 40, b, 2048, idesc);
 }
 
+// 64 rows of a state column: rows `pitch` floats apart, `rows` of them there.  Of whole heads (128 x 128, the pitch known
+// at compile time) a row is one instruction.
+template <typename F>
+__device__ __forceinline__ void column_rows(int pitch, int rows, F f) {
+    if (pitch == kC && rows == 64) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) f(i, i * kC, true);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+            f(i, i * pitch, i < rows);
+            if (i % 16 == 15) asm volatile("" ::: "memory");  // (no more addresses at once)
+        }
+    }
+}
+
 // kStatesOnly: the first pass of a split (end states and decays of segments 0 .. P - 2; only KV is formed).
 template <bool kStatesOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split,
-                          int32_t* status) {
+                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ LinearAttn p,
+                          const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small& sh = *reinterpret_cast<Small*>(sm + kOffSmall);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
-    volatile int* abort = &sh.abort;
     const uint32_t sbase = smem_u32(sm);
-    const long long heads = p.B * p.Hv;
-    const int items = (int)heads * (kStatesOnly ? split.P - 1 : split.P);
 
+    if (sbase & 1023u) {  // (the tiles' descriptors need it, and a launch without static shared memory has it)
+        if (tid == 0 && status) atomicExch(status, (int32_t)GDN_ERR_CUDA);
+        return;
+    }
     if (tid == 0) {
-        // (the tiles' descriptors need 1024-byte alignment, which a launch without static shared memory has)
-        sh.abort = (sbase & 1023u) ? 1 : 0;
+        sh.gave_up = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.kvfull[i], 1);
             mbar_init(&sh.kvfree[i], 1);
             mbar_init(&sh.qfull[i], 1);
             mbar_init(&sh.qfree[i], 1);
             mbar_init(&sh.decfull[i], 32);
-            mbar_init(&sh.decfree[i], kStatesOnly ? 512 : 768);
+            mbar_init(&sh.decfree[i], kStatesOnly ? 513 : 769);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.vfull[i], 256);
@@ -263,145 +333,137 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tq4 = tmem + ((uint32_t)(quad * 32) << 16);  // this warp's lanes
     griddep_wait();
 
-    int cn = 0;  // chunks so far, over all items
+    int cn = 0;      // chunks so far, over all items
+    bool ok = true;  // no wait has run out
     if (warp < 4) {
         // ------------------------------------------------------------ scores -> P
-        if (!kStatesOnly) {
-            for (int item = blockIdx.x; item < items; item += gridDim.x) {
-                const Chunks w = chunks_of(p, split, item);
-                bool fail = false;
-                for (int c = 0; c < w.n; ++c, ++cn) {
-                    const int s = cn & 1;
-                    fail = !wait_warp(&sh.decfull[s], (cn >> 1) & 1, abort);
-                    if (fail) break;
-                    const int a = quad;
-                    float R = 0.f;
-                    for (int m = 0; m < a; ++m) R += sh.T[s][m];
-                    const float ci = sh.c[s][32 * a + lane], shift = ci - fmaxf(R + ci, kMinRow);
-                    fail = !wait_warp(&sh.qkfull, cn & 1, abort);
-                    if (fail) break;
-                    tc_fence_after();
-                    // 16 columns at a time, in loops that stay small: the roles share the instruction caches
-                    float between = shift;  // c_i - m_i less the end of block b
-                    for (int m = 1; m < a; ++m) between += sh.T[s][m];
+        const int a = quad;
+        for (; !kStatesOnly; ++cn) {
+            const int s = cn & 1;
+            ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
+            if (!ok || sh.n[s] == 0) break;
+            float R = 0.f;
 #pragma unroll 1
-                    for (int b = 0; b < a; ++b) {
-                        const float u = exp2_approx(between);
-                        between -= b + 1 < a ? sh.T[s][b + 1] : 0.f;
+            for (int m = 0; m < a; ++m) R += sh.T[s][m];
+            const float ci = sh.c[s][32 * a + lane], shift = ci - fmaxf(R + ci, kMinRow);
+            ok = wait_warp(&sh.qkfull, cn & 1);
+            if (!ok) break;
+            tc_fence_after();
+            // 16 columns at a time, in loops that stay small: the roles share the instruction caches
+            float between = shift + (a > 0 ? R - sh.T[s][0] : 0.f);  // c_i - m_i less the end of block b
 #pragma unroll 1
-                        for (int j0 = 0; j0 < 32; j0 += 16) {
-                            float x[16];
-                            uint32_t pk[8];
-                            tmem_ld16(tq4 + kColP + 32 * b + j0, x);
-                            const float4* h = reinterpret_cast<const float4*>(&sh.h[s][32 * b + j0]);
-                            tmem_wait_ld();
+            for (int b = 0; b < a; ++b) {
+                const float u = exp2_approx(between);
+                const unsigned long long uu = pair(u, u);
+                between -= b + 1 < a ? sh.T[s][b + 1] : 0.f;
+#pragma unroll 1
+                for (int j0 = 0; j0 < 32; j0 += 16) {
+                    float x[16];
+                    uint32_t pk[8];
+                    tmem_ld16(tq4 + kColP + 32 * b + j0, x);
+                    const float4* h = reinterpret_cast<const float4*>(&sh.h[s][32 * b + j0]);
+                    tmem_wait_ld();
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4) {
-                                const float4 hj = h[j / 4];
-                                pk[j / 2] = pack_bf16x2(x[j] * (u * hj.x), x[j + 1] * (u * hj.y));
-                                pk[j / 2 + 1] = pack_bf16x2(x[j + 2] * (u * hj.z), x[j + 3] * (u * hj.w));
-                            }
-                            // (over score columns that this warp has read)
-                            tmem_st8u(tq4 + kColP + 16 * b + j0 / 2, pk);
-                        }
+                    for (int j = 0; j < 16; j += 4) {
+                        const float4 hj = h[j / 4];
+                        pk[j / 2] = pack2(mul2(pair(x[j], x[j + 1]), mul2(uu, pair(hj.x, hj.y))));
+                        pk[j / 2 + 1] = pack2(mul2(pair(x[j + 2], x[j + 3]), mul2(uu, pair(hj.z, hj.w))));
                     }
-#pragma unroll 1
-                    for (int j0 = 0; j0 < 32; j0 += 16) {  // the diagonal block
-                        float x[16];
-                        uint32_t pk[8];
-                        tmem_ld16(tq4 + kColP + 32 * a + j0, x);
-                        const float4* cc = reinterpret_cast<const float4*>(&sh.c[s][32 * a + j0]);
-                        tmem_wait_ld();
-                        const int k = lane - j0;
-#pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            const float4 cj = cc[j / 4];
-                            const float y0 = j <= k ? x[j] * exp2_approx(shift - cj.x) : 0.f;
-                            const float y1 = j + 1 <= k ? x[j + 1] * exp2_approx(shift - cj.y) : 0.f;
-                            const float y2 = j + 2 <= k ? x[j + 2] * exp2_approx(shift - cj.z) : 0.f;
-                            const float y3 = j + 3 <= k ? x[j + 3] * exp2_approx(shift - cj.w) : 0.f;
-                            pk[j / 2] = pack_bf16x2(y0, y1);
-                            pk[j / 2 + 1] = pack_bf16x2(y2, y3);
-                        }
-                        tmem_st8u(tq4 + kColP + 16 * a + j0 / 2, pk);
-                    }
-#pragma unroll 1
-                    for (int b = 2 * a + 2; b < 8; ++b) {  // columns behind the row's block
-                        const uint32_t zero[8] = {};
-                        tmem_st8u(tq4 + kColP + 8 * b, zero);
-                    }
-                    tmem_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(&sh.pfull);
-                    mbar_arrive(&sh.decfree[s]);
+                    // (over score columns that this warp has read)
+                    tmem_st8u(tq4 + kColP + 16 * b + j0 / 2, pk);
                 }
-                if (fail) break;
             }
+#pragma unroll 1
+            for (int j0 = 0; j0 < 32; j0 += 16) {  // the diagonal block
+                float x[16];
+                uint32_t pk[8];
+                tmem_ld16(tq4 + kColP + 32 * a + j0, x);
+                const float4* cc = reinterpret_cast<const float4*>(&sh.c[s][32 * a + j0]);
+                tmem_wait_ld();
+                const int last = lane - j0;
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 cj = cc[j / 4];
+                    const float y0 = j <= last ? x[j] * exp2_approx(shift - cj.x) : 0.f;
+                    const float y1 = j + 1 <= last ? x[j + 1] * exp2_approx(shift - cj.y) : 0.f;
+                    const float y2 = j + 2 <= last ? x[j + 2] * exp2_approx(shift - cj.z) : 0.f;
+                    const float y3 = j + 3 <= last ? x[j + 3] * exp2_approx(shift - cj.w) : 0.f;
+                    pk[j / 2] = pack_bf16x2(y0, y1);
+                    pk[j / 2 + 1] = pack_bf16x2(y2, y3);
+                }
+                tmem_st8u(tq4 + kColP + 16 * a + j0 / 2, pk);
+            }
+#pragma unroll 1
+            for (int b = 2 * a + 2; b < 8; ++b) {  // columns behind the row's block
+                const uint32_t zero[8] = {};
+                tmem_st8u(tq4 + kColP + 8 * b, zero);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&sh.pfull);
+            mbar_arrive(&sh.decfree[s]);
         }
     } else if (warp < 12) {
         // ------------------------------------------------------------ the state: thread = 64 rows of column dv
         regs_inc<kRegsS>();
         const int dv = quad * 32 + lane, half = (warp - 4) >> 2;
         const int rows = dv < p.Dv ? min(64, p.Dk - 64 * half) : 0;  // of the 64 that are there (<= 0: none)
-        const long long ns = (long long)p.Dk * p.Dv;
+        const long long ns = (long long)p.Dk * p.Dv, heads = it.heads;
+        const int first = 64 * half * p.Dv + dv;
+        uint8_t* const sb = sm + kOffS + half * kHalf + dv * 128;
         float S[64];
-        bool fail = false;
-        for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
-            const Chunks w = chunks_of(p, split, item);
+        for (Walk k = first_item(it); k.seg < it.segs && ok; next_item(k, it)) {
+            tokens_of(k, p, it);
             int pitch = p.Dv;
             asm volatile("" : "+r"(pitch));  // (64 rows' offsets are not kept in registers over the chunks)
-            const int first = 64 * half * pitch + dv;
-            const float* src = p.state_in ? p.state_in + w.bh * ns : nullptr;
-            if (!kStatesOnly && split.P > 1) src = split.parts + (w.seg ? w.bh : (split.P - 1) * heads + w.bh) * ns;
-            if (kStatesOnly && w.seg) src = nullptr;
+            const float* src = p.state_in ? p.state_in + k.bh * ns : nullptr;
+            if (!kStatesOnly && split.P > 1) src = split.parts + (k.seg ? k.bh : (split.P - 1) * heads + k.bh) * ns;
+            if (kStatesOnly && k.seg) src = nullptr;
+            if (src) {
+                src += first;
+                column_rows(pitch, rows, [&](int i, int at, bool in) { S[i] = in ? src[at] : 0.f; });
+            } else {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) {
-                S[i] = src && i < rows ? src[first + i * pitch] : 0.f;
-                if (i % 16 == 15) asm volatile("" ::: "memory");  // (no more loads' addresses at once)
+                for (int i = 0; i < 64; ++i) S[i] = 0.f;
             }
             if (!kStatesOnly && split.P > 1) {
-                for (int m = 1; m < w.seg; ++m) {
-                    const float f = split.decays[m * heads + w.bh];
-                    const float* x = split.parts + (m * heads + w.bh) * ns;
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) {
-                        if (i < rows) S[i] = fmaf(f, S[i], x[first + i * pitch]);
-                        if (i % 16 == 15) asm volatile("" ::: "memory");
-                    }
+#pragma unroll 1
+                for (int m = 1; m < k.seg; ++m) {
+                    const float f = split.decays[m * heads + k.bh];
+                    const float* x = split.parts + (m * heads + k.bh) * ns + first;
+                    column_rows(pitch, rows, [&](int i, int at, bool in) { S[i] = in ? fmaf(f, S[i], x[at]) : 0.f; });
                 }
             }
-            if (kStatesOnly && w.seg == 0) {  // the copy of state_in
-                float* x = split.parts + ((split.P - 1) * heads + w.bh) * ns;
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    if (i < rows) x[first + i * pitch] = S[i];
-                    if (i % 16 == 15) asm volatile("" ::: "memory");
-                }
+            if (kStatesOnly && k.seg == 0) {  // the copy of state_in
+                float* x = split.parts + ((split.P - 1) * heads + k.bh) * ns + first;
+                column_rows(pitch, rows, [&](int i, int at, bool in) {
+                    if (in) x[at] = S[i];
+                });
             }
             float decay = 1.f;
-            for (int c = 0; c < w.n; ++c, ++cn) {
+            for (; k.t < k.end; k.t += kC, ++cn) {
                 const int s = cn & 1;
                 if (!kStatesOnly) {
                     // S^T in bf16, rows dv, when the product that reads the previous one is done
-                    fail = cn > 0 && !wait_warp(&sh.sfree, (cn - 1) & 1, abort);
-                    if (fail) break;
+                    ok = cn == 0 || wait_warp(&sh.sfree, (cn - 1) & 1);
+                    if (!ok) break;
 #pragma unroll
                     for (int ch = 0; ch < 8; ++ch) {
                         const float* x = S + 8 * ch;
-                        *reinterpret_cast<uint4*>(sm + kOffS + half * kHalf + sw128_offset(dv, ch * 16)) =
+                        *reinterpret_cast<uint4*>(sb + ((ch ^ (dv & 7)) << 4)) =
                             make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
                                        pack_bf16x2(x[6], x[7]));
                     }
                     fence_proxy_async_smem();
                     mbar_arrive(&sh.sfull);
                 }
-                fail = !wait_warp(&sh.decfull[s], (cn >> 1) & 1, abort);
-                if (fail) break;
+                ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
+                if (!ok) break;
                 const float e = sh.total[s];
                 decay *= e;
                 mbar_arrive(&sh.decfree[s]);
-                fail = !wait_warp(&sh.xfull, cn & 1, abort);
-                if (fail) break;
+                ok = wait_warp(&sh.xfull, cn & 1);
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
@@ -410,142 +472,143 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld16(tq4 + kColX + 64 * half + 16 * b, x);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) S[16 * b + i] = fmaf(e, S[16 * b + i], x[i]);
+                        for (int i = 0; i < 16; i += 2) {
+                            const unsigned long long y =
+                                fma2(pair(e, e), pair(S[16 * b + i], S[16 * b + i + 1]), pair(x[i], x[i + 1]));
+                            S[16 * b + i] = pair_lo(y);
+                            S[16 * b + i + 1] = pair_hi(y);
+                        }
                     }
                 }
                 tc_fence_before();
                 mbar_arrive(&sh.xfree);
             }
-            if (fail) break;
+            if (!ok) break;
             float* dst = nullptr;
             if (kStatesOnly) {
-                dst = split.parts + (w.seg * heads + w.bh) * ns;
-                if (tid == 128) split.decays[w.seg * heads + w.bh] = decay;
-            } else if (w.seg == split.P - 1) {
-                dst = p.state_out + w.bh * ns;
+                dst = split.parts + (k.seg * heads + k.bh) * ns;
+                if (tid == 128) split.decays[k.seg * heads + k.bh] = decay;
+            } else if (k.seg == split.P - 1) {
+                dst = p.state_out + k.bh * ns;
             }
             if (dst) {
-                asm volatile("" : "+r"(pitch));
-#pragma unroll
-                for (int i = 0; i < 64; ++i) {
-                    if (i < rows) dst[first + i * pitch] = S[i];
-                    if (i % 16 == 15) asm volatile("" ::: "memory");
-                }
+                dst += first;
+                column_rows(pitch, rows, [&](int i, int at, bool in) {
+                    if (in) dst[at] = S[i];
+                });
             }
         }
     } else if (warp < 20) {
         // ------------------------------------------------------------ parts of e^. V
         regs_dec<kRegsV>();
         const int o2 = (warp - 12) >> 2;  // which 16 tokens of a slot
-        int vi = 0;                       // slots so far
-        bool fail = false;
-        for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
-            const Chunks w = chunks_of(p, split, item);
-            for (int c = 0; c < w.n && !fail; ++c, ++cn) {
-                const int s = cn & 1, n = min(kC, w.t1 - w.t0 - c * kC), subs = (n + kSub - 1) / kSub;
-                fail = !wait_warp(&sh.decfull[s], (cn >> 1) & 1, abort) ||
-                       !wait_warp(&sh.kvfull[s], (cn >> 1) & 1, abort);
-                if (fail) break;
-                uint8_t* vt = sm + kOffV + s * kTile;
-                if (n < subs * kSub && p.lengths) {
-                    // rows behind the last token in the last 32: whatever they hold is not multiplied, not even by zero.
-                    // A warp clears the columns that it reads itself, of V and of K (two warps the same ones)
-                    const int rows = subs * kSub - n;
-                    for (int i = lane; i < rows * 8; i += 32) {
-                        const uint32_t at =
-                            (quad >> 1) * kHalf + sw128_offset(n + (i >> 3), (quad & 1) * 64 + (i & 3) * 16);
-                        *reinterpret_cast<uint4*>((i & 4 ? vt : sm + kOffK + s * kTile) + at) = make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const uint32_t vh = smem_u32(vt) + (quad >> 1) * kHalf;
+        const int tok = o2 * 16 + (lane & 7);
+        // the 16-byte piece of a row that this lane's address takes
+        const uint32_t piece = (quad >> 1) * kHalf + sw128_offset(tok, (quad & 1) * 64 + (lane >> 3) * 16);
+        const uint32_t at = tq4 + kColV + 8 * o2;
+        const bool there = quad * 32 < p.Dv;
+        int vi = 0;  // slots so far
+        for (;; ++cn) {
+            const int s = cn & 1;
+            ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
+            const int n = sh.n[s], subs = (n + kSub - 1) / kSub;
+            if (!ok || n == 0) break;
+            ok = wait_warp(&sh.kvfull[s], (cn >> 1) & 1);
+            if (!ok) break;
+            uint8_t* vt = sm + kOffV + s * kTile;
+            if (n < subs * kSub && p.lengths) {
+                // rows behind the last token in the last 32: whatever they hold is not multiplied, not even by zero.
+                // A warp clears the columns that it reads itself, of V and of K (two warps the same ones)
+                const int rows = subs * kSub - n;
 #pragma unroll 1
-                for (int u = 0; u < subs; ++u, ++vi) {
-                    const int slot = vi & 1, turn = vi >> 1;
-                    uint32_t part[3][2][4];  // [part][8 tokens][8 columns dv], made before the slot is free
-                    if (quad * 32 < p.Dv) {
-                        const float wb = sh.w[s][u];
-#pragma unroll
-                        for (int o = 0; o < 2; ++o) {
-                            const int tok = u * kSub + o2 * 16 + o * 8;
-                            uint32_t m[4];
-                            ldmatrix_x4_trans(vh + sw128_offset(tok + (lane & 7), (quad & 1) * 64 + (lane >> 3) * 16), m);
-                            const float2 h = *reinterpret_cast<const float2*>(&sh.h[s][tok + 2 * (lane & 3)]);
-                            const float2 d = make_float2(h.x * wb, h.y * wb);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) three_parts(m[i], d, part[0][o][i], part[1][o][i], part[2][o][i]);
-                        }
-                    }
-                    if (turn > 0) {
-                        fail = !wait_warp(&sh.vfree[slot], (turn - 1) & 1, abort);
-                        if (fail) break;
-                    }
-                    if (quad * 32 < p.Dv) {
-                        tc_fence_after();
-                        const uint32_t at = tq4 + kColV + slot * kSlotCols + 8 * o2;
-#pragma unroll
-                        for (int q = 0; q < 3; ++q) {
-                            tmem_st16x128_x2(at + 16 * q, part[q][0][0], part[q][0][1], part[q][1][0], part[q][1][1]);
-                            tmem_st16x128_x2(at + 16 * q + (16u << 16), part[q][0][2], part[q][0][3], part[q][1][2],
-                                             part[q][1][3]);
-                        }
-                        tmem_wait_st();
-                        tc_fence_before();
-                    }
-                    mbar_arrive(&sh.vfull[slot]);
+                for (int i = lane; i < rows * 8; i += 32) {
+                    const uint32_t to = (quad >> 1) * kHalf + sw128_offset(n + (i >> 3), (quad & 1) * 64 + (i & 3) * 16);
+                    *reinterpret_cast<uint4*>((i & 4 ? vt : sm + kOffK + s * kTile) + to) = make_uint4(0, 0, 0, 0);
                 }
-                if (!fail) mbar_arrive(&sh.decfree[s]);
+                fence_proxy_async_smem();
+                __syncwarp();
             }
+            uint32_t from = smem_u32(vt) + piece;
+            const float* h = &sh.h[s][o2 * 16 + 2 * (lane & 3)];
+#pragma unroll 1
+            for (int u = 0; u < subs; ++u, ++vi, from += kSub * 128, h += kSub) {
+                const int slot = vi & 1, turn = vi >> 1;
+                uint32_t part[3][2][4];  // [part][8 tokens][8 columns dv], made before the slot is free
+                if (there) {
+                    const float wb = sh.w[s][u];
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        uint32_t m[4];
+                        ldmatrix_x4_trans(from + o * 1024, m);
+                        const float2 hh = *reinterpret_cast<const float2*>(h + 8 * o);
+                        const unsigned long long d = mul2(pair(hh.x, hh.y), pair(wb, wb));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) three_parts(m[i], d, part[0][o][i], part[1][o][i], part[2][o][i]);
+                    }
+                }
+                if (turn > 0) {
+                    ok = wait_warp(&sh.vfree[slot], (turn - 1) & 1);
+                    if (!ok) break;
+                }
+                if (there) {
+                    tc_fence_after();
+                    const uint32_t to = at + slot * kSlotCols;
+#pragma unroll
+                    for (int q = 0; q < 3; ++q) {
+                        tmem_st16x128_x2(to + 16 * q, part[q][0][0], part[q][0][1], part[q][1][0], part[q][1][1]);
+                        tmem_st16x128_x2(to + 16 * q + (16u << 16), part[q][0][2], part[q][0][3], part[q][1][2],
+                                         part[q][1][3]);
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                }
+                mbar_arrive(&sh.vfull[slot]);
+            }
+            if (!ok) break;
+            mbar_arrive(&sh.decfree[s]);
         }
     } else if (warp < 24) {
         // ------------------------------------------------------------ outputs
         regs_dec<kRegsO>();
-        if (!kStatesOnly) {
-            const int r = quad * 32 + lane;
-            // a thread writes its token's row: 32 bytes at a time, whole sectors, where rows are multiples of that
-            const bool wide = (((uint32_t)p.Dv * 2) | (uint32_t)reinterpret_cast<uintptr_t>(p.out)) % 32 == 0;
-            bool fail = false;
-            for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
-                const Chunks w = chunks_of(p, split, item);
-                for (int c = 0; c < w.n; ++c, ++cn) {
-                    const int s = cn & 1, t = w.t0 + c * kC;
-                    fail = !wait_warp(&sh.decfull[s], (cn >> 1) & 1, abort);
-                    if (fail) break;
-                    float R = 0.f;
-                    for (int m = 0; m < quad; ++m) R += sh.T[s][m];
-                    const float f = p.scale * exp2_approx(fmaxf(R + sh.c[s][r], kMinRow));
-                    mbar_arrive(&sh.decfree[s]);
-                    uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)w.bh * p.S + t + r) * p.Dv * 2;
-                    const bool in = t + r < w.t1;
-                    fail = !wait_warp(&sh.ofull, cn & 1, abort);
-                    if (fail) break;
-                    tc_fence_after();
+        const int r = quad * 32 + lane;
+        // a thread writes its token's row: 32 bytes at a time, whole sectors, where rows are multiples of that
+        const bool wide = (((uint32_t)p.Dv * 2) | (uint32_t)reinterpret_cast<uintptr_t>(p.out)) % 32 == 0;
+        for (; !kStatesOnly; ++cn) {
+            const int s = cn & 1;
+            ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
+            if (!ok || sh.n[s] == 0) break;
+            float R = sh.c[s][r];
 #pragma unroll 1
-                    for (int b = 0; 16 * b < p.Dv; ++b) {
-                        float x[16];
-                        tmem_ld16(tq4 + kColO + 16 * b, x);
-                        tmem_wait_ld();
-                        uint32_t o[8];
+            for (int m = 0; m < quad; ++m) R += sh.T[s][m];
+            const float f = p.scale * exp2_approx(fmaxf(R, kMinRow));
+            uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Dv * 2;
+            const bool in = r < sh.n[s];
+            mbar_arrive(&sh.decfree[s]);
+            ok = wait_warp(&sh.ofull, cn & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; 16 * b < p.Dv; ++b) {
+                float x[16];
+                tmem_ld16(tq4 + kColO + 16 * b, x);
+                tmem_wait_ld();
+                uint32_t o[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] = pack_bf16x2(f * x[2 * j], f * x[2 * j + 1]);
-                        if (in) {
-                            if (wide) {
-                                asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(row + 32 * b),
-                                             "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]),
-                                             "r"(o[7])
-                                             : "memory");
-                            } else {
-                                *reinterpret_cast<uint4*>(row + 32 * b) = make_uint4(o[0], o[1], o[2], o[3]);
-                                if (16 * b + 8 < p.Dv)
-                                    *reinterpret_cast<uint4*>(row + 32 * b + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-                            }
-                        }
+                for (int j = 0; j < 8; ++j) o[j] = pack2(mul2(pair(f, f), pair(x[2 * j], x[2 * j + 1])));
+                if (in) {
+                    if (wide) {
+                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(row + 32 * b), "r"(o[0]),
+                                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                     : "memory");
+                    } else {
+                        *reinterpret_cast<uint4*>(row + 32 * b) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (16 * b + 8 < p.Dv)
+                            *reinterpret_cast<uint4*>(row + 32 * b + 16) = make_uint4(o[4], o[5], o[6], o[7]);
                     }
-                    tc_fence_before();
-                    mbar_arrive(&sh.ofree);
                 }
             }
+            tc_fence_before();
+            mbar_arrive(&sh.ofree);
         }
     } else {
         regs_dec<kRegsCtl>();
@@ -554,36 +617,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
                 const uint32_t kb = p.Dk > 64 ? kTile : kHalf, vb = p.Dv > 64 ? kTile : kHalf;
                 int kv_issued = 0, q_issued = 0;
-                bool fail = false;
-                for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
-                    const Chunks w = chunks_of(p, split, item);
-                    const int bhk = w.b * p.Hk + w.h / (p.Hv / p.Hk);
-                    for (int c = 0; c < w.n; ++c, ++cn) {
-                        const int s = cn & 1, t = w.t0 + c * kC;
+                // tiles come into L2 two chunks before they are loaded (a load out of DRAM takes longer than a chunk): the
+                // walk is two chunks ahead of the loads
+                Walk k = first_item(it);
+                bool more = settle(k, p, it);
+                int t1 = 0, t2 = 0, bh1 = -1, bh2 = -1;  // the chunk before the walk's, and the one before that (-1: none)
+                while (more || bh1 >= 0 || bh2 >= 0) {
+                    int t0 = 0, bh0 = -1;
+                    if (more) {
+                        t0 = k.t;
+                        bh0 = k.bh;
+                        const int hk = it.group.of(bh0);
+#pragma unroll 1
+                        for (int x = 0; x < 128; x += 64) {
+                            if (x < p.Dk) {
+                                tma_prefetch_l2_3d(&tk, x, t0, hk);
+                                if (!kStatesOnly) tma_prefetch_l2_3d(&tq, x, t0, hk);
+                            }
+                            if (x < p.Dv) tma_prefetch_l2_3d(&tv, x, t0, bh0);
+                        }
+                        more = next_chunk(k, p, it);
+                    }
+                    if (bh2 >= 0) {
+                        const int s = cn & 1, bhk = it.group.of(bh2);
                         if (!kStatesOnly) {
-                            if (cn >= 2) fail = !wait_inline(&sh.qfree[s], ((cn >> 1) - 1) & 1, abort);
-                            if (fail) break;
+                            ok = cn < 2 || wait_one(&sh.qfree[s], ((cn >> 1) - 1) & 1);
+                            if (!ok) break;
                             uint8_t* qt = sm + kOffQ + s * kTile;
                             mbar_arrive_expect_tx(&sh.qfull[s], kb);
-                            tma_load_3d(qt, &tq, &sh.qfull[s], 0, t, bhk);
-                            if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, t, bhk);
+                            tma_load_3d(qt, &tq, &sh.qfull[s], 0, t2, bhk);
+                            if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, t2, bhk);
                             q_issued = cn + 1;
                         }
-                        if (cn >= 2) fail = !wait_inline(&sh.kvfree[s], ((cn >> 1) - 1) & 1, abort);
-                        if (fail) break;
+                        ok = cn < 2 || wait_one(&sh.kvfree[s], ((cn >> 1) - 1) & 1);
+                        if (!ok) break;
                         uint8_t* kt = sm + kOffK + s * kTile;
                         uint8_t* vt = sm + kOffV + s * kTile;
                         mbar_arrive_expect_tx(&sh.kvfull[s], kb + vb);
-                        tma_load_3d(kt, &tk, &sh.kvfull[s], 0, t, bhk);
-                        if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, t, bhk);
-                        tma_load_3d(vt, &tv, &sh.kvfull[s], 0, t, w.bh);
-                        if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, t, w.bh);
-                        kv_issued = cn + 1;
+                        tma_load_3d(kt, &tk, &sh.kvfull[s], 0, t2, bhk);
+                        if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, t2, bhk);
+                        tma_load_3d(vt, &tv, &sh.kvfull[s], 0, t2, bh2);
+                        if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, t2, bh2);
+                        kv_issued = ++cn;
                     }
+                    t2 = t1;
+                    bh2 = bh1;
+                    t1 = t0;
+                    bh1 = bh0;
                 }
                 // every load has landed before the CTA ends (bounded)
-                for (int i = max(0, kv_issued - 2); i < kv_issued; ++i) wait_drain(&sh.kvfull[i & 1], (i >> 1) & 1);
-                for (int i = max(0, q_issued - 2); i < q_issued; ++i) wait_drain(&sh.qfull[i & 1], (i >> 1) & 1);
+#pragma unroll 1
+                for (int i = max(0, kv_issued - 2); i < kv_issued; ++i) (void)wait_one(&sh.kvfull[i & 1], (i >> 1) & 1);
+#pragma unroll 1
+                for (int i = max(0, q_issued - 2); i < q_issued; ++i) (void)wait_one(&sh.qfull[i & 1], (i >> 1) & 1);
             }
             __syncwarp();
         } else if (warp == 25) {
@@ -595,120 +681,127 @@ __global__ void __launch_bounds__(kThreads, 1)
                                id_kv = make_idesc_bf16(128, Nk, 0, 1);
                 const Desc ds = desc_of(sbase + kOffS, 16);
                 int vi = 0;
-                bool fail = false;
-                for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
-                    const Chunks w = chunks_of(p, split, item);
-                    for (int c = 0; c < w.n; ++c, ++cn) {
-                        const int s = cn & 1, n = min(kC, w.t1 - w.t0 - c * kC), subs = (n + kSub - 1) / kSub;
-                        const uint32_t kt = sbase + kOffK + s * kTile, vt = sbase + kOffV + s * kTile;
-                        const Desc dq = desc_of(sbase + kOffQ + s * kTile, 16), dkm = desc_of(kt, kHalf);
-                        fail = !wait_inline(&sh.kvfull[s], (cn >> 1) & 1, abort);
-                        if (fail) break;
-                        if (!kStatesOnly) {
-                            fail = !wait_inline(&sh.qfull[s], (cn >> 1) & 1, abort);
-                            if (fail) break;
-                            tc_fence_after();
-                            product_rows(tmem + kColP, dq, desc_of(kt, 16), kIdQK, ksteps);
-                            mma_commit(&sh.qkfull);
-                        }
-                        // X of the chunk before has been read
-                        if (cn > 0) fail = !wait_inline(&sh.xfree, (cn - 1) & 1, abort);
-                        if (fail) break;
-#pragma unroll 1
-                        for (int u = 0; u < subs; ++u, ++vi) {
-                            const int slot = vi & 1;
-                            fail = !wait_inline(&sh.vfull[slot], (vi >> 1) & 1, abort);
-                            if (fail) break;
-                            tc_fence_after();
-                            const uint32_t av = tmem + kColV + slot * kSlotCols;
-                            Desc b = dkm;
-                            b.lo += u * (kSub * 128 / 16);
-                            if (u == 0)
-                                product_parts<true>(tmem + kColX, av, b, id_kv);
-                            else
-                                product_parts<false>(tmem + kColX, av, b, id_kv);
-                            mma_commit(&sh.vfree[slot]);
-                        }
-                        if (fail) break;
-                        mma_commit(&sh.xfull);
-                        if (kStatesOnly) {
-                            mma_commit(&sh.kvfree[s]);
-                            continue;
-                        }
-                        fail = !wait_inline(&sh.sfull, cn & 1, abort) ||
-                               (cn > 0 && !wait_inline(&sh.ofree, (cn - 1) & 1, abort));
-                        if (fail) break;
+                // the tokens of chunk cn (0: there is none) once its tiles are loaded; -1 after a wait that ran out
+                const auto next = [&] {
+                    const int s = cn & 1, ph = (cn >> 1) & 1;
+                    if (!wait_one(&sh.decfull[s], ph)) return -1;
+                    const int n = sh.n[s];
+                    mbar_arrive(&sh.decfree[s]);
+                    if (n > 0 && (!wait_one(&sh.kvfull[s], ph) || (!kStatesOnly && !wait_one(&sh.qfull[s], ph)))) return -1;
+                    return n;
+                };
+                int n = next();
+                while (n > 0) {
+                    const int s = cn & 1, subs = (n + kSub - 1) / kSub;
+                    n = -1;
+                    const Desc dq = desc_of(sbase + kOffQ + s * kTile, 16);
+                    if (!kStatesOnly) {
                         tc_fence_after();
-                        product_rows(tmem + kColO, dq, ds, id_qs, ksteps);
-                        mma_commit(&sh.sfree);
-                        mma_commit(&sh.qfree[s]);
-                        fail = !wait_inline(&sh.pfull, cn & 1, abort);
-                        if (fail) break;
-                        tc_fence_after();
-                        const Desc dvm = desc_of(vt, kHalf);
-                        if (subs == kC / kSub) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                step_ts<true>(tmem + kColO, tmem + kColP + 8 * k, dvm, k * 2048, id_pv);
-                        } else {
-#pragma unroll 1
-                            for (int k = 0; k < 2 * subs; ++k)
-                                step_ts<true>(tmem + kColO, tmem + kColP + 8 * k, dvm, k * 2048, id_pv);
-                        }
-                        mma_commit(&sh.ofull);
-                        mma_commit(&sh.kvfree[s]);
+                        product_rows(tmem + kColP, dq, desc_of(sbase + kOffK + s * kTile, 16), kIdQK, ksteps);
+                        mma_commit(&sh.qkfull);
                     }
+                    // X of the chunk before has been read
+                    if (cn > 0 && !wait_one(&sh.xfree, (cn - 1) & 1)) break;
+                    Desc b = desc_of(sbase + kOffK + s * kTile, kHalf);
+                    int u = 0;
+#pragma unroll 1
+                    for (; u < subs; ++u, ++vi) {
+                        const int slot = vi & 1;
+                        if (!wait_one(&sh.vfull[slot], (vi >> 1) & 1)) break;
+                        tc_fence_after();
+                        product_parts(tmem + kColX, tmem + kColV + slot * kSlotCols, b, id_kv, u > 0);
+                        mma_commit(&sh.vfree[slot]);
+                        b.lo += kSub * 128 / 16;
+                    }
+                    if (u < subs) break;
+                    mma_commit(&sh.xfull);
+                    if (kStatesOnly) {
+                        mma_commit(&sh.kvfree[s]);
+                        ++cn;
+                        n = next();
+                        continue;
+                    }
+                    if (!wait_one(&sh.sfull, cn & 1) || (cn > 0 && !wait_one(&sh.ofree, (cn - 1) & 1))) break;
+                    tc_fence_after();
+                    product_rows(tmem + kColO, dq, ds, id_qs, ksteps);
+                    mma_commit(&sh.sfree);
+                    mma_commit(&sh.qfree[s]);
+                    // while these run: the next chunk's tiles, so that its scores follow P V at once
+                    ++cn;
+                    const int m = next();
+                    if (m < 0 || !wait_one(&sh.pfull, (cn - 1) & 1)) break;
+                    tc_fence_after();
+                    const Desc dvm = desc_of(sbase + kOffV + s * kTile, kHalf);
+                    if (subs == kC / kSub) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            step_ts<true>(tmem + kColO, tmem + kColP + 8 * i, dvm, i * 2048, id_pv);
+                    } else {
+#pragma unroll 1
+                        for (int i = 0; i < 2 * subs; ++i)
+                            step_ts<true>(tmem + kColO, tmem + kColP + 8 * i, dvm, i * 2048, id_pv);
+                    }
+                    mma_commit(&sh.ofull);
+                    mma_commit(&sh.kvfree[s]);
+                    n = m;
                 }
+                ok = n == 0;
                 // every product has ended before the tensor memory is freed (bounded)
                 mma_commit(&sh.drain);
-                wait_drain(&sh.drain, 0);
+                (void)wait_one(&sh.drain, 0);
             }
             __syncwarp();
         } else if (warp == 26) {
-            // -------------------------------------------------------- decays
-            bool fail = false;
-            for (int item = blockIdx.x; item < items && !fail; item += gridDim.x) {
-                const Chunks w = chunks_of(p, split, item);
-                const float* g = p.head_decay ? p.g_log + w.h : p.g_log + (long long)w.bh * p.S;
-                for (int c = 0; c < w.n; ++c, ++cn) {
-                    const int s = cn & 1, t = w.t0 + c * kC;
-                    float x[4];
+            // -------------------------------------------------------- decays, and the walk that most roles follow
+            Walk k = first_item(it);
+            for (bool more = settle(k, p, it);; ++cn) {
+                const int s = cn & 1, n = more ? min(kC, k.end - k.t) : 0;
+                float x[4] = {};
+                if (more) {
+                    const float* g =
+                        p.g_log + (p.head_decay ? k.bh - it.hv.of(k.bh) * p.Hv : (long long)k.bh * p.S + k.t + lane);
 #pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int tok = t + 32 * b + lane;
-                        x[b] = 0.f;
-                        if (tok < w.t1) x[b] = least_decay(p.head_decay ? *g : g[tok]);
-                    }
-                    if (cn >= 2) {
-                        fail = !wait_warp(&sh.decfree[s], ((cn >> 1) - 1) & 1, abort);
-                        if (fail) break;
-                    }
-                    float T[4], behind = 0.f;
-#pragma unroll
-                    for (int b = 3; b >= 0; --b) {
-                        float up = x[b], down = x[b];
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const float y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_down_sync(0xffffffffu, down, o);
-                            if (lane >= o) up += y;
-                            if (lane + o < 32) down += z;
-                        }
-                        const float after = __shfl_down_sync(0xffffffffu, down, 1);
-                        sh.c[s][32 * b + lane] = kLog2e * up;
-                        sh.h[s][32 * b + lane] = expf(lane < 31 ? after : 0.f);
-                        T[b] = __shfl_sync(0xffffffffu, down, 0);
-                        if (lane == 0) {
-                            sh.T[s][b] = kLog2e * T[b];
-                            sh.w[s][b] = expf(behind);
-                        }
-                        behind += T[b];
-                    }
-                    if (lane == 0) sh.total[s] = expf(behind);
-                    mbar_arrive(&sh.decfull[s]);
+                    for (int b = 0; b < 4; ++b)
+                        if (32 * b + lane < n) x[b] = least_decay(g[p.head_decay ? 0 : 32 * b]);
                 }
+                ok = cn < 2 || wait_warp(&sh.decfree[s], ((cn >> 1) - 1) & 1);
+                if (!ok) break;
+                if (lane == 0) {
+                    sh.bh[s] = k.bh;
+                    sh.t[s] = k.t;
+                    sh.n[s] = n;
+                }
+                if (!more) {
+                    mbar_arrive(&sh.decfull[s]);
+                    break;
+                }
+                more = next_chunk(k, p, it);
+                float behind = 0.f;
+#pragma unroll 1
+                for (int b = 3; b >= 0; --b) {
+                    float up = x[3], down = x[3];
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const float y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_down_sync(0xffffffffu, down, o);
+                        if (lane >= o) up += y;
+                        if (lane + o < 32) down += z;
+                    }
+                    const float after = __shfl_down_sync(0xffffffffu, down, 1), T = __shfl_sync(0xffffffffu, down, 0);
+                    sh.c[s][32 * b + lane] = kLog2e * up;
+                    sh.h[s][32 * b + lane] = expf(lane < 31 ? after : 0.f);
+                    if (lane == 0) {
+                        sh.T[s][b] = kLog2e * T;
+                        sh.w[s][b] = expf(behind);
+                    }
+                    behind += T;
+                    x[3] = x[2], x[2] = x[1], x[1] = x[0];
+                }
+                if (lane == 0) sh.total[s] = expf(behind);
+                mbar_arrive(&sh.decfull[s]);
             }
         }
     }
+    if (!ok) sh.gave_up = 1;
     griddep_launch_dependents();
     tc_fence_before();
     __syncthreads();
@@ -717,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
         tmem_dealloc(tmem, 512);
     }
-    if (tid == 0 && sh.abort && status) atomicExch(status, (int32_t)GDN_ERR_TIMEOUT);
+    if (tid == 0 && sh.gave_up && status) atomicExch(status, (int32_t)GDN_ERR_TIMEOUT);
 }
 
 // ------------------------------------------------------------------ host side
@@ -763,6 +856,7 @@ gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAt
     if (allow_smem(kernel, (int)kSmem, allowed, dev) != cudaSuccess) return GDN_ERR_CUDA;
     const long long items = (long long)p.B * p.Hv * (kStatesOnly ? s.P - 1 : s.P);
     if (items > INT32_MAX - sms) return GDN_ERR_DIMS;  // (items are counted in 32 bits)
+    const Items it{p.B * p.Hv, kStatesOnly ? s.P - 1 : s.P, s.P > 1 ? s.len : p.S, divisor(p.Hv), divisor(p.Hv / p.Hk)};
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
     cfg.blockDim = dim3(kThreads);
@@ -773,7 +867,7 @@ gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], p, s, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
