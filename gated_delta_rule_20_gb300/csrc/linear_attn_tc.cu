@@ -58,7 +58,7 @@ struct Small {
     float w[2][4];       // e^(the log-decays behind the block)
     float total[2];      // e^(the chunk's)
     int bh[2], t[2], n[2];  // its head, its first token, and how many it has (0: there is no further chunk)
-    uint64_t kvfull[2], kvfree[2], qfull[2], qfree[2], decfull[2], decfree[2];
+    uint64_t kvfull[2], kvfree[2], qfull[2], staged[2], decfull[2], decfree[2];
     uint64_t vfull[kSlots], vfree[kSlots];
     uint64_t sfull, sfree, xfull, xfree, qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
@@ -118,11 +118,6 @@ __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigne
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ unsigned long long sub2(unsigned long long a, unsigned long long b) {
-    unsigned long long r;
-    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
     unsigned long long r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -130,19 +125,32 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
 }
 __device__ __forceinline__ uint32_t pack2(unsigned long long x) { return pack_bf16x2(pair_lo(x), pair_hi(x)); }
 
-// The two bf16 values in m, times d, as the sum of three bf16 values each: an fp32 product's 24 bits cut off 8 at a
-// time.  The cut parts' differences are exact.
-__device__ __forceinline__ void three_parts(uint32_t m, unsigned long long d, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
-    constexpr uint32_t kCut = 0xffff0000u;
-    const auto join = [](uint32_t lo, uint32_t hi) { return (unsigned long long)hi << 32 | lo; };
-    const unsigned long long x = mul2(join(m << 16, m & kCut), d);
-    uint32_t a = (uint32_t)x, b = (uint32_t)(x >> 32);
-    p0 = __byte_perm(a, b, 0x7632);
-    const unsigned long long r = sub2(x, join(a & kCut, b & kCut));
-    a = (uint32_t)r, b = (uint32_t)(r >> 32);
-    p1 = __byte_perm(a, b, 0x7632);
-    const unsigned long long r2 = sub2(r, join(a & kCut, b & kCut));
-    p2 = __byte_perm((uint32_t)r2, (uint32_t)(r2 >> 32), 0x7632);
+// The two bf16 values in x, as fp32, and a - (those): products and sums of fp32 with bf16 (fma.rn.f32.bf16), which run on the
+// FMA pipe, where shifts, masks and byte permutations take the ALU's, at half the rate and shared with everything else.
+__device__ __forceinline__ void widen2(uint32_t x, float& lo, float& hi) {
+    asm("{\n\t.reg .b16 l, h, one;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 one, 0x3F80;\n\t"
+        "fma.rn.f32.bf16 %0, l, one, %3;\n\tfma.rn.f32.bf16 %1, h, one, %3;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(x), "f"(-0.f));
+}
+__device__ __forceinline__ void less2(uint32_t x, float& lo, float& hi) {
+    asm("{\n\t.reg .b16 l, h, minus;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 minus, 0xBF80;\n\t"
+        "fma.rn.f32.bf16 %0, l, minus, %0;\n\tfma.rn.f32.bf16 %1, h, minus, %1;\n\t}"
+        : "+f"(lo), "+f"(hi)
+        : "r"(x));
+}
+// The two bf16 values in m, times d, as the sum of three bf16 values each: an fp32 product's 24 bits, 8 at a time (the
+// differences are exact).
+__device__ __forceinline__ void three_parts(uint32_t m, float d0, float d1, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
+    float a, b;
+    widen2(m, a, b);
+    a *= d0;
+    b *= d1;
+    p0 = pack_bf16x2(a, b);
+    less2(p0, a, b);
+    p1 = pack_bf16x2(a, b);
+    less2(p1, a, b);
+    p2 = pack_bf16x2(a, b);
 }
 
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -284,8 +292,8 @@ __device__ __forceinline__ void column_rows(int pitch, int rows, F f) {
 template <bool kStatesOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ LinearAttn p,
-                          const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
+                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                          const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small& sh = *reinterpret_cast<Small*>(sm + kOffSmall);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
@@ -301,9 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.kvfull[i], 1);
             mbar_init(&sh.kvfree[i], 1);
             mbar_init(&sh.qfull[i], 1);
-            mbar_init(&sh.qfree[i], 1);
+            mbar_init(&sh.staged[i], 128);
             mbar_init(&sh.decfull[i], 32);
-            mbar_init(&sh.decfree[i], kStatesOnly ? 513 : 769);
+            mbar_init(&sh.decfree[i], kStatesOnly ? 514 : 770);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.vfull[i], 256);
@@ -324,7 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 24 && elect_one()) {
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
-        if (!kStatesOnly) tma_prefetch_desc(&tq);
+        if (!kStatesOnly) {
+            tma_prefetch_desc(&tq);
+            tma_prefetch_desc(&to);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -349,37 +360,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_warp(&sh.qkfull, cn & 1);
             if (!ok) break;
             tc_fence_after();
-            // 16 columns at a time, in loops that stay small: the roles share the instruction caches
+            // 16 columns at a time, the next 16 on their way; loops that stay small: the roles share the
+            // instruction caches.  What is written lies over score columns that this warp has read
             float between = shift + (a > 0 ? R - sh.T[s][0] : 0.f);  // c_i - m_i less the end of block b
+            float x[16], y[16];
+            tmem_ld16(tq4 + kColP, x);
+            const auto off_diagonal = [&](const float (&v)[16], unsigned long long uu, int col) {
+                uint32_t pk[8];
+                const float4* h = reinterpret_cast<const float4*>(&sh.h[s][col]);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                    const float4 hj = h[j / 4];
+                    pk[j / 2] = pack2(mul2(pair(v[j], v[j + 1]), mul2(uu, pair(hj.x, hj.y))));
+                    pk[j / 2 + 1] = pack2(mul2(pair(v[j + 2], v[j + 3]), mul2(uu, pair(hj.z, hj.w))));
+                }
+                tmem_st8u(tq4 + kColP + col / 2, pk);
+            };
 #pragma unroll 1
             for (int b = 0; b < a; ++b) {
                 const float u = exp2_approx(between);
                 const unsigned long long uu = pair(u, u);
                 between -= b + 1 < a ? sh.T[s][b + 1] : 0.f;
-#pragma unroll 1
-                for (int j0 = 0; j0 < 32; j0 += 16) {
-                    float x[16];
-                    uint32_t pk[8];
-                    tmem_ld16(tq4 + kColP + 32 * b + j0, x);
-                    const float4* h = reinterpret_cast<const float4*>(&sh.h[s][32 * b + j0]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        const float4 hj = h[j / 4];
-                        pk[j / 2] = pack2(mul2(pair(x[j], x[j + 1]), mul2(uu, pair(hj.x, hj.y))));
-                        pk[j / 2 + 1] = pack2(mul2(pair(x[j + 2], x[j + 3]), mul2(uu, pair(hj.z, hj.w))));
-                    }
-                    // (over score columns that this warp has read)
-                    tmem_st8u(tq4 + kColP + 16 * b + j0 / 2, pk);
-                }
+                tmem_wait_ld();
+                tmem_ld16(tq4 + kColP + 32 * b + 16, y);
+                off_diagonal(x, uu, 32 * b);
+                tmem_wait_ld();
+                tmem_ld16(tq4 + kColP + 32 * b + 32, x);
+                off_diagonal(y, uu, 32 * b + 16);
             }
+            tmem_wait_ld();
+            tmem_ld16(tq4 + kColP + 32 * a + 16, y);
 #pragma unroll 1
             for (int j0 = 0; j0 < 32; j0 += 16) {  // the diagonal block
-                float x[16];
                 uint32_t pk[8];
-                tmem_ld16(tq4 + kColP + 32 * a + j0, x);
                 const float4* cc = reinterpret_cast<const float4*>(&sh.c[s][32 * a + j0]);
-                tmem_wait_ld();
                 const int last = lane - j0;
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
@@ -392,6 +406,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pk[j / 2 + 1] = pack_bf16x2(y2, y3);
                 }
                 tmem_st8u(tq4 + kColP + 16 * a + j0 / 2, pk);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = y[j];
             }
 #pragma unroll 1
             for (int b = 2 * a + 2; b < 8; ++b) {  // columns behind the row's block
@@ -530,22 +547,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             uint32_t from = smem_u32(vt) + piece;
             const float* h = &sh.h[s][o2 * 16 + 2 * (lane & 3)];
+            uint32_t m[2][4];
+            float2 hh[2];
+            const auto fetch = [&] {  // a slot's 16 tokens of this warp
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    ldmatrix_x4_trans(from + o * 1024, m[o]);
+                    hh[o] = *reinterpret_cast<const float2*>(h + 8 * o);
+                }
+                from += kSub * 128;
+                h += kSub;
+            };
+            fetch();
 #pragma unroll 1
-            for (int u = 0; u < subs; ++u, ++vi, from += kSub * 128, h += kSub) {
+            for (int u = 0; u < subs; ++u, ++vi) {
                 const int slot = vi & 1, turn = vi >> 1;
                 uint32_t part[3][2][4];  // [part][8 tokens][8 columns dv], made before the slot is free
-                if (there) {
-                    const float wb = sh.w[s][u];
+                const float wb = sh.w[s][u];
 #pragma unroll
-                    for (int o = 0; o < 2; ++o) {
-                        uint32_t m[4];
-                        ldmatrix_x4_trans(from + o * 1024, m);
-                        const float2 hh = *reinterpret_cast<const float2*>(h + 8 * o);
-                        const unsigned long long d = mul2(pair(hh.x, hh.y), pair(wb, wb));
+                for (int o = 0; o < 2; ++o) {
+                    const float d0 = hh[o].x * wb, d1 = hh[o].y * wb;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) three_parts(m[i], d, part[0][o][i], part[1][o][i], part[2][o][i]);
-                    }
+                    for (int i = 0; i < 4; ++i) three_parts(m[o][i], d0, d1, part[0][o][i], part[1][o][i], part[2][o][i]);
                 }
+                if (u + 1 < subs) fetch();
                 if (turn > 0) {
                     ok = wait_warp(&sh.vfree[slot], (turn - 1) & 1);
                     if (!ok) break;
@@ -571,40 +596,55 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ outputs
         regs_dec<kRegsO>();
         const int r = quad * 32 + lane;
-        // a thread writes its token's row: 32 bytes at a time, whole sectors, where rows are multiples of that
-        const bool wide = (((uint32_t)p.Dv * 2) | (uint32_t)reinterpret_cast<uintptr_t>(p.out)) % 32 == 0;
         for (; !kStatesOnly; ++cn) {
             const int s = cn & 1;
             ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
-            if (!ok || sh.n[s] == 0) break;
+            const int n = sh.n[s];
+            if (!ok || n == 0) break;
             float R = sh.c[s][r];
 #pragma unroll 1
             for (int m = 0; m < quad; ++m) R += sh.T[s][m];
             const float f = p.scale * exp2_approx(fmaxf(R, kMinRow));
             uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Dv * 2;
-            const bool in = r < sh.n[s];
+            // whole chunks and the tensor's end go out by TMA, from q's tile (its products are done); where a length
+            // ends inside a chunk, a thread writes its row itself
+            const bool tma = n == kC || sh.t[s] + n == p.S;
             mbar_arrive(&sh.decfree[s]);
             ok = wait_warp(&sh.ofull, cn & 1);
             if (!ok) break;
             tc_fence_after();
-#pragma unroll 1
-            for (int b = 0; 16 * b < p.Dv; ++b) {
-                float x[16];
-                tmem_ld16(tq4 + kColO + 16 * b, x);
-                tmem_wait_ld();
+            uint8_t* tile = sm + kOffQ + s * kTile + r * 128;
+            const auto put = [&](const float (&x)[16], int col) {
                 uint32_t o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = pack2(mul2(pair(f, f), pair(x[2 * j], x[2 * j + 1])));
-                if (in) {
-                    if (wide) {
-                        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(row + 32 * b), "r"(o[0]),
-                                     "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                     : "memory");
-                    } else {
-                        *reinterpret_cast<uint4*>(row + 32 * b) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (16 * b + 8 < p.Dv)
-                            *reinterpret_cast<uint4*>(row + 32 * b + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
+                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                if (tma) {
+                    uint8_t* half = tile + (col >> 6) * kHalf;
+                    const int ch = (col & 63) >> 3;
+                    *reinterpret_cast<uint4*>(half + ((ch ^ (r & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(half + (((ch + 1) ^ (r & 7)) << 4)) = hi;
+                } else if (r < n) {
+                    if (col < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col) = lo;
+                    if (col + 8 < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col + 16) = hi;
+                }
+            };
+            // (columns past Dv come from whatever the tensor memory holds, and are not written)
+            float x[16], y[16];
+            tmem_ld16(tq4 + kColO, x);
+#pragma unroll 1
+            for (int col = 0; col < 128; col += 32) {
+                if (col < p.Dv) {
+                    tmem_wait_ld();
+                    tmem_ld16(tq4 + kColO + col + 16, y);
+                    put(x, col);
+                    tmem_wait_ld();
+                    if (col + 32 < p.Dv) tmem_ld16(tq4 + kColO + col + 32, x);
+                    put(y, col + 16);
+                }
+                if (col & 32) {
+                    fence_proxy_async_smem();
+                    mbar_arrive(&sh.staged[col >> 6]);
                 }
             }
             tc_fence_before();
@@ -617,54 +657,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
                 const uint32_t kb = p.Dk > 64 ? kTile : kHalf, vb = p.Dv > 64 ? kTile : kHalf;
                 int kv_issued = 0, q_issued = 0;
-                // tiles come into L2 two chunks before they are loaded (a load out of DRAM takes longer than a chunk): the
-                // walk is two chunks ahead of the loads
+                // The outputs of chunk cn - 2 leave the q tile that chunk cn takes, a half of the channels at a time
+                struct {
+                    int t, bh, n;
+                } was[2] = {{0, 0, 0}, {0, 0, 0}};  // chunks cn - 2 and cn - 1 (n = 0: none)
+                const auto store_half = [&](int half, int stage, int ph) {
+                    if (!wait_one(&sh.staged[half], ph)) return false;
+                    if (64 * half < p.Dv && (was[0].n == kC || was[0].t + was[0].n == p.S))
+                        tma_store_3d(&to, sm + kOffQ + stage * kTile + half * kHalf, 64 * half, was[0].t, was[0].bh);
+                    tma_store_commit();
+                    return true;
+                };
                 Walk k = first_item(it);
                 bool more = settle(k, p, it);
-                int t1 = 0, t2 = 0, bh1 = -1, bh2 = -1;  // the chunk before the walk's, and the one before that (-1: none)
-                while (more || bh1 >= 0 || bh2 >= 0) {
-                    int t0 = 0, bh0 = -1;
+                for (; more || was[0].n || was[1].n; ++cn) {
+                    const int s = cn & 1, bhk = it.group.of(k.bh);
                     if (more) {
-                        t0 = k.t;
-                        bh0 = k.bh;
-                        const int hk = it.group.of(bh0);
-#pragma unroll 1
-                        for (int x = 0; x < 128; x += 64) {
-                            if (x < p.Dk) {
-                                tma_prefetch_l2_3d(&tk, x, t0, hk);
-                                if (!kStatesOnly) tma_prefetch_l2_3d(&tq, x, t0, hk);
-                            }
-                            if (x < p.Dv) tma_prefetch_l2_3d(&tv, x, t0, bh0);
-                        }
-                        more = next_chunk(k, p, it);
-                    }
-                    if (bh2 >= 0) {
-                        const int s = cn & 1, bhk = it.group.of(bh2);
-                        if (!kStatesOnly) {
-                            ok = cn < 2 || wait_one(&sh.qfree[s], ((cn >> 1) - 1) & 1);
-                            if (!ok) break;
-                            uint8_t* qt = sm + kOffQ + s * kTile;
-                            mbar_arrive_expect_tx(&sh.qfull[s], kb);
-                            tma_load_3d(qt, &tq, &sh.qfull[s], 0, t2, bhk);
-                            if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, t2, bhk);
-                            q_issued = cn + 1;
-                        }
                         ok = cn < 2 || wait_one(&sh.kvfree[s], ((cn >> 1) - 1) & 1);
                         if (!ok) break;
                         uint8_t* kt = sm + kOffK + s * kTile;
                         uint8_t* vt = sm + kOffV + s * kTile;
                         mbar_arrive_expect_tx(&sh.kvfull[s], kb + vb);
-                        tma_load_3d(kt, &tk, &sh.kvfull[s], 0, t2, bhk);
-                        if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, t2, bhk);
-                        tma_load_3d(vt, &tv, &sh.kvfull[s], 0, t2, bh2);
-                        if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, t2, bh2);
-                        kv_issued = ++cn;
+                        tma_load_3d(vt, &tv, &sh.kvfull[s], 0, k.t, k.bh);
+                        if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, k.t, k.bh);
+                        tma_load_3d(kt, &tk, &sh.kvfull[s], 0, k.t, bhk);
+                        if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, k.t, bhk);
+                        kv_issued = cn + 1;
                     }
-                    t2 = t1;
-                    bh2 = bh1;
-                    t1 = t0;
-                    bh1 = bh0;
+                    if (kStatesOnly) {
+                        more = next_chunk(k, p, it);
+                        continue;
+                    }
+                    if (was[0].n) {
+                        ok = store_half(0, s, cn & 1) && store_half(1, s, cn & 1);
+                        if (!ok) break;
+                    }
+                    uint8_t* qt = sm + kOffQ + s * kTile;
+                    if (more) mbar_arrive_expect_tx(&sh.qfull[s], kb);
+                    tma_store_wait_read1();
+                    if (more) tma_load_3d(qt, &tq, &sh.qfull[s], 0, k.t, bhk);
+                    tma_store_wait_read0();
+                    if (more && p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, k.t, bhk);
+                    was[0] = was[1];
+                    was[1].n = 0;
+                    if (more) {
+                        q_issued = cn + 1;
+                        was[1] = {k.t, k.bh, min(kC, k.end - k.t)};
+                        more = next_chunk(k, p, it);
+                    }
                 }
+                tma_store_wait_all0();
                 // every load has landed before the CTA ends (bounded)
 #pragma unroll 1
                 for (int i = max(0, kv_issued - 2); i < kv_issued; ++i) (void)wait_one(&sh.kvfull[i & 1], (i >> 1) & 1);
@@ -725,11 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     product_rows(tmem + kColO, dq, ds, id_qs, ksteps);
                     mma_commit(&sh.sfree);
-                    mma_commit(&sh.qfree[s]);
-                    // while these run: the next chunk's tiles, so that its scores follow P V at once
-                    ++cn;
-                    const int m = next();
-                    if (m < 0 || !wait_one(&sh.pfull, (cn - 1) & 1)) break;
+                    if (!wait_one(&sh.pfull, cn & 1)) break;
                     tc_fence_after();
                     const Desc dvm = desc_of(sbase + kOffV + s * kTile, kHalf);
                     if (subs == kC / kSub) {
@@ -743,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     mma_commit(&sh.ofull);
                     mma_commit(&sh.kvfree[s]);
-                    n = m;
+                    ++cn;
+                    n = next();
                 }
                 ok = n == 0;
                 // every product has ended before the tensor memory is freed (bounded)
@@ -754,28 +793,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 26) {
             // -------------------------------------------------------- decays, and the walk that most roles follow
             Walk k = first_item(it);
-            for (bool more = settle(k, p, it);; ++cn) {
-                const int s = cn & 1, n = more ? min(kC, k.end - k.t) : 0;
-                float x[4] = {};
-                if (more) {
-                    const float* g =
-                        p.g_log + (p.head_decay ? k.bh - it.hv.of(k.bh) * p.Hv : (long long)k.bh * p.S + k.t + lane);
+            bool more = settle(k, p, it);
+            float g[4];  // the log-decays of the walk's chunk, a chunk before they are used
+            const auto fetch = [&] {
+                const float* from =
+                    p.g_log + (p.head_decay ? k.bh - it.hv.of(k.bh) * p.Hv : (long long)k.bh * p.S + k.t + lane);
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        if (32 * b + lane < n) x[b] = least_decay(g[p.head_decay ? 0 : 32 * b]);
-                }
+                for (int b = 0; b < 4; ++b) g[b] = 32 * b + lane < k.end - k.t ? from[p.head_decay ? 0 : 32 * b] : 0.f;
+            };
+            if (more) fetch();
+            for (;; ++cn) {
+                const int s = cn & 1;
                 ok = cn < 2 || wait_warp(&sh.decfree[s], ((cn >> 1) - 1) & 1);
                 if (!ok) break;
                 if (lane == 0) {
                     sh.bh[s] = k.bh;
                     sh.t[s] = k.t;
-                    sh.n[s] = n;
+                    sh.n[s] = more ? min(kC, k.end - k.t) : 0;
                 }
                 if (!more) {
                     mbar_arrive(&sh.decfull[s]);
                     break;
                 }
+                float x[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) x[b] = least_decay(g[b]);
                 more = next_chunk(k, p, it);
+                if (more) fetch();
                 float behind = 0.f;
 #pragma unroll 1
                 for (int b = 3; b >= 0; --b) {
@@ -798,6 +842,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lane == 0) sh.total[s] = expf(behind);
                 mbar_arrive(&sh.decfull[s]);
+            }
+        } else {
+            // -------------------------------------------------------- tiles into L2, ahead of their loads
+            // The CTAs run in step and ask for their tiles at the same time; asked for two chunks early, they come
+            // evenly.  (By plain prefetches: TMA's own would queue in front of its loads.)
+            const auto lines = [&](const void* base, long long row, int n, int D, int size) {
+                const uint8_t* from = static_cast<const uint8_t*>(base) + row * D * size;
+#pragma unroll 1
+                for (int i = lane * 128; i < n * D * size; i += 32 * 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+            };
+            Walk k = first_item(it);
+            bool more = settle(k, p, it);
+            for (;; ++cn) {
+#pragma unroll 1
+                for (int i = cn ? 1 : 3; i > 0 && more; --i, more = next_chunk(k, p, it)) {
+                    const int n = min(kC, k.end - k.t);
+                    const long long hk = (long long)it.group.of(k.bh) * p.S + k.t, hv = (long long)k.bh * p.S + k.t;
+                    if (!p.head_decay) lines(p.g_log, hv, n, 1, 4);
+                    lines(p.k, hk, n, p.Dk, 2);
+                    lines(p.v, hv, n, p.Dv, 2);
+                    if (!kStatesOnly) lines(p.q, hk, n, p.Dk, 2);
+                }
+                const int s = cn & 1;
+                ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
+                if (!ok || sh.n[s] == 0) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.decfree[s]);
             }
         }
     }
@@ -843,7 +915,7 @@ bool encode(CUtensorMap* map, const void* ptr, long long heads, int S, int D) {
 }
 
 template <bool kStatesOnly>
-gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
+gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
                   int32_t* status, cudaStream_t stream) {
     auto* kernel = linear_attn_tc_kernel<kStatesOnly>;
     static const int regs = [&] {
@@ -867,7 +939,7 @@ gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -879,9 +951,10 @@ bool linear_attn_tc_supported(const LinearAttn& p) {
 
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream) {
-    CUtensorMap m[3];
+    CUtensorMap m[4];
     const long long hk = (long long)p.B * p.Hk, hv = (long long)p.B * p.Hv;
-    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv))
+    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv) ||
+        !encode(&m[3], p.out, hv, p.S, p.Dv))
         return GDN_ERR_CUDA;
     if (s.P > 1) {
         const gdn_status e = launch<true>(m, p, s, dev, sms, status, stream);
