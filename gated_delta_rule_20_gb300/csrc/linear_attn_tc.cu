@@ -48,7 +48,7 @@ constexpr uint32_t kColP = 0, kColO = 128, kColX = 256, kColV = 384, kSlotCols =
 constexpr float kMinRow = -64.f * kLog2e;  // least m_i, in powers of two
 
 // Registers a thread of each role; what the block is launched with covers their sum (launch checks it).
-constexpr int kRegsP = 72, kRegsS = 112, kRegsV = 56, kRegsO = 48, kRegsCtl = 48;
+constexpr int kRegsP = 72, kRegsS = 112, kRegsV = 56, kRegsO = 56, kRegsCtl = 40;
 constexpr int kRegsSum = (kRegsP + 2 * kRegsS + 2 * kRegsV + kRegsO + kRegsCtl) * 128;
 
 struct Small {
@@ -58,7 +58,7 @@ struct Small {
     float w[2][4];       // e^(the log-decays behind the block)
     float total[2];      // e^(the chunk's)
     int bh[2], t[2], n[2];  // its head, its first token, and how many it has (0: there is no further chunk)
-    uint64_t kvfull[2], kvfree[2], qfull[2], staged[2], decfull[2], decfree[2];
+    uint64_t kvfull[2], kvfree[2], qfull[2], qfree[2], decfull[2], decfree[2];
     uint64_t vfull[kSlots], vfree[kSlots];
     uint64_t sfull, sfree, xfull, xfree, qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
@@ -93,12 +93,13 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
 }
 
 // Waits, inline (a kernel that shares out its registers cannot call functions) and few instructions long (there are many
-// of them): 4 million tests, each of which blocks for a short time that the hardware chooses, then false.
-constexpr uint32_t kMostTests = 1u << 22;
+// of them): a million tests, each of which suspends the thread for up to 2 us, then false.  (Shorter suspensions are more
+// instructions for the others to wait behind: 4 % of the whole kernel.)
+constexpr uint32_t kMostTests = 1u << 20, kTestNs = 2000;
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
     uint32_t i = 0;
 #pragma unroll 1
-    while (!mbar_try_wait(bar, parity))
+    while (!mbar_try_wait_sleep(bar, parity, kTestNs))
         if (++i == kMostTests) return false;
     return true;
 }
@@ -292,8 +293,8 @@ __device__ __forceinline__ void column_rows(int pitch, int rows, F f) {
 template <bool kStatesOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
-                          const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
+                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ LinearAttn p,
+                          const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small& sh = *reinterpret_cast<Small*>(sm + kOffSmall);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.kvfull[i], 1);
             mbar_init(&sh.kvfree[i], 1);
             mbar_init(&sh.qfull[i], 1);
-            mbar_init(&sh.staged[i], 128);
+            mbar_init(&sh.qfree[i], 1);
             mbar_init(&sh.decfull[i], 32);
             mbar_init(&sh.decfree[i], kStatesOnly ? 514 : 770);
         }
@@ -332,10 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 24 && elect_one()) {
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
-        if (!kStatesOnly) {
-            tma_prefetch_desc(&tq);
-            tma_prefetch_desc(&to);
-        }
+        if (!kStatesOnly) tma_prefetch_desc(&tq);
     }
     tc_fence_before();
     __syncthreads();
@@ -596,6 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ outputs
         regs_dec<kRegsO>();
         const int r = quad * 32 + lane;
+        const bool wide = (((uint32_t)p.Dv * 2) | (uint32_t)reinterpret_cast<uintptr_t>(p.out)) % 32 == 0;
         for (; !kStatesOnly; ++cn) {
             const int s = cn & 1;
             ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
@@ -605,50 +604,74 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int m = 0; m < quad; ++m) R += sh.T[s][m];
             const float f = p.scale * exp2_approx(fmaxf(R, kMinRow));
-            uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Dv * 2;
-            // whole chunks and the tensor's end go out by TMA, from q's tile (its products are done); where a length
-            // ends inside a chunk, a thread writes its row itself
-            const bool tma = n == kC || sh.t[s] + n == p.S;
+            // this lane's rows are lane / 4 of every 8; it writes 16 channels of each 64
+            uint8_t* rows = static_cast<uint8_t*>(p.out) +
+                            (((long long)sh.bh[s] * p.S + sh.t[s] + quad * 32 + (lane >> 2)) * p.Dv + (lane & 3) * 16) * 2;
             mbar_arrive(&sh.decfree[s]);
             ok = wait_warp(&sh.ofull, cn & 1);
             if (!ok) break;
             tc_fence_after();
-            uint8_t* tile = sm + kOffQ + s * kTile + r * 128;
-            const auto put = [&](const float (&x)[16], int col) {
-                uint32_t o[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = pack2(mul2(pair(f, f), pair(x[2 * j], x[2 * j + 1])));
-                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                if (tma) {
-                    uint8_t* half = tile + (col >> 6) * kHalf;
-                    const int ch = (col & 63) >> 3;
-                    *reinterpret_cast<uint4*>(half + ((ch ^ (r & 7)) << 4)) = lo;
-                    *reinterpret_cast<uint4*>(half + (((ch + 1) ^ (r & 7)) << 4)) = hi;
-                } else if (r < n) {
-                    if (col < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col) = lo;
-                    if (col + 8 < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col + 16) = hi;
-                }
-            };
-            // (columns past Dv come from whatever the tensor memory holds, and are not written)
-            float x[16], y[16];
-            tmem_ld16(tq4 + kColO, x);
+            const bool odd = lane & 1, high = lane & 2;
+            // 16 lanes of the tensor memory and 64 columns at a time
 #pragma unroll 1
-            for (int col = 0; col < 128; col += 32) {
-                if (col < p.Dv) {
+            for (int part = 0; part < 4; ++part) {
+                const int r16 = (part & 1) * 16, col = (part >> 1) * 64;
+                if (col >= p.Dv) break;
+                uint32_t w[2][8];  // rows lane / 4 and + 8: word k = columns 8 k + 2 (lane % 4) and + 1
+                float fr[2];
+                fr[0] = __shfl_sync(0xffffffffu, f, r16 + (lane >> 2));
+                fr[1] = __shfl_sync(0xffffffffu, f, r16 + 8 + (lane >> 2));
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x[16];
+                    tmem_ld16x256_x4(tq4 + ((uint32_t)r16 << 16) + kColO + col + 32 * c, x);
                     tmem_wait_ld();
-                    tmem_ld16(tq4 + kColO + col + 16, y);
-                    put(x, col);
-                    tmem_wait_ld();
-                    if (col + 32 < p.Dv) tmem_ld16(tq4 + kColO + col + 32, x);
-                    put(y, col + 16);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            w[i][4 * c + k] = pack2(mul2(pair(fr[i], fr[i]), pair(x[4 * k + 2 * i], x[4 * k + 2 * i + 1])));
                 }
-                if (col & 32) {
-                    fence_proxy_async_smem();
-                    mbar_arrive(&sh.staged[col >> 6]);
+                if (part == 3 || (p.Dv <= 64 && part == 1)) {
+                    tc_fence_before();
+                    mbar_arrive(&sh.ofree);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    // lane j of four has words of all columns: it gives those of columns 16 i' .. 16 i' + 15 to lane i'
+                    uint32_t a[8], o[8];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)      // units of two words; with lane ^ 1: the even ones for the odd ones
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t even = w[i][4 * u + e], odds = w[i][4 * u + 2 + e];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? even : odds, 1);
+                            a[4 * u + e] = odd ? got : even;      // from the even lane of the two
+                            a[4 * u + 2 + e] = odd ? odds : got;  // from the odd one
+                        }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t lo = a[2 * j + e], hi = a[4 + 2 * j + e];
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? lo : hi, 2);
+                            o[4 * e + j] = high ? got : lo;
+                            o[4 * e + 2 + j] = high ? hi : got;
+                        }
+                    uint8_t* to = rows + ((long long)(r16 + 8 * i) * p.Dv + col) * 2;
+                    const int c0 = col + (lane & 3) * 16;
+                    if (quad * 32 + r16 + 8 * i + (lane >> 2) < n && c0 < p.Dv) {
+                        if (wide) {
+                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(o[0]), "r"(o[1]),
+                                         "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                                         : "memory");
+                        } else {
+                            *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (c0 + 8 < p.Dv) *reinterpret_cast<uint4*>(to + 16) = make_uint4(o[4], o[5], o[6], o[7]);
+                        }
+                    }
                 }
             }
-            tc_fence_before();
-            mbar_arrive(&sh.ofree);
         }
     } else {
         regs_dec<kRegsCtl>();
@@ -657,56 +680,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (elect_one()) {
                 const uint32_t kb = p.Dk > 64 ? kTile : kHalf, vb = p.Dv > 64 ? kTile : kHalf;
                 int kv_issued = 0, q_issued = 0;
-                // The outputs of chunk cn - 2 leave the q tile that chunk cn takes, a half of the channels at a time
-                struct {
-                    int t, bh, n;
-                } was[2] = {{0, 0, 0}, {0, 0, 0}};  // chunks cn - 2 and cn - 1 (n = 0: none)
-                const auto store_half = [&](int half, int stage, int ph) {
-                    if (!wait_one(&sh.staged[half], ph)) return false;
-                    if (64 * half < p.Dv && (was[0].n == kC || was[0].t + was[0].n == p.S))
-                        tma_store_3d(&to, sm + kOffQ + stage * kTile + half * kHalf, 64 * half, was[0].t, was[0].bh);
-                    tma_store_commit();
-                    return true;
-                };
                 Walk k = first_item(it);
-                bool more = settle(k, p, it);
-                for (; more || was[0].n || was[1].n; ++cn) {
+                for (bool more = settle(k, p, it); more; ++cn, more = next_chunk(k, p, it)) {
                     const int s = cn & 1, bhk = it.group.of(k.bh);
-                    if (more) {
-                        ok = cn < 2 || wait_one(&sh.kvfree[s], ((cn >> 1) - 1) & 1);
+                    if (!kStatesOnly) {
+                        ok = cn < 2 || wait_one(&sh.qfree[s], ((cn >> 1) - 1) & 1);
                         if (!ok) break;
-                        uint8_t* kt = sm + kOffK + s * kTile;
-                        uint8_t* vt = sm + kOffV + s * kTile;
-                        mbar_arrive_expect_tx(&sh.kvfull[s], kb + vb);
-                        tma_load_3d(vt, &tv, &sh.kvfull[s], 0, k.t, k.bh);
-                        if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, k.t, k.bh);
-                        tma_load_3d(kt, &tk, &sh.kvfull[s], 0, k.t, bhk);
-                        if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, k.t, bhk);
-                        kv_issued = cn + 1;
-                    }
-                    if (kStatesOnly) {
-                        more = next_chunk(k, p, it);
-                        continue;
-                    }
-                    if (was[0].n) {
-                        ok = store_half(0, s, cn & 1) && store_half(1, s, cn & 1);
-                        if (!ok) break;
-                    }
-                    uint8_t* qt = sm + kOffQ + s * kTile;
-                    if (more) mbar_arrive_expect_tx(&sh.qfull[s], kb);
-                    tma_store_wait_read1();
-                    if (more) tma_load_3d(qt, &tq, &sh.qfull[s], 0, k.t, bhk);
-                    tma_store_wait_read0();
-                    if (more && p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, k.t, bhk);
-                    was[0] = was[1];
-                    was[1].n = 0;
-                    if (more) {
+                        uint8_t* qt = sm + kOffQ + s * kTile;
+                        mbar_arrive_expect_tx(&sh.qfull[s], kb);
+                        tma_load_3d(qt, &tq, &sh.qfull[s], 0, k.t, bhk);
+                        if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, k.t, bhk);
                         q_issued = cn + 1;
-                        was[1] = {k.t, k.bh, min(kC, k.end - k.t)};
-                        more = next_chunk(k, p, it);
                     }
+                    ok = cn < 2 || wait_one(&sh.kvfree[s], ((cn >> 1) - 1) & 1);
+                    if (!ok) break;
+                    uint8_t* kt = sm + kOffK + s * kTile;
+                    uint8_t* vt = sm + kOffV + s * kTile;
+                    mbar_arrive_expect_tx(&sh.kvfull[s], kb + vb);
+                    tma_load_3d(vt, &tv, &sh.kvfull[s], 0, k.t, k.bh);
+                    if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, k.t, k.bh);
+                    tma_load_3d(kt, &tk, &sh.kvfull[s], 0, k.t, bhk);
+                    if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, k.t, bhk);
+                    kv_issued = cn + 1;
                 }
-                tma_store_wait_all0();
                 // every load has landed before the CTA ends (bounded)
 #pragma unroll 1
                 for (int i = max(0, kv_issued - 2); i < kv_issued; ++i) (void)wait_one(&sh.kvfull[i & 1], (i >> 1) & 1);
@@ -767,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     product_rows(tmem + kColO, dq, ds, id_qs, ksteps);
                     mma_commit(&sh.sfree);
+                    mma_commit(&sh.qfree[s]);
                     if (!wait_one(&sh.pfull, cn & 1)) break;
                     tc_fence_after();
                     const Desc dvm = desc_of(sbase + kOffV + s * kTile, kHalf);
@@ -915,7 +912,7 @@ bool encode(CUtensorMap* map, const void* ptr, long long heads, int S, int D) {
 }
 
 template <bool kStatesOnly>
-gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
+gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
                   int32_t* status, cudaStream_t stream) {
     auto* kernel = linear_attn_tc_kernel<kStatesOnly>;
     static const int regs = [&] {
@@ -939,7 +936,7 @@ gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -951,10 +948,9 @@ bool linear_attn_tc_supported(const LinearAttn& p) {
 
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream) {
-    CUtensorMap m[4];
+    CUtensorMap m[3];
     const long long hk = (long long)p.B * p.Hk, hv = (long long)p.B * p.Hv;
-    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv) ||
-        !encode(&m[3], p.out, hv, p.S, p.Dv))
+    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv))
         return GDN_ERR_CUDA;
     if (s.P > 1) {
         const gdn_status e = launch<true>(m, p, s, dev, sms, status, stream);
