@@ -58,7 +58,7 @@ struct Small {
     float w[2][4];       // e^(the log-decays behind the block)
     float total[2];      // e^(the chunk's)
     int bh[2], t[2], n[2];  // its head, its first token, and how many it has (0: there is no further chunk)
-    uint64_t kvfull[2], kvfree[2], qfull[2], qfree[2], decfull[2], decfree[2];
+    uint64_t vtile[2], kqfull[2], tfree[2], staged[2], decfull[2], decfree[2];
     uint64_t vfull[kSlots], vfree[kSlots];
     uint64_t sfull, sfree, xfull, xfree, qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
@@ -293,8 +293,8 @@ __device__ __forceinline__ void column_rows(int pitch, int rows, F f) {
 template <bool kStatesOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
-                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ LinearAttn p,
-                          const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
+                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
+                          const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small& sh = *reinterpret_cast<Small*>(sm + kOffSmall);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
@@ -307,12 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0) {
         sh.gave_up = 0;
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.kvfull[i], 1);
-            mbar_init(&sh.kvfree[i], 1);
-            mbar_init(&sh.qfull[i], 1);
-            mbar_init(&sh.qfree[i], 1);
+            mbar_init(&sh.vtile[i], 1);
+            mbar_init(&sh.kqfull[i], 1);
+            mbar_init(&sh.tfree[i], 1);
+            mbar_init(&sh.staged[i], 128);
             mbar_init(&sh.decfull[i], 32);
-            mbar_init(&sh.decfree[i], kStatesOnly ? 514 : 770);
+            mbar_init(&sh.decfree[i], kStatesOnly ? 513 : 769);
         }
         for (int i = 0; i < kSlots; ++i) {
             mbar_init(&sh.vfull[i], 256);
@@ -333,7 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 24 && elect_one()) {
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
-        if (!kStatesOnly) tma_prefetch_desc(&tq);
+        if (!kStatesOnly) {
+            tma_prefetch_desc(&tq);
+            tma_prefetch_desc(&to);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -528,13 +531,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
             const int n = sh.n[s], subs = (n + kSub - 1) / kSub;
             if (!ok || n == 0) break;
-            ok = wait_warp(&sh.kvfull[s], (cn >> 1) & 1);
+            ok = wait_warp(&sh.vtile[s], (cn >> 1) & 1);
             if (!ok) break;
             uint8_t* vt = sm + kOffV + s * kTile;
             if (n < subs * kSub && p.lengths) {
                 // rows behind the last token in the last 32: whatever they hold is not multiplied, not even by zero.
                 // A warp clears the columns that it reads itself, of V and of K (two warps the same ones)
                 const int rows = subs * kSub - n;
+                ok = wait_warp(&sh.kqfull[s], (cn >> 1) & 1);
+                if (!ok) break;
 #pragma unroll 1
                 for (int i = lane; i < rows * 8; i += 32) {
                     const uint32_t to = (quad >> 1) * kHalf + sw128_offset(n + (i >> 3), (quad & 1) * 64 + (i & 3) * 16);
@@ -594,7 +599,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------ outputs
         regs_dec<kRegsO>();
         const int r = quad * 32 + lane;
-        const bool wide = (((uint32_t)p.Dv * 2) | (uint32_t)reinterpret_cast<uintptr_t>(p.out)) % 32 == 0;
         for (; !kStatesOnly; ++cn) {
             const int s = cn & 1;
             ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
@@ -604,74 +608,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int m = 0; m < quad; ++m) R += sh.T[s][m];
             const float f = p.scale * exp2_approx(fmaxf(R, kMinRow));
-            // this lane's rows are lane / 4 of every 8; it writes 16 channels of each 64
-            uint8_t* rows = static_cast<uint8_t*>(p.out) +
-                            (((long long)sh.bh[s] * p.S + sh.t[s] + quad * 32 + (lane >> 2)) * p.Dv + (lane & 3) * 16) * 2;
+            uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Dv * 2;
+            // whole chunks and the tensor's end go out by TMA, from q's tile (its products are done); where a length
+            // ends inside a chunk, a thread writes its row itself
+            const bool tma = n == kC || sh.t[s] + n == p.S;
             mbar_arrive(&sh.decfree[s]);
             ok = wait_warp(&sh.ofull, cn & 1);
             if (!ok) break;
             tc_fence_after();
-            const bool odd = lane & 1, high = lane & 2;
-            // 16 lanes of the tensor memory and 64 columns at a time
+            uint8_t* tile = sm + kOffQ + s * kTile + r * 128;
+            const auto put = [&](const float (&x)[16], int col) {
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = pack2(mul2(pair(f, f), pair(x[2 * j], x[2 * j + 1])));
+                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                if (tma) {
+                    uint8_t* half = tile + (col >> 6) * kHalf;
+                    const int ch = (col & 63) >> 3;
+                    *reinterpret_cast<uint4*>(half + ((ch ^ (r & 7)) << 4)) = lo;
+                    *reinterpret_cast<uint4*>(half + (((ch + 1) ^ (r & 7)) << 4)) = hi;
+                } else if (r < n) {
+                    if (col < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col) = lo;
+                    if (col + 8 < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col + 16) = hi;
+                }
+            };
+            // (columns past Dv come from whatever the tensor memory holds, and are not written)
+            float x[16], y[16];
+            tmem_ld16(tq4 + kColO, x);
 #pragma unroll 1
-            for (int part = 0; part < 4; ++part) {
-                const int r16 = (part & 1) * 16, col = (part >> 1) * 64;
-                if (col >= p.Dv) break;
-                uint32_t w[2][8];  // rows lane / 4 and + 8: word k = columns 8 k + 2 (lane % 4) and + 1
-                float fr[2];
-                fr[0] = __shfl_sync(0xffffffffu, f, r16 + (lane >> 2));
-                fr[1] = __shfl_sync(0xffffffffu, f, r16 + 8 + (lane >> 2));
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x[16];
-                    tmem_ld16x256_x4(tq4 + ((uint32_t)r16 << 16) + kColO + col + 32 * c, x);
+            for (int col = 0; col < 128; col += 32) {
+                if (col < p.Dv) {
                     tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            w[i][4 * c + k] = pack2(mul2(pair(fr[i], fr[i]), pair(x[4 * k + 2 * i], x[4 * k + 2 * i + 1])));
+                    tmem_ld16(tq4 + kColO + col + 16, y);
+                    put(x, col);
+                    tmem_wait_ld();
+                    if (col + 32 < p.Dv) tmem_ld16(tq4 + kColO + col + 32, x);
+                    put(y, col + 16);
                 }
-                if (part == 3 || (p.Dv <= 64 && part == 1)) {
-                    tc_fence_before();
-                    mbar_arrive(&sh.ofree);
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    // lane j of four has words of all columns: it gives those of columns 16 i' .. 16 i' + 15 to lane i'
-                    uint32_t a[8], o[8];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)      // units of two words; with lane ^ 1: the even ones for the odd ones
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t even = w[i][4 * u + e], odds = w[i][4 * u + 2 + e];
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? even : odds, 1);
-                            a[4 * u + e] = odd ? got : even;      // from the even lane of the two
-                            a[4 * u + 2 + e] = odd ? odds : got;  // from the odd one
-                        }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t lo = a[2 * j + e], hi = a[4 + 2 * j + e];
-                            const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? lo : hi, 2);
-                            o[4 * e + j] = high ? got : lo;
-                            o[4 * e + 2 + j] = high ? hi : got;
-                        }
-                    uint8_t* to = rows + ((long long)(r16 + 8 * i) * p.Dv + col) * 2;
-                    const int c0 = col + (lane & 3) * 16;
-                    if (quad * 32 + r16 + 8 * i + (lane >> 2) < n && c0 < p.Dv) {
-                        if (wide) {
-                            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(o[0]), "r"(o[1]),
-                                         "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                                         : "memory");
-                        } else {
-                            *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
-                            if (c0 + 8 < p.Dv) *reinterpret_cast<uint4*>(to + 16) = make_uint4(o[4], o[5], o[6], o[7]);
-                        }
-                    }
+                if (col & 32) {
+                    fence_proxy_async_smem();
+                    mbar_arrive(&sh.staged[col >> 6]);
                 }
             }
+            tc_fence_before();
+            mbar_arrive(&sh.ofree);
         }
     } else {
         regs_dec<kRegsCtl>();
@@ -679,35 +659,76 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- TMA, one thread
             if (elect_one()) {
                 const uint32_t kb = p.Dk > 64 ? kTile : kHalf, vb = p.Dv > 64 ? kTile : kHalf;
-                int kv_issued = 0, q_issued = 0;
+                int v_issued = 0, kq_issued = 0;
+                struct Tile {
+                    int t, bh, n;
+                } was[2] = {{0, 0, 0}, {0, 0, 0}};  // chunks cn - 2 and cn - 1 (n = 0: none)
                 Walk k = first_item(it);
-                for (bool more = settle(k, p, it); more; ++cn, more = next_chunk(k, p, it)) {
-                    const int s = cn & 1, bhk = it.group.of(k.bh);
-                    if (!kStatesOnly) {
-                        ok = cn < 2 || wait_one(&sh.qfree[s], ((cn >> 1) - 1) & 1);
+                bool more = settle(k, p, it);
+                Walk far = k;  // a chunk two ahead, whose tiles are brought into L2
+                bool ahead = more && next_chunk(far, p, it);
+                // The engine works in order: what is needed first goes first.  V, out of which parts are made; the outputs of
+                // chunk cn - 2, which leave the q tile that chunk cn takes; K and q; then the prefetch
+                for (; more || was[0].n || was[1].n; ++cn) {
+                    const int s = cn & 1, ph = (cn >> 1) & 1, bhk = it.group.of(k.bh);
+                    if (more) {
+                        ok = cn < 2 || wait_one(&sh.tfree[s], ph ^ 1);
                         if (!ok) break;
-                        uint8_t* qt = sm + kOffQ + s * kTile;
-                        mbar_arrive_expect_tx(&sh.qfull[s], kb);
-                        tma_load_3d(qt, &tq, &sh.qfull[s], 0, k.t, bhk);
-                        if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.qfull[s], 64, k.t, bhk);
-                        q_issued = cn + 1;
+                        uint8_t* vt = sm + kOffV + s * kTile;
+                        mbar_arrive_expect_tx(&sh.vtile[s], vb);
+                        tma_load_3d(vt, &tv, &sh.vtile[s], 0, k.t, k.bh);
+                        if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.vtile[s], 64, k.t, k.bh);
+                        v_issued = cn + 1;
                     }
-                    ok = cn < 2 || wait_one(&sh.kvfree[s], ((cn >> 1) - 1) & 1);
-                    if (!ok) break;
-                    uint8_t* kt = sm + kOffK + s * kTile;
-                    uint8_t* vt = sm + kOffV + s * kTile;
-                    mbar_arrive_expect_tx(&sh.kvfull[s], kb + vb);
-                    tma_load_3d(vt, &tv, &sh.kvfull[s], 0, k.t, k.bh);
-                    if (p.Dv > 64) tma_load_3d(vt + kHalf, &tv, &sh.kvfull[s], 64, k.t, k.bh);
-                    tma_load_3d(kt, &tk, &sh.kvfull[s], 0, k.t, bhk);
-                    if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kvfull[s], 64, k.t, bhk);
-                    kv_issued = cn + 1;
+                    uint8_t* qt = sm + kOffQ + s * kTile;
+                    if (was[0].n) {
+                        const bool whole = was[0].n == kC || was[0].t + was[0].n == p.S;
+#pragma unroll 1
+                        for (int h = 0; h < 2 && ok; ++h) {
+                            ok = wait_one(&sh.staged[h], cn & 1);
+                            if (ok && whole && 64 * h < p.Dv)
+                                tma_store_3d(&to, qt + h * kHalf, 64 * h, was[0].t, was[0].bh);
+                        }
+                        tma_store_commit();
+                        if (!ok) break;
+                    }
+                    if (more) {
+                        uint8_t* kt = sm + kOffK + s * kTile;
+                        mbar_arrive_expect_tx(&sh.kqfull[s], kStatesOnly ? kb : 2 * kb);
+                        tma_load_3d(kt, &tk, &sh.kqfull[s], 0, k.t, bhk);
+                        if (p.Dk > 64) tma_load_3d(kt + kHalf, &tk, &sh.kqfull[s], 64, k.t, bhk);
+                        kq_issued = cn + 1;
+                    }
+                    tma_store_wait_read0();
+                    was[0] = was[1];
+                    was[1].n = 0;
+                    if (more) {
+                        if (!kStatesOnly) {
+                            tma_load_3d(qt, &tq, &sh.kqfull[s], 0, k.t, bhk);
+                            if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.kqfull[s], 64, k.t, bhk);
+                            was[1] = Tile{k.t, k.bh, min(kC, k.end - k.t)};
+                        }
+                        more = next_chunk(k, p, it);
+                        if (ahead) ahead = next_chunk(far, p, it);
+                        if (ahead) {
+                            const int fhk = it.group.of(far.bh);
+#pragma unroll 1
+                            for (int x = 0; x < 128; x += 64) {
+                                if (x < p.Dv) tma_prefetch_l2_3d(&tv, x, far.t, far.bh);
+                                if (x < p.Dk) {
+                                    tma_prefetch_l2_3d(&tk, x, far.t, fhk);
+                                    if (!kStatesOnly) tma_prefetch_l2_3d(&tq, x, far.t, fhk);
+                                }
+                            }
+                        }
+                    }
                 }
+                tma_store_wait_all0();
                 // every load has landed before the CTA ends (bounded)
 #pragma unroll 1
-                for (int i = max(0, kv_issued - 2); i < kv_issued; ++i) (void)wait_one(&sh.kvfull[i & 1], (i >> 1) & 1);
+                for (int i = max(0, v_issued - 2); i < v_issued; ++i) (void)wait_one(&sh.vtile[i & 1], (i >> 1) & 1);
 #pragma unroll 1
-                for (int i = max(0, q_issued - 2); i < q_issued; ++i) (void)wait_one(&sh.qfull[i & 1], (i >> 1) & 1);
+                for (int i = max(0, kq_issued - 2); i < kq_issued; ++i) (void)wait_one(&sh.kqfull[i & 1], (i >> 1) & 1);
             }
             __syncwarp();
         } else if (warp == 25) {
@@ -725,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!wait_one(&sh.decfull[s], ph)) return -1;
                     const int n = sh.n[s];
                     mbar_arrive(&sh.decfree[s]);
-                    if (n > 0 && (!wait_one(&sh.kvfull[s], ph) || (!kStatesOnly && !wait_one(&sh.qfull[s], ph)))) return -1;
+                    if (n > 0 && !wait_one(&sh.kqfull[s], ph)) return -1;
                     return n;
                 };
                 int n = next();
@@ -754,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (u < subs) break;
                     mma_commit(&sh.xfull);
                     if (kStatesOnly) {
-                        mma_commit(&sh.kvfree[s]);
+                        mma_commit(&sh.tfree[s]);
                         ++cn;
                         n = next();
                         continue;
@@ -763,8 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     product_rows(tmem + kColO, dq, ds, id_qs, ksteps);
                     mma_commit(&sh.sfree);
-                    mma_commit(&sh.qfree[s]);
-                    if (!wait_one(&sh.pfull, cn & 1)) break;
+                    if (!wait_one(&sh.pfull, cn & 1) || !wait_one(&sh.vtile[s], (cn >> 1) & 1)) break;
                     tc_fence_after();
                     const Desc dvm = desc_of(sbase + kOffV + s * kTile, kHalf);
                     if (subs == kC / kSub) {
@@ -777,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             step_ts<true>(tmem + kColO, tmem + kColP + 8 * i, dvm, i * 2048, id_pv);
                     }
                     mma_commit(&sh.ofull);
-                    mma_commit(&sh.kvfree[s]);
+                    mma_commit(&sh.tfree[s]);
                     ++cn;
                     n = next();
                 }
@@ -791,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // -------------------------------------------------------- decays, and the walk that most roles follow
             Walk k = first_item(it);
             bool more = settle(k, p, it);
-            float g[4];  // the log-decays of the walk's chunk, a chunk before they are used
+            float g[4] = {};  // the log-decays of the walk's chunk, on their way while the chunk before is published
             const auto fetch = [&] {
                 const float* from =
                     p.g_log + (p.head_decay ? k.bh - it.hv.of(k.bh) * p.Hv : (long long)k.bh * p.S + k.t + lane);
@@ -801,72 +821,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (more) fetch();
             for (;; ++cn) {
                 const int s = cn & 1;
+                float down[4];  // the log-decays from a token on to the end of its block
+#pragma unroll
+                for (int b = 0; b < 4; ++b) down[b] = least_decay(g[b]);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        const float z = __shfl_down_sync(0xffffffffu, down[b], o);
+                        if (lane + o < 32) down[b] += z;
+                    }
+                float T[4], after[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    T[b] = __shfl_sync(0xffffffffu, down[b], 0);
+                    after[b] = __shfl_down_sync(0xffffffffu, down[b], 1);
+                    if (lane == 31) after[b] = 0.f;
+                }
+                // lane b: what block b's states are multiplied by behind it; lane 4: the whole chunk's
+                const float t3 = T[3], t2 = T[2] + t3, t1 = T[1] + t2, t0 = T[0] + t1;
+                const float behind = expf(lane == 3 ? 0.f : lane == 2 ? t3 : lane == 1 ? t2 : lane == 0 ? t1 : t0);
                 ok = cn < 2 || wait_warp(&sh.decfree[s], ((cn >> 1) - 1) & 1);
                 if (!ok) break;
-                if (lane == 0) {
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    sh.c[s][32 * b + lane] = kLog2e * (T[b] - after[b]);  // (of the scores, which are bf16)
+                    sh.h[s][32 * b + lane] = expf(after[b]);
+                }
+                if (lane < 4) {
+                    sh.T[s][lane] = kLog2e * (lane == 3 ? T[3] : lane == 2 ? T[2] : lane == 1 ? T[1] : T[0]);
+                    sh.w[s][lane] = behind;
+                } else if (lane == 4) {
+                    sh.total[s] = behind;
                     sh.bh[s] = k.bh;
                     sh.t[s] = k.t;
                     sh.n[s] = more ? min(kC, k.end - k.t) : 0;
                 }
-                if (!more) {
-                    mbar_arrive(&sh.decfull[s]);
-                    break;
-                }
-                float x[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) x[b] = least_decay(g[b]);
+                mbar_arrive(&sh.decfull[s]);
+                if (!more) break;
                 more = next_chunk(k, p, it);
                 if (more) fetch();
-                float behind = 0.f;
-#pragma unroll 1
-                for (int b = 3; b >= 0; --b) {
-                    float up = x[3], down = x[3];
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const float y = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_down_sync(0xffffffffu, down, o);
-                        if (lane >= o) up += y;
-                        if (lane + o < 32) down += z;
-                    }
-                    const float after = __shfl_down_sync(0xffffffffu, down, 1), T = __shfl_sync(0xffffffffu, down, 0);
-                    sh.c[s][32 * b + lane] = kLog2e * up;
-                    sh.h[s][32 * b + lane] = expf(lane < 31 ? after : 0.f);
-                    if (lane == 0) {
-                        sh.T[s][b] = kLog2e * T;
-                        sh.w[s][b] = expf(behind);
-                    }
-                    behind += T;
-                    x[3] = x[2], x[2] = x[1], x[1] = x[0];
-                }
-                if (lane == 0) sh.total[s] = expf(behind);
-                mbar_arrive(&sh.decfull[s]);
-            }
-        } else {
-            // -------------------------------------------------------- tiles into L2, ahead of their loads
-            // The CTAs run in step and ask for their tiles at the same time; asked for two chunks early, they come
-            // evenly.  (By plain prefetches: TMA's own would queue in front of its loads.)
-            const auto lines = [&](const void* base, long long row, int n, int D, int size) {
-                const uint8_t* from = static_cast<const uint8_t*>(base) + row * D * size;
-#pragma unroll 1
-                for (int i = lane * 128; i < n * D * size; i += 32 * 128)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
-            };
-            Walk k = first_item(it);
-            bool more = settle(k, p, it);
-            for (;; ++cn) {
-#pragma unroll 1
-                for (int i = cn ? 1 : 3; i > 0 && more; --i, more = next_chunk(k, p, it)) {
-                    const int n = min(kC, k.end - k.t);
-                    const long long hk = (long long)it.group.of(k.bh) * p.S + k.t, hv = (long long)k.bh * p.S + k.t;
-                    if (!p.head_decay) lines(p.g_log, hv, n, 1, 4);
-                    lines(p.k, hk, n, p.Dk, 2);
-                    lines(p.v, hv, n, p.Dv, 2);
-                    if (!kStatesOnly) lines(p.q, hk, n, p.Dk, 2);
-                }
-                const int s = cn & 1;
-                ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
-                if (!ok || sh.n[s] == 0) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.decfree[s]);
             }
         }
     }
@@ -912,7 +906,7 @@ bool encode(CUtensorMap* map, const void* ptr, long long heads, int S, int D) {
 }
 
 template <bool kStatesOnly>
-gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
+gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
                   int32_t* status, cudaStream_t stream) {
     auto* kernel = linear_attn_tc_kernel<kStatesOnly>;
     static const int regs = [&] {
@@ -936,7 +930,7 @@ gdn_status launch(const CUtensorMap (&m)[3], const LinearAttn& p, const LinearAt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -948,9 +942,10 @@ bool linear_attn_tc_supported(const LinearAttn& p) {
 
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream) {
-    CUtensorMap m[3];
+    CUtensorMap m[4];
     const long long hk = (long long)p.B * p.Hk, hv = (long long)p.B * p.Hv;
-    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv))
+    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv) ||
+        !encode(&m[3], p.out, hv, p.S, p.Dv))
         return GDN_ERR_CUDA;
     if (s.P > 1) {
         const gdn_status e = launch<true>(m, p, s, dev, sms, status, stream);
