@@ -226,10 +226,8 @@ __global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, 
                         if (kStatesOnly || split.P == 1) {
                             if (seg == 0 && p.state_in) x[w] = p.state_in[bh * n_state + i];
                             if (kStatesOnly && seg == 0) split.parts[((split.P - 1) * heads + bh) * n_state + i] = x[w];
-                        } else if (seg == 0) {
-                            x[w] = split.parts[((split.P - 1) * heads + bh) * n_state + i];
                         } else {
-                            x[w] = linear_attn_start(split, seg, bh, heads, n_state, i);
+                            x[w] = split.start(seg, bh, heads, n_state)[i];
                         }
                     }
                 }
@@ -350,6 +348,8 @@ cudaError_t launch_ffma_rows(const LinearAttn& p, const LinearAttnSplit& s, int 
         const cudaError_t e = launch_after(linear_attn_ffma_kernel<T, MB, true>,
                                            dim3((unsigned)heads, slices, (unsigned)(s.P - 1)), 32 * warps, 0, stream, p, s);
         if (e != cudaSuccess) return e;
+        const cudaError_t c = launch_linear_attn_combine(p, s, sms, stream);
+        if (c != cudaSuccess) return c;
     }
     return launch_after(linear_attn_ffma_kernel<T, MB, false>, dim3((unsigned)heads, slices, (unsigned)s.P), 32 * warps, 0,
                         stream, p, s);
@@ -364,6 +364,34 @@ cudaError_t launch_ffma(const LinearAttn& p, const LinearAttnSplit& s, int sms, 
         default: return launch_ffma_rows<T, 4>(p, s, sms, stream);
     }
 }
+
+// ------------------------------------------------------------------ the states of a split
+// X_j += F_j X_{j-1} for j = 1 .. P - 2, a thread an element, its loads of all segments independent of the sums.
+__global__ void __launch_bounds__(256) linear_attn_combine_kernel(LinearAttnSplit s, long long heads, long long n) {
+    ptx::griddep_wait();
+    const long long all = heads * n;
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (long long)gridDim.x * blockDim.x) {
+        const long long bh = i / n;
+        float x = s.parts[i];
+#pragma unroll 8
+        for (int j = 1; j < s.P - 1; ++j) {
+            x = fmaf(s.decays[j * heads + bh], x, s.parts[j * all + i]);
+            s.parts[j * all + i] = x;
+        }
+    }
+    ptx::griddep_launch_dependents();
+}
+
+}  // namespace
+
+cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream) {
+    if (s.P <= 2) return cudaSuccess;
+    const long long heads = (long long)p.B * p.Hv, n = (long long)p.Dk * p.Dv, blocks = (heads * n + 255) / 256;
+    return launch_after(linear_attn_combine_kernel, dim3((unsigned)(blocks < 8ll * sms ? blocks : 8ll * sms)), 256, 0, stream,
+                        s, heads, n);
+}
+
+namespace {
 
 // ------------------------------------------------------------------ host side
 constexpr uint32_t kKnownFlags = GDN_FORCE_FFMA | GDN_SINGLE_PASS | GDN_HEAD_DECAY;
@@ -413,12 +441,32 @@ bool on_tensor_cores(const LinearAttn& p, const gdn_dims* d) {
     return !(d->flags & GDN_FORCE_FFMA) && linear_attn_tc_supported(p);
 }
 
-// Segments a sequence is cut into.
-int segments(const gdn_dims* d, bool tc, int sms, int* len) {
-    (void)sms;
-    (void)tc;
+// Segments that a sequence is cut into, of *len tokens: as many as make the call shortest by an estimate of its launches, and
+// only if that saves a tenth (by dims alone: operands off 16 bytes, which run on the FMA units, are cut alike).
+// A unit (128 tokens on the tensor cores, 16 on the FMA units) takes `whole` us in the last launch and `states` in the first;
+// a launch of a split costs `launch` more, and a combine step and a state's way to and from memory `state`.
+int segments(const gdn_dims* d, int sms, int* len) {
     *len = (int)d->S;
-    return 1;
+    const bool tc = !(d->flags & GDN_FORCE_FFMA) && d->dtype == GDN_BF16 && d->Dk % 8 == 0 && d->Dv % 8 == 0;
+    const int unit = tc ? 128 : kTok;
+    const double whole = tc ? 2.5 : 8.0, states = tc ? 1.5 : 5.0, launch = 4.0, state = 0.05;
+    const long long heads = (long long)d->B * d->Hv, units = (d->S + unit - 1) / unit, room = tc ? sms : 2ll * sms;
+    if ((d->flags & GDN_SINGLE_PASS) || units < 2) return 1;
+    const auto rounds = [&](long long items) { return (double)((items + room - 1) / room); };
+    double best = 0.9 * rounds(heads) * (units * whole + launch);
+    int P = 1;
+    for (int n = 2; n <= 64 && n <= units; ++n) {
+        const long long each = (units + n - 1) / n;
+        if ((n - 1) * each >= units) continue;  // (the last segment would be empty)
+        const double t = rounds(heads * (n - 1)) * (each * states + launch) + rounds(heads * n) * (each * whole + launch) +
+                         launch + state * n;
+        if (t < best) {
+            best = t;
+            P = n;
+            *len = (int)(each * unit);
+        }
+    }
+    return P;
 }
 
 }  // namespace
@@ -447,7 +495,7 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
     const bool tc = gdn::on_tensor_cores(p, dims);
     gdn::LinearAttnSplit split{1, p.S, nullptr, nullptr};
     int len = 0;
-    const int P = gdn::segments(dims, tc, sms, &len);
+    const int P = gdn::segments(dims, sms, &len);
     bool own = false;
     void* ws = nullptr;
     if (P > 1) {
@@ -499,12 +547,8 @@ gdn_status gdn_linear_attn_step(const void* q, const void* k, const void* v, con
 int32_t gdn_linear_attn_segments(const gdn_dims* dims, int32_t sm_count) {
     if (gdn::check_dims(dims, false) != GDN_OK || sm_count < 1) return 0;
     int len = 0;
-    gdn::LinearAttn p{};
-    p.Dk = (int)dims->Dk;
-    p.Dv = (int)dims->Dv;
-    p.bf16 = dims->dtype == GDN_BF16;
     if (dims->B == 0 || dims->S == 0) return 1;
-    return gdn::segments(dims, gdn::on_tensor_cores(p, dims), sm_count, &len);
+    return gdn::segments(dims, sm_count, &len);
 }
 
 size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims) {

@@ -32,15 +32,18 @@ struct LinearAttn {
 constexpr float kMinLogDecay = -100.f;
 __device__ __forceinline__ float least_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // (NaN stays)
 
-// Segments of every sequence (P = 1: whole).  Segment j holds tokens [j len, (j + 1) len) of S.  The runs of
-// segments 0 .. P - 2 from zero (segment 0: from state_in) come first and leave their end states X_j in
-// `parts` [P][B Hv][Dk Dv] and their decays F_j in `decays` [P][B Hv]; the start state of segment j is then
-// X_{j-1} + F_{j-1} (X_{j-2} + F_{j-2} (...)).  Slot P - 1 of `parts` keeps a copy of state_in, since segment
-// P - 1 may write state_out in its place while segment 0 has not read it.
+// Segments of every sequence (P = 1: whole).  Segment j holds tokens [j len, (j + 1) len) of S.  A first launch runs
+// segments 0 .. P - 2 from zero (segment 0: from state_in) and leaves their end states X_j in `parts` [P][B Hv][Dk Dv]
+// and their decays F_j in `decays` [P][B Hv]; a second adds them up in place, X_j += F_j X_{j-1}, so that slot j is the
+// start state of segment j + 1; a third runs all segments.  Slot P - 1 keeps a copy of state_in for segment 0, since
+// segment P - 1 may write state_out in its place before segment 0 has read it.
 struct LinearAttnSplit {
     int P, len;
     float* parts;
     float* decays;
+    __device__ const float* start(int seg, long long bh, long long heads, long long n) const {
+        return parts + ((seg ? seg - 1 : P - 1) * heads + bh) * n;
+    }
 };
 inline size_t linear_attn_split_bytes(const LinearAttn& p, int P) {
     return P <= 1 ? 0 : (size_t)P * p.B * p.Hv * ((size_t)p.Dk * p.Dv + 1) * sizeof(float);
@@ -48,16 +51,11 @@ inline size_t linear_attn_split_bytes(const LinearAttn& p, int P) {
 
 // bf16 with head dims of whole 16-byte rows, on aligned pointers.
 bool linear_attn_tc_supported(const LinearAttn& p);
-// Both passes of a split, or the one of P = 1.
+// All launches of a split, or the one of P = 1.
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream);
 
-// The start state of segment j at element i of head bh (`stride` = B Hv, `n` = Dk Dv).
-__device__ __forceinline__ float linear_attn_start(const LinearAttnSplit& s, int j, long long bh, long long heads,
-                                                   long long n, long long i) {
-    float x = s.parts[bh * n + i];
-    for (int m = 1; m < j; ++m) x = fmaf(s.decays[m * heads + bh], x, s.parts[(m * heads + bh) * n + i]);
-    return x;
-}
+// The second launch (nothing for P = 2).
+cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream);
 
 }  // namespace gdn

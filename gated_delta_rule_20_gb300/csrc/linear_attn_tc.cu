@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int pitch = p.Dv;
             asm volatile("" : "+r"(pitch));  // (64 rows' offsets are not kept in registers over the chunks)
             const float* src = p.state_in ? p.state_in + k.bh * ns : nullptr;
-            if (!kStatesOnly && split.P > 1) src = split.parts + (k.seg ? k.bh : (split.P - 1) * heads + k.bh) * ns;
+            if (!kStatesOnly && split.P > 1) src = split.start(k.seg, k.bh, heads, ns);
             if (kStatesOnly && k.seg) src = nullptr;
             if (src) {
                 src += first;
@@ -443,14 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
 #pragma unroll
                 for (int i = 0; i < 64; ++i) S[i] = 0.f;
-            }
-            if (!kStatesOnly && split.P > 1) {
-#pragma unroll 1
-                for (int m = 1; m < k.seg; ++m) {
-                    const float f = split.decays[m * heads + k.bh];
-                    const float* x = split.parts + (m * heads + k.bh) * ns + first;
-                    column_rows(pitch, rows, [&](int i, int at, bool in) { S[i] = in ? fmaf(f, S[i], x[at]) : 0.f; });
-                }
             }
             if (kStatesOnly && k.seg == 0) {  // the copy of state_in
                 float* x = split.parts + ((split.P - 1) * heads + k.bh) * ns + first;
@@ -633,16 +625,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             };
             // (columns past Dv come from whatever the tensor memory holds, and are not written)
-            float x[16], y[16];
-            tmem_ld16(tq4 + kColO, x);
 #pragma unroll 1
             for (int col = 0; col < 128; col += 32) {
                 if (col < p.Dv) {
-                    tmem_wait_ld();
+                    float x[16], y[16];
+                    tmem_ld16(tq4 + kColO + col, x);
                     tmem_ld16(tq4 + kColO + col + 16, y);
-                    put(x, col);
                     tmem_wait_ld();
-                    if (col + 32 < p.Dv) tmem_ld16(tq4 + kColO + col + 32, x);
+                    put(x, col);
                     put(y, col + 16);
                 }
                 if (col & 32) {
@@ -950,6 +940,7 @@ gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, 
     if (s.P > 1) {
         const gdn_status e = launch<true>(m, p, s, dev, sms, status, stream);
         if (e != GDN_OK) return e;
+        if (launch_linear_attn_combine(p, s, sms, stream) != cudaSuccess) return GDN_ERR_CUDA;
     }
     return launch<false>(m, p, s, dev, sms, status, stream);
 }
