@@ -186,63 +186,124 @@ __device__ __forceinline__ void scale_state(Pair (&S)[MB][2][4], float a) {
             for (int j = 0; j < 4; ++j) S[m][u][j] = mul2(aa, S[m][u][j]);
 }
 
-// MB: blocks of 32 rows of the state.  States only (the first pass of a split): segments 0 .. P - 2, end states
-// and decays to the split's arrays, no outputs.
-template <typename T, int MB, bool kStatesOnly>
+// Shared memory of a CTA: two buffers of kTok tokens' k, v and q, and the outputs, in fp32.
+template <int MB, bool kStatesOnly>
+struct FfmaBuffers {
+    static constexpr int kDk = 32 * MB;
+    __host__ __device__ static int floats(int cols) {  // of one buffer
+        return kTok * ((kStatesOnly ? 1 : 2) * kDk + cols);
+    }
+    static size_t bytes(int cols) { return sizeof(float) * (2 * floats(cols) + (kStatesOnly ? 0 : kTok * cols)); }
+};
+
+// MB: blocks of 32 rows of the state.  kStatesOnly (the first pass of a split): segments 0 .. P - 2, end states and decays to
+// the split's arrays, no outputs.  kAsync (fp32 with rows of whole 16 bytes): the next tokens are copied into the other
+// buffer while these are computed; else they are loaded, and widened, between.
+template <typename T, int MB, bool kStatesOnly, bool kAsync>
 __global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, LinearAttnSplit split) {
-    constexpr int kDk = 32 * MB;
-    __shared__ __align__(16) float s_q[kStatesOnly ? 1 : kTok][kDk], s_k[kTok][kDk];
-    __shared__ __align__(16) float s_v[kTok][kMaxD];
-    __shared__ float s_o[kStatesOnly ? 1 : kTok][kMaxD];
-    __shared__ float2 s_a[kTok];  // what a token's state is multiplied by before it, and its output by
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d = lane & 7, e = lane >> 3;
-    const int cols = (int)blockDim.x / 2, base = blockIdx.y * cols;  // 16 columns a warp
-    const int mine = warp * 16 + e * 4;                              // this lane's first column of the slice
+    using Buf = FfmaBuffers<MB, kStatesOnly>;
+    constexpr int kDk = Buf::kDk;
+    extern __shared__ __align__(16) float s_mem[];
+    __shared__ float4 s_a[2][kTok];  // what a token's state is multiplied by before it, its values, and its output
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, d = lane & 7, e = lane >> 3, warps = blockDim.x >> 5;
+    const int cols = 16 * warps, base = blockIdx.y * cols;
+    const int mine = warp * 16 + e * 4;  // this lane's first column of the slice
     const long long heads = (long long)p.B * p.Hv, bh = blockIdx.x;
     const int seg = blockIdx.z;
     const int b = (int)(bh / p.Hv), h = (int)(bh - (long long)b * p.Hv), hk = h / (p.Hv / p.Hk);
-    const int Dk = p.Dk, Dv = p.Dv;
+    const int Dk = p.Dk, Dv = p.Dv, size = Buf::floats(cols);
+    float* const s_o = s_mem + 2 * size;
     const long long n_state = (long long)Dk * Dv;
     ptx::griddep_wait();
     int len = p.S;
     if (p.lengths) len = max(0, min(p.S, p.lengths[b]));
-    const int t0 = seg * split.len, t1 = min(len, split.P > 1 ? t0 + split.len : len);
+    const int t0 = split.P > 1 ? seg * split.len : 0, t1 = split.P > 1 && len - t0 > split.len ? t0 + split.len : len;
 
     // the start state
+    const float* src = p.state_in ? p.state_in + bh * n_state : nullptr;
+    if (split.P > 1 && !kStatesOnly) src = split.start(seg, bh, heads, n_state);
+    if (kStatesOnly && seg > 0) src = nullptr;
+    float* copy = kStatesOnly && seg == 0 ? split.parts + ((split.P - 1) * heads + bh) * n_state : nullptr;
     Pair S[MB][2][4];
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
+    for (int m = 0; m < MB; ++m) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+            float x[2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float x[2];
+            for (int w = 0; w < 2; ++w) {
+                const int r = 32 * m + 4 * d + 2 * u + w, at = r * Dv + base + mine;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int r = 32 * m + 4 * d + 2 * u + w, c = base + mine + j;
-                    const long long i = (long long)r * Dv + c;
-                    x[w] = 0.f;
-                    if (r < Dk && c < Dv) {
-                        if (kStatesOnly || split.P == 1) {
-                            if (seg == 0 && p.state_in) x[w] = p.state_in[bh * n_state + i];
-                            if (kStatesOnly && seg == 0) split.parts[((split.P - 1) * heads + bh) * n_state + i] = x[w];
-                        } else {
-                            x[w] = split.start(seg, bh, heads, n_state)[i];
-                        }
-                    }
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = r < Dk && base + mine + j < Dv;
+                    x[w][j] = src && in ? src[at + j] : 0.f;
+                    if (copy && in) copy[at + j] = x[w][j];
                 }
-                S[m][u][j] = pair_of(x[0], x[1]);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) S[m][u][j] = pair_of(x[0][j], x[1][j]);
+        }
+        asm volatile("" ::: "memory");  // (no more addresses at once)
+    }
     const T* qr = static_cast<const T*>(p.q) + ((size_t)b * p.Hk + hk) * p.S * Dk;
     const T* kr = static_cast<const T*>(p.k) + ((size_t)b * p.Hk + hk) * p.S * Dk;
-    const T* vr = static_cast<const T*>(p.v) + (size_t)bh * p.S * Dv;
-    T* orow = static_cast<T*>(p.out) + (size_t)bh * p.S * Dv;
-    float decay = 1.f;
+    const T* vr = static_cast<const T*>(p.v) + (size_t)bh * p.S * Dv + base;
+    T* orow = static_cast<T*>(p.out) + (size_t)bh * p.S * Dv + base;
+    const float* gr = p.g_log + (p.head_decay ? h : (size_t)bh * p.S);
+    const int here = min(cols, Dv - base);  // of the slice's columns
 
-    for (int t = t0; t < t1; t += kTok) {
+    // channels past Dk are zeros; nothing else that is not there is used
+    for (int i = tid; i < 2 * size; i += blockDim.x) s_mem[i] = 0.f;
+    __syncthreads();
+    // tokens t .. t + n - 1 into a buffer; a warp takes every `warps`-th token
+    const auto stage = [&](float* buf, int t, int n) {
+        float* sk = buf;
+        float* sv = buf + kTok * kDk;
+        float* sq = sv + kTok * cols;
+        if (kAsync) {
+            for (int tok = warp; tok < n; tok += warps) {
+                const size_t row = (size_t)(t + tok) * Dk + 4 * lane;
+                if (4 * lane < Dk) {
+                    ptx::cp_async_16(sk + tok * kDk + 4 * lane, kr + row);
+                    if (!kStatesOnly) ptx::cp_async_16(sq + tok * kDk + 4 * lane, qr + row);
+                }
+                if (4 * lane < here)
+                    ptx::cp_async_16(sv + tok * cols + 4 * lane, vr + (size_t)(t + tok) * Dv + 4 * lane);
+            }
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < kTok; ++i) {
+                const int tok = warp + i * warps;
+                if (tok < n) {
+                    const size_t row = (size_t)(t + tok) * Dk;
+#pragma unroll
+                    for (int m = 0; m < MB; ++m) {
+                        const int c = 32 * m + lane;
+                        if (c < Dk) {
+                            sk[tok * kDk + c] = to_f32(kr[row + c]);
+                            if (!kStatesOnly) sq[tok * kDk + c] = to_f32(qr[row + c]);
+                        }
+                    }
+                    for (int c = lane; c < here; c += 32) sv[tok * cols + c] = to_f32(vr[(size_t)(t + tok) * Dv + c]);
+                }
+            }
+        }
+    };
+    if (kAsync && t0 < t1) {
+        stage(s_mem, t0, min(kTok, t1 - t0));
+        ptx::cp_async_commit();
+    }
+    float decay = 1.f, g_next = 0.f;
+    if (t0 + lane < t1 && lane < kTok) g_next = gr[p.head_decay ? 0 : t0 + lane];
+
+    int turn = 0;
+    for (int t = t0; t < t1; t += kTok, ++turn) {
         const int n = min(kTok, t1 - t);
+        float* buf = s_mem + (kAsync ? (turn & 1) * size : 0);
+        if (!kAsync) stage(buf, t, n);
         // every warp sums the log-decays: lane i has token i's
-        const float g = lane >= n ? 0.f : least_decay(p.g_log[p.head_decay ? h : (size_t)bh * p.S + t + lane]);
+        const float g = lane < n ? least_decay(g_next) : 0.f;
+        if (t + kTok + lane < t1 && lane < kTok) g_next = gr[p.head_decay ? 0 : t + kTok + lane];
         float c_in = g;
 #pragma unroll
         for (int o = 1; o < kTok; o <<= 1) {
@@ -250,36 +311,34 @@ __global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, 
             if (lane >= o) c_in += y;
         }
         const bool blockwise = __all_sync(0xffffffffu, !(fabsf(c_in) > kMostBlock) || lane >= kTok);
-        const float fk = blockwise ? expf(-c_in) : 1.f;
         const float total = __shfl_sync(0xffffffffu, c_in, kTok - 1);
-        __syncthreads();  // the previous tokens' operands have been read
-        if (warp == 0 && lane < kTok) s_a[lane] = blockwise ? make_float2(1.f, expf(c_in)) : make_float2(expf(g), 1.f);
-        for (int i = tid; i < kTok * kDk; i += blockDim.x) {
-            const int tok = i / kDk, c = i % kDk;
-            const bool in = tok < n && c < Dk;
-            const float f = __shfl_sync(0xffffffffu, fk, tok);  // (a warp's 32 channels are one token's)
-            s_k[tok][c] = in ? f * to_f32(kr[(size_t)(t + tok) * Dk + c]) : 0.f;
-            if (!kStatesOnly) s_q[tok][c] = in ? to_f32(qr[(size_t)(t + tok) * Dk + c]) : 0.f;
+        if (warp == 0 && lane < kTok)
+            s_a[turn & 1][lane] = blockwise ? make_float4(1.f, expf(-c_in), expf(c_in), 0.f) : make_float4(expf(g), 1.f, 1.f, 0.f);
+        if (kAsync) ptx::cp_async_wait_all();
+        __syncthreads();  // the buffer and s_a are there; the other buffer has been read
+        if (kAsync && t + kTok < t1) {
+            stage(s_mem + ((turn + 1) & 1) * size, t + kTok, min(kTok, t1 - t - kTok));
+            ptx::cp_async_commit();
         }
-        for (int i = tid; i < kTok * cols; i += blockDim.x) {
-            const int tok = i / cols, c = i % cols;
-            s_v[tok][c] = tok < n && base + c < Dv ? to_f32(vr[(size_t)(t + tok) * Dv + base + c]) : 0.f;
-        }
-        __syncthreads();
         if (kStatesOnly) decay *= expf(total);
-        for (int i = 0; i < n; ++i) {
-            const float2 a = s_a[i];
+        const float* sk = buf + 4 * d;
+        const float* sv = buf + kTok * kDk + mine;
+        const float* sq = buf + kTok * (kDk + cols) + 4 * d;
+#pragma unroll 2
+        for (int i = 0; i < n; ++i, sk += kDk, sv += cols, sq += kDk) {
+            const float4 a = s_a[turn & 1][i];
             if (!blockwise) scale_state(S, a.x);
-            const float4 v4 = *reinterpret_cast<const float4*>(&s_v[i][mine]);
-            const Pair vv[4] = {pair_of(v4.x, v4.x), pair_of(v4.y, v4.y), pair_of(v4.z, v4.z), pair_of(v4.w, v4.w)};
+            const float4 v4 = *reinterpret_cast<const float4*>(sv);
+            const Pair vv[4] = {pair_of(a.y * v4.x, a.y * v4.x), pair_of(a.y * v4.y, a.y * v4.y),
+                                pair_of(a.y * v4.z, a.y * v4.z), pair_of(a.y * v4.w, a.y * v4.w)};
             Pair o[4] = {};
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
-                const float4 k4 = *reinterpret_cast<const float4*>(&s_k[i][32 * m + 4 * d]);
+                const float4 k4 = *reinterpret_cast<const float4*>(sk + 32 * m);
                 const Pair kk[2] = {pair_of(k4.x, k4.y), pair_of(k4.z, k4.w)};
                 Pair qq[2] = {};
                 if (!kStatesOnly) {
-                    const float4 q4 = *reinterpret_cast<const float4*>(&s_q[i][32 * m + 4 * d]);
+                    const float4 q4 = *reinterpret_cast<const float4*>(sq + 32 * m);
                     qq[0] = pair_of(q4.x, q4.y);
                     qq[1] = pair_of(q4.z, q4.w);
                 }
@@ -301,17 +360,15 @@ __global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, 
                 const float y1 = (up ? x[3] : x[1]) + __shfl_xor_sync(0xffffffffu, up ? x[1] : x[3], 4);
                 float z = (up2 ? y1 : y0) + __shfl_xor_sync(0xffffffffu, up2 ? y0 : y1, 2);
                 z += __shfl_xor_sync(0xffffffffu, z, 1);
-                if (!(d & 1)) s_o[i][mine + (up ? 2 : 0) + (up2 ? 1 : 0)] = a.y * z;
+                if (!(d & 1)) s_o[i * cols + mine + (up ? 2 : 0) + (up2 ? 1 : 0)] = a.z * z;
             }
         }
         if (blockwise) scale_state(S, expf(total));
-        if (!kStatesOnly) {
-            __syncthreads();
-            for (int i = tid; i < n * cols; i += blockDim.x) {
-                const int tok = i / cols, c = i % cols;
-                if (base + c < Dv) orow[(size_t)(t + tok) * Dv + base + c] = from_f32<T>(p.scale * s_o[tok][c]);
-            }
-        }
+        if (!kStatesOnly || !kAsync) __syncthreads();  // the outputs are there, and the buffer has been read
+        if (!kStatesOnly)
+            for (int tok = warp; tok < n; tok += warps)
+                for (int c = lane; c < here; c += 32)
+                    orow[(size_t)(t + tok) * Dv + c] = from_f32<T>(p.scale * s_o[tok * cols + c]);
     }
     ptx::griddep_launch_dependents();
 
@@ -324,44 +381,56 @@ __global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, 
     }
     if (!dst) return;
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
+    for (int m = 0; m < MB; ++m) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int w = 0; w < 2; ++w) {
+                const int r = 32 * m + 4 * d + 2 * u + w, at = r * Dv + base + mine;
 #pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    const int r = 32 * m + 4 * d + 2 * u + w, c = base + mine + j;
-                    if (r < Dk && c < Dv) dst[(long long)r * Dv + c] = w ? S[m][u][j].f.y : S[m][u][j].f.x;
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (r < Dk && base + mine + j < Dv) dst[at + j] = w ? S[m][u][j].f.y : S[m][u][j].f.x;
+            }
+        asm volatile("" ::: "memory");
+    }
 }
 
-template <typename T, int MB>
-cudaError_t launch_ffma_rows(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream) {
+template <typename T, int MB, bool kStatesOnly, bool kAsync>
+cudaError_t launch_ffma_kernel(const LinearAttn& p, const LinearAttnSplit& s, int warps, int dev, cudaStream_t stream) {
+    using Buf = FfmaBuffers<MB, kStatesOnly>;
+    static std::atomic<bool> allowed[kMaxDevices];
+    auto* kernel = linear_attn_ffma_kernel<T, MB, kStatesOnly, kAsync>;
+    if (Buf::bytes(kMaxD) > 48 * 1024) {
+        const cudaError_t e = allow_smem(kernel, (int)Buf::bytes(kMaxD), allowed, dev);
+        if (e != cudaSuccess) return e;
+    }
+    const dim3 grid((unsigned)(p.B * p.Hv), (unsigned)((p.Dv + 16 * warps - 1) / (16 * warps)),
+                    (unsigned)(kStatesOnly ? s.P - 1 : s.P));
+    return launch_after(kernel, grid, 32 * warps, Buf::bytes(16 * warps), stream, p, s);
+}
+
+template <typename T, int MB, bool kAsync>
+cudaError_t launch_ffma_rows(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, cudaStream_t stream) {
     // as many columns a CTA as leave every SM two CTAs (its warps share the staged q and k)
     const long long heads = (long long)p.B * p.Hv;
     int warps = 8;
     while (warps > 1 && (16 * (warps / 2) >= p.Dv || heads * s.P * ((p.Dv + 16 * warps - 1) / (16 * warps)) < 2 * sms))
         warps /= 2;
-    const unsigned slices = (unsigned)((p.Dv + 16 * warps - 1) / (16 * warps));
     if (s.P > 1) {
-        const cudaError_t e = launch_after(linear_attn_ffma_kernel<T, MB, true>,
-                                           dim3((unsigned)heads, slices, (unsigned)(s.P - 1)), 32 * warps, 0, stream, p, s);
+        cudaError_t e = launch_ffma_kernel<T, MB, true, kAsync>(p, s, warps, dev, stream);
+        if (e == cudaSuccess) e = launch_linear_attn_combine(p, s, sms, stream);
         if (e != cudaSuccess) return e;
-        const cudaError_t c = launch_linear_attn_combine(p, s, sms, stream);
-        if (c != cudaSuccess) return c;
     }
-    return launch_after(linear_attn_ffma_kernel<T, MB, false>, dim3((unsigned)heads, slices, (unsigned)s.P), 32 * warps, 0,
-                        stream, p, s);
+    return launch_ffma_kernel<T, MB, false, kAsync>(p, s, warps, dev, stream);
 }
 
-template <typename T>
-cudaError_t launch_ffma(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream) {
+template <typename T, bool kAsync>
+cudaError_t launch_ffma(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, cudaStream_t stream) {
     switch ((p.Dk + 31) / 32) {
-        case 1: return launch_ffma_rows<T, 1>(p, s, sms, stream);
-        case 2: return launch_ffma_rows<T, 2>(p, s, sms, stream);
-        case 3: return launch_ffma_rows<T, 3>(p, s, sms, stream);
-        default: return launch_ffma_rows<T, 4>(p, s, sms, stream);
+        case 1: return launch_ffma_rows<T, 1, kAsync>(p, s, dev, sms, stream);
+        case 2: return launch_ffma_rows<T, 2, kAsync>(p, s, dev, sms, stream);
+        case 3: return launch_ffma_rows<T, 3, kAsync>(p, s, dev, sms, stream);
+        default: return launch_ffma_rows<T, 4, kAsync>(p, s, dev, sms, stream);
     }
 }
 
@@ -519,8 +588,10 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
         s = gdn::status_word_for_current_device(&status);
         if (s == GDN_OK) s = gdn::launch_linear_attn_tc(p, split, dev, sms, status, st);
     } else {
-        const cudaError_t e = p.bf16 ? gdn::launch_ffma<__nv_bfloat16>(p, split, sms, st)
-                                     : gdn::launch_ffma<float>(p, split, sms, st);
+        const bool async = !p.bf16 && p.Dk % 4 == 0 && p.Dv % 4 == 0 && gdn::aligned16(q) && gdn::aligned16(k) && gdn::aligned16(v);
+        const cudaError_t e = p.bf16  ? gdn::launch_ffma<__nv_bfloat16, false>(p, split, dev, sms, st)
+                              : async ? gdn::launch_ffma<float, true>(p, split, dev, sms, st)
+                                      : gdn::launch_ffma<float, false>(p, split, dev, sms, st);
         s = e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
     }
     if (s != GDN_OK) (void)cudaGetLastError();

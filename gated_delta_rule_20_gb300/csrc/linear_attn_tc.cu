@@ -60,7 +60,7 @@ struct Small {
     int bh[2], t[2], n[2];  // its head, its first token, and how many it has (0: there is no further chunk)
     uint64_t vtile[2], kqfull[2], tfree[2], staged[2], decfull[2], decfree[2];
     uint64_t vfull[kSlots], vfree[kSlots];
-    uint64_t sfull, sfree, xfull, xfree, qkfull, pfull, ofull, ofree, drain;
+    uint64_t sfull, sfree, xfull[2], xfree[2], qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
     int gave_up;
 };
@@ -320,8 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&sh.sfull, 256);
         mbar_init(&sh.sfree, 1);
-        mbar_init(&sh.xfull, 1);
-        mbar_init(&sh.xfree, 256);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.xfull[i], 1);
+            mbar_init(&sh.xfree[i], 256);
+        }
         mbar_init(&sh.qkfull, 1);
         mbar_init(&sh.pfull, 128);
         mbar_init(&sh.ofull, 1);
@@ -472,14 +474,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float e = sh.total[s];
                 decay *= e;
                 mbar_arrive(&sh.decfree[s]);
-                ok = wait_warp(&sh.xfull, cn & 1);
+                const int xb = kStatesOnly ? cn & 1 : 0;  // (see the products)
+                ok = wait_warp(&sh.xfull[xb], kStatesOnly ? (cn >> 1) & 1 : cn & 1);
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (64 * half + 16 * b < p.Dk) {
                         float x[16];
-                        tmem_ld16(tq4 + kColX + 64 * half + 16 * b, x);
+                        tmem_ld16(tq4 + (xb ? kColO : kColX) + 64 * half + 16 * b, x);
                         tmem_wait_ld();
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 tc_fence_before();
-                mbar_arrive(&sh.xfree);
+                mbar_arrive(&sh.xfree[xb]);
             }
             if (!ok) break;
             float* dst = nullptr;
@@ -749,8 +752,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         product_rows(tmem + kColP, dq, desc_of(sbase + kOffK + s * kTile, 16), kIdQK, ksteps);
                         mma_commit(&sh.qkfull);
                     }
-                    // X of the chunk before has been read
-                    if (cn > 0 && !wait_one(&sh.xfree, (cn - 1) & 1)) break;
+                    // X of the chunk before has been read; in the first pass, which has no O, two X take turns
+                    const int xb = kStatesOnly ? cn & 1 : 0;
+                    const uint32_t col_x = tmem + (xb ? kColO : kColX);
+                    if (kStatesOnly ? cn > 1 && !wait_one(&sh.xfree[xb], ((cn >> 1) - 1) & 1)
+                                    : cn > 0 && !wait_one(&sh.xfree[xb], (cn - 1) & 1))
+                        break;
                     Desc b = desc_of(sbase + kOffK + s * kTile, kHalf);
                     int u = 0;
 #pragma unroll 1
@@ -758,12 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int slot = vi & 1;
                         if (!wait_one(&sh.vfull[slot], (vi >> 1) & 1)) break;
                         tc_fence_after();
-                        product_parts(tmem + kColX, tmem + kColV + slot * kSlotCols, b, id_kv, u > 0);
+                        product_parts(col_x, tmem + kColV + slot * kSlotCols, b, id_kv, u > 0);
                         mma_commit(&sh.vfree[slot]);
                         b.lo += kSub * 128 / 16;
                     }
                     if (u < subs) break;
-                    mma_commit(&sh.xfull);
+                    mma_commit(&sh.xfull[xb]);
                     if (kStatesOnly) {
                         mma_commit(&sh.tfree[s]);
                         ++cn;
