@@ -82,15 +82,13 @@ class GdnLinearPlanInfo(ctypes.Structure):
                 ("splits", ctypes.c_int32)]
 
 
-_Strides = ctypes.c_int64 * 3
-
-
 class GdnRotaryDims(ctypes.Structure):
-    _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64), ("S", ctypes.c_int64),
-                ("D", ctypes.c_int64), ("R", ctypes.c_int64), ("q_strides", _Strides), ("k_strides", _Strides),
-                ("q_out_strides", _Strides), ("k_out_strides", _Strides), ("position_stride", ctypes.c_int64),
-                ("first_position", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32),
-                ("amplitude", ctypes.c_float)]
+    # (each of the header's three strides a field of its own: arrays take longer to fill)
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "Hq", "Hk", "S", "D", "R")]
+                + [("%s_stride_%s" % (t, n), ctypes.c_int64) for t in ("q", "k", "q_out", "k_out")
+                   for n in ("batch", "head", "token")]
+                + [("position_stride", ctypes.c_int64), ("first_position", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                   ("flags", ctypes.c_uint32), ("amplitude", ctypes.c_float)])
 
 
 class GdnError(RuntimeError):
@@ -782,39 +780,45 @@ def linear_plan(M, N, K, dtype=GDN_BF16, out_dtype=None, *, weight_layout="kn", 
 
 
 # ------------------------------------------------------------------ linear attention with a decay for each head
-def _linear_attn_operands(q, k, v, g_log, state, state_out, out, stream, lengths=None):
-    """Checked operands of the two calls: ``(dims, device, pointers, out, state_out)``, with new outputs where
-    none were given."""
+def _linear_attn_operands(q, k, v, g_log, state, state_out, out, stream):
+    """Checked operands of the two calls, with new outputs where none were given: ``(dims, device, pointers of q, k, v,
+    g_log, state, state_out and out, out, state_out)``."""
     if _T is None:
         _layer_init()
     if not q.is_cuda or not q.is_contiguous():
         raise ValueError("q must be a contiguous CUDA tensor")
-    dtype, device = q.dtype, q.device
+    dtype, device, qshape, vshape = q.dtype, q.device, q.shape, v.shape
     code = _LAYER_CODES.get(dtype, GDN_F8E4M3)
     if code == GDN_F8E4M3:
         raise TypeError("q must be bfloat16 or float32, got %s" % dtype)
-    if q.dim() != 4 or v.dim() != 4:
+    if len(qshape) != 4 or len(vshape) != 4:
         raise ValueError("q and k must be [B, Hk, S, Dk] and v [B, Hv, S, Dv]")
-    (B, Hk, S, Dk), Hv, Dv = q.shape, v.shape[1], v.shape[3]
-    kp = _layer_ptr("k", k, q.shape, dtype, device)
+    B, Hk, S, Dk = qshape
+    Hv, Dv = vshape[1], vshape[3]
+    kp = _layer_ptr("k", k, qshape, dtype, device)
     vp = _layer_ptr("v", v, (B, Hv, S, Dv), dtype, device)
-    flags = GDN_HEAD_DECAY if g_log.dim() == 1 else 0
-    gp = _layer_ptr("g_log", g_log, (Hv,) if flags else (B, Hv, S), _T.float32, device)
+    f32 = _T.float32
+    if g_log.dim() == 1:
+        flags, gp = GDN_HEAD_DECAY, _layer_ptr("g_log", g_log, (Hv,), f32, device)
+    else:
+        flags, gp = 0, _layer_ptr("g_log", g_log, (B, Hv, S), f32, device)
     sshape = (B, Hv, Dk, Dv)
-    sp = None if state is None else _layer_ptr("state", state, sshape, _T.float32, device)
+    sp = None
+    if state is not None:
+        sp = _layer_ptr("state", state, sshape, f32, device)
+        if state_out is None:
+            state_out = state
     if state_out is None:
-        state_out = state if state is not None else _layer_empty(sshape, _T.float32, device, stream)
-    np_ = _layer_ptr("state_out", state_out, sshape, _T.float32, device)
+        state_out = _layer_empty(sshape, f32, device, stream)
+        np_ = state_out.data_ptr()
+    else:
+        np_ = sp if state_out is state else _layer_ptr("state_out", state_out, sshape, f32, device)
     if out is None:
-        # rows behind a sequence's length are not written: in a new tensor they are zeros
-        out = _layer_empty(v.shape, dtype, device, stream)
-        if lengths is not None:
-            with _T.cuda.stream(stream if stream is not None else _T.cuda.current_stream(device)):
-                out.zero_()
+        out = _T.empty_like(v) if stream is None else _layer_empty(vshape, dtype, device, stream)
         op = out.data_ptr()
     else:
-        op = _layer_ptr("out", out, v.shape, dtype, device)
-    return GdnDims(B, Hk, Hv, S, Dk, Dv, code, flags), device, (q.data_ptr(), kp, vp, gp), sp, np_, op, out, state_out
+        op = _layer_ptr("out", out, vshape, dtype, device)
+    return GdnDims(B, Hk, Hv, S, Dk, Dv, code, flags), device, q.data_ptr(), kp, vp, gp, sp, np_, op, out, state_out
 
 
 def linear_attn_prefill(q, k, v, g_log, scale, state=None, out=None, *, lengths=None, state_out=None, force_ffma=False,
@@ -828,18 +832,29 @@ def linear_attn_prefill(q, k, v, g_log, scale, state=None, out=None, *, lengths=
     behind them have no influence and are not written (zeros in a new ``out``).  ``single_pass`` sets
     ``GDN_SINGLE_PASS``; ``workspace``: a uint8 CUDA tensor of ``linear_attn_workspace_bytes`` bytes (default: torch's).
     Returns ``(out, state_out)``."""
-    d, device, (qp, kp, vp, gp), sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
-                                                                                    stream, lengths)
-    lp = None if lengths is None else _layer_ptr("lengths", lengths, q.shape[:1], _T.int32, device)
-    d.flags |= (GDN_FORCE_FFMA if force_ffma else 0) | (GDN_SINGLE_PASS if single_pass else 0)
-    wp, nbytes = None, 0
+    new = out is None
+    d, device, qp, kp, vp, gp, sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
+                                                                                  stream)
+    if force_ffma:
+        d.flags |= GDN_FORCE_FFMA
+    if single_pass:
+        d.flags |= GDN_SINGLE_PASS
+    lp = wp = None
+    if lengths is not None:
+        lp = _layer_ptr("lengths", lengths, (d.B,), _T.int32, device)
+        if new:
+            with _T.cuda.stream(stream if stream is not None else _T.cuda.current_stream(device)):
+                out.zero_()
     if workspace is not None:
         if workspace.device != device or workspace.dtype != _T.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 CUDA tensor on %s" % device)
         wp, nbytes = workspace.data_ptr(), workspace.numel()
     else:
-        with _T.cuda.device(device):
+        if device.index == _T.cuda.current_device():
             nbytes = _lib.gdn_linear_attn_workspace_bytes(d)
+        else:
+            with _T.cuda.device(device):
+                nbytes = _lib.gdn_linear_attn_workspace_bytes(d)
         if nbytes:  # from torch, which keeps it between calls
             try:
                 workspace = _layer_empty((nbytes,), _T.uint8, device, stream)
@@ -871,26 +886,23 @@ def linear_attn_step(q, k, v, g_log, scale, state, out=None, *, state_out=None, 
     """One token of every sequence (``gdn_linear_attn_step``): q, k [B, Hk, 1, Dk], v [B, Hv, 1, Dv], ``g_log``
     [B, Hv, 1] or [Hv]; the new state goes to ``state_out``, by default ``state`` itself (which may be None, for
     zeros).  Returns ``(out, state_out)``."""
-    d, device, (qp, kp, vp, gp), sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
-                                                                                    stream)
+    d, device, qp, kp, vp, gp, sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
+                                                                                  stream)
     _layer_call(_lib.gdn_linear_attn_step, device, stream, qp, kp, vp, gp, scale, sp, np_, op, d)
     return out, state_out
 
 
 # ------------------------------------------------------------------ rotary positions
-def _rotary_tensor(nm, x, y, like, stream):
-    """``(pointer, strides, heads, output, its pointer, its strides)`` of q or k."""
-    if x.device != like.device or x.dtype != like.dtype:
-        raise ValueError("%s must be a CUDA tensor of q's dtype on %s" % (nm, like.device))
-    if x.dim() != 4 or (x.shape[0], x.shape[2], x.shape[3]) != (like.shape[0], like.shape[2], like.shape[3]):
-        raise ValueError("%s must be [B, H, S, D] with q's B, S and D, got %s" % (nm, tuple(x.shape)))
-    if x.stride(3) != 1 and x.shape[3] > 1:
-        raise ValueError("%s must have contiguous channels" % nm)
+def _rotary_out(nm, x, y, shape, dtype, device, stream):
+    """``(output, its pointer, its strides)`` of q or k."""
     if y is None:
-        y = _layer_empty(x.shape, x.dtype, x.device, stream)
-    elif y.device != x.device or y.dtype != x.dtype or y.shape != x.shape or (y.stride(3) != 1 and y.shape[3] > 1):
-        raise ValueError("%s_out must be %s's shape and dtype, with contiguous channels, on %s" % (nm, nm, x.device))
-    return x.data_ptr(), x.stride()[:3], x.shape[1], y, y.data_ptr(), y.stride()[:3]
+        y = _layer_empty(shape, dtype, device, stream)
+        D = shape[3]
+        return y, y.data_ptr(), (shape[1] * shape[2] * D, shape[2] * D, D)
+    st = y.stride()
+    if y.dtype is not dtype or y.shape != shape or y.device != device or (st[3] != 1 and shape[3] > 1):
+        raise ValueError("%s_out must be %s's shape and dtype, with contiguous channels, on %s" % (nm, nm, device))
+    return y, y.data_ptr(), st
 
 
 def rotary(q, k, inv_freq, positions=None, *, layout="half", amplitude=1.0, inverse=False, first_position=0, q_out=None,
@@ -906,18 +918,21 @@ def rotary(q, k, inv_freq, positions=None, *, layout="half", amplitude=1.0, inve
     (k_out None without k)."""
     if _T is None:
         _layer_init()
-    if not q.is_cuda or q.dim() != 4:
+    shape, device, dtype = q.shape, q.device, q.dtype
+    if len(shape) != 4 or not q.is_cuda:
         raise ValueError("q must be a CUDA tensor [B, H, S, D]")
-    device = q.device
-    code = _LAYER_CODES.get(q.dtype, GDN_F8E4M3)
+    code = _LAYER_CODES.get(dtype, GDN_F8E4M3)
     if code == GDN_F8E4M3:
-        raise TypeError("q must be bfloat16 or float32, got %s" % q.dtype)
+        raise TypeError("q must be bfloat16 or float32, got %s" % dtype)
     flags = ROTARY_LAYOUTS.get(layout)
     if flags is None:
         raise ValueError("layout must be one of %s" % ", ".join(ROTARY_LAYOUTS))
     if inverse:
         flags |= GDN_ROTARY_INVERSE
-    B, _, S, D = q.shape
+    B, Hq, S, D = shape
+    qs = q.stride()
+    if qs[3] != 1 and D > 1:
+        raise ValueError("q must have contiguous channels")
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be [R / 2]")
     fp = _layer_ptr("inv_freq", inv_freq, inv_freq.shape, _T.float64, device)
@@ -927,20 +942,31 @@ def rotary(q, k, inv_freq, positions=None, *, layout="half", amplitude=1.0, inve
             flags |= GDN_ROTARY_POSITIONS_I32
         elif positions.dtype is not _T.int64:
             raise TypeError("positions must be int64 or int32, got %s" % positions.dtype)
-        if positions.device != device or positions.shape not in ((B, S), (S,)) or (S > 1 and positions.stride(-1) != 1):
+        ps = positions.stride()
+        if positions.device != device or positions.shape not in ((B, S), (S,)) or (S > 1 and ps[-1] != 1):
             raise ValueError("positions must be [B, S] or [S] on %s, tokens contiguous" % device)
         pp = positions.data_ptr()
-        pstride = positions.stride(0) if positions.dim() == 2 else 0
-    qp, qs, Hq, q_out, yp, ys = _rotary_tensor("q", q, q_out, q, stream)
+        pstride = ps[0] if len(ps) == 2 else 0
+    q_out, yp, ys = _rotary_out("q", q, q_out, shape, dtype, device, stream)
     kp = zp = None
     ks = zs = (0, 0, 0)
     Hk = 0
     if k is not None:
-        kp, ks, Hk, k_out, zp, zs = _rotary_tensor("k", k, k_out, q, stream)
+        kshape = k.shape
+        if k.dtype is not dtype or k.device != device:
+            raise ValueError("k must be a CUDA tensor of q's dtype on %s" % device)
+        if len(kshape) != 4 or kshape[0] != B or kshape[2] != S or kshape[3] != D:
+            raise ValueError("k must be [B, H, S, D] with q's B, S and D, got %s" % (tuple(kshape),))
+        ks = k.stride()
+        if ks[3] != 1 and D > 1:
+            raise ValueError("k must have contiguous channels")
+        Hk, kp = kshape[1], k.data_ptr()
+        k_out, zp, zs = _rotary_out("k", k, k_out, kshape, dtype, device, stream)
     elif k_out is not None:
         raise ValueError("k_out goes with k only")
-    d = GdnRotaryDims(B, Hq, Hk, S, D, 2 * inv_freq.shape[0], qs, ks, ys, zs, pstride, first_position, code, flags, amplitude)
-    _layer_call(_lib.gdn_rotary, device, stream, qp, kp, fp, pp, yp, zp, d)
+    d = GdnRotaryDims(B, Hq, Hk, S, D, 2 * inv_freq.shape[0], qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], ys[0], ys[1], ys[2],
+                      zs[0], zs[1], zs[2], pstride, first_position, code, flags, amplitude)
+    _layer_call(_lib.gdn_rotary, device, stream, q.data_ptr(), kp, fp, pp, yp, zp, d)
     return q_out, k_out
 
 

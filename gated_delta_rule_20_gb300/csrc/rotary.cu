@@ -8,8 +8,9 @@
 // around as whole turns do.  The product is exact, so that far positions keep the accuracy of near ones: the angle's error is
 // 2^-64 of a turn a position, from f, where an fp32 product loses 2^-24 of the angle itself (a radian at position 10^7).
 //
-// Bound by bytes: a row is read and written once.  A CTA takes a few tokens and all (or some) of their heads; it first
-// makes the tokens' sines and cosines in shared memory, once for all heads, then streams 16-byte pieces.
+// Bound by bytes: a row is read and written once.  A thread takes one piece of a token's head (16 bytes, or two of them half
+// the turned channels apart), makes that piece's sines and cosines, and goes through the heads with them: the trigonometry
+// is done once a token, and a head costs two pointer additions, with 8 loads on their way.
 #include <cuda_bf16.h>
 
 #include "gdn_device.cuh"
@@ -19,9 +20,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTokens = 16;      // of a CTA
-constexpr int kTableFloats = 8192;  // of its sines and cosines
+constexpr int kThreads = 128;
 
 struct RotaryTensor {
     const void* x;
@@ -36,10 +35,9 @@ struct RotaryArgs {
     long long pos_batch;    // its batch stride
     long long first;
     int B, S, R, D;
-    int tokens;        // of a CTA
-    int heads_cta;     // of a CTA, q's and k's counted through
-    int rot_slots;     // pieces of a head that are turned
-    int slots;         // and all of them (the rest are copied)
+    int heads_thread;  // heads that a thread goes through, q's and k's counted through
+    int rot_slots;     // threads of a token whose piece is turned
+    int slots;         // and all of them (the rest copy)
     bool pos32, inverse;
     float amplitude;
 };
@@ -64,115 +62,99 @@ __device__ __forceinline__ unsigned long long turns_of(double f) {
 }
 
 template <typename T, int V>
-struct Piece {
+struct alignas(sizeof(T) * V) Piece {
     T e[V];
 };
-template <typename T, int V>
-struct alignas(sizeof(T) * V) PieceAligned : Piece<T, V> {};
 
-// One 2 V-element pair of pieces (half layout), or one piece (interleaved pairs, copies).
-// V elements an access; interleaved pairs need two elements a thread, which V = 1 takes in two accesses.
+// V elements an access, and two accesses a thread and head: pieces `apart` channels apart (half layout, copies), or, of
+// interleaved pairs, one piece of V elements (V = 1: the pair's two).
 template <typename T, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-    using P = PieceAligned<T, V>;
-    constexpr int W = kInterleaved && V == 1 ? 2 : V;  // elements of a piece
-    constexpr int kUnroll = 4;
-    extern __shared__ __align__(16) float s_cs[];  // [tokens][R / 2] cosines, then sines
-    const int tid = threadIdx.x, half = a.R / 2;
-    const int per_seq = (a.S + a.tokens - 1) / a.tokens;
-    const int b = blockIdx.x / per_seq, s0 = (blockIdx.x - b * per_seq) * a.tokens;
-    const int n = min(a.tokens, a.S - s0);
-    float* s_cos = s_cs;
-    float* s_sin = s_cs + a.tokens * half;
+    using P = Piece<T, V>;
+    constexpr bool kOne = kInterleaved && V > 1;                      // one access a thread and head where it turns
+    constexpr int kPairs = kInterleaved ? (V > 1 ? V / 2 : 1) : V;    // pairs of a thread
+    constexpr int kUnroll = kOne ? 8 : 4;                             // heads on their way
+    const int id = blockIdx.x * kThreads + threadIdx.x, token = id / a.slots, slot = id - token * a.slots;
+    if (token >= a.B * a.S) return;
+    const int b = token / a.S, s = token - b * a.S, half = a.R / 2;
+    const bool turn = slot < a.rot_slots;
+    // the thread's first channel, how far its second piece is, and whether it has one
+    int c, apart;
+    bool two = true;
+    if (turn) {
+        c = slot * (kOne ? V : kInterleaved ? 2 : V);
+        apart = kInterleaved ? 1 : half;
+        two = !kOne;
+    } else {
+        const int copies = a.slots - a.rot_slots;
+        c = a.R + (slot - a.rot_slots) * V;
+        apart = copies * V;
+        two = c + apart < a.D;
+    }
     ptx::griddep_wait();
-    for (int i = tid; i < n * half; i += kThreads) {
-        const int tok = i / half, f = i - tok * half;
-        long long pos = a.first + s0 + tok;
+    float cs[kPairs], sn[kPairs];
+    if (turn) {
+        long long pos = a.first + s;
         if (a.positions) {
-            const long long at = b * a.pos_batch + s0 + tok;
+            const long long at = b * a.pos_batch + s;
             pos = a.pos32 ? (long long)static_cast<const int32_t*>(a.positions)[at]
                           : static_cast<const long long*>(a.positions)[at];
         }
-        const long long angle = (long long)((unsigned long long)pos * turns_of(a.inv_freq[f]));
-        float sn, cs;
-        sincospif(__ll2float_rn(angle) * 0x1p-63f, &sn, &cs);  // half turns in [-1, 1]
-        s_cos[i] = a.amplitude * cs;
-        s_sin[i] = a.amplitude * (a.inverse ? -sn : sn);
-    }
-    __syncthreads();
-
-    const int h_lo = blockIdx.y * a.heads_cta, h_n = min(a.heads_cta, a.t[0].heads + a.t[1].heads - h_lo);
-    const int rows = h_n * n;  // (head, token), tokens fastest
-    // this thread's (row, slot), moved on by kThreads pieces at a time
-    const int step_row = kThreads / a.slots, step_slot = kThreads - step_row * a.slots;
-    int row = tid / a.slots, slot = tid - row * a.slots;
-    while (row < rows) {
-        P x[kUnroll][kInterleaved ? (W / V) : 2];
-        T* dst[kUnroll];
-        int tk[kUnroll], sl[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            sl[u] = -1;
-            if (row < rows) {
-                const int hh = row / n, tok = row - hh * n;
-                int h = h_lo + hh;
-                const int w = h >= a.t[0].heads;
-                if (w) h -= a.t[0].heads;
-                const RotaryTensor& t = a.t[w];
-                const long long s = s0 + tok;
-                int c;  // first channel
-                if (slot < a.rot_slots) c = slot * W;
-                else c = a.R + (slot - a.rot_slots) * V;
-                const T* src = static_cast<const T*>(t.x) + b * t.xs[0] + h * t.xs[1] + s * t.xs[2] + c;
-                dst[u] = static_cast<T*>(t.y) + b * t.ys[0] + h * t.ys[1] + s * t.ys[2] + c;
-                sl[u] = slot;
-                tk[u] = tok;
-                x[u][0] = *reinterpret_cast<const P*>(src);
-                if (slot < a.rot_slots) {
-                    if (kInterleaved) {
-                        if (W != V) x[u][W / V - 1] = *reinterpret_cast<const P*>(src + 1);
-                    } else {
-                        x[u][1 % (kInterleaved ? (W / V) : 2)] = *reinterpret_cast<const P*>(src + half);
-                    }
-                }
-                slot += step_slot;
-                row += step_row;
-                if (slot >= a.slots) {
-                    slot -= a.slots;
-                    ++row;
-                }
-            }
+        for (int i = 0; i < kPairs; ++i) {
+            const unsigned long long f = turns_of(a.inv_freq[slot * kPairs + i]);
+            const long long angle = (long long)((unsigned long long)pos * f);
+            float x, y;
+            sincospif(__ll2float_rn(angle) * 0x1p-63f, &x, &y);  // half turns in [-1, 1]
+            sn[i] = a.amplitude * (a.inverse ? -x : x);
+            cs[i] = a.amplitude * y;
         }
+    }
+    const int lo = blockIdx.y * a.heads_thread, hi = min(lo + a.heads_thread, a.t[0].heads + a.t[1].heads);
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        const RotaryTensor& t = a.t[w];
+        const int before = w ? a.t[0].heads : 0, h0 = max(lo, before), h1 = min(hi, before + t.heads);
+        if (h0 >= h1) continue;
+        const T* x = static_cast<const T*>(t.x) + b * t.xs[0] + (h0 - before) * t.xs[1] + s * t.xs[2] + c;
+        T* y = static_cast<T*>(t.y) + b * t.ys[0] + (h0 - before) * t.ys[1] + s * t.ys[2] + c;
+        const long long dx = t.xs[1], dy = t.ys[1];
+#pragma unroll 1
+        for (int h = h0; h < h1; h += kUnroll, x += kUnroll * dx, y += kUnroll * dy) {
+            P p[kUnroll], q[kOne ? 1 : kUnroll];
+            const int n = h1 - h;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (sl[u] < 0) continue;
-            if (sl[u] < a.rot_slots) {
-                if (kInterleaved) {
-                    const float* cs = s_cos + tk[u] * half + sl[u] * (W / 2);
-                    const float* sn = s_sin + tk[u] * half + sl[u] * (W / 2);
+            for (int u = 0; u < kUnroll; ++u)
+                if (u < n) {
+                    p[u] = *reinterpret_cast<const P*>(x + u * dx);
+                    if (!kOne && two) q[u] = *reinterpret_cast<const P*>(x + u * dx + apart);
+                }
+            if (turn) {
 #pragma unroll
-                    for (int i = 0; i < W / 2; ++i) {
-                        T& ea = x[u][0].e[V == 1 ? 0 : 2 * i];
-                        T& eb = x[u][W / V - 1].e[V == 1 ? 0 : 2 * i + 1];
+                for (int u = 0; u < kUnroll; ++u)
+#pragma unroll
+                    for (int i = 0; i < kPairs; ++i) {
+                        T& ea = p[u].e[kOne ? 2 * i : i];
+                        T& eb = kOne ? p[u].e[(2 * i + 1) % V] : q[kOne ? 0 : u].e[kOne ? 0 : i];
                         const float fa = to_f32(ea), fb = to_f32(eb);
                         ea = from_f32<T>(fa * cs[i] - fb * sn[i]);
                         eb = from_f32<T>(fb * cs[i] + fa * sn[i]);
                     }
-                    if (W != V) *reinterpret_cast<P*>(dst[u] + 1) = x[u][W / V - 1];
-                } else {
-                    const float* cs = s_cos + tk[u] * half + sl[u] * V;
-                    const float* sn = s_sin + tk[u] * half + sl[u] * V;
-                    constexpr int k1 = kInterleaved ? 0 : 1;
-#pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float fa = to_f32(x[u][0].e[i]), fb = to_f32(x[u][k1].e[i]);
-                        x[u][0].e[i] = from_f32<T>(fa * cs[i] - fb * sn[i]);
-                        x[u][k1].e[i] = from_f32<T>(fb * cs[i] + fa * sn[i]);
-                    }
-                    *reinterpret_cast<P*>(dst[u] + half) = x[u][k1];
-                }
             }
-            *reinterpret_cast<P*>(dst[u]) = x[u][0];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (u < n) {
+                    *reinterpret_cast<P*>(y + u * dy) = p[u];
+                    if (!kOne && two) *reinterpret_cast<P*>(y + u * dy + apart) = q[u];
+                }
+            if (kOne && two) {  // (a copying thread's second pieces)
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+                    if (u < n) p[u] = *reinterpret_cast<const P*>(x + u * dx + apart);
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u)
+                    if (u < n) *reinterpret_cast<P*>(y + u * dy + apart) = p[u];
+            }
         }
     }
     ptx::griddep_launch_dependents();
@@ -180,25 +162,19 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 
 template <typename T, int V, bool kInterleaved>
 cudaError_t launch(RotaryArgs a, int sms, cudaStream_t stream) {
-    constexpr int W = kInterleaved && V == 1 ? 2 : V;
-    a.rot_slots = kInterleaved ? a.R / W : a.R / 2 / V;
+    a.rot_slots = a.R / 2 / (kInterleaved ? (V > 1 ? V / 2 : 1) : V);
     const bool copies = a.t[0].x != a.t[0].y || (a.t[1].heads && a.t[1].x != a.t[1].y);
-    a.slots = a.rot_slots + (copies ? (a.D - a.R) / V : 0);
-    // tokens of a CTA: many, so that a sine serves all heads of a wave of CTAs' worth of work; fewer where
-    // they would leave SMs without a CTA, and then the heads are shared out too
-    const int heads = a.t[0].heads + a.t[1].heads, half = a.R / 2;
-    int tokens = kMaxTokens;
-    while (tokens > 1 && (tokens * half * 2 > kTableFloats || (long long)a.B * ((a.S + tokens - 1) / tokens) < 2 * sms))
-        tokens /= 2;
-    a.tokens = tokens;
-    const long long ctas = (long long)a.B * ((a.S + tokens - 1) / tokens);
-    int split = 1;
-    while (ctas * split < sms && (long long)heads * tokens * a.slots > (long long)split * kThreads) split *= 2;
-    a.heads_cta = (heads + split - 1) / split;
+    a.slots = a.rot_slots + (copies ? ((a.D - a.R) / V + 1) / 2 : 0);
+    // heads of a thread: all, so that its sines serve them all, unless that leaves an SM fewer than 1024 threads; then
+    // half as many, down to one
+    const int heads = a.t[0].heads + a.t[1].heads;
+    const long long threads = (long long)a.B * a.S * a.slots;
+    a.heads_thread = heads;
+    while (a.heads_thread > 1 && threads * ((heads + a.heads_thread - 1) / a.heads_thread) < 1024ll * sms)
+        a.heads_thread = (a.heads_thread + 1) / 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)((heads + a.heads_cta - 1) / a.heads_cta));
+    cfg.gridDim = dim3((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)((heads + a.heads_thread - 1) / a.heads_thread));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = (size_t)tokens * half * 2 * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -252,7 +228,8 @@ extern "C" gdn_status gdn_rotary(const void* q, const void* k, const double* inv
     if (d->B < 0 || d->S < 0 || d->Hq < 0 || d->Hk < 0 || d->D < 1 || d->R < 2 || d->R > d->D || d->R % 2 ||
         d->D > GDN_ROTARY_MAX_D || d->Hq > 65536 || d->Hk > 65536)
         return GDN_ERR_DIMS;
-    if (d->B > INT32_MAX || d->S > INT32_MAX || d->B * d->S > INT32_MAX) return GDN_ERR_DIMS;
+    // (a thread a piece of a token's channels, counted in 32 bits)
+    if (d->B > INT32_MAX || d->S > INT32_MAX || d->B * d->S > (INT32_MAX - 4096) / d->D) return GDN_ERR_DIMS;
     if (d->B == 0 || d->S == 0 || d->Hq + d->Hk == 0) return GDN_OK;
     if (!inv_freq || (d->Hq && (!q || !q_out)) || (d->Hk && (!k || !k_out))) return GDN_ERR_NULL;
     const int el = d->dtype == GDN_BF16 ? 2 : 4;

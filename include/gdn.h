@@ -546,7 +546,7 @@ enum {
 #define GDN_ROTARY_MAX_D 4096
 
 /*
- * B, S >= 0 (B S < 2^31); Hq, Hk in [0, 65536] heads of q and of k (0: that tensor is not there); head dim
+ * B, S >= 0 (B S D < 2^31 - 4096); Hq, Hk in [0, 65536] heads of q and of k (0: that tensor is not there); head dim
  * 1 <= D <= GDN_ROTARY_MAX_D, of which the first R are turned (even, 2 <= R <= D).  Strides in elements over
  * (batch, head, token), >= 0; channels are contiguous.
  */

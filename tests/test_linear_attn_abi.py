@@ -83,8 +83,8 @@ def test_linear_attn_segments(L):
 
 def rotary_dims(B=2, Hq=4, Hk=2, S=8, D=128, R=64, dtype=gdn.GDN_BF16, flags=0, qs=None, ks=None, qo=None, ko=None):
     hm = lambda H: (H * S * D, S * D, D)  # noqa: E731
-    return gdn.GdnRotaryDims(B, Hq, Hk, S, D, R, qs or hm(Hq), ks or hm(Hk), qo or hm(Hq), ko or hm(Hk), S, 0, dtype, flags,
-                             1.0)
+    return gdn.GdnRotaryDims(B, Hq, Hk, S, D, R, *(qs or hm(Hq)), *(ks or hm(Hk)), *(qo or hm(Hq)), *(ko or hm(Hk)), S, 0,
+                             dtype, flags, 1.0)
 
 
 def test_rotary_argument_checks(L):
