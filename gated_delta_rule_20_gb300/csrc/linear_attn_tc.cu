@@ -50,6 +50,8 @@ constexpr float kMinRow = -64.f * kLog2e;  // least m_i, in powers of two
 // Registers a thread of each role; what the block is launched with covers their sum (launch checks it).
 constexpr int kRegsP = 72, kRegsS = 112, kRegsV = 56, kRegsO = 56, kRegsCtl = 40;
 constexpr int kRegsSum = (kRegsP + 2 * kRegsS + 2 * kRegsV + kRegsO + kRegsCtl) * 128;
+// (the first role keeps what it is launched with: the others' rise and fall add up without it)
+static_assert(kRegsP == 65536 / kThreads / 8 * 8, "registers a thread at launch");
 
 struct Small {
     float c[2][kC];      // sums of log2-decays within blocks of 32
@@ -126,32 +128,24 @@ __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigne
 }
 __device__ __forceinline__ uint32_t pack2(unsigned long long x) { return pack_bf16x2(pair_lo(x), pair_hi(x)); }
 
-// The two bf16 values in x, as fp32, and a - (those): products and sums of fp32 with bf16 (fma.rn.f32.bf16), which run on the
-// FMA pipe, where shifts, masks and byte permutations take the ALU's, at half the rate and shared with everything else.
-__device__ __forceinline__ void widen2(uint32_t x, float& lo, float& hi) {
-    asm("{\n\t.reg .b16 l, h, one;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 one, 0x3F80;\n\t"
-        "fma.rn.f32.bf16 %0, l, one, %3;\n\tfma.rn.f32.bf16 %1, h, one, %3;\n\t}"
-        : "=f"(lo), "=f"(hi)
-        : "r"(x), "f"(-0.f));
-}
+// lo and hi less the two bf16 values in x (fma.rn.f32.bf16: on the FMA pipe, and no widening of x first).
 __device__ __forceinline__ void less2(uint32_t x, float& lo, float& hi) {
     asm("{\n\t.reg .b16 l, h, minus;\n\tmov.b32 {l, h}, %2;\n\tmov.b16 minus, 0xBF80;\n\t"
         "fma.rn.f32.bf16 %0, l, minus, %0;\n\tfma.rn.f32.bf16 %1, h, minus, %1;\n\t}"
         : "+f"(lo), "+f"(hi)
         : "r"(x));
 }
-// The two bf16 values in m, times d, as the sum of three bf16 values each: an fp32 product's 24 bits, 8 at a time (the
-// differences are exact).
+// The two bf16 values in m, times d, as the sum of three bf16 values each: an fp32 product's 24 bits, cut off 8 at a time
+// (the differences are exact).  The work is spread over the pipes: widening and cutting on the ALU (a byte permutation cuts
+// two values and packs them), products and differences on the FMA pipe; either pipe alone is 2 to 4 us slower of 87.
 __device__ __forceinline__ void three_parts(uint32_t m, float d0, float d1, uint32_t& p0, uint32_t& p1, uint32_t& p2) {
-    float a, b;
-    widen2(m, a, b);
-    a *= d0;
-    b *= d1;
-    p0 = pack_bf16x2(a, b);
+    const auto cut = [](float a, float b) { return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632); };
+    float a = bf16lo_to_f32(m) * d0, b = bf16hi_to_f32(m) * d1;
+    p0 = cut(a, b);
     less2(p0, a, b);
-    p1 = pack_bf16x2(a, b);
+    p1 = cut(a, b);
     less2(p1, a, b);
-    p2 = pack_bf16x2(a, b);
+    p2 = cut(a, b);
 }
 
 __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]) {
