@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } was[2] = {{0, 0, 0}, {0, 0, 0}};  // chunks cn - 2 and cn - 1 (n = 0: none)
                 Walk k = first_item(it);
                 bool more = settle(k, p, it);
-                Walk far = k;  // a chunk two ahead, whose tiles are brought into L2
+                Walk far = k;  // a chunk two ahead, whose K and q are brought into L2 (V's load has the time)
                 bool ahead = more && next_chunk(far, p, it);
                 // The engine works in order: what is needed first goes first.  V, out of which parts are made; the outputs of
                 // chunk cn - 2, which leave the q tile that chunk cn takes; K and q; then the prefetch
@@ -701,7 +701,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int fhk = it.group.of(far.bh);
 #pragma unroll 1
                             for (int x = 0; x < 128; x += 64) {
-                                if (x < p.Dv) tma_prefetch_l2_3d(&tv, x, far.t, far.bh);
                                 if (x < p.Dk) {
                                     tma_prefetch_l2_3d(&tk, x, far.t, fhk);
                                     if (!kStatesOnly) tma_prefetch_l2_3d(&tq, x, far.t, fhk);

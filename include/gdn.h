@@ -509,10 +509,15 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * tokens: products of bf16 operands with fp32 sums; the decayed scores and the copy of the state that the queries
  * read are rounded to bf16 once (the outputs' own type).  The state itself is fp32 and is updated with
  * three bf16 parts of exp(.) v, which add up to its 24 bits.  What a chunk's decays leave of the state is taken as
- * e^-64 of it at least in the chunk's outputs (1.6e-28).  fp32, and other head dims, run the recurrence on the FMA units.
+ * e^-64 of it at least in the chunk's outputs (1.6e-28).  An infinity in v or k makes what it reaches NaN there.
+ * fp32, and other head dims, run the recurrence itself on the FMA units.
  * Few sequences of many tokens are cut into segments that run at once (gdn_linear_attn_segments; GDN_SINGLE_PASS:
- * never): a first launch runs all but the last from zero and keeps their states and decays, the second starts each segment
- * from the state that they add up to.  Results of a split agree with one pass's to within rounding.
+ * never): a first launch runs all but the last from zero and keeps their states and decays, a second adds them up to the
+ * segments' start states (nothing to do for two segments), and the last runs every segment.  Results of a split agree with one
+ * pass's to within rounding.  The same call on the same device gives the same bits; a batch's sequences do not
+ * influence one another's, unless another batch size changes the split.
+ * A wait inside the tensor-core kernel that runs out (a second or two) ends it with GDN_ERR_TIMEOUT in the device's status
+ * word (gdn_device_status) and undefined outputs.
  */
 gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, const float* g_log,
                                    const int32_t* lengths, float scale, const float* state_in, float* state_out,
@@ -529,7 +534,7 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims);
 
 /*
  * gdn_linear_attn_step -- one token of every sequence (dims->S == 1, else GDN_ERR_DIMS): the arguments of
- * gdn_linear_attn_prefill, in fp32 throughout.  The state is read once and written once, in one launch.
+ * gdn_linear_attn_prefill (no lengths), in fp32 throughout.  The state is read once and written once, in one launch.
  */
 gdn_status gdn_linear_attn_step(const void* q, const void* k, const void* v, const float* g_log, float scale,
                                 const float* state_in, float* state_out, void* out, const gdn_dims* dims,

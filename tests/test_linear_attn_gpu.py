@@ -206,11 +206,10 @@ def test_step_from_nothing_and_reset():
 def test_operands_off_16_bytes():
     """Views that start at odd elements: no tensor-core tiles, no vectors, the same results."""
     x = inputs(1, 1, 2, 140, 128, 128, "bf16")
-    shift = lambda t: torch.cat([t.flatten()[:1], t.flatten()])[1:].view(t.shape)  # noqa: E731
     scale = 0.1
     out, st, size = ref.recurrence(x["q"], x["k"], x["v"], x["g"], scale, x["state"])
     d = {n: torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t) for n, t in x.items()}
-    assert all(t.data_ptr() % 16 for t in d.values()) and shift is not None
+    assert all(t.data_ptr() % 16 for t in d.values())
     new = torch.empty(d["state"].numel() + 1, device="cuda")[1:].view(d["state"].shape)
     y = gdn.linear_attn_prefill(d["q"], d["k"], d["v"], d["g"], scale, d["state"], state_out=new)
     compare(y, (out, st), size, "bf16", False, "unaligned")
