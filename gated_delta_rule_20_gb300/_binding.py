@@ -832,7 +832,11 @@ def linear_attn_prefill(q, k, v, g_log, scale, state=None, out=None, *, lengths=
     behind them have no influence and are not written (zeros in a new ``out``).  ``single_pass`` sets
     ``GDN_SINGLE_PASS``; ``workspace``: a uint8 CUDA tensor of ``linear_attn_workspace_bytes`` bytes (default: torch's).
     Returns ``(out, state_out)``."""
-    new = out is None
+    if out is None and lengths is not None and stream is None:
+        out = _torch().zeros_like(v)
+        new = False
+    else:
+        new = out is None
     d, device, qp, kp, vp, gp, sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
                                                                                   stream)
     if force_ffma:
@@ -843,7 +847,7 @@ def linear_attn_prefill(q, k, v, g_log, scale, state=None, out=None, *, lengths=
     if lengths is not None:
         lp = _layer_ptr("lengths", lengths, (d.B,), _T.int32, device)
         if new:
-            with _T.cuda.stream(stream if stream is not None else _T.cuda.current_stream(device)):
+            with _T.cuda.stream(stream):
                 out.zero_()
     if workspace is not None:
         if workspace.device != device or workspace.dtype != _T.uint8 or not workspace.is_contiguous():
