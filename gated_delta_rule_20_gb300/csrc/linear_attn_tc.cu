@@ -85,6 +85,10 @@ __device__ __forceinline__ void tmem_st16x128_x2(uint32_t taddr, uint32_t r0, ui
                  : "memory");
 }
 
+// The same for 4 columns.
+__device__ __forceinline__ void tmem_st16x128_x1(uint32_t taddr, uint32_t r0, uint32_t r1) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x1.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(r0), "r"(r1) : "memory");
+}
 // 32 lanes x 16 consecutive columns.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
     asm volatile(
@@ -306,10 +310,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.tfree[i], 1);
             mbar_init(&sh.staged[i], 128);
             mbar_init(&sh.decfull[i], 32);
-            mbar_init(&sh.decfree[i], kStatesOnly ? 513 : 769);
+            mbar_init(&sh.decfree[i], 769);  // 24 warps and the thread of the products
         }
         for (int i = 0; i < kSlots; ++i) {
-            mbar_init(&sh.vfull[i], 256);
+            mbar_init(&sh.vfull[i], 128 * (kStatesOnly ? 4 : 2));
             mbar_init(&sh.vfree[i], 1);
         }
         mbar_init(&sh.sfull, 256);
@@ -343,10 +347,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     int cn = 0;      // chunks so far, over all items
     bool ok = true;  // no wait has run out
-    if (warp < 4) {
+    // the first pass has no scores and no outputs: their warps make parts of V too
+    constexpr int kGroups = kStatesOnly ? 4 : 2;
+    const bool parts_role = kStatesOnly ? warp < 4 || (warp >= 12 && warp < 24) : warp >= 12 && warp < 20;
+    if (!kStatesOnly && warp < 4) {
         // ------------------------------------------------------------ scores -> P
         const int a = quad;
-        for (; !kStatesOnly; ++cn) {
+        for (;; ++cn) {
             const int s = cn & 1;
             ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
             if (!ok || sh.n[s] == 0) break;
@@ -417,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(&sh.pfull);
             mbar_arrive(&sh.decfree[s]);
         }
-    } else if (warp < 12) {
+    } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------ the state: thread = 64 rows of column dv
         regs_inc<kRegsS>();
         const int dv = quad * 32 + lane, half = (warp - 4) >> 2;
@@ -505,14 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 });
             }
         }
-    } else if (warp < 20) {
+    } else if (parts_role) {
         // ------------------------------------------------------------ parts of e^. V
         regs_dec<kRegsV>();
-        const int o2 = (warp - 12) >> 2;  // which 16 tokens of a slot
-        const int tok = o2 * 16 + (lane & 7);
+        constexpr int kOct = 4 / kGroups;  // of 8 tokens, of a slot's four, a warp
+        const int group = warp < 4 ? 3 : (warp - 12) >> 2;
+        const int tok = group * (kSub / kGroups) + (lane & 7);
         // the 16-byte piece of a row that this lane's address takes
         const uint32_t piece = (quad >> 1) * kHalf + sw128_offset(tok, (quad & 1) * 64 + (lane >> 3) * 16);
-        const uint32_t at = tq4 + kColV + 8 * o2;
+        const uint32_t at = tq4 + kColV + 4 * kOct * group;
         const bool there = quad * 32 < p.Dv;
         int vi = 0;  // slots so far
         for (;; ++cn) {
@@ -525,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* vt = sm + kOffV + s * kTile;
             if (n < subs * kSub && p.lengths) {
                 // rows behind the last token in the last 32: whatever they hold is not multiplied, not even by zero.
-                // A warp clears the columns that it reads itself, of V and of K (two warps the same ones)
+                // A warp clears the columns that it reads itself, of V and of K (some warps the same ones)
                 const int rows = subs * kSub - n;
                 ok = wait_warp(&sh.kqfull[s], (cn >> 1) & 1);
                 if (!ok) break;
@@ -538,12 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             uint32_t from = smem_u32(vt) + piece;
-            const float* h = &sh.h[s][o2 * 16 + 2 * (lane & 3)];
-            uint32_t m[2][4];
-            float2 hh[2];
-            const auto fetch = [&] {  // a slot's 16 tokens of this warp
+            const float* h = &sh.h[s][group * (kSub / kGroups) + 2 * (lane & 3)];
+            uint32_t m[kOct][4];
+            float2 hh[kOct];
+            const auto fetch = [&] {  // a slot's tokens of this warp
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
+                for (int o = 0; o < kOct; ++o) {
                     ldmatrix_x4_trans(from + o * 1024, m[o]);
                     hh[o] = *reinterpret_cast<const float2*>(h + 8 * o);
                 }
@@ -554,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int u = 0; u < subs; ++u, ++vi) {
                 const int slot = vi & 1, turn = vi >> 1;
-                uint32_t part[3][2][4];  // [part][8 tokens][8 columns dv], made before the slot is free
+                uint32_t part[3][kOct][4];  // [part][8 tokens][8 columns dv], made before the slot is free
                 const float wb = sh.w[s][u];
 #pragma unroll
-                for (int o = 0; o < 2; ++o) {
+                for (int o = 0; o < kOct; ++o) {
                     const float d0 = hh[o].x * wb, d1 = hh[o].y * wb;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) three_parts(m[o][i], d0, d1, part[0][o][i], part[1][o][i], part[2][o][i]);
@@ -571,11 +579,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_after();
                     const uint32_t to = at + slot * kSlotCols;
 #pragma unroll
-                    for (int q = 0; q < 3; ++q) {
-                        tmem_st16x128_x2(to + 16 * q, part[q][0][0], part[q][0][1], part[q][1][0], part[q][1][1]);
-                        tmem_st16x128_x2(to + 16 * q + (16u << 16), part[q][0][2], part[q][0][3], part[q][1][2],
-                                         part[q][1][3]);
-                    }
+                    for (int q = 0; q < 3; ++q)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {  // 16 of the warp's columns dv each
+                            const uint32_t dst = to + 16 * q + (r ? 16u << 16 : 0u);
+                            const uint32_t *x = part[q][0] + 2 * r, *y = part[q][kOct - 1] + 2 * r;
+                            if (kOct == 2)
+                                tmem_st16x128_x2(dst, x[0], x[1], y[0], y[1]);
+                            else
+                                tmem_st16x128_x1(dst, x[0], x[1]);
+                        }
                     tmem_wait_st();
                     tc_fence_before();
                 }
@@ -584,11 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             mbar_arrive(&sh.decfree[s]);
         }
-    } else if (warp < 24) {
+    } else if (!kStatesOnly && warp >= 20 && warp < 24) {
         // ------------------------------------------------------------ outputs
         regs_dec<kRegsO>();
         const int r = quad * 32 + lane;
-        for (; !kStatesOnly; ++cn) {
+        for (;; ++cn) {
             const int s = cn & 1;
             ok = wait_warp(&sh.decfull[s], (cn >> 1) & 1);
             const int n = sh.n[s];
