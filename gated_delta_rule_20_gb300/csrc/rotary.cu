@@ -178,14 +178,16 @@ cudaError_t launch(RotaryArgs a, int sms, cudaStream_t stream) {
     const bool copies = a.t[0].x != a.t[0].y || (a.t[1].heads && a.t[1].x != a.t[1].y);
     a.slots = a.rot_slots + (!copies ? 0 : kInterleaved && V > 1 ? (a.D - a.R) / V : ((a.D - a.R) / V + 1) / 2);
     // heads of a thread: all, so that its sines serve them all, unless that leaves an SM fewer than 1024 threads; then
-    // half as many, down to one
+    // half as many, down to one or to the most parts that a grid has
+    constexpr int kMostParts = 65535;
     const int heads = a.t[0].heads + a.t[1].heads;
     const long long threads = (long long)a.B * a.S * a.slots;
     a.heads_thread = heads;
-    while (a.heads_thread > 1 && threads * ((heads + a.heads_thread - 1) / a.heads_thread) < 1024ll * sms)
+    const auto parts = [&](int each) { return (heads + each - 1) / each; };
+    while (a.heads_thread > 1 && threads * parts(a.heads_thread) < 1024ll * sms && parts((a.heads_thread + 1) / 2) <= kMostParts)
         a.heads_thread = (a.heads_thread + 1) / 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)((heads + a.heads_thread - 1) / a.heads_thread));
+    cfg.gridDim = dim3((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)parts(a.heads_thread));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -227,6 +229,31 @@ bool rows_meet(const int64_t* sizes, const int64_t* st, int64_t D) {
     return false;
 }
 
+// Whether rows a and b (D elements each) share no memory though what they span does: there is a period that all longer
+// strides of both are multiples of, and in it what the shorter ones of a reach ends before b's begins, and the other way
+// round.  (q and k in packed rows: the period is a token's stride, a head's, or a batch's.)
+bool apart(const void* a, const int64_t* na, const int64_t* sa, const void* b, const int64_t* nb, const int64_t* sb, int64_t D,
+           int el) {
+    const int64_t from = (int64_t)(reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / el;
+    for (int c = 0; c < 6; ++c) {
+        const int64_t period = c < 3 ? sa[c] : sb[c - 3];
+        if (period == 0) continue;
+        const auto reach = [&](const int64_t* n, const int64_t* st) {  // -1: a longer stride is not a multiple
+            int64_t r = D;
+            for (int j = 0; j < 3; ++j) {
+                if (st[j] < period)
+                    r += (n[j] - 1) * st[j];
+                else if (st[j] % period)
+                    return (int64_t)-1;
+            }
+            return r;
+        };
+        const int64_t ra = reach(na, sa), rb = reach(nb, sb), at = (from % period + period) % period;
+        if (ra > 0 && rb > 0 && at >= ra && at + rb <= period) return true;
+    }
+    return false;
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -245,6 +272,7 @@ extern "C" gdn_status gdn_rotary(const void* q, const void* k, const double* inv
     if (d->B == 0 || d->S == 0 || d->Hq + d->Hk == 0) return GDN_OK;
     if (!inv_freq || (d->Hq && (!q || !q_out)) || (d->Hk && (!k || !k_out))) return GDN_ERR_NULL;
     const int el = d->dtype == GDN_BF16 ? 2 : 4;
+    constexpr int64_t kSpan = int64_t(1) << 56;  // elements that a dim's rows may lie apart (byte counts stay within 64 bits)
     const bool i32 = (d->flags & GDN_ROTARY_POSITIONS_I32) != 0;
     if ((reinterpret_cast<uintptr_t>(inv_freq) & 7) || (reinterpret_cast<uintptr_t>(positions) & (i32 ? 3 : 7)))
         return GDN_ERR_ALIGN;
@@ -256,7 +284,11 @@ extern "C" gdn_status gdn_rotary(const void* q, const void* k, const double* inv
     void* ys[2] = {q_out, k_out};
     const int64_t* xst[2] = {d->q_strides, d->k_strides};
     const int64_t* yst[2] = {d->q_out_strides, d->k_out_strides};
-    const int64_t heads[2] = {d->Hq, d->Hk};
+    const int64_t heads[2] = {d->Hq, d->Hk}, sizes[2][3] = {{d->B, d->Hq, d->S}, {d->B, d->Hk, d->S}};
+    long long nx[2], ny[2];
+    bool in_place[2];
+    if (d->position_stride < 0 || (d->B > 1 && d->position_stride > kSpan / (d->B - 1))) return GDN_ERR_DIMS;
+    const long long np = ((d->B - 1) * d->position_stride + d->S) * (i32 ? 4 : 8);
     for (int i = 0; i < 2; ++i) {
         a.t[i].heads = (int)heads[i];
         if (!heads[i]) continue;
@@ -264,23 +296,34 @@ extern "C" gdn_status gdn_rotary(const void* q, const void* k, const double* inv
         if ((px | py) & (el - 1)) return GDN_ERR_ALIGN;
         a.t[i].x = xs[i];
         a.t[i].y = ys[i];
-        const int64_t sizes[3] = {d->B, heads[i], d->S};
         bool same = true;
         for (int j = 0; j < 3; ++j) {
-            constexpr int64_t kMost = int64_t(1) << 40;  // (what a tensor spans is below 2^31 2^40 elements a dim)
-            if (xst[i][j] < 0 || yst[i][j] < 0 || (sizes[j] > 1 && (xst[i][j] > kMost || yst[i][j] > kMost)))
-                return GDN_ERR_DIMS;
-            const bool used = sizes[j] > 1;  // a stride that is never taken may be anything
+            const bool used = sizes[i][j] > 1;  // a stride that is never taken may be anything
+            if (xst[i][j] < 0 || yst[i][j] < 0) return GDN_ERR_DIMS;
+            if (used && (xst[i][j] > kSpan / (sizes[i][j] - 1) || yst[i][j] > kSpan / (sizes[i][j] - 1))) return GDN_ERR_DIMS;
             a.t[i].xs[j] = used ? xst[i][j] : 0;
             a.t[i].ys[j] = used ? yst[i][j] : 0;
             odd |= (uint64_t)a.t[i].xs[j] | (uint64_t)a.t[i].ys[j];
             same = same && a.t[i].xs[j] == a.t[i].ys[j];
         }
-        if (rows_meet(sizes, a.t[i].ys, d->D)) return GDN_ERR_DIMS;
+        if (rows_meet(sizes[i], a.t[i].ys, d->D)) return GDN_ERR_DIMS;
         odd |= (px | py) / el;
-        const long long nx = extent(d, heads[i], a.t[i].xs) * el, ny = extent(d, heads[i], a.t[i].ys) * el;
-        if (overlap(xs[i], nx, ys[i], ny) && !(px == py && same)) return GDN_ERR_UNSUPPORTED;
-        if (overlap(ys[i], ny, inv_freq, d->R * 4)) return GDN_ERR_UNSUPPORTED;
+        nx[i] = extent(d, heads[i], a.t[i].xs) * el;
+        ny[i] = extent(d, heads[i], a.t[i].ys) * el;
+        in_place[i] = px == py && same;
+        if (overlap(ys[i], ny[i], inv_freq, d->R * 4) || overlap(ys[i], ny[i], positions, np)) return GDN_ERR_UNSUPPORTED;
+    }
+    // an output shares no memory with the other one, nor with an input but its own in place
+    for (int i = 0; i < 2; ++i) {
+        for (int j = 0; j < 2; ++j) {
+            if (!heads[i] || !heads[j]) continue;
+            if (!(i == j && in_place[i]) && overlap(ys[i], ny[i], xs[j], nx[j]) &&
+                !apart(ys[i], sizes[i], a.t[i].ys, xs[j], sizes[j], a.t[j].xs, d->D, el))
+                return GDN_ERR_UNSUPPORTED;
+            if (i < j && overlap(ys[i], ny[i], ys[j], ny[j]) &&
+                !apart(ys[i], sizes[i], a.t[i].ys, ys[j], sizes[j], a.t[j].ys, d->D, el))
+                return GDN_ERR_UNSUPPORTED;
+        }
     }
     int v = 16 / el;
     while (v > 1 && odd % v) v /= 2;

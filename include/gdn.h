@@ -553,7 +553,7 @@ enum {
 /*
  * B, S >= 0 (B S D < 2^31 - 4096); Hq, Hk in [0, 65536] heads of q and of k (0: that tensor is not there); head dim
  * 1 <= D <= GDN_ROTARY_MAX_D, of which the first R are turned (even, 2 <= R <= D).  Strides in elements over
- * (batch, head, token), >= 0; channels are contiguous.
+ * (batch, head, token), >= 0, a dim's last row at most 2^56 elements from its first; channels are contiguous.
  */
 typedef struct {
     int64_t B, Hq, Hk, S, D, R;
@@ -570,8 +570,9 @@ typedef struct {
  *     y_a = amplitude (x_a cos theta - x_b sin theta),   y_b = amplitude (x_b cos theta + x_a sin theta)
  * for the channel pairs (a, b) = (i, i + R/2), or (2i, 2i + 1), i < R/2; channels from R on are copied.
  *   q, q_out   [B, Hq, S, D] in dtype at their strides (views into packed rows, head-major or token-major);
- *              q_out may be q at the same strides, and otherwise may not share memory with it
- *              (GDN_ERR_UNSUPPORTED); its rows may not lie over one another (GDN_ERR_DIMS).  k, k_out likewise
+ *              q_out may be q at the same strides, and otherwise may not share memory with an input or with k_out
+ *              (GDN_ERR_UNSUPPORTED; rows that lie among one another are taken where their strides show them apart, as
+ *              those of packed rows do); its rows may not lie over one another (GDN_ERR_DIMS).  k, k_out likewise
  *   inv_freq   [R/2] fp64, radians a position (fp32 ones of a model: widened)
  *   positions  int64 (or int32) [B, S], tokens contiguous, or NULL
  * theta is taken mod one turn exactly (2^-64 of a turn a position), so that its accuracy does not fall with

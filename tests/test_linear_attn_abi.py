@@ -114,6 +114,40 @@ def test_rotary_argument_checks(L):
     assert call(D(), f=OUT) == gdn.GDN_ERR_UNSUPPORTED
 
 
+def test_rotary_refuses_outputs_over_other_operands(L):
+    D = rotary_dims
+    call = lambda d, q=Q, k=K, pos=G, qo=OUT, ko=WS: L.gdn_rotary(q, k, V, pos, qo, ko, d, None)  # noqa: E731
+    same = dict(Hq=2, Hk=2)
+    assert call(D(**same), qo=K) == gdn.GDN_ERR_UNSUPPORTED                # q_out over k, k_out over q, one another
+    assert call(D(**same), ko=Q) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(D(**same), qo=K, ko=Q) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(D(**same), qo=WS) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(D(**same), q=K, qo=K) == gdn.GDN_ERR_UNSUPPORTED           # q in place while k is the same rows
+    assert call(D(**same), pos=OUT + 64) == gdn.GDN_ERR_UNSUPPORTED
+    # packed rows of 6 heads (q 4, k 2), in place: k that begins one channel inside q's last head, or whose last
+    # head runs into the next token's q
+    row = dict(qs=(8 * 768, 128, 768), ks=(8 * 768, 128, 768), qo=(8 * 768, 128, 768), ko=(8 * 768, 128, 768))
+    assert call(D(**row), k=Q + 2 * 511, qo=Q, ko=Q + 2 * 511) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(D(**row), k=Q + 2 * 513, qo=Q, ko=Q + 2 * 513) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(D(**row), k=Q - 2 * 255, qo=Q, ko=Q - 2 * 255) == gdn.GDN_ERR_UNSUPPORTED
+    # other strides, which show nothing
+    assert call(D(**dict(row, ks=(8 * 700, 128, 700))), k=Q + 1024, qo=Q, ko=WS) == gdn.GDN_ERR_UNSUPPORTED
+
+
+def test_rotary_refuses_strides_past_64_bits(L):
+    D = rotary_dims
+    call = lambda d: L.gdn_rotary(Q, K, V, G, OUT, WS, d, None)  # noqa: E731
+    far = 1 << 56
+    for name in ("qs", "ks", "qo", "ko"):
+        assert call(D(**{name: (far + 1, 8 * 128, 128)})) == gdn.GDN_ERR_DIMS, name
+    assert call(D(B=3, Hq=1, S=1, R=64, qs=(far // 2 + 1, 128, 128))) == gdn.GDN_ERR_DIMS
+    assert call(D(B=1 << 20, Hq=1, Hk=1, S=1, qs=(1 << 40, 128, 128))) == gdn.GDN_ERR_DIMS
+    for stride in (-1, far + 1):
+        d = D()
+        d.position_stride = stride
+        assert call(d) == gdn.GDN_ERR_DIMS
+
+
 def test_bindings_refuse_host_tensors():
     bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
     with pytest.raises(ValueError):

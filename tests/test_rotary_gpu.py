@@ -153,3 +153,25 @@ def test_refusals():
     flat = torch.zeros(2 * 2 * 4 * 16 + 8, device="cuda", dtype=torch.bfloat16)
     with pytest.raises(gdn.GdnError):
         gdn.rotary(flat[:256].view(2, 2, 4, 16), None, f, q_out=flat[8:].view(2, 2, 4, 16))
+
+
+def test_more_heads_than_a_grid_has_parts():
+    # one token of 2 x 65536 heads: a thread takes two heads, for want of a 65536th row of blocks
+    q, k = (torch.randn(1, 65536, 1, 2, generator=torch.Generator().manual_seed(i)).cuda() for i in (1, 2))
+    f = freq(2)
+    yq, yk = gdn.rotary(q, k, f, first_position=3)
+    check(yq, q, f, np.array([3]), "f32", 2)
+    check(yk, k, f, np.array([3]), "f32", 2)
+
+
+def test_heads_of_q_and_k_in_turn_in_place():
+    # [B, S, H, 2, D]: every q head beside its k head, and [B, 2, H, S, D]: q's heads before k's within a sequence
+    B, S, H, D = 2, 5, 3, 16
+    f = freq(D)
+    for shape, q_of, k_of in (((B, S, H, 2, D), lambda x: x[:, :, :, 0].transpose(1, 2), lambda x: x[:, :, :, 1].transpose(1, 2)),
+                              ((B, 2, H, S, D), lambda x: x[:, 0], lambda x: x[:, 1])):
+        x = torch.randn(shape, generator=torch.Generator().manual_seed(len(shape))).cuda()
+        was = x.clone()
+        gdn.rotary(q_of(x), k_of(x), f, first_position=7, q_out=q_of(x), k_out=k_of(x))
+        check(q_of(x), q_of(was), f, np.arange(7, 7 + S), "f32", D)
+        check(k_of(x), k_of(was), f, np.arange(7, 7 + S), "f32", D)
