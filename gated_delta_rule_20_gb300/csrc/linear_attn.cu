@@ -471,7 +471,8 @@ gdn_status check_dims(const gdn_dims* d, bool step) {
     if (d->flags & ~kKnownFlags) return GDN_ERR_UNSUPPORTED;
     if (d->B < 0 || d->Hk < 1 || d->Hv < 1 || d->S < 0 || d->Dk < 1 || d->Dv < 1) return GDN_ERR_DIMS;
     if (d->Dk > kMaxD || d->Dv > kMaxD || d->Hv % d->Hk != 0 || (step && d->S != 1)) return GDN_ERR_DIMS;
-    if (d->B > INT32_MAX || d->Hv > INT32_MAX || d->S > INT32_MAX || d->B * d->Hv > INT32_MAX) return GDN_ERR_DIMS;
+    // (tokens are counted in 32 bits, to the end of the last chunk of 128)
+    if (d->B > INT32_MAX || d->Hv > INT32_MAX || d->S > INT32_MAX - 4096 || d->B * d->Hv > INT32_MAX) return GDN_ERR_DIMS;
     if (d->B * d->Hv > (int64_t(1) << 48) / (d->S + 1)) return GDN_ERR_DIMS;  // byte counts stay within 64 bits
     return GDN_OK;
 }

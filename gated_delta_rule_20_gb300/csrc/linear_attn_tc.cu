@@ -912,10 +912,13 @@ template <bool kStatesOnly>
 gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
                   int32_t* status, cudaStream_t stream) {
     auto* kernel = linear_attn_tc_kernel<kStatesOnly>;
-    static const int regs = [&] {
+    static std::atomic<int> launched{0};  // registers a thread of the block at launch
+    int regs = launched.load(std::memory_order_relaxed);
+    if (regs == 0) {
         cudaFuncAttributes a{};
-        return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;
-    }();
+        if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return GDN_ERR_CUDA;
+        launched.store(regs = a.numRegs, std::memory_order_relaxed);
+    }
     static std::atomic<bool> allowed[kMaxDevices];
     // the roles' registers come out of what the block is launched with: short of that they would wait for ever
     if (regs * kThreads < kRegsSum) return GDN_ERR_CUDA;

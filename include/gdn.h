@@ -498,7 +498,8 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  *   state_in    [B, Hv, Dk, Dv] fp32, Dv contiguous, or NULL: zeros
  *   state_out   the same, receives the state behind the last token; may be state_in
  *   out         [B, Hv, S, Dv]  compute dtype
- *   dims        gdn_dims; flags: GDN_HEAD_DECAY, GDN_FORCE_FFMA, GDN_SINGLE_PASS.  S = 0 copies the state
+ *   dims        gdn_dims (S < 2^31 - 4096); flags: GDN_HEAD_DECAY, GDN_FORCE_FFMA, GDN_SINGLE_PASS.  S = 0 copies the
+ *               state
  *   workspace   device memory of workspace_bytes >= gdn_linear_attn_workspace_bytes(dims) bytes, 16-byte
  *               aligned, not touched by anything else until the call's work on `stream` has finished; NULL: the call
  *               takes what it needs with cudaMallocAsync on `stream`, and runs one pass where that fails.  Too small:
@@ -509,7 +510,9 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * tokens: products of bf16 operands with fp32 sums; the decayed scores and the copy of the state that the queries
  * read are rounded to bf16 once (the outputs' own type).  The state itself is fp32 and is updated with
  * three bf16 parts of exp(.) v, which add up to its 24 bits.  What a chunk's decays leave of the state is taken as
- * e^-64 of it at least in the chunk's outputs (1.6e-28).  An infinity in v or k makes what it reaches NaN there.
+ * e^-64 of it at least in the chunk's outputs (1.6e-28).  An infinity or NaN in v may make NaN of its column's
+ * outputs from the beginning of its chunk on (a score of zero in front of it is multiplied too), one in k from its
+ * token on, one in q of its token's; |q . k| of 5e10 and more behind decays of e^-64 passes bf16's range.
  * fp32, and other head dims, run the recurrence itself on the FMA units.
  * Few sequences of many tokens are cut into segments that run at once (gdn_linear_attn_segments; GDN_SINGLE_PASS:
  * never): a first launch runs all but the last from zero and keeps their states and decays, a second adds them up to the
