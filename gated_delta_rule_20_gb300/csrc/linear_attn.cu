@@ -418,7 +418,7 @@ cudaError_t launch_ffma_rows(const LinearAttn& p, const LinearAttnSplit& s, int 
         warps /= 2;
     if (s.P > 1) {
         cudaError_t e = launch_ffma_kernel<T, MB, true, kAsync>(p, s, warps, dev, stream);
-        if (e == cudaSuccess) e = launch_linear_attn_combine(p, s, sms, stream);
+        if (e == cudaSuccess) e = launch_linear_attn_combine(p, s, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_ffma_kernel<T, MB, false, kAsync>(p, s, warps, dev, stream);
@@ -435,17 +435,39 @@ cudaError_t launch_ffma(const LinearAttn& p, const LinearAttnSplit& s, int dev, 
 }
 
 // ------------------------------------------------------------------ the states of a split
-// X_j += F_j X_{j-1} for j = 1 .. P - 2, a thread an element, its loads of all segments independent of the sums.
-__global__ void __launch_bounds__(256) linear_attn_combine_kernel(LinearAttnSplit s, long long heads, long long n) {
+// X_j += F_j X_{j-1} for j = 1 .. P - 2: a thread V elements of a state, the loads of eight segments at once in front of their
+// sums.  n elements of a state are `slices` CTAs' work.
+template <int V>
+__global__ void __launch_bounds__(256) linear_attn_combine_kernel(LinearAttnSplit s, int heads, int slices, int n) {
+    struct alignas(4 * V) Some {
+        float e[V];
+    };
+    const int bh = blockIdx.x / slices, at = ((blockIdx.x - bh * slices) * 256 + threadIdx.x) * V;
     ptx::griddep_wait();
-    const long long all = heads * n;
-    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (long long)gridDim.x * blockDim.x) {
-        const long long bh = i / n;
-        float x = s.parts[i];
-#pragma unroll 8
-        for (int j = 1; j < s.P - 1; ++j) {
-            x = fmaf(s.decays[j * heads + bh], x, s.parts[j * all + i]);
-            s.parts[j * all + i] = x;
+    if (at < n) {
+        float* part = s.parts + (long long)bh * n + at;
+        const float* decay = s.decays + bh;
+        const long long next = (long long)heads * n;
+        Some x = *reinterpret_cast<const Some*>(part);
+#pragma unroll 1
+        for (int left = s.P - 2; left > 0; left -= 8) {
+            Some y[8];
+            float f[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (u < left) {
+                    y[u] = *reinterpret_cast<const Some*>(part + (u + 1) * next);
+                    f[u] = decay[(long long)(u + 1) * heads];
+                }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (u < left) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) x.e[i] = fmaf(f[u], x.e[i], y[u].e[i]);
+                    *reinterpret_cast<Some*>(part + (u + 1) * next) = x;
+                }
+            part += 8 * next;
+            decay += 8ll * heads;
         }
     }
     ptx::griddep_launch_dependents();
@@ -453,11 +475,12 @@ __global__ void __launch_bounds__(256) linear_attn_combine_kernel(LinearAttnSpli
 
 }  // namespace
 
-cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream) {
+cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSplit& s, cudaStream_t stream) {
     if (s.P <= 2) return cudaSuccess;
-    const long long heads = (long long)p.B * p.Hv, n = (long long)p.Dk * p.Dv, blocks = (heads * n + 255) / 256;
-    return launch_after(linear_attn_combine_kernel, dim3((unsigned)(blocks < 8ll * sms ? blocks : 8ll * sms)), 256, 0, stream,
-                        s, heads, n);
+    const int heads = p.B * p.Hv, n = p.Dk * p.Dv, V = n % 4 == 0 ? 4 : 1, slices = (n + 256 * V - 1) / (256 * V);
+    const dim3 grid((unsigned)(heads * slices));  // (a split's states fit in memory: far fewer than 2^31)
+    if (V == 4) return launch_after(linear_attn_combine_kernel<4>, grid, 256, 0, stream, s, heads, slices, n);
+    return launch_after(linear_attn_combine_kernel<1>, grid, 256, 0, stream, s, heads, slices, n);
 }
 
 namespace {

@@ -56,6 +56,6 @@ gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, 
                                  cudaStream_t stream);
 
 // The second launch (nothing for P = 2).
-cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSplit& s, int sms, cudaStream_t stream);
+cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSplit& s, cudaStream_t stream);
 
 }  // namespace gdn

@@ -956,7 +956,7 @@ gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, 
     if (s.P > 1) {
         const gdn_status e = launch<true>(m, p, s, dev, sms, status, stream);
         if (e != GDN_OK) return e;
-        if (launch_linear_attn_combine(p, s, sms, stream) != cudaSuccess) return GDN_ERR_CUDA;
+        if (launch_linear_attn_combine(p, s, stream) != cudaSuccess) return GDN_ERR_CUDA;
     }
     return launch<false>(m, p, s, dev, sms, status, stream);
 }
