@@ -4,8 +4,9 @@
 //     S_t = e^{g_t} S_{t-1} + k_t v_t^T,     o_t = scale * S_t^T q_t        S fp32 [Dk, Dv] per (batch, value head)
 //
 // Step.  One pass over the state: S' = e^g S + k v^T is written as it is read and o = scale q^T S' summed on the
-// way, so the state's bytes bound it.  Columns of S are independent: a CTA owns one head's slice of 32, 64 or
-// 128 columns.
+// way, so the state's bytes bound it.  A thread has all of its loads (32 numbers, in registers) on their way at once and makes
+// its stores before the sums over rows go through shared memory; 64 registers a thread let an SM hold 128 KB of loads.
+// Measured (128 x 128): 64 x 32 heads 41 us, 6.6 TB/s of the 6.8 that a copy reaches; 4 x 32 heads 3.2 us, 1 x 32 heads 2.0 us.
 //
 // Prefill on the FMA units (fp32 compute, and head dims off the tensor-core kernel): the recurrence itself, token by
 // token, with the state in registers.  Its 2 Dk Dv multiply-adds a token are the fewest of any form (a chunked one adds
@@ -32,87 +33,94 @@ namespace {
 constexpr int kMaxD = 128;
 
 // ------------------------------------------------------------------ single-token step
-constexpr int kStepThreads = 256;
+// How a CTA's threads lie over its slice of V C columns: thread = V neighbouring columns of every rgs-th row, so that
+// whole rows are read and written as one piece of memory.  kFlat (whole rows that are no multiple of 16 bytes, of heads that
+// are): rgs rows are cut into C pieces of 4, whichever rows these begin and end in; as rgs Dv is a multiple of 4, a thread's
+// pieces lie in the same columns all the same.
+struct StepShape {
+    int C, rgs;   // threads of a row (kFlat: of rgs rows); rows at once
+    int group;    // value heads of a key head
+    uint32_t by;  // tid / C = tid by >> 16
+};
+template <int V>
+struct alignas(4 * V) StepPiece {
+    float e[V];
+};
 
-template <typename T, int C4, bool kVec>
-__global__ void __launch_bounds__(kStepThreads) linear_attn_step_kernel(LinearAttn p) {
-    constexpr int kRg = kStepThreads / C4, kRows = kMaxD / kRg, kCols = 4 * C4;
-    __shared__ float s_q[kMaxD], s_k[kMaxD];
-    __shared__ __align__(16) float s_red[kRg][kCols];
-    const long long bh = blockIdx.x;
-    const int b = (int)(bh / p.Hv), h = (int)(bh - (long long)b * p.Hv), hk = h / (p.Hv / p.Hk);
-    const int tid = threadIdx.x, cg = tid % C4, rg = tid / C4, base = blockIdx.y * kCols;
-    const int Dk = p.Dk, Dv = p.Dv;
-    // a thread's 4 columns: neighbours for 128-bit accesses, else C4 apart so that lanes are neighbours
-    int c[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c[j] = base + (kVec ? 4 * cg + j : cg + j * C4);
-    const size_t at = (size_t)bh * Dk * Dv;
+// kRows: a thread's rows at most, all of them on their way at once.
+template <typename T, int V, bool kFlat, int kRows, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) linear_attn_step_kernel(LinearAttn p, StepShape w) {
+    using P = StepPiece<V>;
+    __shared__ float s_q[kMaxD + 1], s_k[kMaxD + 1];
+    __shared__ __align__(16) float s_red[V * kThreads];
+    const int bh = blockIdx.x, C = w.C, rgs = w.rgs, tid = threadIdx.x, Dk = p.Dk, Dv = p.Dv;
+    const int cols = kFlat ? Dv : V * C, base = blockIdx.y * cols;
+    const int rg = kFlat ? V * tid / Dv : (int)(tid * w.by >> 16), c = base + V * tid - rg * cols;
+    const bool live = kFlat ? tid < C : rg < rgs;
+    const int rows = live && c < Dv ? Dk : 0;  // (the last few threads may have none)
+    const size_t at = (size_t)bh * Dk * Dv + (size_t)rg * Dv + c;
+    const int down = rgs * Dv;  // to a thread's next row
     ptx::griddep_wait();
 
-    float4 S[kRows];
+    P S[kRows] = {};
+    if (p.state_in) {
+        const float* from = p.state_in + at;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = rg + i * kRg;
-        S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (p.state_in && r < Dk) {
-            const float* row = p.state_in + at + (size_t)r * Dv;
-            if (kVec) {
-                if (c[0] < Dv) S[i] = __ldcs(reinterpret_cast<const float4*>(row + c[0]));
-            } else {
-                if (c[0] < Dv) S[i].x = row[c[0]];
-                if (c[1] < Dv) S[i].y = row[c[1]];
-                if (c[2] < Dv) S[i].z = row[c[2]];
-                if (c[3] < Dv) S[i].w = row[c[3]];
+        for (int i = 0; i < kRows; ++i, from += down) {
+            if (rg + i * rgs < rows) {
+                if constexpr (V == 4)
+                    *reinterpret_cast<float4*>(&S[i]) = __ldcs(reinterpret_cast<const float4*>(from));
+                else
+                    S[i].e[0] = *from;
             }
         }
     }
-    float v[4];
+    const int b = bh / p.Hv, h = bh - b * p.Hv, hk = h / w.group;
+    float v[V] = {}, o[V] = {};
+    if (rows) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = c[j] < Dv ? to_f32(static_cast<const T*>(p.v)[(size_t)bh * Dv + c[j]]) : 0.f;
-    if (tid < Dk) {
-        const size_t row = ((size_t)b * p.Hk + hk) * Dk + tid;
-        s_q[tid] = to_f32(static_cast<const T*>(p.q)[row]);
-        s_k[tid] = to_f32(static_cast<const T*>(p.k)[row]);
+        for (int j = 0; j < V; ++j)
+            v[j] = to_f32(static_cast<const T*>(p.v)[(size_t)bh * Dv + c + j - (kFlat && c + j >= Dv ? Dv : 0)]);
+    }
+    for (int i = tid; i < Dk; i += blockDim.x) {
+        const size_t row = ((size_t)b * p.Hk + hk) * Dk + i;
+        s_q[i] = to_f32(static_cast<const T*>(p.q)[row]);
+        s_k[i] = to_f32(static_cast<const T*>(p.k)[row]);
     }
     const float a = expf(least_decay(p.g_log[p.head_decay ? h : bh]));
     __syncthreads();
 
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+    float* to = p.state_out + at;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int r = rg + i * kRg;
-        if (r < Dk) {
-            const float k = s_k[r], q = s_q[r];
-            float4 x;
-            x.x = fmaf(a, S[i].x, k * v[0]);
-            x.y = fmaf(a, S[i].y, k * v[1]);
-            x.z = fmaf(a, S[i].z, k * v[2]);
-            x.w = fmaf(a, S[i].w, k * v[3]);
-            o[0] = fmaf(q, x.x, o[0]);
-            o[1] = fmaf(q, x.y, o[1]);
-            o[2] = fmaf(q, x.z, o[2]);
-            o[3] = fmaf(q, x.w, o[3]);
-            float* row = p.state_out + at + (size_t)r * Dv;
-            if (kVec) {
-                if (c[0] < Dv) __stcs(reinterpret_cast<float4*>(row + c[0]), x);
-            } else {
-                if (c[0] < Dv) row[c[0]] = x.x;
-                if (c[1] < Dv) row[c[1]] = x.y;
-                if (c[2] < Dv) row[c[2]] = x.z;
-                if (c[3] < Dv) row[c[3]] = x.w;
+    for (int i = 0; i < kRows; ++i, to += down) {
+        const int r = rg + i * rgs;
+        if (r < rows) {
+            const float k0 = s_k[r], q0 = s_q[r], k1 = kFlat ? s_k[r + 1] : 0.f, q1 = kFlat ? s_q[r + 1] : 0.f;
+            P x;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const bool next = kFlat && c + j >= Dv;
+                const float k = next ? k1 : k0, q = next ? q1 : q0;
+                x.e[j] = fmaf(a, S[i].e[j], k * v[j]);
+                o[j] = fmaf(q, x.e[j], o[j]);
             }
+            if constexpr (V == 4)
+                __stcs(reinterpret_cast<float4*>(to), *reinterpret_cast<const float4*>(&x));
+            else
+                *to = x.e[0];
         }
     }
     ptx::griddep_launch_dependents();
+    if (live) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s_red[rg][c[j] - base] = o[j];
+        for (int j = 0; j < V; ++j) s_red[V * tid + j] = o[j];
+    }
     __syncthreads();
-    if (tid < kCols && base + tid < Dv) {
+    for (int i = tid; i < cols && base + i < Dv; i += blockDim.x) {
         float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kRg; ++i) sum += s_red[i][tid];
-        static_cast<T*>(p.out)[(size_t)bh * Dv + base + tid] = from_f32<T>(p.scale * sum);
+#pragma unroll 8
+        for (int g = 0; g < rgs; ++g) sum += s_red[g * cols + i];
+        static_cast<T*>(p.out)[(size_t)bh * Dv + base + i] = from_f32<T>(p.scale * sum);
     }
 }
 
@@ -133,22 +141,53 @@ cudaError_t launch_after(K* kernel, dim3 grid, int threads, size_t smem, cudaStr
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-template <typename T, int C4>
-cudaError_t launch_step_cols(const LinearAttn& p, cudaStream_t stream) {
-    const dim3 grid((unsigned)(p.B * p.Hv), (unsigned)((p.Dv + 4 * C4 - 1) / (4 * C4)));
-    if (p.Dv % 4 == 0 && aligned16(p.state_in) && aligned16(p.state_out))
-        return launch_after(linear_attn_step_kernel<T, C4, true>, grid, kStepThreads, 0, stream, p);
-    return launch_after(linear_attn_step_kernel<T, C4, false>, grid, kStepThreads, 0, stream, p);
+template <typename T, int V, bool kFlat>
+cudaError_t launch_step_shape(const LinearAttn& p, const StepShape& w, int slices, int threads, cudaStream_t stream) {
+    constexpr int kMost = 32 / V;  // rows of a thread
+    const dim3 grid((unsigned)(p.B * p.Hv), (unsigned)slices);
+    if (threads > 256) return launch_after(linear_attn_step_kernel<T, V, kFlat, kMost, 512>, grid, threads, 0, stream, p, w);
+    if (p.Dk > kMost / 2 * w.rgs)
+        return launch_after(linear_attn_step_kernel<T, V, kFlat, kMost, 256>, grid, threads, 0, stream, p, w);
+    return launch_after(linear_attn_step_kernel<T, V, kFlat, kMost / 2, 256>, grid, threads, 0, stream, p, w);
+}
+
+template <typename T, int V>
+cudaError_t launch_step_rows(const LinearAttn& p, int sms, cudaStream_t stream) {
+    const long long heads = (long long)p.B * p.Hv;
+    // Columns of a head are independent: a CTA takes a slice of them.  Slices of 32 columns spread a few heads over the card (32
+    // heads of 128 x 128 2.0 us, whole 3.1; 160 heads 3.7 and 4.7); of many heads, slices that keep to lines of 128 bytes finish
+    // more evenly than whole heads (2048 heads of 128 x 96 in 32s 32 us, whole 33), others are slower (128 x 100: 46 and 29).
+    const int width = heads < 2 * sms ? 32 : p.Dv % 64 == 0 ? 64 : p.Dv % 32 == 0 ? 32 : 128;
+    const int slices = (p.Dv + width - 1) / width;
+    StepShape w;
+    w.C = ((p.Dv + slices - 1) / slices + V - 1) / V;
+    w.group = p.Hv / p.Hk;
+    w.by = 65536u / w.C + 1;
+    // CTAs as small as leave a thread 32 numbers: an SM holds the more of them (2048 heads of 32 x 32: 3.8 us in 64 threads, 6.2 in
+    // 256).
+    const auto fits = [&](int threads) { return threads / w.C * (32 / V) >= p.Dk; };
+    int threads = fits(256) ? 256 : 512;
+    if (heads * slices >= 2 * sms)
+        while (threads > 64 && fits(threads / 2)) threads /= 2;
+    w.rgs = threads / w.C;
+    return launch_step_shape<T, V, false>(p, w, slices, threads, stream);
 }
 
 template <typename T>
 cudaError_t launch_step(const LinearAttn& p, int sms, cudaStream_t stream) {
-    // Slices as wide as leave every SM a CTA: whole rows of 128 columns keep the most loads in flight a
-    // thread, narrow ones spread a few heads over the card.
-    const long long heads = (long long)p.B * p.Hv;
-    if (p.Dv > 64 && heads >= sms) return launch_step_cols<T, 32>(p, stream);
-    if (p.Dv > 32 && heads * ((p.Dv + 63) / 64) >= sms) return launch_step_cols<T, 16>(p, stream);
-    return launch_step_cols<T, 8>(p, stream);
+    const bool aligned = aligned16(p.state_in) && aligned16(p.state_out);
+    if (aligned && p.Dv % 4 == 0) return launch_step_rows<T, 4>(p, sms, stream);
+    if (aligned && p.Dk * p.Dv % 4 == 0 && p.Dv >= 4 && (long long)p.B * p.Hv >= 2 * sms) {
+        // (2048 heads of 96 x 75: 21 us instead of 24 by single numbers, of 128 x 33 14 and 17)
+        const int unit = p.Dv % 2 ? 4 : 2;  // of rows that are pieces of 16 bytes together
+        StepShape w;
+        w.rgs = ((p.Dk + 7) / 8 + unit - 1) / unit * unit;
+        w.C = w.rgs * p.Dv / 4;
+        w.group = p.Hv / p.Hk;
+        w.by = 0;
+        return launch_step_shape<T, 4, true>(p, w, 1, (w.C + 31) / 32 * 32, stream);
+    }
+    return launch_step_rows<T, 1>(p, sms, stream);
 }
 
 // ------------------------------------------------------------------ prefill on the FMA units
@@ -313,7 +352,8 @@ __global__ void __launch_bounds__(256, 2) linear_attn_ffma_kernel(LinearAttn p, 
         const bool blockwise = __all_sync(0xffffffffu, !(fabsf(c_in) > kMostBlock) || lane >= kTok);
         const float total = __shfl_sync(0xffffffffu, c_in, kTok - 1);
         if (warp == 0 && lane < kTok)
-            s_a[turn & 1][lane] = blockwise ? make_float4(1.f, expf(-c_in), expf(c_in), 0.f) : make_float4(expf(g), 1.f, 1.f, 0.f);
+            s_a[turn & 1][lane] =
+                blockwise ? make_float4(1.f, expf(-c_in), expf(c_in), 0.f) : make_float4(expf(g), 1.f, 1.f, 0.f);
         if (kAsync) ptx::cp_async_wait_all();
         __syncthreads();  // the buffer and s_a are there; the other buffer has been read
         if (kAsync && t + kTok < t1) {
@@ -612,7 +652,8 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
         s = gdn::status_word_for_current_device(&status);
         if (s == GDN_OK) s = gdn::launch_linear_attn_tc(p, split, dev, sms, status, st);
     } else {
-        const bool async = !p.bf16 && p.Dk % 4 == 0 && p.Dv % 4 == 0 && gdn::aligned16(q) && gdn::aligned16(k) && gdn::aligned16(v);
+        const bool async =
+            !p.bf16 && p.Dk % 4 == 0 && p.Dv % 4 == 0 && gdn::aligned16(q) && gdn::aligned16(k) && gdn::aligned16(v);
         const cudaError_t e = p.bf16  ? gdn::launch_ffma<__nv_bfloat16, false>(p, split, dev, sms, st)
                               : async ? gdn::launch_ffma<float, true>(p, split, dev, sms, st)
                                       : gdn::launch_ffma<float, false>(p, split, dev, sms, st);

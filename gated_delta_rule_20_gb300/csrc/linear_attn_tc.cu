@@ -292,7 +292,8 @@ template <bool kStatesOnly>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
-                          const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split, const __grid_constant__ Items it, int32_t* status) {
+                          const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split,
+                          const __grid_constant__ Items it, int32_t* status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small& sh = *reinterpret_cast<Small*>(sm + kOffSmall);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;

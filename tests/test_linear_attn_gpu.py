@@ -178,7 +178,11 @@ def test_prompt_in_two_halves_and_token_by_token(dtype):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("shape", [(1, 1, 1, 128, 128), (1, 16, 32, 128, 128), (64, 4, 8, 128, 128), (3, 2, 6, 64, 128),
-                                   (5, 1, 3, 75, 33), (2, 2, 2, 1, 1), (7, 3, 3, 128, 96), (300, 1, 1, 16, 8), (2, 1, 1, 96, 75)],
+                                   (5, 1, 3, 75, 33), (2, 2, 2, 1, 1), (7, 3, 3, 128, 96), (300, 1, 1, 16, 8), (2, 1, 1, 96, 75),
+                                   # many heads: rows of whole 16 bytes, pieces that run from one row into the next, single numbers
+                                   (80, 8, 8, 24, 96), (80, 4, 8, 128, 64), (41, 3, 9, 96, 75), (40, 2, 8, 128, 127), (77, 4, 4, 2, 6),
+                                   (152, 1, 2, 8, 5), (39, 8, 8, 127, 4), (80, 8, 8, 44, 33), (80, 8, 8, 45, 33), (50, 4, 8, 7, 100),
+                                   (70, 9, 9, 128, 3), (80, 8, 8, 98, 90), (77, 8, 8, 1, 128), (40, 8, 8, 127, 127)],
                          ids=lambda s: "x".join(map(str, s)))
 @pytest.mark.parametrize("decay", ["token", "head"])
 def test_step(shape, dtype, decay):
