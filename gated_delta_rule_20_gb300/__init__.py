@@ -32,7 +32,7 @@ from ._binding import (ACTIVATIONS, EXPORTED, GDN_F8E4M3, GDN_LINEAR_FORCE_FFMA,
                        GDN_LINEAR_WEIGHT_NK, GDN_BF16, GDN_ERR_ALIGN, GDN_ERR_CUDA, GDN_ERR_DIMS, GDN_ERR_NULL,
                        GDN_ERR_TIMEOUT, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE, GDN_F32, GDN_FORCE_FFMA, GDN_HEAD_DECAY, GDN_OK,
                        GDN_ROTARY_INTERLEAVED, GDN_ROTARY_INVERSE, GDN_ROTARY_POSITIONS_I32,
-                       GDN_SINGLE_PASS, GDN_ZERO_INITIAL_STATE, LIB_PATH, GdnBlockDims, GdnConvDims, GdnDims,
+                       GDN_SINGLE_PASS, GDN_ZERO_INITIAL_STATE, GDN_ZERO_PADDING, LIB_PATH, GdnBlockDims, GdnConvDims, GdnDims,
                        GdnError, GdnLinearDims, GdnRotaryDims, conv1d_decode, conv1d_prefill, decode_block, decode_block_noalloc,
                        decode_block_workspace_bytes, decode_gated, decode_step, device_status, kernels_per_call, lib,
                        linear, linear_attn_prefill, linear_attn_segments, linear_attn_step,
@@ -49,5 +49,5 @@ __all__ = ["prefill", "prefill_segments", "prefill_segment_starts", "decode_step
            "GDN_FORCE_FFMA", "GDN_SINGLE_PASS", "rmsnorm_residual", "linear", "linear_gated", "linear_plan",
            "GdnLinearDims", "ACTIVATIONS", "GDN_F8E4M3", "GDN_LINEAR_WEIGHT_NK", "GDN_LINEAR_GATED",
            "GDN_LINEAR_FORCE_FFMA", "linear_attn_prefill", "linear_attn_step", "linear_attn_segments",
-           "linear_attn_workspace_bytes", "rotary", "rotary_frequencies", "GdnRotaryDims", "GDN_HEAD_DECAY",
+           "linear_attn_workspace_bytes", "rotary", "rotary_frequencies", "GdnRotaryDims", "GDN_HEAD_DECAY", "GDN_ZERO_PADDING",
            "GDN_ROTARY_INTERLEAVED", "GDN_ROTARY_INVERSE", "GDN_ROTARY_POSITIONS_I32"]

@@ -31,6 +31,7 @@ GDN_ZERO_INITIAL_STATE = 1 << 0
 GDN_FORCE_FFMA = 1 << 1
 GDN_SINGLE_PASS = 1 << 2
 GDN_HEAD_DECAY = 1 << 3
+GDN_ZERO_PADDING = 1 << 4
 
 GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_GELU, GDN_ACT_RELU = range(4)
 ACTIVATIONS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU, "gelu": GDN_ACT_GELU, "relu": GDN_ACT_RELU}
@@ -554,15 +555,22 @@ def decode_block_noalloc(hidden, W_qkv, W_z, W_a, W_b, conv_weight, conv_state, 
 _T = None          # torch
 _LAYER_CODES = {}  # torch dtype -> gdn_dtype
 _raw_stream = None
+_raw_alloc = _raw_free = None
 
 
 def _layer_init():
-    global _T, _raw_stream
+    global _T, _raw_stream, _raw_alloc, _raw_free
     import torch
     _LAYER_CODES.update({torch.bfloat16: GDN_BF16, torch.float32: GDN_F32, torch.float8_e4m3fn: GDN_F8E4M3})
     # the handle of a device's current stream without a Stream object (2 us less), where torch has it
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
+    # torch's memory without a tensor around it (5 us less between two calls)
+    _raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+    _raw_free = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+    if _raw_alloc is None or _raw_free is None:
+        _raw_alloc, _raw_free = torch.cuda.caching_allocator_alloc, torch.cuda.caching_allocator_delete
+        _raw_alloc = lambda size, stream, alloc=_raw_alloc: alloc(size, None, stream)  # noqa: E731
     lib()
     _T = torch
 
@@ -832,41 +840,46 @@ def linear_attn_prefill(q, k, v, g_log, scale, state=None, out=None, *, lengths=
     behind them have no influence and are not written (zeros in a new ``out``).  ``single_pass`` sets
     ``GDN_SINGLE_PASS``; ``workspace``: a uint8 CUDA tensor of ``linear_attn_workspace_bytes`` bytes (default: torch's).
     Returns ``(out, state_out)``."""
-    if out is None and lengths is not None and stream is None:
-        out = _torch().zeros_like(v)
-        new = False
-    else:
-        new = out is None
+    zero = GDN_ZERO_PADDING if out is None and lengths is not None else 0
     d, device, qp, kp, vp, gp, sp, np_, op, out, state_out = _linear_attn_operands(q, k, v, g_log, state, state_out, out,
                                                                                   stream)
+    flags = d.flags | zero
     if force_ffma:
-        d.flags |= GDN_FORCE_FFMA
+        flags |= GDN_FORCE_FFMA
     if single_pass:
-        d.flags |= GDN_SINGLE_PASS
-    lp = wp = None
-    if lengths is not None:
-        lp = _layer_ptr("lengths", lengths, (d.B,), _T.int32, device)
-        if new:
-            with _T.cuda.stream(stream):
-                out.zero_()
+        flags |= GDN_SINGLE_PASS
+    d.flags = flags
+    lp = None if lengths is None else _layer_ptr("lengths", lengths, (d.B,), _T.int32, device)
     if workspace is not None:
         if workspace.device != device or workspace.dtype != _T.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous uint8 CUDA tensor on %s" % device)
-        wp, nbytes = workspace.data_ptr(), workspace.numel()
+        _layer_call(_lib.gdn_linear_attn_prefill, device, stream, qp, kp, vp, gp, lp, scale, sp, np_, op, d,
+                    workspace.data_ptr(), workspace.numel())
+    elif device.index == _T.cuda.current_device():
+        _linear_attn_prefill(device, stream, (qp, kp, vp, gp, lp, scale, sp, np_, op, d))
     else:
-        if device.index == _T.cuda.current_device():
-            nbytes = _lib.gdn_linear_attn_workspace_bytes(d)
-        else:
-            with _T.cuda.device(device):
-                nbytes = _lib.gdn_linear_attn_workspace_bytes(d)
-        if nbytes:  # from torch, which keeps it between calls
-            try:
-                workspace = _layer_empty((nbytes,), _T.uint8, device, stream)
-                wp = workspace.data_ptr()
-            except _T.OutOfMemoryError:
-                nbytes = 0  # the library asks for its own, and runs one pass where there is none
-    _layer_call(_lib.gdn_linear_attn_prefill, device, stream, qp, kp, vp, gp, lp, scale, sp, np_, op, d, wp, nbytes)
+        with _T.cuda.device(device):
+            _linear_attn_prefill(device, stream, (qp, kp, vp, gp, lp, scale, sp, np_, op, d))
     return out, state_out
+
+
+def _linear_attn_prefill(device, stream, args):
+    """The call with a workspace of torch's, which goes back to torch behind it, in the stream's order."""
+    nbytes = _lib.gdn_linear_attn_workspace_bytes(args[-1])
+    handle = _raw_stream(device.index) if stream is None else stream.cuda_stream
+    ws = None
+    if nbytes:
+        try:
+            ws = _raw_alloc(nbytes, handle)
+        except _T.OutOfMemoryError:
+            nbytes = 0  # the library asks for its own, and runs one pass where there is none
+    try:
+        code = _lib.gdn_linear_attn_prefill(*args, ws, nbytes, handle)
+    finally:
+        if ws is not None:
+            _raw_free(ws)
+    if code:
+        _check(code)
 
 
 def linear_attn_segments(B, Hk, Hv, S, Dk=128, Dv=128, dtype=GDN_BF16, sm_count=None, *, single_pass=False,

@@ -530,12 +530,12 @@ cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSpli
 namespace {
 
 // ------------------------------------------------------------------ host side
-constexpr uint32_t kKnownFlags = GDN_FORCE_FFMA | GDN_SINGLE_PASS | GDN_HEAD_DECAY;
+constexpr uint32_t kKnownFlags = GDN_FORCE_FFMA | GDN_SINGLE_PASS | GDN_HEAD_DECAY;  // (and GDN_ZERO_PADDING of a prompt)
 
 gdn_status check_dims(const gdn_dims* d, bool step) {
     if (!d) return GDN_ERR_NULL;
     if (d->dtype != GDN_F32 && d->dtype != GDN_BF16) return GDN_ERR_UNSUPPORTED;
-    if (d->flags & ~kKnownFlags) return GDN_ERR_UNSUPPORTED;
+    if (d->flags & ~(kKnownFlags | (step ? 0u : (uint32_t)GDN_ZERO_PADDING))) return GDN_ERR_UNSUPPORTED;
     if (d->B < 0 || d->Hk < 1 || d->Hv < 1 || d->S < 0 || d->Dk < 1 || d->Dv < 1) return GDN_ERR_DIMS;
     if (d->Dk > kMaxD || d->Dv > kMaxD || d->Hv % d->Hk != 0 || (step && d->S != 1)) return GDN_ERR_DIMS;
     // (tokens are counted in 32 bits, to the end of the last chunk of 128)
@@ -570,7 +570,7 @@ gdn_status check(const void* q, const void* k, const void* v, const float* g_log
         overlap_in_part(state_out, st, state_in, st))
         return GDN_ERR_UNSUPPORTED;
     *p = LinearAttn{q, k, v, g_log, lengths, state_in, state_out, out, scale, (int)d->B, (int)d->Hk, (int)d->Hv, (int)d->S,
-                    (int)d->Dk, (int)d->Dv, d->dtype == GDN_BF16, (d->flags & GDN_HEAD_DECAY) != 0};
+                    (int)d->Dk, (int)d->Dv, d->dtype == GDN_BF16, (d->flags & GDN_HEAD_DECAY) != 0, lengths && (d->flags & GDN_ZERO_PADDING)};
     return GDN_OK;
 }
 
@@ -661,9 +661,12 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
     } else {
         const bool async =
             !p.bf16 && p.Dk % 4 == 0 && p.Dv % 4 == 0 && gdn::aligned16(q) && gdn::aligned16(k) && gdn::aligned16(v);
-        const cudaError_t e = p.bf16  ? gdn::launch_ffma<__nv_bfloat16, false>(p, split, dev, sms, st)
-                              : async ? gdn::launch_ffma<float, true>(p, split, dev, sms, st)
-                                      : gdn::launch_ffma<float, false>(p, split, dev, sms, st);
+        cudaError_t e = cudaSuccess;
+        if (p.zero_rest) e = cudaMemsetAsync(out, 0, (size_t)p.B * p.Hv * p.S * p.Dv * (p.bf16 ? 2 : 4), st);
+        if (e == cudaSuccess)
+            e = p.bf16  ? gdn::launch_ffma<__nv_bfloat16, false>(p, split, dev, sms, st)
+                : async ? gdn::launch_ffma<float, true>(p, split, dev, sms, st)
+                        : gdn::launch_ffma<float, false>(p, split, dev, sms, st);
         s = e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
     }
     if (s != GDN_OK) (void)cudaGetLastError();

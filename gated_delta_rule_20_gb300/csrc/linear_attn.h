@@ -24,6 +24,7 @@ struct LinearAttn {
     float scale;
     int B, Hk, Hv, S, Dk, Dv;
     bool bf16, head_decay;
+    bool zero_rest;  // rows of out behind a sequence's length are zeroed (only with lengths)
 };
 
 // Least log-decay that is told from the others: e^-100 = 3.7e-44 is (nearly) the least fp32 number, so that

@@ -622,8 +622,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = p.scale * exp2_approx(fmaxf(R, kMinRow));
             uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Dv * 2;
             // whole chunks and the tensor's end go out by TMA, from q's tile (its products are done); where a length
-            // ends inside a chunk, a thread writes its row itself
-            const bool tma = n == kC || sh.t[s] + n == p.S;
+            // ends inside a chunk, a thread writes its row itself (or zeros go out behind it)
+            const bool tma = n == kC || sh.t[s] + n == p.S || p.zero_rest;
             mbar_arrive(&sh.decfree[s]);
             ok = wait_warp(&sh.ofull, cn & 1);
             if (!ok) break;
@@ -633,8 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = pack2(mul2(pair(f, f), pair(x[2 * j], x[2 * j + 1])));
-                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
                 if (tma) {
+                    if (r >= n) lo = hi = make_uint4(0, 0, 0, 0);
                     uint8_t* half = tile + (col >> 6) * kHalf;
                     const int ch = (col & 63) >> 3;
                     *reinterpret_cast<uint4*>(half + ((ch ^ (r & 7)) << 4)) = lo;
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* qt = sm + kOffQ + s * kTile;
                     if (was[0].n) {
-                        const bool whole = was[0].n == kC || was[0].t + was[0].n == p.S;
+                        const bool whole = was[0].n == kC || was[0].t + was[0].n == p.S || p.zero_rest;
 #pragma unroll 1
                         for (int h = 0; h < 2 && ok; ++h) {
                             ok = wait_one(&sh.staged[h], cn & 1);
@@ -874,6 +875,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!more) break;
                 more = next_chunk(k, p, it);
                 if (more) fetch();
+            }
+        } else if (!kStatesOnly && p.zero_rest) {
+            // -------------------------------------------------------- zeros behind the lengths, from the next chunk on
+#pragma unroll 1
+            for (Walk k = first_item(it); k.seg < it.segs; next_item(k, it)) {
+                tokens_of(k, p, it);
+                const int end = p.S - k.t > it.len ? k.t + it.len : p.S;
+                const int from = k.end > k.t ? k.t + (k.end - k.t + kC - 1) / kC * kC : k.t;
+                const int row = p.Dv / 8;  // in pieces of 16 bytes
+                uint4* to = reinterpret_cast<uint4*>(p.out) + ((long long)k.bh * p.S + from) * row + lane;
+                uint4* const stop = to + (long long)(end - from) * row - lane;  // (not past `to` where the tokens go to the end)
+#pragma unroll 1
+                for (; to < stop; to += 32) __stcs(to, make_uint4(0, 0, 0, 0));
             }
         }
     }

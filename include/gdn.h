@@ -72,7 +72,9 @@ enum {
      * every sequence, whatever the SM count, so results do not depend on it. */
     GDN_SINGLE_PASS = 1u << 2,
     /* Linear attention only (gdn_linear_attn_*): g_log is [Hv], one decay a head for all tokens. */
-    GDN_HEAD_DECAY = 1u << 3
+    GDN_HEAD_DECAY = 1u << 3,
+    /* gdn_linear_attn_prefill only: rows of out behind a sequence's length are set to zero. */
+    GDN_ZERO_PADDING = 1u << 4
 };
 
 /*
@@ -495,11 +497,12 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  *               count as -100 (e^-100 is 3.7e-44): -infinity drops what came before the token
  *   lengths     [B] int32 or NULL: sequence b has lengths[b] tokens (below 0: 0, above S: S).  Rows of q, k, v
  *               and g_log behind them have no influence, whatever they hold, and rows of out are left as they were
+ *               (GDN_ZERO_PADDING: set to zero)
  *   state_in    [B, Hv, Dk, Dv] fp32, Dv contiguous, or NULL: zeros
  *   state_out   the same, receives the state behind the last token; may be state_in
  *   out         [B, Hv, S, Dv]  compute dtype
- *   dims        gdn_dims (S < 2^31 - 4096); flags: GDN_HEAD_DECAY, GDN_FORCE_FFMA, GDN_SINGLE_PASS.  S = 0 copies the
- *               state
+ *   dims        gdn_dims (S < 2^31 - 4096); flags: GDN_HEAD_DECAY, GDN_FORCE_FFMA, GDN_SINGLE_PASS, GDN_ZERO_PADDING.
+ *               S = 0 copies the state
  *   workspace   device memory of workspace_bytes >= gdn_linear_attn_workspace_bytes(dims) bytes, 16-byte
  *               aligned, not touched by anything else until the call's work on `stream` has finished; NULL: the call
  *               takes what it needs with cudaMallocAsync on `stream`, and runs one pass where that fails.  Too small:
@@ -537,7 +540,7 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims);
 
 /*
  * gdn_linear_attn_step -- one token of every sequence (dims->S == 1, else GDN_ERR_DIMS): the arguments of
- * gdn_linear_attn_prefill (no lengths), in fp32 throughout.  The state is read once and written once, in one launch.
+ * gdn_linear_attn_prefill (no lengths, no GDN_ZERO_PADDING), in fp32 throughout.  The state is read once and written once, in one launch.
  */
 gdn_status gdn_linear_attn_step(const void* q, const void* k, const void* v, const float* g_log, float scale,
                                 const float* state_in, float* state_out, void* out, const gdn_dims* dims,

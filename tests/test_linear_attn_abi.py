@@ -40,13 +40,14 @@ def test_linear_attn_argument_checks(L, call, S):
     assert call(L, None) == gdn.GDN_ERR_NULL
     assert call(L, d(B=0)) == gdn.GDN_OK and call(L, d(B=0), q=None, out=None, s_out=None) == gdn.GDN_OK
     assert call(L, d(dtype=7)) == gdn.GDN_ERR_UNSUPPORTED and call(L, d(dtype=gdn.GDN_F8E4M3)) == gdn.GDN_ERR_UNSUPPORTED
-    assert call(L, d(flags=1 << 4)) == gdn.GDN_ERR_UNSUPPORTED
+    assert call(L, d(flags=1 << 5)) == gdn.GDN_ERR_UNSUPPORTED
     assert call(L, d(flags=gdn.GDN_ZERO_INITIAL_STATE)) == gdn.GDN_ERR_UNSUPPORTED  # (a NULL state_in says that)
     for bad in (dict(B=-1), dict(Hk=0), dict(Hv=0), dict(Hk=3), dict(Dk=0), dict(Dv=0), dict(Dk=129), dict(Dv=129),
                 dict(S=-1), dict(S=1 << 31), dict(B=1, Hk=1, Hv=1, S=(1 << 31) - 4096), dict(B=1 << 31), dict(B=1 << 29, Hv=8), dict(Hv=1 << 62, B=4, Hk=1)):
         assert call(L, d(**bad)) == gdn.GDN_ERR_DIMS, bad
     if call is step:
         assert call(L, d(S=2)) == gdn.GDN_ERR_DIMS and call(L, d(S=0)) == gdn.GDN_ERR_DIMS
+        assert call(L, d(flags=gdn.GDN_ZERO_PADDING)) == gdn.GDN_ERR_UNSUPPORTED      # (there is no padding)
     for name in ("q", "k", "v", "g", "s_out", "out"):
         assert call(L, d(), **{name: None}) == gdn.GDN_ERR_NULL, name
     for name, at in (("q", Q), ("k", K), ("v", V), ("out", OUT)):

@@ -224,6 +224,35 @@ def test_operands_off_16_bytes():
     compare(y, (out, st), size, "bf16", False, "unaligned step")
 
 
+@pytest.mark.parametrize("dtype, B, Hv, S, Dv, split", [
+    ("bf16", 7, 2, 300, 128, False), ("bf16", 6, 3, 1000, 64, True), ("bf16", 80, 4, 300, 8, False), ("f32", 6, 2, 300, 64, True),
+    ("bf16", 5, 1, 77, 75, True)])
+def test_zero_padding(dtype, B, Hv, S, Dv, split):
+    """Rows of out behind the lengths set to zero, whatever the inputs and out held there; all others as without."""
+    lengths = ([S, 0, 130, 128, 257, S - 1, -3] * 12)[:B]
+    x = inputs(B, 1, Hv, S, 64, Dv, dtype, "head")
+    d = {n: t.cuda() for n, t in x.items()}
+    at = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+    for b, n in enumerate(lengths):
+        for name in ("q", "k", "v"):
+            d[name][b, :, max(n, 0):] = float("nan")
+    code = gdn.GDN_BF16 if dtype == "bf16" else gdn.GDN_F32
+    assert (gdn.linear_attn_segments(B, 1, Hv, S, 64, Dv, code) > 1) == split
+    outs = []
+    for flags in (0, gdn.GDN_ZERO_PADDING):
+        out, st = torch.full_like(d["v"], 7.0), torch.empty_like(d["state"])
+        dims = gdn.make_dims(B, 1, Hv, S, 64, Dv, code, flags | gdn.GDN_HEAD_DECAY)
+        assert gdn.lib().gdn_linear_attn_prefill(
+            *(d[n].data_ptr() for n in ("q", "k", "v", "g")), at.data_ptr(), 0.1, d["state"].data_ptr(), st.data_ptr(),
+            out.data_ptr(), dims, None, 0, torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        outs.append((out, st))
+    assert gdn.device_status(0) == 0 and torch.equal(outs[0][1], outs[1][1])
+    for b, n in enumerate(max(n, 0) for n in lengths):
+        assert torch.equal(outs[0][0][b, :, :n], outs[1][0][b, :, :n])
+        assert bool((outs[0][0][b, :, n:] == 7.0).all()) and bool((outs[1][0][b, :, n:] == 0).all())
+
+
 def test_refusals_of_the_binding():
     x = {n: t.cuda() for n, t in inputs(2, 1, 2, 8, 64, 64, "bf16").items()}
     call = lambda **kw: gdn.linear_attn_prefill(*(kw.pop(n, x[n]) for n in ("q", "k", "v", "g")), 1.0,  # noqa: E731
