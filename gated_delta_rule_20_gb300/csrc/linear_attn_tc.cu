@@ -622,8 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f = p.scale * exp2_approx(fmaxf(R, kMinRow));
             uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Dv * 2;
             // whole chunks and the tensor's end go out by TMA, from q's tile (its products are done); where a length
-            // ends inside a chunk, a thread writes its row itself (or zeros go out behind it)
-            const bool tma = n == kC || sh.t[s] + n == p.S || p.zero_rest;
+            // ends inside a chunk, a thread writes its row itself (rows behind the length: zeros, or nothing)
+            const bool tma = n == kC || sh.t[s] + n == p.S;
+            const int rows = p.zero_rest ? p.S - sh.t[s] : n;  // that are written so
             mbar_arrive(&sh.decfree[s]);
             ok = wait_warp(&sh.ofull, cn & 1);
             if (!ok) break;
@@ -633,16 +634,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t o[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = pack2(mul2(pair(f, f), pair(x[2 * j], x[2 * j + 1])));
-                uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
                 if (tma) {
-                    if (r >= n) lo = hi = make_uint4(0, 0, 0, 0);
                     uint8_t* half = tile + (col >> 6) * kHalf;
                     const int ch = (col & 63) >> 3;
                     *reinterpret_cast<uint4*>(half + ((ch ^ (r & 7)) << 4)) = lo;
                     *reinterpret_cast<uint4*>(half + (((ch + 1) ^ (r & 7)) << 4)) = hi;
-                } else if (r < n) {
-                    if (col < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col) = lo;
-                    if (col + 8 < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col + 16) = hi;
+                } else if (r < rows) {
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    if (col < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col) = r < n ? lo : zero;
+                    if (col + 8 < p.Dv) *reinterpret_cast<uint4*>(row + 2 * col + 16) = r < n ? hi : zero;
                 }
             };
             // (columns past Dv come from whatever the tensor memory holds, and are not written)
@@ -693,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     uint8_t* qt = sm + kOffQ + s * kTile;
                     if (was[0].n) {
-                        const bool whole = was[0].n == kC || was[0].t + was[0].n == p.S || p.zero_rest;
+                        const bool whole = was[0].n == kC || was[0].t + was[0].n == p.S;
 #pragma unroll 1
                         for (int h = 0; h < 2 && ok; ++h) {
                             ok = wait_one(&sh.staged[h], cn & 1);
