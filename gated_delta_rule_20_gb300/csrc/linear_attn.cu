@@ -609,6 +609,20 @@ int segments(const gdn_dims* d, int sms, int* len) {
     return P;
 }
 
+// CTAs that run parts of the heads left over by whole rounds of all SMs (see Items in linear_attn_tc.cu), of *len tokens; 0: none.
+// A head is cut into as many parts as there are rounds in front of the last and CTAs for, if that saves 4 chunks of 128 tokens:
+// the hand-over costs some 8 us.
+int handed_parts(const gdn_dims* d, int sms, int* len) {
+    const long long heads = (long long)d->B * d->Hv, units = (d->S + 127) / 128, whole = heads / sms, rest = heads % sms;
+    if ((d->flags & (GDN_SINGLE_PASS | GDN_FORCE_FFMA)) || d->dtype != GDN_BF16 || d->Dk % 8 || d->Dv % 8) return 0;
+    if (whole < 1 || rest < 1 || heads > INT32_MAX - sms) return 0;
+    long long n = sms / rest < whole + 1 ? sms / rest : whole + 1;
+    while (n > 1 && (n - 1) * ((units + n - 1) / n) >= units) --n;  // (the last part would be empty)
+    if (n < 2 || units - (units + n - 1) / n < 4) return 0;
+    *len = (int)((units + n - 1) / n * 128);
+    return (int)(n * rest);
+}
+
 }  // namespace
 }  // namespace gdn
 
@@ -633,13 +647,13 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
     s = gdn::current_device_sms(&dev, &sms);
     if (s != GDN_OK) return s;
     const bool tc = gdn::on_tensor_cores(p, dims);
-    gdn::LinearAttnSplit split{1, p.S, nullptr, nullptr};
+    gdn::LinearAttnSplit split{1, p.S, nullptr, nullptr, 0, nullptr};
     int len = 0;
-    const int P = gdn::segments(dims, sms, &len);
+    const int P = gdn::segments(dims, sms, &len), handed = P == 1 && tc ? gdn::handed_parts(dims, sms, &len) : 0;
     bool own = false;
     void* ws = nullptr;
-    if (P > 1) {
-        const size_t need = gdn::linear_attn_split_bytes(p, P);
+    if (P > 1 || handed) {
+        const size_t need = P > 1 ? gdn::linear_attn_split_bytes(p, P) : gdn::linear_attn_flag_bytes(handed);
         if (workspace) {
             if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
             ws = workspace;
@@ -649,9 +663,13 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
             (void)cudaGetLastError();  // one pass instead
             ws = nullptr;
         }
-        if (ws) {
+        if (ws && handed) {
+            split.len = len;
+            split.handed = handed;
+            split.flags = static_cast<uint32_t*>(ws);
+        } else if (ws) {
             float* f = static_cast<float*>(ws);
-            split = {P, len, f, f + (size_t)P * p.B * p.Hv * p.Dk * p.Dv};
+            split = {P, len, f, f + (size_t)P * p.B * p.Hv * p.Dk * p.Dv, 0, nullptr};
         }
     }
     if (tc) {
@@ -709,7 +727,9 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims) {
     p.Hv = (int)dims->Hv;
     p.Dk = (int)dims->Dk;
     p.Dv = (int)dims->Dv;
-    return gdn::linear_attn_split_bytes(p, gdn_linear_attn_segments(dims, sms));
+    const int P = gdn_linear_attn_segments(dims, sms);
+    int len = 0;
+    return P > 1 ? gdn::linear_attn_split_bytes(p, P) : gdn::linear_attn_flag_bytes(gdn::handed_parts(dims, sms, &len));
 }
 
 }  // extern "C"

@@ -42,6 +42,10 @@ struct LinearAttnSplit {
     int P, len;
     float* parts;
     float* decays;
+    // P = 1 on the tensor cores, where the heads are some rounds of all SMs and a few more: CTAs that run parts of `len` tokens of
+    // these, handing the state on (0: none), and their flags
+    int handed;
+    uint32_t* flags;
     __device__ const float* start(int seg, long long bh, long long heads, long long n) const {
         return parts + ((seg ? seg - 1 : P - 1) * heads + bh) * n;
     }
@@ -49,6 +53,8 @@ struct LinearAttnSplit {
 inline size_t linear_attn_split_bytes(const LinearAttn& p, int P) {
     return P <= 1 ? 0 : (size_t)P * p.B * p.Hv * ((size_t)p.Dk * p.Dv + 1) * sizeof(float);
 }
+
+inline size_t linear_attn_flag_bytes(int handed) { return handed ? ((size_t)handed * 8 + 1) * sizeof(uint32_t) : 0; }
 
 // bf16 with head dims of whole 16-byte rows, on aligned pointers.
 bool linear_attn_tc_supported(const LinearAttn& p);

@@ -32,7 +32,7 @@
 // active 56 % of the cycles, schedulers issuing 56 %).  One CTA an SM: two chunks of q, k and v and the state fill its shared
 // memory; scores, O, X and the parts its tensor memory.
 // Measured (bf16, 128 x 128 state): 4 x 32 heads (16 of keys) x 4096 tokens 84 to 86 us, 5.0 TB/s, 73 % of the copy's rate;
-// 16 x 32 heads (8 of keys) x 2048 168 us; 1 x 32 heads x 32768 in 9 segments 262 us (one pass: 562).
+// 16 x 32 heads (8 of keys) x 2048 160 us; 1 x 32 heads x 32768 in 9 segments 262 us (one pass: 562).
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -74,6 +74,7 @@ struct Small {
     uint64_t sfull, sfree, xfull[2], xfree[2], qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
     int gave_up;
+    int cta, items;  // with kHanded: this CTA's number, and how many items it has at most
 };
 constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -179,47 +180,91 @@ Divisor divisor(int d) {
     return Divisor{(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s};
 }
 // What the kernel's walk over its items needs: (segment, head) pairs, heads fastest, every gridDim-th of them a CTA's.
+// kHanded (one segment): every CTA has `whole` heads, and the heads that are left over are each cut into parts of `len` tokens,
+// which `handed` CTAs run: part j of the r-th is CTA j rest + r's, after j of its whole heads, so that part j - 1 has left
+// its state in state_out long before.  (152 SMs, us, whole heads alone and with parts: 16 x 32 heads x 2048 172, 162; 5 x 32
+// x 4096 163, 133; 5 x 32 x 1024 50, 48; 40 x 16 x 800 104, 99.  Whole heads stay where they were, beside those that share their key
+// head, whose q and k then come from L2.)
 struct Items {
     int heads, segs, len;  // B Hv; segments that this launch runs; tokens of one (S where there is one)
     Divisor hv, group;     // by Hv: the batch; by Hv / Hk: the key head, counted over the batch
+    int whole, rest, handed;
+    uint32_t* flags;       // kHanded: how many CTAs have begun; 8 a CTA: whether its part's state has been written
 };
 struct Walk {  // a CTA's chunks one after another, over all of its items that have any
-    int bh, seg, t, end;  // head (over the batch), segment, the chunk's first token and the item's end
+    int bh, seg, t, end;  // head (over the batch), segment (kHanded: items before), the chunk's first token, the item's end
+    int part;             // of a head that is cut into parts: which (else -1)
 };
-__device__ __forceinline__ void next_item(Walk& k, const Items& it) {
+__device__ __forceinline__ void place(Walk& k, const Items& it, const Small& sh) {  // (kHanded)
+    const int j = sh.cta < it.handed ? sh.cta / it.rest : it.whole + 1, grid = gridDim.x;
+    k.part = k.seg == j ? j : -1;
+    k.bh = k.seg == j ? it.whole * grid + sh.cta - j * it.rest : sh.cta + (k.seg - (k.seg > j ? 1 : 0)) * grid;
+}
+template <bool kHanded>
+__device__ __forceinline__ void next_item(Walk& k, const Items& it, const Small& sh) {
+    if (kHanded) {
+        ++k.seg;
+        place(k, it, sh);
+        return;
+    }
     k.bh += gridDim.x;
     while (k.bh >= it.heads) {
         k.bh -= it.heads;
         ++k.seg;
     }
 }
-__device__ __forceinline__ void tokens_of(Walk& k, const LinearAttn& p, const Items& it) {
+template <bool kHanded>
+__device__ __forceinline__ int tokens_of(Walk& k, const LinearAttn& p, const Items& it) {  // the item's end without lengths
     int len = p.S;
     if (p.lengths) len = max(0, min(len, p.lengths[it.hv.of(k.bh)]));
-    k.t = k.seg * it.len;
-    k.end = len - k.t > it.len ? k.t + it.len : len;
+    const int most = kHanded && k.part < 0 ? p.S : it.len;
+    k.t = kHanded ? max(k.part, 0) * it.len : k.seg * it.len;
+    k.end = len - k.t > most ? k.t + most : len;
+    return p.S - k.t > most ? k.t + most : p.S;
 }
-__device__ __forceinline__ bool settle(Walk& k, const LinearAttn& p, const Items& it) {
+template <bool kHanded>
+__device__ __forceinline__ int items_of(const Items& it, const Small& sh) {
+    return kHanded ? sh.items : it.segs;
+}
+template <bool kHanded>
+__device__ __forceinline__ bool settle(Walk& k, const LinearAttn& p, const Items& it, const Small& sh) {
 #pragma unroll 1
-    for (; k.seg < it.segs; next_item(k, it)) {
-        tokens_of(k, p, it);
+    for (; k.seg < items_of<kHanded>(it, sh); next_item<kHanded>(k, it, sh)) {
+        (void)tokens_of<kHanded>(k, p, it);
         if (k.t < k.end) return true;
     }
     return false;
 }
-__device__ __forceinline__ Walk first_item(const Items& it) {
-    Walk k{(int)blockIdx.x, 0, 0, 0};
+template <bool kHanded>
+__device__ __forceinline__ Walk first_item(const Items& it, const Small& sh) {
+    Walk k{(int)blockIdx.x, 0, 0, 0, -1};
+    if (kHanded) {
+        place(k, it, sh);
+        return k;
+    }
     while (k.bh >= it.heads) {
         k.bh -= it.heads;
         ++k.seg;
     }
     return k;
 }
-__device__ __forceinline__ bool next_chunk(Walk& k, const LinearAttn& p, const Items& it) {
+template <bool kHanded>
+__device__ __forceinline__ bool next_chunk(Walk& k, const LinearAttn& p, const Items& it, const Small& sh) {
     k.t += kC;
     if (k.t < k.end) return true;
-    next_item(k, it);
-    return settle(k, p, it);
+    next_item<kHanded>(k, it, sh);
+    return settle<kHanded>(k, p, it, sh);
+}
+// The flag of a part that another CTA runs (bounded: a second or two).
+__device__ __forceinline__ bool wait_flag(const uint32_t* flag) {
+    uint32_t v = 0;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kMostTests; ++i) {
+        asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
+        if (v) return true;
+        asm volatile("nanosleep.u32 1000;");
+    }
+    return false;
 }
 
 // Descriptors in two words: an offset within shared memory is added to the low one (no carry leaves its address field).
@@ -296,8 +341,9 @@ __device__ __forceinline__ void column_rows(int pitch, int rows, F f) {
     }
 }
 
-// kStatesOnly: the first pass of a split (end states and decays of segments 0 .. P - 2; only KV is formed).
-template <bool kStatesOnly>
+// kStatesOnly: the first pass of a split (end states and decays of segments 0 .. P - 2; only KV is formed).  kHanded: heads that
+// are left over go in parts (see Items).
+template <bool kStatesOnly, bool kHanded>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
@@ -354,6 +400,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sh.tmem;
     const uint32_t tq4 = tmem + ((uint32_t)(quad * 32) << 16);  // this warp's lanes
     griddep_wait();
+    if (kHanded) {
+        // numbers in the order of beginning: a CTA that is waited for runs already
+        if (tid == 0) {
+            sh.cta = (int)atomicAdd(it.flags, 1u);
+            sh.items = it.whole + (sh.cta < it.handed ? 1 : 0);
+        }
+        __syncthreads();
+    }
 
     int cn = 0;      // chunks so far, over all items
     bool ok = true;  // no wait has run out
@@ -443,16 +497,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first = 64 * half * p.Dv + dv;
         uint8_t* const sb = sm + kOffS + half * kHalf + dv * 128;
         float S[64];
-        for (Walk k = first_item(it); k.seg < it.segs && ok; next_item(k, it)) {
-            tokens_of(k, p, it);
+        for (Walk k = first_item<kHanded>(it, sh); k.seg < items_of<kHanded>(it, sh) && ok; next_item<kHanded>(k, it, sh)) {
+            (void)tokens_of<kHanded>(k, p, it);
             int pitch = p.Dv;
             asm volatile("" : "+r"(pitch));  // (64 rows' offsets are not kept in registers over the chunks)
             const float* src = p.state_in ? p.state_in + k.bh * ns : nullptr;
             if (!kStatesOnly && split.P > 1) src = split.start(k.seg, k.bh, heads, ns);
             if (kStatesOnly && k.seg) src = nullptr;
+            if (kHanded && k.part > 0) {  // (each warp left what its namesake reads)
+                ok = __all_sync(0xffffffffu, wait_flag(it.flags + 1 + 8 * (sh.cta - it.rest) + warp - 4));
+                if (!ok) break;
+                src = p.state_out + k.bh * ns;
+            }
             if (src) {
                 src += first;
-                column_rows(pitch, rows, [&](int i, int at, bool in) { S[i] = in ? src[at] : 0.f; });
+                column_rows(pitch, rows, [&](int i, int at, bool in) { S[i] = !in ? 0.f : kHanded ? __ldcg(src + at) : src[at]; });
             } else {
 #pragma unroll
                 for (int i = 0; i < 64; ++i) S[i] = 0.f;
@@ -512,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (kStatesOnly) {
                 dst = split.parts + (k.seg * heads + k.bh) * ns;
                 if (tid == 128) split.decays[k.seg * heads + k.bh] = decay;
-            } else if (k.seg == split.P - 1) {
+            } else if (kHanded || k.seg == split.P - 1) {
                 dst = p.state_out + k.bh * ns;
             }
             if (dst) {
@@ -520,6 +579,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 column_rows(pitch, rows, [&](int i, int at, bool in) {
                     if (in) dst[at] = S[i];
                 });
+                if (kHanded && k.part >= 0) {
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("fence.acq_rel.gpu;\n\tst.release.gpu.global.u32 [%0], %1;" ::"l"(
+                                         it.flags + 1 + 8 * sh.cta + warp - 4),
+                                     "r"(1u)
+                                     : "memory");
+                }
             }
         }
     } else if (parts_role) {
@@ -675,10 +742,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 struct Tile {
                     int t, bh, n;
                 } was[2] = {{0, 0, 0}, {0, 0, 0}};  // chunks cn - 2 and cn - 1 (n = 0: none)
-                Walk k = first_item(it);
-                bool more = settle(k, p, it);
+                Walk k = first_item<kHanded>(it, sh);
+                bool more = settle<kHanded>(k, p, it, sh);
                 Walk far = k;  // a chunk two ahead, whose K and q are brought into L2 (V's load has the time)
-                bool ahead = more && next_chunk(far, p, it);
+                bool ahead = more && next_chunk<kHanded>(far, p, it, sh);
                 // The engine works in order: what is needed first goes first.  V, out of which parts are made; the outputs of
                 // chunk cn - 2, which leave the q tile that chunk cn takes; K and q; then the prefetch
                 for (; more || was[0].n || was[1].n; ++cn) {
@@ -720,8 +787,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (p.Dk > 64) tma_load_3d(qt + kHalf, &tq, &sh.kqfull[s], 64, k.t, bhk);
                             was[1] = Tile{k.t, k.bh, min(kC, k.end - k.t)};
                         }
-                        more = next_chunk(k, p, it);
-                        if (ahead) ahead = next_chunk(far, p, it);
+                        more = next_chunk<kHanded>(k, p, it, sh);
+                        if (ahead) ahead = next_chunk<kHanded>(far, p, it, sh);
                         if (ahead) {
                             const int fhk = it.group.of(far.bh);
 #pragma unroll 1
@@ -824,8 +891,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         } else if (warp == 26) {
             // -------------------------------------------------------- decays, and the walk that most roles follow
-            Walk k = first_item(it);
-            bool more = settle(k, p, it);
+            Walk k = first_item<kHanded>(it, sh);
+            bool more = settle<kHanded>(k, p, it, sh);
             float g[4] = {};  // the log-decays of the walk's chunk, on their way while the chunk before is published
             const auto fetch = [&] {
                 const float* from =
@@ -874,15 +941,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mbar_arrive(&sh.decfull[s]);
                 if (!more) break;
-                more = next_chunk(k, p, it);
+                more = next_chunk<kHanded>(k, p, it, sh);
                 if (more) fetch();
             }
         } else if (!kStatesOnly && p.zero_rest) {
             // -------------------------------------------------------- zeros behind the lengths, from the next chunk on
 #pragma unroll 1
-            for (Walk k = first_item(it); k.seg < it.segs; next_item(k, it)) {
-                tokens_of(k, p, it);
-                const int end = p.S - k.t > it.len ? k.t + it.len : p.S;
+            for (Walk k = first_item<kHanded>(it, sh); k.seg < items_of<kHanded>(it, sh); next_item<kHanded>(k, it, sh)) {
+                const int end = tokens_of<kHanded>(k, p, it);
                 const int from = k.end > k.t ? k.t + (k.end - k.t + kC - 1) / kC * kC : k.t;
                 const int row = p.Dv / 8;  // in pieces of 16 bytes
                 uint4* to = reinterpret_cast<uint4*>(p.out) + ((long long)k.bh * p.S + from) * row + lane;
@@ -933,10 +999,10 @@ bool encode(CUtensorMap* map, const void* ptr, long long heads, int S, int D) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kStatesOnly>
+template <bool kStatesOnly, bool kHanded>
 gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
                   int32_t* status, cudaStream_t stream) {
-    auto* kernel = linear_attn_tc_kernel<kStatesOnly>;
+    auto* kernel = linear_attn_tc_kernel<kStatesOnly, kHanded>;
     static std::atomic<int> launched{0};  // registers a thread of the block at launch
     int regs = launched.load(std::memory_order_relaxed);
     if (regs == 0) {
@@ -950,7 +1016,15 @@ gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAt
     if (allow_smem(kernel, (int)kSmem, allowed, dev) != cudaSuccess) return GDN_ERR_CUDA;
     const long long items = (long long)p.B * p.Hv * (kStatesOnly ? s.P - 1 : s.P);
     if (items > INT32_MAX - sms) return GDN_ERR_DIMS;  // (items are counted in 32 bits)
-    const Items it{p.B * p.Hv, kStatesOnly ? s.P - 1 : s.P, s.P > 1 ? s.len : p.S, divisor(p.Hv), divisor(p.Hv / p.Hk)};
+    Items it{p.B * p.Hv, kStatesOnly ? s.P - 1 : s.P, s.P > 1 || kHanded ? s.len : p.S, divisor(p.Hv), divisor(p.Hv / p.Hk),
+             0, 0, 0, nullptr};
+    if (kHanded) {
+        it.whole = it.heads / sms;
+        it.rest = it.heads % sms;
+        it.handed = s.handed;
+        it.flags = s.flags;
+        if (cudaMemsetAsync(s.flags, 0, linear_attn_flag_bytes(s.handed), stream) != cudaSuccess) return GDN_ERR_CUDA;
+    }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(items < sms ? items : sms));
     cfg.blockDim = dim3(kThreads);
@@ -979,11 +1053,12 @@ gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, 
         !encode(&m[3], p.out, hv, p.S, p.Dv))
         return GDN_ERR_CUDA;
     if (s.P > 1) {
-        const gdn_status e = launch<true>(m, p, s, dev, sms, status, stream);
+        const gdn_status e = launch<true, false>(m, p, s, dev, sms, status, stream);
         if (e != GDN_OK) return e;
         if (launch_linear_attn_combine(p, s, stream) != cudaSuccess) return GDN_ERR_CUDA;
     }
-    return launch<false>(m, p, s, dev, sms, status, stream);
+    if (s.handed) return launch<false, true>(m, p, s, dev, sms, status, stream);
+    return launch<false, false>(m, p, s, dev, sms, status, stream);
 }
 
 }  // namespace gdn

@@ -520,7 +520,8 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * Few sequences of many tokens are cut into segments that run at once (gdn_linear_attn_segments; GDN_SINGLE_PASS:
  * never): a first launch runs all but the last from zero and keeps their states and decays, a second adds them up to the
  * segments' start states (nothing to do for two segments), and the last runs every segment.  Results of a split agree with one
- * pass's to within rounding.  The same call on the same device gives the same bits; a batch's sequences do not
+ * pass's to within rounding.  Many heads that are no whole number of rounds of the SMs: those left over run in parts on several
+ * SMs, one handing the state on to the next through state_out (the same bits as one pass's; GDN_SINGLE_PASS: never).  The same call on the same device gives the same bits; a batch's sequences do not
  * influence one another's, unless another batch size changes the split.
  * A wait inside the tensor-core kernel that runs out (a second or two) ends it with GDN_ERR_TIMEOUT in the device's status
  * word (gdn_device_status) and undefined outputs.
@@ -534,8 +535,8 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
  * invalid dims or sm_count < 1.  Host only. */
 int32_t gdn_linear_attn_segments(const gdn_dims* dims, int32_t sm_count);
 
-/* Device scratch of gdn_linear_attn_prefill on the current device: a state a segment and head; 0 for one pass,
- * for invalid dims and without a device.  Host only. */
+/* Device scratch of gdn_linear_attn_prefill on the current device: a state a segment and head; a few KB of flags where
+ * heads are handed on; 0 for one pass without either, for invalid dims and without a device.  Host only. */
 size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims);
 
 /*

@@ -189,3 +189,55 @@ def test_infinities_and_nan_in_the_data(dtype):
     keep = [c for c in range(64) if c != 5]
     assert torch.equal(y[0][1, 1][:, keep], want[0][1, 1][:, keep]) and torch.equal(y[1][1, 1][:, keep], want[1][1, 1][:, keep])
     assert bool(torch.isnan(y[1][1, 1, :, 5]).all())
+
+
+@pytest.mark.parametrize("rounds, rest, S, Dk, Dv, start", [
+    (1, 8, 1500, 128, 128, True), (1, 8, 1024, 64, 128, False), (2, 3, 2000, 96, 64, True), (3, 56, 2048, 128, 128, True),
+    (1, 76, 1100, 8, 128, True), (4, 1, 3001, 128, 8, True)])
+def test_heads_handed_on(rounds, rest, S, Dk, Dv, start):
+    """A few heads more than whole rounds of all SMs: they are run in parts by CTAs that hand their states on.  The bits are one
+    pass's, with lengths (some end in an early part) and without, in place, from a graph, on two streams at once."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    Hv = rounds * sms + rest
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v = n(1, 1, S, Dk).bfloat16(), n(1, 1, S, Dk).bfloat16(), n(1, Hv, S, Dv).bfloat16()
+    g = -0.2 * torch.rand(1, Hv, S, generator=gen, device="cuda")
+    state = n(1, Hv, Dk, Dv) if start else None
+    assert gdn.linear_attn_segments(1, 1, Hv, S, Dk, Dv) == 1
+    assert gdn.linear_attn_workspace_bytes(1, 1, Hv, S, Dk, Dv) > 0                     # (they are handed on)
+    assert gdn.linear_attn_workspace_bytes(1, 1, Hv, S, Dk, Dv, single_pass=True) == 0
+    new = lambda: torch.full((1, Hv, Dk, Dv), float("nan"), device="cuda")  # noqa: E731
+    call = lambda **kw: gdn.linear_attn_prefill(q, k, v, g, 0.1, state, state_out=new(), **kw)  # noqa: E731
+    want = call(single_pass=True)
+    for _ in range(3):
+        y = call()
+        assert torch.equal(y[0], want[0]) and torch.equal(y[1], want[1])
+    last = slice(Hv - 1, Hv)
+    o, st, size = ref.recurrence(q.cpu(), k.cpu(), v[:, last].cpu(), g[:, last].cpu(), 0.1, state[:, last].cpu() if start else None)
+    compare((want[0][:, last], want[1][:, last]), (o, st), size, "bf16", True, "handed on")
+    for length in (0, 1, S // 2 - 1, S - 1, 130):
+        at = torch.tensor([length], dtype=torch.int32, device="cuda")
+        a, b = call(lengths=at), call(lengths=at, single_pass=True)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    if start:
+        s = state.clone()
+        y = gdn.linear_attn_prefill(q, k, v, g, 0.1, s)
+        assert y[1] is s and torch.equal(s, want[1]) and torch.equal(y[0], want[0])
+    # two streams at once, each with its own scratch
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    ys = [call(stream=st) for _ in range(3) for st in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y[0], want[0]) and torch.equal(y[1], want[1]) for y in ys)
+    out, st = torch.empty_like(v), new()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.linear_attn_prefill(q, k, v, g, 0.1, state, out, state_out=st)
+    for _ in range(2):
+        out.zero_()
+        st.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(st, want[1])
+    assert gdn.device_status(0) == 0
