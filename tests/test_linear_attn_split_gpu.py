@@ -241,3 +241,36 @@ def test_heads_handed_on(rounds, rest, S, Dk, Dv, start):
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(st, want[1])
     assert gdn.device_status(0) == 0
+
+
+@pytest.mark.parametrize("Hv, S, dtype", [(2, 1000, "bf16"), (160, 1100, "bf16"), (2, 300, "f32")])
+def test_own_scratch_in_a_graph(Hv, S, dtype):
+    """The C entry point without a workspace, captured: segments, heads handed on, and the FMA units' segments, with zeroed padding;
+    two graphs of the same call keep their own scratch."""
+    code = gdn.GDN_BF16 if dtype == "bf16" else gdn.GDN_F32
+    assert gdn.linear_attn_workspace_bytes(1, 1, Hv, S, 64, 64, code) > 0
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(TYPES[dtype])  # noqa: E731
+    q, k, v, g = n(1, 1, S, 64), n(1, 1, S, 64), n(1, Hv, S, 64), torch.full((Hv,), -0.01, device="cuda")
+    at = torch.tensor([S - 70], dtype=torch.int32, device="cuda")
+    want = gdn.linear_attn_prefill(q, k, v, g, 0.1, lengths=at)
+    dims = gdn.make_dims(1, 1, Hv, S, 64, 64, code, gdn.GDN_HEAD_DECAY | gdn.GDN_ZERO_PADDING)
+    graphs = []
+    for _ in range(2):
+        out, st = torch.empty_like(v), torch.empty_like(want[1])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            assert gdn.lib().gdn_linear_attn_prefill(
+                q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), at.data_ptr(), 0.1, None, st.data_ptr(), out.data_ptr(),
+                dims, None, 0, torch.cuda.current_stream().cuda_stream) == gdn.GDN_OK
+        graphs.append((graph, out, st))
+    for _ in range(2):
+        for graph, out, st in graphs:
+            out.fill_(float("nan"))
+            st.fill_(float("nan"))
+        for graph, out, st in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for graph, out, st in graphs:
+            assert torch.equal(out, want[0]) and torch.equal(st, want[1])
+    assert gdn.device_status(0) == 0
