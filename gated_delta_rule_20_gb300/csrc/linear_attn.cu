@@ -443,7 +443,7 @@ cudaError_t launch_ffma_kernel(const LinearAttn& p, const LinearAttnSplit& s, in
     using Buf = FfmaBuffers<MB, kStatesOnly>;
     static std::atomic<bool> allowed[kMaxDevices];
     auto* kernel = linear_attn_ffma_kernel<T, MB, kStatesOnly, kAsync>;
-    if (Buf::bytes(kMaxD) > 48 * 1024) {
+    if (Buf::bytes(kMaxD) + 1024 > 48 * 1024) {  // (with s_a)
         const cudaError_t e = allow_smem(kernel, (int)Buf::bytes(kMaxD), allowed, dev);
         if (e != cudaSuccess) return e;
     }

@@ -274,3 +274,13 @@ def test_own_scratch_in_a_graph(Hv, S, dtype):
         for graph, out, st in graphs:
             assert torch.equal(out, want[0]) and torch.equal(st, want[1])
     assert gdn.device_status(0) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("Dk", [30, 64, 65, 96, 97, 128])
+def test_widest_ctas_of_the_fma_units(Dk, dtype):
+    """Heads enough for CTAs of 128 columns, whose tokens' shared memory is 48 KB with 65 to 96 rows, at every number of rows."""
+    x = inputs(40, 4, 8, 19, Dk, 127, dtype)
+    out, st, size = ref.recurrence(x["q"], x["k"], x["v"], x["g"], 0.1, x["state"])
+    y = call(x)
+    compare(y, (out, st), size, dtype, False, "wide")
