@@ -529,6 +529,71 @@ cudaError_t launch_linear_attn_combine(const LinearAttn& p, const LinearAttnSpli
 
 namespace {
 
+// ------------------------------------------------------------------ rows for the tensor-core kernel
+// q and k, or v, with their channels padded with zeros to multiples of 8 (rows that TMA can read).  A thread 8 channels of a row;
+// rows behind a length are left out.  Bound by bytes.
+struct PadRows {
+    const __nv_bfloat16* src[3];  // q, k, v
+    __nv_bfloat16* dst[3];        // (null: not padded)
+    int heads[3], D[3], P[3];
+    Divisor pieces[3], tokens[3], batch[3];  // of a row; by S; by heads S
+    const int32_t* lengths;
+    int B, S;
+};
+__global__ void __launch_bounds__(256) linear_attn_pad_kernel(const __grid_constant__ PadRows a) {
+    ptx::griddep_wait();
+    const int w = blockIdx.y;
+    if (a.dst[w]) {
+        const int D = a.D[w], P = a.P[w], all = a.B * a.heads[w] * a.S * (P / 8);
+        for (long long n0 = (long long)blockIdx.x * 256 + threadIdx.x; n0 < all; n0 += (long long)gridDim.x * 256) {
+            const int n = (int)n0, row = a.pieces[w].of(n), c = 8 * (n - row * (P / 8));
+            if (a.lengths && row - a.tokens[w].of(row) * a.S >= a.lengths[a.batch[w].of(row)]) continue;
+            const unsigned short* from = reinterpret_cast<const unsigned short*>(a.src[w]) + (long long)row * D + c;
+            uint32_t x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = c + i < D ? from[i] : 0;
+            *reinterpret_cast<uint4*>(a.dst[w] + (long long)row * P + c) =
+                make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+        }
+    }
+    ptx::griddep_launch_dependents();
+}
+
+// Outputs out of padded rows: a thread 8 elements of a head's [S, Dv] that are 16 aligned bytes; rows behind a length are left as
+// they are, or zeroed.  `blocks` CTAs a head.
+__global__ void __launch_bounds__(256) linear_attn_unpad_kernel(LinearAttn p, const unsigned short* padded, Divisor row_of, int blocks) {
+    ptx::griddep_wait();
+    const int bh = blockIdx.x / blocks, all = p.S * p.Dv;
+    unsigned short* out = static_cast<unsigned short*>(p.out) + (long long)bh * all;
+    const int before = (int)((reinterpret_cast<uintptr_t>(out) & 15) / 2);  // elements from 16 aligned bytes to the head's first
+    int len = p.S;
+    if (p.lengths) len = max(0, min(p.S, p.lengths[bh / p.Hv]));
+    const int written = p.zero_rest ? all : len * p.Dv, given = len * p.Dv;
+    const unsigned short* from = padded + (long long)bh * p.S * p.Pv;
+    for (int e0 = ((blockIdx.x - bh * blocks) * 256 + threadIdx.x) * 8 - before; e0 < written; e0 += blocks * 2048) {
+        uint32_t x[8];
+        int row = row_of.of(max(e0, 0)), c = max(e0, 0) - row * p.Dv;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = e0 + i;
+            x[i] = e >= 0 && e < given ? from[(long long)row * p.Pv + c] : 0;
+            if (e >= 0 && ++c == p.Dv) {
+                c = 0;
+                ++row;
+            }
+        }
+        if (e0 >= 0 && e0 + 8 <= written) {
+            *reinterpret_cast<uint4*>(out + e0) =
+                make_uint4(x[0] | x[1] << 16, x[2] | x[3] << 16, x[4] | x[5] << 16, x[6] | x[7] << 16);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (e0 + i >= 0 && e0 + i < written) out[e0 + i] = (unsigned short)x[i];
+        }
+    }
+    ptx::griddep_launch_dependents();
+}
+
 // ------------------------------------------------------------------ host side
 constexpr uint32_t kKnownFlags = GDN_FORCE_FFMA | GDN_SINGLE_PASS | GDN_HEAD_DECAY;  // (and GDN_ZERO_PADDING of a prompt)
 
@@ -570,12 +635,32 @@ gdn_status check(const void* q, const void* k, const void* v, const float* g_log
         overlap_in_part(state_out, st, state_in, st))
         return GDN_ERR_UNSUPPORTED;
     *p = LinearAttn{q, k, v, g_log, lengths, state_in, state_out, out, scale, (int)d->B, (int)d->Hk, (int)d->Hv, (int)d->S,
-                    (int)d->Dk, (int)d->Dv, d->dtype == GDN_BF16, (d->flags & GDN_HEAD_DECAY) != 0, lengths && (d->flags & GDN_ZERO_PADDING)};
+                    (int)d->Dk, (int)d->Dv, d->dtype == GDN_BF16, (d->flags & GDN_HEAD_DECAY) != 0, lengths && (d->flags & GDN_ZERO_PADDING), (int)d->Dk, (int)d->Dv};
     return GDN_OK;
 }
 
-bool on_tensor_cores(const LinearAttn& p, const gdn_dims* d) {
-    return !(d->flags & GDN_FORCE_FFMA) && linear_attn_tc_supported(p);
+// Whether rows are padded for the tensor cores: bf16 with channels that are no multiple of 8, of more than kPadWork state elements
+// over all tokens (below, the FMA units are done before two more launches are worth it).
+constexpr double kPadWork = 1.5e8;
+bool padded(const gdn_dims* d) {
+    return d->dtype == GDN_BF16 && !(d->flags & GDN_FORCE_FFMA) && (d->Dk % 8 || d->Dv % 8) &&
+           (double)d->B * d->Hv * d->S * d->Dk * d->Dv > kPadWork && d->B * d->Hv * d->S < INT32_MAX / 16 - 4096 &&
+           d->S * d->Dv < INT32_MAX / 2;  // (what these launches count in 32 bits)
+}
+bool tensor_core_dims(const gdn_dims* d) {
+    return d->dtype == GDN_BF16 && !(d->flags & GDN_FORCE_FFMA) && ((d->Dk % 8 == 0 && d->Dv % 8 == 0) || padded(d));
+}
+// Bytes of the padded q and k (each), and v and out.
+struct PadBytes {
+    size_t qk, vo;
+    size_t all() const { return 2 * (qk + vo); }
+};
+PadBytes pad_bytes(const gdn_dims* d) {
+    if (!padded(d)) return {0, 0};
+    const auto of = [&](int64_t heads, int64_t D) {
+        return D % 8 ? ((size_t)(d->B * heads * d->S * ((D + 7) / 8 * 8)) * 2 + 255) / 256 * 256 : 0;
+    };
+    return {of(d->Hk, d->Dk), of(d->Hv, d->Dv)};
 }
 
 // Segments that a sequence is cut into, of *len tokens: as many as make the call shortest by an estimate of its launches, and
@@ -587,7 +672,7 @@ bool on_tensor_cores(const LinearAttn& p, const gdn_dims* d) {
 // segments 88); 4 x 32 heads x 4096 stay whole, 86 us (2 segments: 122).
 int segments(const gdn_dims* d, int sms, int* len) {
     *len = (int)d->S;
-    const bool tc = !(d->flags & GDN_FORCE_FFMA) && d->dtype == GDN_BF16 && d->Dk % 8 == 0 && d->Dv % 8 == 0;
+    const bool tc = tensor_core_dims(d);
     const int unit = tc ? 128 : kTok;
     const double whole = tc ? 2.5 : 8.0, states = tc ? 1.5 : 5.0, launch = 4.0, state = 0.05;
     const long long heads = (long long)d->B * d->Hv, units = (d->S + unit - 1) / unit, room = tc ? sms : 2ll * sms;
@@ -614,13 +699,63 @@ int segments(const gdn_dims* d, int sms, int* len) {
 // the hand-over costs some 8 us.
 int handed_parts(const gdn_dims* d, int sms, int* len) {
     const long long heads = (long long)d->B * d->Hv, units = (d->S + 127) / 128, whole = heads / sms, rest = heads % sms;
-    if ((d->flags & (GDN_SINGLE_PASS | GDN_FORCE_FFMA)) || d->dtype != GDN_BF16 || d->Dk % 8 || d->Dv % 8) return 0;
+    if ((d->flags & GDN_SINGLE_PASS) || !tensor_core_dims(d)) return 0;
     if (whole < 1 || rest < 1 || heads > INT32_MAX - sms) return 0;
     long long n = sms / rest < whole + 1 ? sms / rest : whole + 1;
     while (n > 1 && (n - 1) * ((units + n - 1) / n) >= units) --n;  // (the last part would be empty)
     if (n < 2 || units - (units + n - 1) / n < 4) return 0;
     *len = (int)((units + n - 1) / n * 128);
     return (int)(n * rest);
+}
+
+// q, k and v into padded rows at `to`, and *r the call on these.
+gdn_status pad_rows(const LinearAttn& p, const PadBytes& pb, uint8_t* to, int sms, cudaStream_t stream, LinearAttn* r) {
+    PadRows a{};
+    const void* src[3] = {p.q, p.k, p.v};
+    const size_t at[3] = {0, pb.qk, 2 * pb.qk};
+    const auto up = [](int D) { return (D + 7) / 8 * 8; };
+    long long most = 0;
+    for (int w = 0; w < 3; ++w) {
+        const bool vo = w == 2;
+        a.src[w] = static_cast<const __nv_bfloat16*>(src[w]);
+        a.dst[w] = (vo ? pb.vo : pb.qk) ? reinterpret_cast<__nv_bfloat16*>(to + at[w]) : nullptr;
+        a.heads[w] = vo ? p.Hv : p.Hk;
+        a.D[w] = vo ? p.Dv : p.Dk;
+        a.P[w] = up(a.D[w]);
+        a.pieces[w] = divisor(a.P[w] / 8);
+        a.tokens[w] = divisor(p.S);
+        a.batch[w] = divisor(a.heads[w] * p.S);
+        const long long n = (long long)p.B * a.heads[w] * p.S * (a.P[w] / 8);
+        if (a.dst[w] && n > most) most = n;
+    }
+    a.lengths = p.lengths;
+    a.B = p.B;
+    a.S = p.S;
+    const long long blocks = (most + 255) / 256;
+    const dim3 grid((unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), 3);
+    if (launch_after(linear_attn_pad_kernel, grid, 256, 0, stream, a) != cudaSuccess) return GDN_ERR_CUDA;
+    if (pb.qk) {
+        r->q = a.dst[0];
+        r->k = a.dst[1];
+        r->Pk = a.P[0];
+    }
+    if (pb.vo) {
+        r->v = a.dst[2];
+        r->out = to + 2 * pb.qk + pb.vo;
+        r->Pv = a.P[2];
+        r->zero_rest = false;
+    }
+    return GDN_OK;
+}
+gdn_status unpad_rows(const LinearAttn& p, const LinearAttn& r, cudaStream_t stream) {
+    LinearAttn o = p;
+    o.Pv = r.Pv;
+    const long long pieces = ((long long)p.S * p.Dv + 7) / 8 + 1, per_head = (pieces + 1023) / 1024, heads = (long long)p.B * p.Hv;
+    const int blocks = (int)(heads * per_head > INT32_MAX ? 1 : per_head);
+    return launch_after(linear_attn_unpad_kernel, dim3((unsigned)(heads * blocks)), 256, 0, stream, o,
+                        static_cast<const unsigned short*>(r.out), divisor(p.Dv), blocks) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -646,28 +781,34 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
     int dev = 0, sms = 0;
     s = gdn::current_device_sms(&dev, &sms);
     if (s != GDN_OK) return s;
-    const bool tc = gdn::on_tensor_cores(p, dims);
+    // the rows that the tensor cores read and write: the caller's, or padded ones
+    const gdn::PadBytes pb = gdn::pad_bytes(dims);
+    const bool pad = pb.all() > 0;
+    bool tc = gdn::tensor_core_dims(dims) && (pb.qk || (gdn::aligned16(q) && gdn::aligned16(k))) &&
+              (pb.vo || (gdn::aligned16(v) && gdn::aligned16(out)));
     gdn::LinearAttnSplit split{1, p.S, nullptr, nullptr, 0, nullptr};
     int len = 0;
     const int P = gdn::segments(dims, sms, &len), handed = P == 1 && tc ? gdn::handed_parts(dims, sms, &len) : 0;
+    const size_t base = P > 1 ? gdn::linear_attn_split_bytes(p, P) : gdn::linear_attn_flag_bytes(handed);
+    const size_t at = (base + 255) / 256 * 256, need = tc && pad ? at + pb.all() : base;
     bool own = false;
     void* ws = nullptr;
-    if (P > 1 || handed) {
-        const size_t need = P > 1 ? gdn::linear_attn_split_bytes(p, P) : gdn::linear_attn_flag_bytes(handed);
+    if (need) {
         if (workspace) {
             if (workspace_bytes < need) return GDN_ERR_WORKSPACE;
             ws = workspace;
         } else if (cudaMallocAsync(&ws, need, st) == cudaSuccess) {
             own = true;
         } else {
-            (void)cudaGetLastError();  // one pass instead
+            (void)cudaGetLastError();  // one pass instead, of the rows as they are
             ws = nullptr;
+            if (pad) tc = false;
         }
         if (ws && handed) {
             split.len = len;
             split.handed = handed;
             split.flags = static_cast<uint32_t*>(ws);
-        } else if (ws) {
+        } else if (ws && P > 1) {
             float* f = static_cast<float*>(ws);
             split = {P, len, f, f + (size_t)P * p.B * p.Hv * p.Dk * p.Dv, 0, nullptr};
         }
@@ -675,7 +816,10 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
     if (tc) {
         int32_t* status = nullptr;
         s = gdn::status_word_for_current_device(&status);
-        if (s == GDN_OK) s = gdn::launch_linear_attn_tc(p, split, dev, sms, status, st);
+        gdn::LinearAttn r = p;
+        if (s == GDN_OK && pad) s = gdn::pad_rows(p, pb, static_cast<uint8_t*>(ws) + at, sms, st, &r);
+        if (s == GDN_OK) s = gdn::launch_linear_attn_tc(r, split, dev, sms, status, st);
+        if (s == GDN_OK && pb.vo) s = gdn::unpad_rows(p, r, st);
     } else {
         const bool async =
             !p.bf16 && p.Dk % 4 == 0 && p.Dv % 4 == 0 && gdn::aligned16(q) && gdn::aligned16(k) && gdn::aligned16(v);
@@ -729,7 +873,10 @@ size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims) {
     p.Dv = (int)dims->Dv;
     const int P = gdn_linear_attn_segments(dims, sms);
     int len = 0;
-    return P > 1 ? gdn::linear_attn_split_bytes(p, P) : gdn::linear_attn_flag_bytes(gdn::handed_parts(dims, sms, &len));
+    const size_t base =
+        P > 1 ? gdn::linear_attn_split_bytes(p, P) : gdn::linear_attn_flag_bytes(gdn::handed_parts(dims, sms, &len));
+    const size_t pad = gdn::pad_bytes(dims).all();
+    return pad ? (base + 255) / 256 * 256 + pad : base;
 }
 
 }  // extern "C"

@@ -25,6 +25,7 @@ struct LinearAttn {
     int B, Hk, Hv, S, Dk, Dv;
     bool bf16, head_decay;
     bool zero_rest;  // rows of out behind a sequence's length are zeroed (only with lengths)
+    int Pk, Pv;      // channels from a row to the next, of q and k and of v and out (the FMA units: Dk and Dv)
 };
 
 // Least log-decay that is told from the others: e^-100 = 3.7e-44 is (nearly) the least fp32 number, so that
@@ -32,6 +33,18 @@ struct LinearAttn {
 // starts a new sequence).
 constexpr float kMinLogDecay = -100.f;
 __device__ __forceinline__ float least_decay(float g) { return g < kMinLogDecay ? kMinLogDecay : g; }  // (NaN stays)
+
+// n / d for 0 <= n < 2^31 as the high half of a product: m = ceil(2^(31 + s) / d), 2^(s - 1) < d <= 2^s.
+struct Divisor {
+    uint32_t m;
+    int s;
+    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi(2u * (uint32_t)n, m) >> s); }
+};
+inline Divisor divisor(int d) {
+    int s = 0;
+    while ((1ll << s) < d) ++s;
+    return Divisor{(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s};
+}
 
 // Segments of every sequence (P = 1: whole).  Segment j holds tokens [j len, (j + 1) len) of S.  A first launch runs
 // segments 0 .. P - 2 from zero (segment 0: from state_in) and leaves their end states X_j in `parts` [P][B Hv][Dk Dv]
@@ -56,9 +69,7 @@ inline size_t linear_attn_split_bytes(const LinearAttn& p, int P) {
 
 inline size_t linear_attn_flag_bytes(int handed) { return handed ? ((size_t)handed * 8 + 1) * sizeof(uint32_t) : 0; }
 
-// bf16 with head dims of whole 16-byte rows, on aligned pointers.
-bool linear_attn_tc_supported(const LinearAttn& p);
-// All launches of a split, or the one of P = 1.
+// bf16, rows (of Pk and Pv channels) and pointers of whole 16 bytes: all launches of a split, or the one of P = 1.
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream);
 

@@ -168,17 +168,6 @@ __device__ __forceinline__ void tmem_st8u(uint32_t taddr, const uint32_t (&r)[8]
                  : "memory");
 }
 
-// n / d for 0 <= n < 2^31 as the high half of a product: m = ceil(2^(31 + s) / d), 2^(s - 1) < d <= 2^s.
-struct Divisor {
-    uint32_t m;
-    int s;
-    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi(2u * (uint32_t)n, m) >> s); }
-};
-Divisor divisor(int d) {
-    int s = 0;
-    while ((1ll << s) < d) ++s;
-    return Divisor{(uint32_t)(((1ull << (31 + s)) + d - 1) / d), s};
-}
 // What the kernel's walk over its items needs: (segment, head) pairs, heads fastest, every gridDim-th of them a CTA's.
 // kHanded (one segment): every CTA has `whole` heads, and the heads that are left over are each cut into parts of `len` tokens,
 // which `handed` CTAs run: part j of the r-th is CTA j rest + r's, after j of its whole heads, so that part j - 1 has left
@@ -687,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int m = 0; m < quad; ++m) R += sh.T[s][m];
             const float f = p.scale * exp2_approx(fmaxf(R, kMinRow));
-            uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Dv * 2;
+            uint8_t* row = static_cast<uint8_t*>(p.out) + ((long long)sh.bh[s] * p.S + sh.t[s] + r) * p.Pv * 2;
             // whole chunks and the tensor's end go out by TMA, from q's tile (its products are done); where a length
             // ends inside a chunk, a thread writes its row itself (rows behind the length: zeros, or nothing)
             const bool tma = n == kC || sh.t[s] + n == p.S;
@@ -950,7 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (Walk k = first_item<kHanded>(it, sh); k.seg < items_of<kHanded>(it, sh); next_item<kHanded>(k, it, sh)) {
                 const int end = tokens_of<kHanded>(k, p, it);
                 const int from = k.end > k.t ? k.t + (k.end - k.t + kC - 1) / kC * kC : k.t;
-                const int row = p.Dv / 8;  // in pieces of 16 bytes
+                const int row = p.Pv / 8;  // in pieces of 16 bytes
                 uint4* to = reinterpret_cast<uint4*>(p.out) + ((long long)k.bh * p.S + from) * row + lane;
                 uint4* const stop = to + (long long)(end - from) * row - lane;  // (not past `to` where the tokens go to the end)
 #pragma unroll 1
@@ -1040,17 +1029,12 @@ gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAt
 
 }  // namespace
 
-bool linear_attn_tc_supported(const LinearAttn& p) {
-    const auto off = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15u) != 0; };
-    return p.bf16 && p.Dk % 8 == 0 && p.Dv % 8 == 0 && !off(p.q) && !off(p.k) && !off(p.v) && !off(p.out);
-}
-
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream) {
     CUtensorMap m[4];
     const long long hk = (long long)p.B * p.Hk, hv = (long long)p.B * p.Hv;
-    if (!encode(&m[0], p.q, hk, p.S, p.Dk) || !encode(&m[1], p.k, hk, p.S, p.Dk) || !encode(&m[2], p.v, hv, p.S, p.Dv) ||
-        !encode(&m[3], p.out, hv, p.S, p.Dv))
+    if (!encode(&m[0], p.q, hk, p.S, p.Pk) || !encode(&m[1], p.k, hk, p.S, p.Pk) || !encode(&m[2], p.v, hv, p.S, p.Pv) ||
+        !encode(&m[3], p.out, hv, p.S, p.Pv))
         return GDN_ERR_CUDA;
     if (s.P > 1) {
         const gdn_status e = launch<true, false>(m, p, s, dev, sms, status, stream);
