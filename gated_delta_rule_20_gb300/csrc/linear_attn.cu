@@ -8,7 +8,7 @@
 // its stores before the sums over rows go through shared memory; 64 registers a thread let an SM hold 128 KB of loads.
 // Measured (128 x 128): 64 x 32 heads 41 us, 6.6 TB/s of the 6.8 that a copy reaches; 4 x 32 heads 3.2 us, 1 x 32 heads 2.0 us.
 //
-// Prefill on the FMA units (fp32 compute, and head dims off the tensor-core kernel): the recurrence itself, token by
+// Prefill on the FMA units (fp32 compute, and small bf16 calls of head dims off the tensor-core kernel): the recurrence itself, token by
 // token, with the state in registers.  Its 2 Dk Dv multiply-adds a token are the fewest of any form (a chunked one adds
 // C (Dk + Dv) / 2), and every one is an fp32 FMA on operands that lie in shared memory.  A warp owns 16
 // columns: lane (d, e) = (lane % 8, lane / 8) holds rows 32 m + 4 d + {0..3} of columns 4 e + {0..3}, so that the 8 lanes of a
@@ -639,13 +639,17 @@ gdn_status check(const void* q, const void* k, const void* v, const float* g_log
     return GDN_OK;
 }
 
-// Whether rows are padded for the tensor cores: bf16 with channels that are no multiple of 8, of more than kPadWork state elements
-// over all tokens (below, the FMA units are done before two more launches are worth it).
-constexpr double kPadWork = 1.5e8;
+// Whether rows are padded for the tensor cores: bf16 with channels that are no multiple of 8.  Small calls keep the recurrence on
+// the FMA units (two more launches), and so do heads of a few tokens: a chunk of 128 takes the tensor cores 2.5 us an SM however
+// few of them there are.  us, FMA units and tensor cores: 4 x 32 heads x 4096 x 77 x 75 1824, 176; 1 x 8 x 500 x 77 x 75 36, 18;
+// 8 x 4 x 100 x 33 x 35 23, 10; 64 x 32 x 2 x 100 x 100 82, 62; but 64 x 32 x 20 x 30 x 30 28, 56.
+constexpr double kPadWork = 3e6;    // state elements over all tokens
+constexpr int64_t kPadHead = 24576;  // and over a head's, as the FMA units take them: 32 rows and 16 columns at once
 bool padded(const gdn_dims* d) {
     return d->dtype == GDN_BF16 && !(d->flags & GDN_FORCE_FFMA) && (d->Dk % 8 || d->Dv % 8) &&
-           (double)d->B * d->Hv * d->S * d->Dk * d->Dv > kPadWork && d->B * d->Hv * d->S < INT32_MAX / 16 - 4096 &&
-           d->S * d->Dv < INT32_MAX / 2;  // (what these launches count in 32 bits)
+           (double)d->B * d->Hv * d->S * d->Dk * d->Dv > kPadWork &&
+           d->S * ((d->Dk + 31) / 32 * 32) * ((d->Dv + 15) / 16 * 16) > kPadHead &&
+           d->B * d->Hv * d->S < INT32_MAX / 16 - 4096 && d->S * d->Dv < INT32_MAX / 2;  // (what these launches count in 32 bits)
 }
 bool tensor_core_dims(const gdn_dims* d) {
     return d->dtype == GDN_BF16 && !(d->flags & GDN_FORCE_FFMA) && ((d->Dk % 8 == 0 && d->Dv % 8 == 0) || padded(d));

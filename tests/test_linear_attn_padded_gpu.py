@@ -19,9 +19,14 @@ def bytes_of(x, **kw):
     (1, 2, 2, 7001, 90, 121, "weak", None),
     (3, 1, 3, 1400, 128, 127, "head", [1400, 700, 0]),
     (4, 2, 4, 1100, 73, 128, "strong", [1100, 1, 129, 1023]),
-    (40, 3, 6, 300, 65, 33, "token", None)])
+    (40, 3, 6, 300, 65, 33, "token", None),
+    (1, 1, 1, 700, 77, 75, "head", None),
+    (8, 4, 4, 100, 33, 35, "token", [100, 0, 1, 31, 32, 33, 99, 64]),
+    (64, 16, 32, 2, 100, 100, "token", None),
+    (150, 1, 3, 64, 1, 128, "weak", None),
+    (300, 1, 1, 90, 128, 1, "token", None)])
 def test_padded_rows(B, Hk, Hv, S, Dk, Dv, decay, lengths):
-    assert B * Hv * S * Dk * Dv > 1.5e8
+    assert B * Hv * S * Dk * Dv > 3e6
     x = inputs(B, Hk, Hv, S, Dk, Dv, "bf16", decay, True, seed=S)
     need = bytes_of(x, single_pass=True)
     assert need >= 2 * (x["q"].numel() if Dk % 8 else x["v"].numel())
@@ -63,6 +68,14 @@ def test_padded_rows(B, Hk, Hv, S, Dk, Dv, decay, lengths):
         assert torch.equal(o[b, :, :n], y[0][b, :, :n])
     assert torch.equal(w[1], y[1]) and bool((u[:5] == 7.0).all()) and bool((u[-4:] == 7.0).all())
     assert gdn.device_status(0) == 0
+
+
+def test_what_is_padded():
+    need = lambda *s, **kw: gdn.linear_attn_workspace_bytes(*s, single_pass=True, **kw)  # noqa: E731
+    assert need(4, 2, 4, 500, 77, 75) > 0 and need(4, 2, 4, 500, 80, 72) == 0
+    assert need(4, 2, 4, 500, 77, 75, gdn.GDN_F32) == 0 and need(4, 2, 4, 500, 77, 75, force_ffma=True) == 0
+    assert need(1, 1, 1, 500, 77, 75) == 0                                      # small
+    assert need(64, 16, 32, 20, 30, 30) == 0 and need(64, 16, 32, 40, 30, 30) > 0   # heads of a few tokens
 
 
 def test_padded_heads_handed_on_and_graph():

@@ -282,5 +282,5 @@ def test_widest_ctas_of_the_fma_units(Dk, dtype):
     """Heads enough for CTAs of 128 columns, whose tokens' shared memory is 48 KB with 65 to 96 rows, at every number of rows."""
     x = inputs(40, 4, 8, 19, Dk, 127, dtype)
     out, st, size = ref.recurrence(x["q"], x["k"], x["v"], x["g"], 0.1, x["state"])
-    y = call(x)
+    y = call(x, force_ffma=True)
     compare(y, (out, st), size, dtype, False, "wide")
