@@ -69,7 +69,8 @@ struct Small {
     float w[2][4];       // e^(the log-decays behind the block)
     float total[2];      // e^(the chunk's)
     int bh[2], t[2], n[2];  // its head, its first token, and how many it has (0: there is no further chunk)
-    uint64_t vtile[2], kqfull[2], tfree[2], staged[2], decfull[2], decfree[2];
+    uint64_t vtile[2], kqfull[2], tfree[2], decfull[2], decfree[2];
+    uint64_t staged[2][2];  // a q tile's outputs, by halves of the channels
     uint64_t vfull[kSlots], vfree[kSlots];
     uint64_t sfull, sfree, xfull[2], xfree[2], qkfull, pfull, ofull, ofree, drain;
     uint32_t tmem;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.vtile[i], 1);
             mbar_init(&sh.kqfull[i], 1);
             mbar_init(&sh.tfree[i], 1);
-            mbar_init(&sh.staged[i], 128);
+            for (int h = 0; h < 2; ++h) mbar_init(&sh.staged[i][h], 128);
             mbar_init(&sh.decfull[i], 32);
             mbar_init(&sh.decfree[i], 769);  // 24 warps and the thread of the products
         }
@@ -715,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (col & 32) {
                     fence_proxy_async_smem();
-                    mbar_arrive(&sh.staged[col >> 6]);
+                    mbar_arrive(&sh.staged[s][col >> 6]);
                 }
             }
             tc_fence_before();
@@ -753,7 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const bool whole = was[0].n == kC || was[0].t + was[0].n == p.S;
 #pragma unroll 1
                         for (int h = 0; h < 2 && ok; ++h) {
-                            ok = wait_one(&sh.staged[h], cn & 1);
+                            // (a barrier a tile: its next phase is that of chunk cn, whose q is loaded behind this wait.  This thread may
+                            // come late, from a walk over many items without tokens, and the outputs of chunk cn - 1 be there too)
+                            ok = wait_one(&sh.staged[s][h], ph ^ 1);
                             if (ok && whole && 64 * h < p.Dv)
                                 tma_store_3d(&to, qt + h * kHalf, 64 * h, was[0].t, was[0].bh);
                         }
