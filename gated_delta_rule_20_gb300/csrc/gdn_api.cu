@@ -239,6 +239,7 @@ gdn_status gdn_test_stall_prefill(int device, int on) {
     if (cudaSetDevice(device) != cudaSuccess) return GDN_ERR_CUDA;
     gdn_status s = GDN_OK;
     if (cudaDeviceSynchronize() != cudaSuccess || gdn::set_prefill_tc_test_stall(on) != cudaSuccess) s = GDN_ERR_CUDA;
+    if (s == GDN_OK && device < gdn::kMaxDevices) gdn::set_linear_attn_test_stall(device, on);
     cudaSetDevice(prev);
     return s;
 }

@@ -85,6 +85,8 @@ gdn_status launch_prefill_tc(const Problem& p, int* status_word, cudaStream_t st
 cudaError_t set_prefill_tc_wait_limit(unsigned long long ns);
 // The tensor-core prefill's test hook on the current device (see gdn_test_stall_prefill).
 cudaError_t set_prefill_tc_test_stall(int on);
+// The same hook of linear attention's prefill, for launches on device `dev` from then on.
+void set_linear_attn_test_stall(int dev, int on);
 
 // The conv1d decode step folded into the gated step: q|k|v are computed from the
 // already shifted windows [B, conv_dim, K] bf16 (the newest token last) and the

@@ -72,7 +72,7 @@ struct Small {
     uint64_t vtile[2], kqfull[2], tfree[2], decfull[2], decfree[2];
     uint64_t staged[2][2];  // a q tile's outputs, by halves of the channels
     uint64_t vfull[kSlots], vfree[kSlots];
-    uint64_t sfull, sfree, xfull[2], xfree[2], qkfull, pfull, ofull, ofree, drain;
+    uint64_t sfull, sfree, xfull[2], xfree[2], qkfull, pfull, ofull, ofree, drain, stall;
     uint32_t tmem;
     int gave_up;
     int cta, items;  // with kHanded: this CTA's number, and how many items it has at most
@@ -110,9 +110,10 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&r)[16]) {
 }
 
 // Waits, inline (a kernel that shares out its registers cannot call functions) and few instructions long (there are many
-// of them): a million tests, each of which suspends the thread for up to 2 us, then false.  (Shorter suspensions are more
-// instructions for the others to wait behind: 4 % of the whole kernel.)
-constexpr uint32_t kMostTests = 1u << 20, kTestNs = 2000;
+// of them): half a million tests, then false.  A test suspends the thread for 3.7 us (of the 2 that it asks for), so
+// that it gives up after some 2 s.  (Shorter suspensions are more instructions for the others to wait behind: 4 % of the
+// whole kernel.  A limit that a launch is given: 0.5 to 1 %.)
+constexpr uint32_t kMostTests = 1u << 19, kTestNs = 2000;
 __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity) {
     uint32_t i = 0;
 #pragma unroll 1
@@ -249,7 +250,7 @@ __device__ __forceinline__ bool next_chunk(Walk& k, const LinearAttn& p, const I
 __device__ __forceinline__ bool wait_flag(const uint32_t* flag) {
     uint32_t v = 0;
 #pragma unroll 1
-    for (uint32_t i = 0; i < kMostTests; ++i) {
+    for (uint32_t i = 0; i < 2 * kMostTests; ++i) {
         asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flag) : "memory");
         if (v) return true;
         asm volatile("nanosleep.u32 1000;");
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     linear_attn_tc_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                           const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
                           const __grid_constant__ LinearAttn p, const __grid_constant__ LinearAttnSplit split,
-                          const __grid_constant__ Items it, int32_t* status) {
+                          const __grid_constant__ Items it, int stall, int32_t* status) {
     extern __shared__ __align__(1024) uint8_t sm[];
     Small& sh = *reinterpret_cast<Small*>(sm + kOffSmall);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, quad = warp & 3;
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&sh.ofull, 1);
         mbar_init(&sh.ofree, 128);
         mbar_init(&sh.drain, 1);
+        mbar_init(&sh.stall, 1);
         fence_mbar_init();
     }
     if (warp == 25) tmem_alloc(&sh.tmem, 512);
@@ -893,7 +895,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int b = 0; b < 4; ++b) g[b] = 32 * b + lane < k.end - k.t ? from[p.head_decay ? 0 : 32 * b] : 0.f;
             };
             if (more) fetch();
-            for (;; ++cn) {
+            if (stall) ok = wait_warp(&sh.stall, 0);  // (on which nothing arrives: gdn_test_stall_prefill)
+            for (; ok; ++cn) {
                 const int s = cn & 1;
                 float down[4];  // the log-decays from a token on to the end of its block
 #pragma unroll
@@ -991,6 +994,8 @@ bool encode(CUtensorMap* map, const void* ptr, long long heads, int S, int D) {
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+std::atomic<int> g_stall[kMaxDevices];  // gdn_test_stall_prefill
+
 template <bool kStatesOnly, bool kHanded>
 gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms,
                   int32_t* status, cudaStream_t stream) {
@@ -1027,10 +1032,14 @@ gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAt
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], p, s, it, status) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    const int stall = g_stall[dev].load(std::memory_order_relaxed);
+    return cudaLaunchKernelEx(&cfg, kernel, m[0], m[1], m[2], m[3], p, s, it, stall, status) == cudaSuccess ? GDN_OK
+                                                                                                            : GDN_ERR_CUDA;
 }
 
 }  // namespace
+
+void set_linear_attn_test_stall(int dev, int on) { g_stall[dev].store(on, std::memory_order_relaxed); }
 
 gdn_status launch_linear_attn_tc(const LinearAttn& p, const LinearAttnSplit& s, int dev, int sms, int32_t* status,
                                  cudaStream_t stream) {

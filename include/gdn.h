@@ -525,7 +525,7 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * pass's to within rounding.  Many heads that are no whole number of rounds of the SMs: those left over run in parts on several
  * SMs, one handing the state on to the next through state_out (the same bits as one pass's; GDN_SINGLE_PASS: never).  The same call on the same device gives the same bits; a batch's sequences do not
  * influence one another's, unless another batch size changes the split.
- * A wait inside the tensor-core kernel that runs out (a second or two) ends it with GDN_ERR_TIMEOUT in the device's status
+ * A wait inside the tensor-core kernel that runs out (some two seconds) ends it with GDN_ERR_TIMEOUT in the device's status
  * word (gdn_device_status) and undefined outputs.
  */
 gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, const float* g_log,
@@ -649,6 +649,8 @@ gdn_status gdn_device_status(int device, int clear, int32_t* code);
  * and exits; the outputs of such a call are undefined.  This exists to exercise
  * that path without a GPU fault (a limit of a few microseconds makes ordinary
  * waits run out); it synchronises the device.  The pages define no such knob.
+ * gdn_linear_attn_prefill's waits keep a bound of their own, some two seconds,
+ * whatever is set here.
  * Returns GDN_ERR_CUDA if the device cannot be selected or the value not set.
  */
 gdn_status gdn_set_wait_limit_ns(int device, uint64_t ns);
@@ -658,7 +660,9 @@ gdn_status gdn_set_wait_limit_ns(int device, uint64_t ns);
  * while on != 0, every CTA of the tensor-core prefill first waits on a barrier
  * that nothing arrives at, so that the wait runs out after the wait limit (set
  * it low with gdn_set_wait_limit_ns) and the call takes its give-up path:
- * GDN_ERR_TIMEOUT in the status word, nothing computed.  No GPU fault is
+ * GDN_ERR_TIMEOUT in the status word, nothing computed.  So does every CTA of
+ * gdn_linear_attn_prefill's tensor-core kernel, in calls made (or captured) while
+ * on != 0; its launches take some two seconds each.  No GPU fault is
  * involved.  Synchronises the device.  Off by default; the pages define no
  * such hook.  Returns GDN_ERR_CUDA if the device cannot be selected or the
  * value not set.
