@@ -639,6 +639,15 @@ gdn_status check(const void* q, const void* k, const void* v, const float* g_log
     return GDN_OK;
 }
 
+// Heads that the tensor-core kernel takes.  Its CTAs walk theirs one by one, 1.2 to 4 us for one without a token, while other
+// roles wait, and waits are bounded (2 s): 2^24 heads are 0.14 s for an SM.  (Of 2^28 without tokens, 8 x 8 each, the waits would
+// run out.)  So many heads have some hundreds of tokens at the most in any memory, and fare as well on the FMA units: 2^22 heads of
+// 1 token 91 ms on the tensor cores and 5.4, 2^20 of 130 tokens 32 and 38.
+constexpr int64_t kMostHeads = 1 << 24;
+bool tensor_core_call(const gdn_dims* d) {
+    return d->dtype == GDN_BF16 && !(d->flags & GDN_FORCE_FFMA) && d->B * d->Hv <= kMostHeads;
+}
+
 // Whether rows are padded for the tensor cores: bf16 with channels that are no multiple of 8.  Small calls keep the recurrence on
 // the FMA units (two more launches), and so do heads of a few tokens: a chunk of 128 takes the tensor cores 2.5 us an SM however
 // few of them there are.  us, FMA units and tensor cores: 4 x 32 heads x 4096 x 77 x 75 1824, 176; 1 x 8 x 500 x 77 x 75 36, 18;
@@ -646,13 +655,13 @@ gdn_status check(const void* q, const void* k, const void* v, const float* g_log
 constexpr double kPadWork = 3e6;    // state elements over all tokens
 constexpr int64_t kPadHead = 24576;  // and over a head's, as the FMA units take them: 32 rows and 16 columns at once
 bool padded(const gdn_dims* d) {
-    return d->dtype == GDN_BF16 && !(d->flags & GDN_FORCE_FFMA) && (d->Dk % 8 || d->Dv % 8) &&
+    return tensor_core_call(d) && (d->Dk % 8 || d->Dv % 8) &&
            (double)d->B * d->Hv * d->S * d->Dk * d->Dv > kPadWork &&
            d->S * ((d->Dk + 31) / 32 * 32) * ((d->Dv + 15) / 16 * 16) > kPadHead &&
            d->B * d->Hv * d->S < INT32_MAX / 16 - 4096 && d->S * d->Dv < INT32_MAX / 2;  // (what these launches count in 32 bits)
 }
 bool tensor_core_dims(const gdn_dims* d) {
-    return d->dtype == GDN_BF16 && !(d->flags & GDN_FORCE_FFMA) && ((d->Dk % 8 == 0 && d->Dv % 8 == 0) || padded(d));
+    return tensor_core_call(d) && ((d->Dk % 8 == 0 && d->Dv % 8 == 0) || padded(d));
 }
 // Bytes of the padded q and k (each), and v and out.
 struct PadBytes {
@@ -704,7 +713,7 @@ int segments(const gdn_dims* d, int sms, int* len) {
 int handed_parts(const gdn_dims* d, int sms, int* len) {
     const long long heads = (long long)d->B * d->Hv, units = (d->S + 127) / 128, whole = heads / sms, rest = heads % sms;
     if ((d->flags & GDN_SINGLE_PASS) || !tensor_core_dims(d)) return 0;
-    if (whole < 1 || rest < 1 || heads > INT32_MAX - sms) return 0;
+    if (whole < 1 || rest < 1) return 0;
     long long n = sms / rest < whole + 1 ? sms / rest : whole + 1;
     while (n > 1 && (n - 1) * ((units + n - 1) / n) >= units) --n;  // (the last part would be empty)
     if (n < 2 || units - (units + n - 1) / n < 4) return 0;

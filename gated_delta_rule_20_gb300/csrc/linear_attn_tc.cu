@@ -246,7 +246,7 @@ __device__ __forceinline__ bool next_chunk(Walk& k, const LinearAttn& p, const I
     next_item<kHanded>(k, it, sh);
     return settle<kHanded>(k, p, it, sh);
 }
-// The flag of a part that another CTA runs (bounded: a second or two).
+// The flag of a part that another CTA runs (bounded: a second at the least).
 __device__ __forceinline__ bool wait_flag(const uint32_t* flag) {
     uint32_t v = 0;
 #pragma unroll 1
@@ -1011,8 +1011,7 @@ gdn_status launch(const CUtensorMap (&m)[4], const LinearAttn& p, const LinearAt
     // the roles' registers come out of what the block is launched with: short of that they would wait for ever
     if (regs * kThreads < kRegsSum) return GDN_ERR_CUDA;
     if (allow_smem(kernel, (int)kSmem, allowed, dev) != cudaSuccess) return GDN_ERR_CUDA;
-    const long long items = (long long)p.B * p.Hv * (kStatesOnly ? s.P - 1 : s.P);
-    if (items > INT32_MAX - sms) return GDN_ERR_DIMS;  // (items are counted in 32 bits)
+    const int items = p.B * p.Hv * (kStatesOnly ? s.P - 1 : s.P);  // (at most 2^24 heads, of 64 segments)
     Items it{p.B * p.Hv, kStatesOnly ? s.P - 1 : s.P, s.P > 1 || kHanded ? s.len : p.S, divisor(p.Hv), divisor(p.Hv / p.Hk),
              0, 0, 0, nullptr};
     if (kHanded) {

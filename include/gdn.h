@@ -516,9 +516,9 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * e^-64 of it at least in the chunk's outputs (1.6e-28).  An infinity or NaN in v may make NaN of its column's
  * outputs from the beginning of its chunk on (a score of zero in front of it is multiplied too), one in k from its
  * token on, one in q of its token's; |q . k| of 5e10 and more behind decays of e^-64 passes bf16's range.
- * fp32 runs the recurrence itself on the FMA units.  So does bf16 with other head dims in small calls (B Hv S Dk Dv up to 3e6) and
- * for heads of a few tokens; other such calls go to the tensor cores by copies of q, k, v and out with padded rows, in the
- * workspace, and round as above.
+ * fp32 runs the recurrence itself on the FMA units.  So does bf16 with more than 2^24 heads (B Hv), and with other head
+ * dims in small calls (B Hv S Dk Dv up to 3e6) and for heads of a few tokens; other such calls go to the tensor cores by
+ * copies of q, k, v and out with padded rows, in the workspace, and round as above.
  * Few sequences of many tokens are cut into segments that run at once (gdn_linear_attn_segments; GDN_SINGLE_PASS:
  * never): a first launch runs all but the last from zero and keeps their states and decays, a second adds them up to the
  * segments' start states (nothing to do for two segments), and the last runs every segment.  Results of a split agree with one
