@@ -17,9 +17,11 @@
 // e^64, inside bf16's range.  The output's last product is scale e^{m_i}.  (Rows past c_i = -64 so keep e^-64 of S instead of
 // less: 1.6e-28.)
 //
-// Exponents.  c is summed within blocks of 32 tokens: no difference of two large sums is ever taken.  With block sums T_b,
-// a score off the diagonal blocks takes e^{c_i - R} e^{R - c_j}, R the end of j's block, a factor of its row and one of its
-// column, and only the 32 x 32 diagonal blocks take an exponential an element.
+// Exponents.  c is summed within blocks of 32 tokens, forward for a row's factor and backward for a column's.  With block sums
+// T_b, a score off the diagonal blocks takes e^{c_i - R} e^{R - c_j}, R the end of j's block, a factor of its row and one of its
+// column, both of sums of what lies between the two alone; only the 32 x 32 diagonal blocks take an exponential an element, of
+// c_i - c_j.  That is a difference of large sums for tokens behind several in the same 32 that start anew (of -100 each): it is off
+// by a few 2^-24 of these, 1e-4 behind ten of them, where the score is rounded to 2^-8.
 //
 // Roles (896 threads): 4 warps turn scores into P, 8 hold the state (a thread: 64 rows of a column dv in fp32 registers), 8
 // make the parts of e^. V, 4 write the outputs; one warp each for TMA, the products and the decays.  A CTA walks its
@@ -422,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             // 16 columns at a time, the next 16 on their way; loops that stay small: the roles share the
             // instruction caches.  What is written lies over score columns that this warp has read
-            float between = shift + (a > 0 ? R - sh.T[s][0] : 0.f);  // c_i - m_i less the end of block b
+            // c_i - m_i less the end of block b, for this block and the next one (sums of what lies between alone)
+            float next = shift + (a > 2 ? sh.T[s][2] : 0.f), between = a > 2 ? next + sh.T[s][1] : a > 1 ? shift + sh.T[s][1] : shift;
             float x[16], y[16];
             tmem_ld16(tq4 + kColP, x);
             const auto off_diagonal = [&](const float (&v)[16], unsigned long long uu, int col) {
@@ -440,7 +443,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int b = 0; b < a; ++b) {
                 const float u = exp2_approx(between);
                 const unsigned long long uu = pair(u, u);
-                between -= b + 1 < a ? sh.T[s][b + 1] : 0.f;
+                between = next;
+                next = shift;
                 tmem_wait_ld();
                 tmem_ld16(tq4 + kColP + 32 * b + 16, y);
                 off_diagonal(x, uu, 32 * b);
@@ -908,6 +912,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float z = __shfl_down_sync(0xffffffffu, down[b], o);
                         if (lane + o < 32) down[b] += z;
                     }
+                // and from its block's beginning on to the token: a sum of its own, since the block's less what is behind the
+                // token is a difference of two large ones where a block starts anew several times
+                float up[4] = {};
+                if (!kStatesOnly) {  // (which has no scores)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) up[b] = least_decay(g[b]);
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            const float z = __shfl_up_sync(0xffffffffu, up[b], o);
+                            if (lane >= o) up[b] += z;
+                        }
+                }
                 float T[4], after[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
@@ -922,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
-                    sh.c[s][32 * b + lane] = kLog2e * (T[b] - after[b]);  // (of the scores, which are bf16)
+                    if (!kStatesOnly) sh.c[s][32 * b + lane] = kLog2e * up[b];
                     sh.h[s][32 * b + lane] = expf(after[b]);
                 }
                 if (lane < 4) {
