@@ -494,7 +494,8 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  *   q, k        [B, Hk, S, Dk]  compute dtype (need not be normalised)
  *   v           [B, Hv, S, Dv]  compute dtype
  *   g_log       [B, Hv, S] fp32 log-decays, or [Hv] under GDN_HEAD_DECAY; <= 0 (not checked).  Values below -100
- *               count as -100 (e^-100 is 3.7e-44): -infinity drops what came before the token
+ *               count as -100 (e^-100 is 3.7e-44): -infinity drops what came before the token (if that is
+ *               finite: an infinity or NaN in the state stays one)
  *   lengths     [B] int32 or NULL: sequence b has lengths[b] tokens (below 0: 0, above S: S).  Rows of q, k, v
  *               and g_log behind them have no influence, whatever they hold, and rows of out are left as they were
  *               (GDN_ZERO_PADDING: set to zero)
@@ -515,7 +516,10 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * three bf16 parts of exp(.) v, which add up to its 24 bits.  What a chunk's decays leave of the state is taken as
  * e^-64 of it at least in the chunk's outputs (1.6e-28).  An infinity or NaN in v may make NaN of its column's
  * outputs from the beginning of its chunk on (a score of zero in front of it is multiplied too), one in k from its
- * token on, one in q of its token's; |q . k| of 5e10 and more behind decays of e^-64 passes bf16's range.
+ * token on, one in q of its token's.  A token's sums over its chunk stand divided by e^c until the end, c >= -64 its
+ * log-decays since the chunk's first token: where |q . k|, or the sum of the scores' products with v, passes 3.4e38 e^c
+ * (5e10 behind decays of e^-64 and more), its outputs are infinite or NaN, although they may fit bf16.  (The FMA units
+ * multiply by e^8 at most: q, k and v, and the state, whose products and sums stay below 1e35 are safe there.)
  * fp32 runs the recurrence itself on the FMA units.  So does bf16 with more than 2^24 heads (B Hv), and with other head
  * dims in small calls (B Hv S Dk Dv up to 3e6) and for heads of a few tokens; other such calls go to the tensor cores by
  * copies of q, k, v and out with padded rows, in the workspace, and round as above.
