@@ -5,8 +5,10 @@
 // on channel pairs (i, i + R/2) or (2i, 2i + 1) of the first R channels; the rest is copied.
 //
 // The angle is kept in turns, as a 64-bit binary fraction of one: f = inv_freq / 2 pi mod 1, and position * f wraps
-// around as whole turns do.  The product is exact, so that far positions keep the accuracy of near ones: the angle's error is
-// 2^-64 of a turn a position, from f, where an fp32 product loses 2^-24 of the angle itself (a radian at position 10^7).
+// around as whole turns do.  That product is exact, so that far positions keep the accuracy of near ones: the angle's
+// error is that of f, 1.5 * 2^-64 of a turn at the most, times the position, where an fp32 product loses 2^-24 of the
+// angle itself (a radian at position 10^7).  (Frequencies above 1 radian, which no model has, take whole turns out of the 64
+// bits of 2 / pi: their f is off by as many times as much.)
 //
 // Bound by bytes: a row is read and written once.  A thread takes one piece of a token's head (16 bytes, or two of them half
 // the turned channels apart), makes that piece's sines and cosines, and goes through the heads with them: the trigonometry

@@ -588,8 +588,9 @@ typedef struct {
  *              those of packed rows do); its rows may not lie over one another (GDN_ERR_DIMS).  k, k_out likewise
  *   inv_freq   [R/2] fp64, radians a position (fp32 ones of a model: widened)
  *   positions  int64 (or int32) [B, S], tokens contiguous, or NULL
- * theta is taken mod one turn exactly (2^-64 of a turn a position), so that its accuracy does not fall with
- * the position; cos and sin in fp32, one rounding to dtype.  Infinite and NaN frequencies turn nothing.
+ * theta is taken mod one turn as a 64-bit fraction, off by at most 1.5 * 2^-64 of a turn a position, times |inv_freq|
+ * where that is above 1 (2/pi is kept to 64 bits): frequencies of a model, up to 1, are as accurate at far positions as at
+ * near ones.  cos and sin in fp32, one rounding to dtype.  Infinite and NaN frequencies turn nothing.
  * Pointers aligned to their element; accesses are as wide, up to 16 bytes, as every pointer, stride, R/2 (R for
  * GDN_ROTARY_INTERLEAVED) and D - R are multiples of.
  */

@@ -175,3 +175,23 @@ def test_heads_of_q_and_k_in_turn_in_place():
         gdn.rotary(q_of(x), k_of(x), f, first_position=7, q_out=q_of(x), k_out=k_of(x))
         check(q_of(x), q_of(was), f, np.arange(7, 7 + S), "f32", D)
         check(k_of(x), k_of(was), f, np.arange(7, 7 + S), "f32", D)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_large_frequencies_at_far_positions(layout):
+    """inv_freq far above 1, where f = inv_freq / 2 pi mod 1 is off by 1.5 * 2^-64 of a turn times inv_freq: in front of
+    cos and sin's own 2^-21 of |a| + |b| the angle's error, 2 pi times that and the position, moves an output by at most
+    as much of |a| + |b| again."""
+    f = torch.tensor([1.0, 3.7, 1e3, -2.5e4, 1e6, 7e8, -1e10, 3e11], dtype=torch.float64, device="cuda")
+    R = 16
+    x = torch.randn(1, 2, 5, R, generator=torch.Generator().manual_seed(2)).cuda()
+    pos = np.array([0, 1, 1000, (1 << 20) + 1, -(1 << 21)])
+    y, _ = gdn.rotary(x, None, f, torch.from_numpy(pos).cuda(), layout=layout)
+    want = ref.rotary(x, f.cpu().numpy(), pos, layout)
+    a = np.abs(x.double().cpu().numpy())
+    ia, ib = (slice(0, 8), slice(8, 16)) if layout == "half" else (slice(0, 16, 2), slice(1, 16, 2))
+    angle = 2 * np.pi * 1.5 * 2.0 ** -64 * np.abs(pos)[:, None] * np.maximum(1, np.abs(f.cpu().numpy()))
+    for i in (ia, ib):
+        most = (a[..., ia] + a[..., ib]) * (2.0 ** -21 + angle) + 2.0 ** -24 * np.abs(want[..., i])
+        off = np.abs(y.double().cpu().numpy()[..., i] - want[..., i])
+        assert (off <= most).all(), "%.3g times what is allowed" % (off / most).max()
