@@ -16,11 +16,13 @@
 // (fma.rn.f32x2).  The state is kept as S~_t = e^{-c_t} S_t, with c the sum of the log-decays since the first of 16
 // staged tokens: S~ += (e^{-c_t} k_t) v_t^T, o_t = e^{c_t} scale S~^T q_t, and one product by e^{c_16} a block.  That is a third
 // fewer operations than a decay a token, and one rounding of a decay in 16: with decays near 1 the functions' errors
-// would add up (1.5e-6 after 290 tokens at e^-0.0005).  Blocks that decay by more than e^-8 take a product a token; they
-// forget within a few tokens.  64 packed FMAs a warp and token are 128 cycles of a scheduler; with the loads, the sums over
-// lanes and what prepares v it issues some 200 instructions, and 32 heads of 8 warps leave a scheduler one warp or two, whose
-// latencies show: 4 x 32 heads x 512 x 128 x 128 in fp32 251 us in one pass, 228 in two segments (the FMAs alone: 58);
-// 2 x 16 heads x 2048 222 us in segments and 1022 in one pass.
+// would add up (1.5e-6 after 290 tokens at e^-0.0005).  c is an fp32 sum, whose roundings are the largest error left
+// (1.4e-7 of the outputs' norm, 1.9e-7 of the state's, at e^-0.25 a token); kept as two numbers (1.1e-7 and 0.7e-7) it takes
+// up to 8 % longer.  Blocks that decay by more than e^-8 take a product a token; they forget within a few tokens.  64 packed
+// FMAs a warp and token are 128 cycles of a scheduler; with the loads, the sums over lanes and what prepares v it issues some
+// 200 instructions, and 32 heads of 8 warps leave a scheduler one warp or two, whose latencies show: 4 x 32 heads x 512 x 128 x
+// 128 in fp32 249 us in one pass, 224 in two segments (the FMAs alone: 58); 2 x 16 heads x 2048 218 us in segments and 1022 in
+// one pass.
 #include <cuda_bf16.h>
 
 #include <atomic>

@@ -512,25 +512,29 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * another, but for state_out in state_in's place (GDN_ERR_UNSUPPORTED).
  * bf16 with Dk and Dv multiples of 8 and q, k, v and out on 16 bytes runs on the tensor cores, in chunks of 128
  * tokens: products of bf16 operands with fp32 sums; the decayed scores and the copy of the state that the queries
- * read are rounded to bf16 once (the outputs' own type).  The state itself is fp32 and is updated with
- * three bf16 parts of exp(.) v, which add up to its 24 bits.  What a chunk's decays leave of the state is taken as
- * e^-64 of it at least in the chunk's outputs (1.6e-28).  An infinity or NaN in v may make NaN of its column's
- * outputs from the beginning of its chunk on (a score of zero in front of it is multiplied too), one in k from its
- * token on, one in q of its token's.  A token's sums over its chunk stand divided by e^c until the end, c >= -64 its
- * log-decays since the chunk's first token: where |q . k|, or the sum of the scores' products with v, passes 3.4e38 e^c
- * (5e10 behind decays of e^-64 and more), its outputs are infinite or NaN, although they may fit bf16.  (The FMA units
- * multiply by e^8 at most: q, k and v, and the state, whose products and sums stay below 1e35 are safe there.)
+ * read are rounded to bf16 once (the outputs' own type): outputs are some 0.0023 of their norm off, where their own
+ * rounding makes 0.0017 (GDN_FORCE_FFMA: no others).  The state itself is fp32 and is updated with three bf16 parts
+ * of exp(.) v, which add up to its 24 bits.  What a chunk's decays leave of the state is taken as e^-64 of it at least
+ * in the chunk's outputs (1.6e-28).  An infinity or NaN in v may make NaN of its column's outputs from the beginning
+ * of its chunk on (a score of zero in front of it is multiplied too), one in k from its token on, one in q of its
+ * token's.  A token's sums over its chunk stand divided by e^c until the end, c >= -64 its log-decays since the chunk's
+ * first token: where |q . k|, or the sum of the scores' products with v, passes 3.4e38 e^c (5e10 behind decays of
+ * e^-64 and more), its outputs are infinite or NaN, although they may fit bf16.
  * fp32 runs the recurrence itself on the FMA units.  So does bf16 with more than 2^24 heads (B Hv), and with other head
  * dims in small calls (B Hv S Dk Dv up to 3e6) and for heads of a few tokens; other such calls go to the tensor cores by
- * copies of q, k, v and out with padded rows, in the workspace, and round as above.
+ * copies of q, k, v and out with padded rows, in the workspace, and round as above.  The FMA units work in fp32
+ * throughout.  They sum the log-decays of up to 16 tokens, and those sums' roundings (2^-22 at most) are their largest
+ * error: outputs and states are some 1.5e-7 of their norm off behind decays of e^-0.25 a token.  Products stand
+ * multiplied by e^8 at most there: q, k and v, and the state, whose products and sums stay below 1e35 are safe.
  * Few sequences of many tokens are cut into segments that run at once (gdn_linear_attn_segments; GDN_SINGLE_PASS:
  * never): a first launch runs all but the last from zero and keeps their states and decays, a second adds them up to the
- * segments' start states (nothing to do for two segments), and the last runs every segment.  Results of a split agree with one
- * pass's to within rounding.  Many heads that are no whole number of rounds of the SMs: those left over run in parts on several
- * SMs, one handing the state on to the next through state_out (the same bits as one pass's; GDN_SINGLE_PASS: never).  The same call on the same device gives the same bits; a batch's sequences do not
- * influence one another's, unless another batch size changes the split.
- * A wait inside the tensor-core kernel that runs out (some two seconds) ends it with GDN_ERR_TIMEOUT in the device's status
- * word (gdn_device_status) and undefined outputs.
+ * segments' start states (nothing to do for two segments), and the last runs every segment.  Results of a split agree
+ * with one pass's to within rounding.  Many heads that are no whole number of rounds of the SMs: those left over run in
+ * parts on several SMs, one handing the state on to the next through state_out (the same bits as one pass's;
+ * GDN_SINGLE_PASS: never).  The same call on the same device gives the same bits; a batch's sequences do not influence
+ * one another's, unless another batch size changes the split.
+ * A wait inside the tensor-core kernel that runs out (some two seconds) ends it with GDN_ERR_TIMEOUT in the device's
+ * status word (gdn_device_status) and undefined outputs.
  */
 gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, const float* g_log,
                                    const int32_t* lengths, float scale, const float* state_in, float* state_out,
@@ -542,7 +546,8 @@ gdn_status gdn_linear_attn_prefill(const void* q, const void* k, const void* v, 
 int32_t gdn_linear_attn_segments(const gdn_dims* dims, int32_t sm_count);
 
 /* Device scratch of gdn_linear_attn_prefill on the current device: a state a segment and head; a few KB of flags where
- * heads are handed on; copies of operands whose rows are padded; 0 without any of these, for invalid dims and without a device.  Host only. */
+ * heads are handed on; copies of operands whose rows are padded; 0 without any of these, for invalid dims and without a
+ * device.  Host only. */
 size_t gdn_linear_attn_workspace_bytes(const gdn_dims* dims);
 
 /*
