@@ -681,10 +681,12 @@ PadBytes pad_bytes(const gdn_dims* d) {
 // Segments that a sequence is cut into, of *len tokens: as many as make the call shortest by an estimate of its launches, and
 // only if that saves a tenth (by dims alone: operands off 16 bytes, which run on the FMA units, are cut alike).
 // A unit (128 tokens on the tensor cores, 16 on the FMA units) takes `whole` us in the last launch and `states` in the first;
-// a launch of a split costs `launch` more, and a combine step and a state's way to and from memory `state`.  (Measured on the
-// tensor cores: 2.2 and 1.6 us a unit.)  Of forced splits of 1 x 32 heads x 32768 tokens into 4 to 37 segments the 9 that it picks
-// are the fastest, 262 us (4: 271, 14: 266, 10: 291, one pass: 562); of 8192 tokens 4 segments, 81 us (one pass 147, 8
-// segments 88); 4 x 32 heads x 4096 stay whole, 86 us (2 segments: 122).
+// a launch of a split costs `launch` more, and a combine step and a state's way to and from memory `state`.  Measured on the
+// tensor cores: a unit 2.2 us where 32 CTAs have HBM to themselves and 2.6 where 128 share it, and 1.6 in the first launch;
+// the others are estimates.  With 2.6 and 1.6 instead of 2.5 and 1.5 none of twelve shapes (1 to 128 heads, 1000 to 131072
+// tokens) is cut otherwise, with 2.2 and 1.6 one (36 heads x 1237, whole).  Of forced splits of 1 x 32 heads x 32768 tokens into 4
+// to 37 segments the 9 that it picks are the fastest, 262 us (4: 271, 14: 266, 10: 291, one pass: 562); of 8192 tokens 4
+// segments, 81 us (one pass 147, 8 segments 88); 4 x 32 heads x 4096 stay whole, 86 us (2 segments: 122).  (All in a graph.)
 int segments(const gdn_dims* d, int sms, int* len) {
     *len = (int)d->S;
     const bool tc = tensor_core_dims(d);

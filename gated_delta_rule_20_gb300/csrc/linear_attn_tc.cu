@@ -31,10 +31,11 @@
 // What bounds it.  A chunk brings in 96 KB and takes 32 KB away; where two value heads share a key head, 96 KB of these pass
 // HBM, 1.85 us of the measured copy's rate among 128 CTAs.  Its products are 48 steps of 66 cycles, 1.6 us.  It takes 2.6 us, and
 // 2.2 where 32 CTAs have HBM to themselves: the products wait for the parts and for P, which wait for products (tensor pipe
-// active 56 % of the cycles, schedulers issuing 56 %).  One CTA an SM: two chunks of q, k and v and the state fill its shared
+// active 64 % of the cycles, schedulers issuing 63 %).  One CTA an SM: two chunks of q, k and v and the state fill its shared
 // memory; scores, O, X and the parts its tensor memory.
-// Measured (bf16, 128 x 128 state): 4 x 32 heads (16 of keys) x 4096 tokens 84 to 86 us, 5.0 TB/s, 73 % of the copy's rate;
-// 16 x 32 heads (8 of keys) x 2048 160 us; 1 x 32 heads x 32768 in 9 segments 262 us (one pass: 562).
+// Measured (bf16, 128 x 128 state), in a graph and, behind the commas, called from Python with inputs and outputs of its own each
+// time: 4 x 32 heads (16 of keys) x 4096 tokens 84 to 85 us, 92; that is 5.0 TB/s, 73 % of the copy's rate, and 4.6; 16 x 32 heads (8
+// of keys) x 2048 157 to 164, 174; 1 x 32 heads x 32768 in 9 segments 260 to 265, 276 (one pass: 562).
 #include <cuda_bf16.h>
 
 #include <atomic>
