@@ -1002,8 +1002,10 @@ def rotary_frequencies(rotary_dim, base=10000.0, *, scaling=None, factor=1.0, or
     R = int(rotary_dim)
     if R < 2 or R % 2:
         raise ValueError("rotary_dim must be even and at least 2, got %s" % rotary_dim)
-    if not base > 0 or not factor >= 1:
-        raise ValueError("base must be positive and factor at least 1")
+    if not 0 < base < math.inf or not 1 <= factor < math.inf:
+        raise ValueError("base must be positive, factor at least 1, and both finite")
+    if scaling == "yarn" and not base > 1:
+        raise ValueError("scaling 'yarn' needs a base above 1")
     i = torch.arange(R // 2, dtype=torch.float64)
     if scaling == "ntk":
         if R == 2:

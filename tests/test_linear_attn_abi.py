@@ -204,3 +204,18 @@ def test_oracle_rotary_hand_worked():
     assert np.allclose(y[..., [0, 2]].ravel(), [-3, 1], atol=1e-6)
     z = ref.rotary(y, np.array([2 * math.pi / 1024, 0.25]), np.array([1024 * 1000000 + 256]), inverse=True)
     assert np.allclose(z, x, atol=1e-12)
+
+
+@pytest.mark.parametrize("bad", [dict(base=1.0, scaling="yarn"), dict(base=0.5, scaling="yarn"), dict(base=math.inf),
+                                 dict(base=math.nan), dict(factor=math.inf, scaling="linear"), dict(factor=math.nan)],
+                         ids=str)
+def test_rotary_frequencies_that_have_none(bad):
+    """The ramp of "yarn" is over log base, which is zero or falls; infinite bases and factors leave no frequency."""
+    with pytest.raises(ValueError):
+        gdn.rotary_frequencies(16, original_length=4096, **bad)
+
+
+def test_rotary_frequencies_of_one_base():
+    for scaling in (None, "linear", "bands"):  # (bases up to 1 are nobody's, and these forms have no trouble with them)
+        f, _ = gdn.rotary_frequencies(16, 1.0, scaling=scaling, factor=2.0, original_length=4096)
+        assert torch.isfinite(f).all() and (f > 0).all()
