@@ -524,7 +524,9 @@ gdn_status gdn_linear_plan(const void* x, const void* weight, const gdn_linear_d
  * dims in small calls (B Hv S Dk Dv up to 3e6) and for heads of a few tokens; other such calls go to the tensor cores by
  * copies of q, k, v and out with padded rows, in the workspace, and round as above.  The FMA units work in fp32
  * throughout.  They sum the log-decays of up to 16 tokens, and those sums' roundings (2^-22 at most) are their largest
- * error: outputs and states are some 1.5e-7 of their norm off behind decays of e^-0.25 a token.  Products stand
+ * error: outputs and states are some 1.5e-7 of their norm off behind decays of e^-0.25 a token.  A state is rounded and
+ * multiplied by a rounded decay once in 16 tokens, which adds up over those that it remembers: 5e-6 after 8000 tokens at
+ * one decay of e^-0.0005 for all (the tensor cores, once in 128: 5e-7 to 1.5e-6).  Products stand
  * multiplied by e^8 at most there: q, k and v, and the state, whose products and sums stay below 1e35 are safe.
  * Few sequences of many tokens are cut into segments that run at once (gdn_linear_attn_segments; GDN_SINGLE_PASS:
  * never): a first launch runs all but the last from zero and keeps their states and decays, a second adds them up to the
